@@ -294,6 +294,47 @@ int w12_concat_rows(const w12_weight *parts, int count, w12_weight *out, uint64_
                     void *stream);
 
 /*
+ * w12_embed -- embedding lookup: out[j][c] = scale * W[ids[j]][c], with W read from its W12 record, so
+ * a model whose embedding table is its LM head keeps one record for both ends of a step.  ids:
+ * `count` int32, or int64 with W12_IDS_I64 (device, naturally aligned); an id outside 0 .. n-1
+ * (padding) reads nothing and gives a row of zeros.  out: [count][k] float (device, 16-byte
+ * aligned, fully overwritten): the weight times scale in float; with W12_OUT_BF16 bfloat16 bits,
+ * that product rounded to nearest even, or for scale = 1 the weight's own bits (NaN payloads and -0
+ * included).  flags: W12_OUT_BF16, W12_IDS_I64.  Uses no workspace.
+ */
+#define W12_IDS_I64 0x40u
+int w12_embed(const void *ids, int64_t count, const w12_weight *wt, float scale, void *out,
+              uint32_t flags, void *stream);
+
+/*
+ * w12_logprobs -- log probabilities of given tokens, entropy and the top alternatives of m rows of
+ * logits (the outputs of a GEMM call over an LM head), in one pass over them: what a verification
+ * step, a draft tree (the sum of log probabilities along a path orders its nodes: summary page,
+ * best-first tree) or the scoring of a given text reads off the logits.
+ * y: rows of n logits, row j at y + j * ldy elements (ldy >= n): float, 4-byte aligned, or
+ * bfloat16 bits (W12_LOGITS_BF16), 2-byte aligned.  tokens: [m][n_tok] int32, or int64 with
+ * W12_IDS_I64 (n_tok = 0: none, tokens and logp may be NULL).  Outputs (device, 4-byte aligned):
+ *   logp[j][t]      = y[j][token] - log(sum_c e^y[j][c]); -Inf for a token outside 0 .. n-1
+ *   entropy[j]      = -sum_c p log p (natural logarithm; p = 0 contributes 0)
+ *   top_idx[j][i], top_logp[j][i], i < top: the columns of the `top` largest logits in descending
+ *                     order and their log probabilities; equal logits (-0 equals +0) by the lower
+ *                     column, a NaN logit above every number.  0 <= top <= 64 and top <= n
+ *                     (W12_ERR_RANGE otherwise); with top = 0 both may be NULL.
+ * -Inf logits (masked tokens) have probability 0.  A row of -Inf alone has no distribution: its
+ * log probabilities are -Inf, its entropy 0, its alternatives columns 0 .. top-1.  A row with a NaN
+ * or +Inf logit gives NaN log probabilities (a token outside 0 .. n-1 still -Inf) and entropy.
+ * All sums are held in float.  scratch: w12_logprobs_scratch bytes of device memory of the caller's
+ * (16-byte aligned; needs no particular contents; NULL when that is 0), in use until the call's
+ * work on `stream` is finished; W12_ERR_CAPACITY if scratch_bytes is smaller.  Calls with
+ * different scratch never touch each other's, on any streams or in any graphs.
+ */
+#define W12_LOGITS_BF16 0x80u
+int w12_logprobs_scratch(int64_t m, int64_t n, int top, uint32_t flags, uint64_t *bytes);
+int w12_logprobs(const void *y, int64_t m, int64_t n, int64_t ldy, const void *tokens, int64_t n_tok,
+                 int top, float *logp, float *entropy, int32_t *top_idx, float *top_logp,
+                 void *scratch, uint64_t scratch_bytes, uint32_t flags, void *stream);
+
+/*
  * w12_bf16_gemm -- same-build dense baseline: y = x * W^T with W bfloat16 in the same tiled
  * storage order as the W12 planes (npad * k values, from w12_bf16_to_tiles), same kernel
  * structure and flags as w12_gemm, 2 bytes per weight.

@@ -547,6 +547,79 @@ int w12_i8_top1(const uint16_t* x, int64_t m, const w12_i8* cp, const w12_weight
   return ok();
 }
 
+int w12_embed(const void* ids, int64_t count, const w12_weight* wt, float scale, void* out, uint32_t flags,
+              void* stream) {
+  int rc = check_record(wt, true);
+  if (rc) return rc;
+  if (!ids || !out) return fail(W12_ERR_ARG, "ids or out is NULL");
+  if (flags & ~(W12_OUT_BF16 | W12_IDS_I64)) return fail(W12_ERR_ARG, "unknown flags 0x%x", flags);
+  if (count <= 0) return fail(W12_ERR_ARG, "count must be positive (count=%lld)", (long long)count);
+  if (count >= kMaxDim) return fail(W12_ERR_RANGE, "count too large");
+  const bool ids64 = (flags & W12_IDS_I64) != 0;
+  if (reinterpret_cast<uintptr_t>(ids) & (ids64 ? 7u : 3u))
+    return fail(W12_ERR_ALIGN, "ids must be naturally aligned");
+  if (!aligned16(out)) return fail(W12_ERR_ALIGN, "out must be 16-byte aligned");
+  hipError_t e = w12::launch_embed(ids, ids64, count, planes_of(wt), wt->n, wt->k, scale, out,
+                                   (flags & W12_OUT_BF16) != 0, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "embedding launch");
+  return ok();
+}
+
+namespace {
+int check_logprobs(int64_t m, int64_t n, int top, uint32_t flags) {
+  if (m <= 0 || n <= 0) return fail(W12_ERR_ARG, "m and n must be positive (m=%lld, n=%lld)", (long long)m, (long long)n);
+  if (m >= kMaxDim || n >= kMaxDim) return fail(W12_ERR_RANGE, "m or n too large");
+  if (top < 0 || top > 64 || top > n) return fail(W12_ERR_RANGE, "top must be 0..64 and at most n (top=%d)", top);
+  if (flags & ~(W12_IDS_I64 | W12_LOGITS_BF16)) return fail(W12_ERR_ARG, "unknown flags 0x%x", flags);
+  return W12_OK;
+}
+}  // namespace
+
+int w12_logprobs_scratch(int64_t m, int64_t n, int top, uint32_t flags, uint64_t* bytes) {
+  if (!bytes) return fail(W12_ERR_ARG, "bytes is NULL");
+  int rc = check_logprobs(m, n, top, flags);
+  if (rc) return rc;
+  w12::DevInfo di;
+  hipError_t e = w12::dev_info(&di);
+  if (e != hipSuccess) return hip_fail(e, "device query");
+  *bytes = w12::logprobs_scratch(di, m, n, top, (flags & W12_LOGITS_BF16) != 0);
+  return ok();
+}
+
+int w12_logprobs(const void* y, int64_t m, int64_t n, int64_t ldy, const void* tokens, int64_t n_tok, int top,
+                 float* logp, float* entropy, int32_t* top_idx, float* top_logp, void* scratch,
+                 uint64_t scratch_bytes, uint32_t flags, void* stream) {
+  int rc = check_logprobs(m, n, top, flags);
+  if (rc) return rc;
+  if (!y || !entropy) return fail(W12_ERR_ARG, "y or entropy is NULL");
+  if (n_tok < 0) return fail(W12_ERR_ARG, "n_tok is negative (%lld)", (long long)n_tok);
+  if (n_tok >= kMaxDim) return fail(W12_ERR_RANGE, "n_tok too large");
+  if (n_tok > 0 && (!tokens || !logp)) return fail(W12_ERR_ARG, "tokens or logp is NULL but n_tok > 0");
+  if (top > 0 && (!top_idx || !top_logp)) return fail(W12_ERR_ARG, "top_idx or top_logp is NULL but top > 0");
+  if (ldy < n) return fail(W12_ERR_ARG, "ldy=%lld is smaller than n=%lld", (long long)ldy, (long long)n);
+  const bool bf = (flags & W12_LOGITS_BF16) != 0, i64 = (flags & W12_IDS_I64) != 0;
+  if (ldy > (int64_t(1) << 40)) return fail(W12_ERR_RANGE, "ldy too large");
+  if (reinterpret_cast<uintptr_t>(y) & (bf ? 1u : 3u)) return fail(W12_ERR_ALIGN, "y must be naturally aligned");
+  if (n_tok > 0 && ((reinterpret_cast<uintptr_t>(tokens) & (i64 ? 7u : 3u)) || !aligned4(logp)))
+    return fail(W12_ERR_ALIGN, "tokens and logp must be naturally aligned");
+  if (!aligned4(entropy) || (top > 0 && (!aligned4(top_idx) || !aligned4(top_logp))))
+    return fail(W12_ERR_ALIGN, "entropy, top_idx and top_logp must be 4-byte aligned");
+  w12::DevInfo di;
+  hipError_t e = w12::dev_info(&di);
+  if (e != hipSuccess) return hip_fail(e, "device query");
+  const uint64_t need = w12::logprobs_scratch(di, m, n, top, bf);
+  if (need > 0) {
+    if (!scratch || scratch_bytes < need)
+      return fail(W12_ERR_CAPACITY, "scratch of %llu bytes is needed (%llu given)", (unsigned long long)need,
+                  scratch ? (unsigned long long)scratch_bytes : 0ull);
+    if (!aligned16(scratch)) return fail(W12_ERR_ALIGN, "scratch must be 16-byte aligned");
+  }
+  e = w12::launch_logprobs(y, bf, m, n, ldy, tokens, i64, (int)n_tok, top, logp, entropy, top_idx, top_logp,
+                           scratch, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "log probabilities launch");
+  return ok();
+}
+
 int w12_bf16_gemm(const uint16_t* x, int64_t m, const uint16_t* w, int64_t n, int64_t k, float* y,
                   uint32_t flags, void* stream) {
   if (!w) return fail(W12_ERR_ARG, "w is NULL");

@@ -135,6 +135,16 @@ hipError_t launch_interleave(const Planes& gate, const Planes& up, int64_t rows,
                              hipStream_t s);
 // 8-bit Q-pass copy of a record: per-row scales, codes in the AE storage order, escaped slots 0
 hipError_t launch_i8_build(const Planes& p, int64_t n, int64_t k, int8_t* q, float* scale, hipStream_t s);
+// out[j] = scale * row ids[j] of the record (bfloat16 or float, [cnt][k]); an id outside 0 .. n-1
+// gives zeros
+hipError_t launch_embed(const void* ids, bool ids64, int64_t cnt, const Planes& p, int64_t n, int64_t k,
+                        float scale, void* out, bool out16, hipStream_t s);
+// log probabilities of tokens [m][nt], entropy and the `top` (0..64) best of rows of logits (float,
+// or bfloat16 with bf); scratch: logprobs_scratch bytes (0: none)
+uint64_t logprobs_scratch(const DevInfo& di, int64_t m, int64_t n, int top, bool bf);
+hipError_t launch_logprobs(const void* y, bool bf, int64_t m, int64_t n, int64_t ldy, const void* tokens,
+                           bool tok64, int nt, int top, float* logp, float* ent, int32_t* tidx,
+                           float* tlogp, void* scratch, hipStream_t s);
 // dense bf16 [n][k] -> tiled storage order (baseline layout)
 hipError_t launch_bf16_tile(const uint16_t* w, int64_t n, int64_t k, uint16_t* out, hipStream_t s);
 // bandwidth probe

@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -26,6 +27,8 @@ W12_ERR_HIP = -6
 PATH_AUTO, PATH_GEMV, PATH_MFMA, PATH_STREAM = 0, 1, 2, 3
 Q8_MIDPOINT = 0x10
 OUT_BF16 = 0x20
+IDS_I64 = 0x40
+LOGITS_BF16 = 0x80
 _PATHS = {None: PATH_AUTO, "auto": PATH_AUTO, "gemv": PATH_GEMV, "mfma": PATH_MFMA, "stream": PATH_STREAM}
 
 
@@ -83,6 +86,14 @@ EXPORTS = {
     "w12_concat_rows": (ctypes.c_int, [ctypes.POINTER(_W12Weight), ctypes.c_int,
                                        ctypes.POINTER(_W12Weight), ctypes.POINTER(ctypes.c_uint64),
                                        ctypes.c_void_p]),
+    "w12_embed": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(_W12Weight), ctypes.c_float,
+                                 ctypes.c_void_p, ctypes.c_uint32, ctypes.c_void_p]),
+    "w12_logprobs_scratch": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_uint32,
+                                            ctypes.POINTER(ctypes.c_uint64)]),
+    "w12_logprobs": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                    ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
+                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                    ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p]),
     "w12_bf16_gemm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                      ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                      ctypes.c_uint32, ctypes.c_void_p]),
@@ -460,6 +471,93 @@ def i8_top1(x: torch.Tensor, cp: I8Copy, out=None):
     c = cp.c_struct()
     return _top1(lambda xp, m, s, ip, vp, fl, st: lib().w12_i8_top1(xp, m, ctypes.byref(c), s, ip, vp, fl, st),
                  x, cp.rec, False, out)
+
+
+def _ids_flag(ids: torch.Tensor, device, what: str):
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError(f"{what} must be a torch tensor")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{what} must be int32 or int64, got {ids.dtype}")
+    if ids.device != device:
+        raise ValueError(f"{what} is on {ids.device}, expected {device}")
+    return IDS_I64 if ids.dtype == torch.int64 else 0
+
+
+def embed(ids: torch.Tensor, wt: W12Weight, scale: float = 1.0, out: torch.Tensor | None = None,
+          out_f32: bool = False):
+    """Embedding lookup: scale * W[ids], W read from its W12 record.  ids: int32 or int64 of any shape
+    on the weights' device; returns [*ids.shape, k] bfloat16 (scale 1: the weight's own bits), or
+    float32 with ``out_f32`` / a float32 ``out``.  An id outside 0 .. n-1 gives a row of zeros."""
+    flag = _ids_flag(ids, wt.device, "ids")
+    shape = (*ids.shape, wt.k)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32 if out_f32 else torch.bfloat16, device=wt.device)
+    else:
+        _check_out(out, shape, (torch.float32, torch.bfloat16), wt.device)
+    if ids.numel() == 0:
+        return out
+    ids = ids.contiguous()
+    s = wt.c_struct()
+    with torch.cuda.device(wt.device):
+        _check(lib().w12_embed(ids.data_ptr(), ids.numel(), ctypes.byref(s), float(scale), out.data_ptr(),
+                               flag | _out_flag(out), _stream_handle(wt.device)))
+    return out
+
+
+class LogProbs(NamedTuple):
+    """Result of logprobs: ``logp`` (the shape of tokens; [m, 0] without), ``entropy`` [m],
+    ``top_index`` int32 [m, top] and ``top_logp`` [m, top], descending."""
+    logp: torch.Tensor
+    entropy: torch.Tensor
+    top_index: torch.Tensor
+    top_logp: torch.Tensor
+
+
+def logprobs(y: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0) -> LogProbs:
+    """Log probabilities of given tokens, entropy and the ``top`` (0..64) best alternatives of rows of
+    logits, in one pass.  y [m, n] float32 or bfloat16 on the GPU, rows at any stride, columns
+    contiguous (others are copied); tokens int32 or int64, [m] or [m, t] (a token outside 0 .. n-1 has
+    log probability -Inf).  Equal logits go by the lower index; a row of -Inf alone gives -Inf and
+    entropy 0; a row with NaN or +Inf gives NaN."""
+    if not isinstance(y, torch.Tensor) or y.dim() != 2 or not y.is_cuda:
+        raise ValueError("y must be a 2-D CUDA tensor")
+    if y.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"y must be float32 or bfloat16, got {y.dtype}")
+    m, n = y.shape
+    top = int(top)
+    if not 0 <= top <= min(64, n):
+        raise ValueError(f"top must be 0..{min(64, n)}, got {top}")
+    if n > 0 and (y.stride(1) != 1 and n > 1 or y.stride(0) < n and m > 1):
+        y = y.contiguous()
+    flags = LOGITS_BF16 if y.dtype == torch.bfloat16 else 0
+    nt = 0
+    if tokens is not None:
+        flags |= _ids_flag(tokens, y.device, "tokens")
+        if tokens.dim() not in (1, 2) or tokens.shape[0] != m:
+            raise ValueError(f"tokens must be [{m}] or [{m}, t], got {tuple(tokens.shape)}")
+        nt = 1 if tokens.dim() == 1 else tokens.shape[1]
+        tokens = tokens.contiguous()
+    f32 = torch.float32
+    r = LogProbs(torch.empty((m, 0) if tokens is None else tokens.shape, dtype=f32, device=y.device),
+                 torch.empty(m, dtype=f32, device=y.device),
+                 torch.empty((m, top), dtype=torch.int32, device=y.device),
+                 torch.empty((m, top), dtype=f32, device=y.device))
+    if m == 0:
+        return r
+    if n == 0:
+        raise ValueError("y has no columns")
+    with torch.cuda.device(y.device):
+        need = ctypes.c_uint64(0)
+        _check(lib().w12_logprobs_scratch(m, n, top, flags, ctypes.byref(need)))
+        # from torch's allocator, so every call in flight and every captured graph has its own
+        scratch = torch.empty(need.value, dtype=torch.uint8, device=y.device) if need.value else None
+        _check(lib().w12_logprobs(y.data_ptr(), m, n, y.stride(0) if m > 1 else n,
+                                  tokens.data_ptr() if nt else None, nt, top,
+                                  r.logp.data_ptr() if nt else None, r.entropy.data_ptr(),
+                                  r.top_index.data_ptr() if top else None,
+                                  r.top_logp.data_ptr() if top else None, _ptr(scratch), need.value, flags,
+                                  _stream_handle(y.device)))
+    return r
 
 
 class Bf16Tiles:

@@ -20,3 +20,4 @@ from .w12 import (  # noqa: F401
     gemm64_f, abs_bound64_f, I8Copy, escaped_mask, i8_copy, i8_weights64, i8_gemm64,
     SILU_GROUP, interleave_rows, silu_rows, silu64, silu_mul64, silu_mul_bound,
 )
+from .vocab import embed_bits, logprobs64, logprobs_tol  # noqa: F401
