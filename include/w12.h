@@ -277,6 +277,50 @@ int w12_i8_top1(const uint16_t *x, int64_t m, const w12_i8 *cp, const w12_weight
                 float *val, uint32_t flags, void *stream);
 
 /*
+ * The microscaled 4-bit copy for the Q pass: block floating point with the element and block sizes
+ * of the OCP microscaling formats (E2M1 elements, blocks of 32 columns, power-of-two scales),
+ * beside a W12 record whose window bottoms and exact escape list it shares; 17/32 byte per weight.
+ * Per block, e = the largest exponent field among its in-window weights (the window bottom for a
+ * block with none), scale 2^(e - 129); an in-window weight becomes the code of the value nearest to
+ * weight / scale among +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}, ties to the even code, larger magnitudes
+ * than 6 to 6; escaped slots hold code 0.  The Q pass then sees scale * value for in-window weights
+ * and the exact value for escapes.
+ * Storage: a record of 1088 bytes per tile of 16 rows x 128 columns, row-tile-major, rows padded
+ * with zero bytes: for row r and column group g (columns 32 g .. +31) of the tile the 32 codes are the
+ * 16 bytes at 16 (r + 16 g), column 2 i in the low and 2 i + 1 in the high nibble of byte i (sign in
+ * bit 3), and the scale is the byte e - 2 - base + 112 (110..125) at 1024 + r + 16 g.
+ */
+typedef struct w12_mx4 {
+    int64_t  n;        /* rows of W (must equal the record's)    */
+    int64_t  k;        /* columns of W (must equal the record's) */
+    uint8_t *q;        /* [npad * k * 17 / 32] tile records (device, 16-byte aligned) */
+} w12_mx4;
+
+/*
+ * w12_mx4_build -- the 4-bit copy of record `wt` into the caller's out->q (out->n, out->k set by the
+ * caller to the record's).  Reads the planes and the escape columns.  Enqueued on `stream`, no
+ * synchronisation.
+ */
+int w12_mx4_build(const w12_weight *wt, w12_mx4 *out, void *stream);
+
+/*
+ * w12_mx4_decode -- the bfloat16 matrix [n, k] (device, row-major) the Q pass on the copy multiplies:
+ * scale * value at in-window slots (exact in bfloat16), the record's own bits at escaped ones.  Reads
+ * cp->q and wt's base and escape arrays (wt->ae and wt->lo may be NULL).
+ */
+int w12_mx4_decode(const w12_mx4 *cp, const w12_weight *wt, uint16_t *w_out, void *stream);
+
+/*
+ * w12_mx4_gemm / w12_mx4_top1 -- the Q pass on the 4-bit copy and its top-1 per row of x, as
+ * w12_i8_gemm and w12_i8_top1 (same x, outputs, flags, kernel families, workspace and error bound,
+ * against the weights w12_mx4_decode gives).  Read cp->q and wt's base and escape arrays.
+ */
+int w12_mx4_gemm(const uint16_t *x, int64_t m, const w12_mx4 *cp, const w12_weight *wt, float *y,
+                 uint32_t flags, void *stream);
+int w12_mx4_top1(const uint16_t *x, int64_t m, const w12_mx4 *cp, const w12_weight *wt, int32_t *idx,
+                 float *val, uint32_t flags, void *stream);
+
+/*
  * w12_concat_rows -- the record of W = [W_0; W_1; ...; W_{count-1}] (the parts' rows stacked in
  * order) built on the device from the parts' records, without decoding or re-encoding.  Windows
  * and escape lists are per output row (figure-captions page, Fig. 5(a)), so the stacked record is

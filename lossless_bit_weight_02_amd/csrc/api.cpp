@@ -285,6 +285,32 @@ w12::Planes planes_i8(const w12_i8* cp, const w12_weight* wt) {
   p.scale = cp->scale;
   return p;
 }
+
+// The 4-bit copy and the record whose window bottoms and escape list it shares.
+int check_mx4(const w12_mx4* cp, const w12_weight* wt) {
+  if (!cp || !wt) return fail(W12_ERR_ARG, "the 4-bit copy or the record is NULL");
+  int rc = check_nk(wt->n, wt->k);
+  if (rc) return rc;
+  if (cp->n != wt->n || cp->k != wt->k)
+    return fail(W12_ERR_ARG, "the 4-bit copy is [%lld, %lld], the record [%lld, %lld]", (long long)cp->n,
+                (long long)cp->k, (long long)wt->n, (long long)wt->k);
+  if (!cp->q || !wt->base || !wt->esc_ptr) return fail(W12_ERR_ARG, "q, base or esc_ptr is NULL");
+  if (wt->esc_cap > 0 && (!wt->esc_col || !wt->esc_val))
+    return fail(W12_ERR_ARG, "escape arrays are NULL but esc_cap > 0");
+  if (!aligned16(cp->q)) return fail(W12_ERR_ALIGN, "q must be 16-byte aligned");
+  if (!aligned4(wt->esc_ptr) || (wt->esc_col && !aligned4(wt->esc_col)) ||
+      (wt->esc_val && (reinterpret_cast<uintptr_t>(wt->esc_val) & 1u)))
+    return fail(W12_ERR_ALIGN, "escape arrays must be naturally aligned");
+  return W12_OK;
+}
+
+w12::Planes planes_mx4(const w12_mx4* cp, const w12_weight* wt) {
+  w12::Planes p = planes_of(wt);
+  p.ae = nullptr;
+  p.lo = nullptr;
+  p.mx4 = cp->q;
+  return p;
+}
 }  // namespace
 
 extern "C" {
@@ -542,6 +568,54 @@ int w12_i8_top1(const uint16_t* x, int64_t m, const w12_i8* cp, const w12_weight
   if (!aligned16(x)) return fail(W12_ERR_ALIGN, "x must be 16-byte aligned");
   if (!aligned4(idx) || !aligned4(val)) return fail(W12_ERR_ALIGN, "idx and val must be 4-byte aligned");
   hipError_t e = launch_top1_auto(w12::kFmtI8, x, m, planes_i8(cp, wt), wt->n, wt->k, idx, val,
+                                  reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "top-1 launch");
+  return ok();
+}
+
+int w12_mx4_build(const w12_weight* wt, w12_mx4* out, void* stream) {
+  int rc = check_record(wt, true);
+  if (rc) return rc;
+  if (!out) return fail(W12_ERR_ARG, "out is NULL");
+  if (out->n != wt->n || out->k != wt->k)
+    return fail(W12_ERR_ARG, "out is [%lld, %lld], the record [%lld, %lld]", (long long)out->n,
+                (long long)out->k, (long long)wt->n, (long long)wt->k);
+  if (!out->q) return fail(W12_ERR_ARG, "out->q is NULL");
+  if (!aligned16(out->q)) return fail(W12_ERR_ALIGN, "q must be 16-byte aligned");
+  hipError_t e = w12::launch_mx4_build(planes_of(wt), wt->n, wt->k, out->q, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "4-bit copy launch");
+  return ok();
+}
+
+int w12_mx4_decode(const w12_mx4* cp, const w12_weight* wt, uint16_t* w_out, void* stream) {
+  int rc = check_mx4(cp, wt);
+  if (rc) return rc;
+  if (!w_out) return fail(W12_ERR_ARG, "w_out is NULL");
+  if (!aligned16(w_out)) return fail(W12_ERR_ALIGN, "w_out must be 16-byte aligned");
+  hipError_t e = w12::launch_mx4_decode(planes_mx4(cp, wt), wt->n, wt->k, w_out, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "4-bit decode launch");
+  return ok();
+}
+
+int w12_mx4_gemm(const uint16_t* x, int64_t m, const w12_mx4* cp, const w12_weight* wt, float* y,
+                 uint32_t flags, void* stream) {
+  int rc = check_mx4(cp, wt);
+  if (rc) return rc;
+  if (flags & W12_Q8_MIDPOINT) return fail(W12_ERR_ARG, "W12_Q8_MIDPOINT does not apply to the 4-bit copy");
+  return run_gemm(w12::kFmtMX4, x, m, planes_mx4(cp, wt), wt->n, wt->k, y, flags, stream);
+}
+
+int w12_mx4_top1(const uint16_t* x, int64_t m, const w12_mx4* cp, const w12_weight* wt, int32_t* idx,
+                 float* val, uint32_t flags, void* stream) {
+  int rc = check_mx4(cp, wt);
+  if (rc) return rc;
+  if (!x || !idx || !val) return fail(W12_ERR_ARG, "x, idx or val is NULL");
+  if (flags != 0) return fail(W12_ERR_ARG, "unknown flags 0x%x", flags);
+  if (m <= 0) return fail(W12_ERR_ARG, "m must be positive (m=%lld)", (long long)m);
+  if (m >= kMaxDim) return fail(W12_ERR_RANGE, "m too large");
+  if (!aligned16(x)) return fail(W12_ERR_ALIGN, "x must be 16-byte aligned");
+  if (!aligned4(idx) || !aligned4(val)) return fail(W12_ERR_ALIGN, "idx and val must be 4-byte aligned");
+  hipError_t e = launch_top1_auto(w12::kFmtMX4, x, m, planes_mx4(cp, wt), wt->n, wt->k, idx, val,
                                   reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "top-1 launch");
   return ok();

@@ -3,6 +3,7 @@
 // a row's four column-group lanes.
 #pragma once
 
+#include "mx4_device.hpp"
 #include "w12_device.hpp"
 #include "w12_launch.hpp"
 
@@ -12,6 +13,11 @@ namespace w12 {
 template <int FMT>
 struct BlockRegs {
   u32x4 v[FMT == kFmtBF16 ? 4 : FMT == kFmtW12 ? 3 : 2];
+};
+template <>
+struct BlockRegs<kFmtMX4> {
+  u32x4 v;          // 32 codes
+  uint32_t s;       // their scale byte
 };
 
 // Buffers over one tile's blocks of the planes (or the dense baseline); an absent tile reads zeros.
@@ -29,6 +35,9 @@ __device__ __forceinline__ void load_block(const TileRsrc<FMT>& t, uint32_t kb, 
     const uint32_t off = kb == ~0u ? kOOB : kb * kTileBF + lane16;
 #pragma unroll
     for (int q = 0; q < 4; ++q) r.v[q] = __builtin_amdgcn_raw_buffer_load_b128(t.r0, off + 1024 * q, 0, kAuxNT);
+  } else if constexpr (FMT == kFmtMX4) {
+    r.v = __builtin_amdgcn_raw_buffer_load_b128(t.r0, kb == ~0u ? kOOB : kb * kTileMX + lane16, 0, kAuxNT);
+    r.s = __builtin_amdgcn_raw_buffer_load_b8(t.r0, kb == ~0u ? kOOB : kb * kTileMX + 1024 + lane16 / 16, 0, kAuxNT);
   } else {
     const uint32_t off = kb == ~0u ? kOOB : kb * kTileAE + lane16;
     r.v[0] = __builtin_amdgcn_raw_buffer_load_b128(t.r0, off, 0, kAuxNT);
@@ -51,6 +60,8 @@ __device__ __forceinline__ void block_pairs(const BlockRegs<FMT>& r, uint32_t e1
     window_group8(r.v[0].z, r.v[0].w, r.v[2].y, e112, p + 4);
     window_group8(r.v[1].x, r.v[1].y, r.v[2].z, e112, p + 8);
     window_group8(r.v[1].z, r.v[1].w, r.v[2].w, e112, p + 12);
+  } else if constexpr (FMT == kFmtMX4) {
+    mx4_pairs(r.v, r.s, p);
   } else if constexpr (FMT == kFmtI8) {
     i8_group16(r.v[0], p);
     i8_group16(r.v[1], p + 8);

@@ -50,6 +50,7 @@ struct GemvArgs {
   const uint16_t* esc_val;
   const uint16_t* w;      // dense bfloat16 W (baseline), tiled storage
   const float* scale;     // per-row scale of the 8-bit copy (its codes are in `ae`)
+  const uint8_t* mx4;     // tile records of the 4-bit copy
   float* y;               // y[m][ldy]; with splits > 1, range j writes y + j * ysplit
   int64_t ldy;
   int64_t n, k;           // rows of W, row length
@@ -70,6 +71,9 @@ __device__ __forceinline__ TileRsrc<FMT> tile_rsrc(const GemvArgs& a, int64_t ti
   const int64_t t0 = valid ? tile : 0;
   if constexpr (FMT == kFmtBF16) {
     t.r0 = make_rsrc(a.w + t0 * ktiles * (kTileBF / 2), valid ? ktiles * (uint32_t)kTileBF : 0u);
+    t.r1 = t.r0;
+  } else if constexpr (FMT == kFmtMX4) {
+    t.r0 = make_rsrc(a.mx4 + t0 * ktiles * kTileMX, valid ? ktiles * (uint32_t)kTileMX : 0u);
     t.r1 = t.r0;
   } else {
     t.r0 = make_rsrc(a.ae + t0 * ktiles * kTileAE, valid ? ktiles * (uint32_t)kTileAE : 0u);
@@ -368,6 +372,7 @@ static GemvKernel pick_kernel(Fmt f, int m, bool few) {
   if (f == kFmtQ8) return pick<kFmtQ8>(m, few);
   if (f == kFmtQ8M) return pick<kFmtQ8M>(m, few);
   if (f == kFmtI8) return pick<kFmtI8>(m, few);
+  if (f == kFmtMX4) return pick<kFmtMX4>(m, few);
   return pick<kFmtBF16>(m, few);
 }
 
@@ -425,6 +430,7 @@ hipError_t launch_gemv(Fmt f, const uint16_t* x, int64_t m, const Planes& p, int
     a.esc_ptr = p.esc_ptr; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
     a.w = p.w;
     a.scale = p.scale;
+    a.mx4 = p.mx4;
     a.ldy = n;
     a.n = n; a.k = k;
     a.x = x + m0 * k;

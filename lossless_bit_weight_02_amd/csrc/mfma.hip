@@ -212,6 +212,9 @@ void k_mfma(MfmaArgs a) {
     if constexpr (FMT == kFmtBF16) {
       ra = make_rsrc(a.w + row0 * a.k + (int64_t)kb0 * (kTileBF / 2), valid ? nkb * (uint32_t)kTileBF : 0u);
       rl = ra;
+    } else if constexpr (FMT == kFmtMX4) {
+      ra = make_rsrc(a.mx4 + (row0 / kTileRows * (int64_t)KB + kb0) * kTileMX, valid ? nkb * (uint32_t)kTileMX : 0u);
+      rl = ra;
     } else {
       ra = make_rsrc(a.ae + row0 * a.k + (int64_t)kb0 * kTileAE, valid ? nkb * (uint32_t)kTileAE : 0u);
       rl = make_rsrc(a.lo + row0 * a.k / 2 + (int64_t)kb0 * kTileLO, valid ? nkb * (uint32_t)kTileLO : 0u);
@@ -631,6 +634,7 @@ static MfmaKernel pick_top1(Fmt f, int nt) {
   if (f == kFmtW12) return nt == 1 ? k_mfma<kFmtW12, 1, kWaves, true> : k_mfma<kFmtW12, 2, kWaves, true>;
   if (f == kFmtQ8M) return nt == 1 ? k_mfma<kFmtQ8M, 1, kWaves, true> : k_mfma<kFmtQ8M, 2, kWaves, true>;
   if (f == kFmtI8) return nt == 1 ? k_mfma<kFmtI8, 1, kWaves, true> : k_mfma<kFmtI8, 2, kWaves, true>;
+  if (f == kFmtMX4) return nt == 1 ? k_mfma<kFmtMX4, 1, kWaves, true> : k_mfma<kFmtMX4, 2, kWaves, true>;
   return nt == 1 ? k_mfma<kFmtQ8, 1, kWaves, true> : k_mfma<kFmtQ8, 2, kWaves, true>;
 }
 
@@ -649,6 +653,7 @@ static MfmaKernel pick_kernel(Fmt f, int nt, int waves, bool silu) {
   if (f == kFmtQ8) return pick<kFmtQ8, 12>(nt);
   if (f == kFmtQ8M) return pick<kFmtQ8M, 12>(nt);
   if (f == kFmtI8) return pick<kFmtI8, 12>(nt);
+  if (f == kFmtMX4) return pick<kFmtMX4, 12>(nt);
   return pick<kFmtBF16, 12>(nt);
 }
 
@@ -704,6 +709,7 @@ static hipError_t mfma_pass(Fmt f, const DevInfo& di, const uint16_t* x, int mb,
   a.esc_ptr = p.esc_ptr; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
   a.w = p.w;
   a.scale = p.scale;
+  a.mx4 = p.mx4;
   a.y = ws ? ws : y.f;
   a.y16 = ws ? nullptr : y.h;
   const bool silu = !ws && y.silu;             // a split pairs the outputs in its sum instead
@@ -817,6 +823,7 @@ hipError_t launch_mfma_top1(Fmt f, const uint16_t* x, int64_t m, const Planes& p
     a.esc_ptr = p.esc_ptr; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
     a.w = p.w;
     a.scale = p.scale;
+  a.mx4 = p.mx4;
     a.y = nullptr;
     a.y16 = nullptr;
     a.ldy = nh;

@@ -9,6 +9,7 @@
 // pairs A columns 32 g + 8 t .. +7 with the same columns of x.
 #pragma once
 
+#include "mx4_device.hpp"
 #include "w12_device.hpp"
 #include "w12_launch.hpp"
 
@@ -25,6 +26,7 @@ struct MfmaArgs {
   const uint16_t* esc_val;
   const uint16_t* w;   // dense bfloat16 W (baseline), tiled storage
   const float* scale;  // per-row scale of the 8-bit copy (its codes are in `ae`)
+  const uint8_t* mx4;  // tile records of the 4-bit copy
   float* y;            // y[m][ldy]; with splits > 1, split j writes y + j * ysplit
   int64_t ldy;
   int64_t n, k;
@@ -61,6 +63,11 @@ template <int FMT>
 struct ABlock {
   u32x4 v[FMT == kFmtBF16 ? 4 : FMT == kFmtW12 ? 3 : 2];
 };
+template <>
+struct ABlock<kFmtMX4> {
+  u32x4 v;          // 32 codes
+  uint32_t s;       // their scale byte
+};
 
 // Block kb of the wave's tile; offsets past the tile's range read zeros.
 template <int FMT>
@@ -70,6 +77,9 @@ __device__ __forceinline__ void load_ablock(Rsrc r0, Rsrc r1, uint32_t kb, uint3
     const uint32_t off = kb * kTileBF + lane16;
 #pragma unroll
     for (int q = 0; q < 4; ++q) b.v[q] = __builtin_amdgcn_raw_buffer_load_b128(r0, off + 1024 * q, 0, kAuxNT);
+  } else if constexpr (FMT == kFmtMX4) {
+    b.v = __builtin_amdgcn_raw_buffer_load_b128(r0, kb * kTileMX + lane16, 0, kAuxNT);
+    b.s = __builtin_amdgcn_raw_buffer_load_b8(r0, kb * kTileMX + 1024 + lane16 / 16, 0, kAuxNT);
   } else {
     const uint32_t off = kb * kTileAE + lane16;
     b.v[0] = __builtin_amdgcn_raw_buffer_load_b128(r0, off, 0, kAuxNT);
@@ -91,6 +101,8 @@ __device__ __forceinline__ void ablock_pairs(const ABlock<FMT>& r, uint32_t e112
     window_group8(r.v[0].z, r.v[0].w, r.v[2].y, e112, p + 4);
     window_group8(r.v[1].x, r.v[1].y, r.v[2].z, e112, p + 8);
     window_group8(r.v[1].z, r.v[1].w, r.v[2].w, e112, p + 12);
+  } else if constexpr (FMT == kFmtMX4) {
+    mx4_pairs(r.v, r.s, p);
   } else if constexpr (FMT == kFmtI8) {
     i8_group16(r.v[0], p);
     i8_group16(r.v[1], p + 8);

@@ -1,0 +1,145 @@
+// The microscaled 4-bit copy of a W12 record for the Q pass (SpecPilot, arXiv 2611.02501, summary
+// page, Main Findings: the RTX PRO 6000 port reads a separate low-bit copy in the Q pass; the pages
+// give no quantiser).  It is block floating point with 4-bit elements, the element and block sizes
+// of the OCP microscaling formats:
+//   a block is 32 columns of a row; e = the largest exponent field among the block's in-window
+//   weights (the window bottom for a block with none), scale 2^(e - 127 - 2);
+//   an in-window weight becomes the E2M1 code (sign, 2 exponent bits, 1 mantissa bit: magnitudes 0,
+//   0.5, 1, 1.5, 2, 3, 4, 6) nearest to weight / scale, ties to the even code, saturating at 6;
+//   escaped slots hold code 0 and stay exact through the record's escape list.
+// The scale is stored as the exponent field the decoded weight w' = w / 2^(base - 112) needs
+// (w12_device.hpp), s = e - 2 - base + 112 in 110..125, so decoding never leaves the normal range
+// and the GEMMs finish a row with the same 2^(base - 112) as the exact pass.
+//
+// Storage: one tile record of 1088 bytes per 16 rows x 128 columns, row-tile-major.  Lane
+// l = r + 16 g of a wave owns row r, columns 32 g .. 32 g + 31 -- one block: its 32 codes are the 16
+// bytes at 16 l (column 2 i in the low nibble of byte i), its scale the byte at 1024 + l.
+#include "mx4_device.hpp"
+#include "w12_launch.hpp"
+
+namespace w12 {
+
+// One wave per tile: lane l decodes its block's 32 window values, takes their largest exponent
+// (an escaped slot's placeholder has the window's lowest, so it never raises it and stands for a
+// block without weights), and converts.  Rows past n get zeros.
+__global__ __launch_bounds__(kBlock) void k_mx4_build(const uint8_t* __restrict__ ae,
+                                                      const uint8_t* __restrict__ lo, int64_t n, int64_t k,
+                                                      uint8_t* __restrict__ q) {
+  const int lane = threadIdx.x & 63;
+  const int64_t ktiles = k / kTileCols;
+  const int64_t tiles = (n + kTileRows - 1) / kTileRows * ktiles;
+  const uint32_t e112 = exp112_pair();
+  const int64_t step = (int64_t)gridDim.x * (kBlock / 64);
+  for (int64_t t = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6); t < tiles; t += step) {
+    const bool live = t / ktiles * kTileRows + (lane & 15) < n;
+    const u32x4 a0 = load_nt(reinterpret_cast<const u32x4*>(ae + t * kTileAE + 16 * lane));
+    const u32x4 a1 = load_nt(reinterpret_cast<const u32x4*>(ae + t * kTileAE + 1024 + 16 * lane));
+    const u32x4 b = load_nt(reinterpret_cast<const u32x4*>(lo + t * kTileLO + 16 * lane));
+    uint32_t p[16];
+    window_group8(a0.x, a0.y, b.x, e112, p);
+    window_group8(a0.z, a0.w, b.y, e112, p + 4);
+    window_group8(a1.x, a1.y, b.z, e112, p + 8);
+    window_group8(a1.z, a1.w, b.w, e112, p + 12);
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t l16 = p[i] & 0x7F80u, h16 = (p[i] >> 16) & 0x7F80u;
+      big = big > l16 ? big : l16;
+      big = big > h16 ? big : h16;
+    }
+    const uint32_t s = (big >> 7) - 2u;
+    const float scale = __uint_as_float(s << 23);
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = mx4_encode8(p + 4 * i, scale);
+    if (!live) o = (u32x4){0u, 0u, 0u, 0u};
+    uint8_t* dst = q + t * kTileMX;
+    *reinterpret_cast<u32x4*>(dst + 16 * lane) = o;
+    dst[1024 + lane] = live ? (uint8_t)s : (uint8_t)0;
+  }
+}
+
+// Code 0 at every escaped slot.  Two escapes may share a byte: each clears its nibble of the
+// 32-bit word atomically (an AND: the result does not depend on the order).
+__global__ __launch_bounds__(kBlock) void k_mx4_zero_escapes(const uint32_t* __restrict__ esc_ptr,
+                                                             const uint32_t* __restrict__ esc_col, int64_t n,
+                                                             int64_t k, uint8_t* __restrict__ q) {
+  const int lane = threadIdx.x & 63;
+  const int64_t ktiles = k / kTileCols;
+  const int64_t nw = (int64_t)gridDim.x * (kBlock / 64);
+  for (int64_t row = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6); row < n; row += nw) {
+    const uint32_t e1 = esc_ptr[row + 1];
+    const int64_t r = row % kTileRows;
+    for (uint32_t e = esc_ptr[row] + lane; e < e1; e += 64) {
+      const int64_t c = esc_col[e], cc = c % kTileCols;
+      const int64_t t = (row / kTileRows) * ktiles + c / kTileCols;
+      const int j = (int)(cc % 32);                // column within the block: nibble j
+      uint32_t* word = reinterpret_cast<uint32_t*>(q + t * kTileMX + 16 * (r + 16 * (cc / 32))) + j / 8;
+      atomicAnd(word, ~(0xFu << (4 * (j % 8))));
+    }
+  }
+}
+
+// The bfloat16 matrix the Q pass multiplies (escaped slots get their values from a second kernel).
+// One wave per tile; w' times 2^(base - 112) is exact in bfloat16 (at the lowest windows as a
+// subnormal), so the high half of the float product is the value.
+__global__ __launch_bounds__(kBlock) void k_mx4_decode(const uint8_t* __restrict__ q,
+                                                       const uint8_t* __restrict__ base, int64_t n, int64_t k,
+                                                       uint16_t* __restrict__ out) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int64_t ktiles = k / kTileCols;
+  const int64_t tiles = (n + kTileRows - 1) / kTileRows * ktiles;
+  const int64_t step = (int64_t)gridDim.x * (kBlock / 64);
+  for (int64_t t = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6); t < tiles; t += step) {
+    const int64_t tr = t / ktiles, row = tr * kTileRows + r;
+    const u32x4 v = load_nt(reinterpret_cast<const u32x4*>(q + t * kTileMX + 16 * lane));
+    const uint32_t s = q[t * kTileMX + 1024 + lane];
+    if (row >= n) continue;
+    const float rs = window_scale(base[row]);
+    uint32_t p[16];
+    mx4_pairs(v, s, p);
+    u32x4* dst = reinterpret_cast<u32x4*>(out + row * k + (t - tr * ktiles) * kTileCols + 32 * g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u32x4 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = p[4 * i + j];
+        const uint32_t f0 = __float_as_uint(bf16_to_float(w & 0xFFFFu) * rs);
+        const uint32_t f1 = __float_as_uint(__uint_as_float(w & 0xFFFF0000u) * rs);
+        o[j] = __builtin_amdgcn_perm(f1, f0, 0x07060302u);
+      }
+      dst[i] = o;
+    }
+  }
+}
+
+static unsigned mx4_grid(const DevInfo& di, int64_t waves) {
+  const int64_t blocks = (waves + 3) / 4, cap = (int64_t)di.cus * 32;
+  return (unsigned)(blocks < cap ? blocks : cap);
+}
+
+hipError_t launch_mx4_build(const Planes& p, int64_t n, int64_t k, uint8_t* q, hipStream_t s) {
+  DevInfo di;
+  hipError_t err = dev_info(&di);
+  if (err != hipSuccess) return err;
+  const int64_t tiles = (n + kTileRows - 1) / kTileRows * (k / kTileCols);
+  hipLaunchKernelGGL(k_mx4_build, dim3(mx4_grid(di, tiles)), dim3(kBlock), 0, s, p.ae, p.lo, n, k, q);
+  err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(k_mx4_zero_escapes, dim3(mx4_grid(di, n)), dim3(kBlock), 0, s, p.esc_ptr, p.esc_col, n, k, q);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_decode(const Planes& p, int64_t n, int64_t k, uint16_t* out, hipStream_t s) {
+  DevInfo di;
+  hipError_t err = dev_info(&di);
+  if (err != hipSuccess) return err;
+  const int64_t tiles = (n + kTileRows - 1) / kTileRows * (k / kTileCols);
+  hipLaunchKernelGGL(k_mx4_decode, dim3(mx4_grid(di, tiles)), dim3(kBlock), 0, s, p.mx4, p.base, n, k, out);
+  err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  return launch_escape_scatter(p, n, k, out, s);
+}
+
+}  // namespace w12

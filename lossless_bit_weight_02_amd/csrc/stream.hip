@@ -52,6 +52,7 @@ struct StreamArgs {
   const uint16_t* esc_val;
   const uint16_t* w;
   const float* scale;
+  const uint8_t* mx4;
   float* y;               // y[m][ldy] (or y16)
   uint16_t* y16;
   int64_t ldy;
@@ -75,6 +76,9 @@ __device__ __forceinline__ TileRsrc<FMT> stream_rsrc(const StreamArgs& a, int64_
   const int64_t t0 = valid ? tile : 0;
   if constexpr (FMT == kFmtBF16) {
     t.r0 = make_rsrc(a.w + t0 * nkb * (kTileBF / 2), valid ? nkb * (uint32_t)kTileBF : 0u);
+    t.r1 = t.r0;
+  } else if constexpr (FMT == kFmtMX4) {
+    t.r0 = make_rsrc(a.mx4 + t0 * nkb * kTileMX, valid ? nkb * (uint32_t)kTileMX : 0u);
     t.r1 = t.r0;
   } else {
     t.r0 = make_rsrc(a.ae + t0 * nkb * kTileAE, valid ? nkb * (uint32_t)kTileAE : 0u);
@@ -629,6 +633,7 @@ static StreamKernel stream_kernel(Fmt f, int mr, int ft) {
   if (f == kFmtQ8) return stream_pick<kFmtQ8>(mr, ft);
   if (f == kFmtQ8M) return stream_pick<kFmtQ8M>(mr, ft);
   if (f == kFmtI8) return stream_pick<kFmtI8>(mr, ft);
+  if (f == kFmtMX4) return stream_pick<kFmtMX4>(mr, ft);
   return stream_pick<kFmtBF16>(mr, ft);
 }
 
@@ -751,6 +756,7 @@ hipError_t launch_stream(Fmt f, const uint16_t* x, int64_t m, const Planes& p, i
     a.esc_ptr = p.esc_ptr; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
     a.w = p.w;
     a.scale = p.scale;
+    a.mx4 = p.mx4;
     const YOut yp = y + m0 * n;
     a.y = yp.f;
     a.y16 = yp.h;

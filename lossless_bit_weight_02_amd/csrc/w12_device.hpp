@@ -95,9 +95,9 @@ constexpr float kPlaceholderMid = 3.24249267578125e-05f;
 template <int FMT>
 constexpr float placeholder_of() { return FMT == 3 ? kPlaceholderMid : kPlaceholder; }
 // Whether an escaped slot contributes a placeholder that the escape patch must take back out:
-// every format but the 8-bit copy (format 4), whose escaped slots hold the code 0.
+// every format but the 8-bit and 4-bit copies (formats 4, 5), whose escaped slots hold the code 0.
 template <int FMT>
-constexpr bool has_placeholder() { return FMT != 4; }
+constexpr bool has_placeholder() { return FMT != 4 && FMT != 5; }
 
 // Sixteen signed 8-bit codes (one 128-bit word, columns in order) -> eight dwords of bfloat16
 // pairs (c0, c1) (c2, c3) ...: each code converts exactly to float (a sign-extended byte select),

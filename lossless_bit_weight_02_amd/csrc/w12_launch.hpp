@@ -8,8 +8,9 @@ namespace w12 {
 
 // kFmtQ8M: the Q pass with the dropped B nibble read as 8 (the midpoint of its 16 values);
 // kFmtI8: the Q pass on the separate 8-bit copy (int8 codes in the AE plane's storage order, one
-// float scale per row, escapes exact from the record's list)
-enum Fmt : int { kFmtW12 = 0, kFmtQ8 = 1, kFmtBF16 = 2, kFmtQ8M = 3, kFmtI8 = 4 };
+// float scale per row, escapes exact from the record's list); kFmtMX4: the Q pass on the microscaled
+// 4-bit copy (mx4.hip), escapes and window bottoms from the record
+enum Fmt : int { kFmtW12 = 0, kFmtQ8 = 1, kFmtBF16 = 2, kFmtQ8M = 3, kFmtI8 = 4, kFmtMX4 = 5 };
 
 struct DevInfo {
   int device = -1;
@@ -96,6 +97,7 @@ struct Planes {
   const uint16_t* esc_val = nullptr;
   const uint16_t* w = nullptr;  // kFmtBF16 only: the dense bfloat16 weight, tiled storage order
   const float* scale = nullptr; // kFmtI8 only: per-row scale (the codes are in `ae`)
+  const uint8_t* mx4 = nullptr; // kFmtMX4 only: the copy's tile records
 };
 
 // The record's rows r0 .. n as a record of their own (r0 a multiple of 16; escape offsets stay
@@ -108,6 +110,7 @@ inline Planes rows_from(const Planes& p, int64_t r0, int64_t k) {
   if (t.esc_ptr) t.esc_ptr += r0;
   if (t.w) t.w += r0 * k;
   if (t.scale) t.scale += r0;
+  if (t.mx4) t.mx4 += r0 * k / 32 * 17;   // 1088 bytes per 16 x 128 tile
   return t;
 }
 
@@ -135,6 +138,12 @@ hipError_t launch_interleave(const Planes& gate, const Planes& up, int64_t rows,
                              hipStream_t s);
 // 8-bit Q-pass copy of a record: per-row scales, codes in the AE storage order, escaped slots 0
 hipError_t launch_i8_build(const Planes& p, int64_t n, int64_t k, int8_t* q, float* scale, hipStream_t s);
+// every escape's value over its slot of the dense matrix out [n][k]
+hipError_t launch_escape_scatter(const Planes& p, int64_t n, int64_t k, uint16_t* out, hipStream_t s);
+// microscaled 4-bit copy of a record (padded_rows(n) * k * 17 / 32 bytes), and the bfloat16 matrix it
+// stands for (p.mx4, p.base, escapes)
+hipError_t launch_mx4_build(const Planes& p, int64_t n, int64_t k, uint8_t* q, hipStream_t s);
+hipError_t launch_mx4_decode(const Planes& p, int64_t n, int64_t k, uint16_t* out, hipStream_t s);
 // out[j] = scale * row ids[j] of the record (bfloat16 or float, [cnt][k]); an id outside 0 .. n-1
 // gives zeros
 hipError_t launch_embed(const void* ids, bool ids64, int64_t cnt, const Planes& p, int64_t n, int64_t k,

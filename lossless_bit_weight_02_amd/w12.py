@@ -50,6 +50,10 @@ class _W12I8(ctypes.Structure):
                 ("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
+class _W12MX4(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("q", ctypes.c_void_p)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -86,6 +90,15 @@ EXPORTS = {
     "w12_concat_rows": (ctypes.c_int, [ctypes.POINTER(_W12Weight), ctypes.c_int,
                                        ctypes.POINTER(_W12Weight), ctypes.POINTER(ctypes.c_uint64),
                                        ctypes.c_void_p]),
+    "w12_mx4_build": (ctypes.c_int, [ctypes.POINTER(_W12Weight), ctypes.POINTER(_W12MX4), ctypes.c_void_p]),
+    "w12_mx4_decode": (ctypes.c_int, [ctypes.POINTER(_W12MX4), ctypes.POINTER(_W12Weight), ctypes.c_void_p,
+                                      ctypes.c_void_p]),
+    "w12_mx4_gemm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(_W12MX4),
+                                    ctypes.POINTER(_W12Weight), ctypes.c_void_p, ctypes.c_uint32,
+                                    ctypes.c_void_p]),
+    "w12_mx4_top1": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(_W12MX4),
+                                    ctypes.POINTER(_W12Weight), ctypes.c_void_p, ctypes.c_void_p,
+                                    ctypes.c_uint32, ctypes.c_void_p]),
     "w12_embed": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(_W12Weight), ctypes.c_float,
                                  ctypes.c_void_p, ctypes.c_uint32, ctypes.c_void_p]),
     "w12_logprobs_scratch": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_uint32,
@@ -470,6 +483,72 @@ def i8_top1(x: torch.Tensor, cp: I8Copy, out=None):
     """Top-1 of the Q pass on the 8-bit copy per row of x: (index int32 [m], value float32 [m])."""
     c = cp.c_struct()
     return _top1(lambda xp, m, s, ip, vp, fl, st: lib().w12_i8_top1(xp, m, ctypes.byref(c), s, ip, vp, fl, st),
+                 x, cp.rec, False, out)
+
+
+class Mx4Copy:
+    """The microscaled 4-bit Q-pass copy of a W12 record: tile records of 32-column blocks (layout of
+    include/w12.h); it shares ``rec``'s window bottoms and escape list."""
+
+    def __init__(self, rec: W12Weight, q):
+        self.rec, self.q = rec, q
+        self.n, self.k = rec.n, rec.k
+
+    @property
+    def device(self):
+        return self.q.device
+
+    def nbytes(self) -> int:
+        return self.q.numel()
+
+    def c_struct(self) -> _W12MX4:
+        return _W12MX4(self.n, self.k, self.q.data_ptr())
+
+    def to_numpy(self) -> dict:
+        return dict(q_s=self.q.cpu().numpy())
+
+
+def mx4_build(rec: W12Weight) -> Mx4Copy:
+    """The microscaled 4-bit Q-pass copy of ``rec`` (blocks of 32 columns, power-of-two scales, E2M1 codes
+    rounded to nearest even, escaped slots 0), built on the device."""
+    q = torch.empty(padded_rows(rec.n) * rec.k // 32 * 17, dtype=torch.uint8, device=rec.device)
+    cp = Mx4Copy(rec, q)
+    s, c = rec.c_struct(), cp.c_struct()
+    _check(lib().w12_mx4_build(ctypes.byref(s), ctypes.byref(c), _stream_handle(rec.device)))
+    return cp
+
+
+def mx4_decode(cp: Mx4Copy, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The bfloat16 matrix [n, k] the Q pass on the copy multiplies (escaped slots exact)."""
+    if out is None:
+        out = torch.empty((cp.n, cp.k), dtype=torch.bfloat16, device=cp.device)
+    else:
+        _check_out(out, (cp.n, cp.k), (torch.bfloat16,), cp.device)
+    c, s = cp.c_struct(), cp.rec.c_struct()
+    s.ae = None
+    s.lo = None
+    _check(lib().w12_mx4_decode(ctypes.byref(c), ctypes.byref(s), out.data_ptr(), _stream_handle(cp.device)))
+    return out
+
+
+def mx4_gemm(x: torch.Tensor, cp: Mx4Copy, path: str | None = None, out: torch.Tensor | None = None,
+             out_bf16: bool = False):
+    """Q pass on the 4-bit copy: y = x Wq^T with Wq = mx4_decode(cp); outputs as in gemm."""
+    x, out = _gemm_io(x, cp.n, cp.k, cp.device, out, out_bf16)
+    if x.shape[0] == 0:
+        return out
+    c, s = cp.c_struct(), cp.rec.c_struct()
+    s.ae = None
+    s.lo = None
+    _check(lib().w12_mx4_gemm(x.data_ptr(), x.shape[0], ctypes.byref(c), ctypes.byref(s), out.data_ptr(),
+                              _PATHS[path] | _out_flag(out), _stream_handle(x.device)))
+    return out
+
+
+def mx4_top1(x: torch.Tensor, cp: Mx4Copy, out=None):
+    """Top-1 of the Q pass on the 4-bit copy per row of x: (index int32 [m], value float32 [m])."""
+    c = cp.c_struct()
+    return _top1(lambda xp, m, s, ip, vp, fl, st: lib().w12_mx4_top1(xp, m, ctypes.byref(c), s, ip, vp, fl, st),
                  x, cp.rec, False, out)
 
 

@@ -21,3 +21,4 @@ from .w12 import (  # noqa: F401
     SILU_GROUP, interleave_rows, silu_rows, silu64, silu_mul64, silu_mul_bound,
 )
 from .vocab import embed_bits, logprobs64, logprobs_tol  # noqa: F401
+from .mx4 import E2M1, MX4_BLOCK, Mx4Copy, e2m1_code, mx4_copy, mx4_to_storage, mx4_weights64  # noqa: F401

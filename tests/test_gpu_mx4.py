@@ -1,0 +1,199 @@
+"""GPU parity of the microscaled 4-bit copy (w12_mx4_build, w12_mx4_decode, w12_mx4_gemm,
+w12_mx4_top1) against the oracle.
+
+Bars: the copy byte-identical to the oracle's and its decode bit for bit the oracle's weights;
+outputs within 1e-3 * sum_k |x w| of the float64 oracle per element (the GEMMs' documented bound);
+one-hot x returns every weight of a column exactly; top-1 a maximum within the bound.
+"""
+import numpy as np
+import pytest
+
+import oracle
+from lossless_bit_weight_02_amd import synth
+from tests.gpu_util import check_y, check_y_bf16, say, to_dev, to_host_bits
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from lossless_bit_weight_02_amd import w12
+    w12.lib()
+
+
+def _w12():
+    from lossless_bit_weight_02_amd import w12
+    return w12
+
+
+def _weights(n, k, seed, p_zero=0.01, p_out=5e-4):
+    rng = np.random.default_rng(seed)
+    w = synth.f32_to_bf16_bits((rng.standard_normal((n, k)) * 0.02 * np.exp(rng.standard_normal((n, 1)))).astype(np.float32))
+    w[rng.random((n, k)) < p_zero] = 0
+    w[rng.random((n, k)) < p_out] = 0x4400
+    return w
+
+
+def _bits64(w64):
+    """bfloat16 bits of float64 values that bfloat16 holds exactly (NaN apart)."""
+    b = (w64.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    assert np.array_equal(oracle.bf16_to_f64(b)[~np.isnan(w64)], w64[~np.isnan(w64)])
+    return b
+
+
+def _copy_check(w_bits, what):
+    w12 = _w12()
+    say(f"mx4 build {what} {w_bits.shape}")
+    rec = w12.encode(to_dev(w_bits))
+    cp = w12.mx4_build(rec)
+    ref = oracle.encode(w_bits)
+    ocp = oracle.mx4_copy(ref)
+    got, want = cp.to_numpy()["q_s"], oracle.mx4_to_storage(ocp)
+    if not np.array_equal(got, want):
+        bad = np.argwhere(got != want)
+        raise AssertionError(f"{what}: bytes differ at {bad[:5].tolist()} ({len(bad)}), got "
+                             f"{got[bad[:5]].tolist()} want {want[bad[:5]].tolist()}")
+    say(f"mx4 decode {what}")
+    dec = to_host_bits(w12.mx4_decode(cp))
+    w64 = oracle.mx4_weights64(ref, ocp)
+    esc = oracle.escaped_mask(ref)
+    assert np.array_equal(dec[esc], w_bits[esc]), f"{what}: escapes"
+    assert np.array_equal(dec[~esc], _bits64(w64[~esc])), f"{what}: decoded values"
+    return rec, cp, ref, ocp, w64
+
+
+@pytest.mark.parametrize("n,k,ms", [
+    (16, 128, (1, 3, 16)),                             # one tile
+    (1, 128, (1, 2, 64)),                              # one row
+    (300, 1152, (1, 2, 4, 5, 8, 16, 17, 32, 40, 64, 100, 200)),
+    (6160, 256, (1, 16, 40, 64, 100)),                 # 385 tiles: the wider kernels
+    (64, 5120, (1, 2, 16, 32)),                        # few tiles: k ranges
+    (320, 17408, (1, 7, 32, 64)),                      # long rows
+    (1037, 640, (4, 33)),
+    (8200, 896, (3, 8, 24, 48)),                       # two tiles per CU and a ragged last one
+])
+def test_mx4_shapes(n, k, ms):
+    w12 = _w12()
+    rec, cp, ref, ocp, w64 = _copy_check(_weights(n, k, n + k), f"{n}x{k}")
+    x_bits = synth.gen_x(max(ms), k, tensor_id=n)
+    y64, absum = oracle.gemm64_f(x_bits, w64), oracle.abs_bound64_f(x_bits, w64)
+    x = to_dev(x_bits)
+    for m in ms:
+        for path in ("gemv", "mfma", "stream", "auto"):
+            say(f"mx4 gemm {n}x{k} m={m} {path}")
+            try:
+                y = w12.mx4_gemm(x[:m], cp, path=path)
+            except w12.W12Error as e:
+                assert path == "stream" and e.status == w12.W12_ERR_SHAPE
+                continue
+            check_y(y.cpu().numpy(), y64[:m], absum[:m], f"mx4 {n}x{k} m={m} {path}")
+            y2 = w12.mx4_gemm(x[:m], cp, path=path)
+            assert torch.equal(y, y2), "not repeatable"
+
+
+def test_mx4_edge_rows():
+    """Windows at both ends of the exponent range, all-zero rows, blocks of escapes alone, Inf and NaN
+    escapes, a constant row, every rounding of every code."""
+    k = 512
+    rng = np.random.default_rng(3)
+    w = synth.f32_to_bf16_bits((rng.standard_normal((48, k)) * 0.02).astype(np.float32))
+    w[0, 5] = 0x6F00                      # far above the row's window
+    w[1] = 0                              # nothing in the window
+    w[2, 7] = 0x7F80                      # +Inf
+    w[3] = 0x3F80                         # constant 1.0
+    w[4, :64] = 0x0001                    # subnormals: two blocks of escapes alone
+    w[5] = (rng.integers(0, 2, k) << 15 | rng.integers(1, 17, k) << 7 | rng.integers(0, 128, k)).astype(np.uint16)
+    w[6] = (rng.integers(0, 2, k) << 15 | rng.integers(239, 255, k) << 7 | rng.integers(0, 128, k)).astype(np.uint16)
+    w[7, 100] = 0x7FC1                    # NaN
+    w[8] = rng.integers(0, 65536, k)      # any bits
+    w[9] = np.tile(np.arange(128, dtype=np.uint16), 4) + np.repeat([126, 127, 125, 124], 128).astype(np.uint16) * 128
+    w[9, ::32] = 127 << 7                 # every mantissa at several exponents under one scale
+    w[10] = w[9] | 0x8000
+    rec, cp, ref, ocp, w64 = _copy_check(w, "edge rows")
+    w12 = _w12()
+    x_bits = synth.gen_x(20, k, tensor_id=9)
+    keep = np.isfinite(w64).all(axis=1) & (np.abs(w64).max(axis=1) < 1e30)
+    y64, absum = oracle.gemm64_f(x_bits, w64[keep]), oracle.abs_bound64_f(x_bits, w64[keep])
+    for m, path in ((1, "gemv"), (16, "mfma"), (20, "mfma"), (4, "stream")):
+        y = w12.mx4_gemm(to_dev(x_bits[:m]), cp, path=path).cpu().numpy()
+        check_y(y[:, keep], y64[:m], absum[:m], f"edge rows {path}")
+        assert np.isinf(y[:, 2]).all() and np.isnan(y[:, 7]).all()
+
+
+def test_mx4_one_hot_exact():
+    rec, cp, ref, ocp, w64 = _copy_check(_weights(48, 512, 11), "one-hot")
+    w12 = _w12()
+    for kk in (0, 1, 2, 7, 31, 32, 127, 128, 300, 511):
+        x = np.zeros((16, 512), dtype=np.uint16)
+        x[:, kk] = 0x3F80
+        for path, m in (("gemv", 1), ("mfma", 16), ("stream", 4)):
+            y = w12.mx4_gemm(to_dev(x[:m]), cp, path=path).cpu().numpy()
+            assert np.array_equal(y[m - 1].astype(np.float64), w64[:, kk]), (kk, path)
+
+
+def test_mx4_top1_and_bf16_out():
+    w12 = _w12()
+    for n in (4000, 9000):
+        rec, cp, ref, ocp, w64 = _copy_check(_weights(n, 1024, n), "top1")
+        x_bits = synth.gen_x(40, 1024, tensor_id=21)
+        x = to_dev(x_bits)
+        y64, absum = oracle.gemm64_f(x_bits, w64), oracle.abs_bound64_f(x_bits, w64)
+        for m in (1, 9, 40):
+            say(f"mx4 top1 n={n} m={m}")
+            idx, val = (t.cpu().numpy() for t in w12.mx4_top1(x[:m], cp))
+            for j in range(m):
+                a = int(idx[j])
+                assert y64[j, a] >= y64[j].max() - 1e-3 * (absum[j, a] + absum[j, np.argmax(y64[j])])
+                assert abs(val[j] - y64[j, a]) <= 1e-3 * absum[j, a]
+        for m, path in ((1, "gemv"), (16, "mfma"), (40, "mfma"), (40, "stream"), (12, "auto")):
+            say(f"mx4 bf16 out m={m} {path}")
+            y = w12.mx4_gemm(x[:m], cp, path=path).cpu().numpy()
+            y16 = w12.mx4_gemm(x[:m], cp, path=path, out_bf16=True)
+            check_y_bf16(y16, y, y64[:m], absum[:m], f"mx4 bf16 out m={m} {path}")
+
+
+def test_mx4_graph_replays():
+    """A captured product (one that splits k through the workspace, one that does not) replayed among
+    eager calls on other data gives the eager bits."""
+    w12 = _w12()
+    for n, k, m in ((64, 5120, 8), (4800, 640, 5)):
+        w = _weights(n, k, 5)
+        rec = w12.encode(to_dev(w))
+        cp = w12.mx4_build(rec)
+        xa, xb = to_dev(synth.gen_x(m, k, tensor_id=1)), to_dev(synth.gen_x(m, k, tensor_id=2))
+        ya, yb = w12.mx4_gemm(xa, cp), w12.mx4_gemm(xb, cp)
+        st = xa.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = w12.mx4_gemm(st, cp)
+        for src, want in ((xb, yb), (xa, ya), (xb, yb)):
+            st.copy_(src)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+            assert torch.equal(w12.mx4_gemm(xa, cp), ya)
+
+
+def test_mx4_larger_shapes_against_decode():
+    """Shapes too large for the float64 oracle on the host: the product against float64 on the GPU over
+    the decoded copy (its decode is pinned by the tests above), at the automatic path."""
+    w12 = _w12()
+    for n, k, ms in ((34816, 5120, (1, 2, 5, 16, 24, 64, 130)), (5120, 17408, (1, 4, 16, 64)), (152064, 1280, (1, 16, 32, 64))):
+        g = torch.Generator(device="cuda").manual_seed(n)
+        w = (torch.randn(n, k, generator=g, device="cuda") * 0.02).to(torch.bfloat16)
+        w[torch.rand(n, k, generator=g, device="cuda") < 1e-3] = 0
+        rec = w12.encode(w)
+        del w
+        cp = w12.mx4_build(rec)
+        wd = w12.mx4_decode(cp).double()
+        x = torch.randn(max(ms), k, generator=g, device="cuda").to(torch.bfloat16)
+        y64, ab = x.double() @ wd.t(), x.double().abs() @ wd.abs().t()
+        del wd
+        for m in ms:
+            say(f"mx4 large {n}x{k} m={m}")
+            y = w12.mx4_gemm(x[:m], cp).double()
+            assert bool(((y - y64[:m]).abs() <= 1e-3 * ab[:m]).all())

@@ -1,0 +1,105 @@
+"""Host-only checks of the 4-bit copy: refusals before any launch, and the oracle's quantiser on
+values worked out by hand."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import oracle
+from lossless_bit_weight_02_amd import synth, w12
+from tests.test_abi_cpu import _lib, _rec
+
+
+def _cp(n=64, k=128, q=0x8000):
+    return w12._W12MX4(n, k, q)
+
+
+def test_build_and_decode_refusals():
+    L = _lib()
+    assert L.w12_mx4_build(ctypes.byref(_rec()), None, None) == w12.W12_ERR_ARG
+    assert L.w12_mx4_build(None, ctypes.byref(_cp()), None) == w12.W12_ERR_ARG
+    assert L.w12_mx4_build(ctypes.byref(_rec()), ctypes.byref(_cp(n=63)), None) == w12.W12_ERR_ARG
+    assert L.w12_mx4_build(ctypes.byref(_rec()), ctypes.byref(_cp(q=None)), None) == w12.W12_ERR_ARG
+    assert L.w12_mx4_build(ctypes.byref(_rec()), ctypes.byref(_cp(q=0x8008)), None) == w12.W12_ERR_ALIGN
+    assert L.w12_mx4_build(ctypes.byref(_rec(k=96)), ctypes.byref(_cp(k=96)), None) == w12.W12_ERR_SHAPE
+    assert L.w12_mx4_build(ctypes.byref(_rec(lo=None)), ctypes.byref(_cp()), None) == w12.W12_ERR_ARG
+    assert L.w12_mx4_decode(ctypes.byref(_cp()), ctypes.byref(_rec()), None, None) == w12.W12_ERR_ARG
+    assert L.w12_mx4_decode(ctypes.byref(_cp()), ctypes.byref(_rec()), 0x1002, None) == w12.W12_ERR_ALIGN
+    assert L.w12_mx4_decode(ctypes.byref(_cp(k=256)), ctypes.byref(_rec()), 0x1000, None) == w12.W12_ERR_ARG
+    assert L.w12_mx4_decode(ctypes.byref(_cp()), ctypes.byref(_rec(base=None)), 0x1000, None) == w12.W12_ERR_ARG
+    assert L.w12_mx4_decode(ctypes.byref(_cp()), ctypes.byref(_rec(esc_col=None)), 0x1000, None) == w12.W12_ERR_ARG
+
+
+def test_product_refusals():
+    L = _lib()
+
+    def gemm(x=0x1000, m=1, cp=None, rec=None, y=0x9000, flags=0):
+        return L.w12_mx4_gemm(x, m, ctypes.byref(cp or _cp()), ctypes.byref(rec or _rec(ae=None, lo=None)), y, flags, None)
+
+    def top1(x=0x1000, m=1, cp=None, idx=0x9000, val=0xA000, flags=0):
+        return L.w12_mx4_top1(x, m, ctypes.byref(cp or _cp()), ctypes.byref(_rec(ae=None, lo=None)), idx, val, flags, None)
+
+    assert gemm(x=None) == w12.W12_ERR_ARG
+    assert gemm(y=None) == w12.W12_ERR_ARG
+    assert gemm(m=0) == w12.W12_ERR_ARG
+    assert gemm(m=1 << 31) == w12.W12_ERR_RANGE
+    assert gemm(x=0x1008) == w12.W12_ERR_ALIGN
+    assert gemm(y=0x9002) == w12.W12_ERR_ALIGN
+    assert gemm(y=0x9001, flags=w12.OUT_BF16) == w12.W12_ERR_ALIGN
+    assert gemm(flags=w12.Q8_MIDPOINT) == w12.W12_ERR_ARG
+    assert gemm(flags=7) == w12.W12_ERR_ARG
+    assert gemm(cp=_cp(n=65)) == w12.W12_ERR_ARG
+    assert gemm(cp=_cp(q=0x8004)) == w12.W12_ERR_ALIGN
+    assert gemm(rec=_rec(esc_ptr=None)) == w12.W12_ERR_ARG
+    assert gemm(rec=_rec(k=1 << 25), cp=_cp(k=1 << 25)) == w12.W12_ERR_RANGE
+    assert top1(idx=None) == w12.W12_ERR_ARG
+    assert top1(flags=1) == w12.W12_ERR_ARG
+    assert top1(val=0xA002) == w12.W12_ERR_ALIGN
+    assert top1(m=-1) == w12.W12_ERR_ARG
+    with pytest.raises(ValueError):
+        torch = pytest.importorskip("torch")
+        rec = w12.W12Weight(16, 128, *([torch.zeros(16, dtype=torch.uint8)] * 3), *([torch.zeros(17, dtype=torch.int32)] * 3))
+        w12.mx4_gemm(torch.zeros(1, 128, dtype=torch.bfloat16), w12.Mx4Copy(rec, torch.zeros(17, dtype=torch.uint8)))
+
+
+def test_code_table_and_ties():
+    for c, v in enumerate(oracle.E2M1):
+        assert oracle.e2m1_code(v) == c
+    ties = {0.25: 0, 0.75: 2, 1.25: 2, 1.75: 4, 2.5: 4, 3.5: 6, 5.0: 6}
+    for v, c in ties.items():
+        assert oracle.e2m1_code(v) == c, v
+    assert oracle.e2m1_code(0.26) == 1 and oracle.e2m1_code(5.1) == 7 and oracle.e2m1_code(7.9) == 7
+
+
+def test_quantiser_on_worked_values():
+    """One row of two blocks: the first holds 2^0 * (1.75, 1.0, -0.375, 0 (escaped)) among 2^-9, the
+    second only zeros (escapes): the window bottom's scale."""
+    w = np.full((1, 128), 2.0 ** -9, dtype=np.float32)
+    w[0, :4] = [1.75, 1.0, -0.375, 0.0]
+    w[0, 32:64] = 0.0
+    rec = oracle.encode(synth.f32_to_bf16_bits(w))
+    cp = oracle.mx4_copy(rec)
+    base = int(rec.base[0])
+    # block 0: e = 127, scale 2^-2: 7 -> 6, 4 -> 4, -1.5 -> -1.5, the rest 2^-7 -> 0
+    assert cp.code[0, :5].tolist() == [7, 6, 8 + 3, 0, 0]
+    assert cp.scale[0, 0] == 127 - base + 110
+    assert cp.scale[0, 1] == 110 and not cp.code[0, 32:64].any()
+    v = oracle.mx4_weights64(rec, cp)
+    assert v[0, :5].tolist() == [1.5, 1.0, -0.375, 0.0, 0.0]
+    # blocks 2, 3: e = 118, scale 2^-11: 2^-9 / 2^-11 = 4, exact
+    assert (v[0, 64:] == 2.0 ** -9).all()
+
+
+def test_storage_order():
+    n, k = 17, 256
+    code = np.arange(n * k, dtype=np.int64).reshape(n, k) % 16
+    scale = (110 + np.arange(n * k // 32) % 16).astype(np.uint8).reshape(n, k // 32)
+    s = oracle.mx4_to_storage(oracle.Mx4Copy(n, k, code.astype(np.uint8), scale))
+    assert s.size == 32 * k // 32 * 17
+    for row, col in ((0, 0), (0, 129), (5, 77), (16, 255), (15, 128)):
+        t = (row // 16) * 2 + col // 128
+        r, g, j = row % 16, col % 128 // 32, col % 32
+        byte = s[1088 * t + 16 * (r + 16 * g) + j // 2]
+        assert (byte >> (4 * (j % 2))) & 15 == code[row, col]
+        assert s[1088 * t + 1024 + r + 16 * g] == scale[row, col // 32]
+    assert not s[1088 * 2 + 16 * 1:1088 * 2 + 16 * 16].any()   # padding rows
