@@ -368,9 +368,11 @@ int w12_embed(const void *ids, int64_t count, const w12_weight *wt, float scale,
  * log probabilities are -Inf, its entropy 0, its alternatives columns 0 .. top-1.  A row with a NaN
  * or +Inf logit gives NaN log probabilities (a token outside 0 .. n-1 still -Inf) and entropy.
  * All sums are held in float.  scratch: w12_logprobs_scratch bytes of device memory of the caller's
- * (16-byte aligned; needs no particular contents; NULL when that is 0), in use until the call's
- * work on `stream` is finished; W12_ERR_CAPACITY if scratch_bytes is smaller.  Calls with
- * different scratch never touch each other's, on any streams or in any graphs.
+ * (16-byte aligned; NULL when that is 0; W12_ERR_CAPACITY if scratch_bytes is smaller), in use until
+ * the call's work on `stream` is finished.  Its first bytes are counters that must be zero when
+ * the work starts and are zero again when it ends: clear it once, then reuse it for calls of any
+ * sizes that follow each other on one stream.  Calls with different scratch never touch each
+ * other's, on any streams or in any graphs.
  */
 #define W12_LOGITS_BF16 0x80u
 int w12_logprobs_scratch(int64_t m, int64_t n, int top, uint32_t flags, uint64_t *bytes);

@@ -656,7 +656,7 @@ int w12_logprobs_scratch(int64_t m, int64_t n, int top, uint32_t flags, uint64_t
   w12::DevInfo di;
   hipError_t e = w12::dev_info(&di);
   if (e != hipSuccess) return hip_fail(e, "device query");
-  *bytes = w12::logprobs_scratch(di, m, n, top, (flags & W12_LOGITS_BF16) != 0);
+  *bytes = w12::logprobs_scratch(di, m, n, top);
   return ok();
 }
 
@@ -681,7 +681,7 @@ int w12_logprobs(const void* y, int64_t m, int64_t n, int64_t ldy, const void* t
   w12::DevInfo di;
   hipError_t e = w12::dev_info(&di);
   if (e != hipSuccess) return hip_fail(e, "device query");
-  const uint64_t need = w12::logprobs_scratch(di, m, n, top, bf);
+  const uint64_t need = w12::logprobs_scratch(di, m, n, top);
   if (need > 0) {
     if (!scratch || scratch_bytes < need)
       return fail(W12_ERR_CAPACITY, "scratch of %llu bytes is needed (%llu given)", (unsigned long long)need,

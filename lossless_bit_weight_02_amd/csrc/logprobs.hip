@@ -12,15 +12,16 @@
 //   s = s_a + f (1 + s_b),   T = T_a + f (T_b + (1 + s_b) d).
 //
 // Work split.  A row's logits are split over S workgroups of 4 waves (S = 1 when the rows alone
-// fill the chip), a workgroup's part over its waves batch by batch: 64 lanes x 16 floats (32
-// bfloat16) per batch, four 16-byte loads a lane, the next batch in flight.  The running maximum
-// is the wave's (a scalar compare per batch finds the rare batch that raises it), sums are each
-// lane's own and join at the end in a fixed order.  With S > 1 the parts go to the caller's
-// scratch and a second kernel of one wave per row joins them, lane by part.
+// fill the chip), a workgroup's part over its waves batch by batch: 64 lanes x 16 logits per batch in
+// 16-byte loads, the next batch in flight.  The running maximum
+// is the wave's (one compare per batch finds the rare batch that raises it), sums are each lane's
+// own and join at the end in a fixed order.  With S > 1 each workgroup leaves its part in the
+// caller's scratch and counts itself off; the row's last one joins the parts in part order, lane
+// by part, so the result does not depend on which came last, and there is no second launch.
 //
 // Top alternatives.  A candidate is a 64-bit key: the logit's order (NaN above +Inf, -0 as +0), then
 // the complement of its index, so equal logits go by the lower index and every order is total.
-// Each lane keeps the largest order it has seen; the K-th largest of the 64 lanes' is a bound that
+// Each lane keeps the largest logit it has seen; the K-th largest of the 64 lanes' is a bound that
 // K logits already reach, so a batch without a logit above it needs one compare in all.  Otherwise
 // the batch's logits at or above the new bound are appended to the wave's list in LDS, and a full
 // list is cut back to its K best (each key's rank is the number of larger keys).
@@ -31,10 +32,16 @@ namespace w12 {
 
 constexpr int kLpCap = 256;                      // keys of a wave's candidate list
 constexpr int kLpWaves = 4;
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kLpElems = 16;                     // logits of a lane per batch
+constexpr int kLpAhead = 4;                      // keys of a part loaded together when parts join
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+
+struct LpPart {
+  float M, s, T, pad;
+};
 
 struct LpArgs {
   const void* y;          // logits [m][ldy], float or bfloat16
@@ -47,16 +54,28 @@ struct LpArgs {
   float* tlogp;           // [m][top]
   int splits;             // workgroups per row
   int64_t part;           // logits per workgroup (a multiple of a workgroup's batch)
-  uint8_t* scratch;       // splits > 1: [m][splits] LpPart, then [m][splits][top] keys
-};
-
-struct LpPart {
-  float M, s, T, pad;
+  // splits > 1: a count per row (zero between calls), then [m][splits] LpPart, [m][splits][top] keys
+  uint32_t* count;
+  LpPart* parts;
+  uint64_t* keys;
 };
 
 __device__ __forceinline__ void lp_wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
+}
+
+// Stores and loads that every die of the device sees at once, and the wait for this wave's stores.
+template <typename T>
+__device__ __forceinline__ void dev_store(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ __forceinline__ T dev_load(const T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void stores_done() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 // e^d for d <= 0 (or NaN)
@@ -93,7 +112,7 @@ struct LpTop {
   uint64_t* list;         // [kLpCap], this wave's
   int K;
   int cnt = 0;            // keys in the list (uniform)
-  uint32_t thr = 0;       // orders below this are out (uniform)
+  uint32_t seen = 0;      // K logits have been seen at or above this order (uniform)
 
   // the list cut back to its K largest keys, in descending order; with K keys left, nothing below
   // the last can enter
@@ -126,7 +145,7 @@ struct LpTop {
     if (cnt >= K) {
       cnt = K;
       const uint32_t last = __builtin_amdgcn_readfirstlane((uint32_t)(list[K - 1] >> 32));
-      if (last > thr) thr = last;
+      if (last > seen) seen = last;
     }
   }
 
@@ -138,10 +157,10 @@ struct LpTop {
   }
 };
 
-// the K-th largest of the 64 lanes' values
+// The K-th largest of the 64 lanes' values, bit by bit from the top.
 __device__ __forceinline__ uint32_t lp_kth(uint32_t v, int K) {
   uint32_t t = 0;
-#pragma unroll
+#pragma unroll 8
   for (int b = 31; b >= 0; --b) {
     const uint32_t c = t | (1u << b);
     if (__popcll(__ballot(v >= c)) >= K) t = c;
@@ -181,9 +200,11 @@ __device__ __forceinline__ void lp_finish(const LpArgs& a, int64_t row, float M,
 }
 
 template <bool BF>
-__global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(LpArgs a) {
+__global__ __launch_bounds__(64 * kLpWaves) __attribute__((amdgpu_waves_per_eu(4)))
+void k_logprobs(LpArgs a) {
   constexpr int V = BF ? 8 : 4;                    // logits per 16-byte load
-  constexpr int E = 4 * V;                         // logits of a lane per batch
+  constexpr int E = kLpElems;                      // logits of a lane per batch
+  constexpr int Q = E / V;                         // its loads
   constexpr int B = 64 * E;                        // logits of a wave per batch
   __shared__ uint64_t s_list[kLpWaves][kLpCap];
   __shared__ float s_run[kLpWaves][4];
@@ -197,17 +218,17 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(LpArgs a) {
   const uint8_t* const yr = static_cast<const uint8_t*>(a.y) + row * a.ldy * (BF ? 2 : 4);
 
   // element e of the lane's batch at column c: c + 64 V (e / V) + V lane + e % V
-  const auto load = [&](int64_t c, u32x4 v[4]) {
+  const auto load = [&](int64_t c, u32x4 v[Q]) {
     if (c + B <= c1) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < Q; ++q) {
         const uint8_t* src = yr + (c + 64 * V * q + V * lane) * (BF ? 2 : 4);
         if constexpr (BF) v[q] = *reinterpret_cast<const u32x4_a2*>(src);
         else v[q] = *reinterpret_cast<const u32x4_a4*>(src);
       }
     } else {                                       // the part's end: -Inf past it
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int64_t cc = c + 64 * V * q + V * lane + (V / 4) * i;
@@ -223,51 +244,62 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(LpArgs a) {
   };
 
   float M = -INFINITY, s = 0.0f, T = 0.0f;         // M uniform; s, T the lane's
+  float sf = 0.0f, Tf = 0.0f, ML = 0.0f;           // sums in units of log 2 not yet in s, T; fl(M L)
+  // with p = 2^-del p' the true terms: s += 2^-del s', T += 2^-del (T' - del s') / L
+  const auto fold = [&]() {
+    if (fabsf(M) < 1e37f) {
+      const float del = fmaf(M, kLog2e, -ML), f = 1.0f - del * kLn2;
+      s += f * sf;
+      T += f * (Tf - del * sf) * kLn2;
+      sf = Tf = 0.0f;
+    }
+  };
   int owner = 0;                                   // the lane that left the maximum out
   LpTop top;
   top.list = s_list[w];
   top.K = a.top;
-  uint32_t lmax = 0;                               // the lane's largest order so far
+  float lmax = -INFINITY;                          // the lane's largest logit so far (NaN passed over)
   float thrf = -INFINITY;                          // a logit below this cannot enter the list
-  bool anynan = false;
+  int batch = 0;
+  bool anynan = false, closed = a.top == 0;        // closed: nothing can enter any more
 
   int64_t c = c0 + (int64_t)w * B;
-  u32x4 cur[4], nxt[4];
-  if (c < c1) load(c, cur);
-  for (; c < c1; c += (int64_t)kLpWaves * B) {
-    const int64_t cn = c + (int64_t)kLpWaves * B;
-    if (cn < c1) load(cn, nxt);
+  constexpr int64_t kStep = (int64_t)kLpWaves * B;
+  u32x4 raw[Q];
+  if (c < c1) load(c, raw);
+  for (; c < c1; c += kStep) {
     float x[E];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < Q; ++q)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (BF) {
-          x[8 * q + 2 * i] = bf16_to_float(cur[q][i] & 0xFFFFu);
-          x[8 * q + 2 * i + 1] = __uint_as_float(cur[q][i] & 0xFFFF0000u);
+          x[8 * q + 2 * i] = bf16_to_float(raw[q][i] & 0xFFFFu);
+          x[8 * q + 2 * i + 1] = __uint_as_float(raw[q][i] & 0xFFFF0000u);
         } else {
-          x[4 * q + i] = __uint_as_float(cur[q][i]);
+          x[4 * q + i] = __uint_as_float(raw[q][i]);
         }
       }
+    if (c + kStep < c1) load(c + kStep, raw);      // the next batch, in flight while this one is summed
     float mx = x[0];
 #pragma unroll
     for (int e = 1; e < E; ++e) mx = fmaxf(mx, x[e]);   // (a NaN is passed over)
-    bool leave = false;                            // the lane leaves one maximum out of this batch
     if (__ballot(mx > M)) {
+      // a new maximum: the sums so far relative to it, and one logit that equals it left out
       float mn = mx;
 #pragma unroll
       for (int sh = 32; sh >= 1; sh /= 2) mn = fmaxf(mn, __shfl_xor(mn, sh));
       if (M > -INFINITY) {
+        fold();
         const float d = M - mn, f = lp_exp(d);
         if (lane == owner) s += 1.0f;
         T = f > 0.0f ? f * (T + s * d) : s != s ? s : 0.0f;   // (s d may overflow where f is 0)
         s *= f;
       }
       M = mn;
+      ML = M * kLog2e;
       owner = __ffsll((unsigned long long)__ballot(mx == M)) - 1;
-      leave = lane == owner;
-    }
-    if (M > -INFINITY) {
+      bool leave = lane == owner;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float d = x[e] - M;
@@ -279,43 +311,81 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(LpArgs a) {
         s += p;
         T = fmaf(p, fmaxf(d, -200.0f), T);         // (a masked logit: 0 times a finite number)
       }
+    } else if (fabsf(M) < 1e37f) {
+      // in units of log 2, the product and the difference in one rounding: a = x L - fl(M L), which
+      // is (x - M) L + del with one del = M L - fl(M L) for all logits under this maximum (put
+      // right when the maximum changes and at the end)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float d = fmaf(x[e], kLog2e, -ML);
+        const float p = __builtin_amdgcn_exp2f(d);
+        sf += p;
+        Tf = fmaf(p, fmaxf(d, -300.0f), Tf);       // (a masked logit: 0 times a finite number)
+      }
+    } else if (M > -INFINITY) {                    // (M L could overflow)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float d = x[e] - M;
+        const float p = lp_exp(d);
+        s += p;
+        T = fmaf(p, fmaxf(d, -200.0f), T);
+      }
     } else {
       bool bad = false;
 #pragma unroll
       for (int e = 0; e < E; ++e) bad |= x[e] != x[e];
       if (bad) s = __uint_as_float(0x7FC00000u);
     }
-    if (a.top > 0) {
-      anynan = anynan || __ballot(s != s) != 0;
+    ++batch;
+    if (!closed) {
+      anynan = anynan || __ballot(s + sf != s + sf) != 0;
       if (anynan || __ballot(mx >= thrf)) {
-        uint32_t ord[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          ord[e] = lp_order(x[e]);
-          lmax = ord[e] > lmax ? ord[e] : lmax;
-        }
-        const uint32_t kth = lp_kth(lmax, a.top);
-        if (kth > top.thr) top.thr = kth;
-        // the lane's logits that enter, a bit each
-        uint32_t in = 0;
-        int tot = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
+        lmax = fmaxf(lmax, mx);
+        // the bound again at the batches 1, 2, 4, 8, ...: a bound twice as old lets through about
+        // twice as many logits, each cheaper than the bound itself
+        float lowf = thrf;
+        const auto bound = [&]() {
+          const uint32_t kth = a.top == 1 ? lp_order(M) : lp_kth(lp_order(lmax), a.top);
+          if (kth > top.seen) top.seen = kth;
+          // earlier batches have lower indices: of the logits equal to a bound they reached none
+          // can enter (thrf), of those equal to one that this batch reached the first can
+          lowf = lp_value(top.seen);               // (NaN: the comparisons below let all through)
+          if (lowf < thrf) lowf = thrf;
+        };
+        if (a.top == 1 || (batch & (batch - 1)) == 0) bound();
+        const auto key_of = [&](int e) {
           const int64_t cc = c + 64 * V * (e / V) + V * lane + e % V;
-          const bool ok = ord[e] >= top.thr && cc < c1;
-          in |= (ok ? 1u : 0u) << e;
-          tot += __popcll(__ballot(ok));
-        }
-        if (tot > 64) {
-          // many: of those equal to the bound (a masked row: all of them) only the K of the lowest
-          // indices can stay
-          uint32_t eq = 0;
+          return (uint64_t)lp_order(x[e]) << 32 | (0xFFFFFFFFu - (uint32_t)cc);
+        };
+        int from = c + B > c1 ? 0 : E;             // (the part's end: with the column checks below)
+        if (from == E) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) eq |= (ord[e] == top.thr ? 1u : 0u) << e;
-          eq &= in;
+          for (int e = 0; e < E; ++e) {
+            const bool ok = !(x[e] < lowf);        // (NaN enters)
+            const uint64_t bl = __ballot(ok);
+            if (bl == 0 || from < E) continue;
+            if (!top.fits(bl)) {
+              from = e;
+              continue;
+            }
+            top.put(ok, bl, key_of(e), lane);
+          }
+        }
+        if (from < E) {
+          // more than the list holds, or the part's end: the lane's logits that enter, a bit each
+          bound();
+          uint32_t in = 0, eq = 0;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const bool ok = e >= from && !(x[e] < lowf) && c + 64 * V * (e / V) + V * lane + e % V < c1;
+            in |= (ok ? 1u : 0u) << e;
+            eq |= (ok && x[e] == lowf ? 1u : 0u) << e;
+          }
+          // of those equal to the bound (a masked row: all of them) only the K of the lowest
+          // indices can stay
           int before = 0;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < Q; ++q) {
             uint32_t g = eq & (((1u << V) - 1u) << (V * q));
             const int mine = __popc(g);
             int pre = before;
@@ -332,35 +402,32 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(LpArgs a) {
               in ^= high;
             }
           }
-        }
-        int from = 0;
-        while (from < E) {
-          int full = E;
+          while (from < E) {
+            int full = E;
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            if (e < from || full < E) continue;
-            const bool ok = ((in >> e) & 1u) && ord[e] >= top.thr;
-            const uint64_t bl = __ballot(ok);
-            if (bl == 0) continue;
-            if (!top.fits(bl)) {
-              full = e;
-              continue;
+            for (int e = 0; e < E; ++e) {
+              const bool ok = (in >> e) & 1u;
+              const uint64_t bl = __ballot(ok);
+              if (bl == 0 || e < from || full < E) continue;
+              if (!top.fits(bl)) {
+                full = e;
+                continue;
+              }
+              top.put(ok, bl, key_of(e), lane);
             }
-            const int64_t cc = c + 64 * V * (e / V) + V * lane + e % V;
-            top.put(ok, bl, (uint64_t)ord[e] << 32 | (0xFFFFFFFFu - (uint32_t)cc), lane);
+            from = full;
+            if (full < E) top.cut(lane);
           }
-          from = full;
-          if (full < E) top.cut(lane);
         }
-        // later batches have higher indices: only a larger logit can still enter
-        if (kth >= top.thr && kth != 0xFFFFFFFFu && kth > 0) top.thr = kth + 1;
-        thrf = top.thr <= 0x007FFFFFu ? -INFINITY : lp_value(top.thr);
+        // later batches: only above the bound (its order's successor; nothing is above a NaN)
+        if (top.seen == 0xFFFFFFFFu) closed = true;
+        else if (top.seen > 0) thrf = lp_value(top.seen + 1);
+        if (top.seen >= 0xFF800000u && top.seen < 0xFFFFFFFFu) thrf = INFINITY;   // above +Inf: NaN only
       }
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) cur[q] = nxt[q];
   }
 
+  fold();
   // the lanes' sums (relative to the same M) in a fixed order
 #pragma unroll
   for (int sh = 32; sh >= 1; sh /= 2) {
@@ -390,65 +457,78 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(LpArgs a) {
     lp_finish<BF>(a, row, M, s, T, top.list, lane);
     return;
   }
+  // ---- several workgroups: this one's part to the scratch; the last of the row joins them ----
+  // Parts move by device-scope atomic stores and loads, which other dies' caches see as they are, so
+  // no cache needs writing back or invalidating (a device-scope fence per workgroup cost 64 rows
+  // 36.6 us in all against XX); the wait orders the part before the count.
   const int64_t at = row * a.splits + sp;
-  if (lane == 0) reinterpret_cast<LpPart*>(a.scratch)[at] = LpPart{M, s, T, 0.0f};
-  uint64_t* keys = reinterpret_cast<uint64_t*>(a.scratch + a.m * a.splits * sizeof(LpPart));
-  if (lane < a.top) keys[at * a.top + lane] = lane < top.cnt ? top.list[lane] : 0;
-}
-
-// The parts of each row joined: one wave per row, lane l takes part l (splits <= 64).
-template <bool BF>
-__global__ __launch_bounds__(64) void k_logprobs_join(LpArgs a) {
-  __shared__ uint64_t s_list[kLpCap];
-  const int lane = threadIdx.x;
-  const int64_t row = blockIdx.x;
-  const LpPart* parts = reinterpret_cast<const LpPart*>(a.scratch) + row * a.splits;
-  const uint64_t* keys = reinterpret_cast<const uint64_t*>(a.scratch + a.m * a.splits * sizeof(LpPart)) +
-                         row * a.splits * a.top;
-  float M = -INFINITY, s = 0.0f, T = 0.0f;
+  if (lane < 3) dev_store(reinterpret_cast<uint32_t*>(a.parts + at) + lane, __float_as_uint(lane == 0 ? M : lane == 1 ? s : T));
+  if (lane < a.top) dev_store(a.keys + at * a.top + lane, lane < top.cnt ? top.list[lane] : (uint64_t)0);
+  stores_done();
+  uint32_t done = 0;
+  if (lane == 0) done = __hip_atomic_fetch_add(a.count + row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  done = __builtin_amdgcn_readfirstlane(done);
+  if (done + 1 != (uint32_t)a.splits) return;
+  asm volatile("" ::: "memory");
+  if (lane == 0) dev_store(a.count + row, 0u);     // zero again for the next call
+  M = -INFINITY;
+  s = T = 0.0f;
   if (lane < a.splits) {
-    const LpPart p = parts[lane];
-    M = p.M;
-    s = p.s;
-    T = p.T;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(a.parts + row * a.splits + lane);
+    M = __uint_as_float(dev_load(p));
+    s = __uint_as_float(dev_load(p + 1));
+    T = __uint_as_float(dev_load(p + 2));
   }
+  const uint64_t* keys = a.keys + (row * a.splits + lane) * a.top;
+  uint64_t key[kLpAhead];
+#pragma unroll
+  for (int r = 0; r < kLpAhead; ++r) key[r] = lane < a.splits && r < a.top ? dev_load(keys + r) : 0;
 #pragma unroll
   for (int sh = 1; sh < 64; sh *= 2) {
-    const float Mb = __shfl_xor(M, sh), sb = __shfl_xor(s, sh), Tb = __shfl_xor(T, sh);
     // the lower lane's run first on both sides, so all lanes hold the same bits
-    float M2 = (lane & sh) ? Mb : M, s2 = (lane & sh) ? sb : s, T2 = (lane & sh) ? Tb : T;
-    lp_join(M2, s2, T2, (lane & sh) ? M : Mb, (lane & sh) ? s : sb, (lane & sh) ? T : Tb);
+    const float Mo = __shfl_xor(M, sh), so = __shfl_xor(s, sh), To = __shfl_xor(T, sh);
+    const bool up = (lane & sh) != 0;
+    float M2 = up ? Mo : M, s2 = up ? so : s, T2 = up ? To : T;
+    lp_join(M2, s2, T2, up ? M : Mo, up ? s : so, up ? T : To);
     M = M2;
     s = s2;
     T = T2;
   }
-  LpTop top;
-  top.list = s_list;
-  top.K = a.top;
   if (a.top > 0) {
-    // each part's keys descend: its first bounds the rest, and a part whose next key is below the
-    // bound is done
-    uint64_t key = lane < a.splits ? keys[(int64_t)lane * a.top] : 0;
-    top.thr = lp_kth((uint32_t)(key >> 32), a.top);
-    for (int r = 0; r < a.top; ++r) {
-      const bool in = key != 0 && (uint32_t)(key >> 32) >= top.thr;
-      const uint64_t bl = __ballot(in);
-      if (bl == 0) break;
-      if (!top.fits(bl)) top.cut(lane);
-      top.put(in, bl, key, lane);
-      key = in && r + 1 < a.top ? keys[(int64_t)lane * a.top + r + 1] : 0;
+    // each part's keys descend: the K-th of their firsts bounds the rest, and a part whose next key
+    // is below the bound is done
+    top.cnt = 0;
+    top.seen = lp_kth((uint32_t)(key[0] >> 32), a.top);
+    bool more = true;
+    for (int r0 = 0; r0 < a.top && more; r0 += kLpAhead) {
+      if (r0 > 0) {
+#pragma unroll
+        for (int r = 0; r < kLpAhead; ++r) key[r] = lane < a.splits && r0 + r < a.top ? dev_load(keys + r0 + r) : 0;
+      }
+#pragma unroll
+      for (int r = 0; r < kLpAhead; ++r) {
+        const bool ok = key[r] != 0 && (uint32_t)(key[r] >> 32) >= top.seen;
+        const uint64_t bl = __ballot(ok);
+        if (bl == 0) more = false;
+        if (!more) continue;
+        if (!top.fits(bl)) top.cut(lane);
+        top.put(ok, bl, key[r], lane);
+      }
     }
     top.cut(lane);
   }
   lp_finish<BF>(a, row, M, s, T, top.list, lane);
 }
 
+constexpr int kLpPerCu = 4;                      // workgroups wanted per CU
+
 // Workgroups per row: the whole row in one where the rows fill the chip, otherwise as many parts
-// as give it about eight workgroups per CU, of at least one batch per wave, and at most 64.
-static void lp_plan(const DevInfo& di, int64_t m, int64_t n, bool bf, int* splits, int64_t* part) {
-  const int64_t unit = (bf ? 2048 : 1024) * kLpWaves;
+// as give it kLpPerCu workgroups per CU, of at least one batch per wave, and at most 64.
+static void lp_plan(const DevInfo& di, int64_t m, int64_t n, int* splits, int64_t* part) {
+  const int64_t unit = 64 * kLpElems * kLpWaves;
   const int64_t units = (n + unit - 1) / unit;
-  int64_t want = ((int64_t)di.cus * 8 + m - 1) / m;
+  int64_t want = (int64_t)di.cus * kLpPerCu / m;
+  if (want < 1) want = 1;
   if (want > units) want = units;
   if (want > 64) want = 64;
   const int64_t per = (units + want - 1) / want;
@@ -456,12 +536,15 @@ static void lp_plan(const DevInfo& di, int64_t m, int64_t n, bool bf, int* split
   *splits = (int)((units + per - 1) / per);
 }
 
-uint64_t logprobs_scratch(const DevInfo& di, int64_t m, int64_t n, int top, bool bf) {
+// The counts of the rows that can be split (fewer rows than workgroups wanted), ahead of the parts.
+static uint64_t lp_counts(const DevInfo& di) { return (uint64_t)di.cus * kLpPerCu * sizeof(uint32_t); }
+
+uint64_t logprobs_scratch(const DevInfo& di, int64_t m, int64_t n, int top) {
   int splits;
   int64_t part;
-  lp_plan(di, m, n, bf, &splits, &part);
+  lp_plan(di, m, n, &splits, &part);
   if (splits == 1) return 0;
-  return (uint64_t)m * splits * (sizeof(LpPart) + 8ull * top);
+  return lp_counts(di) + (uint64_t)m * splits * (sizeof(LpPart) + 8ull * top);
 }
 
 hipError_t launch_logprobs(const void* y, bool bf, int64_t m, int64_t n, int64_t ldy, const void* tokens,
@@ -474,15 +557,13 @@ hipError_t launch_logprobs(const void* y, bool bf, int64_t m, int64_t n, int64_t
   a.y = y; a.m = m; a.n = n; a.ldy = ldy;
   a.tokens = tokens; a.tok64 = tok64; a.nt = nt; a.top = top;
   a.logp = logp; a.ent = ent; a.tidx = tidx; a.tlogp = tlogp;
-  a.scratch = static_cast<uint8_t*>(scratch);
-  lp_plan(di, m, n, bf, &a.splits, &a.part);
+  lp_plan(di, m, n, &a.splits, &a.part);
+  a.count = static_cast<uint32_t*>(scratch);
+  a.parts = reinterpret_cast<LpPart*>(static_cast<uint8_t*>(scratch) + lp_counts(di));
+  a.keys = reinterpret_cast<uint64_t*>(a.parts + m * a.splits);
   const dim3 grid((unsigned)(m * a.splits)), block(64 * kLpWaves);
   if (bf) hipLaunchKernelGGL(k_logprobs<true>, grid, block, 0, s, a);
   else hipLaunchKernelGGL(k_logprobs<false>, grid, block, 0, s, a);
-  err = hipGetLastError();
-  if (err != hipSuccess || a.splits == 1) return err;
-  if (bf) hipLaunchKernelGGL(k_logprobs_join<true>, dim3((unsigned)m), dim3(64), 0, s, a);
-  else hipLaunchKernelGGL(k_logprobs_join<false>, dim3((unsigned)m), dim3(64), 0, s, a);
   return hipGetLastError();
 }
 

@@ -149,8 +149,8 @@ hipError_t launch_mx4_decode(const Planes& p, int64_t n, int64_t k, uint16_t* ou
 hipError_t launch_embed(const void* ids, bool ids64, int64_t cnt, const Planes& p, int64_t n, int64_t k,
                         float scale, void* out, bool out16, hipStream_t s);
 // log probabilities of tokens [m][nt], entropy and the `top` (0..64) best of rows of logits (float,
-// or bfloat16 with bf); scratch: logprobs_scratch bytes (0: none)
-uint64_t logprobs_scratch(const DevInfo& di, int64_t m, int64_t n, int top, bool bf);
+// or bfloat16 with bf); scratch: logprobs_scratch bytes (0: none), its counters zero (w12.h)
+uint64_t logprobs_scratch(const DevInfo& di, int64_t m, int64_t n, int top);
 hipError_t launch_logprobs(const void* y, bool bf, int64_t m, int64_t n, int64_t ldy, const void* tokens,
                            bool tok64, int nt, int top, float* logp, float* ent, int32_t* tidx,
                            float* tlogp, void* scratch, hipStream_t s);

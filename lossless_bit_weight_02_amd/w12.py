@@ -147,7 +147,25 @@ def _check(status: int):
 
 
 def _stream_handle(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    """The raw handle of the device's current stream."""
+    if device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+class _on_device:
+    """Makes a tensor's device the current one for a call, at no cost where it already is."""
+
+    def __init__(self, device):
+        self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
 
 
 def _ptr(t) -> int | None:
@@ -577,7 +595,7 @@ def embed(ids: torch.Tensor, wt: W12Weight, scale: float = 1.0, out: torch.Tenso
         return out
     ids = ids.contiguous()
     s = wt.c_struct()
-    with torch.cuda.device(wt.device):
+    with _on_device(wt.device):
         _check(lib().w12_embed(ids.data_ptr(), ids.numel(), ctypes.byref(s), float(scale), out.data_ptr(),
                                flag | _out_flag(out), _stream_handle(wt.device)))
     return out
@@ -590,6 +608,33 @@ class LogProbs(NamedTuple):
     entropy: torch.Tensor
     top_index: torch.Tensor
     top_logp: torch.Tensor
+
+
+_lp_sizes: dict = {}       # (device, m, n, top, flags) -> bytes
+_lp_buffers: dict = {}     # (device, stream) -> zero-counter scratch of the stream's calls
+
+
+def _lp_scratch(m, n, top, flags, device, stream):
+    """(scratch or None, bytes) of a logprobs call on `stream`.  Calls of one stream follow each other,
+    so they share one buffer; a call under graph capture gets its own, cleared by the graph, since
+    graphs may be replayed on any stream."""
+    key = (device.index, m, n, top, flags)
+    need = _lp_sizes.get(key)
+    if need is None:
+        b = ctypes.c_uint64(0)
+        _check(lib().w12_logprobs_scratch(m, n, top, flags, ctypes.byref(b)))
+        if len(_lp_sizes) > 4096:
+            _lp_sizes.clear()
+        need = _lp_sizes[key] = b.value
+    if need == 0:
+        return None, 0
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(need, dtype=torch.uint8, device=device), need
+    buf = _lp_buffers.get((device.index, stream))
+    if buf is None or buf.numel() < need:
+        buf = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        _lp_buffers[(device.index, stream)] = buf
+    return buf, need
 
 
 def logprobs(y: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0) -> LogProbs:
@@ -625,17 +670,14 @@ def logprobs(y: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0) 
         return r
     if n == 0:
         raise ValueError("y has no columns")
-    with torch.cuda.device(y.device):
-        need = ctypes.c_uint64(0)
-        _check(lib().w12_logprobs_scratch(m, n, top, flags, ctypes.byref(need)))
-        # from torch's allocator, so every call in flight and every captured graph has its own
-        scratch = torch.empty(need.value, dtype=torch.uint8, device=y.device) if need.value else None
+    with _on_device(y.device):
+        stream = _stream_handle(y.device)
+        scratch, nbytes = _lp_scratch(m, n, top, flags, y.device, stream)
         _check(lib().w12_logprobs(y.data_ptr(), m, n, y.stride(0) if m > 1 else n,
                                   tokens.data_ptr() if nt else None, nt, top,
                                   r.logp.data_ptr() if nt else None, r.entropy.data_ptr(),
                                   r.top_index.data_ptr() if top else None,
-                                  r.top_logp.data_ptr() if top else None, _ptr(scratch), need.value, flags,
-                                  _stream_handle(y.device)))
+                                  r.top_logp.data_ptr() if top else None, _ptr(scratch), nbytes, flags, stream))
     return r
 
 
