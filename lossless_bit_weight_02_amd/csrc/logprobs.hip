@@ -33,6 +33,7 @@ namespace w12 {
 constexpr int kLpCap = 256;                      // keys of a wave's candidate list
 constexpr int kLpWaves = 4;
 constexpr int kLpElems = 16;                     // logits of a lane per batch
+constexpr int kLpCountStep = 32;                 // rows' counts 128 bytes apart: counts of one line wait for each other
 constexpr int kLpAhead = 4;                      // keys of a part loaded together when parts join
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
@@ -91,20 +92,54 @@ __device__ __forceinline__ float lp_value(uint32_t ord) {
   return __uint_as_float((ord & 0x80000000u) ? (ord & 0x7FFFFFFFu) : ~ord);
 }
 
-// (M, s, T) of two runs into one (see the top); -Inf: a run without any logit above -Inf.
-__device__ __forceinline__ void lp_join(float& M, float& s, float& T, float Mb, float sb, float Tb) {
-  const bool sw = Mb > M;
-  const float Mh = sw ? Mb : M, sh = sw ? sb : s, Th = sw ? Tb : T;
-  const float Ml = sw ? M : Mb, sl = sw ? s : sb, Tl = sw ? T : Tb;
-  M = Mh;
-  if (Ml == -INFINITY) {
-    s = sl != sl ? sl : sh;                        // (a NaN among the run's logits stays)
-    T = Th;
-    return;
+// Reductions over the wave's 64 lanes by DPP (row shifts within 16 lanes, then the two row
+// broadcasts); every lane gets the result.  (As shuffles through LDS each cost about 600 cycles.)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_f(float identity, float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(identity), __float_as_uint(v), CTRL, ROWS,
+                                                     0xF, false));
+}
+__device__ __forceinline__ float last_lane(float v) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  const float lo = -INFINITY;
+  v = fmaxf(v, dpp_f<0x111, 0xF>(lo, v));          // row_shr:1
+  v = fmaxf(v, dpp_f<0x112, 0xF>(lo, v));
+  v = fmaxf(v, dpp_f<0x114, 0xF>(lo, v));
+  v = fmaxf(v, dpp_f<0x118, 0xF>(lo, v));
+  v = fmaxf(v, dpp_f<0x142, 0xA>(lo, v));          // row_bcast:15 into rows 1, 3
+  v = fmaxf(v, dpp_f<0x143, 0xC>(lo, v));          // row_bcast:31 into rows 2, 3
+  return last_lane(v);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_f<0x111, 0xF>(0.0f, v);
+  v += dpp_f<0x112, 0xF>(0.0f, v);
+  v += dpp_f<0x114, 0xF>(0.0f, v);
+  v += dpp_f<0x118, 0xF>(0.0f, v);
+  v += dpp_f<0x142, 0xA>(0.0f, v);
+  v += dpp_f<0x143, 0xC>(0.0f, v);
+  return last_lane(v);
+}
+
+// The lanes' runs (M, s, T) into one (see the top), the same in every lane; M = -Inf: a run without
+// any logit above -Inf (its s is 0, or NaN if it has a NaN).
+__device__ __forceinline__ void lp_join(float& M, float& s, float& T) {
+  const float Mx = wave_max(M);
+  const uint64_t own = __ballot(M == Mx);
+  const int owner = own ? __ffsll((unsigned long long)own) - 1 : 0;
+  const float d = M - Mx, f = lp_exp(d), g = 1.0f + s;
+  float s2 = s, T2 = T;
+  if (M == -INFINITY) {
+    s2 = s != s ? s : 0.0f;
+    T2 = 0.0f;
+  } else if ((int)(threadIdx.x & 63) != owner) {
+    s2 = f * g;
+    T2 = f > 0.0f ? f * (T + g * d) : f != f ? f : 0.0f;   // (g d may overflow where f is 0)
   }
-  const float d = Ml - Mh, f = lp_exp(d);
-  s = sh + f * (1.0f + sl);
-  T = f > 0.0f ? Th + f * (Tl + (1.0f + sl) * d) : (f != f ? f : Th);
+  M = Mx;
+  s = wave_sum(s2);
+  T = wave_sum(T2);
 }
 
 // A wave's candidates for the K best keys: a list in LDS, and a bound.
@@ -127,8 +162,12 @@ struct LpTop {
       rank[q] = 0;
     }
     if (cnt <= 64) {
-#pragma unroll 8
-      for (int i = 0; i < cnt; ++i) rank[0] += list[i] > key[0] ? 1 : 0;
+      const uint32_t lo = (uint32_t)key[0], hi = (uint32_t)(key[0] >> 32);
+      for (int i = 0; i < cnt; ++i) {
+        const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, i) << 32 |
+                           (uint32_t)__builtin_amdgcn_readlane(lo, i);
+        rank[0] += o > key[0] ? 1 : 0;
+      }
     } else {
 #pragma unroll 4
       for (int i = 0; i < cnt; ++i) {
@@ -157,21 +196,56 @@ struct LpTop {
   }
 };
 
-// The K-th largest of the 64 lanes' values, bit by bit from the top.
-__device__ __forceinline__ uint32_t lp_kth(uint32_t v, int K) {
+// A bound that at least K of the lanes' values (N a lane) reach: the K-th largest, bit by bit from
+// the top, to 16 bits where that leaves at most 4 values more (a bound a little low costs a
+// candidate or two, the other 16 steps as much as ten), else to all 32.
+template <int N>
+__device__ __forceinline__ uint32_t lp_kth(const uint32_t (&v)[N], int K) {
   uint32_t t = 0;
+  const auto reach = [&](uint32_t c) {
+    int k = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) k += __popcll(__ballot(v[i] >= c));
+    return k;
+  };
 #pragma unroll 8
-  for (int b = 31; b >= 0; --b) {
+  for (int b = 31; b >= 16; --b) {
     const uint32_t c = t | (1u << b);
-    if (__popcll(__ballot(v >= c)) >= K) t = c;
+    if (reach(c) >= K) t = c;
+  }
+  if (reach(t) > K + 4 || K > 64 * N - 8) {
+#pragma unroll 8
+    for (int b = 15; b >= 0; --b) {
+      const uint32_t c = t | (1u << b);
+      if (reach(c) >= K) t = c;
+    }
   }
   return t;
 }
 
+struct LpToken {
+  float x;
+  bool real;
+};
+// The logit of token j of the row.
+template <bool BF>
+__device__ __forceinline__ LpToken lp_token(const LpArgs& a, int64_t row, int j) {
+  const int64_t at = row * a.nt + j;
+  const int64_t t = a.tok64 ? static_cast<const int64_t*>(a.tokens)[at]
+                            : (int64_t)static_cast<const int32_t*>(a.tokens)[at];
+  LpToken r = {0.0f, t >= 0 && t < a.n};
+  if (r.real) {
+    const int64_t o = row * a.ldy + t;
+    r.x = BF ? bf16_to_float(static_cast<const uint16_t*>(a.y)[o]) : static_cast<const float*>(a.y)[o];
+  }
+  return r;
+}
+
 // Outputs of a row from its joined sums and (top > 0) its K best keys in descending order.
+// tok: token `lane` of the row, loaded ahead.
 template <bool BF>
 __device__ __forceinline__ void lp_finish(const LpArgs& a, int64_t row, float M, float s, float T,
-                                          const uint64_t* best, int lane) {
+                                          const uint64_t* best, LpToken tok, int lane) {
   // a row of -Inf alone has no distribution: log probabilities -Inf, entropy 0; one with +Inf or
   // NaN: all NaN
   const bool none = M == -INFINITY && s == s;
@@ -180,16 +254,9 @@ __device__ __forceinline__ void lp_finish(const LpArgs& a, int64_t row, float M,
   const float ls = log1pf(s);
   const auto lp = [&](float x) { return bad ? nan : none ? -INFINITY : (x - M) - ls; };
   for (int j = lane; j < a.nt; j += 64) {
-    const int64_t at = row * a.nt + j;
-    const int64_t t = a.tok64 ? static_cast<const int64_t*>(a.tokens)[at]
-                              : (int64_t)static_cast<const int32_t*>(a.tokens)[at];
-    float v = -INFINITY;                           // a token outside the vocabulary: probability 0
-    if (t >= 0 && t < a.n) {
-      const int64_t o = row * a.ldy + t;
-      v = BF ? bf16_to_float(static_cast<const uint16_t*>(a.y)[o]) : static_cast<const float*>(a.y)[o];
-      v = lp(v);
-    }
-    a.logp[at] = v;
+    if (j >= 64) tok = lp_token<BF>(a, row, j);
+    // (a token outside the vocabulary has probability 0)
+    a.logp[row * a.nt + j] = tok.real ? lp(tok.x) : -INFINITY;
   }
   if (lane == 0) a.ent[row] = bad ? nan : none ? 0.0f : ls - T / (1.0f + s);
   for (int j = lane; j < a.top; j += 64) {
@@ -207,8 +274,11 @@ void k_logprobs(LpArgs a) {
   constexpr int Q = E / V;                         // its loads
   constexpr int B = 64 * E;                        // logits of a wave per batch
   __shared__ uint64_t s_list[kLpWaves][kLpCap];
+  __shared__ uint64_t s_best[kLpCap];
+  __shared__ float s_max[kLpWaves][64];
   __shared__ float s_run[kLpWaves][4];
   __shared__ int s_cnt[kLpWaves];
+  __shared__ uint32_t s_seen[kLpWaves];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t row = blockIdx.x / a.splits;
@@ -267,6 +337,8 @@ void k_logprobs(LpArgs a) {
   constexpr int64_t kStep = (int64_t)kLpWaves * B;
   u32x4 raw[Q];
   if (c < c1) load(c, raw);
+  LpToken tok = {0.0f, false};
+  if (w == 0 && lane < a.nt) tok = lp_token<BF>(a, row, lane);
   for (; c < c1; c += kStep) {
     float x[E];
 #pragma unroll
@@ -286,9 +358,7 @@ void k_logprobs(LpArgs a) {
     for (int e = 1; e < E; ++e) mx = fmaxf(mx, x[e]);   // (a NaN is passed over)
     if (__ballot(mx > M)) {
       // a new maximum: the sums so far relative to it, and one logit that equals it left out
-      float mn = mx;
-#pragma unroll
-      for (int sh = 32; sh >= 1; sh /= 2) mn = fmaxf(mn, __shfl_xor(mn, sh));
+      const float mn = wave_max(mx);
       if (M > -INFINITY) {
         fold();
         const float d = M - mn, f = lp_exp(d);
@@ -345,7 +415,7 @@ void k_logprobs(LpArgs a) {
         // twice as many logits, each cheaper than the bound itself
         float lowf = thrf;
         const auto bound = [&]() {
-          const uint32_t kth = a.top == 1 ? lp_order(M) : lp_kth(lp_order(lmax), a.top);
+          const uint32_t kth = a.top == 1 ? lp_order(M) : lp_kth<1>({lp_order(lmax)}, a.top);
           if (kth > top.seen) top.seen = kth;
           // earlier batches have lower indices: of the logits equal to a bound they reached none
           // can enter (thrf), of those equal to one that this batch reached the first can
@@ -419,42 +489,59 @@ void k_logprobs(LpArgs a) {
             if (full < E) top.cut(lane);
           }
         }
-        // later batches: only above the bound (its order's successor; nothing is above a NaN)
+        // later batches: only above the bound (its order's successor; nothing is above a NaN, and the
+        // order of -Inf is the lowest a logit has)
         if (top.seen == 0xFFFFFFFFu) closed = true;
-        else if (top.seen > 0) thrf = lp_value(top.seen + 1);
-        if (top.seen >= 0xFF800000u && top.seen < 0xFFFFFFFFu) thrf = INFINITY;   // above +Inf: NaN only
+        else if (top.seen >= 0xFF800000u) thrf = INFINITY;
+        else if (top.seen >= 0x007FFFFFu) thrf = lp_value(top.seen + 1);
       }
     }
   }
 
   fold();
-  // the lanes' sums (relative to the same M) in a fixed order
-#pragma unroll
-  for (int sh = 32; sh >= 1; sh /= 2) {
-    s += __shfl_xor(s, sh);
-    T += __shfl_xor(T, sh);
-  }
-  if (a.top > 0) top.cut(lane);
+  // the lanes' sums (relative to the same M) in a fixed order, then the waves'
+  s = wave_sum(s);
+  T = wave_sum(T);
   if (lane == 0) {
     s_run[w][0] = M;
     s_run[w][1] = s;
     s_run[w][2] = T;
     s_cnt[w] = top.cnt;
+    s_seen[w] = top.seen;
   }
+  if (a.top > 0) s_max[w][lane] = lmax;
   __syncthreads();
   if (w != 0) return;
-  for (int v = 1; v < kLpWaves; ++v) lp_join(M, s, T, s_run[v][0], s_run[v][1], s_run[v][2]);
+  M = lane < kLpWaves ? s_run[lane][0] : -INFINITY;
+  s = lane < kLpWaves ? s_run[lane][1] : 0.0f;
+  T = lane < kLpWaves ? s_run[lane][2] : 0.0f;
+  lp_join(M, s, T);
+  top.list = s_best;
+  top.cnt = 0;
   if (a.top > 0) {
-    // (at most 64 keys from each wave: they fit the first wave's list)
-    for (int v = 1; v < kLpWaves; ++v) {
-      const int cv = s_cnt[v];
-      if (lane < cv) top.list[top.cnt + lane] = s_list[v][lane];
-      top.cnt += cv;
+    // one bound for the workgroup, and the keys of all four lists at or above it
+    uint32_t lm[kLpWaves];
+#pragma unroll
+    for (int v = 0; v < kLpWaves; ++v) {
+      lm[v] = lp_order(s_max[v][lane]);
+      top.seen = s_seen[v] > top.seen ? s_seen[v] : top.seen;
+    }
+    const uint32_t kth = lp_kth<kLpWaves>(lm, a.top);
+    top.seen = __builtin_amdgcn_readfirstlane(kth > top.seen ? kth : top.seen);
+    for (int v = 0; v < kLpWaves; ++v) {
+      const int cv = __builtin_amdgcn_readfirstlane(s_cnt[v]);
+      for (int i = 0; i < cv; i += 64) {
+        const uint64_t key = i + lane < cv ? s_list[v][i + lane] : 0;
+        const bool ok = i + lane < cv && (uint32_t)(key >> 32) >= top.seen;
+        const uint64_t bl = __ballot(ok);
+        if (!top.fits(bl)) top.cut(lane);
+        top.put(ok, bl, key, lane);
+      }
     }
     top.cut(lane);
   }
   if (a.splits == 1) {
-    lp_finish<BF>(a, row, M, s, T, top.list, lane);
+    lp_finish<BF>(a, row, M, s, T, top.list, tok, lane);
     return;
   }
   // ---- several workgroups: this one's part to the scratch; the last of the row joins them ----
@@ -466,11 +553,11 @@ void k_logprobs(LpArgs a) {
   if (lane < a.top) dev_store(a.keys + at * a.top + lane, lane < top.cnt ? top.list[lane] : (uint64_t)0);
   stores_done();
   uint32_t done = 0;
-  if (lane == 0) done = __hip_atomic_fetch_add(a.count + row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (lane == 0) done = __hip_atomic_fetch_add(a.count + row * kLpCountStep, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   done = __builtin_amdgcn_readfirstlane(done);
   if (done + 1 != (uint32_t)a.splits) return;
   asm volatile("" ::: "memory");
-  if (lane == 0) dev_store(a.count + row, 0u);     // zero again for the next call
+  if (lane == 0) dev_store(a.count + row * kLpCountStep, 0u);     // zero again for the next call
   M = -INFINITY;
   s = T = 0.0f;
   if (lane < a.splits) {
@@ -483,22 +570,12 @@ void k_logprobs(LpArgs a) {
   uint64_t key[kLpAhead];
 #pragma unroll
   for (int r = 0; r < kLpAhead; ++r) key[r] = lane < a.splits && r < a.top ? dev_load(keys + r) : 0;
-#pragma unroll
-  for (int sh = 1; sh < 64; sh *= 2) {
-    // the lower lane's run first on both sides, so all lanes hold the same bits
-    const float Mo = __shfl_xor(M, sh), so = __shfl_xor(s, sh), To = __shfl_xor(T, sh);
-    const bool up = (lane & sh) != 0;
-    float M2 = up ? Mo : M, s2 = up ? so : s, T2 = up ? To : T;
-    lp_join(M2, s2, T2, up ? M : Mo, up ? s : so, up ? T : To);
-    M = M2;
-    s = s2;
-    T = T2;
-  }
+  lp_join(M, s, T);
   if (a.top > 0) {
     // each part's keys descend: the K-th of their firsts bounds the rest, and a part whose next key
     // is below the bound is done
     top.cnt = 0;
-    top.seen = lp_kth((uint32_t)(key[0] >> 32), a.top);
+    top.seen = lp_kth<1>({(uint32_t)(key[0] >> 32)}, a.top);
     bool more = true;
     for (int r0 = 0; r0 < a.top && more; r0 += kLpAhead) {
       if (r0 > 0) {
@@ -517,7 +594,7 @@ void k_logprobs(LpArgs a) {
     }
     top.cut(lane);
   }
-  lp_finish<BF>(a, row, M, s, T, top.list, lane);
+  lp_finish<BF>(a, row, M, s, T, top.list, tok, lane);
 }
 
 constexpr int kLpPerCu = 4;                      // workgroups wanted per CU
@@ -537,7 +614,7 @@ static void lp_plan(const DevInfo& di, int64_t m, int64_t n, int* splits, int64_
 }
 
 // The counts of the rows that can be split (fewer rows than workgroups wanted), ahead of the parts.
-static uint64_t lp_counts(const DevInfo& di) { return (uint64_t)di.cus * kLpPerCu * sizeof(uint32_t); }
+static uint64_t lp_counts(const DevInfo& di) { return (uint64_t)di.cus * kLpPerCu * kLpCountStep * sizeof(uint32_t); }
 
 uint64_t logprobs_scratch(const DevInfo& di, int64_t m, int64_t n, int top) {
   int splits;

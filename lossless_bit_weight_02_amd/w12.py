@@ -632,7 +632,7 @@ def _lp_scratch(m, n, top, flags, device, stream):
         return torch.zeros(need, dtype=torch.uint8, device=device), need
     buf = _lp_buffers.get((device.index, stream))
     if buf is None or buf.numel() < need:
-        buf = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        buf = torch.zeros(max(need, 1 << 18), dtype=torch.uint8, device=device)
         _lp_buffers[(device.index, stream)] = buf
     return buf, need
 
