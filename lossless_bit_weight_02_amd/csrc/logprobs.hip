@@ -11,20 +11,24 @@
 // Two runs (M, s, T) of a row join into one with the larger M: with f = e^(M_b - M_a), d = M_b - M_a,
 //   s = s_a + f (1 + s_b),   T = T_a + f (T_b + (1 + s_b) d).
 //
-// Work split.  A row's logits are split over S workgroups of 4 waves (S = 1 when the rows alone
-// fill the chip), a workgroup's part over its waves batch by batch: 64 lanes x 16 logits per batch in
-// 16-byte loads, the next batch in flight.  The running maximum
-// is the wave's (one compare per batch finds the rare batch that raises it), sums are each lane's
-// own and join at the end in a fixed order.  With S > 1 each workgroup leaves its part in the
-// caller's scratch and counts itself off; the row's last one joins the parts in part order, lane
-// by part, so the result does not depend on which came last, and there is no second launch.
+// Two kernels share the rest.  Rows that fill the chip by themselves are streamed (k_logprobs): a
+// workgroup of 4 waves takes a row (or a few parts of one), each wave batch after batch of 64 lanes
+// x 16 logits in 16-byte loads with the next batch in flight; the running maximum is the wave's (one
+// compare per batch finds the rare batch that raises it), sums are each lane's own.  Fewer rows are
+// cut into parts of 4096 logits that a workgroup holds in registers (k_logprobs_part): the maximum
+// comes first, so nothing is put right afterwards, and the whole part shares one bound for its
+// candidates below.  The parts of a row go to the caller's scratch, each workgroup counts itself
+// off, and the row's last one joins them in part order, lane by part, so the result does not depend
+// on which came last, and there is no second launch.  At one row what a launch costs is latency: the
+// code runs once, so every line of it is fetched for the occasion, and short code beats few
+// instructions.
 //
 // Top alternatives.  A candidate is a 64-bit key: the logit's order (NaN above +Inf, -0 as +0), then
 // the complement of its index, so equal logits go by the lower index and every order is total.
-// Each lane keeps the largest logit it has seen; the K-th largest of the 64 lanes' is a bound that
-// K logits already reach, so a batch without a logit above it needs one compare in all.  Otherwise
-// the batch's logits at or above the new bound are appended to the wave's list in LDS, and a full
-// list is cut back to its K best (each key's rank is the number of larger keys).
+// The K-th largest of the lanes' own maxima is a bound that K logits already reach; logits at or
+// above it are the candidates (about 1.2 K of them for a part, and about 1.35 K / i of a streaming
+// wave's i-th batch, whose other logits cost one compare per batch).  They are collected in an LDS
+// list; its K best are picked by rank, the number of larger keys.
 #include "w12_device.hpp"
 #include "w12_launch.hpp"
 
@@ -33,6 +37,7 @@ namespace w12 {
 constexpr int kLpCap = 256;                      // keys of a wave's candidate list
 constexpr int kLpWaves = 4;
 constexpr int kLpElems = 16;                     // logits of a lane per batch
+constexpr int kLpBatch = 64 * kLpElems;          // logits of a wave per batch
 constexpr int kLpCountStep = 32;                 // rows' counts 128 bytes apart: counts of one line wait for each other
 constexpr int kLpAhead = 4;                      // keys of a part loaded together when parts join
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
@@ -92,6 +97,10 @@ __device__ __forceinline__ float lp_value(uint32_t ord) {
   return __uint_as_float((ord & 0x80000000u) ? (ord & 0x7FFFFFFFu) : ~ord);
 }
 
+__device__ __forceinline__ uint64_t lp_key(float x, int64_t column) {
+  return (uint64_t)lp_order(x) << 32 | (0xFFFFFFFFu - (uint32_t)column);
+}
+
 // Reductions over the wave's 64 lanes by DPP (row shifts within 16 lanes, then the two row
 // broadcasts); every lane gets the result.  (As shuffles through LDS each cost about 600 cycles.)
 template <int CTRL, int ROWS>
@@ -120,6 +129,17 @@ __device__ __forceinline__ float wave_sum(float v) {
   v += dpp_f<0x142, 0xA>(0.0f, v);
   v += dpp_f<0x143, 0xC>(0.0f, v);
   return last_lane(v);
+}
+
+// Inclusive sum over the lanes up to each.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
 }
 
 // The lanes' runs (M, s, T) into one (see the top), the same in every lane; M = -Inf: a run without
@@ -196,31 +216,202 @@ struct LpTop {
   }
 };
 
-// A bound that at least K of the lanes' values (N a lane) reach: the K-th largest, bit by bit from
-// the top, to 16 bits where that leaves at most 4 values more (a bound a little low costs a
+// A bound that at least K of the lanes' values (N a lane) reach, and that is at most their K-th
+// largest: found bit by bit, from the leading bits of `hi` (at or above every value) where K values
+// share them, down to 16 bits where that leaves at most 4 values more (a bound a little low costs a
 // candidate or two, the other 16 steps as much as ten), else to all 32.
 template <int N>
-__device__ __forceinline__ uint32_t lp_kth(const uint32_t (&v)[N], int K) {
-  uint32_t t = 0;
+__device__ __forceinline__ uint32_t lp_kth(const uint32_t (&v)[N], int K, uint32_t hi) {
   const auto reach = [&](uint32_t c) {
     int k = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) k += __popcll(__ballot(v[i] >= c));
     return k;
   };
-#pragma unroll 8
-  for (int b = 31; b >= 16; --b) {
+  // 22 low bits of a float's order: a half of a binade; 25: four binades
+  uint32_t t = 0;
+  int b = 31;
+  if (reach(hi >> 22 << 22) >= K) {
+    t = hi >> 22 << 22;
+    b = 21;
+  } else if (reach(hi >> 25 << 25) >= K) {
+    t = hi >> 25 << 25;
+    b = 24;
+  }
+  // (rolled: this runs once or twice in a short launch, where each line of code is fetched anew)
+#pragma unroll 1
+  for (; b >= 0; --b) {
     const uint32_t c = t | (1u << b);
     if (reach(c) >= K) t = c;
-  }
-  if (reach(t) > K + 4 || K > 64 * N - 8) {
-#pragma unroll 8
-    for (int b = 15; b >= 0; --b) {
-      const uint32_t c = t | (1u << b);
-      if (reach(c) >= K) t = c;
-    }
+    if (b == 16 && K <= 64 * N - 8 && reach(t) <= K + 4) break;
   }
   return t;
+}
+
+// Element e of a lane's batch at column c of the row: column c + 64 V (e / V) + V lane + e % V, with V
+// the logits of a 16-byte load.  Past c1 the batch reads -Inf.
+template <bool BF>
+struct LpBatch {
+  static constexpr int V = BF ? 8 : 4, Q = kLpElems / V;
+  u32x4 raw[Q];
+  static __device__ __forceinline__ int64_t column(int64_t c, int e, int lane) {
+    return c + 64 * V * (e / V) + V * lane + e % V;
+  }
+  __device__ __forceinline__ void load(const uint8_t* yr, int64_t c, int64_t c1, int lane) {
+    if (c + kLpBatch <= c1) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const uint8_t* src = yr + (c + 64 * V * q + V * lane) * (BF ? 2 : 4);
+        if constexpr (BF) raw[q] = *reinterpret_cast<const u32x4_a2*>(src);
+        else raw[q] = *reinterpret_cast<const u32x4_a4*>(src);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t cc = c + 64 * V * q + V * lane + (V / 4) * i;
+          if constexpr (BF) {
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(yr);
+            const uint32_t lo = cc < c1 ? src[cc] : 0xFF80u, hi = cc + 1 < c1 ? src[cc + 1] : 0xFF80u;
+            raw[q][i] = lo | hi << 16;
+          } else {
+            raw[q][i] = cc < c1 ? reinterpret_cast<const uint32_t*>(yr)[cc] : 0xFF800000u;
+          }
+        }
+    }
+  }
+  __device__ __forceinline__ void values(float (&x)[kLpElems]) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (BF) {
+          x[8 * q + 2 * i] = bf16_to_float(raw[q][i] & 0xFFFFu);
+          x[8 * q + 2 * i + 1] = __uint_as_float(raw[q][i] & 0xFFFF0000u);
+        } else {
+          x[4 * q + i] = __uint_as_float(raw[q][i]);
+        }
+      }
+  }
+};
+
+// Sums of a lane's batch under the maximum M (|M| >= 1e37 too); `leave`: but for one logit equal to M.
+__device__ __forceinline__ void lp_sums(const float (&x)[kLpElems], float M, bool leave, float& s, float& T) {
+#pragma unroll
+  for (int e = 0; e < kLpElems; ++e) {
+    const float d = x[e] - M;
+    float p = lp_exp(d);
+    if (leave && x[e] == M) {
+      p = 0.0f;
+      leave = false;
+    }
+    s += p;
+    T = fmaf(p, fmaxf(d, -200.0f), T);             // (a masked logit: 0 times a finite number)
+  }
+}
+// The same for |M| < 1e37 in units of log 2, the product and the difference in one rounding:
+// a = x L - fl(M L), which is (x - M) L + del with one del = M L - fl(M L) for all logits under this
+// maximum; lp_fold puts it right.
+__device__ __forceinline__ void lp_sums2(const float (&x)[kLpElems], float ML, float& s, float& T) {
+#pragma unroll
+  for (int e = 0; e < kLpElems; ++e) {
+    const float d = fmaf(x[e], kLog2e, -ML);
+    const float p = __builtin_amdgcn_exp2f(d);
+    s += p;
+    T = fmaf(p, fmaxf(d, -300.0f), T);
+  }
+}
+// Sums (sf, Tf) of lp_sums2 into (s, T): with p = 2^-del p' the true terms, s += 2^-del s',
+// T += 2^-del (T' - del s') / L.
+__device__ __forceinline__ void lp_fold(float M, float ML, float sf, float Tf, float& s, float& T) {
+  const float del = fmaf(M, kLog2e, -ML), f = 1.0f - del * kLn2;
+  s += f * sf;
+  T += f * (Tf - del * sf) * kLn2;
+}
+
+// The candidates (at or above lowf, or NaN) of a wave's batch at column c, elements from..15, into the
+// wave's list when they may be more than it holds, or the batch passes the part's end: of those
+// equal to the bound (a masked row: all of them) only the K of the lowest indices can stay.
+template <bool BF>
+__device__ __forceinline__ void lp_enter(LpTop& top, const float (&x)[kLpElems], float lowf, int from, int64_t c,
+                                         int64_t c1, int lane) {
+  constexpr int V = LpBatch<BF>::V, Q = LpBatch<BF>::Q, E = kLpElems;
+  uint32_t in = 0, eq = 0;                         // a bit per element
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const bool ok = e >= from && !(x[e] < lowf) && LpBatch<BF>::column(c, e, lane) < c1;
+    in |= (ok ? 1u : 0u) << e;
+    eq |= (ok && x[e] == lowf ? 1u : 0u) << e;
+  }
+  int before = 0;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    uint32_t g = eq & (((1u << V) - 1u) << (V * q));
+    const int mine = __popc(g);
+    int pre = before;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint64_t bl = __ballot((mine >> b) & 1);
+      pre += __popcll(bl & ((1ull << lane) - 1)) << b;
+      before += __popcll(bl) << b;
+    }
+    int drop = mine - (top.K - pre > 0 ? top.K - pre : 0);
+    while (drop-- > 0) {
+      const uint32_t high = 1u << (31 - __clz(g));
+      g ^= high;
+      in ^= high;
+    }
+  }
+  while (from < E) {
+    int full = E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const bool ok = (in >> e) & 1u;
+      const uint64_t bl = __ballot(ok);
+      if (bl == 0 || e < from || full < E) continue;
+      if (!top.fits(bl)) {
+        full = e;
+        continue;
+      }
+      top.put(ok, bl, lp_key(x[e], LpBatch<BF>::column(c, e, lane)), lane);
+    }
+    from = full;
+    if (full < E) top.cut(lane);
+  }
+}
+
+// The four waves' lists into `best` (wave 0), its K largest keys in descending order: above one
+// bound, the highest of the waves' own, or where the lists are long the K-th largest of the 256
+// lanes' maxima.
+__device__ __forceinline__ void lp_merge(LpTop& top, uint64_t* best, const uint64_t (*lists)[kLpCap], const int* cnt,
+                                         const uint32_t* seen, const float (*lmax)[64], float M, int lane) {
+  top.list = best;
+  top.cnt = 0;
+  int all = 0;
+  for (int v = 0; v < kLpWaves; ++v) {
+    top.seen = seen[v] > top.seen ? seen[v] : top.seen;
+    all += cnt[v];
+  }
+  if (all > 64) {
+    uint32_t lm[kLpWaves];
+#pragma unroll
+    for (int v = 0; v < kLpWaves; ++v) lm[v] = lp_order(lmax[v][lane]);
+    const uint32_t kth = lp_kth<kLpWaves>(lm, top.K, lp_order(M));
+    top.seen = kth > top.seen ? kth : top.seen;
+  }
+  top.seen = __builtin_amdgcn_readfirstlane(top.seen);
+  for (int v = 0; v < kLpWaves; ++v) {
+    const int cv = __builtin_amdgcn_readfirstlane(cnt[v]);
+    for (int i = 0; i < cv; i += 64) {
+      const uint64_t key = i + lane < cv ? lists[v][i + lane] : 0;
+      const bool ok = i + lane < cv && (uint32_t)(key >> 32) >= top.seen;
+      const uint64_t bl = __ballot(ok);
+      if (!top.fits(bl)) top.cut(lane);
+      top.put(ok, bl, key, lane);
+    }
+  }
+  top.cut(lane);
 }
 
 struct LpToken {
@@ -266,13 +457,74 @@ __device__ __forceinline__ void lp_finish(const LpArgs& a, int64_t row, float M,
   }
 }
 
+// One wave, the end of a workgroup: the outputs of a row in one part; or this part to the scratch,
+// and if it is the row's last, the parts joined.  Parts move by device-scope atomic stores and
+// loads, which other dies' caches see as they are, so no cache needs writing back or invalidating
+// (a device-scope fence per workgroup cost 64 rows of 152064 36.6 us in all against 19.2); the wait
+// orders the part before the count.
+template <bool BF>
+__device__ __forceinline__ void lp_end(const LpArgs& a, int64_t row, int sp, float M, float s, float T, LpTop& top,
+                                       LpToken tok, int lane) {
+  if (a.splits > 1) {
+    const int64_t at = row * a.splits + sp;
+    if (lane < 3)
+      dev_store(reinterpret_cast<uint32_t*>(a.parts + at) + lane, __float_as_uint(lane == 0 ? M : lane == 1 ? s : T));
+    if (lane < a.top) dev_store(a.keys + at * a.top + lane, lane < top.cnt ? top.list[lane] : (uint64_t)0);
+    stores_done();
+    uint32_t done = 0;
+    if (lane == 0)
+      done = __hip_atomic_fetch_add(a.count + row * kLpCountStep, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    done = __builtin_amdgcn_readfirstlane(done);
+    if (done + 1 != (uint32_t)a.splits) return;
+    asm volatile("" ::: "memory");
+    if (lane == 0) dev_store(a.count + row * kLpCountStep, 0u);   // zero again for the next call
+    M = -INFINITY;
+    s = T = 0.0f;
+    const bool mine = lane < a.splits;
+    if (mine) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.parts + row * a.splits + lane);
+      M = __uint_as_float(dev_load(p));
+      s = __uint_as_float(dev_load(p + 1));
+      T = __uint_as_float(dev_load(p + 2));
+    }
+    const uint64_t* keys = a.keys + (row * a.splits + lane) * a.top;
+    uint64_t key[kLpAhead];
+#pragma unroll
+    for (int r = 0; r < kLpAhead; ++r) key[r] = mine && r < a.top ? dev_load(keys + r) : 0;
+    const uint32_t first = lp_order(M);
+    lp_join(M, s, T);
+    if (a.top > 0) {
+      // each part's keys descend: the K-th of the parts' maxima bounds the rest, and a part whose
+      // next key is below the bound is done
+      top.cnt = 0;
+      const uint32_t hi = lp_order(M);
+      top.seen = a.top == 1 ? hi : lp_kth<1>({first}, a.top, hi);
+      bool more = true;
+      for (int r0 = 0; r0 < a.top && more; r0 += kLpAhead) {
+        if (r0 > 0) {
+#pragma unroll
+          for (int r = 0; r < kLpAhead; ++r) key[r] = mine && r0 + r < a.top ? dev_load(keys + r0 + r) : 0;
+        }
+#pragma unroll
+        for (int r = 0; r < kLpAhead; ++r) {
+          const bool ok = key[r] != 0 && (uint32_t)(key[r] >> 32) >= top.seen;
+          const uint64_t bl = __ballot(ok);
+          if (bl == 0) more = false;
+          if (!more) continue;
+          if (!top.fits(bl)) top.cut(lane);
+          top.put(ok, bl, key[r], lane);
+        }
+      }
+      top.cut(lane);
+    }
+  }
+  lp_finish<BF>(a, row, M, s, T, top.list, tok, lane);
+}
+
 template <bool BF>
 __global__ __launch_bounds__(64 * kLpWaves) __attribute__((amdgpu_waves_per_eu(4)))
 void k_logprobs(LpArgs a) {
-  constexpr int V = BF ? 8 : 4;                    // logits per 16-byte load
-  constexpr int E = kLpElems;                      // logits of a lane per batch
-  constexpr int Q = E / V;                         // its loads
-  constexpr int B = 64 * E;                        // logits of a wave per batch
+  constexpr int E = kLpElems;
   __shared__ uint64_t s_list[kLpWaves][kLpCap];
   __shared__ uint64_t s_best[kLpCap];
   __shared__ float s_max[kLpWaves][64];
@@ -287,43 +539,8 @@ void k_logprobs(LpArgs a) {
   const int64_t c1 = c0 + a.part < a.n ? c0 + a.part : a.n;
   const uint8_t* const yr = static_cast<const uint8_t*>(a.y) + row * a.ldy * (BF ? 2 : 4);
 
-  // element e of the lane's batch at column c: c + 64 V (e / V) + V lane + e % V
-  const auto load = [&](int64_t c, u32x4 v[Q]) {
-    if (c + B <= c1) {
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        const uint8_t* src = yr + (c + 64 * V * q + V * lane) * (BF ? 2 : 4);
-        if constexpr (BF) v[q] = *reinterpret_cast<const u32x4_a2*>(src);
-        else v[q] = *reinterpret_cast<const u32x4_a4*>(src);
-      }
-    } else {                                       // the part's end: -Inf past it
-#pragma unroll
-      for (int q = 0; q < Q; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t cc = c + 64 * V * q + V * lane + (V / 4) * i;
-          if constexpr (BF) {
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(yr);
-            const uint32_t lo = cc < c1 ? src[cc] : 0xFF80u, hi = cc + 1 < c1 ? src[cc + 1] : 0xFF80u;
-            v[q][i] = lo | hi << 16;
-          } else {
-            v[q][i] = cc < c1 ? reinterpret_cast<const uint32_t*>(yr)[cc] : 0xFF800000u;
-          }
-        }
-    }
-  };
-
   float M = -INFINITY, s = 0.0f, T = 0.0f;         // M uniform; s, T the lane's
-  float sf = 0.0f, Tf = 0.0f, ML = 0.0f;           // sums in units of log 2 not yet in s, T; fl(M L)
-  // with p = 2^-del p' the true terms: s += 2^-del s', T += 2^-del (T' - del s') / L
-  const auto fold = [&]() {
-    if (fabsf(M) < 1e37f) {
-      const float del = fmaf(M, kLog2e, -ML), f = 1.0f - del * kLn2;
-      s += f * sf;
-      T += f * (Tf - del * sf) * kLn2;
-      sf = Tf = 0.0f;
-    }
-  };
+  float sf = 0.0f, Tf = 0.0f, ML = 0.0f;           // sums of lp_sums2 not yet in s, T; fl(M L)
   int owner = 0;                                   // the lane that left the maximum out
   LpTop top;
   top.list = s_list[w];
@@ -333,26 +550,16 @@ void k_logprobs(LpArgs a) {
   int batch = 0;
   bool anynan = false, closed = a.top == 0;        // closed: nothing can enter any more
 
-  int64_t c = c0 + (int64_t)w * B;
-  constexpr int64_t kStep = (int64_t)kLpWaves * B;
-  u32x4 raw[Q];
-  if (c < c1) load(c, raw);
+  int64_t c = c0 + (int64_t)w * kLpBatch;
+  constexpr int64_t kStep = (int64_t)kLpWaves * kLpBatch;
+  LpBatch<BF> bt;
+  if (c < c1) bt.load(yr, c, c1, lane);
   LpToken tok = {0.0f, false};
   if (w == 0 && lane < a.nt) tok = lp_token<BF>(a, row, lane);
   for (; c < c1; c += kStep) {
     float x[E];
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (BF) {
-          x[8 * q + 2 * i] = bf16_to_float(raw[q][i] & 0xFFFFu);
-          x[8 * q + 2 * i + 1] = __uint_as_float(raw[q][i] & 0xFFFF0000u);
-        } else {
-          x[4 * q + i] = __uint_as_float(raw[q][i]);
-        }
-      }
-    if (c + kStep < c1) load(c + kStep, raw);      // the next batch, in flight while this one is summed
+    bt.values(x);
+    if (c + kStep < c1) bt.load(yr, c + kStep, c1, lane);   // the next batch, in flight meanwhile
     float mx = x[0];
 #pragma unroll
     for (int e = 1; e < E; ++e) mx = fmaxf(mx, x[e]);   // (a NaN is passed over)
@@ -360,7 +567,8 @@ void k_logprobs(LpArgs a) {
       // a new maximum: the sums so far relative to it, and one logit that equals it left out
       const float mn = wave_max(mx);
       if (M > -INFINITY) {
-        fold();
+        if (fabsf(M) < 1e37f) lp_fold(M, ML, sf, Tf, s, T);
+        sf = Tf = 0.0f;
         const float d = M - mn, f = lp_exp(d);
         if (lane == owner) s += 1.0f;
         T = f > 0.0f ? f * (T + s * d) : s != s ? s : 0.0f;   // (s d may overflow where f is 0)
@@ -369,37 +577,11 @@ void k_logprobs(LpArgs a) {
       M = mn;
       ML = M * kLog2e;
       owner = __ffsll((unsigned long long)__ballot(mx == M)) - 1;
-      bool leave = lane == owner;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float d = x[e] - M;
-        float p = lp_exp(d);
-        if (leave && x[e] == M) {
-          p = 0.0f;
-          leave = false;
-        }
-        s += p;
-        T = fmaf(p, fmaxf(d, -200.0f), T);         // (a masked logit: 0 times a finite number)
-      }
+      lp_sums(x, M, lane == owner, s, T);
     } else if (fabsf(M) < 1e37f) {
-      // in units of log 2, the product and the difference in one rounding: a = x L - fl(M L), which
-      // is (x - M) L + del with one del = M L - fl(M L) for all logits under this maximum (put
-      // right when the maximum changes and at the end)
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float d = fmaf(x[e], kLog2e, -ML);
-        const float p = __builtin_amdgcn_exp2f(d);
-        sf += p;
-        Tf = fmaf(p, fmaxf(d, -300.0f), Tf);       // (a masked logit: 0 times a finite number)
-      }
-    } else if (M > -INFINITY) {                    // (M L could overflow)
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float d = x[e] - M;
-        const float p = lp_exp(d);
-        s += p;
-        T = fmaf(p, fmaxf(d, -200.0f), T);
-      }
+      lp_sums2(x, ML, sf, Tf);
+    } else if (M > -INFINITY) {
+      lp_sums(x, M, false, s, T);
     } else {
       bool bad = false;
 #pragma unroll
@@ -415,7 +597,8 @@ void k_logprobs(LpArgs a) {
         // twice as many logits, each cheaper than the bound itself
         float lowf = thrf;
         const auto bound = [&]() {
-          const uint32_t kth = a.top == 1 ? lp_order(M) : lp_kth<1>({lp_order(lmax)}, a.top);
+          const uint32_t hi = lp_order(M);
+          const uint32_t kth = a.top == 1 ? hi : lp_kth<1>({lp_order(lmax)}, a.top, hi);
           if (kth > top.seen) top.seen = kth;
           // earlier batches have lower indices: of the logits equal to a bound they reached none
           // can enter (thrf), of those equal to one that this batch reached the first can
@@ -423,11 +606,7 @@ void k_logprobs(LpArgs a) {
           if (lowf < thrf) lowf = thrf;
         };
         if (a.top == 1 || (batch & (batch - 1)) == 0) bound();
-        const auto key_of = [&](int e) {
-          const int64_t cc = c + 64 * V * (e / V) + V * lane + e % V;
-          return (uint64_t)lp_order(x[e]) << 32 | (0xFFFFFFFFu - (uint32_t)cc);
-        };
-        int from = c + B > c1 ? 0 : E;             // (the part's end: with the column checks below)
+        int from = c + kLpBatch > c1 ? 0 : E;
         if (from == E) {
 #pragma unroll
           for (int e = 0; e < E; ++e) {
@@ -438,56 +617,12 @@ void k_logprobs(LpArgs a) {
               from = e;
               continue;
             }
-            top.put(ok, bl, key_of(e), lane);
+            top.put(ok, bl, lp_key(x[e], LpBatch<BF>::column(c, e, lane)), lane);
           }
         }
-        if (from < E) {
-          // more than the list holds, or the part's end: the lane's logits that enter, a bit each
+        if (from < E) {                            // more than the list holds, or the part's end
           bound();
-          uint32_t in = 0, eq = 0;
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const bool ok = e >= from && !(x[e] < lowf) && c + 64 * V * (e / V) + V * lane + e % V < c1;
-            in |= (ok ? 1u : 0u) << e;
-            eq |= (ok && x[e] == lowf ? 1u : 0u) << e;
-          }
-          // of those equal to the bound (a masked row: all of them) only the K of the lowest
-          // indices can stay
-          int before = 0;
-#pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            uint32_t g = eq & (((1u << V) - 1u) << (V * q));
-            const int mine = __popc(g);
-            int pre = before;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint64_t bl = __ballot((mine >> b) & 1);
-              pre += __popcll(bl & ((1ull << lane) - 1)) << b;
-              before += __popcll(bl) << b;
-            }
-            int drop = mine - (a.top - pre > 0 ? a.top - pre : 0);
-            while (drop-- > 0) {
-              const uint32_t high = 1u << (31 - __clz(g));
-              g ^= high;
-              in ^= high;
-            }
-          }
-          while (from < E) {
-            int full = E;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              const bool ok = (in >> e) & 1u;
-              const uint64_t bl = __ballot(ok);
-              if (bl == 0 || e < from || full < E) continue;
-              if (!top.fits(bl)) {
-                full = e;
-                continue;
-              }
-              top.put(ok, bl, key_of(e), lane);
-            }
-            from = full;
-            if (full < E) top.cut(lane);
-          }
+          lp_enter<BF>(top, x, lowf, from, c, c1, lane);
         }
         // later batches: only above the bound (its order's successor; nothing is above a NaN, and the
         // order of -Inf is the lowest a logit has)
@@ -498,7 +633,7 @@ void k_logprobs(LpArgs a) {
     }
   }
 
-  fold();
+  if (fabsf(M) < 1e37f) lp_fold(M, ML, sf, Tf, s, T);
   // the lanes' sums (relative to the same M) in a fixed order, then the waves'
   s = wave_sum(s);
   T = wave_sum(T);
@@ -517,111 +652,174 @@ void k_logprobs(LpArgs a) {
   T = lane < kLpWaves ? s_run[lane][2] : 0.0f;
   lp_join(M, s, T);
   top.list = s_best;
-  top.cnt = 0;
-  if (a.top > 0) {
-    // one bound for the workgroup, and the keys of all four lists at or above it
-    uint32_t lm[kLpWaves];
-#pragma unroll
-    for (int v = 0; v < kLpWaves; ++v) {
-      lm[v] = lp_order(s_max[v][lane]);
-      top.seen = s_seen[v] > top.seen ? s_seen[v] : top.seen;
-    }
-    const uint32_t kth = lp_kth<kLpWaves>(lm, a.top);
-    top.seen = __builtin_amdgcn_readfirstlane(kth > top.seen ? kth : top.seen);
-    for (int v = 0; v < kLpWaves; ++v) {
-      const int cv = __builtin_amdgcn_readfirstlane(s_cnt[v]);
-      for (int i = 0; i < cv; i += 64) {
-        const uint64_t key = i + lane < cv ? s_list[v][i + lane] : 0;
-        const bool ok = i + lane < cv && (uint32_t)(key >> 32) >= top.seen;
-        const uint64_t bl = __ballot(ok);
-        if (!top.fits(bl)) top.cut(lane);
-        top.put(ok, bl, key, lane);
-      }
-    }
-    top.cut(lane);
-  }
-  if (a.splits == 1) {
-    lp_finish<BF>(a, row, M, s, T, top.list, tok, lane);
-    return;
-  }
-  // ---- several workgroups: this one's part to the scratch; the last of the row joins them ----
-  // Parts move by device-scope atomic stores and loads, which other dies' caches see as they are, so
-  // no cache needs writing back or invalidating (a device-scope fence per workgroup cost 64 rows
-  // 36.6 us in all against XX); the wait orders the part before the count.
-  const int64_t at = row * a.splits + sp;
-  if (lane < 3) dev_store(reinterpret_cast<uint32_t*>(a.parts + at) + lane, __float_as_uint(lane == 0 ? M : lane == 1 ? s : T));
-  if (lane < a.top) dev_store(a.keys + at * a.top + lane, lane < top.cnt ? top.list[lane] : (uint64_t)0);
-  stores_done();
-  uint32_t done = 0;
-  if (lane == 0) done = __hip_atomic_fetch_add(a.count + row * kLpCountStep, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  done = __builtin_amdgcn_readfirstlane(done);
-  if (done + 1 != (uint32_t)a.splits) return;
-  asm volatile("" ::: "memory");
-  if (lane == 0) dev_store(a.count + row * kLpCountStep, 0u);     // zero again for the next call
-  M = -INFINITY;
-  s = T = 0.0f;
-  if (lane < a.splits) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(a.parts + row * a.splits + lane);
-    M = __uint_as_float(dev_load(p));
-    s = __uint_as_float(dev_load(p + 1));
-    T = __uint_as_float(dev_load(p + 2));
-  }
-  const uint64_t* keys = a.keys + (row * a.splits + lane) * a.top;
-  uint64_t key[kLpAhead];
-#pragma unroll
-  for (int r = 0; r < kLpAhead; ++r) key[r] = lane < a.splits && r < a.top ? dev_load(keys + r) : 0;
-  lp_join(M, s, T);
-  if (a.top > 0) {
-    // each part's keys descend: the K-th of their firsts bounds the rest, and a part whose next key
-    // is below the bound is done
-    top.cnt = 0;
-    top.seen = lp_kth<1>({(uint32_t)(key[0] >> 32)}, a.top);
-    bool more = true;
-    for (int r0 = 0; r0 < a.top && more; r0 += kLpAhead) {
-      if (r0 > 0) {
-#pragma unroll
-        for (int r = 0; r < kLpAhead; ++r) key[r] = lane < a.splits && r0 + r < a.top ? dev_load(keys + r0 + r) : 0;
-      }
-#pragma unroll
-      for (int r = 0; r < kLpAhead; ++r) {
-        const bool ok = key[r] != 0 && (uint32_t)(key[r] >> 32) >= top.seen;
-        const uint64_t bl = __ballot(ok);
-        if (bl == 0) more = false;
-        if (!more) continue;
-        if (!top.fits(bl)) top.cut(lane);
-        top.put(ok, bl, key[r], lane);
-      }
-    }
-    top.cut(lane);
-  }
-  lp_finish<BF>(a, row, M, s, T, top.list, tok, lane);
+  if (a.top > 0) lp_merge(top, s_best, s_list, s_cnt, s_seen, s_max, M, lane);
+  lp_end<BF>(a, row, sp, M, s, T, top, tok, lane);
 }
 
-constexpr int kLpPerCu = 4;                      // workgroups wanted per CU
+// A part of at most kLpWaves kLpBatch logits, held in the workgroup's registers.
+template <bool BF>
+__global__ __launch_bounds__(64 * kLpWaves) void k_logprobs_part(LpArgs a) {
+  constexpr int E = kLpElems;
+  __shared__ uint64_t s_list[kLpWaves][kLpCap];    // each wave's list, where the shared one overflows
+  __shared__ uint64_t s_best[kLpCap];
+  __shared__ float s_max[kLpWaves][64];
+  __shared__ float s_run[kLpWaves][4];
+  __shared__ int s_cnt[kLpWaves];
+  __shared__ uint32_t s_seen[kLpWaves];
+  __shared__ int s_total;                          // keys offered to the shared list
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t row = blockIdx.x / a.splits;
+  const int sp = (int)(blockIdx.x - row * a.splits);
+  const int64_t c0 = sp * a.part;
+  const int64_t c1 = c0 + a.part < a.n ? c0 + a.part : a.n;
+  const uint8_t* const yr = static_cast<const uint8_t*>(a.y) + row * a.ldy * (BF ? 2 : 4);
+  const int64_t c = c0 + (int64_t)w * kLpBatch;
+  LpBatch<BF> bt;
+  bt.load(yr, c, c1, lane);
+  LpToken tok = {0.0f, false};
+  if (w == 0 && lane < a.nt) tok = lp_token<BF>(a, row, lane);
+  if (tid == 0) s_total = 0;
+  float x[E];
+  bt.values(x);
+  float mx = x[0];
+#pragma unroll
+  for (int e = 1; e < E; ++e) mx = fmaxf(mx, x[e]);   // (a NaN is passed over)
+  s_max[w][lane] = mx;
+  const float wm = wave_max(mx);
+  if (lane == 0) s_run[w][0] = wm;
+  __syncthreads();
 
-// Workgroups per row: the whole row in one where the rows fill the chip, otherwise as many parts
-// as give it kLpPerCu workgroups per CU, of at least one batch per wave, and at most 64.
-static void lp_plan(const DevInfo& di, int64_t m, int64_t n, int* splits, int64_t* part) {
-  const int64_t unit = 64 * kLpElems * kLpWaves;
-  const int64_t units = (n + unit - 1) / unit;
-  int64_t want = (int64_t)di.cus * kLpPerCu / m;
-  if (want < 1) want = 1;
-  if (want > units) want = units;
-  if (want > 64) want = 64;
-  const int64_t per = (units + want - 1) / want;
-  *part = per * unit;
-  *splits = (int)((units + per - 1) / per);
+  // the part's maximum; the first lane of the first wave that has it leaves one out
+  float M = -INFINITY;
+  int wo = 0;
+#pragma unroll
+  for (int v = kLpWaves - 1; v >= 0; --v) {
+    const float mv = s_run[v][0];
+    if (mv >= M) {
+      M = mv;
+      wo = v;
+    }
+  }
+  M = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(M)));
+  wo = __builtin_amdgcn_readfirstlane(wo);
+  float s = 0.0f, T = 0.0f;
+  if (M == -INFINITY) {
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) bad |= x[e] != x[e];
+    if (bad) s = __uint_as_float(0x7FC00000u);
+  } else if (w == wo || fabsf(M) >= 1e37f) {
+    const int owner = __ffsll((unsigned long long)__ballot(mx == M)) - 1;
+    lp_sums(x, M, w == wo && lane == owner, s, T);
+  } else {
+    float sf = 0.0f, Tf = 0.0f;
+    const float ML = M * kLog2e;
+    lp_sums2(x, ML, sf, Tf);
+    lp_fold(M, ML, sf, Tf, s, T);
+  }
+  s = wave_sum(s);
+  T = wave_sum(T);
+  if (lane == 0) {
+    s_run[w][1] = s;
+    s_run[w][2] = T;
+  }
+  LpTop top;
+  top.K = a.top;
+  top.list = s_best;
+  float lowf = 0.0f;
+  if (a.top > 0) {
+    const uint32_t hi = lp_order(M);
+    if (a.top == 1) {
+      top.seen = hi;
+    } else {
+      uint32_t lm[kLpWaves];
+#pragma unroll
+      for (int v = 0; v < kLpWaves; ++v) lm[v] = lp_order(s_max[v][lane]);
+      top.seen = lp_kth<kLpWaves>(lm, a.top, hi);
+    }
+    lowf = lp_value(top.seen);                     // (NaN: the comparisons let all through)
+    uint32_t in = 0;                               // a bit per candidate of the lane
+#pragma unroll
+    for (int e = 0; e < E; ++e) in |= (!(x[e] < lowf) ? 1u : 0u) << e;
+    if (c + kLpBatch > c1) {                       // the row's end
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (LpBatch<BF>::column(c, e, lane) >= c1) in &= ~(1u << e);
+    }
+    if (__ballot(in != 0)) {
+      const int mine = __popc(in), upto = wave_scan(mine);
+      const int tot = __builtin_amdgcn_readlane(upto, 63);
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&s_total, tot);
+      at = __builtin_amdgcn_readfirstlane(at);
+      if (at + tot <= kLpCap) {
+        at += upto - mine;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if ((in >> e) & 1u) s_best[at++] = lp_key(x[e], LpBatch<BF>::column(c, e, lane));
+      }
+    }
+  }
+  __syncthreads();
+  const int total = a.top > 0 ? __builtin_amdgcn_readfirstlane(s_total) : 0;
+  if (total > kLpCap) {
+    // more candidates than the shared list holds (many equal to the bound): by each wave's own
+    top.list = s_list[w];
+    lp_enter<BF>(top, x, lowf, 0, c, c1, lane);
+    if (lane == 0) {
+      s_cnt[w] = top.cnt;
+      s_seen[w] = top.seen;
+    }
+    __syncthreads();
+  }
+  if (w != 0) return;
+  // (the waves' sums are relative to the same maximum)
+  s = ((s_run[0][1] + s_run[1][1]) + s_run[2][1]) + s_run[3][1];
+  T = ((s_run[0][2] + s_run[1][2]) + s_run[2][2]) + s_run[3][2];
+  if (total > kLpCap) {
+    lp_merge(top, s_best, s_list, s_cnt, s_seen, s_max, M, lane);
+  } else if (a.top > 0) {
+    top.cnt = total;
+    top.cut(lane);
+  }
+  lp_end<BF>(a, row, sp, M, s, T, top, tok, lane);
 }
 
-// The counts of the rows that can be split (fewer rows than workgroups wanted), ahead of the parts.
-static uint64_t lp_counts(const DevInfo& di) { return (uint64_t)di.cus * kLpPerCu * kLpCountStep * sizeof(uint32_t); }
-
-uint64_t logprobs_scratch(const DevInfo& di, int64_t m, int64_t n, int top) {
+// Parts in registers while they are few for the chip; else whole rows, or if those are still fewer
+// than it runs at once, as many streamed parts as fill it.
+constexpr int kLpParts = 16;                     // workgroups per CU up to which rows are cut into register parts
+constexpr int kLpPerCu = 4;                      // streaming workgroups per CU
+constexpr int64_t kLpUnit = (int64_t)kLpWaves * kLpBatch;
+struct LpPlan {
+  bool regs;              // k_logprobs_part
   int splits;
   int64_t part;
-  lp_plan(di, m, n, &splits, &part);
-  if (splits == 1) return 0;
-  return lp_counts(di) + (uint64_t)m * splits * (sizeof(LpPart) + 8ull * top);
+};
+static LpPlan lp_plan(const DevInfo& di, int64_t m, int64_t n) {
+  const int64_t units = (n + kLpUnit - 1) / kLpUnit;
+  LpPlan p;
+  p.regs = units <= 64 && m * units <= (int64_t)di.cus * kLpParts;
+  int64_t want = p.regs ? units : (int64_t)di.cus * kLpPerCu / m;
+  if (want < 1) want = 1;
+  if (want > 64) want = 64;
+  if (want > units) want = units;
+  const int64_t per = (units + want - 1) / want;
+  p.part = per * kLpUnit;
+  p.splits = (int)((units + per - 1) / per);
+  return p;
+}
+
+// The counts of the rows, ahead of the parts: as many rows as either rule cuts in two or more.
+static uint64_t lp_counts(const DevInfo& di) {
+  static_assert(kLpPerCu <= kLpParts, "register parts are the rule for more rows");
+  return (uint64_t)di.cus * (kLpParts / 2) * kLpCountStep * sizeof(uint32_t);
+}
+
+uint64_t logprobs_scratch(const DevInfo& di, int64_t m, int64_t n, int top) {
+  const LpPlan p = lp_plan(di, m, n);
+  if (p.splits == 1) return 0;
+  return lp_counts(di) + (uint64_t)m * p.splits * (sizeof(LpPart) + 8ull * top);
 }
 
 hipError_t launch_logprobs(const void* y, bool bf, int64_t m, int64_t n, int64_t ldy, const void* tokens,
@@ -630,16 +828,20 @@ hipError_t launch_logprobs(const void* y, bool bf, int64_t m, int64_t n, int64_t
   DevInfo di;
   hipError_t err = dev_info(&di);
   if (err != hipSuccess) return err;
+  const LpPlan p = lp_plan(di, m, n);
   LpArgs a;
   a.y = y; a.m = m; a.n = n; a.ldy = ldy;
   a.tokens = tokens; a.tok64 = tok64; a.nt = nt; a.top = top;
   a.logp = logp; a.ent = ent; a.tidx = tidx; a.tlogp = tlogp;
-  lp_plan(di, m, n, &a.splits, &a.part);
+  a.splits = p.splits;
+  a.part = p.part;
   a.count = static_cast<uint32_t*>(scratch);
   a.parts = reinterpret_cast<LpPart*>(static_cast<uint8_t*>(scratch) + lp_counts(di));
   a.keys = reinterpret_cast<uint64_t*>(a.parts + m * a.splits);
   const dim3 grid((unsigned)(m * a.splits)), block(64 * kLpWaves);
-  if (bf) hipLaunchKernelGGL(k_logprobs<true>, grid, block, 0, s, a);
+  if (p.regs && bf) hipLaunchKernelGGL(k_logprobs_part<true>, grid, block, 0, s, a);
+  else if (p.regs) hipLaunchKernelGGL(k_logprobs_part<false>, grid, block, 0, s, a);
+  else if (bf) hipLaunchKernelGGL(k_logprobs<true>, grid, block, 0, s, a);
   else hipLaunchKernelGGL(k_logprobs<false>, grid, block, 0, s, a);
   return hipGetLastError();
 }
