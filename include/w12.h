@@ -294,12 +294,20 @@ typedef struct w12_mx4 {
     int64_t  n;        /* rows of W (must equal the record's)    */
     int64_t  k;        /* columns of W (must equal the record's) */
     uint8_t *q;        /* [npad * k * 17 / 32] tile records (device, 16-byte aligned) */
+    /* the record's escapes that are not zero (a zero's slot holds code 0, so the product needs no
+     * correction there), in the record's order: row i's are entries nz_ptr[i] .. nz_end[i] - 1; the
+     * rows of a 16-row tile follow each other, tiles may have gaps between them */
+    uint32_t *nz_ptr;  /* [n + 1], nz_ptr[n] = nz_end[n - 1]     */
+    uint32_t *nz_end;  /* [n]                                    */
+    uint32_t *nz_col;  /* [nz_cap]                               */
+    uint16_t *nz_val;  /* [nz_cap]                               */
+    uint64_t  nz_cap;  /* entries available, at least the record's esc_cap */
 } w12_mx4;
 
 /*
- * w12_mx4_build -- the 4-bit copy of record `wt` into the caller's out->q (out->n, out->k set by the
- * caller to the record's).  Reads the planes and the escape columns.  Enqueued on `stream`, no
- * synchronisation.
+ * w12_mx4_build -- the 4-bit copy of record `wt` into the caller's arrays of `out` (out->n, out->k and
+ * out->nz_cap set by the caller; W12_ERR_CAPACITY if nz_cap < wt->esc_cap).  Reads the planes and
+ * the escape list.  Enqueued on `stream`, no synchronisation.
  */
 int w12_mx4_build(const w12_weight *wt, w12_mx4 *out, void *stream);
 
@@ -313,7 +321,8 @@ int w12_mx4_decode(const w12_mx4 *cp, const w12_weight *wt, uint16_t *w_out, voi
 /*
  * w12_mx4_gemm / w12_mx4_top1 -- the Q pass on the 4-bit copy and its top-1 per row of x, as
  * w12_i8_gemm and w12_i8_top1 (same x, outputs, flags, kernel families, workspace and error bound,
- * against the weights w12_mx4_decode gives).  Read cp->q and wt's base and escape arrays.
+ * against the weights w12_mx4_decode gives).  Read the copy and wt->base (wt's other arrays may be
+ * NULL).
  */
 int w12_mx4_gemm(const uint16_t *x, int64_t m, const w12_mx4 *cp, const w12_weight *wt, float *y,
                  uint32_t flags, void *stream);

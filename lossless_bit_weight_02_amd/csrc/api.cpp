@@ -69,6 +69,7 @@ w12::Planes planes_of(const w12_weight* wt) {
   p.ae = wt->ae;
   p.lo = wt->lo;
   p.esc_ptr = wt->esc_ptr;
+  p.esc_end = wt->esc_ptr ? wt->esc_ptr + 1 : nullptr;
   p.esc_col = wt->esc_col;
   p.esc_val = wt->esc_val;
   return p;
@@ -286,29 +287,48 @@ w12::Planes planes_i8(const w12_i8* cp, const w12_weight* wt) {
   return p;
 }
 
-// The 4-bit copy and the record whose window bottoms and escape list it shares.
-int check_mx4(const w12_mx4* cp, const w12_weight* wt) {
+// The 4-bit copy's own arrays (shape checks apart).
+int check_mx4_arrays(const w12_mx4* cp) {
+  if (!cp->q || !cp->nz_ptr || !cp->nz_end) return fail(W12_ERR_ARG, "q, nz_ptr or nz_end is NULL");
+  if (cp->nz_cap > 0 && (!cp->nz_col || !cp->nz_val))
+    return fail(W12_ERR_ARG, "nz_col or nz_val is NULL but nz_cap > 0");
+  if (!aligned16(cp->q)) return fail(W12_ERR_ALIGN, "q must be 16-byte aligned");
+  if (!aligned4(cp->nz_ptr) || !aligned4(cp->nz_end) || (cp->nz_col && !aligned4(cp->nz_col)) ||
+      (cp->nz_val && (reinterpret_cast<uintptr_t>(cp->nz_val) & 1u)))
+    return fail(W12_ERR_ALIGN, "the nz arrays must be naturally aligned");
+  return W12_OK;
+}
+
+// The 4-bit copy and the record whose window bottoms (decode: escapes too) it shares.
+int check_mx4(const w12_mx4* cp, const w12_weight* wt, bool esc) {
   if (!cp || !wt) return fail(W12_ERR_ARG, "the 4-bit copy or the record is NULL");
   int rc = check_nk(wt->n, wt->k);
   if (rc) return rc;
   if (cp->n != wt->n || cp->k != wt->k)
     return fail(W12_ERR_ARG, "the 4-bit copy is [%lld, %lld], the record [%lld, %lld]", (long long)cp->n,
                 (long long)cp->k, (long long)wt->n, (long long)wt->k);
-  if (!cp->q || !wt->base || !wt->esc_ptr) return fail(W12_ERR_ARG, "q, base or esc_ptr is NULL");
+  rc = check_mx4_arrays(cp);
+  if (rc) return rc;
+  if (!wt->base) return fail(W12_ERR_ARG, "base is NULL");
+  if (!esc) return W12_OK;
+  if (!wt->esc_ptr) return fail(W12_ERR_ARG, "esc_ptr is NULL");
   if (wt->esc_cap > 0 && (!wt->esc_col || !wt->esc_val))
     return fail(W12_ERR_ARG, "escape arrays are NULL but esc_cap > 0");
-  if (!aligned16(cp->q)) return fail(W12_ERR_ALIGN, "q must be 16-byte aligned");
   if (!aligned4(wt->esc_ptr) || (wt->esc_col && !aligned4(wt->esc_col)) ||
       (wt->esc_val && (reinterpret_cast<uintptr_t>(wt->esc_val) & 1u)))
     return fail(W12_ERR_ALIGN, "escape arrays must be naturally aligned");
   return W12_OK;
 }
 
+// For the product: the escapes that are not zero (a zero's code is 0 already).
 w12::Planes planes_mx4(const w12_mx4* cp, const w12_weight* wt) {
-  w12::Planes p = planes_of(wt);
-  p.ae = nullptr;
-  p.lo = nullptr;
+  w12::Planes p;
+  p.base = wt->base;
   p.mx4 = cp->q;
+  p.esc_ptr = cp->nz_ptr;
+  p.esc_end = cp->nz_end;
+  p.esc_col = cp->nz_col;
+  p.esc_val = cp->nz_val;
   return p;
 }
 }  // namespace
@@ -580,26 +600,32 @@ int w12_mx4_build(const w12_weight* wt, w12_mx4* out, void* stream) {
   if (out->n != wt->n || out->k != wt->k)
     return fail(W12_ERR_ARG, "out is [%lld, %lld], the record [%lld, %lld]", (long long)out->n,
                 (long long)out->k, (long long)wt->n, (long long)wt->k);
-  if (!out->q) return fail(W12_ERR_ARG, "out->q is NULL");
-  if (!aligned16(out->q)) return fail(W12_ERR_ALIGN, "q must be 16-byte aligned");
-  hipError_t e = w12::launch_mx4_build(planes_of(wt), wt->n, wt->k, out->q, reinterpret_cast<hipStream_t>(stream));
+  rc = check_mx4_arrays(out);
+  if (rc) return rc;
+  if (out->nz_cap < wt->esc_cap)
+    return fail(W12_ERR_CAPACITY, "nz_cap %llu < the record's esc_cap %llu", (unsigned long long)out->nz_cap,
+                (unsigned long long)wt->esc_cap);
+  hipError_t e = w12::launch_mx4_build(planes_of(wt), wt->n, wt->k, out->q, out->nz_ptr, out->nz_end, out->nz_col,
+                                       out->nz_val, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "4-bit copy launch");
   return ok();
 }
 
 int w12_mx4_decode(const w12_mx4* cp, const w12_weight* wt, uint16_t* w_out, void* stream) {
-  int rc = check_mx4(cp, wt);
+  int rc = check_mx4(cp, wt, true);
   if (rc) return rc;
   if (!w_out) return fail(W12_ERR_ARG, "w_out is NULL");
   if (!aligned16(w_out)) return fail(W12_ERR_ALIGN, "w_out must be 16-byte aligned");
-  hipError_t e = w12::launch_mx4_decode(planes_mx4(cp, wt), wt->n, wt->k, w_out, reinterpret_cast<hipStream_t>(stream));
+  w12::Planes p = planes_of(wt);
+  p.mx4 = cp->q;
+  hipError_t e = w12::launch_mx4_decode(p, wt->n, wt->k, w_out, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "4-bit decode launch");
   return ok();
 }
 
 int w12_mx4_gemm(const uint16_t* x, int64_t m, const w12_mx4* cp, const w12_weight* wt, float* y,
                  uint32_t flags, void* stream) {
-  int rc = check_mx4(cp, wt);
+  int rc = check_mx4(cp, wt, false);
   if (rc) return rc;
   if (flags & W12_Q8_MIDPOINT) return fail(W12_ERR_ARG, "W12_Q8_MIDPOINT does not apply to the 4-bit copy");
   return run_gemm(w12::kFmtMX4, x, m, planes_mx4(cp, wt), wt->n, wt->k, y, flags, stream);
@@ -607,7 +633,7 @@ int w12_mx4_gemm(const uint16_t* x, int64_t m, const w12_mx4* cp, const w12_weig
 
 int w12_mx4_top1(const uint16_t* x, int64_t m, const w12_mx4* cp, const w12_weight* wt, int32_t* idx,
                  float* val, uint32_t flags, void* stream) {
-  int rc = check_mx4(cp, wt);
+  int rc = check_mx4(cp, wt, false);
   if (rc) return rc;
   if (!x || !idx || !val) return fail(W12_ERR_ARG, "x, idx or val is NULL");
   if (flags != 0) return fail(W12_ERR_ARG, "unknown flags 0x%x", flags);

@@ -46,6 +46,7 @@ struct GemvArgs {
   const uint8_t* ae;      // tiled storage
   const uint8_t* lo;
   const uint32_t* esc_ptr;
+  const uint32_t* esc_end;
   const uint32_t* esc_col;
   const uint16_t* esc_val;
   const uint16_t* w;      // dense bfloat16 W (baseline), tiled storage
@@ -131,7 +132,7 @@ __global__ __launch_bounds__(64 * NW) void k_gemv(GemvArgs a) {
     const bool use = kEsc && part == 0 && ps < passes && t < tiles;
     const int64_t r = use ? t * kTileRows + r16 : 0;
     e0 = use ? a.esc_ptr[r < a.n ? r : a.n] : 0u;
-    e1 = use ? a.esc_ptr[r + 1 < a.n ? r + 1 : a.n] : 0u;
+    e1 = use ? (r < a.n ? a.esc_end[r] : a.esc_ptr[a.n]) : 0u;
     if constexpr (FMT == kFmtI8) bs = use ? __float_as_uint(a.scale[r < a.n ? r : a.n - 1]) : 0u;
     else bs = use ? a.base[r < a.n ? r : a.n - 1] : 0u;
     te0 = use ? a.esc_ptr[t * kTileRows] : 0u;   // made uniform only when used, a tile later:
@@ -346,7 +347,8 @@ static bool few_tiles(Fmt f, int m, int64_t tiles, const DevInfo& di) {
 }
 template <int FMT, int M>
 static GemvKernel pick_m(bool few) {
-  if constexpr (M <= 2) return few ? k_gemv<FMT, M, 3, kNWFew, kNWFew> : k_gemv<FMT, M, 3, kNWSmall, kNWSmall>;
+  if constexpr (FMT == kFmtMX4 && M <= 2) return few ? k_gemv<FMT, M, 3, kNWFew, kNWFew> : k_gemv<FMT, M, 5, kNWSmall, kNWSmall>;
+  else if constexpr (M <= 2) return few ? k_gemv<FMT, M, 3, kNWFew, kNWFew> : k_gemv<FMT, M, 3, kNWSmall, kNWSmall>;
   else if constexpr (M <= 4) return k_gemv<FMT, M, 4, 2, 4>;
   else return k_gemv<FMT, M, 4, 1, 4>;
 }
@@ -427,7 +429,7 @@ hipError_t launch_gemv(Fmt f, const uint16_t* x, int64_t m, const Planes& p, int
     GemvArgs a;
     a.ldx = k;
     a.base = p.base; a.ae = p.ae; a.lo = p.lo;
-    a.esc_ptr = p.esc_ptr; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
+    a.esc_ptr = p.esc_ptr; a.esc_end = p.esc_end; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
     a.w = p.w;
     a.scale = p.scale;
     a.mx4 = p.mx4;

@@ -201,7 +201,8 @@ void k_mfma(MfmaArgs a) {
       const auto ptr_at = [&](int64_t r) { return a.esc_ptr[r < a.n ? r : a.n]; };
       if constexpr (kStage) {
 #pragma unroll
-        for (int r = 0; r < 5; ++r) st[r] = ptr_at(rg + r);
+        for (int r = 0; r < 4; ++r) st[r] = ptr_at(rg + r);
+        st[4] = rg + 3 < a.n ? a.esc_end[rg + 3] : a.esc_ptr[a.n];
       }
       rsc.load(a, rg);
     }
@@ -706,7 +707,7 @@ static hipError_t mfma_pass(Fmt f, const DevInfo& di, const uint16_t* x, int mb,
   a.x = x;
   a.m = mb;
   a.base = p.base; a.ae = p.ae; a.lo = p.lo;
-  a.esc_ptr = p.esc_ptr; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
+  a.esc_ptr = p.esc_ptr; a.esc_end = p.esc_end; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
   a.w = p.w;
   a.scale = p.scale;
   a.mx4 = p.mx4;
@@ -820,7 +821,7 @@ hipError_t launch_mfma_top1(Fmt f, const uint16_t* x, int64_t m, const Planes& p
     a.x = x + m0 * k;
     a.m = mb;
     a.base = p.base; a.ae = p.ae; a.lo = p.lo;
-    a.esc_ptr = p.esc_ptr; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
+    a.esc_ptr = p.esc_ptr; a.esc_end = p.esc_end; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
     a.w = p.w;
     a.scale = p.scale;
   a.mx4 = p.mx4;

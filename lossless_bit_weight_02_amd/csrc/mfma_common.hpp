@@ -22,6 +22,7 @@ struct MfmaArgs {
   const uint8_t* ae;   // tiled storage
   const uint8_t* lo;
   const uint32_t* esc_ptr;
+  const uint32_t* esc_end;
   const uint32_t* esc_col;
   const uint16_t* esc_val;
   const uint16_t* w;   // dense bfloat16 W (baseline), tiled storage

@@ -148,10 +148,12 @@ void k_mfma_wide(MfmaArgs a) {
       const int64_t rg = row0 + 4 * g;
       const auto ptr_at = [&](int64_t r) { return a.esc_ptr[r < a.n ? r : a.n]; };
 #pragma unroll
-      for (int r = 0; r < 5; ++r) st[r] = ptr_at(rg + r);
+      for (int r = 0; r < 4; ++r) st[r] = ptr_at(rg + r);
+      const auto end_at = [&](int64_t r) { return r < a.n ? a.esc_end[r] : a.esc_ptr[a.n]; };
+      st[4] = end_at(rg + 3);
       rsc.load(a, rg);
       t_e0 = __builtin_amdgcn_readfirstlane(a.esc_ptr[row0]);
-      const uint32_t t_e1 = __builtin_amdgcn_readfirstlane(valid ? ptr_at(row0 + kTileRows) : t_e0);
+      const uint32_t t_e1 = __builtin_amdgcn_readfirstlane(valid ? end_at(row0 + kTileRows - 1) : t_e0);
       const uint32_t cnt = t_e1 - t_e0 < (uint32_t)kEscCap ? t_e1 - t_e0 : (uint32_t)kEscCap;
       const Rsrc r_col = make_rsrc(a.esc_col + t_e0, cnt * 4u);
       const Rsrc r_val = make_rsrc(a.esc_val + t_e0, cnt * 2u);

@@ -59,23 +59,60 @@ __global__ __launch_bounds__(kBlock) void k_mx4_build(const uint8_t* __restrict_
   }
 }
 
-// Code 0 at every escaped slot.  Two escapes may share a byte: each clears its nibble of the
-// 32-bit word atomically (an AND: the result does not depend on the order).
-__global__ __launch_bounds__(kBlock) void k_mx4_zero_escapes(const uint32_t* __restrict__ esc_ptr,
-                                                             const uint32_t* __restrict__ esc_col, int64_t n,
-                                                             int64_t k, uint8_t* __restrict__ q) {
+// One wave per 16-row tile row: the tile row's escapes in order, 64 at a time.  Each escaped slot gets
+// code 0 (the build wrote the code of its placeholder, the window's lowest magnitude, which is 0
+// already unless the block's own exponent is within 3 of the window bottom: 2^-2 of the scale ties
+// to 0).  The escapes that are not zero go to the copy's own list, packed from the place of the
+// tile row's first escape in the record's list: the product reads only those, since a zero
+// contributes what its code does.
+__global__ __launch_bounds__(kBlock) void k_mx4_escapes(Planes p, int64_t n, int64_t k, uint8_t* __restrict__ q,
+                                                        uint32_t* __restrict__ nz_ptr, uint32_t* __restrict__ nz_end,
+                                                        uint32_t* __restrict__ nz_col, uint16_t* __restrict__ nz_val) {
   const int lane = threadIdx.x & 63;
   const int64_t ktiles = k / kTileCols;
+  const int64_t trows = (n + kTileRows - 1) / kTileRows;
   const int64_t nw = (int64_t)gridDim.x * (kBlock / 64);
-  for (int64_t row = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6); row < n; row += nw) {
-    const uint32_t e1 = esc_ptr[row + 1];
-    const int64_t r = row % kTileRows;
-    for (uint32_t e = esc_ptr[row] + lane; e < e1; e += 64) {
-      const int64_t c = esc_col[e], cc = c % kTileCols;
-      const int64_t t = (row / kTileRows) * ktiles + c / kTileCols;
-      const int j = (int)(cc % 32);                // column within the block: nibble j
-      uint32_t* word = reinterpret_cast<uint32_t*>(q + t * kTileMX + 16 * (r + 16 * (cc / 32))) + j / 8;
-      atomicAnd(word, ~(0xFu << (4 * (j % 8))));
+  for (int64_t tr = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6); tr < trows; tr += nw) {
+    const int64_t row0 = tr * kTileRows;
+    // lane r <= 16: where row row0 + r starts (rows past n: the end)
+    const int64_t rr = row0 + (lane < kTileRows ? lane : kTileRows);
+    const uint32_t start = p.esc_ptr[rr < n ? rr : n];
+    const uint32_t t0 = __builtin_amdgcn_readfirstlane(start);
+    const uint32_t t1 = (uint32_t)__builtin_amdgcn_readlane(start, kTileRows);
+    uint32_t kept = t0, mine = t0;                 // kept so far; kept ahead of this lane's row
+    for (uint32_t e0 = t0; e0 < t1; e0 += 64) {
+      const uint32_t e = e0 + (uint32_t)lane;
+      const bool in = e < t1;
+      const uint32_t col = in ? p.esc_col[e] : 0u;
+      const uint16_t val = in ? p.esc_val[e] : (uint16_t)0;
+      int r = 0;                                   // the entry's row
+#pragma unroll
+      for (int i = 1; i < kTileRows; ++i) r += e >= (uint32_t)__builtin_amdgcn_readlane(start, i) ? 1 : 0;
+      if (in) {
+        const int64_t cc = col % kTileCols;
+        uint8_t* tile = q + (tr * ktiles + col / kTileCols) * kTileMX;
+        const int l = r + 16 * (int)(cc / 32), j = (int)(cc % 32);
+        // (two escapes may share a word: the AND of both, in any order)
+        if (tile[1024 + l] <= kMXLowest + 3)
+          atomicAnd(reinterpret_cast<uint32_t*>(tile + 16 * l) + j / 8, ~(0xFu << (4 * (j % 8))));
+      }
+      const bool keep = in && (val & 0x7FFFu) != 0;
+      const uint64_t b = __ballot(keep);
+      if (keep) {
+        const uint32_t at = kept + (uint32_t)__popcll(b & ((1ull << lane) - 1));
+        nz_col[at] = col;
+        nz_val[at] = val;
+      }
+      if (start >= e0 && start < e0 + 64)
+        mine = kept + (uint32_t)__popcll(b & ((1ull << (start - e0)) - 1));
+      kept += (uint32_t)__popcll(b);
+    }
+    if (start >= t1 && t1 > t0) mine = kept;       // rows that start at the list's end
+    const uint32_t next = (uint32_t)__shfl_down((int)mine, 1);
+    if (lane < kTileRows && row0 + lane < n) {
+      nz_ptr[row0 + lane] = mine;
+      nz_end[row0 + lane] = lane == kTileRows - 1 ? kept : next;
+      if (row0 + lane == n - 1) nz_ptr[n] = kept;
     }
   }
 }
@@ -119,7 +156,8 @@ static unsigned mx4_grid(const DevInfo& di, int64_t waves) {
   return (unsigned)(blocks < cap ? blocks : cap);
 }
 
-hipError_t launch_mx4_build(const Planes& p, int64_t n, int64_t k, uint8_t* q, hipStream_t s) {
+hipError_t launch_mx4_build(const Planes& p, int64_t n, int64_t k, uint8_t* q, uint32_t* nz_ptr, uint32_t* nz_end,
+                            uint32_t* nz_col, uint16_t* nz_val, hipStream_t s) {
   DevInfo di;
   hipError_t err = dev_info(&di);
   if (err != hipSuccess) return err;
@@ -127,7 +165,8 @@ hipError_t launch_mx4_build(const Planes& p, int64_t n, int64_t k, uint8_t* q, h
   hipLaunchKernelGGL(k_mx4_build, dim3(mx4_grid(di, tiles)), dim3(kBlock), 0, s, p.ae, p.lo, n, k, q);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(k_mx4_zero_escapes, dim3(mx4_grid(di, n)), dim3(kBlock), 0, s, p.esc_ptr, p.esc_col, n, k, q);
+  hipLaunchKernelGGL(k_mx4_escapes, dim3(mx4_grid(di, (n + kTileRows - 1) / kTileRows)), dim3(kBlock), 0, s, p, n, k, q,
+                     nz_ptr, nz_end, nz_col, nz_val);
   return hipGetLastError();
 }
 

@@ -5,6 +5,7 @@
 
 namespace w12 {
 
+constexpr uint32_t kMXLowest = 110;   // scale byte of a block whose largest weight is at the window bottom
 constexpr int kTileMX = 1088;    // bytes of a tile: 64 lanes x 16 bytes of codes, 64 block scales
 
 // A block's 32 codes and its scale byte -> the 16 dwords of bfloat16 pairs w' of its columns: each

@@ -48,6 +48,7 @@ struct StreamArgs {
   const uint8_t* ae;
   const uint8_t* lo;
   const uint32_t* esc_ptr;
+  const uint32_t* esc_end;
   const uint32_t* esc_col;
   const uint16_t* esc_val;
   const uint16_t* w;
@@ -189,12 +190,9 @@ __global__ __launch_bounds__(64 * W) void k_stream(StreamArgs a) {
   const auto load_meta = [&]() {
 #pragma unroll
     for (int f = 0; f < FT; ++f) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int64_t rr = row0[f] + r16 + r;
-        st[f][r] = kEsc && fin[f] ? a.esc_ptr[rr < a.n ? rr : a.n] : 0u;
-      }
       const int64_t rr = row0[f] + r16, rc = rr < a.n ? rr : a.n - 1;
+      st[f][0] = kEsc && fin[f] ? a.esc_ptr[rr < a.n ? rr : a.n] : 0u;
+      st[f][1] = kEsc && fin[f] ? (rr < a.n ? a.esc_end[rr] : a.esc_ptr[a.n]) : 0u;
       if constexpr (FMT == kFmtI8) fsc[f] = fin[f] ? __float_as_uint(a.scale[rc]) : 0u;
       else if constexpr (kEsc) fsc[f] = fin[f] ? a.base[rc] : 0u;
       else fsc[f] = 0u;
@@ -753,7 +751,7 @@ hipError_t launch_stream(Fmt f, const uint16_t* x, int64_t m, const Planes& p, i
     a.x = x + m0 * k;
     a.mrows = (int)mb;
     a.base = p.base; a.ae = p.ae; a.lo = p.lo;
-    a.esc_ptr = p.esc_ptr; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
+    a.esc_ptr = p.esc_ptr; a.esc_end = p.esc_end; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
     a.w = p.w;
     a.scale = p.scale;
     a.mx4 = p.mx4;

@@ -93,6 +93,9 @@ struct Planes {
   const uint8_t* ae = nullptr;
   const uint8_t* lo = nullptr;
   const uint32_t* esc_ptr = nullptr;
+  // end of each row's escapes: esc_ptr + 1, but for the 4-bit copy, whose tiles' lists have gaps
+  // between them (esc_ptr[n] is then row n - 1's end too)
+  const uint32_t* esc_end = nullptr;
   const uint32_t* esc_col = nullptr;
   const uint16_t* esc_val = nullptr;
   const uint16_t* w = nullptr;  // kFmtBF16 only: the dense bfloat16 weight, tiled storage order
@@ -108,6 +111,7 @@ inline Planes rows_from(const Planes& p, int64_t r0, int64_t k) {
   if (t.ae) t.ae += r0 * k;
   if (t.lo) t.lo += r0 * k / 2;
   if (t.esc_ptr) t.esc_ptr += r0;
+  if (t.esc_end) t.esc_end += r0;
   if (t.w) t.w += r0 * k;
   if (t.scale) t.scale += r0;
   if (t.mx4) t.mx4 += r0 * k / 32 * 17;   // 1088 bytes per 16 x 128 tile
@@ -140,9 +144,11 @@ hipError_t launch_interleave(const Planes& gate, const Planes& up, int64_t rows,
 hipError_t launch_i8_build(const Planes& p, int64_t n, int64_t k, int8_t* q, float* scale, hipStream_t s);
 // every escape's value over its slot of the dense matrix out [n][k]
 hipError_t launch_escape_scatter(const Planes& p, int64_t n, int64_t k, uint16_t* out, hipStream_t s);
-// microscaled 4-bit copy of a record (padded_rows(n) * k * 17 / 32 bytes), and the bfloat16 matrix it
-// stands for (p.mx4, p.base, escapes)
-hipError_t launch_mx4_build(const Planes& p, int64_t n, int64_t k, uint8_t* q, hipStream_t s);
+// microscaled 4-bit copy of a record (padded_rows(n) * k * 17 / 32 bytes) with its list of escapes that
+// are not zero (nz_ptr [n + 1], nz_end [n], columns and values), and the bfloat16 matrix it stands
+// for (p.mx4, p.base, the record's escapes)
+hipError_t launch_mx4_build(const Planes& p, int64_t n, int64_t k, uint8_t* q, uint32_t* nz_ptr, uint32_t* nz_end,
+                            uint32_t* nz_col, uint16_t* nz_val, hipStream_t s);
 hipError_t launch_mx4_decode(const Planes& p, int64_t n, int64_t k, uint16_t* out, hipStream_t s);
 // out[j] = scale * row ids[j] of the record (bfloat16 or float, [cnt][k]); an id outside 0 .. n-1
 // gives zeros

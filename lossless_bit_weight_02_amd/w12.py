@@ -51,7 +51,9 @@ class _W12I8(ctypes.Structure):
 
 
 class _W12MX4(ctypes.Structure):
-    _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("q", ctypes.c_void_p)]
+    _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("q", ctypes.c_void_p),
+                ("nz_ptr", ctypes.c_void_p), ("nz_end", ctypes.c_void_p), ("nz_col", ctypes.c_void_p),
+                ("nz_val", ctypes.c_void_p), ("nz_cap", ctypes.c_uint64)]
 
 
 _lib = None
@@ -505,11 +507,13 @@ def i8_top1(x: torch.Tensor, cp: I8Copy, out=None):
 
 
 class Mx4Copy:
-    """The microscaled 4-bit Q-pass copy of a W12 record: tile records of 32-column blocks (layout of
-    include/w12.h); it shares ``rec``'s window bottoms and escape list."""
+    """The microscaled 4-bit Q-pass copy of a W12 record: tile records of 32-column blocks and the list of
+    the record's escapes that are not zero (layout of include/w12.h); it shares ``rec``'s window
+    bottoms."""
 
-    def __init__(self, rec: W12Weight, q):
+    def __init__(self, rec: W12Weight, q, nz_ptr, nz_end, nz_col, nz_val):
         self.rec, self.q = rec, q
+        self.nz_ptr, self.nz_end, self.nz_col, self.nz_val = nz_ptr, nz_end, nz_col, nz_val
         self.n, self.k = rec.n, rec.k
 
     @property
@@ -517,22 +521,31 @@ class Mx4Copy:
         return self.q.device
 
     def nbytes(self) -> int:
-        return self.q.numel()
+        return sum(t.numel() * t.element_size() for t in
+                   (self.q, self.nz_ptr, self.nz_end, self.nz_col, self.nz_val))
 
     def c_struct(self) -> _W12MX4:
-        return _W12MX4(self.n, self.k, self.q.data_ptr())
+        return _W12MX4(self.n, self.k, _ptr(self.q), _ptr(self.nz_ptr), _ptr(self.nz_end), _ptr(self.nz_col),
+                       _ptr(self.nz_val), self.nz_col.numel())
 
     def to_numpy(self) -> dict:
-        return dict(q_s=self.q.cpu().numpy())
+        import numpy as np
+        return dict(q_s=self.q.cpu().numpy(), nz_ptr=self.nz_ptr.cpu().numpy().view(np.uint32),
+                    nz_end=self.nz_end.cpu().numpy().view(np.uint32),
+                    nz_col=self.nz_col.cpu().numpy().view(np.uint32),
+                    nz_val=self.nz_val.cpu().numpy().view(np.uint16))
 
 
 def mx4_build(rec: W12Weight) -> Mx4Copy:
     """The microscaled 4-bit Q-pass copy of ``rec`` (blocks of 32 columns, power-of-two scales, E2M1 codes
     rounded to nearest even, escaped slots 0), built on the device."""
-    q = torch.empty(padded_rows(rec.n) * rec.k // 32 * 17, dtype=torch.uint8, device=rec.device)
-    cp = Mx4Copy(rec, q)
+    dev, i32 = rec.device, torch.int32
+    cap = rec.n_esc
+    cp = Mx4Copy(rec, torch.empty(padded_rows(rec.n) * rec.k // 32 * 17, dtype=torch.uint8, device=dev),
+                 torch.empty(rec.n + 1, dtype=i32, device=dev), torch.empty(rec.n, dtype=i32, device=dev),
+                 torch.empty(cap, dtype=i32, device=dev), torch.empty(cap, dtype=torch.int16, device=dev))
     s, c = rec.c_struct(), cp.c_struct()
-    _check(lib().w12_mx4_build(ctypes.byref(s), ctypes.byref(c), _stream_handle(rec.device)))
+    _check(lib().w12_mx4_build(ctypes.byref(s), ctypes.byref(c), _stream_handle(dev)))
     return cp
 
 
@@ -543,8 +556,6 @@ def mx4_decode(cp: Mx4Copy, out: torch.Tensor | None = None) -> torch.Tensor:
     else:
         _check_out(out, (cp.n, cp.k), (torch.bfloat16,), cp.device)
     c, s = cp.c_struct(), cp.rec.c_struct()
-    s.ae = None
-    s.lo = None
     _check(lib().w12_mx4_decode(ctypes.byref(c), ctypes.byref(s), out.data_ptr(), _stream_handle(cp.device)))
     return out
 
@@ -556,8 +567,6 @@ def mx4_gemm(x: torch.Tensor, cp: Mx4Copy, path: str | None = None, out: torch.T
     if x.shape[0] == 0:
         return out
     c, s = cp.c_struct(), cp.rec.c_struct()
-    s.ae = None
-    s.lo = None
     _check(lib().w12_mx4_gemm(x.data_ptr(), x.shape[0], ctypes.byref(c), ctypes.byref(s), out.data_ptr(),
                               _PATHS[path] | _out_flag(out), _stream_handle(x.device)))
     return out

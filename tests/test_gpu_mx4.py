@@ -57,6 +57,16 @@ def _copy_check(w_bits, what):
         bad = np.argwhere(got != want)
         raise AssertionError(f"{what}: bytes differ at {bad[:5].tolist()} ({len(bad)}), got "
                              f"{got[bad[:5]].tolist()} want {want[bad[:5]].tolist()}")
+    d, r = cp.to_numpy(), rec.to_numpy()
+    for i in range(rec.n):
+        a, b = int(r["esc_ptr"][i]), int(r["esc_ptr"][i + 1])
+        keep = (r["esc_val"][a:b] & 0x7FFF) != 0
+        ra, rb = int(d["nz_ptr"][i]), int(d["nz_end"][i])
+        assert 0 <= ra and rb <= d["nz_col"].size
+        assert np.array_equal(d["nz_col"][ra:rb], r["esc_col"][a:b][keep]), f"{what}: list of row {i}"
+        assert np.array_equal(d["nz_val"][ra:rb], r["esc_val"][a:b][keep]), f"{what}: list of row {i}"
+        assert i % 16 == 15 or i == rec.n - 1 or rb == int(d["nz_ptr"][i + 1]), f"{what}: gap inside a tile"
+    assert int(d["nz_ptr"][rec.n]) == int(d["nz_end"][rec.n - 1])
     say(f"mx4 decode {what}")
     dec = to_host_bits(w12.mx4_decode(cp))
     w64 = oracle.mx4_weights64(ref, ocp)

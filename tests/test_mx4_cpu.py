@@ -10,8 +10,11 @@ from lossless_bit_weight_02_amd import synth, w12
 from tests.test_abi_cpu import _lib, _rec
 
 
-def _cp(n=64, k=128, q=0x8000):
-    return w12._W12MX4(n, k, q)
+def _cp(n=64, k=128, q=0x8000, **over):
+    s = w12._W12MX4(n, k, q, 0xB000, 0xC000, 0xD000, 0xE000, 10)
+    for key, v in over.items():
+        setattr(s, key, v)
+    return s
 
 
 def test_build_and_decode_refusals():
@@ -23,6 +26,11 @@ def test_build_and_decode_refusals():
     assert L.w12_mx4_build(ctypes.byref(_rec()), ctypes.byref(_cp(q=0x8008)), None) == w12.W12_ERR_ALIGN
     assert L.w12_mx4_build(ctypes.byref(_rec(k=96)), ctypes.byref(_cp(k=96)), None) == w12.W12_ERR_SHAPE
     assert L.w12_mx4_build(ctypes.byref(_rec(lo=None)), ctypes.byref(_cp()), None) == w12.W12_ERR_ARG
+    for bad, want in ((dict(nz_ptr=None), w12.W12_ERR_ARG), (dict(nz_end=None), w12.W12_ERR_ARG),
+                      (dict(nz_col=None), w12.W12_ERR_ARG), (dict(nz_val=None), w12.W12_ERR_ARG),
+                      (dict(nz_ptr=0xB002), w12.W12_ERR_ALIGN), (dict(nz_val=0xE001), w12.W12_ERR_ALIGN),
+                      (dict(nz_cap=9), w12.W12_ERR_CAPACITY)):
+        assert L.w12_mx4_build(ctypes.byref(_rec()), ctypes.byref(_cp(**bad)), None) == want, bad
     assert L.w12_mx4_decode(ctypes.byref(_cp()), ctypes.byref(_rec()), None, None) == w12.W12_ERR_ARG
     assert L.w12_mx4_decode(ctypes.byref(_cp()), ctypes.byref(_rec()), 0x1002, None) == w12.W12_ERR_ALIGN
     assert L.w12_mx4_decode(ctypes.byref(_cp(k=256)), ctypes.byref(_rec()), 0x1000, None) == w12.W12_ERR_ARG
@@ -50,7 +58,9 @@ def test_product_refusals():
     assert gemm(flags=7) == w12.W12_ERR_ARG
     assert gemm(cp=_cp(n=65)) == w12.W12_ERR_ARG
     assert gemm(cp=_cp(q=0x8004)) == w12.W12_ERR_ALIGN
-    assert gemm(rec=_rec(esc_ptr=None)) == w12.W12_ERR_ARG
+    assert gemm(rec=_rec(base=None)) == w12.W12_ERR_ARG
+    assert gemm(cp=_cp(nz_col=None)) == w12.W12_ERR_ARG
+    assert gemm(cp=_cp(nz_end=0xC001)) == w12.W12_ERR_ALIGN
     assert gemm(rec=_rec(k=1 << 25), cp=_cp(k=1 << 25)) == w12.W12_ERR_RANGE
     assert top1(idx=None) == w12.W12_ERR_ARG
     assert top1(flags=1) == w12.W12_ERR_ARG
@@ -59,7 +69,9 @@ def test_product_refusals():
     with pytest.raises(ValueError):
         torch = pytest.importorskip("torch")
         rec = w12.W12Weight(16, 128, *([torch.zeros(16, dtype=torch.uint8)] * 3), *([torch.zeros(17, dtype=torch.int32)] * 3))
-        w12.mx4_gemm(torch.zeros(1, 128, dtype=torch.bfloat16), w12.Mx4Copy(rec, torch.zeros(17, dtype=torch.uint8)))
+        i32 = torch.zeros(17, dtype=torch.int32)
+        w12.mx4_gemm(torch.zeros(1, 128, dtype=torch.bfloat16),
+                     w12.Mx4Copy(rec, torch.zeros(17, dtype=torch.uint8), i32, i32, i32, i32.to(torch.int16)))
 
 
 def test_code_table_and_ties():
