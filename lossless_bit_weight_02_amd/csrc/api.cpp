@@ -189,6 +189,7 @@ int run_gemm(w12::Fmt f, const uint16_t* x, int64_t m, const w12::Planes& p, int
   }
   hipError_t e = use_stream ? w12::launch_stream(f, x, m, p, n, k, yo, s)
                  : gemv     ? w12::launch_gemv(f, x, m, p, n, k, yo, s, sc)
+                 : f == w12::kFmtMX4 ? w12::launch_mx4_gemm(x, m, p, n, k, yo, s, sc)
                             : w12::launch_mfma(f, x, m, p, n, k, yo, s, sc);
   if (e != hipSuccess) return hip_fail(e, use_stream ? "stream launch" : gemv ? "gemv launch" : "mfma launch");
   return ok();
