@@ -103,6 +103,7 @@ w12::Planes planes_of(const w12_weight* wt) {
 // vs 140.9, [5120, 6144] 55.6 vs 73.9, [8192, 5120] 54.7 vs 69.3, [12288, 5120] 68.6 vs 70.8).
 bool stream_auto_pick(w12::Fmt f, int64_t m, int64_t tiles, int64_t k, int64_t cus) {
   const bool dense = f == w12::kFmtBF16;
+  if (f == w12::kFmtMX4) return false;
   if (m <= 32)
     return k <= 8192 && (!dense || tiles <= 6 * cus) &&
            ((m >= 3 && m <= 16 && 2 * tiles >= 3 * cus) ||
@@ -189,7 +190,7 @@ int run_gemm(w12::Fmt f, const uint16_t* x, int64_t m, const w12::Planes& p, int
   }
   hipError_t e = use_stream ? w12::launch_stream(f, x, m, p, n, k, yo, s)
                  : gemv     ? w12::launch_gemv(f, x, m, p, n, k, yo, s, sc)
-                 : f == w12::kFmtMX4 ? w12::launch_mx4_gemm(x, m, p, n, k, yo, s, sc)
+                 : f == w12::kFmtMX4 && m > 32 ? w12::launch_mx4_gemm(x, m, p, n, k, yo, s, sc)
                             : w12::launch_mfma(f, x, m, p, n, k, yo, s, sc);
   if (e != hipSuccess) return hip_fail(e, use_stream ? "stream launch" : gemv ? "gemv launch" : "mfma launch");
   return ok();

@@ -22,6 +22,15 @@ __device__ __forceinline__ void mx4_pairs(u32x4 v, uint32_t s, uint32_t p[16]) {
   }
 }
 
+// Eight codes -> the four bfloat16 pairs of one operand.
+__device__ __forceinline__ u32x4 mx4_quarter(uint32_t v, uint32_t s) {
+  const float scale = __uint_as_float(s << 23);
+  return (u32x4){__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 3))};
+}
+
 // Eight bfloat16 values (four pairs) -> eight codes of value / scale, nearest with ties to even,
 // magnitudes above 6 to 6.
 __device__ __forceinline__ uint32_t mx4_encode8(const uint32_t p[4], float scale) {

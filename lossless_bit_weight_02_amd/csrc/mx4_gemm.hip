@@ -27,6 +27,7 @@
 namespace w12 {
 
 constexpr int kMxWaves = 8;
+constexpr int kMxTiles = 3;      // tiles per wave pair and round at most
 
 struct Mx4Args {
   const uint16_t* x;             // x[m][k]
@@ -62,7 +63,7 @@ void k_mx4_gemm(Mx4Args a) {
   constexpr int W = kMxWaves;
   constexpr int F = 4 * NT * S;                    // 1 KiB x pieces per chunk
   constexpr int FW = F / W;
-  static_assert(F % W == 0 && S % (2 * D) == 0, "whole rings and 256-column pieces per chunk");
+  static_assert(F % W == 0 && FW % 4 == 0 && S % (2 * D) == 0, "whole rings and 256-column pieces per chunk");
   static_assert(4 * TP * NT * 2 <= 2 * F, "the odd blocks' sums and the escapes' products fit the x buffers");
   constexpr int kLoads = 2 * TP;                   // loads per step
   __shared__ __attribute__((aligned(16))) u32x4 s_x[2][F * 64];
@@ -92,10 +93,10 @@ void k_mx4_gemm(Mx4Args a) {
   // 16-byte column slot c16; wave w loads pieces w + 8 i.
   const uint32_t prow = (uint32_t)lane >> 5, pslot = (uint32_t)lane & 31u;
   // (pos: the chunk's place in the workgroup's order, n_chunks and past it: nothing)
-  const auto x_fetch = [&](uint32_t pos, uint32_t buf) {
+  const auto x_fetch = [&](uint32_t pos, uint32_t buf, int from, int to) {
     const uint32_t c = chunk_at(pos);
 #pragma unroll
-    for (int i = 0; i < FW; ++i) {
+    for (int i = from; i < to; ++i) {
       const uint32_t P = (uint32_t)(w + W * i);
       const uint32_t q = P % (8u * NT), hb = P / (8u * NT);
       const uint32_t row = 2u * q + prow;
@@ -134,8 +135,20 @@ void k_mx4_gemm(Mx4Args a) {
       row0[j] = tile * kTileRows;
       rq[j] = make_rsrc(a.q + (tile * KB + kb0) * kTileMX, have[j] ? nkb * (uint32_t)kTileMX : 0u);
     }
+    u32x4 bv[D][TP];
+    uint32_t bs[D][TP];
+    const auto load = [&](uint32_t kb, int d) {
+#pragma unroll
+      for (int j = 0; j < TP; ++j) {
+        const uint32_t off = kb < nkb ? kb * kTileMX : kOOB;
+        bv[d][j] = __builtin_amdgcn_raw_buffer_load_b128(rq[j], off + 16u * lane, 0, kAuxNT);
+        bs[d][j] = __builtin_amdgcn_raw_buffer_load_b8(rq[j], off + 1024u + lane, 0, kAuxNT);
+      }
+    };
     __builtin_amdgcn_sched_barrier(0);
-    x_fetch(0, 0u);
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(S * first + 2u * d + half, d);
+    x_fetch(0, 0u, 0, FW);
     __builtin_amdgcn_sched_barrier(0);
     // escape lists of the round's tiles: wave w looks after tiles w, w + 8, ...: where the list lies
     // and how long it is, and (first k range) its first 64 entries, a lane each, with their rows
@@ -160,23 +173,7 @@ void k_mx4_gemm(Mx4Args a) {
       for (int r = 0; r < 4; ++r)
         bases[j] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rb, (uint32_t)(row0[j] + 4 * g + r), 0, 0) << (8 * r);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    u32x4 bv[D][TP];
-    uint32_t bs[D][TP];
-    const auto load = [&](uint32_t kb, int d) {
-#pragma unroll
-      for (int j = 0; j < TP; ++j) {
-        const uint32_t off = kb < nkb ? kb * kTileMX : kOOB;
-        bv[d][j] = __builtin_amdgcn_raw_buffer_load_b128(rq[j], off + 16u * lane, 0, kAuxNT);
-        bs[d][j] = __builtin_amdgcn_raw_buffer_load_b8(rq[j], off + 1024u + lane, 0, kAuxNT);
-      }
-    };
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      load(S * first + 2u * d + half, d);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    mx_wait_le<D * kLoads>();                      // the first chunk of x is in LDS
+    mx_wait_le<0>();                               // the first chunk of x is in LDS
     lds_barrier();
     uint32_t lent[EL], lval[EL];                   // entry: column, row of the tile in bits 28..31
 #pragma unroll
@@ -190,6 +187,19 @@ void k_mx4_gemm(Mx4Args a) {
         lval[q] = a.esc_val[lt0[q] + lane];
       }
     }
+    // the x values of the first eight: lane m's of x row m, needed after the blocks
+    const int xm = lane & (16 * NT - 1);
+    const bool xlive = lane < 16 * NT && xm < a.m;
+    const auto gather = [&](uint32_t ent, uint32_t cntl, uint32_t i0, uint32_t (&xe)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t col = (uint32_t)__builtin_amdgcn_readlane(ent, i0 + i);
+        xe[i] = __builtin_amdgcn_raw_buffer_load_b16(rx, xlive && i0 + i < cntl ? 2u * (xm * kx + col) : kOOB, 0, 0);
+      }
+    };
+    uint32_t xe[EL][8];
+#pragma unroll
+    for (int q = 0; q < EL; ++q) gather(lent[q], lcnt[q], 0, xe[q]);
 
     floatx4 acc[TP][NT];
 #pragma unroll
@@ -200,71 +210,71 @@ void k_mx4_gemm(Mx4Args a) {
     for (uint32_t c = 0; c < n_chunks; ++c) {
       const uint32_t b = c & 1u;
       const uint32_t kb_here = S * chunk_at(c), kb_next = c + 1 < n_chunks ? S * chunk_at(c + 1) : nkb;
+      // Stage i = 4 s + t multiplies k-group t of block 2 s + half; meanwhile the next stage's x fragments
+      // are read and its quarter of the block decodes, in the shadow of the products.
+      constexpr int kStages = 2 * S;
+      u32x4 xv[2][NT], p[2][TP];
+      const u32x4* const xb = &s_x[b][0];
+      const auto fetch = [&](int i, u32x4 (&x)[NT], u32x4 (&pq)[TP]) {
+        const int s = i >> 2, t = i & 3;
 #pragma unroll
-      for (int s = 0; s < S / 2; ++s) {            // block 2 s + half of the chunk
-        const int slot = s % D;
-        // the x fragments of k-group t + 1 are read while those of t multiply (the first ones while
-        // the blocks decode): left to itself each read is waited for just behind its issue
-        const u32x4* xb = &s_x[b][s * 512 * NT];
-        u32x4 xv[2][NT];
+        for (int cc = 0; cc < NT; ++cc) x[cc] = xb[s * 512 * NT + 512 * cc + xo[cc & 1][t]];
 #pragma unroll
-        for (int cc = 0; cc < NT; ++cc) xv[0][cc] = xb[512 * cc + xo[cc & 1][0]];
-        __builtin_amdgcn_sched_barrier(0);
-        uint32_t p[TP][16];
+        for (int j = 0; j < TP; ++j) pq[j] = mx4_quarter(bv[s % D][j][t], bs[s % D][j]);
+      };
+      fetch(0, xv[0], p[0]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < TP; ++j) {
-          mx4_pairs(bv[slot][j], bs[slot][j], p[j]);
-          pin16(p[j]);
+      for (int i = 0; i < kStages; ++i) {
+        const int s = i >> 2;
+        if (i + 1 < kStages) fetch(i + 1, xv[(i + 1) & 1], p[(i + 1) & 1]);
+        // the next chunk of x in the first four stages (past the last chunk: nothing, as zeros; the load
+        // pattern stays fixed, so the compiler's wait counts stay exact)
+        if (i < 4) x_fetch(c + 1, b ^ 1u, i * FW / 4, (i + 1) * FW / 4);
+        // the block's last quarter has just been decoded: its slot takes the block D steps on
+        if ((i & 3) == 2)
+          load((s + D < S / 2 ? kb_here + 2u * (s + D) : kb_next + 2u * (s + D - S / 2)) + half, s % D);
+#pragma unroll
+        for (int cc = 0; cc < NT; ++cc)
+#pragma unroll
+          for (int j = 0; j < TP; ++j)
+            acc[j][cc] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p[i & 1][j]),
+                                                                 __builtin_bit_cast(bf16x8, xv[i & 1][cc]), acc[j][cc],
+                                                                 0, 0, 0);
+        // the reads first, then products and conversions in turn
+        __builtin_amdgcn_sched_group_barrier(0x100, NT, 0);
+#pragma unroll
+        for (int g2 = 0; g2 < NT * TP; ++g2) {
+          __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x2, NT == 1 ? 5 : NT == 2 ? 3 : 2, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
-        // (past the last chunk: nothing, as zeros; the load pattern stays fixed, so the compiler's
-        // wait counts stay exact)
-        if (s == 0) x_fetch(c + 1, b ^ 1u);
-        load((s + D < S / 2 ? kb_here + 2u * (s + D) : kb_next + 2u * (s + D - S / 2)) + half, slot);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          if (t < 3) {
-#pragma unroll
-            for (int cc = 0; cc < NT; ++cc) xv[(t + 1) & 1][cc] = xb[512 * cc + xo[cc & 1][t + 1]];
-          }
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int cc = 0; cc < NT; ++cc)
-#pragma unroll
-            for (int j = 0; j < TP; ++j) {
-              const u32x4 av = {p[j][4 * t], p[j][4 * t + 1], p[j][4 * t + 2], p[j][4 * t + 3]};
-              acc[j][cc] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av),
-                                                                   __builtin_bit_cast(bf16x8, xv[t & 1][cc]),
-                                                                   acc[j][cc], 0, 0, 0);
-            }
-          __builtin_amdgcn_sched_barrier(0);
-        }
       }
-      // the next chunk is in LDS: its loads went out before this chunk's S refills
-      mx_wait_le<S / 2 * kLoads>();
+      // the next chunk is in LDS: all refills but the first went out after its loads
+      mx_wait_le<(S / 2 - 1) * kLoads>();
       lds_barrier();
     }
 
-    // Into the x buffers, which nothing reads any more: the odd blocks' sums, for the even blocks'
-    // waves; and behind them, per tile with escapes, their products, [16 rows][16 NT x rows]: lane m
-    // adds x row m's, entry by entry in order.
+    // Into the x buffers, which nothing reads any more: each half's sums of the tiles the other half
+    // finishes (the even ones the first half, the odd ones the second); and behind them, per tile, the
+    // escapes' products, [16 rows][16 NT x rows]: lane m adds x row m's, entry by entry in order (a
+    // row's entries follow each other, so its sum is stored once).
     u32x4* const part = &s_x[0][0] + sub * (TP * NT * 64) + lane;
-    if (half == 1) {
 #pragma unroll
-      for (int j = 0; j < TP; ++j)
+    for (int j = 0; j < TP; ++j)
+      if ((j & 1) != (int)half) {
 #pragma unroll
         for (int cc = 0; cc < NT; ++cc) part[(j * NT + cc) * 64] = __builtin_bit_cast(u32x4, acc[j][cc]);
-    }
+      }
     float* const s_q = reinterpret_cast<float*>(&s_x[0][0] + 4 * TP * NT * 64);   // [4 TP][16][16 NT]
 #pragma unroll
     for (int q = 0; q < EL; ++q) {
-      if (w + W * q >= cnt) continue;
+      if (w + W * q >= cnt || sp != 0) continue;
       float* const tq = s_q + (w + W * q) * (256 * NT);
 #pragma unroll
       for (int i = 0; i < 4 * NT; ++i) tq[64 * i + lane] = 0.0f;
-      const int xm = lane & (16 * NT - 1);
-      const bool live = lane < 16 * NT && xm < a.m;
+      uint32_t row = 0;
+      float sum = 0.0f;
       for (uint32_t e0 = 0; e0 < lcnt[q]; e0 += 64) {
         if (e0 > 0) {                              // past the first 64: from memory
           const bool in = e0 + lane < lcnt[q];
@@ -278,28 +288,28 @@ void k_mx4_gemm(Mx4Args a) {
           er += lt0[q] + e0 + lane >= (uint32_t)__builtin_amdgcn_readlane(lstart[q], i) ? 1u : 0u;
         const uint32_t here = lcnt[q] - e0 < 64u ? lcnt[q] - e0 : 64u;
         for (uint32_t i0 = 0; i0 < here; i0 += 8) {
-          uint32_t xe[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t col = (uint32_t)__builtin_amdgcn_readlane(lent[q], i0 + i);
-            xe[i] = __builtin_amdgcn_raw_buffer_load_b16(rx, live && i0 + i < here ? 2u * (xm * kx + col) : kOOB, 0, 0);
-          }
+          if (e0 + i0 > 0) gather(lent[q], here, i0, xe[q]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (i0 + i >= here) break;
-            const uint32_t row = (uint32_t)__builtin_amdgcn_readlane(er, i0 + i);
+            const uint32_t r = (uint32_t)__builtin_amdgcn_readlane(er, i0 + i);
             const float v = bf16_to_float((uint32_t)__builtin_amdgcn_readlane(lval[q], i0 + i));
-            if (live) tq[row * (16 * NT) + xm] = fmaf(bf16_to_float(xe[i]), v, tq[row * (16 * NT) + xm]);
+            if (r != row) {
+              if (xlive) tq[row * (16 * NT) + xm] = sum;
+              row = r;
+              sum = 0.0f;
+            }
+            sum = fmaf(bf16_to_float(xe[q][i]), v, sum);
           }
         }
       }
+      if (xlive) tq[row * (16 * NT) + xm] = sum;   // (without entries: zeros over zeros)
     }
     lds_barrier();
-    // sums, scale and store: lane (g, r16) holds rows 4 g .. 4 g + 3
-    // of x row 16 cc + r16
+    // sums, scale and store: lane (g, r16) holds rows 4 g .. 4 g + 3 of x row 16 cc + r16
 #pragma unroll
     for (int j = 0; j < TP; ++j) {
-      if (half == 1 || !have[j]) continue;
+      if ((j & 1) != (int)half || !have[j]) continue;
       float qv[NT][4];
 #pragma unroll
       for (int cc = 0; cc < NT; ++cc) {
@@ -344,14 +354,16 @@ void k_mx4_gemm(Mx4Args a) {
 // launcher
 // ---------------------------------------------------------------------------------------------
 typedef void (*Mx4Kernel)(Mx4Args);
-struct Mx4Shape {
-  Mx4Kernel kern;
-  int tp, s;
-};
-static Mx4Shape mx4_shape(int nt) {
-  if (nt == 1) return {k_mx4_gemm<1, 3, 8, 4>, 3, 8};
-  if (nt == 2) return {k_mx4_gemm<2, 3, 8, 4>, 3, 8};
-  return {k_mx4_gemm<4, 3, 4, 2>, 3, 4};
+// blocks per x chunk
+static int mx4_chunk(int nt) { return nt == 1 ? 16 : nt == 2 ? 8 : 4; }
+template <int NT, int S, int D>
+static Mx4Kernel mx4_pick(int tp) {
+  return tp == 1 ? k_mx4_gemm<NT, 1, S, D> : tp == 2 ? k_mx4_gemm<NT, 2, S, D> : k_mx4_gemm<NT, 3, S, D>;
+}
+static Mx4Kernel mx4_kernel(int nt, int tp) {
+  if (nt == 1) return mx4_pick<1, 16, 4>(tp);
+  if (nt == 2) return mx4_pick<2, 8, 4>(tp);
+  return mx4_pick<4, 4, 2>(tp);
 }
 
 hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_t n, int64_t k, YOut y,
@@ -362,8 +374,8 @@ hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_
   const int64_t tiles = (n + kTileRows - 1) / kTileRows, kb = k / kTileCols;
   for (int64_t m0 = 0; m0 < m; m0 += 64) {
     const int mb = (int)(m - m0 < 64 ? m - m0 : 64);
-    const Mx4Shape sh = mx4_shape((mb + 15) / 16);
-    const int64_t chunks = (kb + sh.s - 1) / sh.s;
+    const int nt = (mb + 15) / 16, cb = mx4_chunk(nt);
+    const int64_t chunks = (kb + cb - 1) / cb;
     const int64_t slots = di.cus;
     // k ranges: as many as give every wave pair of the chip a tile, of at least one chunk
     int64_t ranges = slots * (kMxWaves / 2) / tiles;
@@ -382,7 +394,7 @@ hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_
     if (groups > tiles) groups = tiles;
     if (groups < 1) groups = 1;
     const int64_t most = (tiles + groups - 1) / groups;             // tiles of the busiest workgroup
-    const int64_t rounds = (most + kMxWaves / 2 * sh.tp - 1) / (kMxWaves / 2 * sh.tp);
+    const int64_t rounds = (most + kMxWaves / 2 * kMxTiles - 1) / (kMxWaves / 2 * kMxTiles);
     const YOut yp = y + m0 * n;
     Mx4Args a;
     a.x = x + m0 * k;
@@ -400,7 +412,7 @@ hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_
     a.ysplit = (int64_t)mb * n;
     a.yvec = a.y16 ? (reinterpret_cast<uintptr_t>(a.y16) & 7u) == 0 && n % 4 == 0
                    : (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0 && n % 4 == 0;
-    hipLaunchKernelGGL(sh.kern, dim3((unsigned)(groups * ranges)), dim3(64 * kMxWaves), 0, s, a);
+    hipLaunchKernelGGL(mx4_kernel(nt, (a.tpr + kMxWaves / 2 - 1) / (kMxWaves / 2)), dim3((unsigned)(groups * ranges)), dim3(64 * kMxWaves), 0, s, a);
     err = hipGetLastError();
     if (err != hipSuccess) return err;
     if (ws) {
