@@ -420,14 +420,6 @@ hipError_t launch_decode(const Planes& p, int64_t n, int64_t k, uint16_t* out, h
                      p.ae, p.lo, n, k, out);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
-  return launch_escape_scatter(p, n, k, out, s);
-}
-
-hipError_t launch_escape_scatter(const Planes& p, int64_t n, int64_t k, uint16_t* out, hipStream_t s) {
-  DevInfo di;
-  hipError_t err = dev_info(&di);
-  if (err != hipSuccess) return err;
-  const int64_t cap = (int64_t)di.cus * 8;
   int64_t sblocks = (n + 3) / 4;
   if (sblocks > cap) sblocks = cap;
   hipLaunchKernelGGL(k_escape_scatter, dim3((unsigned)sblocks), dim3(kBlock), 0, s, p.esc_ptr,

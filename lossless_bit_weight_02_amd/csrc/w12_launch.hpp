@@ -142,8 +142,6 @@ hipError_t launch_interleave(const Planes& gate, const Planes& up, int64_t rows,
                              hipStream_t s);
 // 8-bit Q-pass copy of a record: per-row scales, codes in the AE storage order, escaped slots 0
 hipError_t launch_i8_build(const Planes& p, int64_t n, int64_t k, int8_t* q, float* scale, hipStream_t s);
-// every escape's value over its slot of the dense matrix out [n][k]
-hipError_t launch_escape_scatter(const Planes& p, int64_t n, int64_t k, uint16_t* out, hipStream_t s);
 // microscaled 4-bit copy of a record (padded_rows(n) * k * 17 / 32 bytes) with its list of escapes that
 // are not zero (nz_ptr [n + 1], nz_end [n], columns and values), and the bfloat16 matrix it stands
 // for (p.mx4, p.base, the record's escapes)
