@@ -38,6 +38,7 @@ constexpr int kLpCap = 256;                      // keys of a wave's candidate l
 constexpr int kLpWaves = 4;
 constexpr int kLpElems = 16;                     // logits of a lane per batch
 constexpr int kLpBatch = 64 * kLpElems;          // logits of a wave per batch
+constexpr uint32_t kLpMasked = 0x007FFFFFu;      // the order of -Inf
 constexpr int kLpCountStep = 32;                 // rows' counts 128 bytes apart: counts of one line wait for each other
 constexpr int kLpAhead = 4;                      // keys of a part loaded together when parts join
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
@@ -187,6 +188,13 @@ struct LpTop {
         const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, i) << 32 |
                            (uint32_t)__builtin_amdgcn_readlane(lo, i);
         rank[0] += o > key[0] ? 1 : 0;
+      }
+    } else if (cnt <= 128) {
+#pragma unroll 8
+      for (int i = 0; i < cnt; ++i) {
+        const uint64_t o = list[i];
+        rank[0] += o > key[0] ? 1 : 0;
+        rank[1] += o > key[1] ? 1 : 0;
       }
     } else {
 #pragma unroll 4
@@ -491,14 +499,16 @@ __device__ __forceinline__ void lp_end(const LpArgs& a, int64_t row, int sp, flo
     uint64_t key[kLpAhead];
 #pragma unroll
     for (int r = 0; r < kLpAhead; ++r) key[r] = mine && r < a.top ? dev_load(keys + r) : 0;
-    const uint32_t first = lp_order(M);
     lp_join(M, s, T);
     if (a.top > 0) {
-      // each part's keys descend: the K-th of the parts' maxima bounds the rest, and a part whose
+      // each part's keys descend: the K-th of their first four each bounds the rest, and a part whose
       // next key is below the bound is done
       top.cnt = 0;
-      const uint32_t hi = lp_order(M);
-      top.seen = a.top == 1 ? hi : lp_kth<1>({first}, a.top, hi);
+      uint32_t heads[kLpAhead];
+#pragma unroll
+      for (int r = 0; r < kLpAhead; ++r) heads[r] = (uint32_t)(key[r] >> 32);
+      // (the largest: the row's maximum, or a NaN)
+      top.seen = lp_kth<kLpAhead>(heads, a.top, __ballot(heads[0] == 0xFFFFFFFFu) ? 0xFFFFFFFFu : lp_order(M));
       bool more = true;
       for (int r0 = 0; r0 < a.top && more; r0 += kLpAhead) {
         if (r0 > 0) {
@@ -507,7 +517,9 @@ __device__ __forceinline__ void lp_end(const LpArgs& a, int64_t row, int sp, flo
         }
 #pragma unroll
         for (int r = 0; r < kLpAhead; ++r) {
-          const bool ok = key[r] != 0 && (uint32_t)(key[r] >> 32) >= top.seen;
+          // (of the masked logits, those of the first part alone: its K keys come before the others')
+          const uint32_t ord = (uint32_t)(key[r] >> 32);
+          const bool ok = key[r] != 0 && ord >= top.seen && (ord != kLpMasked || lane == 0);
           const uint64_t bl = __ballot(ok);
           if (bl == 0) more = false;
           if (!more) continue;
@@ -728,7 +740,10 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs_part(LpArgs a) {
   top.K = a.top;
   top.list = s_best;
   float lowf = 0.0f;
-  if (a.top > 0) {
+  // nothing but masked logits: the first columns
+  const bool masked = M == -INFINITY && __ballot(s != s) == 0;
+  if (lane == 0) s_cnt[w] = masked ? 1 : 0;
+  if (a.top > 0 && !masked) {
     const uint32_t hi = lp_order(M);
     if (a.top == 1) {
       top.seen = hi;
@@ -762,7 +777,16 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs_part(LpArgs a) {
     }
   }
   __syncthreads();
-  const int total = a.top > 0 ? __builtin_amdgcn_readfirstlane(s_total) : 0;
+  const bool none = __builtin_amdgcn_readfirstlane(s_cnt[0] + s_cnt[1] + s_cnt[2] + s_cnt[3]) == kLpWaves;
+  int total = a.top > 0 ? __builtin_amdgcn_readfirstlane(s_total) : 0;
+  if (a.top > 0 && M == -INFINITY && !none) {      // masked logits and a NaN: the long way
+    lowf = -INFINITY;
+    top.seen = 0;
+    total = kLpCap + 1;
+  }
+  if (a.top > 0 && none) {
+    if (w == 0 && lane < a.top && c0 + lane < c1) s_best[lane] = (uint64_t)kLpMasked << 32 | (0xFFFFFFFFu - (uint32_t)(c0 + lane));
+  }
   if (total > kLpCap) {
     // more candidates than the shared list holds (many equal to the bound): by each wave's own
     top.list = s_list[w];
@@ -779,6 +803,9 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs_part(LpArgs a) {
   T = ((s_run[0][2] + s_run[1][2]) + s_run[2][2]) + s_run[3][2];
   if (total > kLpCap) {
     lp_merge(top, s_best, s_list, s_cnt, s_seen, s_max, M, lane);
+  } else if (a.top > 0 && none) {
+    lp_wave_fence();
+    top.cnt = c1 - c0 < a.top ? (int)(c1 - c0) : a.top;   // (already in order)
   } else if (a.top > 0) {
     top.cnt = total;
     top.cut(lane);

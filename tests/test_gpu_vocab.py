@@ -149,7 +149,7 @@ def test_logprobs_sizes(m, n, top, dt):
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("m,n", [(6, 9000), (2060, 5000)])
+@pytest.mark.parametrize("m,n", [(6, 9000), (24, 9000), (24, 120000), (24, 700), (600, 9000), (2060, 5000)])
 def test_logprobs_masks(m, n, dt):
     """-Inf masks up to whole rows, the type's lowest value, +Inf, NaN (either sign), equal logits, -0."""
     inf = math.inf
@@ -166,7 +166,7 @@ def test_logprobs_masks(m, n, dt):
     y[4, :] = -0.0
     y[4, 100] = 0.0
     y[5, 8000 % n] = inf
-    if m > 100:
+    if m > 20:
         y[10, n - 1] = math.nan
         y[11, 0] = -math.nan
         y[11, 77] = math.nan
@@ -174,9 +174,16 @@ def test_logprobs_masks(m, n, dt):
         y[12, 3] = math.nan
         y[13] = torch.finfo(dt).max
         y[14, ::2] = -inf
+        y[16] = -inf
+        y[16, 2000 % n] = -math.nan                  # masked logits and a NaN, in different places
+        y[16, n - 1] = math.nan
+        y[17] = math.nan
+        y[18] = -inf
+        y[18, n // 2] = inf
         y[15] = -inf
         y[15, 1::900] = torch.linspace(-1, 1, len(range(1, n, 900))).to(dt)
-    _check_lp(y, tok, 9, "masks")
+    for top in (1, 9, 64):
+        _check_lp(y, tok, top, "masks")
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
