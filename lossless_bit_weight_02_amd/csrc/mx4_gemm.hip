@@ -63,7 +63,7 @@ void k_mx4_gemm(Mx4Args a) {
   constexpr int W = kMxWaves;
   constexpr int F = 4 * NT * S;                    // 1 KiB x pieces per chunk
   constexpr int FW = F / W;
-  static_assert(F % W == 0 && FW % 4 == 0 && S % (2 * D) == 0, "whole rings and 256-column pieces per chunk");
+  static_assert(F % W == 0 && S % (2 * D) == 0, "whole rings and 256-column pieces per chunk");
   static_assert(4 * TP * NT * 2 <= 2 * F, "the odd blocks' sums and the escapes' products fit the x buffers");
   constexpr int kLoads = 2 * TP;                   // loads per step
   __shared__ __attribute__((aligned(16))) u32x4 s_x[2][F * 64];
@@ -92,19 +92,26 @@ void k_mx4_gemm(Mx4Args a) {
   // (q = P % 8 NT) of its 256-column half P / 8 NT, 512 bytes a row, slot (c16 + row) % 32 the row's
   // 16-byte column slot c16; wave w loads pieces w + 8 i.
   const uint32_t prow = (uint32_t)lane >> 5, pslot = (uint32_t)lane & 31u;
-  // (pos: the chunk's place in the workgroup's order, n_chunks and past it: nothing)
-  const auto x_fetch = [&](uint32_t pos, uint32_t buf, int from, int to) {
-    const uint32_t c = chunk_at(pos);
+  uint32_t xoff[FW];                               // the lane's bytes of a piece in the first chunk
 #pragma unroll
-    for (int i = from; i < to; ++i) {
-      const uint32_t P = (uint32_t)(w + W * i);
-      const uint32_t q = P % (8u * NT), hb = P / (8u * NT);
-      const uint32_t row = 2u * q + prow;
-      const uint32_t c16 = (pslot - row) & 31u;
-      const uint32_t col = col0 + 128u * S * c + 256u * hb + 8u * c16;
-      const bool ok = (int)row < a.m && col < col1 && pos < n_chunks;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (__attribute__((address_space(3))) void*)&s_x[buf][P * 64u], 16,
-                                               ok ? 2u * (row * kx + col) : kOOB, 0, 0, 0);
+  for (int i = 0; i < FW; ++i) {
+    const uint32_t P = (uint32_t)(w + W * i), q = P % (8u * NT), hb = P / (8u * NT);
+    const uint32_t row = 2u * q + prow, c16 = (pslot - row) & 31u;
+    xoff[i] = (int)row < a.m ? 2u * (row * kx + col0 + 256u * hb + 8u * c16) : kOOB;
+  }
+  // (pos: the chunk's place in the workgroup's order; n_chunks and past it: nothing, as zeros -- the
+  // load pattern stays fixed, so the compiler's wait counts stay exact)
+  const auto x_fetch = [&](uint32_t pos, uint32_t buf) {
+    const uint32_t c = chunk_at(pos), at = 128u * S * c;   // columns from the range's start
+    const bool whole = pos < n_chunks && at + 128u * S <= col1 - col0;
+#pragma unroll
+    for (int i = 0; i < FW; ++i) {
+      const uint32_t P = (uint32_t)(w + W * i), q = P % (8u * NT), hb = P / (8u * NT);
+      const uint32_t c16 = (pslot - (2u * q + prow)) & 31u;
+      const bool ok = whole || (pos < n_chunks && at + 256u * hb + 8u * c16 < col1 - col0);
+      const uint32_t off = ok && xoff[i] != kOOB ? xoff[i] + 2u * at : kOOB;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (__attribute__((address_space(3))) void*)&s_x[buf][P * 64u], 16, off,
+                                               0, 0, 0);
     }
   };
   // operand reads: block 2 s + half, k-group t, activation tile cc at 512 NT s + 512 cc +
@@ -146,9 +153,7 @@ void k_mx4_gemm(Mx4Args a) {
       }
     };
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int d = 0; d < D; ++d) load(S * first + 2u * d + half, d);
-    x_fetch(0, 0u, 0, FW);
+    x_fetch(0, 0u);
     __builtin_amdgcn_sched_barrier(0);
     // escape lists of the round's tiles: wave w looks after tiles w, w + 8, ...: where the list lies
     // and how long it is, and (first k range) its first 64 entries, a lane each, with their rows
@@ -173,7 +178,11 @@ void k_mx4_gemm(Mx4Args a) {
       for (int r = 0; r < 4; ++r)
         bases[j] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rb, (uint32_t)(row0[j] + 4 * g + r), 0, 0) << (8 * r);
     }
-    mx_wait_le<0>();                               // the first chunk of x is in LDS
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(S * first + 2u * d + half, d);
+    __builtin_amdgcn_sched_barrier(0);
+    mx_wait_le<D * kLoads>();                      // the first chunk of x is in LDS
     lds_barrier();
     uint32_t lent[EL], lval[EL];                   // entry: column, row of the tile in bits 28..31
 #pragma unroll
@@ -187,7 +196,6 @@ void k_mx4_gemm(Mx4Args a) {
         lval[q] = a.esc_val[lt0[q] + lane];
       }
     }
-    // the x values of the first eight: lane m's of x row m, needed after the blocks
     const int xm = lane & (16 * NT - 1);
     const bool xlive = lane < 16 * NT && xm < a.m;
     const auto gather = [&](uint32_t ent, uint32_t cntl, uint32_t i0, uint32_t (&xe)[8]) {
@@ -197,9 +205,6 @@ void k_mx4_gemm(Mx4Args a) {
         xe[i] = __builtin_amdgcn_raw_buffer_load_b16(rx, xlive && i0 + i < cntl ? 2u * (xm * kx + col) : kOOB, 0, 0);
       }
     };
-    uint32_t xe[EL][8];
-#pragma unroll
-    for (int q = 0; q < EL; ++q) gather(lent[q], lcnt[q], 0, xe[q]);
 
     floatx4 acc[TP][NT];
 #pragma unroll
@@ -224,13 +229,12 @@ void k_mx4_gemm(Mx4Args a) {
       };
       fetch(0, xv[0], p[0]);
       __builtin_amdgcn_sched_barrier(0);
+      x_fetch(c + 1, b ^ 1u);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < kStages; ++i) {
         const int s = i >> 2;
         if (i + 1 < kStages) fetch(i + 1, xv[(i + 1) & 1], p[(i + 1) & 1]);
-        // the next chunk of x in the first four stages (past the last chunk: nothing, as zeros; the load
-        // pattern stays fixed, so the compiler's wait counts stay exact)
-        if (i < 4) x_fetch(c + 1, b ^ 1u, i * FW / 4, (i + 1) * FW / 4);
         // the block's last quarter has just been decoded: its slot takes the block D steps on
         if ((i & 3) == 2)
           load((s + D < S / 2 ? kb_here + 2u * (s + D) : kb_next + 2u * (s + D - S / 2)) + half, s % D);
@@ -250,8 +254,8 @@ void k_mx4_gemm(Mx4Args a) {
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      // the next chunk is in LDS: all refills but the first went out after its loads
-      mx_wait_le<(S / 2 - 1) * kLoads>();
+      // the next chunk is in LDS: its loads went out before this chunk's refills
+      mx_wait_le<S / 2 * kLoads>();
       lds_barrier();
     }
 
@@ -288,7 +292,8 @@ void k_mx4_gemm(Mx4Args a) {
           er += lt0[q] + e0 + lane >= (uint32_t)__builtin_amdgcn_readlane(lstart[q], i) ? 1u : 0u;
         const uint32_t here = lcnt[q] - e0 < 64u ? lcnt[q] - e0 : 64u;
         for (uint32_t i0 = 0; i0 < here; i0 += 8) {
-          if (e0 + i0 > 0) gather(lent[q], here, i0, xe[q]);
+          uint32_t xe[8];                          // lane m's: x row m's value at each entry
+          gather(lent[q], here, i0, xe);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (i0 + i >= here) break;
@@ -299,7 +304,7 @@ void k_mx4_gemm(Mx4Args a) {
               row = r;
               sum = 0.0f;
             }
-            sum = fmaf(bf16_to_float(xe[q][i]), v, sum);
+            sum = fmaf(bf16_to_float(xe[i]), v, sum);
           }
         }
       }
