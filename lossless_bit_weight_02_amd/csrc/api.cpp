@@ -101,9 +101,12 @@ w12::Planes planes_of(const w12_weight* wt) {
 // kernel wins on 1.5 to 2.5 tiles per CU (128 rows: [6144, 5120] 73.1 vs 85.3, [8192, 5120] 74.7
 // vs 85.2; [12288, 5120] ties, 87.1 vs 86.4), the dense baseline's up to 3 ([5120, 17408] 121.2
 // vs 140.9, [5120, 6144] 55.6 vs 73.9, [8192, 5120] 54.7 vs 69.3, [12288, 5120] 68.6 vs 70.8).
+// The 4-bit copy takes it only at 13..16 rows above 24 tiles per CU ([152064, 5120], 16 rows, vs the
+// matrix cores: 90.2 vs 93.8; 8 rows 91.6 vs 86.3; [34816, 5120], 16 rows: 27.1 vs 22.4): on fewer
+// tiles its cost per workgroup outweighs the halved bytes, at other widths the matrix cores win.
 bool stream_auto_pick(w12::Fmt f, int64_t m, int64_t tiles, int64_t k, int64_t cus) {
   const bool dense = f == w12::kFmtBF16;
-  if (f == w12::kFmtMX4) return false;
+  if (f == w12::kFmtMX4) return tiles > 24 * cus && m >= 13 && m <= 16 && k <= 8192;
   if (m <= 32)
     return k <= 8192 && (!dense || tiles <= 6 * cus) &&
            ((m >= 3 && m <= 16 && 2 * tiles >= 3 * cus) ||
@@ -163,7 +166,13 @@ int run_gemm(w12::Fmt f, const uint16_t* x, int64_t m, const w12::Planes& p, int
     return fail(silu ? W12_ERR_ARG : W12_ERR_SHAPE, "the streaming kernel does not take this call "
                 "(rows of fewer than 2^26 columns whose x phases fit the LDS; no SiLU epilogue)");
   const bool stream_auto = stream_ok && stream_auto_pick(f, m, tiles, k, dinfo.cus);
-  const bool gemv_auto = m <= 2 || (m <= 5 && tiles <= 1024 && k <= 8192);
+  // The 4-bit copy's bytes are half of the 8-bit view's while the GEMV's work per weight and row of x
+  // stays, so the matrix cores win from 3 rows everywhere ([5120, 17408], us, GEMV vs matrix core:
+  // 33.4 vs 16.0; [8192, 5120] 12.9 vs 12.1; [5120, 5120] 10.8 vs 10.7), and at 2 rows on long rows
+  // ([5120, 17408] 19.9 vs 16.0) and above 6 tiles per CU ([34816, 5120] 24.4 vs 22.8, [152064,
+  // 5120] 98.6 vs 82.2; below it [17408, 5120] 14.8 vs 16.5, [5120, 5120] 8.5 vs 10.9).
+  const bool gemv_auto = f == w12::kFmtMX4 ? m == 1 || (m == 2 && k <= 8192 && tiles <= 6 * (int64_t)dinfo.cus)
+                                           : m <= 2 || (m <= 5 && tiles <= 1024 && k <= 8192);
   const bool use_stream = flags == W12_PATH_STREAM || (flags == W12_PATH_AUTO && stream_auto);
   const bool gemv = !use_stream && (flags == W12_PATH_GEMV || (flags == W12_PATH_AUTO && gemv_auto));
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -190,7 +199,7 @@ int run_gemm(w12::Fmt f, const uint16_t* x, int64_t m, const w12::Planes& p, int
   }
   hipError_t e = use_stream ? w12::launch_stream(f, x, m, p, n, k, yo, s)
                  : gemv     ? w12::launch_gemv(f, x, m, p, n, k, yo, s, sc)
-                 : f == w12::kFmtMX4 && m > 32 ? w12::launch_mx4_gemm(x, m, p, n, k, yo, s, sc)
+                 : f == w12::kFmtMX4 ? w12::launch_mx4_gemm(x, m, p, n, k, yo, s, sc)
                             : w12::launch_mfma(f, x, m, p, n, k, yo, s, sc);
   if (e != hipSuccess) return hip_fail(e, use_stream ? "stream launch" : gemv ? "gemv launch" : "mfma launch");
   return ok();

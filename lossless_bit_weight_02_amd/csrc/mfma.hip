@@ -623,9 +623,11 @@ void k_mfma(MfmaArgs a) {
 // ---------------------------------------------------------------------------------------------
 template <int FMT, int W>
 static MfmaKernel pick(int nt) {
-  if constexpr (W == 12 && FMT != kFmtI8)   // the 8-bit copy runs passes of at most 64 rows
-    if (nt == 8) return k_mfma<FMT, 8, W, false>;
-  if (nt >= 3) return mfma_wide_kernel(static_cast<Fmt>(FMT), nt);
+  if constexpr (FMT != kFmtMX4) {            // the 4-bit copy's passes of more than 32 rows: mx4_gemm.hip
+    if constexpr (W == 12 && FMT != kFmtI8)  // the 8-bit copy runs passes of at most 64 rows
+      if (nt == 8) return k_mfma<FMT, 8, W, false>;
+    if (nt >= 3) return mfma_wide_kernel(static_cast<Fmt>(FMT), nt);
+  }
   return nt == 1 ? k_mfma<FMT, 1, W, false> : k_mfma<FMT, 2, W, false>;
 }
 
@@ -765,7 +767,7 @@ hipError_t launch_mfma(Fmt f, const uint16_t* x, int64_t m, const Planes& p, int
   const bool wide_ok = f == kFmtBF16 ? 256 * k < (int64_t(1) << 32)
                       : f == kFmtI8   ? false
                                       : k * 128 * 2 <= (int64_t)sc.bytes;
-  const int64_t max_step = wide_ok ? 128 : 64;
+  const int64_t max_step = f == kFmtMX4 ? 32 : wide_ok ? 128 : 64;
   for (int64_t m0 = 0, step = 0; m0 < m; m0 += step) {
     step = (m - m0) < max_step ? (m - m0) : max_step;
     // Fewer than 1.5 tiles per CU: passes of 32 rows, which split k over the chip's waves, instead
@@ -824,7 +826,7 @@ hipError_t launch_mfma_top1(Fmt f, const uint16_t* x, int64_t m, const Planes& p
     a.esc_ptr = p.esc_ptr; a.esc_end = p.esc_end; a.esc_col = p.esc_col; a.esc_val = p.esc_val;
     a.w = p.w;
     a.scale = p.scale;
-  a.mx4 = p.mx4;
+    a.mx4 = p.mx4;
     a.y = nullptr;
     a.y16 = nullptr;
     a.ldy = nh;

@@ -179,9 +179,6 @@ void k_mfma_wide(MfmaArgs a) {
     if constexpr (FMT == kFmtBF16) {
       ra = make_rsrc(a.w + row0 * a.k, valid ? KB * (uint32_t)kTileBF : 0u);
       rl = ra;
-    } else if constexpr (FMT == kFmtMX4) {
-      ra = make_rsrc(a.mx4 + row0 / kTileRows * (int64_t)KB * kTileMX, valid ? KB * (uint32_t)kTileMX : 0u);
-      rl = ra;
     } else {
       ra = make_rsrc(a.ae + row0 * a.k, valid ? KB * (uint32_t)kTileAE : 0u);
       rl = make_rsrc(a.lo + row0 * a.k / 2, valid ? KB * (uint32_t)kTileLO : 0u);
@@ -354,7 +351,6 @@ MfmaKernel mfma_wide_kernel(Fmt f, int nt, bool silu) {
   if (f == kFmtQ8) return nt == 3 ? k_mfma_wide<kFmtQ8, 3> : k_mfma_wide<kFmtQ8, 4>;
   if (f == kFmtQ8M) return nt == 3 ? k_mfma_wide<kFmtQ8M, 3> : k_mfma_wide<kFmtQ8M, 4>;
   if (f == kFmtI8) return nt == 3 ? k_mfma_wide<kFmtI8, 3> : k_mfma_wide<kFmtI8, 4>;
-  if (f == kFmtMX4) return nt == 3 ? k_mfma_wide<kFmtMX4, 3> : k_mfma_wide<kFmtMX4, 4>;
   return nt == 3 ? k_mfma_wide<kFmtBF16, 3> : k_mfma_wide<kFmtBF16, 4>;
 }
 

@@ -28,6 +28,7 @@ namespace w12 {
 
 constexpr int kMxWaves = 8;
 constexpr int kMxTiles = 3;      // tiles per wave pair and round at most
+constexpr int kMxChunk = 4;      // blocks per x chunk
 
 struct Mx4Args {
   const uint16_t* x;             // x[m][k]
@@ -55,12 +56,14 @@ __device__ __forceinline__ void mx_wait_le() {
   __builtin_amdgcn_s_waitcnt((M & 15) | ((M >> 4) << 14) | 0x70 | 0xF00);
 }
 
-// NT: 16-row activation tiles; TP: weight tiles per wave; S: blocks per x chunk (a wave takes S / 2 of
-// them); D: blocks in flight per wave and tile.
-template <int NT, int TP, int S, int D>
+// TP: weight tiles per wave.
+template <int TP>
 __global__ __launch_bounds__(64 * kMxWaves) __attribute__((amdgpu_waves_per_eu(2)))
 void k_mx4_gemm(Mx4Args a) {
   constexpr int W = kMxWaves;
+  constexpr int NT = 4;                            // 16-row activation tiles
+  constexpr int S = kMxChunk;                      // blocks per x chunk: a wave takes S / 2 of them
+  constexpr int D = 2;                             // blocks in flight per wave and tile
   constexpr int F = 4 * NT * S;                    // 1 KiB x pieces per chunk
   constexpr int FW = F / W;
   static_assert(F % W == 0 && S % (2 * D) == 0, "whole rings and 256-column pieces per chunk");
@@ -250,7 +253,7 @@ void k_mx4_gemm(Mx4Args a) {
 #pragma unroll
         for (int g2 = 0; g2 < NT * TP; ++g2) {
           __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x2, NT == 1 ? 5 : NT == 2 ? 3 : 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -359,17 +362,7 @@ void k_mx4_gemm(Mx4Args a) {
 // launcher
 // ---------------------------------------------------------------------------------------------
 typedef void (*Mx4Kernel)(Mx4Args);
-// blocks per x chunk
-static int mx4_chunk(int nt) { return nt == 1 ? 16 : nt == 2 ? 8 : 4; }
-template <int NT, int S, int D>
-static Mx4Kernel mx4_pick(int tp) {
-  return tp == 1 ? k_mx4_gemm<NT, 1, S, D> : tp == 2 ? k_mx4_gemm<NT, 2, S, D> : k_mx4_gemm<NT, 3, S, D>;
-}
-static Mx4Kernel mx4_kernel(int nt, int tp) {
-  if (nt == 1) return mx4_pick<1, 16, 4>(tp);
-  if (nt == 2) return mx4_pick<2, 8, 4>(tp);
-  return mx4_pick<4, 4, 2>(tp);
-}
+static Mx4Kernel mx4_pick(int tp) { return tp == 1 ? k_mx4_gemm<1> : tp == 2 ? k_mx4_gemm<2> : k_mx4_gemm<3>; }
 
 hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_t n, int64_t k, YOut y,
                            hipStream_t s, const Scratch& sc) {
@@ -377,10 +370,10 @@ hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_
   hipError_t err = dev_info(&di);
   if (err != hipSuccess) return err;
   const int64_t tiles = (n + kTileRows - 1) / kTileRows, kb = k / kTileCols;
+  const int64_t chunks = (kb + kMxChunk - 1) / kMxChunk;
   for (int64_t m0 = 0; m0 < m; m0 += 64) {
     const int mb = (int)(m - m0 < 64 ? m - m0 : 64);
-    const int nt = (mb + 15) / 16, cb = mx4_chunk(nt);
-    const int64_t chunks = (kb + cb - 1) / cb;
+    if (mb <= 32) return launch_mfma(kFmtMX4, x + m0 * k, mb, p, n, k, y + m0 * n, s, sc);
     const int64_t slots = di.cus;
     // k ranges: as many as give every wave pair of the chip a tile, of at least one chunk
     int64_t ranges = slots * (kMxWaves / 2) / tiles;
@@ -417,7 +410,8 @@ hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_
     a.ysplit = (int64_t)mb * n;
     a.yvec = a.y16 ? (reinterpret_cast<uintptr_t>(a.y16) & 7u) == 0 && n % 4 == 0
                    : (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0 && n % 4 == 0;
-    hipLaunchKernelGGL(mx4_kernel(nt, (a.tpr + kMxWaves / 2 - 1) / (kMxWaves / 2)), dim3((unsigned)(groups * ranges)), dim3(64 * kMxWaves), 0, s, a);
+    hipLaunchKernelGGL(mx4_pick((a.tpr + kMxWaves / 2 - 1) / (kMxWaves / 2)), dim3((unsigned)(groups * ranges)),
+                       dim3(64 * kMxWaves), 0, s, a);
     err = hipGetLastError();
     if (err != hipSuccess) return err;
     if (ws) {
