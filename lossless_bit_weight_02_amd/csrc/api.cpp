@@ -101,12 +101,12 @@ w12::Planes planes_of(const w12_weight* wt) {
 // kernel wins on 1.5 to 2.5 tiles per CU (128 rows: [6144, 5120] 73.1 vs 85.3, [8192, 5120] 74.7
 // vs 85.2; [12288, 5120] ties, 87.1 vs 86.4), the dense baseline's up to 3 ([5120, 17408] 121.2
 // vs 140.9, [5120, 6144] 55.6 vs 73.9, [8192, 5120] 54.7 vs 69.3, [12288, 5120] 68.6 vs 70.8).
-// The 4-bit copy takes it only at 13..16 rows above 24 tiles per CU ([152064, 5120], 16 rows, vs the
-// matrix cores: 90.2 vs 93.8; 8 rows 91.6 vs 86.3; [34816, 5120], 16 rows: 27.1 vs 22.4): on fewer
-// tiles its cost per workgroup outweighs the halved bytes, at other widths the matrix cores win.
+// The 4-bit copy never takes it: with half of the bytes its cost per workgroup outweighs the rest
+// (streaming vs the matrix cores, 16 rows: [34816, 5120] 27.1 vs 22.4, [152064, 5120] 90.2 vs 87.3,
+// [8192, 5120] 14.4 vs 13.0, [5120, 17408] 28.5 vs 17.1; 4 rows: 28.1 vs 21.5, 92.3 vs 81.1).
 bool stream_auto_pick(w12::Fmt f, int64_t m, int64_t tiles, int64_t k, int64_t cus) {
   const bool dense = f == w12::kFmtBF16;
-  if (f == w12::kFmtMX4) return tiles > 24 * cus && m >= 13 && m <= 16 && k <= 8192;
+  if (f == w12::kFmtMX4) return false;
   if (m <= 32)
     return k <= 8192 && (!dense || tiles <= 6 * cus) &&
            ((m >= 3 && m <= 16 && 2 * tiles >= 3 * cus) ||

@@ -749,7 +749,7 @@ static hipError_t mfma_pass(Fmt f, const DevInfo& di, const uint16_t* x, int mb,
 }
 
 // First row of the tail launch (0: none) -- see launch_mfma.
-static int64_t tail_split_row(const DevInfo& di, int mb, int64_t tiles) {
+int64_t mfma_tail_row(const DevInfo& di, int mb, int64_t tiles) {
   const int64_t per_round = (int64_t)di.cus * kWaves;
   const int64_t full = tiles / per_round, tail = tiles - full * per_round;
   return mb <= 32 && full >= 1 && tail > 0 && 2 * tail <= per_round ? full * per_round * kTileRows : 0;
@@ -780,7 +780,7 @@ hipError_t launch_mfma(Fmt f, const uint16_t* x, int64_t m, const Planes& p, int
     // last round would keep at most half of the waves busy (the LM head: 9504 tiles = 3 rounds
     // of 3072 and 288), the full rounds run as one launch and the remaining tiles as a second,
     // split-k launch over the same record's last rows, so they take a fraction of a round.
-    const int64_t r0 = tail_split_row(di, mb, tiles);
+    const int64_t r0 = mfma_tail_row(di, mb, tiles);
     if (r0 > 0) {
       err = mfma_pass(f, di, x + m0 * k, mb, p, r0, k, y + m0 * n, n, s, sc);
       if (err != hipSuccess) return err;
@@ -815,7 +815,7 @@ hipError_t launch_mfma_top1(Fmt f, const uint16_t* x, int64_t m, const Planes& p
     const int nt = (mb + 15) / 16;
     // the same launches as the full outputs: the full rounds in top-1 mode, the tail rows (if
     // any) through the split path into the workspace and then scanned for their best key
-    const int64_t r0 = tail_split_row(di, mb, tiles);
+    const int64_t r0 = mfma_tail_row(di, mb, tiles);
     const int64_t nh = r0 > 0 ? r0 : n;
     const int64_t th = (nh + kTileRows - 1) / kTileRows;
     const int64_t groups = th < di.cus ? th : di.cus;

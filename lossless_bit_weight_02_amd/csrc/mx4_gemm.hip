@@ -1,19 +1,27 @@
-// Skinny GEMM on the microscaled 4-bit copy (mx4.hip) for 3..64 rows of x on the matrix cores:
+// Skinny GEMM on the microscaled 4-bit copy (mx4.hip) on the matrix cores, several weight tiles per wave:
 // y[m][n] = 2^(base_n - 112) sum_k x[m][k] w'[n][k] + sum over the escapes that are not zero of x v.
 //
 // A block of 16 weight rows x 128 columns is 1088 bytes, half of the 8-bit view's, and decodes in 16
 // instructions (a scaled conversion yields two bfloat16), so what bounds the other formats' kernels
-// here is no longer the weight stream but what a wave does per block: its loop, and above 16 rows
-// of x the LDS reads of x (16 KiB per block at 64 rows).  So a wave takes TP tiles at a time: each x
-// fragment it reads from LDS multiplies TP decoded blocks, and the loop's instructions are spread
-// over them.
+// here is no longer the weight stream but what a wave does per block: its loop, the reads of x from
+// LDS (16 KiB per block at 64 rows) and, with many tiles, every workgroup's passes over x in L2.  So
+// a wave takes TP tiles at a time: each x fragment it reads from LDS multiplies TP decoded blocks,
+// and the loop's instructions, a round's start and its reads of x are spread over them.
+//
+// Measured (us; weights alone at the rate of a large read, 6.4 TB/s, in parentheses): 64 rows,
+// [34816, 5120] 39.2 (16.3; k_mfma_wide's loop 54.2), [152064, 5120] 139 to 152 (71), [5120, 17408]
+// 31.4 (8.0), [5120, 5120] 18.0 (2.5); 16 rows, [152064, 5120] 87.3 (66.4; one tile per wave 93.5); 32
+// rows 96.3 (67.9; 109.5).  At 64 rows the weights, the matrix cores (the fullest SIMD's) and the LDS
+// reads take about 15 us each of the 39, the start and the end of the kernel 7: what is missing is
+// their overlap in two waves per SIMD.
 //
 // Work split.  One workgroup of 8 waves per CU, in two halves: four waves take the even and four the odd
 // blocks of the same tiles (two waves a SIMD, so one multiplies while the other decodes, yet only
 // four read each block of x), and their sums meet in LDS at the end.  The tiles are dealt
 // round-robin over the workgroups and a workgroup's over its four wave pairs, TP each and round at
 // most, as evenly as that allows.  Shapes with few tiles split k into ranges of whole chunks, whose
-// partial sums a second kernel adds in range order.
+// partial sums a second kernel adds in range order.  Two blocks of each tile are in flight per wave:
+// with four, [152064, 5120] at 16 rows took 97.7 us instead of 88.4.
 //
 // x: chunks of S blocks (128 S columns) of all rows in LDS, double buffered, loaded straight from
 // memory (global-to-LDS) while the chunk before is multiplied, rows rotated against bank conflicts as
@@ -27,8 +35,6 @@
 namespace w12 {
 
 constexpr int kMxWaves = 8;
-constexpr int kMxTiles = 3;      // tiles per wave pair and round at most
-constexpr int kMxChunk = 4;      // blocks per x chunk
 
 struct Mx4Args {
   const uint16_t* x;             // x[m][k]
@@ -56,13 +62,11 @@ __device__ __forceinline__ void mx_wait_le() {
   __builtin_amdgcn_s_waitcnt((M & 15) | ((M >> 4) << 14) | 0x70 | 0xF00);
 }
 
-// TP: weight tiles per wave.
-template <int TP>
+// NT: 16-row activation tiles; TP: weight tiles per wave; S: blocks per x chunk, of which a wave takes S / 2.
+template <int NT, int TP, int S>
 __global__ __launch_bounds__(64 * kMxWaves) __attribute__((amdgpu_waves_per_eu(2)))
 void k_mx4_gemm(Mx4Args a) {
   constexpr int W = kMxWaves;
-  constexpr int NT = 4;                            // 16-row activation tiles
-  constexpr int S = kMxChunk;                      // blocks per x chunk: a wave takes S / 2 of them
   constexpr int D = 2;                             // blocks in flight per wave and tile
   constexpr int F = 4 * NT * S;                    // 1 KiB x pieces per chunk
   constexpr int FW = F / W;
@@ -253,7 +257,7 @@ void k_mx4_gemm(Mx4Args a) {
 #pragma unroll
         for (int g2 = 0; g2 < NT * TP; ++g2) {
           __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x2, NT == 1 ? 5 : NT == 2 ? 3 : 2, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -362,7 +366,17 @@ void k_mx4_gemm(Mx4Args a) {
 // launcher
 // ---------------------------------------------------------------------------------------------
 typedef void (*Mx4Kernel)(Mx4Args);
-static Mx4Kernel mx4_pick(int tp) { return tp == 1 ? k_mx4_gemm<1> : tp == 2 ? k_mx4_gemm<2> : k_mx4_gemm<3>; }
+struct Mx4Shape {
+  int tiles, chunk;              // tiles per wave and round at most, blocks per x chunk
+};
+static Mx4Shape mx4_shape(int nt) { return nt <= 2 ? Mx4Shape{5, 8} : Mx4Shape{3, 4}; }
+// tp: tiles per wave.  Passes of at most 32 rows come here with at least 13 tiles per workgroup and
+// round (launch_mx4_gemm), so with four or five per wave.
+static Mx4Kernel mx4_pick(int nt, int tp) {
+  if (nt == 1) return tp <= 4 ? k_mx4_gemm<1, 4, 8> : k_mx4_gemm<1, 5, 8>;
+  if (nt == 2) return tp <= 4 ? k_mx4_gemm<2, 4, 8> : k_mx4_gemm<2, 5, 8>;
+  return tp == 1 ? k_mx4_gemm<4, 1, 4> : tp == 2 ? k_mx4_gemm<4, 2, 4> : k_mx4_gemm<4, 3, 4>;
+}
 
 hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_t n, int64_t k, YOut y,
                            hipStream_t s, const Scratch& sc) {
@@ -370,10 +384,17 @@ hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_
   hipError_t err = dev_info(&di);
   if (err != hipSuccess) return err;
   const int64_t tiles = (n + kTileRows - 1) / kTileRows, kb = k / kTileCols;
-  const int64_t chunks = (kb + kMxChunk - 1) / kMxChunk;
   for (int64_t m0 = 0; m0 < m; m0 += 64) {
     const int mb = (int)(m - m0 < 64 ? m - m0 : 64);
-    if (mb <= 32) return launch_mfma(kFmtMX4, x + m0 * k, mb, p, n, k, y + m0 * n, s, sc);
+    // At most 32 rows: k_mfma (mfma.hip), which deals one tile per wave and round, unless its last round
+    // would be so empty that it runs as a launch of its own ([152064, 5120], 16 and 32 rows: 93.5 and
+    // 109.5 us there, 87.3 and 96.3 here; [65536, 5120] 51.4 and 63.9, 38.4 and 45.0; with full rounds,
+    // [49152, 5120], 29.2 and 35.0 there, 31.0 and 36.4 here, [98304, 5120] 55.6 and 65.6, 62.0 and 74.1).
+    if (mb <= 32 && mfma_tail_row(di, mb, tiles) == 0)
+      return launch_mfma(kFmtMX4, x + m0 * k, mb, p, n, k, y + m0 * n, s, sc);
+    const int nt = (mb + 15) / 16;
+    const Mx4Shape sh = mx4_shape(nt);
+    const int64_t chunks = (kb + sh.chunk - 1) / sh.chunk;
     const int64_t slots = di.cus;
     // k ranges: as many as give every wave pair of the chip a tile, of at least one chunk
     int64_t ranges = slots * (kMxWaves / 2) / tiles;
@@ -392,7 +413,7 @@ hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_
     if (groups > tiles) groups = tiles;
     if (groups < 1) groups = 1;
     const int64_t most = (tiles + groups - 1) / groups;             // tiles of the busiest workgroup
-    const int64_t rounds = (most + kMxWaves / 2 * kMxTiles - 1) / (kMxWaves / 2 * kMxTiles);
+    const int64_t rounds = (most + kMxWaves / 2 * sh.tiles - 1) / (kMxWaves / 2 * sh.tiles);
     const YOut yp = y + m0 * n;
     Mx4Args a;
     a.x = x + m0 * k;
@@ -410,7 +431,7 @@ hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_
     a.ysplit = (int64_t)mb * n;
     a.yvec = a.y16 ? (reinterpret_cast<uintptr_t>(a.y16) & 7u) == 0 && n % 4 == 0
                    : (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0 && n % 4 == 0;
-    hipLaunchKernelGGL(mx4_pick((a.tpr + kMxWaves / 2 - 1) / (kMxWaves / 2)), dim3((unsigned)(groups * ranges)),
+    hipLaunchKernelGGL(mx4_pick(nt, (a.tpr + kMxWaves / 2 - 1) / (kMxWaves / 2)), dim3((unsigned)(groups * ranges)),
                        dim3(64 * kMxWaves), 0, s, a);
     err = hipGetLastError();
     if (err != hipSuccess) return err;

@@ -186,8 +186,10 @@ hipError_t launch_stream_top1(Fmt f, const uint16_t* x, int64_t m, const Planes&
 // MFMA family (bf16 v_mfma_f32_16x16x32), any m (blocks of <= 64 rows of x)
 hipError_t launch_mfma(Fmt f, const uint16_t* x, int64_t m, const Planes& p, int64_t n, int64_t k,
                        YOut y, hipStream_t s, const Scratch& sc);
-// The 4-bit copy's matrix-core family, any m: passes of 33..64 rows (up to three tiles per wave), a
-// shorter one on launch_mfma; no
+// first weight row of the tail launch that launch_mfma runs for a pass of mb rows over `tiles` tiles (0: none)
+int64_t mfma_tail_row(const DevInfo& di, int mb, int64_t tiles);
+// The 4-bit copy's matrix-core family, any m: passes of up to 64 rows with several tiles per wave, those
+// of at most 32 rows without a tail launch on launch_mfma; no
 // SiLU pairing
 hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_t n, int64_t k, YOut y,
                            hipStream_t s, const Scratch& sc);

@@ -105,6 +105,32 @@ def test_mx4_shapes(n, k, ms):
             assert torch.equal(y, y2), "not repeatable"
 
 
+@pytest.mark.parametrize("n,k,p_out", [
+    (49300, 256, 5e-4),      # 3082 tiles: 13 a workgroup, in one round
+    (73000, 128, 0.05),      # 4563 tiles: 18 a workgroup; more than 64 escapes in many tiles
+    (152064, 128, 5e-4),     # 9504 tiles: two rounds
+])
+def test_mx4_many_tiles(n, k, p_out):
+    w12 = _w12()
+    rng = np.random.default_rng(n)
+    w = synth.f32_to_bf16_bits((rng.standard_normal((n, k)) * 0.02).astype(np.float32))
+    w[rng.random((n, k)) < p_out] = 0x4400
+    rec = w12.encode(to_dev(w))
+    cp = w12.mx4_build(rec)
+    ref = oracle.encode(w)
+    w64 = oracle.mx4_weights64(ref, oracle.mx4_copy(ref))
+    x_bits = synth.gen_x(96, k, tensor_id=n)
+    y64, absum = oracle.gemm64_f(x_bits, w64), oracle.abs_bound64_f(x_bits, w64)
+    x = to_dev(x_bits)
+    for m in (1, 2, 3, 16, 17, 32, 33, 64, 70, 96):
+        say(f"mx4 gemm {n}x{k} m={m}")
+        y = w12.mx4_gemm(x[:m], cp)
+        check_y(y.cpu().numpy(), y64[:m], absum[:m], f"mx4 {n}x{k} m={m}")
+        assert torch.equal(y, w12.mx4_gemm(x[:m], cp)), "not repeatable"
+    y16 = w12.mx4_gemm(x[:20], cp, out_bf16=True)
+    check_y_bf16(y16, w12.mx4_gemm(x[:20], cp).cpu().numpy(), y64[:20], absum[:20], f"mx4 bf16 out {n}x{k}")
+
+
 def test_mx4_edge_rows():
     """Windows at both ends of the exponent range, all-zero rows, blocks of escapes alone, Inf and NaN
     escapes, a constant row, every rounding of every code."""
