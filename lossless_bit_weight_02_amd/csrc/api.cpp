@@ -63,6 +63,13 @@ int check_record(const w12_weight* wt, bool need_lo) {
   return W12_OK;
 }
 
+// For kernels that step through an escape list 64 places at a time with 32-bit places.
+int check_escape_places(const w12_weight* wt) {
+  if (wt->esc_cap > 0xFFFFFF00ull)
+    return fail(W12_ERR_RANGE, "esc_cap %llu is too large (at most 2^32 - 256)", (unsigned long long)wt->esc_cap);
+  return W12_OK;
+}
+
 w12::Planes planes_of(const w12_weight* wt) {
   w12::Planes p;
   p.base = wt->base;
@@ -613,6 +620,8 @@ int w12_mx4_build(const w12_weight* wt, w12_mx4* out, void* stream) {
                 (long long)out->k, (long long)wt->n, (long long)wt->k);
   rc = check_mx4_arrays(out);
   if (rc) return rc;
+  rc = check_escape_places(wt);
+  if (rc) return rc;
   if (out->nz_cap < wt->esc_cap)
     return fail(W12_ERR_CAPACITY, "nz_cap %llu < the record's esc_cap %llu", (unsigned long long)out->nz_cap,
                 (unsigned long long)wt->esc_cap);
@@ -661,6 +670,8 @@ int w12_mx4_top1(const uint16_t* x, int64_t m, const w12_mx4* cp, const w12_weig
 int w12_embed(const void* ids, int64_t count, const w12_weight* wt, float scale, void* out, uint32_t flags,
               void* stream) {
   int rc = check_record(wt, true);
+  if (rc) return rc;
+  rc = check_escape_places(wt);
   if (rc) return rc;
   if (!ids || !out) return fail(W12_ERR_ARG, "ids or out is NULL");
   if (flags & ~(W12_OUT_BF16 | W12_IDS_I64)) return fail(W12_ERR_ARG, "unknown flags 0x%x", flags);

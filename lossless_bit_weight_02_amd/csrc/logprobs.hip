@@ -865,12 +865,30 @@ hipError_t launch_logprobs(const void* y, bool bf, int64_t m, int64_t n, int64_t
   a.count = static_cast<uint32_t*>(scratch);
   a.parts = reinterpret_cast<LpPart*>(static_cast<uint8_t*>(scratch) + lp_counts(di));
   a.keys = reinterpret_cast<uint64_t*>(a.parts + m * a.splits);
-  const dim3 grid((unsigned)(m * a.splits)), block(64 * kLpWaves);
-  if (p.regs && bf) hipLaunchKernelGGL(k_logprobs_part<true>, grid, block, 0, s, a);
-  else if (p.regs) hipLaunchKernelGGL(k_logprobs_part<false>, grid, block, 0, s, a);
-  else if (bf) hipLaunchKernelGGL(k_logprobs<true>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(k_logprobs<false>, grid, block, 0, s, a);
-  return hipGetLastError();
+  // a launch holds fewer than 2^32 work items: more rows (whole ones, then) in several
+  constexpr int64_t kRows = int64_t(1) << 23;
+  static_assert(kRows * 64 * kLpWaves < (int64_t(1) << 32), "work items of a launch");
+  for (int64_t r0 = 0; r0 < m; r0 += kRows) {
+    a.m = m - r0 < kRows ? m - r0 : kRows;
+    const dim3 grid((unsigned)(a.m * a.splits)), block(64 * kLpWaves);
+    if (p.regs && bf) hipLaunchKernelGGL(k_logprobs_part<true>, grid, block, 0, s, a);
+    else if (p.regs) hipLaunchKernelGGL(k_logprobs_part<false>, grid, block, 0, s, a);
+    else if (bf) hipLaunchKernelGGL(k_logprobs<true>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(k_logprobs<false>, grid, block, 0, s, a);
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    a.y = static_cast<const uint8_t*>(a.y) + kRows * ldy * (bf ? 2 : 4);
+    if (nt > 0) {
+      a.tokens = static_cast<const uint8_t*>(a.tokens) + kRows * nt * (tok64 ? 8 : 4);
+      a.logp += kRows * nt;
+    }
+    a.ent += kRows;
+    if (top > 0) {
+      a.tidx += kRows * top;
+      a.tlogp += kRows * top;
+    }
+  }
+  return hipSuccess;
 }
 
 }  // namespace w12

@@ -545,7 +545,8 @@ def mx4_build(rec: W12Weight) -> Mx4Copy:
                  torch.empty(rec.n + 1, dtype=i32, device=dev), torch.empty(rec.n, dtype=i32, device=dev),
                  torch.empty(cap, dtype=i32, device=dev), torch.empty(cap, dtype=torch.int16, device=dev))
     s, c = rec.c_struct(), cp.c_struct()
-    _check(lib().w12_mx4_build(ctypes.byref(s), ctypes.byref(c), _stream_handle(dev)))
+    with _on_device(dev):
+        _check(lib().w12_mx4_build(ctypes.byref(s), ctypes.byref(c), _stream_handle(dev)))
     return cp
 
 
@@ -556,7 +557,8 @@ def mx4_decode(cp: Mx4Copy, out: torch.Tensor | None = None) -> torch.Tensor:
     else:
         _check_out(out, (cp.n, cp.k), (torch.bfloat16,), cp.device)
     c, s = cp.c_struct(), cp.rec.c_struct()
-    _check(lib().w12_mx4_decode(ctypes.byref(c), ctypes.byref(s), out.data_ptr(), _stream_handle(cp.device)))
+    with _on_device(cp.device):
+        _check(lib().w12_mx4_decode(ctypes.byref(c), ctypes.byref(s), out.data_ptr(), _stream_handle(cp.device)))
     return out
 
 
@@ -567,16 +569,18 @@ def mx4_gemm(x: torch.Tensor, cp: Mx4Copy, path: str | None = None, out: torch.T
     if x.shape[0] == 0:
         return out
     c, s = cp.c_struct(), cp.rec.c_struct()
-    _check(lib().w12_mx4_gemm(x.data_ptr(), x.shape[0], ctypes.byref(c), ctypes.byref(s), out.data_ptr(),
-                              _PATHS[path] | _out_flag(out), _stream_handle(x.device)))
+    with _on_device(x.device):
+        _check(lib().w12_mx4_gemm(x.data_ptr(), x.shape[0], ctypes.byref(c), ctypes.byref(s), out.data_ptr(),
+                                  _PATHS[path] | _out_flag(out), _stream_handle(x.device)))
     return out
 
 
 def mx4_top1(x: torch.Tensor, cp: Mx4Copy, out=None):
     """Top-1 of the Q pass on the 4-bit copy per row of x: (index int32 [m], value float32 [m])."""
     c = cp.c_struct()
-    return _top1(lambda xp, m, s, ip, vp, fl, st: lib().w12_mx4_top1(xp, m, ctypes.byref(c), s, ip, vp, fl, st),
-                 x, cp.rec, False, out)
+    with _on_device(cp.device):
+        return _top1(lambda xp, m, s, ip, vp, fl, st: lib().w12_mx4_top1(xp, m, ctypes.byref(c), s, ip, vp, fl, st),
+                     x, cp.rec, False, out)
 
 
 def _ids_flag(ids: torch.Tensor, device, what: str):

@@ -267,3 +267,90 @@ def test_logprobs_repeat_graph_and_streams():
         torch.cuda.synchronize()
         assert all(torch.equal(u, v) for u, v in zip(rg, want))
         assert all(torch.equal(u, v) for u, v in zip(eager, q0))
+
+
+def test_logprobs_far_rows():
+    """Rows more than 4 GiB apart on both kernels: the second of two, and the last ones of a tall matrix."""
+    w12 = _w12()
+    y, tok = _logits(2, 5000, 21, torch.float32)
+    stride = (1 << 30) + 8
+    buf = torch.empty(stride + 5000, device="cuda:0")
+    far = buf.as_strided((2, 5000), (stride, 1))
+    far.copy_(y)
+    say("logprobs rows 4 GiB apart")
+    _compare_lp(w12.logprobs(far, tok.cuda(), top=7), y, tok, 7, "far rows")
+    del buf, far
+    m, n = 70000, 32768                                # 4.6 GB of bfloat16
+    y, tok = _logits(3, n, 22, torch.bfloat16)
+    tall = torch.zeros((m, n), dtype=torch.bfloat16, device="cuda:0")
+    at = torch.tensor([0, 65540, m - 1], device="cuda:0")
+    tall[at] = y.cuda()
+    t = torch.zeros((m, tok.shape[1]), dtype=torch.int64, device="cuda:0")
+    t[at] = tok.cuda()
+    say("logprobs tall matrix")
+    r = w12.logprobs(tall, t, top=4)
+    _compare_lp(type(r)(*(f[at] for f in r)), y, tok, 4, "tall matrix")
+    assert (r.entropy[1000:2000] - math.log(n)).abs().max() < 1e-5 * math.log(n)
+
+
+def test_logprobs_more_rows_than_a_launch():
+    """2^23 + 5 rows: each result within the roundings of a three-term sum (8 of 2^-24) of the formula in
+    float64."""
+    w12 = _w12()
+    m = (1 << 23) + 5
+    say("logprobs 2^23 + 5 rows")
+    y = torch.randn((m, 3), generator=torch.Generator("cuda").manual_seed(5), device="cuda").to(torch.bfloat16)
+    tok = torch.arange(m, device="cuda") % 3
+    r = w12.logprobs(y, tok, top=1)
+    ls = torch.log_softmax(y.double(), dim=1)
+    want = ls.gather(1, tok[:, None])[:, 0]
+    assert ((r.logp - want).abs() <= 2.0 ** -21 * (1 + want.abs())).all()
+    ent = -(ls.exp() * ls).sum(1)
+    assert ((r.entropy - ent).abs() <= 2.0 ** -21 * (1 + ent)).all()
+    best = y.float().max(dim=1).values
+    assert torch.equal(y.float().gather(1, r.top_index.long())[:, 0], best)
+
+
+def test_embed_and_copy_past_32_bits():
+    """A table of 560005 x 16384: planes, copy and outputs past 4 GiB.  Far rows equal the same rows of a
+    small record; products within the documented bound."""
+    w12 = _w12()
+    n, k, cut = 560005, 16384, 69                      # the last 69 rows start a tile
+    g = torch.Generator("cuda").manual_seed(6)
+    say("embedding table of 18 GB")
+    part = (torch.randn((4000, k), generator=g, device="cuda") * 0.02).to(torch.bfloat16)
+    w = torch.empty((n, k), dtype=torch.bfloat16, device="cuda")
+    for r0 in range(0, n, 4000):
+        w[r0:r0 + 4000] = part[:min(4000, n - r0)]
+    w[n - cut:] = (torch.randn((cut, k), generator=g, device="cuda") * 0.3).to(torch.bfloat16)
+    w[n - 5, 100:300] = 0
+    rec = w12.encode(w)
+    ids = torch.tensor([0, n - 1, n - 5, 270000, n - 1, n, -1, (1 << 32) + 1], device="cuda")
+    got = w12.embed(ids, rec)
+    assert torch.equal(got[:5].view(torch.int16), w[ids[:5]].view(torch.int16))
+    assert not got[5:].view(torch.int16).any()
+    say("embedding, 4.6 GB out")
+    many = torch.randint(0, n, (140000,), generator=g, device="cuda")
+    got = w12.embed(many, rec)
+    assert torch.equal(got[-3000:].view(torch.int16), w[many[-3000:]].view(torch.int16))
+    del got
+    say("4-bit copy of 4.9 GB")
+    cp, small = w12.mx4_build(rec), w12.mx4_build(w12.encode(w[n - cut:].contiguous()))
+    tail = w12.mx4_decode(small)
+    dec = w12.mx4_decode(cp)
+    assert torch.equal(dec[n - cut:].view(torch.int16), tail.view(torch.int16))
+    assert torch.equal(dec[8000:8016].view(torch.int16), dec[:16].view(torch.int16))
+    first = oracle.bf16_to_f64(to_host_bits(dec[:16].contiguous()))
+    del dec
+    w64 = oracle.bf16_to_f64(to_host_bits(tail))
+    x_bits = synth.gen_x(40, k, tensor_id=3)
+    y64, absum = oracle.gemm64_f(x_bits, w64), oracle.abs_bound64_f(x_bits, w64)
+    f64, fsum = oracle.gemm64_f(x_bits, first), oracle.abs_bound64_f(x_bits, first)
+    x = to_dev(x_bits)
+    for m, path in ((1, "auto"), (3, "auto"), (4, "stream"), (16, "mfma"), (20, "auto"), (40, "auto")):
+        say(f"4-bit product m={m} {path}")
+        y = w12.mx4_gemm(x[:m], cp, path=path)
+        assert (np.abs(y[:, n - cut:].cpu().numpy().astype(np.float64) - y64[:m]) <= 1e-3 * absum[:m]).all()
+        for r0 in (0, 556000):                         # the same weight rows, 9 GB apart
+            got = y[:, r0:r0 + 16].cpu().numpy().astype(np.float64)
+            assert (np.abs(got - f64[:m]) <= 1e-3 * fsum[:m]).all()

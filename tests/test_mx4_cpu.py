@@ -31,6 +31,8 @@ def test_build_and_decode_refusals():
                       (dict(nz_ptr=0xB002), w12.W12_ERR_ALIGN), (dict(nz_val=0xE001), w12.W12_ERR_ALIGN),
                       (dict(nz_cap=9), w12.W12_ERR_CAPACITY)):
         assert L.w12_mx4_build(ctypes.byref(_rec()), ctypes.byref(_cp(**bad)), None) == want, bad
+    cap = (1 << 32) - 255
+    assert L.w12_mx4_build(ctypes.byref(_rec(esc_cap=cap)), ctypes.byref(_cp(nz_cap=cap)), None) == w12.W12_ERR_RANGE
     assert L.w12_mx4_decode(ctypes.byref(_cp()), ctypes.byref(_rec()), None, None) == w12.W12_ERR_ARG
     assert L.w12_mx4_decode(ctypes.byref(_cp()), ctypes.byref(_rec()), 0x1002, None) == w12.W12_ERR_ALIGN
     assert L.w12_mx4_decode(ctypes.byref(_cp(k=256)), ctypes.byref(_rec()), 0x1000, None) == w12.W12_ERR_ARG

@@ -31,6 +31,7 @@ def test_embed_refusals():
     assert _embed(count=1 << 31) == w12.W12_ERR_RANGE
     assert _embed(rec=_rec(lo=None)) == w12.W12_ERR_ARG
     assert _embed(rec=_rec(k=130)) == w12.W12_ERR_SHAPE
+    assert _embed(rec=_rec(esc_cap=(1 << 32) - 255)) == w12.W12_ERR_RANGE
     assert _embed(ids=0x1002) == w12.W12_ERR_ALIGN
     assert _embed(ids=0x1004, flags=w12.IDS_I64) == w12.W12_ERR_ALIGN
     assert _embed(out=0x2008) == w12.W12_ERR_ALIGN
