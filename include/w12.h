@@ -86,7 +86,8 @@ extern "C" {
                            * every shape), and above 64 rows on 1.5 to 2.5 (the dense baseline:
                            * at most 3); otherwise the GEMV
                            * with wave reductions for m <= 2, and for m <= 5 on shapes of at most
-                           * 1024 tiles and k <= 8192; bf16 MFMA otherwise */
+                           * 1024 tiles and k <= 8192; bf16 MFMA otherwise (w12_mx4_gemm: its own
+                           * choice, stated there) */
 #define W12_PATH_GEMV 1u  /* force the GEMV (m > 8 runs as several passes of <= 8 rows) */
 #define W12_PATH_MFMA 2u  /* force the MFMA kernel (any m; columns padded to 16; passes of 32
                            * rows above 32 on shapes of fewer than 1.5 tiles per unit) */
@@ -320,9 +321,11 @@ int w12_mx4_decode(const w12_mx4 *cp, const w12_weight *wt, uint16_t *w_out, voi
 
 /*
  * w12_mx4_gemm / w12_mx4_top1 -- the Q pass on the 4-bit copy and its top-1 per row of x, as
- * w12_i8_gemm and w12_i8_top1 (same x, outputs, flags, kernel families, workspace and error bound,
- * against the weights w12_mx4_decode gives).  Read the copy and wt->base (wt's other arrays may be
- * NULL).
+ * w12_i8_gemm and w12_i8_top1 (same x, outputs, flags, workspace and error bound, against the weights
+ * w12_mx4_decode gives).  Read the copy and wt->base (wt's other arrays may be NULL).  W12_PATH_AUTO
+ * here: the GEMV at one row of x, and at two for k <= 8192 and at most 6 tiles per compute unit;
+ * the matrix cores otherwise, in passes of up to 64 rows.  The top-1 takes y from the kernel of 32
+ * rows a pass, so where w12_mx4_gemm runs another one their values differ in the last bits.
  */
 int w12_mx4_gemm(const uint16_t *x, int64_t m, const w12_mx4 *cp, const w12_weight *wt, float *y,
                  uint32_t flags, void *stream);

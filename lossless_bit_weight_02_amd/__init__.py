@@ -2,7 +2,8 @@
 
 Submodules:
   w12    -- ctypes binding of libw12.so over torch device tensors (encode, decode, gemm, q8_gemm,
-            bf16_gemm, read_probe)
+            bf16_gemm, read_probe; the 4-bit Q-pass copy mx4_build, mx4_decode, mx4_gemm, mx4_top1;
+            the vocabulary ends of a step: embed, logprobs)
   synth  -- seeded synthetic inputs (no W12 arithmetic)
   build  -- hipcc build of libw12.so for gfx950
 """

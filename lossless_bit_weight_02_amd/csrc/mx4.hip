@@ -71,7 +71,10 @@ __device__ __forceinline__ void nonzero_escapes(const Planes& p, int64_t tr, int
 // block without weights), and converts.  Rows past n get zeros.  The placeholder's code is 0
 // already, as an escaped slot's has to be, unless the block's own exponent is within 3 of the window
 // bottom (2^-2 of the scale ties to 0): only such a block looks its escapes up.
-// The last list_blocks workgroups write the list of escapes that are not zero, a wave per tile row.
+// The last list_blocks workgroups write the list of escapes that are not zero, a wave per tile row
+// (as a launch of its own, and one more for the escaped slots, [5120, 5120] built and read back in
+// 33 us instead of 27).  Bound by memory, 1.5 bytes read and 17/32 written per weight:
+// [5120, 5120] 11.6 us (4.6 TB/s), [34816, 5120] 58 us (6.2 TB/s).
 __global__ __launch_bounds__(kBlock) void k_mx4_build(Planes p, int64_t n, int64_t k, uint8_t* __restrict__ q,
                                                       uint32_t* __restrict__ nz_ptr, uint32_t* __restrict__ nz_end,
                                                       uint32_t* __restrict__ nz_col, uint16_t* __restrict__ nz_val,
@@ -129,12 +132,14 @@ __global__ __launch_bounds__(kBlock) void k_mx4_build(Planes p, int64_t n, int64
   }
 }
 
-// The bfloat16 matrix the Q pass multiplies.  One wave per tile; w' times 2^(base - 112) is exact in bfloat16 (at the lowest windows as a
-// subnormal), so the high half of the float product is the value.  A lane's 32 columns are 64 bytes
-// of its row, but stored as they lie each store would touch 16 bytes of 64 pieces; so the tile turns
-// in LDS and leaves as whole 256-byte row pieces (16 lanes each, rotated by the row against bank
-// conflicts): gate+up [34816, 5120] 136.1 -> 85.2 us.  The escapes go over their slots there: each
-// lane finds those of its own block in its row's list.
+// The bfloat16 matrix the Q pass multiplies.  One wave per tile; w' times 2^(base - 112) is exact in
+// bfloat16 (at the lowest windows as a subnormal), so the high half of the float product is the
+// value.  A lane's 32 columns are 64 bytes of its row, but stored as they lie each store would touch
+// 16 bytes of 64 pieces; so the tile turns in LDS and leaves as whole 256-byte row pieces (16 lanes
+// each, rotated by the row against bank conflicts): gate+up [34816, 5120] 136.1 -> 86 us.  The
+// escapes go over their slots there: each lane finds those of its own block in its row's list.
+// Bound by memory, 17/32 bytes read and 2 written per weight: those 86 us are 5.2 TB/s, [5120,
+// 5120] takes 15.2 us (4.4 TB/s).
 __global__ __launch_bounds__(kBlock) void k_mx4_decode(Planes pl, int64_t n, int64_t k, uint16_t* __restrict__ out) {
   __shared__ __attribute__((aligned(16))) u32x4 s_t[kBlock / 64][256];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
