@@ -32,7 +32,7 @@
 //
 // Measured (152064 float logits a row unless said): 1024 rows 111.6 us (5.6 TB/s; bfloat16 63.0, 4.9
 // TB/s), with 8 alternatives 119.7 (89.7): bound by memory, and in bfloat16 by the instructions per
-// logit.  64 rows 15.3 us, with 16 alternatives 24.6: six of the 15 are the read at 6.4 TB/s, the rest
+// logit.  64 rows 14.9 us, with 16 alternatives 24.3: six of the 15 are the read at 6.4 TB/s, the rest
 // is what one part waits for in turn -- its logits, the maximum, the bound, the candidates, the last
 // part's join (7.1 us at one row, 11.9 with 8 alternatives) -- little of which other parts fill.
 #include "w12_device.hpp"
@@ -674,9 +674,12 @@ void k_logprobs(LpArgs a) {
   lp_end<BF>(a, row, sp, M, s, T, top, tok, lane);
 }
 
-// A part of at most kLpWaves kLpBatch logits, held in the workgroup's registers.
+// A part of at most kLpWaves kLpBatch logits, held in the workgroup's registers.  (Six waves per SIMD, 80
+// registers: 64 rows of 152064, 8 alternatives, 22.6 us; as the compiler leaves it, 83 and five,
+// 23.3; held to 64 registers, 23.4.)
 template <bool BF>
-__global__ __launch_bounds__(64 * kLpWaves) void k_logprobs_part(LpArgs a) {
+__global__ __launch_bounds__(64 * kLpWaves) __attribute__((amdgpu_waves_per_eu(6)))
+void k_logprobs_part(LpArgs a) {
   constexpr int E = kLpElems;
   __shared__ uint64_t s_list[kLpWaves][kLpCap];    // each wave's list, where the shared one overflows
   __shared__ uint64_t s_best[kLpCap];
