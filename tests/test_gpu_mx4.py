@@ -131,6 +131,38 @@ def test_mx4_many_tiles(n, k, p_out):
     check_y_bf16(y16, w12.mx4_gemm(x[:20], cp).cpu().numpy(), y64[:20], absum[:20], f"mx4 bf16 out {n}x{k}")
 
 
+@pytest.mark.parametrize("n,k", [
+    (17603, 640),        # 1101 tiles: five a workgroup; a short last chunk of x
+    (20500, 384),        # 1282 tiles: six
+    (34000, 256),        # 2125 tiles: nine
+    (38395, 128),        # 2400 tiles: ten; one block per row
+    (38395, 1152),       # ten; an odd number of chunks
+    (5456, 1664),        # 341 tiles: three k ranges, five tiles
+    (68032, 256),        # 4252 tiles: two rounds of nine
+])
+def test_mx4_uneven_tiles(n, k):
+    w12 = _w12()
+    w = _weights(n, k, n + k, p_out=0.01)
+    rec = w12.encode(to_dev(w))
+    cp = w12.mx4_build(rec)
+    ref = oracle.encode(w)
+    w64 = oracle.mx4_weights64(ref, oracle.mx4_copy(ref))
+    x_bits = synth.gen_x(100, k, tensor_id=n)
+    y64, absum = oracle.gemm64_f(x_bits, w64), oracle.abs_bound64_f(x_bits, w64)
+    x = to_dev(x_bits)
+    for m in (33, 48, 64, 100):
+        say(f"mx4 gemm {n}x{k} m={m}")
+        y = w12.mx4_gemm(x[:m], cp)
+        check_y(y.cpu().numpy(), y64[:m], absum[:m], f"mx4 {n}x{k} m={m}")
+        assert torch.equal(y, w12.mx4_gemm(x[:m], cp)), "not repeatable"
+    y16 = w12.mx4_gemm(x[:50], cp, out_bf16=True)
+    check_y_bf16(y16, w12.mx4_gemm(x[:50], cp).cpu().numpy(), y64[:50], absum[:50], f"mx4 bf16 out {n}x{k}")
+    one = np.zeros((40, k), dtype=np.uint16)           # one-hot rows: every weight of a column exactly
+    one[:, k - 1] = 0x3F80
+    y = w12.mx4_gemm(to_dev(one), cp).cpu().numpy()
+    assert np.array_equal(y[39].astype(np.float64), w64[:, k - 1])
+
+
 def test_mx4_edge_rows():
     """Windows at both ends of the exponent range, all-zero rows, blocks of escapes alone, Inf and NaN
     escapes, a constant row, every rounding of every code."""
