@@ -325,7 +325,8 @@ int w12_mx4_decode(const w12_mx4 *cp, const w12_weight *wt, uint16_t *w_out, voi
  * w12_mx4_decode gives).  Read the copy and wt->base (wt's other arrays may be NULL).  W12_PATH_AUTO
  * here: the GEMV at one row of x, and at two for k <= 8192 and at most 6 tiles per compute unit;
  * the matrix cores otherwise, in passes of up to 64 rows.  The top-1 takes y from the kernel of 32
- * rows a pass, so where w12_mx4_gemm runs another one their values differ in the last bits.
+ * rows a pass, so where w12_mx4_gemm runs another one their values differ in the last bits.  A row of
+ * x with an infinity or a NaN gives infinities or NaN (an escaped slot's code 0 meets it too).
  */
 int w12_mx4_gemm(const uint16_t *x, int64_t m, const w12_mx4 *cp, const w12_weight *wt, float *y,
                  uint32_t flags, void *stream);

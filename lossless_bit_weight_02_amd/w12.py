@@ -6,6 +6,7 @@ If the library is missing, loading fails loudly: there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -155,19 +156,12 @@ def _stream_handle(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-class _on_device:
+_HERE = contextlib.nullcontext()
+
+
+def _on_device(device):
     """Makes a tensor's device the current one for a call, at no cost where it already is."""
-
-    def __init__(self, device):
-        self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+    return _HERE if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
 
 
 def _ptr(t) -> int | None:
@@ -568,7 +562,7 @@ def mx4_gemm(x: torch.Tensor, cp: Mx4Copy, path: str | None = None, out: torch.T
     x, out = _gemm_io(x, cp.n, cp.k, cp.device, out, out_bf16)
     if x.shape[0] == 0:
         return out
-    c, s = cp.c_struct(), cp.rec.c_struct()
+    c, s = cp.c_struct(), _W12Weight(cp.n, cp.k, _ptr(cp.rec.base))   # (the record's other arrays are not read)
     with _on_device(x.device):
         _check(lib().w12_mx4_gemm(x.data_ptr(), x.shape[0], ctypes.byref(c), ctypes.byref(s), out.data_ptr(),
                                   _PATHS[path] | _out_flag(out), _stream_handle(x.device)))
@@ -598,19 +592,20 @@ def embed(ids: torch.Tensor, wt: W12Weight, scale: float = 1.0, out: torch.Tenso
     """Embedding lookup: scale * W[ids], W read from its W12 record.  ids: int32 or int64 of any shape
     on the weights' device; returns [*ids.shape, k] bfloat16 (scale 1: the weight's own bits), or
     float32 with ``out_f32`` / a float32 ``out``.  An id outside 0 .. n-1 gives a row of zeros."""
-    flag = _ids_flag(ids, wt.device, "ids")
+    dev = wt.device
+    flag = _ids_flag(ids, dev, "ids")
     shape = (*ids.shape, wt.k)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32 if out_f32 else torch.bfloat16, device=wt.device)
+        out = wt.ae.new_empty(shape, dtype=torch.float32 if out_f32 else torch.bfloat16)
     else:
-        _check_out(out, shape, (torch.float32, torch.bfloat16), wt.device)
+        _check_out(out, shape, (torch.float32, torch.bfloat16), dev)
     if ids.numel() == 0:
         return out
     ids = ids.contiguous()
     s = wt.c_struct()
-    with _on_device(wt.device):
+    with _on_device(dev):
         _check(lib().w12_embed(ids.data_ptr(), ids.numel(), ctypes.byref(s), float(scale), out.data_ptr(),
-                               flag | _out_flag(out), _stream_handle(wt.device)))
+                               flag | _out_flag(out), _stream_handle(dev)))
     return out
 
 
@@ -675,10 +670,8 @@ def logprobs(y: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0) 
         nt = 1 if tokens.dim() == 1 else tokens.shape[1]
         tokens = tokens.contiguous()
     f32 = torch.float32
-    r = LogProbs(torch.empty((m, 0) if tokens is None else tokens.shape, dtype=f32, device=y.device),
-                 torch.empty(m, dtype=f32, device=y.device),
-                 torch.empty((m, top), dtype=torch.int32, device=y.device),
-                 torch.empty((m, top), dtype=f32, device=y.device))
+    r = LogProbs(y.new_empty((m, 0) if tokens is None else tokens.shape, dtype=f32), y.new_empty(m, dtype=f32),
+                 y.new_empty((m, top), dtype=torch.int32), y.new_empty((m, top), dtype=f32))
     if m == 0:
         return r
     if n == 0:
