@@ -15,7 +15,7 @@
 //
 // What bounds it: the record's tile order, made for the GEMMs.  A row's bytes lie in it as 16-byte
 // pieces 256 bytes apart, each fetched as 64, so 4096 rows of 5120 columns read 128 MB (counted)
-// for their 31 MB, and write 42 MB: 52 us, 3.3 TB/s.  (The dense gather with its scaling, reading 42
+// for their 31 MB, and write 42 MB: 49 us, 3.5 TB/s.  (The dense gather with its scaling, reading 42
 // MB: 79.7 us as elementary operations.)  16 rows: 5 us, a launch's latency.
 #include "w12_device.hpp"
 #include "w12_launch.hpp"
@@ -31,9 +31,15 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// ids: int32 or (ids64) int64.  An id outside 0 .. n-1 reads nothing and gives a row of zeros.
+template <bool PAST, class T>
+__device__ __forceinline__ void put(void* at, const T& v) {
+  if constexpr (PAST) __builtin_nontemporal_store(v, static_cast<T*>(at));
+  else *static_cast<T*>(at) = v;
+}
+
+// PAST: stores go past the caches.  ids: int32 or (ids64) int64.  An id outside 0 .. n-1 reads nothing and gives a row of zeros.
 // OUT16: bfloat16 outputs, else float.  RAW (with OUT16): scale is 1, the weight's own bits.
-template <bool OUT16, bool RAW>
+template <bool OUT16, bool RAW, bool PAST>
 __global__ __launch_bounds__(kBlock) void k_embed(const void* __restrict__ ids, int ids64, int64_t cnt,
                                                   Planes p, int64_t n, int64_t k, float scale,
                                                   void* __restrict__ out) {
@@ -106,7 +112,7 @@ __global__ __launch_bounds__(kBlock) void k_embed(const void* __restrict__ ids, 
       if (c0 + c >= k) continue;                 // (k is a multiple of 128: whole stores)
       const int64_t at = j * k + c0 + c;
       if constexpr (RAW) {
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + at) = x;
+        put<PAST>(static_cast<uint16_t*>(out) + at, x);
       } else {
         float f[8];
 #pragma unroll
@@ -119,11 +125,10 @@ __global__ __launch_bounds__(kBlock) void k_embed(const void* __restrict__ ids, 
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             o[i] = (uint32_t)float_to_bf16_rne(f[2 * i]) | (uint32_t)float_to_bf16_rne(f[2 * i + 1]) << 16;
-          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + at) = o;
+          put<PAST>(static_cast<uint16_t*>(out) + at, o);
         } else {
-          floatx4* o = reinterpret_cast<floatx4*>(static_cast<float*>(out) + at);
-          o[0] = (floatx4){f[0], f[1], f[2], f[3]};
-          o[1] = (floatx4){f[4], f[5], f[6], f[7]};
+          put<PAST>(static_cast<float*>(out) + at, (floatx4){f[0], f[1], f[2], f[3]});
+          put<PAST>(static_cast<float*>(out) + at + 4, (floatx4){f[4], f[5], f[6], f[7]});
         }
       }
     }
@@ -138,12 +143,15 @@ hipError_t launch_embed(const void* ids, bool ids64, int64_t cnt, const Planes& 
   if (blocks > (1 << 20)) blocks = 1 << 20;
   const dim3 grid((unsigned)blocks), block(kBlock);
   const int i64 = ids64 ? 1 : 0;
-  if (out16 && scale == 1.0f)
-    hipLaunchKernelGGL((k_embed<true, true>), grid, block, 0, s, ids, i64, cnt, p, n, k, scale, out);
-  else if (out16)
-    hipLaunchKernelGGL((k_embed<true, false>), grid, block, 0, s, ids, i64, cnt, p, n, k, scale, out);
-  else
-    hipLaunchKernelGGL((k_embed<false, false>), grid, block, 0, s, ids, i64, cnt, p, n, k, scale, out);
+  // Outputs of more than an L2's 4 MiB go past the caches, which hold the sectors of the table meanwhile
+  // (5120 columns: 4096 rows 53.6 -> 48.9 us, 1024 rows 16.2 -> 15.0; 256 rows 6.3 -> 6.5, 16 rows 4.8 ->
+  // 5.4, left to the caches).
+  const bool past = cnt * k * (out16 ? 2 : 4) > (int64_t(4) << 20);
+  typedef void (*Kernel)(const void*, int, int64_t, Planes, int64_t, int64_t, float, void*);
+  const Kernel f = !out16          ? (past ? k_embed<false, false, true> : k_embed<false, false, false>)
+                   : scale == 1.0f ? (past ? k_embed<true, true, true> : k_embed<true, true, false>)
+                                   : (past ? k_embed<true, false, true> : k_embed<true, false, false>);
+  hipLaunchKernelGGL(f, grid, block, 0, s, ids, i64, cnt, p, n, k, scale, out);
   return hipGetLastError();
 }
 

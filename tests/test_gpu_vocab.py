@@ -42,7 +42,8 @@ def _weights(n, k, seed, p_zero=0.01):
     return w
 
 
-@pytest.mark.parametrize("n,k,count", [(1, 128, 1), (16, 128, 5), (37, 1152, 64), (300, 5120, 33), (257, 2048, 700)])
+@pytest.mark.parametrize("n,k,count", [(1, 128, 1), (16, 128, 5), (37, 1152, 64), (300, 5120, 33), (257, 2048, 700),
+                                       (80, 5120, 900)])
 @pytest.mark.parametrize("idt", [torch.int32, torch.int64])
 def test_embed_rows(n, k, count, idt):
     w12 = _w12()
