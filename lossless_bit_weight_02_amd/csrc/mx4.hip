@@ -136,10 +136,10 @@ __global__ __launch_bounds__(kBlock) void k_mx4_build(Planes p, int64_t n, int64
 // bfloat16 (at the lowest windows as a subnormal), so the high half of the float product is the
 // value.  A lane's 32 columns are 64 bytes of its row, but stored as they lie each store would touch
 // 16 bytes of 64 pieces; so the tile turns in LDS and leaves as whole 256-byte row pieces (16 lanes
-// each, rotated by the row against bank conflicts): gate+up [34816, 5120] 136.1 -> 86 us.  The
-// escapes go over their slots there: each lane finds those of its own block in its row's list.
-// Bound by memory, 17/32 bytes read and 2 written per weight: those 86 us are 5.2 TB/s, [5120,
-// 5120] takes 15.2 us (4.4 TB/s).
+// each, rotated by the row against bank conflicts): gate+up [34816, 5120] 136.1 -> 86 us; and past
+// the caches, which nothing of it would stay in: 73 us.  The escapes go over their slots there: each
+// lane finds those of its own block in its row's list.  Bound by memory, 17/32 bytes read and 2
+// written per weight: those 73 us are 6.2 TB/s, [5120, 5120] takes 14.2 us (4.7 TB/s).
 __global__ __launch_bounds__(kBlock) void k_mx4_decode(Planes pl, int64_t n, int64_t k, uint16_t* __restrict__ out) {
   __shared__ __attribute__((aligned(16))) u32x4 s_t[kBlock / 64][256];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -184,7 +184,8 @@ __global__ __launch_bounds__(kBlock) void k_mx4_decode(Planes pl, int64_t n, int
       const int rr = 4 * i + g;                    // 16 lanes a row
       const u32x4 o = st[16 * rr + ((r + rr) & 15)];
       if (tr * kTileRows + rr < n)
-        *reinterpret_cast<u32x4*>(out + (tr * kTileRows + rr) * k + (t - tr * ktiles) * kTileCols + 8 * r) = o;
+        __builtin_nontemporal_store(
+            o, reinterpret_cast<u32x4*>(out + (tr * kTileRows + rr) * k + (t - tr * ktiles) * kTileCols + 8 * r));
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
