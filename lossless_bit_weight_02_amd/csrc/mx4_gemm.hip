@@ -9,9 +9,9 @@
 // and the loop's instructions, a round's start and its reads of x are spread over them.
 //
 // Measured (us; weights alone at the rate of a large read, 6.4 TB/s, in parentheses): 64 rows,
-// [34816, 5120] 39.2 (16.3; k_mfma_wide's loop 54.2), [152064, 5120] 139 to 152 (71), [5120, 17408]
-// 31.4 (8.0), [5120, 5120] 18.0 (2.5); 16 rows, [152064, 5120] 87.3 (66.4; one tile per wave 93.5); 32
-// rows 96.3 (67.9; 109.5).  At 64 rows the weights, the matrix cores (the fullest SIMD's) and the LDS
+// [34816, 5120] 36 to 39 (16.3; k_mfma_wide's loop 54.2), [152064, 5120] 150 (71), [5120, 17408] 31.4
+// (8.0), [5120, 5120] 18.0 (2.5); 16 rows, [152064, 5120] 81.6 (66.4; one tile per wave 93.5); 32 rows
+// 97 (67.9; 109.5).  At 64 rows the weights, the matrix cores (the fullest SIMD's) and the LDS
 // reads take about 15 us each of the 39, the start and the end of the kernel 7: what is missing is
 // their overlap in two waves per SIMD.
 //
@@ -56,6 +56,13 @@ struct Mx4Args {
   int yvec;                      // 4 outputs of a row as one store (aligned, ldy % 4 == 0)
 };
 
+// PAST: past the caches
+template <bool PAST, class T>
+__device__ __forceinline__ void mx_put(void* at, const T& v) {
+  if constexpr (PAST) __builtin_nontemporal_store(v, static_cast<T*>(at));
+  else *static_cast<T*>(at) = v;
+}
+
 template <int N>
 __device__ __forceinline__ void mx_wait_le() {
   constexpr int M = N < 63 ? N : 63;
@@ -63,7 +70,9 @@ __device__ __forceinline__ void mx_wait_le() {
 }
 
 // NT: 16-row activation tiles; TP: weight tiles per wave; S: blocks per x chunk, of which a wave takes S / 2.
-template <int NT, int TP, int S>
+// PAST: y is final (one k range) and goes past the caches ([152064, 5120], 16 rows 87.8 -> 81.6 us, 64
+// rows 155.2 -> 149.5; [17408, 5120], 64 rows 28.3 -> 28.1); partial sums are read again at once.
+template <int NT, int TP, int S, bool PAST>
 __global__ __launch_bounds__(64 * kMxWaves) __attribute__((amdgpu_waves_per_eu(2)))
 void k_mx4_gemm(Mx4Args a) {
   constexpr int W = kMxWaves;
@@ -341,16 +350,16 @@ void k_mx4_gemm(Mx4Args a) {
         const int64_t col = row0[j] + 4 * g, at = row * a.ldy + col;
         if (a.y16) {
           if (a.yvec && col + 3 < a.n) {
-            *reinterpret_cast<u32x2*>(a.y16 + at) =
-                (u32x2){(uint32_t)float_to_bf16_rne(v[0]) | (uint32_t)float_to_bf16_rne(v[1]) << 16,
-                        (uint32_t)float_to_bf16_rne(v[2]) | (uint32_t)float_to_bf16_rne(v[3]) << 16};
+            mx_put<PAST>(a.y16 + at,
+                         (u32x2){(uint32_t)float_to_bf16_rne(v[0]) | (uint32_t)float_to_bf16_rne(v[1]) << 16,
+                                 (uint32_t)float_to_bf16_rne(v[2]) | (uint32_t)float_to_bf16_rne(v[3]) << 16});
           } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
               if (col + r < a.n) a.y16[at + r] = float_to_bf16_rne(v[r]);
           }
         } else if (a.yvec && col + 3 < a.n) {
-          *reinterpret_cast<floatx4*>(yout + at) = (floatx4){v[0], v[1], v[2], v[3]};
+          mx_put<PAST>(yout + at, (floatx4){v[0], v[1], v[2], v[3]});
         } else {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
@@ -372,10 +381,11 @@ struct Mx4Shape {
 static Mx4Shape mx4_shape(int nt) { return nt <= 2 ? Mx4Shape{5, 8} : Mx4Shape{3, 4}; }
 // tp: tiles per wave.  Passes of at most 32 rows come here with at least 13 tiles per workgroup and
 // round (launch_mx4_gemm), so with four or five per wave.
-static Mx4Kernel mx4_pick(int nt, int tp) {
-  if (nt == 1) return tp <= 4 ? k_mx4_gemm<1, 4, 8> : k_mx4_gemm<1, 5, 8>;
-  if (nt == 2) return tp <= 4 ? k_mx4_gemm<2, 4, 8> : k_mx4_gemm<2, 5, 8>;
-  return tp == 1 ? k_mx4_gemm<4, 1, 4> : tp == 2 ? k_mx4_gemm<4, 2, 4> : k_mx4_gemm<4, 3, 4>;
+static Mx4Kernel mx4_pick(int nt, int tp, bool split) {
+  if (nt == 1) return tp <= 4 ? k_mx4_gemm<1, 4, 8, true> : k_mx4_gemm<1, 5, 8, true>;
+  if (nt == 2) return tp <= 4 ? k_mx4_gemm<2, 4, 8, true> : k_mx4_gemm<2, 5, 8, true>;
+  if (split) return tp == 1 ? k_mx4_gemm<4, 1, 4, false> : k_mx4_gemm<4, 2, 4, false>;   // at most eight tiles
+  return tp == 1 ? k_mx4_gemm<4, 1, 4, true> : tp == 2 ? k_mx4_gemm<4, 2, 4, true> : k_mx4_gemm<4, 3, 4, true>;
 }
 
 hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_t n, int64_t k, YOut y,
@@ -431,7 +441,7 @@ hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_
     a.ysplit = (int64_t)mb * n;
     a.yvec = a.y16 ? (reinterpret_cast<uintptr_t>(a.y16) & 7u) == 0 && n % 4 == 0
                    : (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0 && n % 4 == 0;
-    hipLaunchKernelGGL(mx4_pick(nt, (a.tpr + kMxWaves / 2 - 1) / (kMxWaves / 2)), dim3((unsigned)(groups * ranges)),
+    hipLaunchKernelGGL(mx4_pick(nt, (a.tpr + kMxWaves / 2 - 1) / (kMxWaves / 2), ws != nullptr), dim3((unsigned)(groups * ranges)),
                        dim3(64 * kMxWaves), 0, s, a);
     err = hipGetLastError();
     if (err != hipSuccess) return err;
