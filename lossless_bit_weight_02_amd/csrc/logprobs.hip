@@ -685,7 +685,8 @@ void k_logprobs_part(LpArgs a) {
   __shared__ uint64_t s_best[kLpCap];
   __shared__ float s_max[kLpWaves][64];
   __shared__ float s_run[kLpWaves][4];
-  __shared__ int s_cnt[kLpWaves];
+  __shared__ int s_cnt[kLpWaves];                  // keys in each wave's own list
+  __shared__ int s_masked[kLpWaves];               // (apart from s_cnt: a slow wave may still read it when a fast one counts)
   __shared__ uint32_t s_seen[kLpWaves];
   __shared__ int s_total;                          // keys offered to the shared list
   const int tid = threadIdx.x, lane = tid & 63;
@@ -751,7 +752,7 @@ void k_logprobs_part(LpArgs a) {
   float lowf = 0.0f;
   // nothing but masked logits: the first columns
   const bool masked = M == -INFINITY && __ballot(s != s) == 0;
-  if (lane == 0) s_cnt[w] = masked ? 1 : 0;
+  if (lane == 0) s_masked[w] = masked ? 1 : 0;
   if (a.top > 0 && !masked) {
     const uint32_t hi = lp_order(M);
     if (a.top == 1) {
@@ -786,7 +787,7 @@ void k_logprobs_part(LpArgs a) {
     }
   }
   __syncthreads();
-  const bool none = __builtin_amdgcn_readfirstlane(s_cnt[0] + s_cnt[1] + s_cnt[2] + s_cnt[3]) == kLpWaves;
+  const bool none = __builtin_amdgcn_readfirstlane(s_masked[0] + s_masked[1] + s_masked[2] + s_masked[3]) == kLpWaves;
   int total = a.top > 0 ? __builtin_amdgcn_readfirstlane(s_total) : 0;
   if (a.top > 0 && M == -INFINITY && !none) {      // masked logits and a NaN: the long way
     lowf = -INFINITY;

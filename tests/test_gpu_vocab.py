@@ -188,6 +188,26 @@ def test_logprobs_masks(m, n, dt):
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [3 * 1024 + 1, 4096, 8192 + 3 * 1024 + 1])
+def test_logprobs_more_candidates_than_the_list(n, dt):
+    """Parts whose candidates overflow the shared list, so each wave counts its own: equal logits (all
+    of them, or all but one wave's), and -Inf with a lone NaN in one wave's range.  With 1 or 4
+    alternatives the waves' counts add up to the number of waves."""
+    y, tok = _logits(6, n, n, dt)
+    y[0] = 0.25
+    y[1, :1024] = -1.0
+    y[1, 1024:] = 7.0
+    y[2] = -math.inf
+    y[2, n - 1] = math.nan
+    y[3] = -math.inf
+    y[3, 5] = math.nan
+    y[4] = -math.inf
+    y[4, 300:900] = 1.0
+    for top in (1, 2, 4, 64):
+        _check_lp(y, tok, top, "many candidates")
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("order", ["up", "down"])
 def test_logprobs_sorted_rows(order, dt):
     """Ascending logits enter the candidate list one after the other; descending ones never again."""
