@@ -380,7 +380,8 @@ int w12_embed(const void *ids, int64_t count, const w12_weight *wt, float scale,
  * -Inf logits (masked tokens) have probability 0.  A row of -Inf alone has no distribution: its
  * log probabilities are -Inf, its entropy 0, its alternatives columns 0 .. top-1.  A row with a NaN
  * or +Inf logit gives NaN log probabilities (a token outside 0 .. n-1 still -Inf) and entropy.
- * All sums are held in float.  scratch: w12_logprobs_scratch bytes of device memory of the caller's
+ * All sums are held in float; finite logits may have any magnitude; a logit whose e^(y - max) is below
+ * 2^-126 may count as 0.  scratch: w12_logprobs_scratch bytes of device memory of the caller's
  * (16-byte aligned; NULL when that is 0; W12_ERR_CAPACITY if scratch_bytes is smaller), in use until
  * the call's work on `stream` is finished.  Its first bytes are counters that must be zero when
  * the work starts and are zero again when it ends: clear it once, then reuse it for calls of any

@@ -1,0 +1,87 @@
+"""GPU tests of w12_logprobs over the whole range of finite logits, against the oracle.
+
+Bounds: oracle.logprobs_tol for the sums -- a term's argument is x - M rounded once and times log2 e
+rounded in both factors, or (|M| < 4096) one rounding of x log2 e - fl(M log2 e), whose common residue
+of at most 2^-12 is taken out to first order, wrong by (2^-12 ln 2)^2 / 2 < 2^-24 / 4 -- and four
+roundings of the result.  A term below 2^-126, the least normal float, may count as 0: n terms lose at
+most n 2^-126 of the sum s, and of the entropy's other half at most n 2^-126 (126 ln 2), since
+p |log p| rises up to p = 1 / e; 126 ln 2 < 88, so the entropy loses less than 89 n 2^-126 in all.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from lossless_bit_weight_02_amd import w12
+    w12.lib()
+
+
+def _compare(r, y, tokens, top, what):
+    y64, n = y.double().numpy(), y.shape[1]
+    lp, ent, idx, tlp = oracle.logprobs64(y64, tokens.numpy(), top)
+    stol, etol = oracle.logprobs_tol(y64)
+    u, least = 2.0 ** -24, n * 2.0 ** -126
+
+    def close(got, want, tol, name):
+        got = got.double().cpu().numpy()
+        fin = np.isfinite(want)
+        assert np.array_equal(got[~fin], want[~fin], equal_nan=True), f"{what}: {name}: not finite"
+        off = np.abs(got[fin] - want[fin]) - (tol + 4 * u * np.abs(np.where(fin, want, 0.0)))[fin]
+        assert (off <= 0).all(), f"{what}: {name}: {np.count_nonzero(~(off <= 0))} outside, by up to {off.max():.3g}"
+
+    close(r.logp, lp, (stol + least)[:, None], "logp")
+    close(r.entropy, ent, etol + 89 * least, "entropy")
+    assert np.array_equal(r.top_index.cpu().numpy(), idx), f"{what}: alternatives differ"
+    close(r.top_logp, tlp, (stol + least)[:, None], "top_logp")
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,reps", [(3000, 1), (9000, 1), (300000, 1), (5000, 130)])
+def test_logprobs_large_magnitudes(n, reps, dt):
+    """Maxima of any magnitude: whole rows of one finite value (a finite mask, -1e9, over everything),
+    such masks beside -Inf and beside ordinary logits, logits around an offset, logits divided by a
+    small temperature, and rows that rise or fall through the magnitudes.  Sixteen rows, `reps` times:
+    in register parts (one, and several), streamed in parts, and streamed whole."""
+    from lossless_bit_weight_02_amd import w12
+
+    def check(y, top, what):
+        say(f"logprobs {what} n={n} reps={reps} {dt} top={top}")
+        r = w12.logprobs(y.cuda().repeat(reps, 1), tok.cuda().repeat(reps, 1), top=top)
+        for r0 in {0, 16 * (reps - 1)}:
+            _compare(type(r)(*(f[r0:r0 + 16] for f in r)), y, tok, top, what)
+
+    g = torch.Generator().manual_seed(7)
+    y = torch.randn(16, n, generator=g) * 3
+    y[torch.arange(16), torch.randint(0, n, (16,), generator=g)] += torch.rand(16, generator=g) * 25
+    y, tok = y.to(dt), torch.randint(0, n, (16, 3), generator=g)
+    noise = torch.randn(16, n, generator=torch.Generator().manual_seed(8)).double() * 3
+    for j, v in enumerate((-1e4, -1e9, -1e8, 1e6, 3e7, -1e30)):
+        y[j] = v
+    y[6, ::2], y[6, 1::2] = -1e9, -math.inf
+    y[7, 40:] = -1e9
+    y[8] = torch.linspace(-3e4, 3e4, n).to(dt)
+    y[9] = torch.linspace(3e4, -3e4, n).to(dt)
+    y[10] = (torch.linspace(-1.0, 1.0, n) ** 9 * 1e12).to(dt)
+    y[11, n // 2:] += 4080.0                         # maxima around the limit of the shared residue
+    y[12] = (0.01 * noise[12] - 4096.0).to(dt)
+    y[13] = -4095.0
+    y[14] = 4096.0
+    check(y, 1, "fills")
+    check(y, 9, "fills")
+    for off in (1e3, 1e4, 1e5, 1e6, 1e7, 1e8, 1e12, 1e30, 1e37, 3e38):
+        sign = torch.tensor([1.0, -1.0], dtype=torch.float64).repeat(8)[:, None]
+        check((noise + sign * off).to(dt), 3, f"offset {off:g}")
+    for temp in (1e-2, 1e-4, 1e-6, 1e-8):
+        check((noise / temp).to(dt), 3, f"temperature {temp:g}")
