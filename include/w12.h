@@ -354,10 +354,11 @@ int w12_concat_rows(const w12_weight *parts, int count, w12_weight *out, uint64_
  * w12_embed -- embedding lookup: out[j][c] = scale * W[ids[j]][c], with W read from its W12 record, so
  * a model whose embedding table is its LM head keeps one record for both ends of a step.  ids:
  * `count` int32, or int64 with W12_IDS_I64 (device, naturally aligned); an id outside 0 .. n-1
- * (padding) reads nothing and gives a row of zeros.  out: [count][k] float (device, 16-byte
- * aligned, fully overwritten): the weight times scale in float; with W12_OUT_BF16 bfloat16 bits,
- * that product rounded to nearest even, or for scale = 1 the weight's own bits (NaN payloads and -0
- * included).  flags: W12_OUT_BF16, W12_IDS_I64.  Uses no workspace.
+ * (padding) reads nothing and gives a row of zeros at any scale (-0 at a negative finite one).
+ * out: [count][k] float (device, 16-byte aligned, fully overwritten): the weight times scale in
+ * float; with W12_OUT_BF16 bfloat16 bits, that product rounded to nearest even, or for scale = 1 the
+ * weight's own bits (NaN payloads and -0 included).  flags: W12_OUT_BF16, W12_IDS_I64.  Uses no
+ * workspace.
  */
 #define W12_IDS_I64 0x40u
 int w12_embed(const void *ids, int64_t count, const w12_weight *wt, float scale, void *out,

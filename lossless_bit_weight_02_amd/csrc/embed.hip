@@ -115,10 +115,11 @@ __global__ __launch_bounds__(kBlock) void k_embed(const void* __restrict__ ids, 
         put<PAST>(static_cast<uint16_t*>(out) + at, x);
       } else {
         float f[8];
+        const float sc = real || fabsf(scale) < INFINITY ? scale : 0.0f;   // (padding: zeros at any scale)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          f[2 * i] = bf16_to_float(x[i] & 0xFFFFu) * scale;
-          f[2 * i + 1] = bf16_to_float(x[i] >> 16) * scale;
+          f[2 * i] = bf16_to_float(x[i] & 0xFFFFu) * sc;
+          f[2 * i + 1] = bf16_to_float(x[i] >> 16) * sc;
         }
         if constexpr (OUT16) {
           u32x4 o;

@@ -94,6 +94,22 @@ def test_embed_edges():
         w12.embed(torch.zeros(2, dtype=torch.int64), rec)
 
 
+@pytest.mark.parametrize("f32", [False, True])
+def test_embed_padding_at_any_scale(f32):
+    """An id outside the rows gives zeros whatever the scale; the rows beside it are scaled."""
+    w12 = _w12()
+    w = _weights(40, 256, 4)
+    rec = w12.encode(to_dev(w))
+    ids = torch.tensor([-1, 7, 40, 1 << 33, 39], device="cuda:0")
+    rows = torch.from_numpy(synth.bf16_bits_to_f32(w[[7, 39]]))
+    for scale in (math.inf, -math.inf, math.nan, -2.0, 0.0):
+        say(f"embed padding scale={scale} f32={f32}")
+        got = w12.embed(ids, rec, scale=scale, out_f32=f32).cpu()
+        assert (got[[0, 2, 3]] == 0).all(), scale
+        want = (rows * scale).to(got.dtype)
+        assert torch.equal(got[[1, 4]].isnan(), want.isnan()) and torch.equal(got[[1, 4]].nan_to_num(), want.nan_to_num())
+
+
 # ---------------------------------------------------------------------------------------------
 # log probabilities
 # ---------------------------------------------------------------------------------------------
