@@ -624,8 +624,8 @@ _lp_buffers: dict = {}     # (device, stream) -> zero-counter scratch of the str
 
 def _lp_scratch(m, n, top, flags, device, stream):
     """(scratch or None, bytes) of a logprobs call on `stream`.  Calls of one stream follow each other,
-    so they share one buffer; a call under graph capture gets its own, cleared by the graph, since
-    graphs may be replayed on any stream."""
+    so they share one buffer, kept until release_workspace; a call under graph capture gets its own,
+    cleared by the graph, since graphs may be replayed on any stream."""
     key = (device.index, m, n, top, flags)
     need = _lp_sizes.get(key)
     if need is None:
@@ -650,7 +650,8 @@ def logprobs(y: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0) 
     logits, in one pass.  y [m, n] float32 or bfloat16 on the GPU, rows at any stride, columns
     contiguous (others are copied); tokens int32 or int64, [m] or [m, t] (a token outside 0 .. n-1 has
     log probability -Inf).  Equal logits go by the lower index; a row of -Inf alone gives -Inf and
-    entropy 0; a row with NaN or +Inf gives NaN."""
+    entropy 0; a row with NaN or +Inf gives NaN.  Calls that cut rows in parts keep a scratch buffer
+    per stream (256 KiB and up); release_workspace frees it."""
     if not isinstance(y, torch.Tensor) or y.dim() != 2 or not y.is_cuda:
         raise ValueError("y must be a 2-D CUDA tensor")
     if y.dtype not in (torch.float32, torch.bfloat16):
@@ -728,10 +729,15 @@ def read_probe(buf: torch.Tensor, sink: torch.Tensor | None = None):
 
 
 def release_workspace(stream: "torch.cuda.Stream | None" = None, device=None):
-    """Free the library's GEMM workspace of ``stream`` (default: the current stream of
-    ``device``) on its device; waits for the stream's work first.  A later GEMM call on the
-    stream allocates a new one."""
+    """Free what calls on ``stream`` (default: the current stream of ``device``) have left allocated for
+    the next ones: the library's GEMM workspace and the scratch of logprobs; waits for the stream's
+    work first.  A later call on the stream allocates anew.  To be called before a stream that either
+    ran on is destroyed: a new stream may get its handle."""
     if stream is None:
         stream = torch.cuda.current_stream(device)
     with torch.cuda.device(stream.device):
         _check(lib().w12_release_workspace(stream.cuda_stream))
+    key = (stream.device.index, stream.cuda_stream)
+    if key in _lp_buffers:
+        stream.synchronize()
+        _lp_buffers.pop(key, None)

@@ -306,6 +306,30 @@ def test_logprobs_repeat_graph_and_streams():
         assert all(torch.equal(u, v) for u, v in zip(eager, q0))
 
 
+def test_logprobs_scratch_released():
+    """release_workspace gives a stream's scratch back (a stream with no GEMM workspace among them); the
+    next call on the stream is right, and a released stream or one without scratch may be released again."""
+    w12 = _w12()
+    y, tok = _logits(9, 20000, 13, torch.float32)
+    a, t = y.cuda(), tok.cuda()
+    want = w12.logprobs(a, t, top=12)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    w12.release_workspace(side)
+    before = torch.cuda.memory_allocated()
+    for rep in range(2):
+        say(f"logprobs on a side stream, call {rep}")
+        with torch.cuda.stream(side):
+            r = w12.logprobs(a, t, top=12)
+        side.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(r, want))
+        del r
+        w12.release_workspace(side)
+        assert torch.cuda.memory_allocated() == before
+        w12.release_workspace(side)
+    torch.cuda.synchronize()
+
+
 def test_logprobs_far_rows():
     """Rows more than 4 GiB apart on both kernels: the second of two, and the last ones of a tall matrix."""
     w12 = _w12()
