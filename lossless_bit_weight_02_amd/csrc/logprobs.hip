@@ -47,8 +47,7 @@ constexpr int kLpBatch = 64 * kLpElems;          // logits of a wave per batch
 constexpr uint32_t kLpMasked = 0x007FFFFFu;      // the order of -Inf
 constexpr int kLpCountStep = 32;                 // rows' counts 128 bytes apart: counts of one line wait for each other
 constexpr int kLpAhead = 4;                      // keys of a part loaded together when parts join
-constexpr float kLpFused = 4096.0f;              // maxima below this in magnitude: lp_sums2
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
 
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
@@ -311,7 +310,10 @@ struct LpBatch {
   }
 };
 
-// Sums of a lane's batch under any maximum M; `leave`: but for one logit equal to M.
+// Sums of a lane's batch under the maximum M; `leave`: but for one logit equal to M.  x - M comes first:
+// it rounds once, relative to itself, at any magnitude.  (x log2 e - M log2 e as one operation carries
+// the rounding of M log2 e, which grows with M, and is no faster: 1024 rows of 152064 112.4 us
+// against 109.5, 64 rows, 16 alternatives 23.2 against 23.4.)
 __device__ __forceinline__ void lp_sums(const float (&x)[kLpElems], float M, bool leave, float& s, float& T) {
 #pragma unroll
   for (int e = 0; e < kLpElems; ++e) {
@@ -324,27 +326,6 @@ __device__ __forceinline__ void lp_sums(const float (&x)[kLpElems], float M, boo
     s += p;
     T = fmaf(p, fmaxf(d, -200.0f), T);             // (a masked logit: 0 times a finite number)
   }
-}
-// The same for |M| < kLpFused in units of log 2, the product and the difference in one rounding:
-// a = x L - fl(M L), which is (x - M) L + del with one del = M L - fl(M L) for all logits under this
-// maximum; lp_fold puts it right.
-__device__ __forceinline__ void lp_sums2(const float (&x)[kLpElems], float ML, float& s, float& T) {
-#pragma unroll
-  for (int e = 0; e < kLpElems; ++e) {
-    const float d = fmaf(x[e], kLog2e, -ML);
-    const float p = __builtin_amdgcn_exp2f(d);
-    s += p;
-    T = fmaf(p, fmaxf(d, -300.0f), T);
-  }
-}
-// Sums (sf, Tf) of lp_sums2 into (s, T): with p = 2^-del p' the true terms, s += 2^-del s',
-// T += 2^-del (T' - del s') / L.  2^-del to first order: del is at most half a unit in the last place of
-// M L, 2^-12 below kLpFused, so the next term is (2^-12 ln 2)^2 / 2 < 2^-24 / 4 of the sums.  (It grows
-// with M^2: 1e-6 at 1e5, and past 1e8 2^-del itself leaves the range of a float.)
-__device__ __forceinline__ void lp_fold(float M, float ML, float sf, float Tf, float& s, float& T) {
-  const float del = fmaf(M, kLog2e, -ML), f = 1.0f - del * kLn2;
-  s += f * sf;
-  T += f * (Tf - del * sf) * kLn2;
 }
 
 // The candidates (at or above lowf, or NaN) of a wave's batch at column c, elements from..15, into the
@@ -561,7 +542,6 @@ void k_logprobs(LpArgs a) {
   const uint8_t* const yr = static_cast<const uint8_t*>(a.y) + row * a.ldy * (BF ? 2 : 4);
 
   float M = -INFINITY, s = 0.0f, T = 0.0f;         // M uniform; s, T the lane's
-  float sf = 0.0f, Tf = 0.0f, ML = 0.0f;           // sums of lp_sums2 not yet in s, T; fl(M L)
   int owner = 0;                                   // the lane that left the maximum out
   LpTop top;
   top.list = s_list[w];
@@ -588,19 +568,14 @@ void k_logprobs(LpArgs a) {
       // a new maximum: the sums so far relative to it, and one logit that equals it left out
       const float mn = wave_max(mx);
       if (M > -INFINITY) {
-        if (fabsf(M) < kLpFused) lp_fold(M, ML, sf, Tf, s, T);
-        sf = Tf = 0.0f;
         const float d = M - mn, f = lp_exp(d);
         if (lane == owner) s += 1.0f;
         T = f > 0.0f ? f * (T + s * d) : s != s ? s : 0.0f;   // (s d may overflow where f is 0)
         s *= f;
       }
       M = mn;
-      ML = M * kLog2e;
       owner = __ffsll((unsigned long long)__ballot(mx == M)) - 1;
       lp_sums(x, M, lane == owner, s, T);
-    } else if (fabsf(M) < kLpFused) {
-      lp_sums2(x, ML, sf, Tf);
     } else if (M > -INFINITY) {
       lp_sums(x, M, false, s, T);
     } else {
@@ -611,7 +586,7 @@ void k_logprobs(LpArgs a) {
     }
     ++batch;
     if (!closed) {
-      anynan = anynan || __ballot(s + sf != s + sf) != 0;
+      anynan = anynan || __ballot(s != s) != 0;
       if (anynan || __ballot(mx >= thrf)) {
         lmax = fmaxf(lmax, mx);
         // the bound again at the batches 1, 2, 4, 8, ...: a bound twice as old lets through about
@@ -654,7 +629,6 @@ void k_logprobs(LpArgs a) {
     }
   }
 
-  if (fabsf(M) < kLpFused) lp_fold(M, ML, sf, Tf, s, T);
   // the lanes' sums (relative to the same M) in a fixed order, then the waves'
   s = wave_sum(s);
   T = wave_sum(T);
@@ -734,14 +708,9 @@ void k_logprobs_part(LpArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) bad |= x[e] != x[e];
     if (bad) s = __uint_as_float(0x7FC00000u);
-  } else if (w == wo || fabsf(M) >= kLpFused) {
+  } else {
     const int owner = __ffsll((unsigned long long)__ballot(mx == M)) - 1;
     lp_sums(x, M, w == wo && lane == owner, s, T);
-  } else {
-    float sf = 0.0f, Tf = 0.0f;
-    const float ML = M * kLog2e;
-    lp_sums2(x, ML, sf, Tf);
-    lp_fold(M, ML, sf, Tf, s, T);
   }
   s = wave_sum(s);
   T = wave_sum(T);

@@ -1,11 +1,10 @@
 """GPU tests of w12_logprobs over the whole range of finite logits, against the oracle.
 
-Bounds: oracle.logprobs_tol for the sums -- a term's argument is x - M rounded once and times log2 e
-rounded in both factors, or (|M| < 4096) one rounding of x log2 e - fl(M log2 e), whose common residue
-of at most 2^-12 is taken out to first order, wrong by (2^-12 ln 2)^2 / 2 < 2^-24 / 4 -- and four
-roundings of the result.  A term below 2^-126, the least normal float, may count as 0: n terms lose at
-most n 2^-126 of the sum s, and of the entropy's other half at most n 2^-126 (126 ln 2), since
-p |log p| rises up to p = 1 / e; 126 ln 2 < 88, so the entropy loses less than 89 n 2^-126 in all.
+Bounds: oracle.logprobs_tol for the sums (a term's argument is x - M rounded once and times log2 e
+rounded in both factors) and four roundings of the result.  A term below 2^-126, the least normal
+float, may count as 0: n terms lose at most n 2^-126 of the sum s, and of the entropy's other half at
+most n 2^-126 (126 ln 2), since p |log p| rises up to p = 1 / e; 126 ln 2 < 88, so the entropy loses
+less than 89 n 2^-126 in all.
 """
 import math
 
@@ -74,7 +73,7 @@ def test_logprobs_large_magnitudes(n, reps, dt):
     y[8] = torch.linspace(-3e4, 3e4, n).to(dt)
     y[9] = torch.linspace(3e4, -3e4, n).to(dt)
     y[10] = (torch.linspace(-1.0, 1.0, n) ** 9 * 1e12).to(dt)
-    y[11, n // 2:] += 4080.0                         # maxima around the limit of the shared residue
+    y[11, n // 2:] += 4080.0                         # maxima around a power of two
     y[12] = (0.01 * noise[12] - 4096.0).to(dt)
     y[13] = -4095.0
     y[14] = 4096.0

@@ -104,23 +104,3 @@ def test_oracle_logprobs_conventions():
     assert idx[3].tolist() == [0, 2, 3]
     # a confident row keeps its small probability mass
     assert np.isclose(logp[4, 0], -math.exp(-50), rtol=1e-12) and idx[4].tolist() == [0, 3, 1]
-
-
-def test_logprobs_first_order_residue():
-    """In float steps: the factor that the log-probability kernels take their sums' common residue out
-    with is 2^-del to a quarter of 2^-24 (the next term, (del ln 2)^2 / 2) and its own two roundings, at
-    every maximum below the limit that they use it under."""
-    src = open(os.path.join(os.path.dirname(w12.__file__), "csrc", "logprobs.hip")).read()
-    limit = float(re.search(r"kLpFused = ([0-9.]+)f;", src).group(1))
-    rng = np.random.default_rng(1)
-    M = np.concatenate([rng.uniform(-limit, limit, 200000), [np.nextafter(np.float32(limit), np.float32(0)), 1.0, 0.0, -17.5]])
-    M = M.astype(np.float32)
-    M = M[np.abs(M) < limit]
-    log2e, ln2 = np.float32(1.44269504088896340736), np.float32(0.69314718055994530942)
-    ML = M * log2e
-    exact = M.astype(np.float64) * np.float64(log2e) - ML.astype(np.float64)
-    del_ = exact.astype(np.float32)
-    f = np.float32(1) - (del_ * ln2).astype(np.float32)
-    assert np.abs(del_).max() <= 2.0 ** -12
-    err = np.abs(f.astype(np.float64) * np.exp2(exact) - 1.0)
-    assert err.max() <= (0.25 + 1.0 + 2.0 ** -10) * 2.0 ** -24
