@@ -109,8 +109,8 @@ w12::Planes planes_of(const w12_weight* wt) {
 // vs 85.2; [12288, 5120] ties, 87.1 vs 86.4), the dense baseline's up to 3 ([5120, 17408] 121.2
 // vs 140.9, [5120, 6144] 55.6 vs 73.9, [8192, 5120] 54.7 vs 69.3, [12288, 5120] 68.6 vs 70.8).
 // The 4-bit copy never takes it: with half of the bytes its cost per workgroup outweighs the rest
-// (streaming vs the matrix cores, 16 rows: [34816, 5120] 27.1 vs 22.4, [152064, 5120] 90.2 vs 87.3,
-// [8192, 5120] 14.4 vs 13.0, [5120, 17408] 28.5 vs 17.1; 4 rows: 28.1 vs 21.5, 92.3 vs 81.1).
+// (streaming vs the matrix cores, 16 rows: [34816, 5120] 27.6 vs 22.7, [152064, 5120] 90.3 vs 80.6,
+// [8192, 5120] 14.1 vs 13.1, [5120, 17408] 29.2 vs 17.4; 4 rows, the first two: 27.5 vs 21.4, 91.2 vs 78.6).
 bool stream_auto_pick(w12::Fmt f, int64_t m, int64_t tiles, int64_t k, int64_t cus) {
   const bool dense = f == w12::kFmtBF16;
   if (f == w12::kFmtMX4) return false;
@@ -174,10 +174,10 @@ int run_gemm(w12::Fmt f, const uint16_t* x, int64_t m, const w12::Planes& p, int
                 "(rows of fewer than 2^26 columns whose x phases fit the LDS; no SiLU epilogue)");
   const bool stream_auto = stream_ok && stream_auto_pick(f, m, tiles, k, dinfo.cus);
   // The 4-bit copy's bytes are half of the 8-bit view's while the GEMV's work per weight and row of x
-  // stays, so the matrix cores win from 3 rows everywhere ([5120, 17408], us, GEMV vs matrix core:
-  // 33.4 vs 16.0; [8192, 5120] 12.9 vs 12.1; [5120, 5120] 10.8 vs 10.7), and at 2 rows on long rows
-  // ([5120, 17408] 19.9 vs 16.0) and above 6 tiles per CU ([34816, 5120] 24.4 vs 22.8, [152064,
-  // 5120] 98.6 vs 82.2; below it [17408, 5120] 14.8 vs 16.5, [5120, 5120] 8.5 vs 10.9).
+  // stays, so the matrix cores win or tie from 3 rows on ([5120, 17408], us, GEMV vs matrix core:
+  // 34.3 vs 16.2; [8192, 5120] 12.9 vs 12.1; [5120, 5120] 10.7 vs 10.9), and at 2 rows on long rows
+  // ([5120, 17408] 20.1 vs 16.2) and above 6 tiles per CU ([34816, 5120] 24.1 vs 22.3, [152064,
+  // 5120] 96.2 vs 78.8; below it [17408, 5120] 15.7 vs 17.2, [5120, 5120] 8.4 vs 10.7).
   const bool gemv_auto = f == w12::kFmtMX4 ? m == 1 || (m == 2 && k <= 8192 && tiles <= 6 * (int64_t)dinfo.cus)
                                            : m <= 2 || (m <= 5 && tiles <= 1024 && k <= 8192);
   const bool use_stream = flags == W12_PATH_STREAM || (flags == W12_PATH_AUTO && stream_auto);

@@ -15,8 +15,9 @@
 //
 // What bounds it: the record's tile order, made for the GEMMs.  A row's bytes lie in it as 16-byte
 // pieces 256 bytes apart, each fetched as 64, so 4096 rows of 5120 columns read 128 MB (counted)
-// for their 31 MB, and write 42 MB: 49 us, 3.5 TB/s.  (The dense gather with its scaling, reading 42
-// MB: 79.7 us as elementary operations.)  16 rows: 5 us, a launch's latency.
+// for their 31 MB, and write 42 MB: 49 us back to back, 3.5 TB/s (52 as one call among others; float
+// rows, 84 MB written, 57.5).  (The dense gather with its scaling, reading 42 MB: 79.6 us as elementary
+// operations.)  16 rows: 3.4 us, a launch's latency.
 #include "w12_device.hpp"
 #include "w12_launch.hpp"
 
@@ -145,8 +146,8 @@ hipError_t launch_embed(const void* ids, bool ids64, int64_t cnt, const Planes& 
   const dim3 grid((unsigned)blocks), block(kBlock);
   const int i64 = ids64 ? 1 : 0;
   // Outputs of more than an L2's 4 MiB go past the caches, which hold the sectors of the table meanwhile
-  // (5120 columns: 4096 rows 53.6 -> 48.9 us, 1024 rows 16.2 -> 15.0; 256 rows 6.3 -> 6.5, 16 rows 4.8 ->
-  // 5.4, left to the caches).
+  // (5120 columns, scaled: 4096 rows 53.7 -> 49.0 us, 1024 rows 16.9 -> 15.2; 256 rows 7.2 and 6.8, 16
+  // rows 3.4 and 3.4: small ones are left to the caches for whoever reads them next).
   const bool past = cnt * k * (out16 ? 2 : 4) > (int64_t(4) << 20);
   typedef void (*Kernel)(const void*, int, int64_t, Planes, int64_t, int64_t, float, void*);
   const Kernel f = !out16          ? (past ? k_embed<false, false, true> : k_embed<false, false, false>)

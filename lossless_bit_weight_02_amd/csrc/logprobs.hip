@@ -30,11 +30,12 @@
 // wave's i-th batch, whose other logits cost one compare per batch).  They are collected in an LDS
 // list; its K best are picked by rank, the number of larger keys.
 //
-// Measured (152064 float logits a row unless said): 1024 rows 111.6 us (5.6 TB/s; bfloat16 63.0, 4.9
-// TB/s), with 8 alternatives 119.7 (89.7): bound by memory, and in bfloat16 by the instructions per
-// logit.  64 rows 14.9 us, with 16 alternatives 24.3: six of the 15 are the read at 6.4 TB/s, the rest
-// is what one part waits for in turn -- its logits, the maximum, the bound, the candidates, the last
-// part's join (7.1 us at one row, 11.9 with 8 alternatives) -- little of which other parts fill.
+// Measured (152064 float logits a row unless said, calls back to back): 1024 rows 109.5 us (5.7 TB/s;
+// bfloat16 63.0, 4.9 TB/s), with 8 alternatives 118.4 (92.5): bound by memory, and in bfloat16 by the
+// instructions per logit.  64 rows 14.7 us, with 16 alternatives 23.4: six of the 15 are the read at
+// 6.4 TB/s, the rest is what one part waits for in turn -- its logits, the maximum, the bound, the
+// candidates, the last part's join (5.0 us at one row, 9.9 with 8 alternatives) -- little of which
+// other parts fill.
 #include "w12_device.hpp"
 #include "w12_launch.hpp"
 
@@ -797,8 +798,8 @@ void k_logprobs_part(LpArgs a) {
 
 // Parts in registers while they are few for the chip; else whole rows, or if those are still fewer
 // than it runs at once, as many streamed parts as fill it.  (Rows of 152064 float logits, parts in
-// registers against streamed: 32 rows, 8 alternatives 16.3 vs 21.3 us, 64 rows, 16 alternatives 24.6
-// vs 28.0; 128 rows, 8 alternatives 34.5 vs 33.1, 256 rows 59.4 vs 46.3.)
+// registers against streamed: 32 rows, 8 alternatives 15.3 vs 20.3 us, 64 rows, 16 alternatives 23.3
+// vs 26.4, without any 14.7 vs 13.4; 128 rows, 8 alternatives 33.0 vs 32.0, 256 rows 54.8 vs 45.6.)
 constexpr int kLpParts = 16;                     // workgroups per CU up to which rows are cut into register parts
 constexpr int kLpPerCu = 4;                      // streaming workgroups per CU
 constexpr int64_t kLpUnit = (int64_t)kLpWaves * kLpBatch;

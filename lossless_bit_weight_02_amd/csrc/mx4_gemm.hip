@@ -9,9 +9,10 @@
 // and the loop's instructions, a round's start and its reads of x are spread over them.
 //
 // Measured (us; weights alone at the rate of a large read, 6.4 TB/s, in parentheses): 64 rows,
-// [34816, 5120] 36 to 39 (16.3; k_mfma_wide's loop 54.2), [152064, 5120] 150 (71), [5120, 17408] 31.4
-// (8.0), [5120, 5120] 18.0 (2.5); 16 rows, [152064, 5120] 81.6 (66.4; one tile per wave 93.5); 32 rows
-// 97 (67.9; 109.5).  At 64 rows the weights, the matrix cores (the fullest SIMD's) and the LDS
+// [34816, 5120] 37 to 39 (16.3; k_mfma_wide's loop 54.2), [152064, 5120] 139 to 147 (71), [5120, 17408]
+// 31.6 (8.0), [5120, 5120] 18.2 (2.5); 16 rows, [152064, 5120] 81.3 (66.4; one tile per wave 95.3); 32
+// rows 93.2 (67.9; 111.2).  More than 64 rows run as passes of 64 that each read the copy again ([34816,
+// 5120], 128 rows: 73.6).  At 64 rows the weights, the matrix cores (the fullest SIMD's) and the LDS
 // reads take about 15 us each of the 39, the start and the end of the kernel 7: what is missing is
 // their overlap in two waves per SIMD.
 //
@@ -70,8 +71,10 @@ __device__ __forceinline__ void mx_wait_le() {
 }
 
 // NT: 16-row activation tiles; TP: weight tiles per wave; S: blocks per x chunk, of which a wave takes S / 2.
-// PAST: y is final (one k range) and goes past the caches ([152064, 5120], 16 rows 87.8 -> 81.6 us, 64
-// rows 155.2 -> 149.5; [17408, 5120], 64 rows 28.3 -> 28.1); partial sums are read again at once.
+// PAST: y is final (one k range) and goes past the caches ([152064, 5120], 16 rows 94.3 -> 87.7 us
+// through a y kept from call to call; also where log probabilities read it next: 16 rows, both
+// together, 100.5 -> 95.9, 64 rows 162.4 -> 162.7; [34816, 5120], 64 rows 50.8 -> 48.8; [17408, 5120]
+// 38.1 -> 37.9); partial sums are read again at once.
 template <int NT, int TP, int S, bool PAST>
 __global__ __launch_bounds__(64 * kMxWaves) __attribute__((amdgpu_waves_per_eu(2)))
 void k_mx4_gemm(Mx4Args a) {
@@ -172,7 +175,8 @@ void k_mx4_gemm(Mx4Args a) {
     x_fetch(0, 0u);
     __builtin_amdgcn_sched_barrier(0);
     // escape lists of the round's tiles: wave w looks after tiles w, w + 8, ...: where the list lies
-    // and how long it is, and (first k range) its first 64 entries, a lane each, with their rows
+    // and how long it is, and (first k range) its first 64 entries, a lane each; row r's start in lane
+    // r of lstart, from which the sums below find an entry's row by its place
     constexpr int EL = (4 * TP + W - 1) / W;
     uint32_t lt0[EL], lcnt[EL], lstart[EL];
 #pragma unroll
@@ -200,7 +204,7 @@ void k_mx4_gemm(Mx4Args a) {
     __builtin_amdgcn_sched_barrier(0);
     mx_wait_le<D * kLoads>();                      // the first chunk of x is in LDS
     lds_barrier();
-    uint32_t lent[EL], lval[EL];                   // entry: column, row of the tile in bits 28..31
+    uint32_t lent[EL], lval[EL];                   // entry: column, bfloat16 bits
 #pragma unroll
     for (int q = 0; q < EL; ++q) {
       lt0[q] = __builtin_amdgcn_readfirstlane(lt0[q]);
@@ -397,9 +401,9 @@ hipError_t launch_mx4_gemm(const uint16_t* x, int64_t m, const Planes& p, int64_
   for (int64_t m0 = 0; m0 < m; m0 += 64) {
     const int mb = (int)(m - m0 < 64 ? m - m0 : 64);
     // At most 32 rows: k_mfma (mfma.hip), which deals one tile per wave and round, unless its last round
-    // would be so empty that it runs as a launch of its own ([152064, 5120], 16 and 32 rows: 93.5 and
-    // 109.5 us there, 87.3 and 96.3 here; [65536, 5120] 51.4 and 63.9, 38.4 and 45.0; with full rounds,
-    // [49152, 5120], 29.2 and 35.0 there, 31.0 and 36.4 here, [98304, 5120] 55.6 and 65.6, 62.0 and 74.1).
+    // would be so empty that it runs as a launch of its own ([152064, 5120], 16 and 32 rows: 95.3 and
+    // 111.2 us there, 81.3 and 93.2 here; [65536, 5120] 52.2 and 65.2, 36.7 and 44.2; with full rounds,
+    // [49152, 5120], 28.2 and 34.1 there, 29.0 and 36.3 here, [98304, 5120] 56.3 and 66.4, 55.4 and 65.8).
     if (mb <= 32 && mfma_tail_row(di, mb, tiles) == 0)
       return launch_mfma(kFmtMX4, x + m0 * k, mb, p, n, k, y + m0 * n, s, sc);
     const int nt = (mb + 15) / 16;
