@@ -396,6 +396,121 @@ int w12_logprobs(const void *y, int64_t m, int64_t n, int64_t ldy, const void *t
                  void *scratch, uint64_t scratch_bytes, uint32_t flags, void *stream);
 
 /*
+ * The paged key/value cache of a decoding step, and the new tokens of a batch of sequences.
+ *
+ * A cache is pages of `page` token places for each of `heads` key/value heads of `dim` values:
+ * element (p, h, r, c) of page p, head h, place r, column c lies at k (or v) + p * page_stride +
+ * h * head_stride + r * token_stride + c elements, so a head's places may lie side by side
+ * ([pages, heads, page, dim]) or a place's heads ([pages, page, heads, dim]).  Values are bfloat16, or with
+ * W12_KV_E4M3 8-bit floats (OCP e4m3fn) that stand for value * k_scale[h] (v_scale[h]).
+ */
+#define W12_KV_E4M3 0x1u
+typedef struct w12_kv {
+    int64_t pages;        /* 1 .. 2^31 - 1                                      */
+    int64_t heads;        /* key/value heads, at most 2^16                      */
+    int64_t page;         /* token places of a page: a multiple of 16, at most 2^16 */
+    int64_t dim;          /* 64, 128 or 256                                     */
+    void   *k, *v;        /* device, 16-byte aligned                            */
+    int64_t page_stride;  /* in elements, multiples of 16 (8 in bfloat16), not negative; */
+    int64_t head_stride;  /* the same for k and v                               */
+    int64_t token_stride; /* at most 2^24                                       */
+    const float *k_scale; /* [heads], W12_KV_E4M3 only (both NULL: 1)           */
+    const float *v_scale;
+    uint32_t flags;       /* W12_KV_E4M3 or 0                                   */
+} w12_kv;
+
+/*
+ * The new tokens of a step: sequence s has lens[s] places in the cache, the last T_s of them its new
+ * tokens; new token j is row q_start[s] + j of the step's rows, T_s = q_start[s + 1] - q_start[s]
+ * (without q_start: row s, T_s = 1).  Its place is c = lens[s] - T_s + j, on page table[s][c / page].
+ * Rows from q_start[seqs] on (padding) belong to no sequence: nothing is read or written for them.
+ * All arrays are device memory, read when the work runs, so a captured graph takes new lengths and
+ * tables on each replay.  A place outside the table, or on a page outside 0 .. pages - 1, does not exist:
+ * nothing is appended there and nobody sees it.  q_start must not fall; with other values the result is
+ * undefined, but nothing outside the arrays is accessed.
+ */
+typedef struct w12_kv_batch {
+    int64_t seqs;             /* below 2^20                                        */
+    const int32_t *table;     /* [seqs][table_cols], rows table_stride apart       */
+    int64_t table_cols;       /* 1 .. 2^31 / page                                  */
+    int64_t table_stride;
+    const int32_t *lens;      /* [seqs]                                            */
+    const int32_t *q_start;   /* [seqs + 1], or NULL                               */
+    const int32_t *positions; /* [rows] position of the rotation, or NULL: the place */
+    const uint64_t *tree;     /* [rows] masks, or NULL (w12_attention)             */
+} w12_kv_batch;
+
+/*
+ * w12_kv_append -- rotates the new tokens' q and k by position and puts k and v into the cache.
+ * q, k, v: rows of hq, kv->heads and kv->heads heads of kv->dim values, row i at q + i * ldq (k + i *
+ * ldk, v + i * ldv) elements (16-byte aligned, strides multiples of 8, or of 4 in float): bfloat16 bits,
+ * or float with W12_IN_F32 -- the rows of a GEMM over stacked q, k and v records, for instance.
+ * rope: [rope_rows][rot] float, row p the cosines of position p's rot / 2 angles and then their sines
+ * (16-byte aligned; rot a multiple of 16 up to dim; rot = 0: no rotation, rope NULL).  The pair (x_a, x_b)
+ * becomes (x_a cos - x_b sin, x_b cos + x_a sin) in float, a = i, b = i + rot / 2, or with
+ * W12_ROPE_PAIRS a = 2 i, b = 2 i + 1; columns from rot on stay.  Results are rounded once, to nearest
+ * even: q to q_out [m][hq * dim] bfloat16, k and v to the cache's type (e4m3: divided by the scale and
+ * clamped to +-448 first; NaN stays NaN).  q and q_out may be NULL (hq = 0).  A token without a place
+ * in the cache, or with a position outside 0 .. rope_rows - 1, is not appended; the latter's row of
+ * q_out is zero.  Two tokens with one place (a page shared by tables) leave either's values.
+ * q_out must not overlap q, k or v.  Uses no workspace.
+ */
+#define W12_IN_F32     0x100u
+#define W12_ROPE_PAIRS 0x200u
+int w12_kv_append(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                  int64_t m, int64_t hq, const float *rope, int64_t rope_rows, int64_t rot,
+                  const w12_kv *kv, const w12_kv_batch *batch, uint16_t *q_out, uint32_t flags, void *stream);
+
+/*
+ * w12_attention -- attention of the new tokens over the cache: y[i][h] = sum_t p_t v_t with p the
+ * softmax over the places t that row i sees of scale * q[i][h] . k_t, keys and values of head h /
+ * (hq / kv->heads); hq a multiple of kv->heads.  Row i, new token j of its sequence, sees the places
+ * before the new tokens (t < lens - T) and of the new ones those up to its own -- or with batch->tree
+ * those t = lens - T + b, b < min(T, 64), whose bit b its mask tree[i] has (the nodes of a draft tree on its path:
+ * figure-captions page, Fig. 6).  A row that sees nothing, or only scores of -Inf, gives zeros.
+ * Values of places that a row does not see never reach it, NaN and infinities included; a NaN it
+ * sees gives NaN.  q: bfloat16, row i at q + i * ldq elements (16-byte aligned, ldq a multiple of 8); y:
+ * [m][hq * dim] bfloat16 (16-byte aligned), rounded once to nearest even.  Scores, softmax and sums
+ * are held in float, the probabilities that meet v in 16 significant bits.
+ * scratch: w12_attention_scratch bytes of the caller's device memory (16-byte aligned), in use until
+ * the call's work on `stream` is finished.  Its first w12_attention_scratch's *zero bytes are counters
+ * that must be zero when the work starts and are zero again when it ends: clear them once, then reuse
+ * the scratch for calls of any sizes that follow each other on one stream.  Calls with different
+ * scratch never touch each other's.  Which places are summed together depends on the lengths of the
+ * whole batch and the device; equal calls give equal bits.
+ */
+int w12_attention_scratch(int64_t m, int64_t hq, const w12_kv *kv, const w12_kv_batch *batch, uint64_t *bytes,
+                          uint64_t *zero);
+int w12_attention(const uint16_t *q, int64_t ldq, int64_t m, int64_t hq, const w12_kv *kv,
+                  const w12_kv_batch *batch, float scale, uint16_t *y, void *scratch, uint64_t scratch_bytes,
+                  uint32_t flags, void *stream);
+
+/*
+ * w12_sample -- a token for each of m rows of logits, drawn with the caller's random numbers.
+ * y, n, ldy and W12_LOGITS_BF16 as in w12_logprobs.  Per row (each array [m] on the device, or NULL
+ * for the value that switches it off): temperature (NULL: 1), top_k (0 or less: off), top_p (1 or more,
+ * or NaN: off), min_p (0 or less, or NaN: off), and u, the random number in [0, 1).
+ * With x the row, M its largest logit and w_c = e^((x_c - M) / temperature), tokens are ordered by
+ * descending logit, equal ones (-0 equals +0) by the lower column, and kept as follows:
+ *   the first top_k of them, but none of -Inf;
+ *   of those each one that the ones before it do not yet give the mass top_p * (mass of those);
+ *   of those the ones with w >= min_p; the first token of the order always.
+ * token[j] is the first kept column, in column order, at which the mass of the kept columns up to and with
+ * it exceeds u * (mass of all kept) (u below 0 or NaN: as 0; 1 or more: the last kept column of any mass),
+ * logp[j] = ln(w / mass of all kept) its log probability among the kept ones, kept[j] their number
+ * (token or logp or kept may be NULL).  A temperature of 0 or less takes the first token of the order.
+ * A row of -Inf alone gives token -1, logp -Inf and kept 0, one with a NaN or +Inf logit, or a
+ * temperature of NaN, token -1, logp NaN and kept 0.
+ * Weights are computed in double and summed as integers of a step of 2^-62 times the power of two that
+ * reaches n, so sums do not depend on their order.  flags: W12_LOGITS_BF16.
+ * scratch: w12_sample_scratch bytes, its first *zero bytes counters, as in w12_attention (NULL when 0).
+ */
+int w12_sample_scratch(int64_t m, int64_t n, uint32_t flags, uint64_t *bytes, uint64_t *zero);
+int w12_sample(const void *y, int64_t m, int64_t n, int64_t ldy, const float *temperature, const int32_t *top_k,
+               const float *top_p, const float *min_p, const float *u, int32_t *token, float *logp,
+               int32_t *kept, void *scratch, uint64_t scratch_bytes, uint32_t flags, void *stream);
+
+/*
  * w12_bf16_gemm -- same-build dense baseline: y = x * W^T with W bfloat16 in the same tiled
  * storage order as the W12 planes (npad * k values, from w12_bf16_to_tiles), same kernel
  * structure and flags as w12_gemm, 2 bytes per weight.

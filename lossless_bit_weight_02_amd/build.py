@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libw12.so")
 ARCH = "gfx950"
 
 SOURCES = ["codec.hip", "gemv.hip", "stream.hip", "mfma.hip", "mfma_wide.hip", "splitk.hip", "i8copy.hip", "interleave.hip", "noalloc.hip",
-           "mx4.hip", "mx4_gemm.hip", "embed.hip", "logprobs.hip", "api.cpp"]
+           "mx4.hip", "mx4_gemm.hip", "embed.hip", "logprobs.hip", "append.hip", "attention.hip", "sample.hip", "api.cpp"]
 
 # Packed-FP32 instructions are disabled in device code (see the design notes); the host pass
 # reports the feature as unknown, which is harmless.

@@ -742,6 +742,203 @@ int w12_logprobs(const void* y, int64_t m, int64_t n, int64_t ldy, const void* t
   return ok();
 }
 
+namespace {
+// The cache and the batch: what w12.h asks of them, apart from the lengths and tables on the device.
+int check_kv(const w12_kv* kv, const w12_kv_batch* b, int64_t m) {
+  if (!kv || !b) return fail(W12_ERR_ARG, "the cache or the batch is NULL");
+  if (kv->flags & ~W12_KV_E4M3) return fail(W12_ERR_ARG, "unknown flags 0x%x of the cache", kv->flags);
+  if (!kv->k || !kv->v) return fail(W12_ERR_ARG, "k or v of the cache is NULL");
+  if (kv->pages <= 0 || kv->heads <= 0 || kv->page <= 0)
+    return fail(W12_ERR_ARG, "pages, heads and page must be positive (%lld, %lld, %lld)", (long long)kv->pages,
+                (long long)kv->heads, (long long)kv->page);
+  if (kv->pages >= kMaxDim || kv->heads > 65536 || kv->page > 65536)
+    return fail(W12_ERR_RANGE, "pages, heads or page too large (below 2^31, at most 2^16, at most 2^16)");
+  if (kv->dim != 64 && kv->dim != 128 && kv->dim != 256)
+    return fail(W12_ERR_SHAPE, "dim must be 64, 128 or 256 (dim=%lld)", (long long)kv->dim);
+  if (kv->page % 16) return fail(W12_ERR_SHAPE, "page must be a multiple of 16 (page=%lld)", (long long)kv->page);
+  const bool e4m3 = (kv->flags & W12_KV_E4M3) != 0;
+  const int64_t unit = e4m3 ? 16 : 8;
+  if (kv->page_stride < 0 || kv->head_stride < 0 || kv->token_stride < 0)
+    return fail(W12_ERR_ARG, "a stride of the cache is negative");
+  if (kv->page_stride % unit || kv->head_stride % unit || kv->token_stride % unit)
+    return fail(W12_ERR_ALIGN, "the strides of the cache must be multiples of %lld", (long long)unit);
+  if (kv->token_stride > (int64_t(1) << 24) || kv->head_stride > (int64_t(1) << 40) || kv->page_stride > (int64_t(1) << 40))
+    return fail(W12_ERR_RANGE, "a stride of the cache is too large");
+  if (!aligned16(kv->k) || !aligned16(kv->v)) return fail(W12_ERR_ALIGN, "k and v of the cache must be 16-byte aligned");
+  if (!e4m3 && (kv->k_scale || kv->v_scale)) return fail(W12_ERR_ARG, "scales belong to an e4m3 cache");
+  if ((kv->k_scale && !aligned4(kv->k_scale)) || (kv->v_scale && !aligned4(kv->v_scale)))
+    return fail(W12_ERR_ALIGN, "the scales must be 4-byte aligned");
+  if (m <= 0 || b->seqs <= 0) return fail(W12_ERR_ARG, "m and seqs must be positive (m=%lld, seqs=%lld)", (long long)m,
+                                          (long long)b->seqs);
+  if (m >= kMaxDim || b->seqs >= (int64_t(1) << 20)) return fail(W12_ERR_RANGE, "m or seqs too large (below 2^31 and 2^20)");
+  if (!b->table || !b->lens) return fail(W12_ERR_ARG, "table or lens is NULL");
+  if (b->table_cols <= 0) return fail(W12_ERR_ARG, "table_cols must be positive (%lld)", (long long)b->table_cols);
+  if (b->table_cols > kMaxDim / kv->page)
+    return fail(W12_ERR_RANGE, "a table of %lld pages passes 2^31 places", (long long)b->table_cols);
+  if (b->table_stride < b->table_cols && b->seqs > 1)
+    return fail(W12_ERR_ARG, "table_stride=%lld is smaller than table_cols=%lld", (long long)b->table_stride,
+                (long long)b->table_cols);
+  if (b->table_stride > (int64_t(1) << 31)) return fail(W12_ERR_RANGE, "table_stride too large");
+  if (!aligned4(b->table) || !aligned4(b->lens) || (b->q_start && !aligned4(b->q_start)) ||
+      (b->positions && !aligned4(b->positions)) || (reinterpret_cast<uintptr_t>(b->tree) & 7u))
+    return fail(W12_ERR_ALIGN, "table, lens, q_start, positions and tree must be naturally aligned");
+  return W12_OK;
+}
+
+w12::KvArgs kv_of(const w12_kv* kv) {
+  w12::KvArgs r;
+  r.k = kv->k; r.v = kv->v;
+  r.pages = kv->pages; r.heads = kv->heads; r.page = kv->page; r.dim = kv->dim;
+  r.page_stride = kv->page_stride; r.head_stride = kv->head_stride; r.token_stride = kv->token_stride;
+  r.k_scale = kv->k_scale; r.v_scale = kv->v_scale;
+  r.e4m3 = (kv->flags & W12_KV_E4M3) != 0;
+  return r;
+}
+
+w12::BatchArgs batch_of(const w12_kv_batch* b) {
+  w12::BatchArgs r;
+  r.seqs = b->seqs;
+  r.table = b->table; r.cols = b->table_cols; r.table_stride = b->table_stride;
+  r.lens = b->lens; r.q_start = b->q_start; r.positions = b->positions; r.tree = b->tree;
+  return r;
+}
+
+int check_heads(int64_t hq, const w12_kv* kv) {
+  if (hq <= 0 || hq % kv->heads)
+    return fail(W12_ERR_SHAPE, "hq=%lld must be a positive multiple of the cache's %lld heads", (long long)hq,
+                (long long)kv->heads);
+  if (hq > 65536) return fail(W12_ERR_RANGE, "hq too large (at most 2^16)");
+  return W12_OK;
+}
+}  // namespace
+
+int w12_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv, int64_t m,
+                  int64_t hq, const float* rope, int64_t rope_rows, int64_t rot, const w12_kv* kv,
+                  const w12_kv_batch* batch, uint16_t* q_out, uint32_t flags, void* stream) {
+  int rc = check_kv(kv, batch, m);
+  if (rc) return rc;
+  if (flags & ~(W12_IN_F32 | W12_ROPE_PAIRS)) return fail(W12_ERR_ARG, "unknown flags 0x%x", flags);
+  if (hq != 0 && (rc = check_heads(hq, kv))) return rc;
+  if (!k || !v) return fail(W12_ERR_ARG, "k or v is NULL");
+  if (hq > 0 ? !q || !q_out : q || q_out) return fail(W12_ERR_ARG, "q and q_out must be given with hq, and not without");
+  const bool f32 = (flags & W12_IN_F32) != 0;
+  const int64_t unit = f32 ? 4 : 8;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) || !aligned16(rope))
+    return fail(W12_ERR_ALIGN, "q, k, v, q_out and rope must be 16-byte aligned");
+  if (ldk % unit || ldv % unit || (hq > 0 && ldq % unit))
+    return fail(W12_ERR_ALIGN, "the row strides must be multiples of %lld", (long long)unit);
+  if (m > 1 && (ldk < kv->heads * kv->dim || ldv < kv->heads * kv->dim || (hq > 0 && ldq < hq * kv->dim)))
+    return fail(W12_ERR_ARG, "a row stride is smaller than a row (ldq=%lld, ldk=%lld, ldv=%lld)", (long long)ldq,
+                (long long)ldk, (long long)ldv);
+  if (ldq > (int64_t(1) << 31) || ldk > (int64_t(1) << 31) || ldv > (int64_t(1) << 31))
+    return fail(W12_ERR_RANGE, "a row stride is too large");
+  if (rot < 0 || rot > kv->dim || rot % 16)
+    return fail(W12_ERR_SHAPE, "rot must be a multiple of 16 up to dim (rot=%lld)", (long long)rot);
+  if (rot > 0 ? !rope : rope != nullptr) return fail(W12_ERR_ARG, "rope must be given with rot, and not without");
+  if (rot > 0 && (rope_rows <= 0 || rope_rows >= kMaxDim))
+    return fail(W12_ERR_RANGE, "rope_rows must be 1 .. 2^31 - 1 (%lld)", (long long)rope_rows);
+  w12::AppendArgs a;
+  a.q = q; a.k = k; a.v = v;
+  a.ldq = ldq; a.ldk = ldk; a.ldv = ldv; a.m = m; a.hq = hq;
+  a.rope = rope; a.rope_rows = rope_rows; a.rot = rot;
+  a.q_out = q_out; a.f32 = f32; a.pairs = (flags & W12_ROPE_PAIRS) != 0;
+  hipError_t e = w12::launch_kv_append(a, kv_of(kv), batch_of(batch), reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "cache append launch");
+  return ok();
+}
+
+int w12_attention_scratch(int64_t m, int64_t hq, const w12_kv* kv, const w12_kv_batch* batch, uint64_t* bytes,
+                          uint64_t* zero) {
+  if (!bytes || !zero) return fail(W12_ERR_ARG, "bytes or zero is NULL");
+  int rc = check_kv(kv, batch, m);
+  if (rc || (rc = check_heads(hq, kv))) return rc;
+  w12::DevInfo di;
+  hipError_t e = w12::dev_info(&di);
+  if (e != hipSuccess) return hip_fail(e, "device query");
+  *bytes = w12::attention_scratch(di, m, hq, kv_of(kv), batch_of(batch), zero);
+  return ok();
+}
+
+int w12_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t hq, const w12_kv* kv, const w12_kv_batch* batch,
+                  float scale, uint16_t* y, void* scratch, uint64_t scratch_bytes, uint32_t flags, void* stream) {
+  int rc = check_kv(kv, batch, m);
+  if (rc || (rc = check_heads(hq, kv))) return rc;
+  if (flags != 0) return fail(W12_ERR_ARG, "unknown flags 0x%x", flags);
+  if (!q || !y) return fail(W12_ERR_ARG, "q or y is NULL");
+  if (!aligned16(q) || !aligned16(y)) return fail(W12_ERR_ALIGN, "q and y must be 16-byte aligned");
+  if (ldq % 8) return fail(W12_ERR_ALIGN, "ldq must be a multiple of 8 (ldq=%lld)", (long long)ldq);
+  if (m > 1 && ldq < hq * kv->dim) return fail(W12_ERR_ARG, "ldq=%lld is smaller than a row", (long long)ldq);
+  if (ldq > (int64_t(1) << 31)) return fail(W12_ERR_RANGE, "ldq too large");
+  w12::DevInfo di;
+  hipError_t e = w12::dev_info(&di);
+  if (e != hipSuccess) return hip_fail(e, "device query");
+  uint64_t zero = 0;
+  const uint64_t need = w12::attention_scratch(di, m, hq, kv_of(kv), batch_of(batch), &zero);
+  if (need > 0) {
+    if (!scratch || scratch_bytes < need)
+      return fail(W12_ERR_CAPACITY, "scratch of %llu bytes is needed (%llu given)", (unsigned long long)need,
+                  scratch ? (unsigned long long)scratch_bytes : 0ull);
+    if (!aligned16(scratch)) return fail(W12_ERR_ALIGN, "scratch must be 16-byte aligned");
+  }
+  e = w12::launch_attention(q, ldq, m, hq, kv_of(kv), batch_of(batch), scale, y, scratch,
+                            reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "attention launch");
+  return ok();
+}
+
+namespace {
+int check_sample(int64_t m, int64_t n, uint32_t flags) {
+  if (m <= 0 || n <= 0) return fail(W12_ERR_ARG, "m and n must be positive (m=%lld, n=%lld)", (long long)m, (long long)n);
+  if (m >= kMaxDim || n >= kMaxDim) return fail(W12_ERR_RANGE, "m or n too large");
+  if (flags & ~W12_LOGITS_BF16) return fail(W12_ERR_ARG, "unknown flags 0x%x", flags);
+  return W12_OK;
+}
+}  // namespace
+
+int w12_sample_scratch(int64_t m, int64_t n, uint32_t flags, uint64_t* bytes, uint64_t* zero) {
+  if (!bytes || !zero) return fail(W12_ERR_ARG, "bytes or zero is NULL");
+  int rc = check_sample(m, n, flags);
+  if (rc) return rc;
+  w12::DevInfo di;
+  hipError_t e = w12::dev_info(&di);
+  if (e != hipSuccess) return hip_fail(e, "device query");
+  *bytes = w12::sample_scratch(di, m, n, (flags & W12_LOGITS_BF16) != 0, zero);
+  return ok();
+}
+
+int w12_sample(const void* y, int64_t m, int64_t n, int64_t ldy, const float* temperature, const int32_t* top_k,
+               const float* top_p, const float* min_p, const float* u, int32_t* token, float* logp, int32_t* kept,
+               void* scratch, uint64_t scratch_bytes, uint32_t flags, void* stream) {
+  int rc = check_sample(m, n, flags);
+  if (rc) return rc;
+  if (!y || !u) return fail(W12_ERR_ARG, "y or u is NULL");
+  if (ldy < n) return fail(W12_ERR_ARG, "ldy=%lld is smaller than n=%lld", (long long)ldy, (long long)n);
+  if (ldy > (int64_t(1) << 40)) return fail(W12_ERR_RANGE, "ldy too large");
+  const bool bf = (flags & W12_LOGITS_BF16) != 0;
+  if (reinterpret_cast<uintptr_t>(y) & (bf ? 1u : 3u)) return fail(W12_ERR_ALIGN, "y must be naturally aligned");
+  if (!aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) || !aligned4(min_p) || !aligned4(u) ||
+      !aligned4(token) || !aligned4(logp) || !aligned4(kept))
+    return fail(W12_ERR_ALIGN, "the parameters and outputs must be 4-byte aligned");
+  w12::DevInfo di;
+  hipError_t e = w12::dev_info(&di);
+  if (e != hipSuccess) return hip_fail(e, "device query");
+  uint64_t zero = 0;
+  const uint64_t need = w12::sample_scratch(di, m, n, bf, &zero);
+  if (need > 0) {
+    if (!scratch || scratch_bytes < need)
+      return fail(W12_ERR_CAPACITY, "scratch of %llu bytes is needed (%llu given)", (unsigned long long)need,
+                  scratch ? (unsigned long long)scratch_bytes : 0ull);
+    if (!aligned16(scratch)) return fail(W12_ERR_ALIGN, "scratch must be 16-byte aligned");
+  }
+  w12::SampleArgs a;
+  a.y = y; a.m = m; a.n = n; a.ldy = ldy;
+  a.temperature = temperature; a.top_k = top_k; a.top_p = top_p; a.min_p = min_p; a.u = u;
+  a.token = token; a.logp = logp; a.kept = kept;
+  e = w12::launch_sample(a, bf, scratch, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "sampling launch");
+  return ok();
+}
+
 int w12_bf16_gemm(const uint16_t* x, int64_t m, const uint16_t* w, int64_t n, int64_t k, float* y,
                   uint32_t flags, void* stream) {
   if (!w) return fail(W12_ERR_ARG, "w is NULL");

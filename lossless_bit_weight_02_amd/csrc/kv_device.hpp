@@ -1,0 +1,68 @@
+// The paged cache and the batch of new tokens as the kernels see them (w12_kv, w12_kv_batch of
+// w12.h), and a row's way from its number to its place.
+#pragma once
+
+#include "w12_device.hpp"
+#include "w12_launch.hpp"
+
+namespace w12 {
+
+// Inclusive sum over the wave's lanes up to each, by DPP.
+__device__ __forceinline__ int lane_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15, 31
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
+// A sequence's rows and lengths.
+struct SeqRows {
+  int64_t first;      // its first new token's row
+  int64_t count;      // T, 0 for an empty or senseless one
+  int64_t len;        // places it has, new ones included
+};
+
+__device__ __forceinline__ SeqRows seq_rows(const BatchArgs& b, int64_t s, int64_t m) {
+  SeqRows r;
+  r.len = b.lens[s];
+  if (b.q_start == nullptr) {
+    r.first = s;
+    r.count = s < m ? 1 : 0;
+    return r;
+  }
+  r.first = b.q_start[s];
+  int64_t end = b.q_start[s + 1];
+  if (end > m) end = m;
+  r.count = r.first >= 0 && end > r.first ? end - r.first : 0;
+  return r;
+}
+
+// The sequence that row i belongs to, -1 for none: the last s with q_start[s] <= i, by all lanes of a
+// wave at once, a 64th of the range each step.  Every index stays in 0 .. seqs whatever the values.
+__device__ __forceinline__ int64_t find_seq(const BatchArgs& b, int64_t i) {
+  if (b.q_start == nullptr) return i < b.seqs ? i : -1;
+  const int lane = threadIdx.x & 63;
+  int64_t cur = 0, len = b.seqs + 1;
+  while (len > 1) {
+    const int64_t step = (len + 63) / 64;
+    const int64_t at = lane * step;
+    const uint64_t bl = __ballot(at < len && b.q_start[cur + (at < len ? at : 0)] <= i);
+    if (bl == 0) return -1;
+    const int64_t last = (__popcll(bl) - 1) * step;
+    cur += last;
+    len = len - last < step ? len - last : step;
+  }
+  return cur < b.seqs ? cur : -1;
+}
+
+// The page that holds place c of sequence s, -1 where the place does not exist.
+__device__ __forceinline__ int64_t page_of(const KvArgs& kv, const BatchArgs& b, int64_t s, int64_t c) {
+  if (c < 0 || c >= b.cols * kv.page) return -1;
+  const int32_t p = b.table[s * b.table_stride + (uint32_t)c / (uint32_t)kv.page];
+  return p >= 0 && p < kv.pages ? p : -1;
+}
+
+}  // namespace w12

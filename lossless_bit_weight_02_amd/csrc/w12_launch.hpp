@@ -158,6 +158,50 @@ uint64_t logprobs_scratch(const DevInfo& di, int64_t m, int64_t n, int top);
 hipError_t launch_logprobs(const void* y, bool bf, int64_t m, int64_t n, int64_t ldy, const void* tokens,
                            bool tok64, int nt, int top, float* logp, float* ent, int32_t* tidx,
                            float* tlogp, void* scratch, hipStream_t s);
+// ---- the decoding step between the products (w12_kv, w12_kv_batch of w12.h) ----
+struct KvArgs {
+  void *k, *v;
+  int64_t pages, heads, page, dim;
+  int64_t page_stride, head_stride, token_stride;   // elements
+  const float *k_scale, *v_scale;                   // per head, NULL: 1
+  bool e4m3;
+};
+struct BatchArgs {
+  int64_t seqs;
+  const int32_t* table;
+  int64_t cols, table_stride;
+  const int32_t *lens, *q_start, *positions;
+  const uint64_t* tree;
+};
+// q and k rotated, k and v into the cache; q_out [m][hq dim] (w12_kv_append)
+struct AppendArgs {
+  const void *q, *k, *v;
+  int64_t ldq, ldk, ldv, m, hq;
+  const float* rope;
+  int64_t rope_rows, rot;
+  uint16_t* q_out;
+  bool f32, pairs;
+};
+hipError_t launch_kv_append(const AppendArgs& a, const KvArgs& kv, const BatchArgs& b, hipStream_t s);
+// attention of the new tokens over the cache (w12_attention); scratch: attention_scratch bytes, the first
+// *zero of them counters
+uint64_t attention_scratch(const DevInfo& di, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b,
+                           uint64_t* zero);
+hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t hq, const KvArgs& kv,
+                            const BatchArgs& b, float scale, uint16_t* y, void* scratch, hipStream_t s);
+// a token per row of logits (w12_sample); scratch: sample_scratch bytes, the first *zero of them counters
+struct SampleArgs {
+  const void* y;
+  int64_t m, n, ldy;
+  const float* temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p, *u;
+  int32_t* token;
+  float* logp;
+  int32_t* kept;
+};
+uint64_t sample_scratch(const DevInfo& di, int64_t m, int64_t n, bool bf, uint64_t* zero);
+hipError_t launch_sample(const SampleArgs& a, bool bf, void* scratch, hipStream_t s);
 // dense bf16 [n][k] -> tiled storage order (baseline layout)
 hipError_t launch_bf16_tile(const uint16_t* w, int64_t n, int64_t k, uint16_t* out, hipStream_t s);
 // bandwidth probe

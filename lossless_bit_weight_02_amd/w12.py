@@ -30,6 +30,9 @@ Q8_MIDPOINT = 0x10
 OUT_BF16 = 0x20
 IDS_I64 = 0x40
 LOGITS_BF16 = 0x80
+IN_F32 = 0x100
+ROPE_PAIRS = 0x200
+KV_E4M3 = 0x1
 _PATHS = {None: PATH_AUTO, "auto": PATH_AUTO, "gemv": PATH_GEMV, "mfma": PATH_MFMA, "stream": PATH_STREAM}
 
 
@@ -55,6 +58,20 @@ class _W12MX4(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("q", ctypes.c_void_p),
                 ("nz_ptr", ctypes.c_void_p), ("nz_end", ctypes.c_void_p), ("nz_col", ctypes.c_void_p),
                 ("nz_val", ctypes.c_void_p), ("nz_cap", ctypes.c_uint64)]
+
+
+class _W12KV(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int64), ("heads", ctypes.c_int64), ("page", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("flags", ctypes.c_uint32)]
+
+
+class _W12KVBatch(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int64), ("table", ctypes.c_void_p), ("table_cols", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("tree", ctypes.c_void_p)]
 
 
 _lib = None
@@ -110,6 +127,24 @@ EXPORTS = {
                                     ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                     ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p]),
+    "w12_kv_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                     ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                     ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(_W12KV),
+                                     ctypes.POINTER(_W12KVBatch), ctypes.c_void_p, ctypes.c_uint32,
+                                     ctypes.c_void_p]),
+    "w12_attention_scratch": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(_W12KV),
+                                             ctypes.POINTER(_W12KVBatch), ctypes.POINTER(ctypes.c_uint64),
+                                             ctypes.POINTER(ctypes.c_uint64)]),
+    "w12_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                     ctypes.POINTER(_W12KV), ctypes.POINTER(_W12KVBatch), ctypes.c_float,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32,
+                                     ctypes.c_void_p]),
+    "w12_sample_scratch": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_uint32,
+                                          ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)]),
+    "w12_sample": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p]),
     "w12_bf16_gemm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                      ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                      ctypes.c_uint32, ctypes.c_void_p]),
@@ -688,6 +723,288 @@ def logprobs(y: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0) 
     return r
 
 
+class KVCache:
+    """A paged key/value cache: k and v [pages, heads, page, dim], bfloat16 or float8_e4m3fn (then standing
+    for value * scale of the head, k_scale and v_scale float32 [heads]), with equal strides, columns
+    contiguous.  The memory order of pages, heads and places is free (a transposed [pages, page, heads, dim]
+    tensor will do).  page is a multiple of 16, dim 64, 128 or 256."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        for t, what in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor) or t.dim() != 4 or not t.is_cuda:
+                raise ValueError(f"{what} must be a 4-D CUDA tensor [pages, heads, page, dim]")
+            if t.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+                raise TypeError(f"{what} must be bfloat16 or float8_e4m3fn, got {t.dtype}")
+            if t.stride(3) != 1:
+                raise ValueError(f"the columns of {what} must be contiguous")
+        if k.dtype != v.dtype or k.shape != v.shape or k.stride() != v.stride() or k.device != v.device:
+            raise ValueError("k and v differ in type, shape, strides or device")
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None:
+                continue
+            if not e4m3:
+                raise ValueError(f"{what} belongs to a float8_e4m3fn cache")
+            if t.dtype != torch.float32:
+                raise TypeError(f"{what} must be float32, got {t.dtype}")
+            if t.shape != (k.shape[1],) or not t.is_contiguous() or t.device != k.device:
+                raise ValueError(f"{what} must be contiguous [{k.shape[1]}] on {k.device}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.page, self.dim = k.shape
+        self.device = k.device
+        # (in sizes of 1 a stride says nothing, and torch lets it be anything)
+        st = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
+        self._c = _W12KV(self.pages, self.heads, self.page, self.dim, k.data_ptr(), v.data_ptr(), *st,
+                         _ptr(k_scale), _ptr(v_scale), KV_E4M3 if e4m3 else 0)
+        self._ref = ctypes.byref(self._c)
+
+    def nbytes(self) -> int:
+        return 2 * self.k.numel() * self.k.element_size()
+
+
+def kv_cache(pages: int, heads: int, dim: int, page: int = 64, dtype: torch.dtype = torch.bfloat16, k_scale=None,
+             v_scale=None, device="cuda") -> KVCache:
+    """A zeroed cache, a page's places of one head side by side."""
+    k, v = (torch.zeros((pages, heads, page, dim), dtype=dtype, device=device) for _ in range(2))
+    return KVCache(k, v, k_scale, v_scale)
+
+
+class KVBatch:
+    """The new tokens of a step, for every layer's kv_append and attention.  Sequence s has lens[s] places in
+    the cache, the last q_start[s + 1] - q_start[s] of them (without q_start: one) its new tokens, rows
+    q_start[s] .. of the step; place c is on page table[s, c // page].  All int32 on the device and read when
+    the work runs: table [seqs, pages of the longest], lens [seqs], q_start [seqs + 1], positions
+    [rows] for the rotation (default: the place).  tree int64 [rows]: bit b of a row's mask lets it see its
+    sequence's b-th new token (default: those up to its own)."""
+
+    def __init__(self, table, lens, q_start=None, positions=None, tree=None):
+        i32 = torch.int32
+        if not isinstance(table, torch.Tensor) or table.dim() != 2 or not table.is_cuda:
+            raise ValueError("table must be a 2-D CUDA tensor")
+        if table.shape[0] == 0 or table.shape[1] == 0:
+            raise ValueError("table is empty")
+        seqs = table.shape[0]
+        for t, what, dt, n in ((table, "table", i32, None), (lens, "lens", i32, seqs),
+                               (q_start, "q_start", i32, seqs + 1), (positions, "positions", i32, None),
+                               (tree, "tree", torch.int64, None)):
+            if t is None and what != "lens":
+                continue
+            if not isinstance(t, torch.Tensor) or t.dtype != dt:
+                raise TypeError(f"{what} must be a tensor of {dt}")
+            if t.device != table.device:
+                raise ValueError(f"{what} is on {t.device}, expected {table.device}")
+            if t is not table and (t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n)):
+                raise ValueError(f"{what} must be contiguous [{'rows' if n is None else n}]")
+        if table.stride(1) != 1 and table.shape[1] > 1 or table.stride(0) < table.shape[1] and seqs > 1:
+            raise ValueError("the rows of table must be contiguous and apart")
+        self.table, self.lens, self.q_start, self.positions, self.tree = table, lens, q_start, positions, tree
+        self.seqs = seqs
+        self.device = table.device
+        self._c = _W12KVBatch(seqs, table.data_ptr(), table.shape[1], table.stride(0) if seqs > 1 else table.shape[1],
+                              lens.data_ptr(), _ptr(q_start), _ptr(positions), _ptr(tree))
+        self._ref = ctypes.byref(self._c)
+        self._sizes = {}        # scratch of attention calls
+
+    def _rows(self, m: int):
+        if self.q_start is None and m != self.seqs:
+            raise ValueError(f"{m} rows for {self.seqs} sequences of one new token each")
+        for t, what in ((self.positions, "positions"), (self.tree, "tree")):
+            if t is not None and t.shape[0] != m:
+                raise ValueError(f"{what} has {t.shape[0]} entries for {m} rows")
+
+
+def _check_step(kv: KVCache, batch: KVBatch):
+    if kv.device != batch.device:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {kv.device}")
+
+
+def _step_rows(t, m, cols, device, what):
+    """(pointer, row stride) of rows of `cols` values whose columns are contiguous."""
+    if t.dim() != 2 or t.shape[1] != cols or (m is not None and t.shape[0] != m):
+        raise ValueError(f"{what} must be [{'rows' if m is None else m}, {cols}], got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
+    if t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < cols:
+        raise ValueError(f"the rows of {what} must be contiguous and apart")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
+
+
+def kv_append(qkv, kv: KVCache, batch: KVBatch, rope: torch.Tensor | None = None, interleaved: bool = False,
+              out: torch.Tensor | None = None):
+    """Rotates the new tokens' q and k by position and puts k and v into the cache; returns the rotated q
+    [m, hq * dim] bfloat16.  qkv: the stacked product's rows [m, (hq + 2 heads) * dim], bfloat16 or
+    float32, or a tuple of q, k and v rows (q None: only k and v, returns None).  rope float32 [positions,
+    rot]: the cosines of a position's rot / 2 angles, then their sines; pairs are (i, i + rot / 2), or
+    (2 i, 2 i + 1) with ``interleaved``.  A token without a place in the cache, or with a position outside
+    the table, is not appended (the latter's q is zero); rows behind the last sequence are left alone."""
+    _check_step(kv, batch)
+    dev, dim, heads = kv.device, kv.dim, kv.heads
+    if isinstance(qkv, torch.Tensor):
+        if qkv.dim() != 2 or qkv.shape[1] % dim or qkv.shape[1] // dim <= 2 * heads:
+            raise ValueError(f"qkv must be [rows, (hq + {2 * heads}) * {dim}], got {tuple(qkv.shape)}")
+        m, hq = qkv.shape[0], qkv.shape[1] // dim - 2 * heads
+        dt = qkv.dtype
+        k, ldk = _step_rows(qkv, m, qkv.shape[1], dev, "qkv")
+        q, ldq = k, ldk
+        k += hq * dim * qkv.element_size()
+        v, ldv = k + heads * dim * qkv.element_size(), ldk
+    else:
+        tq, tk, tv = qkv
+        m, dt = tk.shape[0], tk.dtype
+        if tv.dtype != dt or tq is not None and tq.dtype != dt:
+            raise TypeError("q, k and v differ in type")
+        k, ldk = _step_rows(tk, m, heads * dim, dev, "k")
+        v, ldv = _step_rows(tv, m, heads * dim, dev, "v")
+        q, ldq, hq = None, 0, 0
+        if tq is not None:
+            if tq.dim() != 2 or tq.shape[1] % dim or tq.shape[1] == 0:
+                raise ValueError(f"q must be [rows, hq * {dim}], got {tuple(tq.shape)}")
+            hq = tq.shape[1] // dim
+            q, ldq = _step_rows(tq, m, hq * dim, dev, "q")
+    if dt not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"q, k and v must be bfloat16 or float32, got {dt}")
+    batch._rows(m)
+    rows = rot = 0
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous() or rope.device != dev:
+            raise ValueError(f"rope must be contiguous float32 [positions, rot] on {dev}")
+        rows, rot = rope.shape
+    if out is not None:
+        if hq == 0:
+            raise ValueError("out without q")
+        _check_out(out, (m, hq * dim), (torch.bfloat16,), dev)
+    elif hq:
+        out = batch.lens.new_empty((m, hq * dim), dtype=torch.bfloat16)
+    if m == 0:
+        return out
+    flags = (IN_F32 if dt == torch.float32 else 0) | (ROPE_PAIRS if interleaved else 0)
+    with _on_device(dev):
+        _check(lib().w12_kv_append(q, ldq, k, ldk, v, ldv, m, hq, _ptr(rope), rows, rot, kv._ref, batch._ref,
+                                   _ptr(out), flags, _stream_handle(dev)))
+    return out
+
+
+_step_buffers: dict = {}   # (operator, device, stream) -> scratch of the stream's calls
+
+
+def _step_scratch(what, need, zero, device, stream):
+    """Scratch of an attention or sample call on `stream`, kept for the stream's next one until
+    release_workspace; a call under graph capture gets its own, its counters cleared by the graph, since
+    graphs may be replayed on any stream."""
+    if torch.cuda.is_current_stream_capturing():
+        buf = torch.empty(need, dtype=torch.uint8, device=device)
+        buf[:zero].zero_()
+        return buf
+    buf = _step_buffers.get((what, device.index, stream))
+    if buf is None or buf.numel() < need:
+        buf = torch.empty(max(need, 1 << 18), dtype=torch.uint8, device=device)
+        buf[:zero].zero_()
+        _step_buffers[(what, device.index, stream)] = buf
+    return buf
+
+
+def attention(q: torch.Tensor, kv: KVCache, batch: KVBatch, scale: float | None = None,
+              out: torch.Tensor | None = None):
+    """Attention of the new tokens over the cache: q [m, hq * dim] bfloat16 (kv_append's result), hq a
+    multiple of the cache's heads; returns [m, hq * dim] bfloat16, the output projection's x.  A row sees
+    its sequence's places before the new tokens and the new ones up to its own (or those of its tree mask).
+    scale: of the scores, default 1 / sqrt(dim).  A row that sees nothing gives zeros; rows behind the last
+    sequence are left alone.  Keeps a scratch buffer per stream; release_workspace frees it."""
+    _check_step(kv, batch)
+    dev, dim = kv.device, kv.dim
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be bfloat16, got {q.dtype}")
+    if q.dim() != 2 or q.shape[1] == 0 or q.shape[1] % (dim * kv.heads):
+        raise ValueError(f"q must be [rows, hq * {dim}] with hq a multiple of {kv.heads}, got {tuple(q.shape)}")
+    m, hq = q.shape[0], q.shape[1] // dim
+    qp, ldq = _step_rows(q, m, hq * dim, dev, "q")
+    batch._rows(m)
+    if out is None:
+        out = q.new_empty((m, hq * dim))
+    else:
+        _check_out(out, (m, hq * dim), (torch.bfloat16,), dev)
+    if m == 0:
+        return out
+    L = lib()
+    with _on_device(dev):
+        stream = _stream_handle(dev)
+        key = (m, hq, kv.heads, dim, kv.page, kv.k.dtype)
+        size = batch._sizes.get(key)
+        if size is None:
+            n, z = ctypes.c_uint64(0), ctypes.c_uint64(0)
+            _check(L.w12_attention_scratch(m, hq, kv._ref, batch._ref, ctypes.byref(n), ctypes.byref(z)))
+            size = batch._sizes[key] = (n.value, z.value)
+        need, zero = size
+        buf = _step_scratch("attention", need, zero, dev, stream) if need else None
+        _check(L.w12_attention(qp, ldq, m, hq, kv._ref, batch._ref, dim ** -0.5 if scale is None else float(scale),
+                               out.data_ptr(), _ptr(buf), need, 0, stream))
+    return out
+
+
+class Samples(NamedTuple):
+    """Result of sample: ``token`` int32 [m], ``logp`` float32 [m] among the kept tokens, ``kept`` int32 [m]."""
+    token: torch.Tensor
+    logp: torch.Tensor
+    kept: torch.Tensor
+
+
+_sample_sizes: dict = {}   # (device, m, n, flags) -> (bytes, counter bytes)
+
+
+def sample(y: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = None,
+           top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+           min_p: torch.Tensor | None = None) -> Samples:
+    """A token per row of logits y [m, n] (float32 or bfloat16, rows at any stride) from the uniform numbers
+    u float32 [m].  Per row, each [m] or None: temperature float32 (0 or less: the largest logit), top_k
+    int32 (0: off), top_p and min_p float32.  top_k comes first, then the shortest run of what it leaves
+    with top_p of its mass, then those of at least min_p times the best one's probability; the token is the
+    first in column order at which the kept mass passes u of it.  Equal logits go by the lower index.  A row
+    of -Inf alone gives -1, log probability -Inf and 0 kept, one with NaN or +Inf -1, NaN and 0.  Calls
+    may keep a scratch buffer per stream; release_workspace frees it."""
+    if not isinstance(y, torch.Tensor) or y.dim() != 2 or not y.is_cuda:
+        raise ValueError("y must be a 2-D CUDA tensor")
+    if y.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"y must be float32 or bfloat16, got {y.dtype}")
+    m, n = y.shape
+    dev = y.device
+    if u is None:
+        raise TypeError("u must be a tensor of torch.float32")
+    for t, what, dt in ((u, "u", torch.float32), (temperature, "temperature", torch.float32),
+                        (top_k, "top_k", torch.int32), (top_p, "top_p", torch.float32), (min_p, "min_p", torch.float32)):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != dt:
+            raise TypeError(f"{what} must be a tensor of {dt}")
+        if t.shape != (m,) or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous [{m}] on {dev}")
+    if n > 0 and (y.stride(1) != 1 and n > 1 or y.stride(0) < n and m > 1):
+        y = y.contiguous()
+    r = Samples(y.new_empty(m, dtype=torch.int32), y.new_empty(m, dtype=torch.float32),
+                y.new_empty(m, dtype=torch.int32))
+    if m == 0:
+        return r
+    if n == 0:
+        raise ValueError("y has no columns")
+    flags = LOGITS_BF16 if y.dtype == torch.bfloat16 else 0
+    L = lib()
+    with _on_device(dev):
+        stream = _stream_handle(dev)
+        key = (dev.index, m, n, flags)
+        size = _sample_sizes.get(key)
+        if size is None:
+            nb, z = ctypes.c_uint64(0), ctypes.c_uint64(0)
+            _check(L.w12_sample_scratch(m, n, flags, ctypes.byref(nb), ctypes.byref(z)))
+            if len(_sample_sizes) > 4096:
+                _sample_sizes.clear()
+            size = _sample_sizes[key] = (nb.value, z.value)
+        need, zero = size
+        buf = _step_scratch("sample", need, zero, dev, stream) if need else None
+        _check(L.w12_sample(y.data_ptr(), m, n, y.stride(0) if m > 1 else n, _ptr(temperature), _ptr(top_k),
+                            _ptr(top_p), _ptr(min_p), u.data_ptr(), r.token.data_ptr(), r.logp.data_ptr(),
+                            r.kept.data_ptr(), _ptr(buf), need, flags, stream))
+    return r
+
+
 class Bf16Tiles:
     """Dense bfloat16 W in the tiled storage order of the baseline kernels."""
 
@@ -730,14 +1047,16 @@ def read_probe(buf: torch.Tensor, sink: torch.Tensor | None = None):
 
 def release_workspace(stream: "torch.cuda.Stream | None" = None, device=None):
     """Free what calls on ``stream`` (default: the current stream of ``device``) have left allocated for
-    the next ones: the library's GEMM workspace and the scratch of logprobs; waits for the stream's
-    work first.  A later call on the stream allocates anew.  To be called before a stream that either
+    the next ones: the library's GEMM workspace and the scratch of logprobs, attention and sample; waits for
+    the stream's work first.  A later call on the stream allocates anew.  To be called before a stream that either
     ran on is destroyed: a new stream may get its handle."""
     if stream is None:
         stream = torch.cuda.current_stream(device)
     with torch.cuda.device(stream.device):
         _check(lib().w12_release_workspace(stream.cuda_stream))
     key = (stream.device.index, stream.cuda_stream)
-    if key in _lp_buffers:
+    held = [d for d in ((_lp_buffers, key), *((_step_buffers, (w, *key)) for w in ("attention", "sample"))) if d[1] in d[0]]
+    if held:
         stream.synchronize()
-        _lp_buffers.pop(key, None)
+        for bufs, k in held:
+            bufs.pop(k, None)

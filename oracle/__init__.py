@@ -22,3 +22,4 @@ from .w12 import (  # noqa: F401
 )
 from .vocab import embed_bits, logprobs64, logprobs_tol  # noqa: F401
 from .mx4 import E2M1, MX4_BLOCK, Mx4Copy, e2m1_code, mx4_copy, mx4_to_storage, mx4_weights64  # noqa: F401
+from .step import append64, attention64, new_tokens, page_of, rotate64, sample64  # noqa: F401

@@ -1,0 +1,551 @@
+"""Cache append with rotation, attention over the paged cache and sampling against the float64 oracle.
+
+Tolerances.  u = 2^-24 is half a float step, h = 2^-8 half a bfloat16 step, both relative.
+  append: two products and a sum in float, 3 u (|a cos| + |b sin|) <= 4 u (|a| + |b|), then one rounding:
+    h |x| for bfloat16, for e4m3 after the division (u more) 2^-4 |x|, or half its smallest step, 2^-10;
+    a float error may move a value over a border between two roundings, so both add up.
+  attention: a score is a sum of dim products and a few scalings, off by (dim + 8) u sum |q k| scale; a
+    probability by twice that and the exponential's own 4 u, and 2^-16 from its 16 bits; the output is
+    a sum over len terms (len + 8) u, all times sum p |v|; then the rounding h |y|.
+  sampling: integers exact; a log probability to u of itself and of the largest term it is the difference of.
+"""
+import numpy as np
+import pytest
+
+import oracle
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U, H = 2.0 ** -24, 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def w12():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from lossless_bit_weight_02_amd import w12 as mod
+    mod.lib()
+    return mod
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+class Step:
+    """A cache of random values, its tables, and the batch."""
+
+    def __init__(self, w12, lens, news=None, heads=2, dim=128, page=16, e4m3=False, nhd=False, tree=None, pad=0, seed=0,
+                 positions=None, spare=3, scales=True):
+        g = torch.Generator().manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        need = [(max(n, 0) + page - 1) // page for n in lens]
+        self.pages = sum(need) + spare
+        cols = max(max(need), 1)
+        ids = rng.permutation(self.pages)
+        self.table = np.full((len(lens), cols), -1, np.int32)
+        at = 0
+        for s, n in enumerate(need):
+            self.table[s, :n] = ids[at:at + n]
+            at += n
+        self.used = np.sort(ids[:at])
+        self.lens, self.page, self.heads, self.dim = np.array(lens, np.int32), page, heads, dim
+        self.start = None if news is None else np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+        self.rows = (len(lens) if news is None else int(self.start[-1])) + pad
+        shape = (self.pages, page, heads, dim) if nhd else (self.pages, heads, page, dim)
+        self.sc = (None, None)
+        kv = []
+        for i in range(2):
+            x = torch.randn(shape, generator=g)
+            if e4m3:
+                x = (x * 60).clamp(-448, 448).to(torch.float8_e4m3fn)
+            else:
+                x = x.to(torch.bfloat16)
+            x = x.cuda()
+            kv.append(x.transpose(1, 2) if nhd else x)
+        if e4m3 and scales:
+            self.sc = tuple((0.01 + 0.02 * torch.rand(heads, generator=g)).cuda() for _ in range(2))
+        self.k, self.v = kv
+        self.tree = tree
+        self.positions = positions
+        self.w12 = w12
+        self.make()
+
+    def make(self):
+        dev = lambda a, t: None if a is None else torch.tensor(np.asarray(a), dtype=t).cuda()  # noqa: E731
+        self.kv = self.w12.KVCache(self.k, self.v, *self.sc)
+        self.batch = self.w12.KVBatch(dev(self.table, torch.int32), dev(self.lens, torch.int32),
+                                      q_start=dev(self.start, torch.int32), positions=dev(self.positions, torch.int32),
+                                      tree=dev(self.tree, torch.int64))
+
+    def values(self, i):
+        """The cache's k (0) or v (1) as float64 [pages, heads, page, dim]."""
+        x = f64((self.k, self.v)[i].float())
+        return x if self.sc[i] is None else x * f64(self.sc[i])[None, :, None, None]
+
+
+def rope_table(n, rot):
+    f = 10000.0 ** (-np.arange(rot // 2) / max(rot // 2, 1))
+    a = np.arange(n)[:, None] * f
+    return np.concatenate([np.cos(a), np.sin(a)], 1).astype(np.float32)
+
+
+def e4m3_ok(got, want, err):
+    """Whether e4m3 values (as float64) are within half a step of want's, err beside."""
+    return np.abs(got - want) <= err + np.maximum(2.0 ** -4 * np.abs(want), 2.0 ** -10)
+
+
+def check_append(st, qkv, hq, rope, pairs, got, before, m):
+    x = f64(qkv).reshape(m, -1, st.dim)
+    heads = st.heads
+    q, k, v = x[:, :hq], x[:, hq:hq + heads], x[:, hq + heads:]
+    out, put = oracle.append64(q, k, v, rope, pairs, st.table, st.lens, st.start, st.positions, st.page, st.pages)
+    mag = lambda z: 4 * U * 2 * np.abs(z).max(axis=-1, keepdims=True)  # noqa: E731
+    if got is not None:
+        g = f64(got).reshape(m, hq, st.dim)
+        mine = ~np.isnan(out)
+        err = np.abs(g - out)
+        assert np.all((err <= H * np.abs(out) + mag(q))[mine])
+        assert np.all(g[~mine] == 7.0)                       # rows behind the last sequence
+    for i, (c, b) in enumerate(zip((st.k, st.v), before)):
+        c, b = f64(c.float()), f64(b.float())
+        for (p, r), kv in put.items():
+            want = kv[i]
+            if st.k.dtype == torch.float8_e4m3fn:
+                sc = np.ones(heads) if st.sc[i] is None else f64(st.sc[i])
+                w = np.clip(want / sc[:, None], -448, 448)
+                e = (mag(want) + 2 * U * np.abs(want)) / sc[:, None]
+                assert np.all(e4m3_ok(c[p, :, r], w, e)), (p, r)
+            else:
+                assert np.all(np.abs(c[p, :, r] - want) <= H * np.abs(want) + (mag(want) if i == 0 else 0)), (p, r)
+            c[p, :, r] = b[p, :, r]
+        assert np.array_equal(c, b, equal_nan=True)          # nothing else was touched
+
+
+APPEND = [
+    # lens, news, heads, hq, dim, page, e4m3, nhd, f32, rot, pairs
+    ([5], None, 1, 1, 64, 16, False, False, False, 64, False),
+    ([700, 1, 33], None, 8, 48, 128, 64, False, False, False, 128, False),
+    ([17, 16, 15, 100], [3, 1, 15, 40], 2, 6, 128, 16, False, True, True, 128, True),
+    ([17, 64, 65], [17, 2, 1], 4, 4, 256, 32, True, False, True, 64, False),
+    ([40, 41], [1, 7], 3, 9, 64, 48, True, True, False, 32, True),
+    ([9, 0, 5, 30], [2, 0, 0, 30], 5, 5, 64, 16, False, False, True, 16, False),
+    ([50, 3], [4, 3], 2, 32, 256, 128, False, True, False, 0, False),
+    ([300] * 70, [1 + i % 3 for i in range(70)], 1, 2, 64, 64, True, False, True, 64, True),
+]
+
+
+@pytest.mark.parametrize("lens,news,heads,hq,dim,page,e4m3,nhd,f32,rot,pairs", APPEND)
+def test_append(w12, lens, news, heads, hq, dim, page, e4m3, nhd, f32, rot, pairs):
+    st = Step(w12, lens, news, heads, dim, page, e4m3, nhd, pad=0 if news is None else 3)
+    m = st.rows
+    say(f"append m={m} hq={hq} heads={heads} dim={dim} page={page} e4m3={e4m3} nhd={nhd} f32={f32} rot={rot} pairs={pairs}")
+    g = torch.Generator().manual_seed(1)
+    wide = torch.randn(m, (hq + 2 * heads) * dim + 32, generator=g).to(torch.float32 if f32 else torch.bfloat16).cuda()
+    qkv = wide[:, :-32]                                       # rows apart
+    rope = rope_table(max(lens) + 1, rot) if rot else None
+    before = (st.k.clone(), st.v.clone())
+    out = torch.full((m, hq * dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    rt = None if rope is None else torch.tensor(rope).cuda()
+    assert w12.kv_append(qkv, st.kv, st.batch, rope=rt, interleaved=pairs, out=out) is out
+    check_append(st, qkv, hq, rope, pairs, out, before, m)
+    # q, k and v apart, and k and v alone, put the same bits
+    one = (st.k.clone(), st.v.clone())
+    for q in (qkv[:, :hq * dim], None):
+        st.k.copy_(before[0])
+        st.v.copy_(before[1])
+        r = w12.kv_append((q, qkv[:, hq * dim:(hq + heads) * dim], qkv[:, (hq + heads) * dim:]), st.kv, st.batch, rope=rt,
+                          interleaved=pairs)
+        assert all(torch.equal(a.view(torch.uint8) if e4m3 else a, b.view(torch.uint8) if e4m3 else b)
+                   for a, b in zip((st.k, st.v), one))
+        last = len(lens) if st.start is None else int(st.start[-1])
+        assert r is None if q is None else torch.equal(r[:last], out[:last])
+
+
+def test_append_without_a_place(w12):
+    """Pages outside the cache, places outside the table, more new tokens than places, positions outside
+    the rotation's table, q_start past the rows."""
+    pos = np.array([0, -1, 5, 49, 50, 3, 2, 1, 10, 11, 12], np.int32)
+    st = Step(w12, [40, 3, 200, 33], [3, 5, 1, 2], 2, 64, 16, positions=pos)
+    st.table[0, 2] = st.pages                                 # places 32 .. 47 of sequence 0
+    st.table[3, 2] = -5
+    st.table[2, :] = 2 ** 31 - 1
+    st.lens[2] = 5000                                         # past its table
+    st.make()
+    g = torch.Generator().manual_seed(2)
+    qkv = torch.randn(11, 6 * 64, generator=g).cuda()
+    rope = rope_table(50, 64)
+    before = (st.k.clone(), st.v.clone())
+    say("append without a place")
+    out = torch.full((11, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    w12.kv_append(qkv, st.kv, st.batch, rope=torch.tensor(rope).cuda(), out=out)
+    check_append(st, qkv, 2, rope, False, out, before, 11)
+
+
+def test_append_e4m3_range(w12):
+    """Values past the largest one, NaN and infinities."""
+    st = Step(w12, [4], [4], 1, 64, 16, e4m3=True, scales=False)
+    x = torch.zeros(4, 192)
+    x[:, 64:] = torch.tensor([[500.0], [-1e30], [float("inf")], [float("nan")]])
+    say("append e4m3 range")
+    w12.kv_append(x.cuda(), st.kv, st.batch)
+    for c in (st.k, st.v):
+        p = int(st.table[0, 0])
+        got = c[p, 0, :4].float().cpu()
+        assert (got[0] == 448).all() and (got[1] == -448).all() and (got[2] == 448).all() and got[3].isnan().all()
+
+
+def check_attention(st, q, hq, y, scale=None):
+    m = q.shape[0]
+    qq = f64(q).reshape(m, hq, st.dim)
+    sc = st.dim ** -0.5 if scale is None else scale
+    want, mag, big = oracle.attention64(qq, st.values(0), st.values(1), st.table, st.lens, st.start, st.tree, sc)
+    got = f64(y).reshape(m, hq, st.dim)
+    mine = ~np.isnan(want).all(axis=2)
+    assert np.all(got[~mine] == 7.0)                          # rows behind the last sequence
+    ds = (st.dim + 8) * U * big
+    rel = 2 * ds + 4 * U + 2.0 ** -16 + (st.lens.max() + 8) * U
+    tol = H * np.abs(want) + (1 + H) * rel[:, :, None] * mag
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad[mine].any(), (np.argwhere(bad & mine[:, :, None])[:5], np.abs(got - want)[mine].max())
+    return mine
+
+
+def attend(w12, st, q, **kw):
+    y = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    assert w12.attention(q, st.kv, st.batch, out=y, **kw) is y
+    return y
+
+
+def queries(st, hq, seed=3, scale=1.5):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(st.rows, hq * st.dim, generator=g) * scale).to(torch.bfloat16).cuda()
+
+
+EDGES = [0, 1, 2, 15, 16, 17, 31, 32, 33, 48, 63, 64, 65, 95, 127, 128, 129, 130, 255, 256, 257, 511, 513, 1000]
+
+
+@pytest.mark.parametrize("dim,page,e4m3,nhd,heads,group", [
+    (128, 16, False, False, 2, 6), (64, 16, False, True, 3, 1), (256, 16, False, False, 1, 4), (128, 48, True, True, 2, 8),
+    (64, 64, True, False, 1, 16), (256, 32, True, False, 2, 3), (128, 128, False, True, 1, 20), (256, 16, True, True, 1, 40)])
+def test_attention_one_token(w12, dim, page, e4m3, nhd, heads, group):
+    st = Step(w12, EDGES, None, heads, dim, page, e4m3, nhd)
+    hq = heads * group
+    say(f"attention dim={dim} page={page} e4m3={e4m3} nhd={nhd} heads={heads} group={group}")
+    q = queries(st, hq)
+    check_attention(st, q, hq, attend(w12, st, q))
+    check_attention(st, q, hq, attend(w12, st, q, scale=-0.3), scale=-0.3)
+
+
+@pytest.mark.parametrize("dim,page,e4m3,nhd,heads,group", [
+    (128, 16, False, False, 2, 6), (64, 32, True, True, 1, 5), (256, 16, False, True, 2, 1), (256, 64, True, False, 1, 6)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attention_drafts(w12, dim, page, e4m3, nhd, heads, group, tree):
+    """Chains and trees of new tokens, sequences without any, masks that leave a row nothing, padding."""
+    lens = [1, 7, 16, 40, 33, 130, 600, 64, 2, 257]
+    news = [1, 7, 3, 16, 33, 0, 5, 64, 2, 30]
+    m = sum(news) + 4
+    masks = None
+    if tree:
+        rng = np.random.default_rng(5)
+        masks = rng.integers(0, 2 ** 63, m, dtype=np.int64)
+        masks[::5] = 0                                        # (a sequence that is all new then sees nothing)
+        masks[1::5] = -1
+    st = Step(w12, lens, news, heads, dim, page, e4m3, nhd, tree=masks, pad=4)
+    hq = heads * group
+    say(f"attention drafts dim={dim} page={page} e4m3={e4m3} nhd={nhd} heads={heads} group={group} tree={tree}")
+    q = queries(st, hq)
+    y = attend(w12, st, q)
+    mine = check_attention(st, q, hq, y)
+    assert mine.sum() == (m - 4) * hq
+    if tree:
+        assert (y[0] == 0).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attention_long(w12, e4m3):
+    """Lengths that many workgroups share, ragged, beside short ones; bits repeat."""
+    st = Step(w12, [9000, 3, 0, 20011, 1, 4097], None, 2, 128, 64, e4m3)
+    say(f"attention long e4m3={e4m3}")
+    q = queries(st, 12)
+    y = attend(w12, st, q)
+    check_attention(st, q, 12, y)
+    for _ in range(3):
+        assert torch.equal(attend(w12, st, q), y)
+
+
+def test_attention_many_sequences(w12):
+    rng = np.random.default_rng(6)
+    lens = rng.integers(0, 300, 333).tolist()
+    news = [min(int(rng.integers(0, 4)), n) for n in lens]
+    st = Step(w12, lens, news, 1, 64, 16, pad=2)
+    say("attention of 333 sequences")
+    q = queries(st, 4)
+    check_attention(st, q, 4, attend(w12, st, q))
+
+
+def test_attention_long_prompt(w12):
+    """More rows of a sequence than any tile holds."""
+    st = Step(w12, [700, 333], [700, 150], 2, 64, 32)
+    say("attention of 850 new tokens")
+    q = queries(st, 6)
+    check_attention(st, q, 6, attend(w12, st, q))
+
+
+@pytest.mark.parametrize("dim,e4m3", [(128, False), (64, False), (256, False), (128, True), (256, True)])
+def test_attention_unseen_values(w12, dim, e4m3):
+    """NaN and infinities in every place that no row sees, and in new tokens that some rows do not see."""
+    lens, news = [1, 20, 45, 100, 300, 17], [1, 4, 6, 1, 20, 17]
+    m = sum(news)
+    masks = np.zeros(m, np.int64)
+    first = np.concatenate([[0], np.cumsum(news)])
+    for s, t in enumerate(news):
+        for j in range(t):
+            masks[first[s] + j] = 1 << j | 1
+    st = Step(w12, lens, news, 1, dim, 16, e4m3, tree=masks)
+    hq = 6
+    seen = np.zeros((st.pages, 16), bool)
+    for s, n in enumerate(lens):
+        for c in range(n):
+            seen[st.table[s, c // 16], c % 16] = True
+    hide = torch.tensor(~seen).cuda()[:, None, :, None].expand(-1, 1, -1, dim)
+    for c, val in ((st.k, float("nan")), (st.v, float("nan") if e4m3 else float("inf"))):
+        x = c.float()
+        x[hide] = val
+        c.copy_(x.to(c.dtype))
+    q = queries(st, hq)
+    say(f"attention unseen values dim={dim} e4m3={e4m3}")
+    check_attention(st, q, hq, attend(w12, st, q))
+    # one new token of the longest sequence bad: its own row alone is
+    s, j = 4, 7
+    c = lens[s] - news[s] + j
+    st.v[int(st.table[s, c // 16]), 0, c % 16, 5] = float("nan")
+    st.k[int(st.table[s, c // 16]), 0, c % 16, 1] = float("nan")
+    row = first[s] + j
+    y = attend(w12, st, q)
+    assert torch.isnan(y[row]).all()
+    keep = [i for i in range(m) if i != row]
+    st.v[int(st.table[s, c // 16]), 0, c % 16, 5] = 0.0
+    st.k[int(st.table[s, c // 16]), 0, c % 16, 1] = 0.0
+    assert torch.equal(attend(w12, st, q)[keep], y[keep])
+    # only its value: the column
+    st.v[int(st.table[s, c // 16]), 0, c % 16, 5] = float("nan")
+    y2 = attend(w12, st, q)
+    bad = torch.isnan(y2).view(m, hq, dim)
+    assert bad[row, :, 5].all() and bad.sum() == hq
+
+
+def test_attention_places_that_do_not_exist(w12):
+    """Pages outside the cache inside a sequence, lengths past the table, negative ones, fewer places
+    than new tokens."""
+    st = Step(w12, [200, 64, 90, 5, 33], [2, 1, 1, 9, 1], 2, 128, 16)
+    st.table[0, 3] = -1
+    st.table[0, 5] = st.pages
+    st.table[0, 12] = -7
+    st.table[1, :] = 2 ** 31 - 1                              # nothing left to see
+    st.lens[2] = 100000                                       # past its table: what the table has
+    st.lens[4] = -3
+    st.make()
+    say("attention without places")
+    q = queries(st, 4)
+    y = attend(w12, st, q)
+    st.lens[2] = st.table.shape[1] * 16 + 1                   # (the same, and small enough for the oracle)
+    check_attention(st, q, 4, y)
+    assert (y[2] == 0).all() and (y[-1] == 0).all()
+
+
+def test_attention_scores(w12):
+    """Large scores, equal ones, scores of -Inf alone, a NaN seen."""
+    st = Step(w12, [40, 40, 40, 40], None, 1, 64, 16)
+    q = queries(st, 2, scale=40.0)
+    q[1] = 0.0
+    p2, p3 = int(st.table[2, 0]), int(st.table[3, 1])
+    st.k[p3, 0, 3] = float("nan")
+    say("attention scores")
+    y = attend(w12, st, q)
+    assert torch.isnan(y[3]).all()
+    st.k[p3, 0, 3] = 0.0
+    y[3] = attend(w12, st, q)[3]
+    check_attention(st, q, 2, y)
+    q[2] = 1.0
+    for c in range(3):
+        st.k[int(st.table[2, c]), 0, :, 0] = float("-inf")
+    y = attend(w12, st, q)
+    assert (y[2] == 0).all()
+    st.k[p2, 0, 4, 0] = 1.0                                   # one finite score among them
+    assert torch.equal(attend(w12, st, q)[2, :64], st.v[p2, 0, 4])
+
+
+def test_attention_strided_queries(w12):
+    st = Step(w12, [50, 200, 3], None, 2, 128, 16)
+    wide = torch.randn(3, 4 * 128 + 64, generator=torch.Generator().manual_seed(9)).to(torch.bfloat16).cuda()
+    q = wide[:, :512]
+    say("attention strided queries")
+    y = w12.attention(q, st.kv, st.batch)
+    check_attention(st, q, 4, y)
+    assert torch.equal(y, w12.attention(q.contiguous(), st.kv, st.batch))
+
+
+def test_past_32_bits(w12):
+    """A cache of more than 2^32 elements, its far pages appended to and read."""
+    page, heads, dim = 64, 8, 128
+    pages = (2 ** 32 + 2 ** 28) // (page * heads * dim)
+    k = torch.empty(pages, heads, page, dim, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    st = Step(w12, [130, 70], [2, 1], heads, dim, page)
+    far = np.array([pages - 1, 3, pages - 7, pages // 2 + 1, pages - 2], np.int32)
+    st.table[0, :3], st.table[1, :2] = far[:3], far[3:]
+    ids = torch.tensor(far.astype(np.int64)).cuda()
+    g = torch.Generator().manual_seed(4)
+    for c in (k, v):
+        c[ids] = torch.randn(5, heads, page, dim, generator=g).to(torch.bfloat16).cuda()
+    small = Step(w12, [130, 70], [2, 1], heads, dim, page)
+    small.table[0, :3], small.table[1, :2] = [0, 1, 2], [3, 4]
+    small.k, small.v = k[ids].clone(), v[ids].clone()
+    small.pages = 5
+    small.make()
+    st.k, st.v, st.pages = k, v, pages
+    st.make()
+    say("cache past 2^32 elements")
+    qkv = torch.randn(3, 64 * dim, generator=g).to(torch.bfloat16).cuda()
+    rope = torch.tensor(rope_table(200, 128)).cuda()
+    a, b = (w12.kv_append(qkv, x.kv, x.batch, rope=rope) for x in (st, small))
+    assert torch.equal(a, b)
+    assert torch.equal(k[ids], small.k) and torch.equal(v[ids], small.v)
+    y = attend(w12, small, a)
+    assert torch.equal(attend(w12, st, a), y)
+    check_attention(small, a, 48, y)
+
+
+# ---- sampling ----
+def params(m, seed):
+    """A mix of settings, per row."""
+    rng = np.random.default_rng(seed)
+    pick = lambda vals: np.array([vals[i] for i in rng.integers(0, len(vals), m)])  # noqa: E731
+    return dict(temperature=pick([0.0, 0.3, 0.7, 1.0, 1.0, 2.0, 30.0]).astype(np.float32),
+                top_k=pick([0, 0, 1, 2, 5, 40, 1000, 10 ** 9]).astype(np.int32),
+                top_p=pick([1.0, 1.0, 0.99, 0.9, 0.5, 0.01, 0.0]).astype(np.float32),
+                min_p=pick([0.0, 0.0, 0.01, 0.2, 1.0, 2.0]).astype(np.float32))
+
+
+def check_sample(w12, y, u, kw, ties=False):
+    dev = {a: torch.tensor(b).cuda() for a, b in kw.items()}
+    r = w12.sample(y, torch.tensor(u).cuda(), **dev)
+    tok, logp, kept = oracle.sample64(f64(y), u.astype(np.float64), **{a: b.astype(np.float64) if b.dtype != np.int32 else b
+                                                                      for a, b in kw.items()})
+    got = r.token.cpu().numpy()
+    assert np.array_equal(r.kept.cpu().numpy(), kept), np.argwhere(r.kept.cpu().numpy() != kept)[:5]
+    assert np.array_equal(got, tok), np.argwhere(got != tok)[:5]
+    lp = r.logp.double().cpu().numpy()
+    fin = np.isfinite(logp)
+    assert np.array_equal(np.isnan(lp), np.isnan(logp)) and np.array_equal(np.isneginf(lp), np.isneginf(logp))
+    assert np.all(np.abs(lp - logp)[fin] <= U * np.abs(logp[fin]) + 1e-9)
+    return r
+
+
+@pytest.mark.parametrize("m,n,bf16", [(1, 1, False), (3, 2, True), (5, 63, False), (40, 1000, True), (40, 1025, False),
+                                      (64, 5003, False), (33, 32001, True), (7, 152064, False), (6, 152064, True),
+                                      (3, 262145, False), (300, 4097, False)])
+def test_sample(w12, m, n, bf16):
+    g = torch.Generator().manual_seed(n)
+    pad = 5
+    y = torch.randn(m, n + pad, generator=g) * 3
+    y[:, ::7] += torch.rand(m, (n + pad + 6) // 7, generator=g) * 9
+    if n > 100:
+        y[1::4, : n // 2] = -float("inf")
+    y = (y.to(torch.bfloat16) if bf16 else y).cuda()[:, :n]
+    rng = np.random.default_rng(n)
+    say(f"sample m={m} n={n} bf16={bf16}")
+    for seed in range(3):
+        u = rng.random(m).astype(np.float32)
+        check_sample(w12, y, u, params(m, seed))
+    check_sample(w12, y, u, {})
+    check_sample(w12, y, u, dict(top_p=np.full(m, 0.7, np.float32)))
+
+
+@pytest.mark.parametrize("sigma", [0.0, 0.01, 1.0, 30.0])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_sample_flat_and_equal(w12, sigma, bf16):
+    """Rows of equal and nearly equal logits: cuts between ties, masses spread over the whole row."""
+    m, n = 24, 20011
+    g = torch.Generator().manual_seed(3)
+    y = torch.randn(m, n, generator=g) * sigma - 4.0
+    y[2::3] = (y[2::3] * 4).round() / 4                        # many ties
+    y[5, 100:9000] = -float("inf")
+    y = (y.to(torch.bfloat16) if bf16 else y).cuda()
+    say(f"sample flat sigma={sigma} bf16={bf16}")
+    for seed in range(4):
+        kw = params(m, seed)
+        kw["top_k"] = np.random.default_rng(seed).choice([0, 0, 1, 777, 15000, 20011], m).astype(np.int32)
+        # (equal masses: a share of 0.7 or so falls between two tokens, one of 0.5 on a border)
+        kw["top_p"] = np.random.default_rng(seed).choice([1.0, 0.7123, 0.9617, 0.0217], m).astype(np.float32)
+        check_sample(w12, y, np.random.default_rng(seed + 9).random(m).astype(np.float32), kw)
+
+
+def test_sample_odd_rows(w12):
+    """Nothing left, NaN, infinities, signed zeros, one token, huge and tiny logits, odd u and parameters."""
+    n = 3001
+    y = torch.zeros(16, n)
+    y[0] = -float("inf")
+    y[1, 77] = float("nan")
+    y[2, 5] = float("inf")
+    y[3] = -float("inf")
+    y[3, n - 1] = -1e30
+    y[4] = -0.0
+    y[4, 1::2] = 0.0
+    y[5] = torch.linspace(-3e38, 3e38, n)
+    y[6] = 1e-40
+    y[7, 9] = 20.0
+    y[12] = -1e9
+    y[12, 17] = 3.0
+    y[13:] = torch.randn(3, n, generator=torch.Generator().manual_seed(1))
+    u = np.array([0.5] * 8 + [-1.0, np.nan, 1.0, 7.0, 0.3, 0.0, 1.0 - 2.0 ** -24, 0.999], np.float32)
+    say("sample odd rows")
+    for t in (1.0, 1e-30, 1e30, float("inf")):
+        kw = dict(temperature=np.full(16, t, np.float32))
+        check_sample(w12, y.cuda(), u, kw)
+    nan = np.full(16, np.nan, np.float32)
+    a = check_sample(w12, y.cuda(), u, dict(top_p=np.full(16, 5.0, np.float32), min_p=np.full(16, -1.0, np.float32),
+                                            top_k=np.full(16, -4, np.int32)))
+    b = w12.sample(y.cuda(), torch.tensor(u).cuda(), top_p=torch.tensor(nan).cuda(), min_p=torch.tensor(nan).cuda())
+    assert torch.equal(a.token, b.token) and torch.equal(a.kept, b.kept)
+    r = w12.sample(y.cuda(), torch.tensor(u).cuda(), temperature=torch.tensor(nan).cuda())
+    assert (r.token == -1).all() and r.logp[1:].isnan().all() and (r.kept == 0).all()
+
+
+def test_sample_column_order(w12):
+    """u walks through the kept tokens in column order, each with its share."""
+    n, steps = 4001, 512
+    y = torch.randn(n, generator=torch.Generator().manual_seed(7)).cuda() * 2
+    u = (np.arange(steps) / steps).astype(np.float32)
+    say("sample column order")
+    r = check_sample(w12, y.expand(steps, n), u, dict(top_k=np.full(steps, 30, np.int32)))
+    t = r.token.cpu().numpy()
+    assert np.all(np.diff(t) >= 0) and len(set(t.tolist())) > 10
+
+
+def test_arguments(w12):
+    st = Step(w12, [20, 20], None, 2, 64, 16)
+    q = queries(st, 4)
+    qkv = torch.zeros(2, 8 * 64, device="cuda")
+    for bad in (lambda: w12.attention(q.float(), st.kv, st.batch), lambda: w12.attention(q[:, :64], st.kv, st.batch),
+                lambda: w12.attention(q[:1], st.kv, st.batch), lambda: w12.attention(q.cpu(), st.kv, st.batch),
+                lambda: w12.kv_append(qkv[:, :256], st.kv, st.batch), lambda: w12.kv_append(qkv.half(), st.kv, st.batch),
+                lambda: w12.kv_append(qkv, st.kv, st.batch, rope=torch.zeros(3, 64)),
+                lambda: w12.kv_append(qkv, st.kv, st.batch, out=torch.zeros(2, 256, device="cuda")),
+                lambda: w12.KVCache(st.k, st.v[:, :1]), lambda: w12.KVCache(st.k, st.v, k_scale=torch.ones(2).cuda()),
+                lambda: w12.KVBatch(st.batch.table, st.batch.lens.long()),
+                lambda: w12.KVBatch(st.batch.table, st.batch.lens, q_start=st.batch.lens),
+                lambda: w12.sample(qkv, torch.zeros(3).cuda()), lambda: w12.sample(qkv.half(), torch.zeros(2).cuda()),
+                lambda: w12.sample(qkv, torch.zeros(2).cuda(), top_k=torch.zeros(2).cuda())):
+        with pytest.raises((TypeError, ValueError)):
+            bad()
+    # the refusals of the library come through as its error
+    with pytest.raises(w12.W12Error) as e:
+        w12.kv_append(qkv, st.kv, st.batch, rope=torch.zeros(30, 24, device="cuda"))
+    assert e.value.status == w12.W12_ERR_SHAPE
+    # no rows: nothing to do
+    assert w12.sample(qkv[:0], torch.zeros(0).cuda()).token.shape == (0,)
