@@ -408,7 +408,7 @@ int w12_logprobs(const void *y, int64_t m, int64_t n, int64_t ldy, const void *t
 typedef struct w12_kv {
     int64_t pages;        /* 1 .. 2^31 - 1                                      */
     int64_t heads;        /* key/value heads, at most 2^16                      */
-    int64_t page;         /* token places of a page: a multiple of 16, at most 2^16 */
+    int64_t page;         /* token places of a page: a multiple of 16, at most 1024 */
     int64_t dim;          /* 64, 128 or 256                                     */
     void   *k, *v;        /* device, 16-byte aligned                            */
     int64_t page_stride;  /* in elements, multiples of 16 (8 in bfloat16), not negative; */
@@ -432,7 +432,7 @@ typedef struct w12_kv {
 typedef struct w12_kv_batch {
     int64_t seqs;             /* below 2^20                                        */
     const int32_t *table;     /* [seqs][table_cols], rows table_stride apart       */
-    int64_t table_cols;       /* 1 .. 2^31 / page                                  */
+    int64_t table_cols;       /* 1 .. 2^30 / page                                  */
     int64_t table_stride;
     const int32_t *lens;      /* [seqs]                                            */
     const int32_t *q_start;   /* [seqs + 1], or NULL                               */

@@ -751,8 +751,8 @@ int check_kv(const w12_kv* kv, const w12_kv_batch* b, int64_t m) {
   if (kv->pages <= 0 || kv->heads <= 0 || kv->page <= 0)
     return fail(W12_ERR_ARG, "pages, heads and page must be positive (%lld, %lld, %lld)", (long long)kv->pages,
                 (long long)kv->heads, (long long)kv->page);
-  if (kv->pages >= kMaxDim || kv->heads > 65536 || kv->page > 65536)
-    return fail(W12_ERR_RANGE, "pages, heads or page too large (below 2^31, at most 2^16, at most 2^16)");
+  if (kv->pages >= kMaxDim || kv->heads > 65536 || kv->page > 1024)
+    return fail(W12_ERR_RANGE, "pages, heads or page too large (below 2^31, at most 2^16, at most 1024)");
   if (kv->dim != 64 && kv->dim != 128 && kv->dim != 256)
     return fail(W12_ERR_SHAPE, "dim must be 64, 128 or 256 (dim=%lld)", (long long)kv->dim);
   if (kv->page % 16) return fail(W12_ERR_SHAPE, "page must be a multiple of 16 (page=%lld)", (long long)kv->page);
@@ -773,8 +773,8 @@ int check_kv(const w12_kv* kv, const w12_kv_batch* b, int64_t m) {
   if (m >= kMaxDim || b->seqs >= (int64_t(1) << 20)) return fail(W12_ERR_RANGE, "m or seqs too large (below 2^31 and 2^20)");
   if (!b->table || !b->lens) return fail(W12_ERR_ARG, "table or lens is NULL");
   if (b->table_cols <= 0) return fail(W12_ERR_ARG, "table_cols must be positive (%lld)", (long long)b->table_cols);
-  if (b->table_cols > kMaxDim / kv->page)
-    return fail(W12_ERR_RANGE, "a table of %lld pages passes 2^31 places", (long long)b->table_cols);
+  if (b->table_cols > (int64_t(1) << 30) / kv->page)
+    return fail(W12_ERR_RANGE, "a table of %lld pages passes 2^30 places", (long long)b->table_cols);
   if (b->table_stride < b->table_cols && b->seqs > 1)
     return fail(W12_ERR_ARG, "table_stride=%lld is smaller than table_cols=%lld", (long long)b->table_stride,
                 (long long)b->table_cols);
@@ -855,6 +855,8 @@ int w12_attention_scratch(int64_t m, int64_t hq, const w12_kv* kv, const w12_kv_
   w12::DevInfo di;
   hipError_t e = w12::dev_info(&di);
   if (e != hipSuccess) return hip_fail(e, "device query");
+  if (!w12::attention_fits(di, m, hq, kv_of(kv), batch_of(batch)))
+    return fail(W12_ERR_RANGE, "the batch is too large (m * hq from 2^30, or its rows of 16 x tiles of 128 places from 2^31 on)");
   *bytes = w12::attention_scratch(di, m, hq, kv_of(kv), batch_of(batch), zero);
   return ok();
 }
@@ -872,6 +874,8 @@ int w12_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t hq, const w
   w12::DevInfo di;
   hipError_t e = w12::dev_info(&di);
   if (e != hipSuccess) return hip_fail(e, "device query");
+  if (!w12::attention_fits(di, m, hq, kv_of(kv), batch_of(batch)))
+    return fail(W12_ERR_RANGE, "the batch is too large (m * hq from 2^30, or its rows of 16 x tiles of 128 places from 2^31 on)");
   uint64_t zero = 0;
   const uint64_t need = w12::attention_scratch(di, m, hq, kv_of(kv), batch_of(batch), &zero);
   if (need > 0) {

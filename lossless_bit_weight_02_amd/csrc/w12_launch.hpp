@@ -187,6 +187,7 @@ hipError_t launch_kv_append(const AppendArgs& a, const KvArgs& kv, const BatchAr
 // *zero of them counters
 uint64_t attention_scratch(const DevInfo& di, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b,
                            uint64_t* zero);
+bool attention_fits(const DevInfo& di, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b);
 hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t hq, const KvArgs& kv,
                             const BatchArgs& b, float scale, uint16_t* y, void* scratch, hipStream_t s);
 // a token per row of logits (w12_sample); scratch: sample_scratch bytes, the first *zero of them counters
