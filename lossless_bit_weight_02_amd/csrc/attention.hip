@@ -13,8 +13,10 @@
 //                  of V^T's operand are those same ones: lane (r, g) loads `kRun` columns (r kRun ..) of
 //                  them, eight rows, and turns the eight rows of 16-bit values in its registers (one byte
 //                  permute per pair).  No value passes between lanes, and nothing goes through LDS.
-// Probabilities meet V as two bfloat16 terms (the leading 8 bits and the rest, 16 bits together): one would
-// be off by as much again as the output's own rounding.
+// Probabilities meet bfloat16 values as two bfloat16 terms (the leading 8 bits and the rest, 16 bits
+// together): one would be off by as much again as the output's own rounding.  e4m3 values are float16
+// exactly, so there one float16 term (11 bits) does, the probabilities brought up to 2^15: those too
+// small for it are off by 2^-32 of the largest.
 //
 // Split.  The work of the whole batch is a line of units of 128 places (of one sequence, key head and
 // block of rows); every workgroup takes an equal run of it, found from the lengths on the device, so
@@ -27,6 +29,8 @@
 namespace w12 {
 
 constexpr int kAtUnit = 128;                      // places of a unit
+constexpr int kAtPiece = 4;                       // units of a segment worth a workgroup of their own
+constexpr int kAtStart = 2;                       // units that a segment's beginning and end cost
 constexpr float kAtLog2e = 1.44269504088896340736f;
 constexpr float kAtSlack = 8.0f;                  // powers of two a probability may pass 1 by
 constexpr int kAuxAgent = 16;                     // sc1: stores and loads that every die of the device sees
@@ -51,6 +55,23 @@ typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// acc + V^T P^T: e4m3 values and their probabilities as float16, bfloat16 ones in bfloat16
+template <bool E4M3>
+__device__ __forceinline__ floatx4 mfma_pv(u32x4 v, u32x4 p, floatx4 acc) {
+  if constexpr (E4M3)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, v), __builtin_bit_cast(f16x8, p), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(v), as_bf16(p), acc, 0, 0, 0);
+}
+
+// a pair of e4m3 values as float16 (exact)
+__device__ __forceinline__ uint32_t e4m3_pair16(uint32_t w, bool high) {
+  return high ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true))
+              : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+}
 // eight e4m3 values as bfloat16
 __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, bool high) {
   return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
@@ -71,103 +92,111 @@ struct AttnShape {
   static constexpr int kRunWords = kRun * kSize / 4;
 };
 
-// The keys of 16 places, a lane's pieces of place lane % 16.
+// A lane's share of 32 places' keys or values as they lie in the cache.
+//   keys:   of place r of either 16, 16 bytes at 64 i + 16 g of the row
+//   values: of places 4 g .. +3 of either 16 (e = 0 .. 3, 4 .. 7), columns kRun r .. of each 16 kRun
 template <int DIM, bool E4M3>
-struct KeyTile {
+struct RawTile {
   using S = AttnShape<DIM, E4M3>;
-  u32x4 w[S::kLoads];
-  __device__ __forceinline__ void load(Rsrc tile, uint32_t off) {
-#pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) w[i] = __builtin_amdgcn_raw_buffer_load_b128(tile, off + 64 * i, 0, 0);
-  }
-  // piece f as the A operand: columns 32 f + 8 g .. +7 (e4m3: 64 (f / 2) + 16 g + 8 (f % 2) ..)
-  __device__ __forceinline__ bf16x8 frag(int f) const {
-    if constexpr (E4M3) return as_bf16(e4m3_run(w[f / 2][2 * (f % 2)], w[f / 2][2 * (f % 2) + 1]));
-    else return as_bf16(w[f]);
-  }
-  static __device__ __forceinline__ int column(int f, int g) {
-    return E4M3 ? 64 * (f / 2) + 16 * g + 8 * (f % 2) : 32 * f + 8 * g;
-  }
-};
+  uint32_t w[DIM * S::kSize / 8];
 
-// The values of 32 places: of places 4 g .. +3 of either 16, columns kRun r .. of each 16 kRun.
-template <int DIM, bool E4M3>
-struct ValueTile {
-  using S = AttnShape<DIM, E4M3>;
-  uint32_t w[8][S::kRuns][S::kRunWords];
-  __device__ __forceinline__ void load4(int e0, Rsrc tile, uint32_t off, uint32_t row_bytes) {
+  __device__ __forceinline__ void load_keys(int h, Rsrc tile, uint32_t off) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int i = 0; i < S::kLoads; ++i) put4(h * S::kLoads + i, __builtin_amdgcn_raw_buffer_load_b128(tile, off + 64 * i, 0, kAuxNT));
+  }
+  __device__ __forceinline__ void put4(int i, u32x4 v) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[4 * i + k] = v[k];
+  }
+  // keys h as the A operand, piece f: columns key_column(f, g) .. +7 of place r
+  __device__ __forceinline__ bf16x8 key(int h, int f) const {
+    const uint32_t* const v = &w[h * S::kLoads * 4];
+    if constexpr (E4M3) return as_bf16(e4m3_run(v[2 * f], v[2 * f + 1]));
+    else return as_bf16(u32x4{v[4 * f], v[4 * f + 1], v[4 * f + 2], v[4 * f + 3]});
+  }
+
+  __device__ __forceinline__ void load_values(int h, Rsrc tile, uint32_t off, uint32_t row_bytes) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
 #pragma unroll
       for (int q = 0; q < S::kRuns; ++q) {
         const uint32_t at = off + 16 * S::kRun * S::kSize * q;
+        const int i = ((4 * h + e) * S::kRuns + q) * S::kRunWords;
         if constexpr (S::kRunWords == 4) {
-          const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(tile, at, e * row_bytes, 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[e0 + e][q][i] = v[i];
+          put4(i / 4, __builtin_amdgcn_raw_buffer_load_b128(tile, at, e * row_bytes, kAuxNT));
         } else if constexpr (S::kRunWords == 2) {
-          const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(tile, at, e * row_bytes, 0);
-          w[e0 + e][q][0] = v[0];
-          w[e0 + e][q][1] = v[1];
+          const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(tile, at, e * row_bytes, kAuxNT);
+          w[i] = v[0];
+          w[i + 1] = v[1];
         } else {
-          w[e0 + e][q][0] = __builtin_amdgcn_raw_buffer_load_b32(tile, at, e * row_bytes, 0);
+          w[i] = __builtin_amdgcn_raw_buffer_load_b32(tile, at, e * row_bytes, kAuxNT);
         }
       }
-    }
   }
-  // block `sub` as the A operand: its rows are the columns kRun r + sub % kRun
-  __device__ __forceinline__ u32x4 frag(int sub) const {
-    const int q = sub / S::kRun, i = sub % S::kRun;
+  __device__ __forceinline__ uint32_t at(int e, int q, int i) const { return w[(e * S::kRuns + q) * S::kRunWords + i]; }
+  // values as the A operand, block c of the output: rows are the columns kRun r + c % kRun of run c / kRun
+  __device__ __forceinline__ u32x4 value(int c) const {
+    const int q = c / S::kRun, i = c % S::kRun;
     u32x4 f;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       if constexpr (E4M3) {
         // two columns' bytes of two places next to each other, the column's pair converted
-        const uint32_t t = __builtin_amdgcn_perm(w[2 * p + 1][q][i / 4], w[2 * p][q][i / 4],
-                                                 (i & 2) ? 0x07030602u : 0x05010400u);
-        f[p] = e4m3_pair(t, i & 1);
+        const uint32_t t = __builtin_amdgcn_perm(at(2 * p + 1, q, i / 4), at(2 * p, q, i / 4), (i & 2) ? 0x07030602u : 0x05010400u);
+        f[p] = e4m3_pair16(t, i & 1);
       } else {
-        f[p] = __builtin_amdgcn_perm(w[2 * p + 1][q][i / 2], w[2 * p][q][i / 2],
-                                     (i & 1) ? 0x07060302u : 0x05040100u);
+        f[p] = __builtin_amdgcn_perm(at(2 * p + 1, q, i / 2), at(2 * p, q, i / 2), (i & 1) ? 0x07060302u : 0x05040100u);
       }
     }
     return f;
   }
-  __device__ __forceinline__ void clear(int e, bool yes) {
-#pragma unroll
-    for (int q = 0; q < S::kRuns; ++q)
-#pragma unroll
-      for (int i = 0; i < S::kRunWords; ++i) w[e][q][i] = yes ? 0u : w[e][q][i];
-  }
-  // whether place e has a NaN or an infinity
+  // whether place e's values have a NaN or an infinity
   __device__ __forceinline__ bool odd(int e) const {
     bool r = false;
 #pragma unroll
-    for (int q = 0; q < S::kRuns; ++q)
+    for (int i = 0; i < S::kRuns * S::kRunWords; ++i) {
+      const uint32_t v = at(e, 0, i);
+      if constexpr (E4M3) {
 #pragma unroll
-      for (int i = 0; i < S::kRunWords; ++i) {
-        const uint32_t v = w[e][q][i];
-        if constexpr (E4M3) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) r |= (v >> (8 * b) & 0x7Fu) == 0x7Fu;
-        } else {
-          r |= (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
-        }
+        for (int b = 0; b < 4; ++b) r |= (v >> (8 * b) & 0x7Fu) == 0x7Fu;
+      } else {
+        r |= ((v & 0x7F80u) == 0x7F80u) | ((v & 0x7F800000u) == 0x7F800000u);
       }
+    }
     return r;
   }
+  __device__ __forceinline__ void clear(int e, bool yes) {
+#pragma unroll
+    for (int i = 0; i < S::kRuns * S::kRunWords; ++i) {
+      uint32_t& v = w[e * S::kRuns * S::kRunWords + i];
+      v = yes ? 0u : v;
+    }
+  }
 };
+// (where key pieces begin: e4m3 loads have two)
+template <bool E4M3>
+__device__ __forceinline__ int key_column(int f, int g) {
+  return E4M3 ? 64 * (f / 2) + 16 * g + 8 * (f % 2) : 32 * f + 8 * g;
+}
 
+__device__ __forceinline__ float part_f(Rsrc part, int at) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part, 4 * at, 0, kAuxAgent));
+}
 __device__ __forceinline__ int lane_get(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
-// The batch's line of units, its sequences 64 at a time, a lane each.
+// The batch as a line that the workgroups share out, its sequences 64 at a time, a lane each.  A segment is
+// one key head and block of rows of a sequence.  While the chip has a workgroup for every kAtPiece units
+// of each segment, the line is those pieces, one a workgroup; else a segment takes its units and
+// kAtStart more, what beginning and ending one costs, so a workgroup with many short ones is not late.
 struct UnitLine {
   const AttnArgs& a;
   int rows;               // rows of q of a block
+  bool pieces = true;
+  int share = 1;          // of a workgroup
   int c0 = 0;             // the 64 sequences c0 ..
-  int base = 0;           // units before them
-  int first = 0, count = 0, len = 0, upto = 0;               // a lane's sequence; units up to and with it
-  int total = 0;          // units of the 64
+  int base = 0;           // the line before them
+  int first = 0, count = 0, len = 0, upto = 0;               // a lane's sequence; the line up to and with it
+  int total = 0;          // of the 64
   __device__ __forceinline__ UnitLine(const AttnArgs& a_, int rows_) : a(a_), rows(rows_) {}
 
   __device__ __forceinline__ int blocks(int count) const {
@@ -178,7 +207,10 @@ struct UnitLine {
     const int n = seen(len);
     return n > 0 ? (n + kAtUnit - 1) / kAtUnit : 1;
   }
-  __device__ __forceinline__ int of(int s) {
+  __device__ __forceinline__ int length(int tiles) const {
+    return pieces ? (tiles + kAtPiece - 1) / kAtPiece : tiles + kAtStart;
+  }
+  __device__ __forceinline__ void read(int s) {
     count = 0;
     if (s < a.b.seqs) {
       const SeqRows r = seq_rows(a.b, s, a.m);
@@ -186,141 +218,340 @@ struct UnitLine {
       count = (int)r.count;
       len = (int)r.len;
     }
-    return blocks(count) * (int)a.kv.heads * tiles(len);
   }
-  __device__ __forceinline__ void fill(int lane) {
-    upto = lane_scan(of(c0 + lane));
+  __device__ __forceinline__ int mine() const { return blocks(count) * (int)a.kv.heads * length(tiles(len)); }
+  __device__ __forceinline__ void scan() {
+    upto = lane_scan(mine());
     total = lane_get(upto, 63);
   }
-  // units of the whole batch
   __device__ __forceinline__ int all(int lane) {
     int sum = 0;
-    for (int s = lane; s < a.b.seqs; s += 64) sum += of(s);
+    for (int s = lane; s < a.b.seqs; s += 64) {
+      read(s);
+      sum += mine();
+    }
     return lane_get(lane_scan(sum), 63);
   }
-  // the lane that has unit u (calls only ever go up the line)
+  // the share of each workgroup; returns the line's length
+  __device__ __forceinline__ int start(int lane) {
+    if (a.b.seqs <= 64) {
+      read(lane);
+      scan();
+      if (total <= a.wgs) return total;
+      pieces = false;
+      scan();
+      share = (total + a.wgs - 1) / a.wgs;
+      return total;
+    }
+    int sum = all(lane);
+    if (sum > a.wgs) {
+      pieces = false;
+      sum = all(lane);
+      share = (sum + a.wgs - 1) / a.wgs;
+    }
+    read(lane);
+    scan();
+    return sum;
+  }
+  // the lane that has place u of the line (calls only ever go up it)
   __device__ __forceinline__ int find(int u, int lane) {
     while (u >= base + total && c0 + 64 < a.b.seqs) {
       base += total;
       c0 += 64;
-      fill(lane);
+      read(c0 + lane);
+      scan();
     }
     const uint64_t bl = __ballot(u < base + upto);
     return bl ? __ffsll((unsigned long long)bl) - 1 : 0;
   }
 };
 
-// kNq blocks of 16 rows of q a wave, kWr waves side by side with other rows, 4 / kWr on other places.
-template <int DIM, bool E4M3, int NQ, int WR>
-__global__ __launch_bounds__(kBlock, (DIM * NQ <= 128 ? 3 : 2)) void k_attention(AttnArgs a) {
+// What a workgroup has of the segment at place u of the line.
+struct Segment {
+  int first, count, len, seen;                               // its sequence
+  int s, hk, block, tiles;
+  int tile0, tile1;                                          // this workgroup's units
+  int from, to;                                              // the workgroups that have some
+  int next;                                                  // where the line goes on
+  bool whole;
+  __device__ __forceinline__ Segment(UnitLine& line, int u, int end, int lane) {
+    const int own = line.find(u, lane);
+    s = line.c0 + own;
+    first = lane_get(line.first, own);
+    count = lane_get(line.count, own);
+    len = lane_get(line.len, own);
+    tiles = line.tiles(len);
+    seen = line.seen(len);
+    const int blocks = line.blocks(count), each = line.length(tiles);
+    const int start = line.base + lane_get(line.upto, own) - blocks * (int)line.a.kv.heads * each;
+    const uint32_t idx = (uint32_t)(u - start) / (uint32_t)each;
+    hk = (int)(idx / (uint32_t)blocks);
+    block = (int)(idx - (uint32_t)hk * blocks);
+    const int seg = start + (int)idx * each;                 // where the segment begins on the line
+    next = seg + each < end ? seg + each : end;
+    if (line.pieces) {
+      const int per = (tiles + each - 1) / each;
+      tile0 = (u - seg) * per;
+      tile1 = tile0 + per < tiles ? tile0 + per : tiles;
+      from = seg;
+    } else {
+      tile0 = u - seg - kAtStart > 0 ? u - seg - kAtStart : 0;
+      tile1 = next - seg - kAtStart;
+      from = (seg + kAtStart) / line.share;
+    }
+    to = (seg + each - 1) / line.share;
+    whole = from == to;
+  }
+  __device__ __forceinline__ int valid(int group, int rows) const {
+    const uint32_t n = (uint32_t)count * (uint32_t)group - (uint32_t)(block * rows);
+    return n < (uint32_t)rows ? (int)n : rows;
+  }
+};
+
+// What a row of q sees of its sequence's new places: those up to `last`, and those of `mask`.  (Arithmetic, not
+// branches: the same few instructions for every lane.)
+struct SeenBy {
+  int last;
+  uint64_t mask;
+  // the place `bit` after the first new one, one that exists (the places before have bit < 0)
+  __device__ __forceinline__ bool operator()(int bit) const {
+    return (bit <= last) | ((bit < 64) & (int)(mask >> (bit & 63) & 1));
+  }
+};
+
+// The row of q at `row` of the segment's block as the B operand of K Q^T, zeros for none.
+template <int DIM, bool E4M3>
+__device__ __forceinline__ SeenBy load_query(const AttnArgs& a, const Segment& sg, uint32_t row, int g, bf16x8* q) {
+  const bool real = row < (uint32_t)sg.count * (uint32_t)a.group;
+  const uint32_t j = real ? row / (uint32_t)a.group : 0, h = real ? row - j * a.group : 0;
+  const int64_t at = sg.first + (int)j;
+  const uint16_t* const qr = a.q + at * a.ldq + ((int64_t)sg.hk * a.group + h) * DIM;
+#pragma unroll
+  for (int f = 0; f < AttnShape<DIM, E4M3>::kFrag; ++f) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(qr + key_column<E4M3>(f, g));
+    q[f] = as_bf16(real ? v : u32x4{0, 0, 0, 0});
+  }
+  return a.b.tree ? SeenBy{-1, a.b.tree[at]} : SeenBy{(int)j, 0};
+}
+
+// Scores of eight places into probabilities relative to the running maximum m (see the top), added to l, as
+// B operands (lo: bfloat16 only).
+template <bool E4M3, int SUBS>
+__device__ __forceinline__ void soften(const float (&x)[8], float& m, float& l, floatx4 (&acc)[SUBS], u32x4& hi, u32x4& lo) {
+  constexpr float kUp = E4M3 ? 7.0f : 0.0f;
+  float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+  if (__ballot(top > m + kAtSlack)) {
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float now = fmaxf(m, top);
+    const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - now);
+    m = now;
+    l *= f;
+#pragma unroll
+    for (int c = 0; c < SUBS; ++c) acc[c] *= f;
+  }
+  const float ref = m == -INFINITY ? 0.0f : m - kUp;
+  float p[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    p[e] = __builtin_amdgcn_exp2f(x[e] - ref);
+    l += p[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (E4M3) {
+      const f16x2 rr = {(_Float16)p[2 * e], (_Float16)p[2 * e + 1]};
+      hi[e] = __builtin_bit_cast(uint32_t, rr);
+    } else {
+      hi[e] = __builtin_amdgcn_perm(__float_as_uint(p[2 * e + 1]), __float_as_uint(p[2 * e]), 0x07060302u);
+      const bf16x2 rr = {(__bf16)(p[2 * e] - __uint_as_float(hi[e] << 16)),
+                         (__bf16)(p[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u))};
+      lo[e] = __builtin_bit_cast(uint32_t, rr);
+    }
+  }
+}
+
+// The pages of a wave's next steps: a lane per 16 places.  A tile that does not exist reads page 0, and is masked.
+template <int SIZE>
+struct Pages {
+  int page = -1, in = 0;
+  __device__ __forceinline__ void fill(const AttnArgs& a, const int32_t* table, int t, int t_end) {
+    const uint32_t tile = (uint32_t)t / 16u;
+    const uint32_t p = a.page_tiles == 1 ? tile : __umulhi(tile, a.page_magic);
+    in = (int)(tile - p * (uint32_t)a.page_tiles);
+    page = -1;
+    if (t < t_end) {
+      const int v = table[p];
+      if (v >= 0 && v < a.kv.pages) page = v;
+    }
+  }
+  __device__ __forceinline__ Rsrc tile(const AttnArgs& a, const uint8_t* p, int i, uint32_t row_bytes) const {
+    const int pg = lane_get(page, i), r = lane_get(in, i);
+    const int64_t at = (int64_t)(pg & ~(pg >> 31)) * a.kv.page_stride * SIZE + (int64_t)r * 16 * row_bytes;
+    return make_rsrc(p + at, 0x7FFFFFFF);
+  }
+};
+
+// Four columns of row `rq` of a sequence's rows for key head hk.
+template <int DIM>
+__device__ __forceinline__ void attn_put(const AttnArgs& a, const Segment& sg, uint32_t rq, int col, floatx4 o) {
+  const uint32_t j = rq / (uint32_t)a.group, h = rq - j * a.group;
+  const bf16x2 lo = {(__bf16)o[0], (__bf16)o[1]}, hi = {(__bf16)o[2], (__bf16)o[3]};
+  u32x2 v;
+  v[0] = __builtin_bit_cast(uint32_t, lo);
+  v[1] = __builtin_bit_cast(uint32_t, hi);
+  *reinterpret_cast<u32x2*>(a.y + ((int64_t)(sg.first + (int)j) * a.hq + (int64_t)sg.hk * a.group + h) * DIM + col) = v;
+}
+
+// Where a workgroup leaves its part of a segment: its second slot if the segment begins there.
+template <int DIM, int ROWS>
+struct Partial {
+  static constexpr int kPart = ROWS * (DIM + 2);
+  Rsrc b;
+  __device__ __forceinline__ Partial(const AttnArgs& a, int wg, bool begins)
+      : b(make_rsrc(a.part + (size_t)(2 * wg + (begins ? 1 : 0)) * kPart, kPart * 4)) {}
+  __device__ __forceinline__ void put(int row, int col, floatx4 o) const {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), b, (row * DIM + col) * 4, 0, kAuxAgent);
+  }
+  __device__ __forceinline__ void put_ml(int row, float m, float l) const {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), b, (ROWS * DIM + row) * 4, 0, kAuxAgent);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(l), b, (ROWS * (DIM + 1) + row) * 4, 0, kAuxAgent);
+  }
+  __device__ __forceinline__ float m(int row) const { return part_f(b, ROWS * DIM + row); }
+  __device__ __forceinline__ float l(int row) const { return part_f(b, ROWS * (DIM + 1) + row); }
+  __device__ __forceinline__ floatx4 o(uint32_t at) const {
+    return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, kAuxAgent));
+  }
+};
+
+// Counts this workgroup off after its partial; the last one of the segment joins them: four columns of a
+// row a thread, the parts' maxima and sums with them, kAhead parts in flight.
+template <int DIM, int ROWS>
+__device__ __forceinline__ void attn_join(const AttnArgs& a, const Segment& sg, int valid, float vs, int tid, int* s_last) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (tid == 0) {
+    const uint32_t old = __hip_atomic_fetch_add(&a.count[sg.from], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *s_last = old == (uint32_t)(sg.to - sg.from) ? 1 : 0;
+    if (*s_last) __hip_atomic_store(&a.count[sg.from], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!*s_last) return;
+  asm volatile("" ::: "memory");
+  constexpr int kItems = ROWS > 32 ? 4 : 1, kAhead = 16 / kItems;   // a thread's columns and parts in flight
+  for (int it0 = tid; it0 < valid * (DIM / 4); it0 += kBlock * kItems) {
+    int row[kItems];
+    uint32_t at[kItems];
+    float top[kItems], sum[kItems];
+    floatx4 o[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int it = it0 + i * kBlock;
+      const bool real = it < valid * (DIM / 4);
+      row[i] = real ? it / (DIM / 4) : 0;
+      at[i] = real ? (row[i] * DIM + it % (DIM / 4) * 4) * 4 : kOOB;
+      top[i] = -INFINITY;
+      sum[i] = 0.0f;
+      o[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    for (int p = sg.from; p <= sg.to; p += kAhead) {
+      float mv[kAhead][kItems], lv[kAhead][kItems];
+      floatx4 ov[kAhead][kItems];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const bool on = p + k <= sg.to;
+        const Partial<DIM, ROWS> part(a, on ? p + k : sg.to, (on ? p + k : sg.to) == sg.from);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+          mv[k][i] = part.m(row[i]);
+          lv[k][i] = part.l(row[i]);
+          ov[k][i] = part.o(on ? at[i] : kOOB);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        float now = top[i];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) now = fmaxf(now, mv[k][i]);
+        if (top[i] > -INFINITY) {
+          const float old = __builtin_amdgcn_exp2f(top[i] - now);
+          sum[i] *= old;
+          o[i] *= old;
+        }
+        top[i] = now;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (p + k > sg.to) continue;
+          // (a part that saw nothing has the sum 0, or NaN)
+          const float f = mv[k][i] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mv[k][i] - now);
+          sum[i] += lv[k][i] * f;
+          o[i] += ov[k][i] * f;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+      if (at[i] != kOOB)
+        attn_put<DIM>(a, sg, sg.block * ROWS + row[i], (int)(at[i] / 4) - row[i] * DIM, o[i] * (sum[i] == 0.0f ? 0.0f : vs / sum[i]));
+  }
+}
+
+// Up to 16 NQ rows of q: each wave all of them on places of its own.
+template <int DIM, bool E4M3, int NQ>
+__global__ __launch_bounds__(kBlock, 1) void k_attention(AttnArgs a) {
   using S = AttnShape<DIM, E4M3>;
-  constexpr int kRows = 16 * NQ * WR, kTg = 4 / WR;
+  constexpr int kRows = 16 * NQ;
   constexpr int kCols = DIM < 128 ? DIM : 128;              // columns joined at a time
   constexpr int kPitch = kCols + 4;
   __shared__ __attribute__((aligned(16))) float s_o[4][16][kPitch];
-  __shared__ float s_m[4][16 * NQ], s_l[4][16 * NQ];
+  __shared__ float s_m[4][kRows], s_l[4][kRows];
   __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wr = w % WR, tg = w / WR;
-  const int wg = blockIdx.x;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   UnitLine line(a, kRows);
-  int total;
-  if (a.b.seqs <= 64) {
-    line.fill(lane);
-    total = line.total;
-  } else {
-    total = line.all(lane);
-    line.fill(lane);
-  }
-  const int share = (total + a.wgs - 1) / a.wgs;
-  int u = wg * share;
-  const int end = u + share < total ? u + share : total;
+  const int total = line.start(lane);
+  int u = blockIdx.x * line.share;
+  const int end = u + line.share < total ? u + line.share : total;
   const uint32_t row_bytes = (uint32_t)a.kv.token_stride * S::kSize;
   const uint32_t k_off = r * row_bytes + 16 * g;
   const uint32_t v_off = 4 * g * row_bytes + r * S::kRun * S::kSize;
 
   while (u < end) {
-    const int own = line.find(u, lane);
-    const int s = line.c0 + own;
-    const int first = lane_get(line.first, own), count = lane_get(line.count, own), len = lane_get(line.len, own);
-    const int blocks = line.blocks(count), tiles = line.tiles(len), seen = line.seen(len);
-    const int start = line.base + lane_get(line.upto, own) - blocks * (int)a.kv.heads * tiles;
-    const uint32_t idx = (uint32_t)(u - start) / (uint32_t)tiles;
-    const int tile0 = (u - start) - (int)idx * tiles;
-    const int tile1 = tiles - tile0 < end - u ? tiles : tile0 + (end - u);
-    const int hk = (int)(idx / (uint32_t)blocks), block = (int)(idx - (uint32_t)hk * blocks);
-    const int seg = u - tile0;                               // the line's place of the segment's first unit
-    u += tile1 - tile0;
-    const int base = (len < 0 ? 0 : len) - count;            // (fewer than 2^30 rows)
-    const int t_end = tile1 * kAtUnit < seen ? tile1 * kAtUnit : seen;
-    const int32_t* const table = a.b.table + (int64_t)s * a.b.table_stride;
-    const uint8_t* const kp = static_cast<const uint8_t*>(a.kv.k) + (int64_t)hk * a.kv.head_stride * S::kSize;
-    const uint8_t* const vp = static_cast<const uint8_t*>(a.kv.v) + (int64_t)hk * a.kv.head_stride * S::kSize;
-    const float scale = a.scale * (a.kv.k_scale ? a.kv.k_scale[hk] : 1.0f);
+    const Segment sg(line, u, end, lane);
+    u = sg.next;
+    if (sg.tile1 <= sg.tile0) continue;
+    const int base = (sg.len < 0 ? 0 : sg.len) - sg.count;   // (fewer than 2^30 rows)
+    const int t_end = sg.tile1 * kAtUnit < sg.seen ? sg.tile1 * kAtUnit : sg.seen;
+    const int32_t* const table = a.b.table + (int64_t)sg.s * a.b.table_stride;
+    const uint8_t* const kp = static_cast<const uint8_t*>(a.kv.k) + (int64_t)sg.hk * a.kv.head_stride * S::kSize;
+    const uint8_t* const vp = static_cast<const uint8_t*>(a.kv.v) + (int64_t)sg.hk * a.kv.head_stride * S::kSize;
+    const float scale = a.scale * (a.kv.k_scale ? a.kv.k_scale[sg.hk] : 1.0f);
 
-    // this wave's rows of q
+    // the first step's keys and values, then q
+    Pages<S::kSize> pages;                                   // of 32 steps, two a step
+    RawTile<DIM, E4M3> key, val;
+    int t = sg.tile0 * kAtUnit + w * 32, i = 0;
+    pages.fill(a, table, t + (lane >> 1) * 128 + (lane & 1) * 16, t_end);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) key.load_keys(h, pages.tile(a, kp, h, row_bytes), k_off);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) val.load_values(h, pages.tile(a, vp, h, row_bytes), v_off, row_bytes);
     bf16x8 q[NQ][S::kFrag];
-    int new_j[NQ];
-    uint64_t tree[NQ];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const uint32_t row = block * kRows + (wr * NQ + n) * 16 + r;
-      const bool real = row < (uint32_t)count * (uint32_t)a.group;
-      const uint32_t j = real ? row / (uint32_t)a.group : 0, h = real ? row - j * a.group : 0;
-      new_j[n] = (int)j;
-      tree[n] = a.b.tree ? a.b.tree[first + (int)j] : 0;
-      const uint16_t* const qr = a.q + (int64_t)(first + (int)j) * a.ldq + ((int64_t)hk * a.group + h) * DIM;
-#pragma unroll
-      for (int f = 0; f < S::kFrag; ++f) {
-        u32x4 v = *reinterpret_cast<const u32x4*>(qr + KeyTile<DIM, E4M3>::column(f, g));
-        if (!real) v = u32x4{0, 0, 0, 0};
-        q[n][f] = as_bf16(v);
-      }
-    }
-
+    SeenBy sees[NQ];
     floatx4 acc[NQ][S::kSubs];
     float m[NQ], l[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
+      sees[n] = load_query<DIM, E4M3>(a, sg, sg.block * kRows + 16 * n + r, g, q[n]);
       m[n] = -INFINITY;
       l[n] = 0.0f;
 #pragma unroll
       for (int c = 0; c < S::kSubs; ++c) acc[n][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // the pages of this wave's next 32 steps, two tiles of 16 places each: a lane per tile
-    int page = -1, in_page = 0;
-    const auto pages = [&](int t0) {
-      const int t = t0 + (lane >> 1) * (32 * kTg) + (lane & 1) * 16;
-      const uint32_t tile = (uint32_t)t / 16u;
-      const uint32_t p = a.page_tiles == 1 ? tile : __umulhi(tile, a.page_magic);
-      in_page = (int)(tile - p * (uint32_t)a.page_tiles);
-      page = -1;
-      if (t < t_end) {
-        const int v = table[p];
-        if (v >= 0 && v < a.kv.pages) page = v;
-      }
-    };
-    // (a tile that does not exist reads page 0, and is masked)
-    const auto tile_at = [&](const uint8_t* p, int i) {
-      const int pg = lane_get(page, i), in = lane_get(in_page, i);
-      const int64_t at = (int64_t)(pg & ~(pg >> 31)) * a.kv.page_stride * S::kSize + (int64_t)in * 16 * row_bytes;
-      return make_rsrc(p + at, 0x7FFFFFFF);
-    };
-
-    KeyTile<DIM, E4M3> key[2];
-    ValueTile<DIM, E4M3> val;
-    int t = tile0 * kAtUnit + tg * 32, i = 0;
-    if (t < t_end) {
-      pages(t);
-      key[0].load(tile_at(kp, 0), k_off);
-      key[1].load(tile_at(kp, 1), k_off);
-      val.load4(0, tile_at(vp, 0), v_off, row_bytes);
-      val.load4(4, tile_at(vp, 1), v_off, row_bytes);
-    }
     while (t < t_end) {
-      const int pg0 = lane_get(page, 2 * i), pg1 = lane_get(page, 2 * i + 1);
+      const int pg0 = lane_get(pages.page, 2 * i), pg1 = lane_get(pages.page, 2 * i + 1);
       floatx4 sc[NQ][2];
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
@@ -330,41 +561,24 @@ __global__ __launch_bounds__(kBlock, (DIM * NQ <= 128 ? 3 : 2)) void k_attention
       for (int f = 0; f < S::kFrag; ++f)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const bf16x8 kf = key[h].frag(f);
+          const bf16x8 kf = key.key(h, f);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) sc[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][f], sc[n][h], 0, 0, 0);
         }
       // the next step's keys, in flight while this one's values are used
-      const int t_next = t + 32 * kTg;
-      ++i;
-      if (i == 32) {
-        pages(t_next);
+      const int t_next = t + 128;
+      if (++i == 32) {
+        pages.fill(a, table, t_next + (lane >> 1) * 128 + (lane & 1) * 16, t_end);
         i = 0;
       }
-      key[0].load(tile_at(kp, 2 * i), k_off);                // (past the end: page 0)
-      key[1].load(tile_at(kp, 2 * i + 1), k_off);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) key.load_keys(h, pages.tile(a, kp, 2 * i + h, row_bytes), k_off);
 
       const bool masked = !(t + 32 <= base && pg0 >= 0 && pg1 >= 0);
-      uint32_t hide[NQ];                                     // places that a row does not see
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) hide[n] = 0;
       int tm = t + 4 * g;                                    // (made here: few steps are masked)
       asm volatile("" : "+v"(tm));
-      const auto there = [&](int e) { return tm + (e < 4 ? e : 12 + e) < seen && (e < 4 ? pg0 : pg1) >= 0; };
-      const auto sees = [&](int n, int bit) {            // place base + bit
-        return bit < 0 || (a.b.tree ? bit < count && bit < 64 && (tree[n] >> (bit & 63) & 1) : bit <= new_j[n]);
-      };
-      if (masked) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int bit = tm + (e < 4 ? e : 12 + e) - base;
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-            if (!there(e) || !sees(n, bit)) hide[n] |= 1u << e;
-        }
-      }
-
-      bf16x8 ph[NQ], pl[NQ];
+      const auto there = [&](int e) { return (tm + (e < 4 ? e : 12 + e) < sg.seen) & ((e < 4 ? pg0 : pg1) >= 0); };
+      u32x4 ph[NQ], pl[NQ];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         float x[8];
@@ -372,46 +586,18 @@ __global__ __launch_bounds__(kBlock, (DIM * NQ <= 128 ? 3 : 2)) void k_attention
         for (int e = 0; e < 8; ++e) x[e] = sc[n][e / 4][e % 4] * scale;
         if (masked) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = hide[n] >> e & 1u ? -INFINITY : x[e];
+          for (int e = 0; e < 8; ++e)
+            x[e] = (there(e) & sees[n](tm + (e < 4 ? e : 12 + e) - base)) ? x[e] : -INFINITY;
         }
-        float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-        if (__ballot(top > m[n] + kAtSlack)) {
-          top = fmaxf(top, __shfl_xor(top, 16));
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const float now = fmaxf(m[n], top);
-          const float f = m[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[n] - now);
-          m[n] = now;
-          l[n] *= f;
-#pragma unroll
-          for (int c = 0; c < S::kSubs; ++c) acc[n][c] *= f;
-        }
-        const float ref = m[n] == -INFINITY ? 0.0f : m[n];
-        uint32_t hi[4], lo[4];
-        float p[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          p[e] = __builtin_amdgcn_exp2f(x[e] - ref);
-          l[n] += p[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          hi[e] = __builtin_amdgcn_perm(__float_as_uint(p[2 * e + 1]), __float_as_uint(p[2 * e]), 0x07060302u);
-          const float r0 = p[2 * e] - __uint_as_float(hi[e] << 16);
-          const float r1 = p[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u);
-          const bf16x2 rr = {(__bf16)r0, (__bf16)r1};
-          lo[e] = __builtin_bit_cast(uint32_t, rr);
-        }
-        ph[n] = as_bf16(u32x4{hi[0], hi[1], hi[2], hi[3]});
-        pl[n] = as_bf16(u32x4{lo[0], lo[1], lo[2], lo[3]});
+        soften<E4M3>(x, m[n], l[n], acc[n], ph[n], pl[n]);
       }
-
       if (masked) {
         // places of V with a NaN or an infinity, where some rows may not see them: one at a time, for the
         // rows that do; then they and the places that do not exist are nothing
         uint32_t odd = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (there(e) && val.odd(e)) odd |= 1u << e;
+          odd |= (there(e) & val.odd(e)) ? 1u << e : 0u;
         if (__ballot(odd != 0)) {
 #pragma unroll 1
           for (int k = 0; k < 32; ++k) {
@@ -421,190 +607,290 @@ __global__ __launch_bounds__(kBlock, (DIM * NQ <= 128 ? 3 : 2)) void k_attention
             const uint32_t mine = g == g1 ? (e & 1) ? 0xFFFF0000u : 0x0000FFFFu : 0u;
 #pragma unroll
             for (int c = 0; c < S::kSubs; ++c) {
-              u32x4 vf = val.frag(c);
+              u32x4 vf = val.value(c);
 #pragma unroll
               for (int p = 0; p < 4; ++p) vf[p] &= p == e >> 1 ? mine : 0u;
 #pragma unroll
               for (int n = 0; n < NQ; ++n) {
                 floatx4 one = {0.0f, 0.0f, 0.0f, 0.0f};
-                one = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf), ph[n], one, 0, 0, 0);
-                one = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(vf), pl[n], one, 0, 0, 0);
-                if (sees(n, bit)) acc[n][c] += one;
+                one = mfma_pv<E4M3>(vf, ph[n], one);
+                if constexpr (!E4M3) one = mfma_pv<E4M3>(vf, pl[n], one);
+                acc[n][c] = sees[n](bit) ? acc[n][c] + one : acc[n][c];
               }
               __builtin_amdgcn_sched_barrier(0);             // (one block's registers at a time)
             }
           }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) val.clear(e, !there(e) || (odd >> e & 1));
+        for (int e = 0; e < 8; ++e) val.clear(e, !there(e) | (odd >> e & 1));
       }
 #pragma unroll
       for (int c = 0; c < S::kSubs; ++c) {
-        const bf16x8 vf = as_bf16(val.frag(c));
+        const u32x4 vf = val.value(c);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          acc[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, ph[n], acc[n][c], 0, 0, 0);
-          acc[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl[n], acc[n][c], 0, 0, 0);
+          acc[n][c] = mfma_pv<E4M3>(vf, ph[n], acc[n][c]);
+          if constexpr (!E4M3) acc[n][c] = mfma_pv<E4M3>(vf, pl[n], acc[n][c]);
         }
       }
-      val.load4(0, tile_at(vp, 2 * i), v_off, row_bytes);
-      val.load4(4, tile_at(vp, 2 * i + 1), v_off, row_bytes);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) val.load_values(h, pages.tile(a, vp, 2 * i + h, row_bytes), v_off, row_bytes);
       t = t_next;
     }
 
     // the waves' sums of the same rows into one (its addresses are made here: no registers kept for them)
     int tj = tid;
     asm volatile("" : "+v"(tj));
-    const int r = tj & 15, g = tj >> 4 & 3;
+    const int rj = tj & 15, gj = tj >> 4 & 3;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       l[n] += __shfl_xor(l[n], 16);
       l[n] += __shfl_xor(l[n], 32);
-      if (g == 0) {
-        s_m[w][16 * n + r] = m[n];
-        s_l[w][16 * n + r] = l[n];
+      if (gj == 0) {
+        s_m[w][16 * n + rj] = m[n];
+        s_l[w][16 * n + rj] = l[n];
       }
     }
     __syncthreads();
-    const bool whole = tile0 == 0 && tile1 == tiles;
-    // a partial's slot: the workgroup's second if the segment begins here, else its first
-    const int slot = 2 * wg + (tile0 == 0 ? 1 : 0);
-    constexpr int kPart = kRows * (DIM + 2);
-    const uint32_t nrows = (uint32_t)count * (uint32_t)a.group - (uint32_t)(block * kRows);
-    const int valid = nrows < (uint32_t)kRows ? (int)nrows : kRows;
-    const Rsrc part = make_rsrc(a.part + (size_t)slot * kPart, kPart * 4);
-    const float vs = a.kv.v_scale ? a.kv.v_scale[hk] : 1.0f;
-#pragma unroll 1
+    const int valid = sg.valid(a.group, kRows);
+    const Partial<DIM, kRows> part(a, blockIdx.x, blockIdx.x == (uint32_t)sg.from);
+    const float vs = a.kv.v_scale ? a.kv.v_scale[sg.hk] : 1.0f;
+#pragma unroll
     for (int n = 0; n < NQ; ++n) {
 #pragma unroll
       for (int blk = 0; blk < DIM / kCols; ++blk) {
         // columns blk kCols .. of the waves' outputs, relative to the rows' common maximum
         if (n > 0 || blk > 0) __syncthreads();
+        const float top = fmaxf(fmaxf(s_m[0][16 * n + rj], s_m[1][16 * n + rj]), fmaxf(s_m[2][16 * n + rj], s_m[3][16 * n + rj]));
+        const float f = m[n] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[n] - top);
 #pragma unroll
-        for (int nn = 0; nn < NQ; ++nn) {
-          if (nn != n) continue;
-          float top = -INFINITY;
+        for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
-          for (int v = 0; v < kTg; ++v) top = fmaxf(top, s_m[v * WR + wr][16 * nn + r]);
-          const float f = m[nn] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[nn] - top);
+          for (int c = 0; c < S::kSubs; ++c) {
+            // column of block c's row 4 g + ii
+            const int col = c / S::kRun * (16 * S::kRun) + S::kRun * (4 * gj + ii) + c % S::kRun;
+            if (col >= blk * kCols && col < (blk + 1) * kCols) s_o[w][rj][col - blk * kCols] = acc[n][c][ii] * f;
+          }
+        __syncthreads();
+        // 16 rows x kCols columns, four columns a thread at a time
+        for (int it = tj; it < 16 * kCols / 4; it += kBlock) {
+          const int c4 = it % (kCols / 4), rr = 16 * n + it / (kCols / 4);
+          if (rr >= valid) continue;
+          const float tp = fmaxf(fmaxf(s_m[0][rr], s_m[1][rr]), fmaxf(s_m[2][rr], s_m[3][rr]));
+          float sum = 0.0f;
+          floatx4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int ii = 0; ii < 4; ++ii) {
+          for (int v = 0; v < 4; ++v) {
+            const float mv = s_m[v][rr];
+            sum += mv == -INFINITY ? s_l[v][rr] : s_l[v][rr] * __builtin_amdgcn_exp2f(mv - tp);
+            o += *reinterpret_cast<const floatx4*>(&s_o[v][rr - 16 * n][4 * c4]);
+          }
+          const int col = blk * kCols + 4 * c4;
+          if (sg.whole) {
+            attn_put<DIM>(a, sg, sg.block * kRows + rr, col, o * (sum == 0.0f ? 0.0f : vs / sum));
+          } else {
+            part.put(rr, col, o);
+            if (col == 0) part.put_ml(rr, tp, sum);
+          }
+        }
+      }
+    }
+    if (!sg.whole) attn_join<DIM, kRows>(a, sg, valid, vs, tj, &s_last);
+    __syncthreads();
+  }
+}
+
+// 64 rows of q, 16 a wave, all waves on the same 64 places: a wave loads the keys or the values of 32 of
+// them (waves 0, 1 and 2, 3), turns them into operands once and leaves those in LDS for all four.
+// Without that every wave would convert and turn everything, which takes longer than to load it.
+template <int DIM, bool E4M3>
+__global__ __launch_bounds__(kBlock, 2) void k_attention_rows(AttnArgs a) {
+  using S = AttnShape<DIM, E4M3>;
+  constexpr int kRows = 64;
+  __shared__ u32x4 s_kv[2][2 * S::kSubs][64];                // per 32 places: keys (two 16s), then values
+  __shared__ uint32_t s_odd[2];                              // per 32 places: those with a NaN or an infinity
+  __shared__ int s_last;
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), half = w & 1;
+  const bool keys = w < 2;
+
+  UnitLine line(a, kRows);
+  const int total = line.start(lane);
+  int u = blockIdx.x * line.share;
+  const int end = u + line.share < total ? u + line.share : total;
+  const uint32_t row_bytes = (uint32_t)a.kv.token_stride * S::kSize;
+  const uint32_t k_off = r * row_bytes + 16 * g;
+  const uint32_t v_off = 4 * g * row_bytes + r * S::kRun * S::kSize;
+
+  while (u < end) {
+    const Segment sg(line, u, end, lane);
+    u = sg.next;
+    if (sg.tile1 <= sg.tile0) continue;
+    const int base = (sg.len < 0 ? 0 : sg.len) - sg.count;
+    const int t_end = sg.tile1 * kAtUnit < sg.seen ? sg.tile1 * kAtUnit : sg.seen;
+    const int32_t* const table = a.b.table + (int64_t)sg.s * a.b.table_stride;
+    const uint8_t* const src = static_cast<const uint8_t*>(keys ? a.kv.k : a.kv.v) + (int64_t)sg.hk * a.kv.head_stride * S::kSize;
+    const float scale = a.scale * (a.kv.k_scale ? a.kv.k_scale[sg.hk] : 1.0f);
+    const int valid = sg.valid(a.group, kRows);
+
+    Pages<S::kSize> pages;                                   // of 16 steps, four a step
+    RawTile<DIM, E4M3> raw;
+    const auto load = [&](int i) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const Rsrc b = pages.tile(a, src, 4 * i + 2 * half + h, row_bytes);
+        if (keys) raw.load_keys(h, b, k_off);
+        else raw.load_values(h, b, v_off, row_bytes);
+      }
+    };
+    int t = sg.tile0 * kAtUnit, i = 0;
+    pages.fill(a, table, t + lane * 16, t_end);
+    load(0);
+    bf16x8 q[S::kFrag];
+    const SeenBy sees = load_query<DIM, E4M3>(a, sg, sg.block * kRows + 16 * w + r, g, q);
+    floatx4 acc[S::kSubs];
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int c = 0; c < S::kSubs; ++c) acc[c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    while (t < t_end) {
+      int pg[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pg[k] = lane_get(pages.page, 4 * i + k);
+      // operands into LDS
+      if (keys) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int f = 0; f < S::kFrag; ++f) s_kv[half][h * S::kFrag + f][lane] = __builtin_bit_cast(u32x4, raw.key(h, f));
+      } else {
+        const int t0 = t + 32 * half, p0 = half ? pg[2] : pg[0], p1 = half ? pg[3] : pg[1];
+        uint32_t odd = 0;
+        if (!(t0 + 32 <= base && p0 >= 0 && p1 >= 0)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const bool there = (t0 + 4 * g + (e < 4 ? e : 12 + e) < sg.seen) & ((e < 4 ? p0 : p1) >= 0);
+            const uint64_t bl = __ballot(there & raw.odd(e));
+#pragma unroll
+            for (int g1 = 0; g1 < 4; ++g1) odd |= (bl >> (16 * g1) & 0xFFFFu) != 0 ? 1u << (4 * e + g1) : 0u;
+            raw.clear(e, !there);
+          }
+        }
+        if (lane == 0) s_odd[half] = odd;
+#pragma unroll
+        for (int c = 0; c < S::kSubs; ++c) s_kv[half][S::kSubs + c][lane] = raw.value(c);
+      }
+      // the next step's, in flight
+      const int t_next = t + 64;
+      if (++i == 16) {
+        pages.fill(a, table, t_next + lane * 16, t_end);
+        i = 0;
+      }
+      load(i);
+      lds_barrier();
+
+      if (16 * w < valid) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int t0 = t + 32 * k;
+          if (k > 0 && t0 >= t_end) break;
+          floatx4 sc[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            sc[h] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int f = 0; f < S::kFrag; ++f)
+              sc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(s_kv[k][h * S::kFrag + f][lane]), q[f], sc[h], 0, 0, 0);
+          }
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = sc[e / 4][e % 4] * scale;
+          if (!(t0 + 32 <= base && pg[2 * k] >= 0 && pg[2 * k + 1] >= 0)) {
+            int tm = t0 + 4 * g;                             // (made here: few steps are masked)
+            asm volatile("" : "+v"(tm));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int at = tm + (e < 4 ? e : 12 + e);
+              x[e] = ((at < sg.seen) & (pg[2 * k + e / 4] >= 0) & sees(at - base)) ? x[e] : -INFINITY;
+            }
+          }
+          u32x4 ph, pl;
+          soften<E4M3>(x, m, l, acc, ph, pl);
+          const uint32_t odd = __builtin_amdgcn_readfirstlane(s_odd[k]);
+          if (odd == 0) {
 #pragma unroll
             for (int c = 0; c < S::kSubs; ++c) {
-              // column of block c's row 4 g + ii
-              const int col0 = c / S::kRun * (16 * S::kRun) + c % S::kRun;
-              constexpr int kHalf = S::kRuns > 1 ? 1 : 0;
-              const int col = col0 + S::kRun * (4 * g + ii);
-              if (kHalf || DIM == kCols) {
-                if (c / (kCols / 16) == blk || DIM == kCols) s_o[w][r][col - blk * kCols] = acc[nn][c][ii] * f;
-              } else if ((4 * g + ii) / 8 == blk) {
-                s_o[w][r][col - blk * kCols] = acc[nn][c][ii] * f;
+              const u32x4 vf = s_kv[k][S::kSubs + c][lane];
+              acc[c] = mfma_pv<E4M3>(vf, ph, acc[c]);
+              if constexpr (!E4M3) acc[c] = mfma_pv<E4M3>(vf, pl, acc[c]);
+            }
+          } else {
+            // places with a NaN or an infinity, which some rows may not see: the others first, then one at
+            // a time, for the rows that do
+#pragma unroll 1
+            for (int z = -1; z < 32; ++z) {
+              if (z >= 0 && !(odd >> z & 1)) continue;
+              u32x4 mine = {0, 0, 0, 0};
+              for (int e = 0; e < 8; ++e) {
+                const bool on = z < 0 ? !(odd >> (4 * e + g) & 1) : 4 * e + g == z;
+                if (on) mine[e / 2] |= (e & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+              }
+              const int e = z >> 2, bit = t0 + 4 * (z & 3) + (e < 4 ? e : 12 + e) - base;
+              const bool mine_too = (z < 0) | sees(bit);
+#pragma unroll
+              for (int c = 0; c < S::kSubs; ++c) {
+                const u32x4 vf = s_kv[k][S::kSubs + c][lane] & mine;
+                floatx4 one = {0.0f, 0.0f, 0.0f, 0.0f};
+                one = mfma_pv<E4M3>(vf, ph, one);
+                if constexpr (!E4M3) one = mfma_pv<E4M3>(vf, pl, one);
+                acc[c] = mine_too ? acc[c] + one : acc[c];
+                __builtin_amdgcn_sched_barrier(0);
               }
             }
           }
         }
-        __syncthreads();
-        // WR blocks of 16 rows x kCols columns, four columns a thread at a time
-        constexpr int kItems = WR * 16 * kCols / 4;
-        for (int it = tj; it < kItems; it += kBlock) {
-          const int c4 = it % (kCols / 4), rr = it / (kCols / 4) % 16, gr = it / (kCols / 4 * 16);
-          const int row = (gr * NQ + n) * 16 + rr;
-          if (row >= valid) continue;
-          float top = -INFINITY;
-#pragma unroll
-          for (int v = 0; v < kTg; ++v) top = fmaxf(top, s_m[v * WR + gr][16 * n + rr]);
-          float sum = 0.0f;
-          floatx4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int v = 0; v < kTg; ++v) {
-            const float mv = s_m[v * WR + gr][16 * n + rr];
-            sum += mv == -INFINITY ? s_l[v * WR + gr][16 * n + rr] : s_l[v * WR + gr][16 * n + rr] * __builtin_amdgcn_exp2f(mv - top);
-            o += *reinterpret_cast<const floatx4*>(&s_o[v * WR + gr][rr][4 * c4]);
-          }
-          const int col = blk * kCols + 4 * c4;
-          if (whole) {
-            const float f = sum == 0.0f ? 0.0f : vs / sum;
-            const uint32_t rq = block * kRows + row, j = rq / (uint32_t)a.group, h = rq - j * a.group;
-            uint16_t* const out = a.y + ((int64_t)(first + (int)j) * a.hq + (int64_t)hk * a.group + h) * DIM + col;
-            u32x2 v;
-            v[0] = (uint32_t)float_to_bf16_rne(o[0] * f) | (uint32_t)float_to_bf16_rne(o[1] * f) << 16;
-            v[1] = (uint32_t)float_to_bf16_rne(o[2] * f) | (uint32_t)float_to_bf16_rne(o[3] * f) << 16;
-            *reinterpret_cast<u32x2*>(out) = v;
-          } else {
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), part, (row * DIM + col) * 4, 0, kAuxAgent);
-            if (col == 0) {
-              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(top), part, (kRows * DIM + row) * 4, 0, kAuxAgent);
-              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), part, (kRows * (DIM + 1) + row) * 4, 0, kAuxAgent);
-            }
-          }
-        }
       }
+      lds_barrier();
+      t = t_next;
     }
-    if (!whole) {
-      // the workgroups that share the segment: first to last of those that own its units
-      const int from = seg / share, to = (seg + tiles - 1) / share;
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      if (tj == 0) {
-        const uint32_t old = __hip_atomic_fetch_add(&a.count[from], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = old == (uint32_t)(to - from) ? 1 : 0;
-        if (s_last) __hip_atomic_store(&a.count[from], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-      __syncthreads();
-      if (s_last) {
-        asm volatile("" ::: "memory");
-        for (int it = tj; it < valid * (DIM / 4); it += kBlock) {
-          const int row = it / (DIM / 4), col = it % (DIM / 4) * 4;
-          float top = -INFINITY, sum = 0.0f;
-          for (int p = from; p <= to; ++p) {
-            const Rsrc b = make_rsrc(a.part + (size_t)(2 * p + (p == from ? 1 : 0)) * kPart, kPart * 4);
-            top = fmaxf(top, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, (kRows * DIM + row) * 4, 0, kAuxAgent)));
-          }
-          floatx4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-          for (int p = from; p <= to; ++p) {
-            const Rsrc b = make_rsrc(a.part + (size_t)(2 * p + (p == from ? 1 : 0)) * kPart, kPart * 4);
-            const float mv = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, (kRows * DIM + row) * 4, 0, kAuxAgent));
-            const float lv = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, (kRows * (DIM + 1) + row) * 4, 0, kAuxAgent));
-            const floatx4 ov = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(b, (row * DIM + col) * 4, 0, kAuxAgent));
-            const float f = mv == -INFINITY ? (lv == lv ? 0.0f : lv) : __builtin_amdgcn_exp2f(mv - top);
-            sum += lv * f;
-            o += ov * f;
-          }
-          const float f = sum == 0.0f ? 0.0f : vs / sum;
-          const uint32_t rq = block * kRows + row, j = rq / (uint32_t)a.group, h = rq - j * a.group;
-          uint16_t* const out = a.y + ((int64_t)(first + (int)j) * a.hq + (int64_t)hk * a.group + h) * DIM + col;
-          u32x2 v;
-          v[0] = (uint32_t)float_to_bf16_rne(o[0] * f) | (uint32_t)float_to_bf16_rne(o[1] * f) << 16;
-          v[1] = (uint32_t)float_to_bf16_rne(o[2] * f) | (uint32_t)float_to_bf16_rne(o[3] * f) << 16;
-          *reinterpret_cast<u32x2*>(out) = v;
+
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    const float vs = a.kv.v_scale ? a.kv.v_scale[sg.hk] : 1.0f;
+    const int row = 16 * w + r;
+    if (row < valid) {
+      const Partial<DIM, kRows> part(a, blockIdx.x, blockIdx.x == (uint32_t)sg.from);
+      const float f = sg.whole ? l == 0.0f ? 0.0f : vs / l : 1.0f;
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+        for (int c = 0; c < S::kSubs; c += 4) {
+          const int col = c / S::kRun * (16 * S::kRun) + S::kRun * (4 * g + ii) + c % S::kRun;
+          const floatx4 o = floatx4{acc[c][ii], acc[c + 1][ii], acc[c + 2][ii], acc[c + 3][ii]} * f;
+          if (sg.whole) attn_put<DIM>(a, sg, sg.block * kRows + row, col, o);
+          else part.put(row, col, o);
         }
-      }
+      if (!sg.whole && g == 0) part.put_ml(row, m, l);
     }
+    if (!sg.whole) attn_join<DIM, kRows>(a, sg, valid, vs, tid, &s_last);
     __syncthreads();
   }
 }
 
 // Rows of q a workgroup takes at once, by the average of a sequence.
 struct AttnPlan {
-  int nq, wr, rows;
+  int rows;               // 16, 32: k_attention, 64: k_attention_rows
   int wgs;
   bool fits;              // the line of units has fewer than 2^31
 };
 static AttnPlan attn_plan(const DevInfo& di, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b) {
   const int64_t group = hq / kv.heads, avg = (m * group + b.seqs - 1) / b.seqs;
   AttnPlan p;
-  if (kv.dim == 256) {
-    p.nq = 1;
-    p.wr = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
-  } else {
-    p.nq = avg <= 16 ? 1 : 2;
-    p.wr = avg <= 32 ? 1 : 2;
-  }
-  p.rows = 16 * p.nq * p.wr;
+  p.rows = avg <= 16 ? 16 : avg <= 32 && kv.dim <= 128 ? 32 : 64;
   const double most = ((double)m * group / p.rows + (double)b.seqs) * (double)kv.heads *
                       ((double)b.cols * kv.page / kAtUnit + 1.0);
   p.fits = most < 2147483648.0 && m * hq < (int64_t(1) << 30);
-  p.wgs = di.cus * 2;
+  p.wgs = di.cus * (p.rows == 64 ? 2 : 1);
   if (p.fits && most < p.wgs) p.wgs = (int)most + 1;
   return p;
 }
@@ -623,11 +909,13 @@ uint64_t attention_scratch(const DevInfo& di, int64_t m, int64_t hq, const KvArg
   return *zero + 2 * (uint64_t)p.wgs * attn_part(p, kv.dim);
 }
 
-template <int DIM, int NQ, int WR>
-static void attn_go(const AttnArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.wgs);
-  if (a.kv.e4m3) hipLaunchKernelGGL((k_attention<DIM, true, NQ, WR>), grid, dim3(kBlock), 0, s, a);
-  else hipLaunchKernelGGL((k_attention<DIM, false, NQ, WR>), grid, dim3(kBlock), 0, s, a);
+template <int DIM, bool E4M3>
+static void attn_go(const AttnPlan& p, const AttnArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)a.wgs), block(kBlock);
+  if (p.rows == 64) hipLaunchKernelGGL((k_attention_rows<DIM, E4M3>), grid, block, 0, s, a);
+  else if constexpr (DIM == 256) hipLaunchKernelGGL((k_attention<DIM, E4M3, 1>), grid, block, 0, s, a);
+  else if (p.rows == 32) hipLaunchKernelGGL((k_attention<DIM, E4M3, 2>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_attention<DIM, E4M3, 1>), grid, block, 0, s, a);
 }
 
 hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t hq, const KvArgs& kv,
@@ -650,19 +938,9 @@ hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t h
   a.wgs = p.wgs;
   a.count = static_cast<uint32_t*>(scratch);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + kAtCounts * sizeof(uint32_t));
-  if (kv.dim == 64) {
-    if (p.wr == 2) attn_go<64, 2, 2>(a, s);
-    else if (p.nq == 2) attn_go<64, 2, 1>(a, s);
-    else attn_go<64, 1, 1>(a, s);
-  } else if (kv.dim == 128) {
-    if (p.wr == 2) attn_go<128, 2, 2>(a, s);
-    else if (p.nq == 2) attn_go<128, 2, 1>(a, s);
-    else attn_go<128, 1, 1>(a, s);
-  } else {
-    if (p.wr == 4) attn_go<256, 1, 4>(a, s);
-    else if (p.wr == 2) attn_go<256, 1, 2>(a, s);
-    else attn_go<256, 1, 1>(a, s);
-  }
+  if (kv.dim == 64) kv.e4m3 ? attn_go<64, true>(p, a, s) : attn_go<64, false>(p, a, s);
+  else if (kv.dim == 128) kv.e4m3 ? attn_go<128, true>(p, a, s) : attn_go<128, false>(p, a, s);
+  else kv.e4m3 ? attn_go<256, true>(p, a, s) : attn_go<256, false>(p, a, s);
   return hipGetLastError();
 }
 

@@ -5,8 +5,10 @@ Tolerances.  u = 2^-24 is half a float step, h = 2^-8 half a bfloat16 step, both
     h |x| for bfloat16, for e4m3 after the division (u more) 2^-4 |x|, or half its smallest step, 2^-10;
     a float error may move a value over a border between two roundings, so both add up.
   attention: a score is a sum of dim products and a few scalings, off by (dim + 8) u sum |q k| scale; a
-    probability by twice that and the exponential's own 4 u, and 2^-16 from its 16 bits; the output is
-    a sum over len terms (len + 8) u, all times sum p |v|; then the rounding h |y|.
+    probability by twice that and the exponential's own 4 u, and 2^-16 from its 16 bits (e4m3: float16's
+    half step 2^-11; below its normal range half its smallest step, 2^-25 of probabilities brought up
+    by 2^7, that is 2^-32 of the largest one for each place); the output is a sum over len terms, (len + 8) u,
+    all times sum p |v| (the last but one times the largest |v|); then the rounding h |y|.
   sampling: integers exact; a log probability to u of itself and of the largest term it is the difference of.
 """
 import numpy as np
@@ -207,8 +209,12 @@ def check_attention(st, q, hq, y, scale=None):
     mine = ~np.isnan(want).all(axis=2)
     assert np.all(got[~mine] == 7.0)                          # rows behind the last sequence
     ds = (st.dim + 8) * U * big
-    rel = 2 * ds + 4 * U + 2.0 ** -16 + (st.lens.max() + 8) * U
+    e4m3 = st.k.dtype == torch.float8_e4m3fn
+    rel = 2 * ds + 4 * U + (2.0 ** -11 if e4m3 else 2.0 ** -16) + (st.lens.max() + 8) * U
     tol = H * np.abs(want) + (1 + H) * rel[:, :, None] * mag
+    if e4m3:
+        v = np.abs(st.values(1))
+        tol += (1 + H) * st.lens.max() * 2.0 ** -32 * v[np.isfinite(v)].max()
     bad = ~(np.abs(got - want) <= tol)
     assert not bad[mine].any(), (np.argwhere(bad & mine[:, :, None])[:5], np.abs(got - want)[mine].max())
     return mine
