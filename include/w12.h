@@ -468,19 +468,16 @@ int w12_kv_append(const void *q, int64_t ldq, const void *k, int64_t ldk, const 
  * before the new tokens (t < lens - T) and of the new ones those up to its own -- or with batch->tree
  * those t = lens - T + b, b < min(T, 64), whose bit b its mask tree[i] has (the nodes of a draft tree on its path:
  * figure-captions page, Fig. 6).  A row that sees nothing, or only scores of -Inf, gives zeros.
- * Values of places that a row does not see never reach it, NaN and infinities included; a NaN it
- * sees gives NaN.  q: bfloat16, row i at q + i * ldq elements (16-byte aligned, ldq a multiple of 8); y:
+ * Values of places that a row does not see never reach it, NaN and infinities included; a NaN or an
+ * infinity it sees gives NaN or an infinity.  q: bfloat16, row i at q + i * ldq elements (16-byte aligned, ldq a multiple of 8); y:
  * [m][hq * dim] bfloat16 (16-byte aligned), rounded once to nearest even.  Scores, softmax and sums
- * are held in float, the probabilities that meet v in 16 significant bits.
+ * are held in float, the probabilities that meet v in 16 significant bits (11 over an e4m3 cache).
  * scratch: w12_attention_scratch bytes of the caller's device memory (16-byte aligned), in use until
- * the call's work on `stream` is finished.  Its first w12_attention_scratch's *zero bytes are counters
- * that must be zero when the work starts and are zero again when it ends: clear them once, then reuse
- * the scratch for calls of any sizes that follow each other on one stream.  Calls with different
+ * the call's work on `stream` is finished; what it holds before does not matter.  Calls with different
  * scratch never touch each other's.  Which places are summed together depends on the lengths of the
  * whole batch and the device; equal calls give equal bits.
  */
-int w12_attention_scratch(int64_t m, int64_t hq, const w12_kv *kv, const w12_kv_batch *batch, uint64_t *bytes,
-                          uint64_t *zero);
+int w12_attention_scratch(int64_t m, int64_t hq, const w12_kv *kv, const w12_kv_batch *batch, uint64_t *bytes);
 int w12_attention(const uint16_t *q, int64_t ldq, int64_t m, int64_t hq, const w12_kv *kv,
                   const w12_kv_batch *batch, float scale, uint16_t *y, void *scratch, uint64_t scratch_bytes,
                   uint32_t flags, void *stream);
@@ -503,7 +500,10 @@ int w12_attention(const uint16_t *q, int64_t ldq, int64_t m, int64_t hq, const w
  * temperature of NaN, token -1, logp NaN and kept 0.
  * Weights are computed in double and summed as integers of a step of 2^-62 times the power of two that
  * reaches n, so sums do not depend on their order.  flags: W12_LOGITS_BF16.
- * scratch: w12_sample_scratch bytes, its first *zero bytes counters, as in w12_attention (NULL when 0).
+ * scratch: w12_sample_scratch bytes of the caller's device memory (16-byte aligned; NULL when 0), in use until
+ * the call's work on `stream` is finished.  Its first *zero bytes are counters that must be zero when the
+ * work starts and are zero again when it ends: clear them once, then reuse the scratch for calls of any
+ * sizes that follow each other on one stream.
  */
 int w12_sample_scratch(int64_t m, int64_t n, uint32_t flags, uint64_t *bytes, uint64_t *zero);
 int w12_sample(const void *y, int64_t m, int64_t n, int64_t ldy, const float *temperature, const int32_t *top_k,

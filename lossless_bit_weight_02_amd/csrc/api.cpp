@@ -847,9 +847,8 @@ int w12_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const 
   return ok();
 }
 
-int w12_attention_scratch(int64_t m, int64_t hq, const w12_kv* kv, const w12_kv_batch* batch, uint64_t* bytes,
-                          uint64_t* zero) {
-  if (!bytes || !zero) return fail(W12_ERR_ARG, "bytes or zero is NULL");
+int w12_attention_scratch(int64_t m, int64_t hq, const w12_kv* kv, const w12_kv_batch* batch, uint64_t* bytes) {
+  if (!bytes) return fail(W12_ERR_ARG, "bytes is NULL");
   int rc = check_kv(kv, batch, m);
   if (rc || (rc = check_heads(hq, kv))) return rc;
   w12::DevInfo di;
@@ -857,7 +856,7 @@ int w12_attention_scratch(int64_t m, int64_t hq, const w12_kv* kv, const w12_kv_
   if (e != hipSuccess) return hip_fail(e, "device query");
   if (!w12::attention_fits(di, m, hq, kv_of(kv), batch_of(batch)))
     return fail(W12_ERR_RANGE, "the batch is too large (m * hq from 2^30, or its rows of 16 x tiles of 128 places from 2^31 on)");
-  *bytes = w12::attention_scratch(di, m, hq, kv_of(kv), batch_of(batch), zero);
+  *bytes = w12::attention_scratch(di, m, hq, kv_of(kv), batch_of(batch));
   return ok();
 }
 
@@ -876,8 +875,7 @@ int w12_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t hq, const w
   if (e != hipSuccess) return hip_fail(e, "device query");
   if (!w12::attention_fits(di, m, hq, kv_of(kv), batch_of(batch)))
     return fail(W12_ERR_RANGE, "the batch is too large (m * hq from 2^30, or its rows of 16 x tiles of 128 places from 2^31 on)");
-  uint64_t zero = 0;
-  const uint64_t need = w12::attention_scratch(di, m, hq, kv_of(kv), batch_of(batch), &zero);
+  const uint64_t need = w12::attention_scratch(di, m, hq, kv_of(kv), batch_of(batch));
   if (need > 0) {
     if (!scratch || scratch_bytes < need)
       return fail(W12_ERR_CAPACITY, "scratch of %llu bytes is needed (%llu given)", (unsigned long long)need,

@@ -29,11 +29,16 @@
 namespace w12 {
 
 constexpr int kAtUnit = 128;                      // places of a unit
-constexpr int kAtPiece = 4;                       // units of a segment worth a workgroup of their own
+
+
+
+constexpr int kAtPiece = 8;                       // units of a segment worth a workgroup of their own
 constexpr int kAtStart = 2;                       // units that a segment's beginning and end cost
 constexpr float kAtLog2e = 1.44269504088896340736f;
 constexpr float kAtSlack = 8.0f;                  // powers of two a probability may pass 1 by
-constexpr int kAuxAgent = 16;                     // sc1: stores and loads that every die of the device sees
+constexpr int kAtWideRows = 128, kAtWide = 512;   // rows and threads of k_attention_rows
+
+struct Split;
 
 struct AttnArgs {
   const uint16_t* q;
@@ -47,7 +52,7 @@ struct AttnArgs {
   float scale;            // of the scores, times log2 e
   uint16_t* y;
   int wgs;
-  uint32_t* count;        // [wgs], zero between calls
+  Split* split;           // [wgs]
   float* part;            // [2 wgs] partials: [rows][dim] sums, [rows] maxima, [rows] sums of probabilities
 };
 
@@ -95,14 +100,17 @@ struct AttnShape {
 // A lane's share of 32 places' keys or values as they lie in the cache.
 //   keys:   of place r of either 16, 16 bytes at 64 i + 16 g of the row
 //   values: of places 4 g .. +3 of either 16 (e = 0 .. 3, 4 .. 7), columns kRun r .. of each 16 kRun
-template <int DIM, bool E4M3>
+// PARTS = 2: of one of the 16s (h = 0 here), of one of the runs of columns.
+template <int DIM, bool E4M3, int PARTS = 1>
 struct RawTile {
   using S = AttnShape<DIM, E4M3>;
-  uint32_t w[DIM * S::kSize / 8];
+  static constexpr int kRuns = S::kRuns / PARTS;
+  uint32_t w[DIM * S::kSize / 8 / PARTS];
 
-  __device__ __forceinline__ void load_keys(int h, Rsrc tile, uint32_t off) {
+  __device__ __forceinline__ void load_keys(int h, const uint8_t* at_tile, uint32_t off) {
+    const Rsrc tile = make_rsrc(at_tile, 0x7FFFFFFF);
 #pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) put4(h * S::kLoads + i, __builtin_amdgcn_raw_buffer_load_b128(tile, off + 64 * i, 0, kAuxNT));
+    for (int i = 0; i < S::kLoads; ++i) put4(h * S::kLoads + i, __builtin_amdgcn_raw_buffer_load_b128(tile, off, 64 * i, kAuxNT));
   }
   __device__ __forceinline__ void put4(int i, u32x4 v) {
 #pragma unroll
@@ -115,25 +123,27 @@ struct RawTile {
     else return as_bf16(u32x4{v[4 * f], v[4 * f + 1], v[4 * f + 2], v[4 * f + 3]});
   }
 
-  __device__ __forceinline__ void load_values(int h, Rsrc tile, uint32_t off, uint32_t row_bytes) {
+  __device__ __forceinline__ void load_values(int h, const uint8_t* at_tile, uint32_t off, uint32_t row_bytes) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 4; ++e) {
+      const Rsrc tile = make_rsrc(at_tile + (uint64_t)e * row_bytes, 0x7FFFFFFF);
 #pragma unroll
-      for (int q = 0; q < S::kRuns; ++q) {
-        const uint32_t at = off + 16 * S::kRun * S::kSize * q;
-        const int i = ((4 * h + e) * S::kRuns + q) * S::kRunWords;
+      for (int q = 0; q < kRuns; ++q) {
+        const int at = 16 * S::kRun * S::kSize * q;
+        const int i = ((4 * h + e) * kRuns + q) * S::kRunWords;
         if constexpr (S::kRunWords == 4) {
-          put4(i / 4, __builtin_amdgcn_raw_buffer_load_b128(tile, at, e * row_bytes, kAuxNT));
+          put4(i / 4, __builtin_amdgcn_raw_buffer_load_b128(tile, off, at, kAuxNT));
         } else if constexpr (S::kRunWords == 2) {
-          const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(tile, at, e * row_bytes, kAuxNT);
+          const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(tile, off, at, kAuxNT);
           w[i] = v[0];
           w[i + 1] = v[1];
         } else {
-          w[i] = __builtin_amdgcn_raw_buffer_load_b32(tile, at, e * row_bytes, kAuxNT);
+          w[i] = __builtin_amdgcn_raw_buffer_load_b32(tile, off, at, kAuxNT);
         }
       }
+    }
   }
-  __device__ __forceinline__ uint32_t at(int e, int q, int i) const { return w[(e * S::kRuns + q) * S::kRunWords + i]; }
+  __device__ __forceinline__ uint32_t at(int e, int q, int i) const { return w[(e * kRuns + q) * S::kRunWords + i]; }
   // values as the A operand, block c of the output: rows are the columns kRun r + c % kRun of run c / kRun
   __device__ __forceinline__ u32x4 value(int c) const {
     const int q = c / S::kRun, i = c % S::kRun;
@@ -154,7 +164,7 @@ struct RawTile {
   __device__ __forceinline__ bool odd(int e) const {
     bool r = false;
 #pragma unroll
-    for (int i = 0; i < S::kRuns * S::kRunWords; ++i) {
+    for (int i = 0; i < kRuns * S::kRunWords; ++i) {
       const uint32_t v = at(e, 0, i);
       if constexpr (E4M3) {
 #pragma unroll
@@ -167,8 +177,8 @@ struct RawTile {
   }
   __device__ __forceinline__ void clear(int e, bool yes) {
 #pragma unroll
-    for (int i = 0; i < S::kRuns * S::kRunWords; ++i) {
-      uint32_t& v = w[e * S::kRuns * S::kRunWords + i];
+    for (int i = 0; i < kRuns * S::kRunWords; ++i) {
+      uint32_t& v = w[e * kRuns * S::kRunWords + i];
       v = yes ? 0u : v;
     }
   }
@@ -179,9 +189,6 @@ __device__ __forceinline__ int key_column(int f, int g) {
   return E4M3 ? 64 * (f / 2) + 16 * g + 8 * (f % 2) : 32 * f + 8 * g;
 }
 
-__device__ __forceinline__ float part_f(Rsrc part, int at) {
-  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part, 4 * at, 0, kAuxAgent));
-}
 __device__ __forceinline__ int lane_get(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
 // The batch as a line that the workgroups share out, its sequences 64 at a time, a lane each.  A segment is
@@ -385,114 +392,145 @@ struct Pages {
       if (v >= 0 && v < a.kv.pages) page = v;
     }
   }
-  __device__ __forceinline__ Rsrc tile(const AttnArgs& a, const uint8_t* p, int i, uint32_t row_bytes) const {
+  __device__ __forceinline__ const uint8_t* tile(const AttnArgs& a, const uint8_t* p, int i, uint32_t row_bytes) const {
     const int pg = lane_get(page, i), r = lane_get(in, i);
     const int64_t at = (int64_t)(pg & ~(pg >> 31)) * a.kv.page_stride * SIZE + (int64_t)r * 16 * row_bytes;
-    return make_rsrc(p + at, 0x7FFFFFFF);
+    return p + at;
   }
 };
 
 // Four columns of row `rq` of a sequence's rows for key head hk.
 template <int DIM>
-__device__ __forceinline__ void attn_put(const AttnArgs& a, const Segment& sg, uint32_t rq, int col, floatx4 o) {
+__device__ __forceinline__ void attn_put(const AttnArgs& a, int first, int hk, uint32_t rq, int col, floatx4 o) {
   const uint32_t j = rq / (uint32_t)a.group, h = rq - j * a.group;
   const bf16x2 lo = {(__bf16)o[0], (__bf16)o[1]}, hi = {(__bf16)o[2], (__bf16)o[3]};
   u32x2 v;
   v[0] = __builtin_bit_cast(uint32_t, lo);
   v[1] = __builtin_bit_cast(uint32_t, hi);
-  *reinterpret_cast<u32x2*>(a.y + ((int64_t)(sg.first + (int)j) * a.hq + (int64_t)sg.hk * a.group + h) * DIM + col) = v;
+  *reinterpret_cast<u32x2*>(a.y + ((int64_t)(first + (int)j) * a.hq + (int64_t)hk * a.group + h) * DIM + col) = v;
 }
 
-// Where a workgroup leaves its part of a segment: its second slot if the segment begins there.
+// A workgroup's part of a segment in the scratch, ROWS x DIM sums in units of four columns (unit u: row and
+// column of unit_at), then the rows' maxima and sums of probabilities.  A workgroup's second slot
+// is for the segment that begins in it.
 template <int DIM, int ROWS>
 struct Partial {
   static constexpr int kPart = ROWS * (DIM + 2);
-  Rsrc b;
+  float* p;
   __device__ __forceinline__ Partial(const AttnArgs& a, int wg, bool begins)
-      : b(make_rsrc(a.part + (size_t)(2 * wg + (begins ? 1 : 0)) * kPart, kPart * 4)) {}
-  __device__ __forceinline__ void put(int row, int col, floatx4 o) const {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), b, (row * DIM + col) * 4, 0, kAuxAgent);
-  }
+      : p(a.part + (size_t)(2 * wg + (begins ? 1 : 0)) * kPart) {}
+  __device__ __forceinline__ void put(int unit, floatx4 o) const { *reinterpret_cast<floatx4*>(p + 4 * unit) = o; }
   __device__ __forceinline__ void put_ml(int row, float m, float l) const {
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), b, (ROWS * DIM + row) * 4, 0, kAuxAgent);
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(l), b, (ROWS * (DIM + 1) + row) * 4, 0, kAuxAgent);
+    p[ROWS * DIM + row] = m;
+    p[ROWS * (DIM + 1) + row] = l;
   }
-  __device__ __forceinline__ float m(int row) const { return part_f(b, ROWS * DIM + row); }
-  __device__ __forceinline__ float l(int row) const { return part_f(b, ROWS * (DIM + 1) + row); }
-  __device__ __forceinline__ floatx4 o(uint32_t at) const {
-    return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, kAuxAgent));
+  __device__ __forceinline__ floatx4 get(int unit) const { return *reinterpret_cast<const floatx4*>(p + 4 * unit); }
+  __device__ __forceinline__ float m(int row) const { return p[ROWS * DIM + row]; }
+  __device__ __forceinline__ float l(int row) const { return p[ROWS * (DIM + 1) + row]; }
+};
+
+// Column of register ii of output block c in the lanes g.
+template <int DIM, bool E4M3>
+__device__ __forceinline__ int out_column(int c, int ii, int g) {
+  constexpr int kRun = AttnShape<DIM, E4M3>::kRun;
+  return c / kRun * (16 * kRun) + kRun * (4 * g + ii) + c % kRun;
+}
+
+// Row and column of a partial's unit: row by row, or (k_attention_rows) as a wave's registers have them, its
+// lanes side by side.
+template <int DIM, bool E4M3, int ROWS>
+__device__ __forceinline__ void unit_at(int unit, int& row, int& col) {
+  if constexpr (ROWS < kAtWideRows) {
+    row = unit / (DIM / 4);
+    col = unit % (DIM / 4) * 4;
+  } else {
+    constexpr int kSubs = DIM / 16;
+    const int lane = unit & 63, q = unit >> 6;
+    row = 16 * (q / kSubs) + (lane & 15);
+    col = out_column<DIM, E4M3>(q / 4 % (kSubs / 4) * 4, q & 3, lane >> 4);
+  }
+}
+
+// The segment that begins in a workgroup and goes on in others: how many have some of it (0: none).
+struct Split {
+  int parts = 0, first = 0, hk = 0, block = 0, valid = 0;
+  __device__ __forceinline__ void add(const Segment& sg, int rows) {
+    if (sg.whole || blockIdx.x != (uint32_t)sg.from) return;
+    parts = sg.to - sg.from + 1;
+    first = sg.first;
+    hk = sg.hk;
+    block = sg.block;
+    valid = rows;
   }
 };
 
-// Counts this workgroup off after its partial; the last one of the segment joins them: four columns of a
-// row a thread, the parts' maxima and sums with them, kAhead parts in flight.
-template <int DIM, int ROWS>
-__device__ __forceinline__ void attn_join(const AttnArgs& a, const Segment& sg, int valid, float vs, int tid, int* s_last) {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  if (tid == 0) {
-    const uint32_t old = __hip_atomic_fetch_add(&a.count[sg.from], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *s_last = old == (uint32_t)(sg.to - sg.from) ? 1 : 0;
-    if (*s_last) __hip_atomic_store(&a.count[sg.from], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  if (!*s_last) return;
-  asm volatile("" ::: "memory");
-  constexpr int kItems = ROWS > 32 ? 4 : 1, kAhead = 16 / kItems;   // a thread's columns and parts in flight
-  for (int it0 = tid; it0 < valid * (DIM / 4); it0 += kBlock * kItems) {
-    int row[kItems];
-    uint32_t at[kItems];
+// Sums the parts of split segments: blockIdx.x the workgroup that one begins in, blockIdx.y some of its units.
+// Few rows: four lanes share a unit's parts, eight each in flight (a long sequence of one request has 32 parts
+// a head).  Many rows: a lane has four units, four parts of each in flight.
+template <int DIM, bool E4M3, int ROWS>
+__global__ __launch_bounds__(kBlock) void k_attention_join(AttnArgs a) {
+  using P = Partial<DIM, ROWS>;
+  constexpr int kShare = ROWS < kAtWideRows ? 4 : 1, kItems = 4 / kShare, kAhead = ROWS < kAtWideRows ? 8 : 4;
+  constexpr int kEach = kBlock / kShare;                     // units of a workgroup at a time
+  const Split sp = a.split[blockIdx.x];
+  if (sp.parts == 0) return;
+  const float vs = a.kv.v_scale ? a.kv.v_scale[sp.hk] : 1.0f;
+  const int part0 = threadIdx.x % kShare;
+  const int units = (sp.valid + 15) / 16 * 16 * (DIM / 4);
+  for (int u0 = blockIdx.y * kEach * kItems + threadIdx.x / kShare; u0 < units; u0 += gridDim.y * kEach * kItems) {
+    int unit[kItems], row[kItems], col[kItems];
     float top[kItems], sum[kItems];
     floatx4 o[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      const int it = it0 + i * kBlock;
-      const bool real = it < valid * (DIM / 4);
-      row[i] = real ? it / (DIM / 4) : 0;
-      at[i] = real ? (row[i] * DIM + it % (DIM / 4) * 4) * 4 : kOOB;
+      unit[i] = u0 + i * kEach;
+      unit_at<DIM, E4M3, ROWS>(unit[i], row[i], col[i]);
+      if (unit[i] >= units || row[i] >= sp.valid) unit[i] = -1;
+      if (unit[i] < 0) row[i] = 0;
       top[i] = -INFINITY;
       sum[i] = 0.0f;
       o[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    for (int p = sg.from; p <= sg.to; p += kAhead) {
+    const auto add = [&](int i, float m, float l, floatx4 v) {   // (a part that saw nothing has the sum 0, or NaN)
+      const float now = fmaxf(top[i], m);
+      const float fa = top[i] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(top[i] - now);
+      const float fb = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+      sum[i] = sum[i] * fa + l * fb;
+      o[i] = o[i] * fa + v * fb;
+      top[i] = now;
+    };
+    for (int p = part0; p < sp.parts; p += kShare * kAhead) {
       float mv[kAhead][kItems], lv[kAhead][kItems];
       floatx4 ov[kAhead][kItems];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const bool on = p + k <= sg.to;
-        const Partial<DIM, ROWS> part(a, on ? p + k : sg.to, (on ? p + k : sg.to) == sg.from);
+        const int at = p + kShare * k < sp.parts ? p + kShare * k : p;   // (again, for nothing)
+        const P part(a, blockIdx.x + at, at == 0);
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
           mv[k][i] = part.m(row[i]);
           lv[k][i] = part.l(row[i]);
-          ov[k][i] = part.o(on ? at[i] : kOOB);
+          ov[k][i] = part.get(unit[i] < 0 ? 0 : unit[i]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        float now = top[i];
+      for (int k = 0; k < kAhead; ++k) {
+        const bool on = p + kShare * k < sp.parts;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) now = fmaxf(now, mv[k][i]);
-        if (top[i] > -INFINITY) {
-          const float old = __builtin_amdgcn_exp2f(top[i] - now);
-          sum[i] *= old;
-          o[i] *= old;
-        }
-        top[i] = now;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          if (p + k > sg.to) continue;
-          // (a part that saw nothing has the sum 0, or NaN)
-          const float f = mv[k][i] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mv[k][i] - now);
-          sum[i] += lv[k][i] * f;
-          o[i] += ov[k][i] * f;
-        }
+        for (int i = 0; i < kItems; ++i) add(i, on ? mv[k][i] : -INFINITY, on ? lv[k][i] : 0.0f, on ? ov[k][i] : floatx4{0.0f, 0.0f, 0.0f, 0.0f});
       }
     }
 #pragma unroll
-    for (int i = 0; i < kItems; ++i)
-      if (at[i] != kOOB)
-        attn_put<DIM>(a, sg, sg.block * ROWS + row[i], (int)(at[i] / 4) - row[i] * DIM, o[i] * (sum[i] == 0.0f ? 0.0f : vs / sum[i]));
+    for (int i = 0; i < kItems; ++i) {
+#pragma unroll
+      for (int d = 1; d < kShare; d <<= 1) {
+        const float m = __shfl_xor(top[i], d), l = __shfl_xor(sum[i], d);
+        const floatx4 v = {__shfl_xor(o[i][0], d), __shfl_xor(o[i][1], d), __shfl_xor(o[i][2], d), __shfl_xor(o[i][3], d)};
+        add(i, m, l, v);
+      }
+      if (unit[i] >= 0 && part0 == 0)
+        attn_put<DIM>(a, sp.first, sp.hk, sp.block * ROWS + row[i], col[i], o[i] * (sum[i] == 0.0f ? 0.0f : vs / sum[i]));
+    }
   }
 }
 
@@ -505,12 +543,12 @@ __global__ __launch_bounds__(kBlock, 1) void k_attention(AttnArgs a) {
   constexpr int kPitch = kCols + 4;
   __shared__ __attribute__((aligned(16))) float s_o[4][16][kPitch];
   __shared__ float s_m[4][kRows], s_l[4][kRows];
-  __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   UnitLine line(a, kRows);
   const int total = line.start(lane);
+  Split split;
   int u = blockIdx.x * line.share;
   const int end = u + line.share < total ? u + line.share : total;
   const uint32_t row_bytes = (uint32_t)a.kv.token_stride * S::kSize;
@@ -599,12 +637,14 @@ __global__ __launch_bounds__(kBlock, 1) void k_attention(AttnArgs a) {
         for (int e = 0; e < 8; ++e)
           odd |= (there(e) & val.odd(e)) ? 1u << e : 0u;
         if (__ballot(odd != 0)) {
+          int go = g;
+          asm volatile("" : "+v"(go));
 #pragma unroll 1
           for (int k = 0; k < 32; ++k) {
             const int e = k >> 2, g1 = k & 3;
-            if (__ballot(g == g1 && (odd >> e & 1)) == 0) continue;
+            if (__ballot((go == g1) & (odd >> e & 1)) == 0) continue;
             const int bit = t + (e < 4 ? 4 * g1 + e : 12 + 4 * g1 + e) - base;
-            const uint32_t mine = g == g1 ? (e & 1) ? 0xFFFF0000u : 0x0000FFFFu : 0u;
+            const uint32_t mine = go == g1 ? (e & 1) ? 0xFFFF0000u : 0x0000FFFFu : 0u;
 #pragma unroll
             for (int c = 0; c < S::kSubs; ++c) {
               u32x4 vf = val.value(c);
@@ -668,7 +708,7 @@ __global__ __launch_bounds__(kBlock, 1) void k_attention(AttnArgs a) {
 #pragma unroll
           for (int c = 0; c < S::kSubs; ++c) {
             // column of block c's row 4 g + ii
-            const int col = c / S::kRun * (16 * S::kRun) + S::kRun * (4 * gj + ii) + c % S::kRun;
+            const int col = out_column<DIM, E4M3>(c, ii, gj);
             if (col >= blk * kCols && col < (blk + 1) * kCols) s_o[w][rj][col - blk * kCols] = acc[n][c][ii] * f;
           }
         __syncthreads();
@@ -687,40 +727,44 @@ __global__ __launch_bounds__(kBlock, 1) void k_attention(AttnArgs a) {
           }
           const int col = blk * kCols + 4 * c4;
           if (sg.whole) {
-            attn_put<DIM>(a, sg, sg.block * kRows + rr, col, o * (sum == 0.0f ? 0.0f : vs / sum));
+            attn_put<DIM>(a, sg.first, sg.hk, sg.block * kRows + rr, col, o * (sum == 0.0f ? 0.0f : vs / sum));
           } else {
-            part.put(rr, col, o);
+            part.put((rr * DIM + col) / 4, o);
             if (col == 0) part.put_ml(rr, tp, sum);
           }
         }
       }
     }
-    if (!sg.whole) attn_join<DIM, kRows>(a, sg, valid, vs, tj, &s_last);
+    split.add(sg, valid);
     __syncthreads();
   }
+  if (tid == 0) a.split[blockIdx.x] = split;
 }
 
-// 64 rows of q, 16 a wave, all waves on the same 64 places: a wave loads the keys or the values of 32 of
-// them (waves 0, 1 and 2, 3), turns them into operands once and leaves those in LDS for all four.
-// Without that every wave would convert and turn everything, which takes longer than to load it.
+// Up to 128 rows of q, 16 a wave, all waves on the same 128 (or 64) places: a wave loads the keys or the values of 32
+// of them (waves 0 .. 3 and 4 .. 7), turns them into operands once and leaves those in LDS for all.
+// Without that every wave would convert and turn everything, which takes longer than to load it; with 64 rows
+// a workgroup, sequences of more would be read again.
 template <int DIM, bool E4M3>
-__global__ __launch_bounds__(kBlock, 2) void k_attention_rows(AttnArgs a) {
+__global__ __launch_bounds__(kAtWide, 2) void k_attention_rows(AttnArgs a) {
   using S = AttnShape<DIM, E4M3>;
-  constexpr int kRows = 64;
-  __shared__ u32x4 s_kv[2][2 * S::kSubs][64];                // per 32 places: keys (two 16s), then values
-  __shared__ uint32_t s_odd[2];                              // per 32 places: those with a NaN or an infinity
-  __shared__ int s_last;
+  constexpr int kRows = kAtWideRows;
+  // two waves share 32 places where one's would take too many registers: steps are of 64 then
+  constexpr int kParts = DIM * S::kSize > 256 ? 2 : 1, kSlices = 4 / kParts, kStep = 32 * kSlices;
+  __shared__ u32x4 s_kv[kSlices][2 * S::kSubs][64];          // per 32 places: keys (two 16s), then values
+  __shared__ uint32_t s_odd[kSlices][kParts];                // per 32 places: those with a NaN or an infinity
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), half = w & 1;
-  const bool keys = w < 2;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), mine = (w & 3) / kParts, sub = (w & 3) % kParts;
+  const bool keys = w < 4;
 
   UnitLine line(a, kRows);
   const int total = line.start(lane);
+  Split split;
   int u = blockIdx.x * line.share;
   const int end = u + line.share < total ? u + line.share : total;
   const uint32_t row_bytes = (uint32_t)a.kv.token_stride * S::kSize;
   const uint32_t k_off = r * row_bytes + 16 * g;
-  const uint32_t v_off = 4 * g * row_bytes + r * S::kRun * S::kSize;
+  const uint32_t v_off = 4 * g * row_bytes + (16 * sub + r) * S::kRun * S::kSize;
 
   while (u < end) {
     const Segment sg(line, u, end, lane);
@@ -733,14 +777,16 @@ __global__ __launch_bounds__(kBlock, 2) void k_attention_rows(AttnArgs a) {
     const float scale = a.scale * (a.kv.k_scale ? a.kv.k_scale[sg.hk] : 1.0f);
     const int valid = sg.valid(a.group, kRows);
 
-    Pages<S::kSize> pages;                                   // of 16 steps, four a step
-    RawTile<DIM, E4M3> raw;
+    Pages<S::kSize> pages;                                   // of 32 / kSlices steps
+    RawTile<DIM, E4M3, kParts> raw;
     const auto load = [&](int i) {
+      const int at = 2 * (kSlices * i + mine);
+      if (keys) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const Rsrc b = pages.tile(a, src, 4 * i + 2 * half + h, row_bytes);
-        if (keys) raw.load_keys(h, b, k_off);
-        else raw.load_values(h, b, v_off, row_bytes);
+        for (int h = 0; h < 2 / kParts; ++h) raw.load_keys(h, pages.tile(a, src, at + h + sub, row_bytes), k_off);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) raw.load_values(h, pages.tile(a, src, at + h, row_bytes), v_off, row_bytes);
       }
     };
     int t = sg.tile0 * kAtUnit, i = 0;
@@ -754,35 +800,44 @@ __global__ __launch_bounds__(kBlock, 2) void k_attention_rows(AttnArgs a) {
     for (int c = 0; c < S::kSubs; ++c) acc[c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
     while (t < t_end) {
-      int pg[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) pg[k] = lane_get(pages.page, 4 * i + k);
-      // operands into LDS
+      // which of the step's tiles of 16 exist
+      const uint32_t have = (uint32_t)(__ballot(pages.page >= 0) >> (2 * kSlices * i));
+      // operands into LDS (a few at a time: their registers are many)
       if (keys) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2 / kParts; ++h)
 #pragma unroll
-          for (int f = 0; f < S::kFrag; ++f) s_kv[half][h * S::kFrag + f][lane] = __builtin_bit_cast(u32x4, raw.key(h, f));
+          for (int f = 0; f < S::kFrag; ++f) {
+            s_kv[mine][(h + sub) * S::kFrag + f][lane] = __builtin_bit_cast(u32x4, raw.key(h, f));
+            if (f & 1) __builtin_amdgcn_sched_barrier(0);
+          }
       } else {
-        const int t0 = t + 32 * half, p0 = half ? pg[2] : pg[0], p1 = half ? pg[3] : pg[1];
+        const int t0 = t + 32 * mine;
+        const uint32_t two = have >> (2 * mine) & 3u;
         uint32_t odd = 0;
-        if (!(t0 + 32 <= base && p0 >= 0 && p1 >= 0)) {
+        if (!(t0 + 32 <= base && two == 3u)) {
+          int tm = t0 + 4 * g;
+          asm volatile("" : "+v"(tm));
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const bool there = (t0 + 4 * g + (e < 4 ? e : 12 + e) < sg.seen) & ((e < 4 ? p0 : p1) >= 0);
+            const bool there = (tm + (e < 4 ? e : 12 + e) < sg.seen) & (two >> (e / 4) & 1u);
             const uint64_t bl = __ballot(there & raw.odd(e));
 #pragma unroll
             for (int g1 = 0; g1 < 4; ++g1) odd |= (bl >> (16 * g1) & 0xFFFFu) != 0 ? 1u << (4 * e + g1) : 0u;
             raw.clear(e, !there);
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
-        if (lane == 0) s_odd[half] = odd;
+        if (lane == 0) s_odd[mine][sub] = odd;
 #pragma unroll
-        for (int c = 0; c < S::kSubs; ++c) s_kv[half][S::kSubs + c][lane] = raw.value(c);
+        for (int c = 0; c < S::kSubs / kParts; ++c) {
+          s_kv[mine][S::kSubs + sub * (S::kSubs / kParts) + c][lane] = raw.value(c);
+          if (c & 1) __builtin_amdgcn_sched_barrier(0);
+        }
       }
       // the next step's, in flight
-      const int t_next = t + 64;
-      if (++i == 16) {
+      const int t_next = t + kStep;
+      if (++i == 32 / kSlices) {
         pages.fill(a, table, t_next + lane * 16, t_end);
         i = 0;
       }
@@ -790,60 +845,79 @@ __global__ __launch_bounds__(kBlock, 2) void k_attention_rows(AttnArgs a) {
       lds_barrier();
 
       if (16 * w < valid) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
+#pragma unroll 1
+        for (int k = 0; k < kSlices; ++k) {
           const int t0 = t + 32 * k;
-          if (k > 0 && t0 >= t_end) break;
+          if (t0 >= t_end) break;
+          // operands four at a time, the next four on their way from LDS
+          u32x4 op[2][4];
+          const auto fetch = [&](int n, u32x4 (&to)[4]) {    // the slice's operands n .. n + 3
+#pragma unroll
+            for (int z = 0; z < 4; ++z) to[z] = s_kv[k][n + z][lane];
+            __builtin_amdgcn_sched_barrier(0);
+          };
           floatx4 sc[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            sc[h] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int h = 0; h < 2; ++h) sc[h] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+          fetch(0, op[0]);
 #pragma unroll
-            for (int f = 0; f < S::kFrag; ++f)
-              sc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(s_kv[k][h * S::kFrag + f][lane]), q[f], sc[h], 0, 0, 0);
+          for (int n = 0; n < S::kSubs; n += 4) {
+            fetch(n + 4, op[(n / 4 + 1) & 1]);
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              sc[(n + z) / S::kFrag] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(op[(n / 4) & 1][z]), q[(n + z) % S::kFrag],
+                                                                              sc[(n + z) / S::kFrag], 0, 0, 0);
           }
           float x[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = sc[e / 4][e % 4] * scale;
-          if (!(t0 + 32 <= base && pg[2 * k] >= 0 && pg[2 * k + 1] >= 0)) {
+          const uint32_t two = have >> (2 * k) & 3u;
+          if (!(t0 + 32 <= base && two == 3u)) {
             int tm = t0 + 4 * g;                             // (made here: few steps are masked)
             asm volatile("" : "+v"(tm));
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int at = tm + (e < 4 ? e : 12 + e);
-              x[e] = ((at < sg.seen) & (pg[2 * k + e / 4] >= 0) & sees(at - base)) ? x[e] : -INFINITY;
+              x[e] = ((at < sg.seen) & (two >> (e / 4) & 1u) & sees(at - base)) ? x[e] : -INFINITY;
             }
           }
           u32x4 ph, pl;
           soften<E4M3>(x, m, l, acc, ph, pl);
-          const uint32_t odd = __builtin_amdgcn_readfirstlane(s_odd[k]);
+          const uint32_t odd = __builtin_amdgcn_readfirstlane(s_odd[k][0] | s_odd[k][kParts - 1]);
           if (odd == 0) {
 #pragma unroll
-            for (int c = 0; c < S::kSubs; ++c) {
-              const u32x4 vf = s_kv[k][S::kSubs + c][lane];
-              acc[c] = mfma_pv<E4M3>(vf, ph, acc[c]);
-              if constexpr (!E4M3) acc[c] = mfma_pv<E4M3>(vf, pl, acc[c]);
+            for (int c = 0; c < S::kSubs; c += 4) {
+              const int now = ((S::kSubs + c) / 4) & 1;
+              if (c + 4 < S::kSubs) fetch(S::kSubs + c + 4, op[now ^ 1]);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                acc[c + z] = mfma_pv<E4M3>(op[now][z], ph, acc[c + z]);
+                if constexpr (!E4M3) acc[c + z] = mfma_pv<E4M3>(op[now][z], pl, acc[c + z]);
+              }
             }
           } else {
             // places with a NaN or an infinity, which some rows may not see: the others first, then one at
             // a time, for the rows that do
+            int go = g;                                      // (made here, too)
+            asm volatile("" : "+v"(go));
 #pragma unroll 1
             for (int z = -1; z < 32; ++z) {
               if (z >= 0 && !(odd >> z & 1)) continue;
-              u32x4 mine = {0, 0, 0, 0};
+              u32x4 part = {0, 0, 0, 0};
+#pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const bool on = z < 0 ? !(odd >> (4 * e + g) & 1) : 4 * e + g == z;
-                if (on) mine[e / 2] |= (e & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+                const bool on = z < 0 ? !(odd >> (4 * e + go) & 1) : 4 * e + go == z;
+                part[e / 2] |= on ? (e & 1) ? 0xFFFF0000u : 0x0000FFFFu : 0u;
               }
               const int e = z >> 2, bit = t0 + 4 * (z & 3) + (e < 4 ? e : 12 + e) - base;
-              const bool mine_too = (z < 0) | sees(bit);
+              const bool seen = (z < 0) | sees(bit);
 #pragma unroll
               for (int c = 0; c < S::kSubs; ++c) {
-                const u32x4 vf = s_kv[k][S::kSubs + c][lane] & mine;
+                const u32x4 vf = s_kv[k][S::kSubs + c][lane] & part;
                 floatx4 one = {0.0f, 0.0f, 0.0f, 0.0f};
                 one = mfma_pv<E4M3>(vf, ph, one);
                 if constexpr (!E4M3) one = mfma_pv<E4M3>(vf, pl, one);
-                acc[c] = mine_too ? acc[c] + one : acc[c];
+                acc[c] = seen ? acc[c] + one : acc[c];
                 __builtin_amdgcn_sched_barrier(0);
               }
             }
@@ -854,10 +928,13 @@ __global__ __launch_bounds__(kBlock, 2) void k_attention_rows(AttnArgs a) {
       t = t_next;
     }
 
+    int tj = tid;                                            // (made here: no registers kept for it)
+    asm volatile("" : "+v"(tj));
+    const int lj = tj & 63, rj = lj & 15, gj = lj >> 4;
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
     const float vs = a.kv.v_scale ? a.kv.v_scale[sg.hk] : 1.0f;
-    const int row = 16 * w + r;
+    const int row = 16 * w + rj;
     if (row < valid) {
       const Partial<DIM, kRows> part(a, blockIdx.x, blockIdx.x == (uint32_t)sg.from);
       const float f = sg.whole ? l == 0.0f ? 0.0f : vs / l : 1.0f;
@@ -865,57 +942,66 @@ __global__ __launch_bounds__(kBlock, 2) void k_attention_rows(AttnArgs a) {
       for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
         for (int c = 0; c < S::kSubs; c += 4) {
-          const int col = c / S::kRun * (16 * S::kRun) + S::kRun * (4 * g + ii) + c % S::kRun;
           const floatx4 o = floatx4{acc[c][ii], acc[c + 1][ii], acc[c + 2][ii], acc[c + 3][ii]} * f;
-          if (sg.whole) attn_put<DIM>(a, sg, sg.block * kRows + row, col, o);
-          else part.put(row, col, o);
+          if (sg.whole) attn_put<DIM>(a, sg.first, sg.hk, sg.block * kRows + row, out_column<DIM, E4M3>(c, ii, gj), o);
+          else part.put(((w * (S::kSubs / 4) + c / 4) * 4 + ii) * 64 + lj, o);   // (a wave's lanes side by side)
         }
-      if (!sg.whole && g == 0) part.put_ml(row, m, l);
+      if (!sg.whole && gj == 0) part.put_ml(row, m, l);
     }
-    if (!sg.whole) attn_join<DIM, kRows>(a, sg, valid, vs, tid, &s_last);
+    split.add(sg, valid);
     __syncthreads();
   }
+  if (tid == 0) a.split[blockIdx.x] = split;
 }
 
 // Rows of q a workgroup takes at once, by the average of a sequence.
 struct AttnPlan {
-  int rows;               // 16, 32: k_attention, 64: k_attention_rows
+  int rows;               // 16, 32: k_attention, 128: k_attention_rows
   int wgs;
   bool fits;              // the line of units has fewer than 2^31
 };
 static AttnPlan attn_plan(const DevInfo& di, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b) {
   const int64_t group = hq / kv.heads, avg = (m * group + b.seqs - 1) / b.seqs;
   AttnPlan p;
-  p.rows = avg <= 16 ? 16 : avg <= 32 && kv.dim <= 128 ? 32 : 64;
+  p.rows = avg <= 16 ? 16 : avg <= 32 && kv.dim <= 128 ? 32 : kAtWideRows;
   const double most = ((double)m * group / p.rows + (double)b.seqs) * (double)kv.heads *
                       ((double)b.cols * kv.page / kAtUnit + 1.0);
   p.fits = most < 2147483648.0 && m * hq < (int64_t(1) << 30);
-  p.wgs = di.cus * (p.rows == 64 ? 2 : 1);
-  if (p.fits && most < p.wgs) p.wgs = (int)most + 1;
+  p.wgs = di.cus;
   return p;
 }
 
-constexpr uint64_t kAtCounts = 4096;                         // counts ahead of the partials
 static uint64_t attn_part(const AttnPlan& p, int64_t dim) { return (uint64_t)p.rows * (dim + 2) * sizeof(float); }
 
 bool attention_fits(const DevInfo& di, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b) {
   return attn_plan(di, m, hq, kv, b).fits;
 }
 
-uint64_t attention_scratch(const DevInfo& di, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b,
-                           uint64_t* zero) {
-  const AttnPlan p = attn_plan(di, m, hq, kv, b);
-  *zero = kAtCounts * sizeof(uint32_t);
-  return *zero + 2 * (uint64_t)p.wgs * attn_part(p, kv.dim);
+// No segment is split where each has a workgroup and the table holds no more than a piece.
+static bool attn_splits(const AttnPlan& p, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b) {
+  const int64_t segments = ((m * (hq / kv.heads) + p.rows - 1) / p.rows + b.seqs) * kv.heads;
+  return b.cols * kv.page > (int64_t)kAtPiece * kAtUnit || segments > p.wgs;
 }
 
+uint64_t attention_scratch(const DevInfo& di, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b) {
+  const AttnPlan p = attn_plan(di, m, hq, kv, b);
+  return p.wgs * sizeof(Split) + 16 + (attn_splits(p, m, hq, kv, b) ? 2 * p.wgs * attn_part(p, kv.dim) : 0);
+}
+
+template <int DIM, bool E4M3, int ROWS>
+static void attn_go(const AttnArgs& a, bool splits, hipStream_t s) {
+  const dim3 grid((unsigned)a.wgs);
+  if constexpr (ROWS == kAtWideRows) hipLaunchKernelGGL((k_attention_rows<DIM, E4M3>), grid, dim3(kAtWide), 0, s, a);
+  else hipLaunchKernelGGL((k_attention<DIM, E4M3, ROWS / 16>), grid, dim3(kBlock), 0, s, a);
+  const dim3 join((unsigned)a.wgs, 8);
+  if (splits) hipLaunchKernelGGL((k_attention_join<DIM, E4M3, ROWS>), join, dim3(kBlock), 0, s, a);
+}
 template <int DIM, bool E4M3>
-static void attn_go(const AttnPlan& p, const AttnArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.wgs), block(kBlock);
-  if (p.rows == 64) hipLaunchKernelGGL((k_attention_rows<DIM, E4M3>), grid, block, 0, s, a);
-  else if constexpr (DIM == 256) hipLaunchKernelGGL((k_attention<DIM, E4M3, 1>), grid, block, 0, s, a);
-  else if (p.rows == 32) hipLaunchKernelGGL((k_attention<DIM, E4M3, 2>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_attention<DIM, E4M3, 1>), grid, block, 0, s, a);
+static void attn_go(const AttnPlan& p, const AttnArgs& a, bool splits, hipStream_t s) {
+  if (p.rows == kAtWideRows) attn_go<DIM, E4M3, kAtWideRows>(a, splits, s);
+  else if constexpr (DIM == 256) attn_go<DIM, E4M3, 16>(a, splits, s);
+  else if (p.rows == 32) attn_go<DIM, E4M3, 32>(a, splits, s);
+  else attn_go<DIM, E4M3, 16>(a, splits, s);
 }
 
 hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t hq, const KvArgs& kv,
@@ -924,7 +1010,7 @@ hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t h
   const hipError_t err = dev_info(&di);
   if (err != hipSuccess) return err;
   const AttnPlan p = attn_plan(di, m, hq, kv, b);
-  if (!p.fits || (uint64_t)p.wgs > kAtCounts) return hipErrorInvalidValue;
+  if (!p.fits) return hipErrorInvalidValue;
   AttnArgs a;
   a.q = q; a.ldq = ldq;
   a.m = (int)m; a.hq = (int)hq; a.group = (int)(hq / kv.heads);
@@ -936,11 +1022,12 @@ hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t h
   a.scale = scale * kAtLog2e;
   a.y = y;
   a.wgs = p.wgs;
-  a.count = static_cast<uint32_t*>(scratch);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + kAtCounts * sizeof(uint32_t));
-  if (kv.dim == 64) kv.e4m3 ? attn_go<64, true>(p, a, s) : attn_go<64, false>(p, a, s);
-  else if (kv.dim == 128) kv.e4m3 ? attn_go<128, true>(p, a, s) : attn_go<128, false>(p, a, s);
-  else kv.e4m3 ? attn_go<256, true>(p, a, s) : attn_go<256, false>(p, a, s);
+  a.split = static_cast<Split*>(scratch);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + (p.wgs * sizeof(Split) + 15) / 16 * 16);
+  const bool splits = attn_splits(p, m, hq, kv, b);
+  if (kv.dim == 64) kv.e4m3 ? attn_go<64, true>(p, a, splits, s) : attn_go<64, false>(p, a, splits, s);
+  else if (kv.dim == 128) kv.e4m3 ? attn_go<128, true>(p, a, splits, s) : attn_go<128, false>(p, a, splits, s);
+  else kv.e4m3 ? attn_go<256, true>(p, a, splits, s) : attn_go<256, false>(p, a, splits, s);
   return hipGetLastError();
 }
 

@@ -183,10 +183,8 @@ struct AppendArgs {
   bool f32, pairs;
 };
 hipError_t launch_kv_append(const AppendArgs& a, const KvArgs& kv, const BatchArgs& b, hipStream_t s);
-// attention of the new tokens over the cache (w12_attention); scratch: attention_scratch bytes, the first
-// *zero of them counters
-uint64_t attention_scratch(const DevInfo& di, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b,
-                           uint64_t* zero);
+// attention of the new tokens over the cache (w12_attention); scratch: attention_scratch bytes
+uint64_t attention_scratch(const DevInfo& di, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b);
 bool attention_fits(const DevInfo& di, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b);
 hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t hq, const KvArgs& kv,
                             const BatchArgs& b, float scale, uint16_t* y, void* scratch, hipStream_t s);

@@ -133,8 +133,7 @@ EXPORTS = {
                                      ctypes.POINTER(_W12KVBatch), ctypes.c_void_p, ctypes.c_uint32,
                                      ctypes.c_void_p]),
     "w12_attention_scratch": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(_W12KV),
-                                             ctypes.POINTER(_W12KVBatch), ctypes.POINTER(ctypes.c_uint64),
-                                             ctypes.POINTER(ctypes.c_uint64)]),
+                                             ctypes.POINTER(_W12KVBatch), ctypes.POINTER(ctypes.c_uint64)]),
     "w12_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                      ctypes.POINTER(_W12KV), ctypes.POINTER(_W12KVBatch), ctypes.c_float,
                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32,
@@ -893,12 +892,14 @@ def _step_scratch(what, need, zero, device, stream):
     graphs may be replayed on any stream."""
     if torch.cuda.is_current_stream_capturing():
         buf = torch.empty(need, dtype=torch.uint8, device=device)
-        buf[:zero].zero_()
+        if zero:
+            buf[:zero].zero_()
         return buf
     buf = _step_buffers.get((what, device.index, stream))
     if buf is None or buf.numel() < need:
         buf = torch.empty(max(need, 1 << 18), dtype=torch.uint8, device=device)
-        buf[:zero].zero_()
+        if zero:
+            buf[:zero].zero_()
         _step_buffers[(what, device.index, stream)] = buf
     return buf
 
@@ -929,15 +930,14 @@ def attention(q: torch.Tensor, kv: KVCache, batch: KVBatch, scale: float | None 
     with _on_device(dev):
         stream = _stream_handle(dev)
         key = (m, hq, kv.heads, dim, kv.page, kv.k.dtype)
-        size = batch._sizes.get(key)
-        if size is None:
-            n, z = ctypes.c_uint64(0), ctypes.c_uint64(0)
-            _check(L.w12_attention_scratch(m, hq, kv._ref, batch._ref, ctypes.byref(n), ctypes.byref(z)))
-            size = batch._sizes[key] = (n.value, z.value)
-        need, zero = size
-        buf = _step_scratch("attention", need, zero, dev, stream) if need else None
+        need = batch._sizes.get(key)
+        if need is None:
+            n = ctypes.c_uint64(0)
+            _check(L.w12_attention_scratch(m, hq, kv._ref, batch._ref, ctypes.byref(n)))
+            need = batch._sizes[key] = n.value
+        buf = _step_scratch("attention", need, 0, dev, stream)
         _check(L.w12_attention(qp, ldq, m, hq, kv._ref, batch._ref, dim ** -0.5 if scale is None else float(scale),
-                               out.data_ptr(), _ptr(buf), need, 0, stream))
+                               out.data_ptr(), buf.data_ptr(), need, 0, stream))
     return out
 
 

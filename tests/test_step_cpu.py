@@ -56,11 +56,10 @@ def _attention(L, kv, b, q=0x100000, ldq=8192, m=3, hq=8, y=0x300000, flags=0):
 @pytest.mark.parametrize("want,over", BAD_KV)
 def test_cache_refused(want, over):
     L = _lib()
-    n, z = ctypes.c_uint64(0), ctypes.c_uint64(0)
+    n = ctypes.c_uint64(0)
     assert _append(L, _kv(**over), _batch()) == E[want] and L.w12_last_error()
     assert _attention(L, _kv(**over), _batch()) == E[want]
-    assert L.w12_attention_scratch(3, 8, ctypes.byref(_kv(**over)), ctypes.byref(_batch()), ctypes.byref(n),
-                                   ctypes.byref(z)) == E[want]
+    assert L.w12_attention_scratch(3, 8, ctypes.byref(_kv(**over)), ctypes.byref(_batch()), ctypes.byref(n)) == E[want]
 
 
 @pytest.mark.parametrize("want,over", BAD_BATCH)
@@ -94,7 +93,7 @@ def test_null_structs_refused():
     assert L.w12_attention(0x1000, 512, 3, 4, None, b(_batch()), 0.1, 0x1000, None, 0, 0, None) == w12.W12_ERR_ARG
     assert L.w12_attention(0x1000, 512, 3, 4, b(_kv()), None, 0.1, 0x1000, None, 0, 0, None) == w12.W12_ERR_ARG
     n = ctypes.c_uint64(0)
-    assert L.w12_attention_scratch(3, 4, b(_kv()), b(_batch()), None, b(n)) == w12.W12_ERR_ARG
+    assert L.w12_attention_scratch(3, 4, b(_kv()), b(_batch()), None) == w12.W12_ERR_ARG
     assert L.w12_sample_scratch(3, 4, 0, b(n), None) == w12.W12_ERR_ARG
 
 
