@@ -484,7 +484,7 @@ int w12_attention(const uint16_t *q, int64_t ldq, int64_t m, int64_t hq, const w
 
 /*
  * w12_sample -- a token for each of m rows of logits, drawn with the caller's random numbers.
- * y, n, ldy and W12_LOGITS_BF16 as in w12_logprobs.  Per row (each array [m] on the device, or NULL
+ * y, n (at most 2^20), ldy and W12_LOGITS_BF16 as in w12_logprobs.  Per row (each array [m] on the device, or NULL
  * for the value that switches it off): temperature (NULL: 1), top_k (0 or less: off), top_p (1 or more,
  * or NaN: off), min_p (0 or less, or NaN: off), and u, the random number in [0, 1).
  * With x the row, M its largest logit and w_c = e^((x_c - M) / temperature), tokens are ordered by
@@ -498,8 +498,8 @@ int w12_attention(const uint16_t *q, int64_t ldq, int64_t m, int64_t hq, const w
  * (token or logp or kept may be NULL).  A temperature of 0 or less takes the first token of the order.
  * A row of -Inf alone gives token -1, logp -Inf and kept 0, one with a NaN or +Inf logit, or a
  * temperature of NaN, token -1, logp NaN and kept 0.
- * Weights are computed in double and summed as integers of a step of 2^-62 times the power of two that
- * reaches n, so sums do not depend on their order.  flags: W12_LOGITS_BF16.
+ * Weights and sums that decide are held in double or in integers of 2^-42 of the largest weight, in a fixed
+ * order: equal calls give equal results.  flags: W12_LOGITS_BF16.
  * scratch: w12_sample_scratch bytes of the caller's device memory (16-byte aligned; NULL when 0), in use until
  * the call's work on `stream` is finished.  Its first *zero bytes are counters that must be zero when the
  * work starts and are zero again when it ends: clear them once, then reuse the scratch for calls of any

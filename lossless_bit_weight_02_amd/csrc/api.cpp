@@ -891,7 +891,7 @@ int w12_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t hq, const w
 namespace {
 int check_sample(int64_t m, int64_t n, uint32_t flags) {
   if (m <= 0 || n <= 0) return fail(W12_ERR_ARG, "m and n must be positive (m=%lld, n=%lld)", (long long)m, (long long)n);
-  if (m >= kMaxDim || n >= kMaxDim) return fail(W12_ERR_RANGE, "m or n too large");
+  if (m >= kMaxDim || n > (int64_t(1) << 20)) return fail(W12_ERR_RANGE, "m or n too large (below 2^31, at most 2^20)");
   if (flags & ~W12_LOGITS_BF16) return fail(W12_ERR_ARG, "unknown flags 0x%x", flags);
   return W12_OK;
 }
