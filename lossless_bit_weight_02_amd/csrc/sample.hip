@@ -4,17 +4,18 @@
 // order (descending logit, equal ones by the lower column), so what is kept is known by its last token.
 // The token drawn is the first kept one in column order at which the mass passes u * (mass of all kept).
 //
-// One launch.  A row is cut into parts of 16 logits a thread, which a workgroup holds in registers.  It
-// leaves the part's maximum, its mass, a histogram (count and mass of bins of a 32nd of a power of two of
-// w, from the part's maximum down) and, in column order, the part's largest logits as far as whole bins of
-// them fit a short list.  The row's last workgroup (counted) joins the parts: the histogram says how far down what is
-// kept can reach, and then
-//   lists    nearly always everything down to there is in the lists: their logits are ranked, cut and drawn from
-//   no cut   without filters the parts' masses say which part the token is in, and that part is scanned
-//   cut bin  else (thousands kept) the row is read again: masses of what lies above the bin that the cut falls
-//            in, the bin's logits into LDS, sorted and cut exactly
-//   radix    if even one bin holds too many (thousands of equal logits), four passes by 8 bits of the logit's order
-// and the last two end with the masses of the parts as the second does.
+// A row is cut into parts of 16 logits a thread, which a workgroup holds in registers (k_sample).  It leaves
+// the part's maximum, its mass, a histogram (count and mass of bins of a 32nd of a power of two of w, from
+// the part's maximum down) and, in column order, the part's largest logits as far as whole bins of them
+// fit a short list.  The row's last workgroup (counted) joins the parts: the histogram says how far down
+// what is kept can reach, and then
+//   lists    where everything down to there is in the lists, their logits are ranked, cut and drawn from;
+//   no cut   without filters the parts' masses say which part the token is in, and that part is scanned;
+//   cut bin  else (thousands kept) a second kernel's parts (k_sample_cut; it has nothing to do for other
+//            rows) sum the masses above the bin that the cut falls in and list the bin's logits; the row's
+//            last sorts those, cuts exactly, and goes on as without a cut;
+//   radix    if even one bin holds too many (thousands of equal logits), or top-p cuts what a top-k of
+//            thousands leaves, one workgroup reads the row, 8 bits of the logits' order a time.
 //
 // A border between two tokens has to fall as it does in the formula: where each border were off by 1e-7, as
 // sums of 152064 floats are, one draw in a hundred from a flat row would be a neighbour's.  So weights
@@ -30,8 +31,10 @@ constexpr int kSmElems = 16;                      // logits of a thread
 constexpr int kSmBins = 1024;
 constexpr float kSmPerOctave = 32.0f;             // bins of a power of two
 constexpr int kSmParts = 64;                      // parts of a row at most
-constexpr int kSmCand = 1024;                     // candidates that the lists' way ranks
+constexpr int kSmCand = 2048;                     // candidates that the lists' way ranks
+constexpr int kSmLists = 4096;                    // entries of the lists that it takes
 constexpr int kSmSort = 2048;                     // logits of the cut's bin that are sorted
+constexpr int kSmAll = 2100000000;                // a cut's bin below every logit's
 constexpr int kSmRows = 4096;                     // rows of a launch, each with a count
 constexpr int kSmCountStep = 16;                  // counts 64 bytes apart
 constexpr uint32_t kSmMasked = 0x007FFFFFu;       // the order of -Inf
@@ -59,8 +62,10 @@ __device__ __forceinline__ float sm_value(uint32_t ord) {
 __device__ __forceinline__ void sm_store(uint64_t* p, uint64_t v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ uint64_t sm_load(const uint64_t* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// (of a row's records, `i` in words: as one of the device's dies stored it a moment ago)
+constexpr int kAuxAgent = 16;                     // sc1
+__device__ __forceinline__ uint64_t sm_load(Rsrc rec, int i) {
+  return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(rec, 8 * i, 0, kAuxAgent));
 }
 
 // 16 logits of a thread: V loads of 16 bytes, the workgroup's threads side by side in each.  Columns from n on are -Inf.
@@ -187,6 +192,14 @@ struct SmCut {
   __device__ __forceinline__ bool in(uint32_t key_, uint32_t col_) const { return key_ > key || (key_ == key && col_ <= col); }
 };
 
+// What a row's first join leaves for the second kernel.
+struct SmPlanned {
+  int state;              // 0: done, 1: cut in a bin, 2: by radix
+  int bin, big;           // the cut's bin (kSmAll: no cut but min-p), the largest logit's bin
+  float M;
+  double W;               // the row's mass (top-k off)
+};
+
 template <bool BF, int T>
 struct SmKernel {
   using S = SmShape<T>;
@@ -197,12 +210,17 @@ struct SmKernel {
     union {
       unsigned long long hist[kSmBins];
       struct {
-        double w[kSmCand];                         // candidates in column order
-        double sorted[kSmCand];
+        union {
+          struct {
+            double w[kSmCand];                     // candidates in column order
+            double sorted[kSmCand];
+          };
+          uint64_t raw[kSmLists];                  // the lists, before
+        };
         uint32_t key[kSmCand], col[kSmCand];
       } cand;
+      unsigned long long sorting[kSmSort];         // the cut's bin: order, then the column's complement
       struct {
-        unsigned long long key[kSmSort];           // order, then the column's complement
         unsigned long long mass[256];
         uint32_t cnt[256];
       } sort;
@@ -534,12 +552,14 @@ struct SmKernel {
   }
 
   // The row, from its parts' records.
-  __device__ __forceinline__ void join(const uint64_t* rec0) {
+  __device__ __forceinline__ void join(uint64_t* rec0, SmPlanned* plan) {
     const bool cuts = r.k < a.n || r.p < 1.0 || r.min_p > 0.0;
+    const Rsrc recs = make_rsrc(rec0, (uint32_t)(parts * S::kRec * 8));
+    if (tid == 0) plan->state = 0;
     __syncthreads();
     if (tid < parts) {
-      const uint64_t* const rec = rec0 + (int64_t)tid * S::kRec;
-      const uint64_t h0 = sm_load(rec), h1 = sm_load(rec + 1), h2 = sm_load(rec + 2), h3 = sm_load(rec + 3);
+      const int at = tid * S::kRec;
+      const uint64_t h0 = sm_load(recs, at), h1 = sm_load(recs, at + 1), h2 = sm_load(recs, at + 2), h3 = sm_load(recs, at + 3);
       s.top[tid] = __uint_as_float((uint32_t)(h0 >> 32));
       s.ties[tid] = (uint32_t)h0;                  // bad
       s.shift[tid] = (int)(uint32_t)(h1 >> 32);
@@ -594,18 +614,27 @@ struct SmKernel {
       cnt[i] = 0;
       ms[i] = 0.0;
     }
-    for (int p = 0; p < parts; ++p) {
-      const uint64_t* const h = rec0 + (int64_t)p * S::kRec + S::kHead + S::kList;
-      const int sh = s.shift[p];
-      const double sc = s.scale[p] * (1.0 / 1073741824.0);
+    constexpr int kAhead = 8;                      // parts in flight
+    for (int p0 = 0; p0 < parts; p0 += kAhead) {
+      uint64_t v[kAhead][kBpt];
 #pragma unroll
-      for (int i = 0; i < kBpt; ++i) {
-        const int b = tid * kBpt + i - sh;
-        // (the last bin takes what lies below in its part, too)
-        if (tid * kBpt + i < kSmBins - 1 && b >= 0 && b < kSmBins - 1) {
-          const uint64_t v = sm_load(h + b);
-          cnt[i] += (int)(v >> 48);
-          ms[i] += sc * (double)(v & 0xFFFFFFFFFFFFull);
+      for (int z = 0; z < kAhead; ++z) {
+        const int p = p0 + z < parts ? p0 + z : parts - 1;
+        const int h = p * S::kRec + S::kHead + S::kList, sh = s.shift[p];
+#pragma unroll
+        for (int i = 0; i < kBpt; ++i) {
+          // (the last bin takes what lies below in its part, too)
+          const int b = tid * kBpt + i - sh;
+          v[z][i] = sm_load(recs, p0 + z < parts && tid * kBpt + i < kSmBins - 1 && b >= 0 ? h + b : (1 << 28) - 1);
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < kAhead; ++z) {
+        const double sc = s.scale[p0 + z < parts ? p0 + z : parts - 1] * (1.0 / 1073741824.0);
+#pragma unroll
+        for (int i = 0; i < kBpt; ++i) {
+          cnt[i] += (int)(v[z][i] >> 48);
+          ms[i] += sc * (double)(v[z][i] & 0xFFFFFFFFFFFFull);
         }
       }
     }
@@ -635,7 +664,7 @@ struct SmKernel {
       __syncthreads();
       kb = s.at[0];
     }
-    int need = kb;
+    int need = kb, pb = kSmBins - 1;
     if (r.p < 1.0 && !(r.k < a.n)) {
       const double want = r.p * W * (1.0 + 1e-5);
       double m = m_before;
@@ -645,7 +674,7 @@ struct SmKernel {
         m += ms[i];
       }
       __syncthreads();
-      const int pb = want > 0.0 ? s.at[1] : 0;
+      pb = want > 0.0 ? s.at[1] : 0;
       need = pb < need ? pb : need;
     }
     // (top-k and top-p together: the mass of all k is asked for)
@@ -664,39 +693,199 @@ struct SmKernel {
       lists = true;                                // (all of every part)
       for (int p = 0; p < parts; ++p) lists = lists && s.bound[p] == kSmBins - 1;
     }
-    if (!lists || !from_lists(rec0, need, by_min, big, W)) whole_row();
+    if (lists && from_lists(recs, need, by_min, big, W)) return;
+    if (tid != 0) return;
+    const int bin = r.k < a.n ? kb : r.p < 1.0 ? pb : kSmAll;
+    plan->state = r.k < a.n && r.p < 1.0 ? 2 : bin == kSmBins - 1 ? 2 : 1;
+    plan->bin = bin;
+    plan->big = big;
+    plan->M = mx;
+    plan->W = W;
+  }
+
+  // The second kernel's part of a row with a plan: masses and counts of what lies above the cut's bin (also of
+  // those that min-p leaves), and the bin's logits, into the record.
+  __device__ __forceinline__ void cut_part(int p, const SmPlanned& plan, uint64_t* rec) {
+    const int64_t c0 = (int64_t)p * S::kPart;
+    float x[kSmElems];
+    L::load(y, c0, a.n, tid, x);
+    if (tid == 0) s.n = 0;
+    __syncthreads();
+    double mass = 0.0;
+    unsigned long long left = 0, counts = 0;       // counts: above, and of those the ones min-p leaves << 32
+#pragma unroll
+    for (int e = 0; e < kSmElems; ++e) {
+      const int d = x[e] > -INFINITY ? plan.big - r.bin(x[e]) : 0x7FFFFFFF;
+      if (d < plan.bin) {
+        const double w = weight(x[e]);
+        mass += w;
+        const bool in = passes(w, sm_order(x[e]));
+        left += in ? fine(w) : 0;
+        counts += in ? 1ull << 32 | 1 : 1;
+      }
+      if (d == plan.bin) {
+        const int at = atomicAdd(&s.n, 1);
+        if (at < kSmBins) sm_store(rec + S::kHead + S::kList + at, (uint64_t)sm_order(x[e]) << 32 | (uint32_t)~(uint32_t)(c0 + L::column(e, tid)));
+      }
+    }
+    mass = sm_sum<T>(mass, s.wd);
+    left = sm_sum<T>(left, s.wu);
+    counts = sm_sum<T>(counts, s.wu);
+    if (tid == 0) {
+      sm_store(rec, (uint64_t)__double_as_longlong(mass));
+      sm_store(rec + 1, left);
+      sm_store(rec + 2, counts);
+      sm_store(rec + 3, (uint64_t)s.n);
+    }
+  }
+
+  // And the row's last one: the bin sorted and cut, the token drawn.
+  __device__ __forceinline__ void cut_join(const SmPlanned& plan, uint64_t* rec0) {
+    const Rsrc recs = make_rsrc(rec0, (uint32_t)(parts * S::kRec * 8));
+    __syncthreads();
+    if (tid < parts) {
+      const int at = tid * S::kRec;
+      s.total[tid] = __longlong_as_double((long long)sm_load(recs, at));
+      s.mass[tid] = sm_load(recs, at + 1);
+      const uint64_t c = sm_load(recs, at + 2);
+      s.ties[tid] = (uint32_t)c;
+      s.live[tid] = (int)(c >> 32);
+      s.list[tid + 1] = (int)sm_load(recs, at + 3);
+    }
+    if (tid == 0) s.list[0] = 0;
+    __syncthreads();
+    double above = 0.0;
+    int64_t count = 0, kept = 0;
+    bool fits = true;
+    int n = 0;
+    for (int p = 0; p < parts; ++p) {
+      above += s.total[p];
+      count += s.ties[p];
+      kept += s.live[p];
+      fits = fits && s.list[p + 1] <= kSmBins;
+      n += s.list[p + 1];
+    }
+    if (!fits || n > kSmSort) {
+      whole_row();
+      return;
+    }
+    SmCut cut = {kSmMasked + 1, 0xFFFFFFFFu};
+    if (plan.bin < kSmBins) {
+      __syncthreads();
+      if (tid == 0)
+        for (int p = 0; p < parts; ++p) s.list[p + 1] += s.list[p];
+      __syncthreads();
+      int size = 64;                               // the sort's, a power of two
+      while (size < n) size <<= 1;
+      for (int i = tid; i < size; i += T) {
+        unsigned long long v = 0;
+        if (i < n) {
+          const int p = part_of(i);
+          v = sm_load(recs, p * S::kRec + S::kHead + S::kList + (i - s.list[p]));
+        }
+        s.sorting[i] = v;
+      }
+      // descending, by runs of twice the length each round
+      for (int len = 2; len <= size; len <<= 1)
+        for (int step = len >> 1; step > 0; step >>= 1) {
+          __syncthreads();
+          for (int z = tid; z < size / 2; z += T) {
+            const int i = (z / step * 2) * step + z % step, j = i + step;
+            const unsigned long long u = s.sorting[i], v = s.sorting[j];
+            if ((u < v) == ((i & len) == 0)) {
+              s.sorting[i] = v;
+              s.sorting[j] = u;
+            }
+          }
+        }
+      __syncthreads();
+      // the last one kept of them
+      constexpr int kMine = kSmSort / T;
+      double w[kMine], mine = 0.0, before;
+#pragma unroll
+      for (int q = 0; q < kMine; ++q) {
+        const int i = tid * kMine + q;
+        w[q] = i < n ? weight(sm_value((uint32_t)(s.sorting[i] >> 32))) : 0.0;
+        mine += w[q];
+      }
+      const double all = sm_scan<T>(mine, s.wd, &before);
+      int upto;                                    // how many are kept
+      if (r.k < a.n) {
+        upto = (int)(r.k - count);
+        if (r.k <= count || r.k > count + n) upto = 0;
+      } else {
+        const double want = r.p * plan.W - above;
+        int short_of = 0;
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+          before += w[q];
+          short_of += tid * kMine + q < n && before < want ? 1 : 0;
+        }
+        upto = sm_sum<T>(short_of, reinterpret_cast<int*>(s.wf)) + 1;
+        if ((want <= 0.0 && count > 0) || upto > n || all < want) upto = 0;
+      }
+      if (upto == 0) {                             // (the histogram's masses were off by a bin)
+        whole_row();
+        return;
+      }
+      const unsigned long long last = s.sorting[upto - 1];
+      cut = {(uint32_t)(last >> 32), ~(uint32_t)last};
+      unsigned long long more = 0;
+      for (int i = tid; i < upto; i += T) {
+        const unsigned long long v = s.sorting[i];
+        const double wi = weight(sm_value((uint32_t)(v >> 32)));
+        if (passes(wi, (uint32_t)(v >> 32))) {
+          atomicAdd(&s.mass[~(uint32_t)v / (uint32_t)S::kPart], fine(wi));
+          ++more;
+        }
+      }
+      kept += (int64_t)sm_sum<T>(more, s.wu);
+    }
+    __syncthreads();
+    draw(cut, kept);
+  }
+
+  // the part that entry i of the lists is in
+  __device__ __forceinline__ int part_of(int i) const {
+    int lo = 0, hi = parts;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.list[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    return lo;
   }
 
   // Cuts and draws from the lists' logits down to bin `need`; false if they turn out not to reach the cut.
-  __device__ __forceinline__ bool from_lists(const uint64_t* rec0, int need, bool by_min, int big, double W) {
+  __device__ __forceinline__ bool from_lists(Rsrc recs, int need, bool by_min, int big, double W) {
     __syncthreads();
     const int all = s.list[parts];
-    int n = 0;
-    for (int i0 = 0; i0 < all; i0 += T) {
-      const int i = i0 + tid;
-      bool in = false;
-      uint64_t v = 0;
-      if (i < all) {
-        int lo = 0, hi = parts;                    // the part that entry i is in
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (s.list[mid] <= i) lo = mid;
-          else hi = mid;
-        }
-        v = sm_load(rec0 + (int64_t)lo * S::kRec + S::kHead + (i - s.list[lo]));
-        in = need >= kSmBins - 1 || big - r.bin(sm_value((uint32_t)(v >> 32))) <= need;
-      }
-      int before;
-      const int got = sm_scan<T>(in ? 1 : 0, reinterpret_cast<int*>(s.wf), &before);
-      if (n + got > kSmCand) return false;
-      if (in) {
-        const float x = sm_value((uint32_t)(v >> 32));
-        s.cand.key[n + before] = (uint32_t)(v >> 32);
-        s.cand.col[n + before] = (uint32_t)v;
-        s.cand.w[n + before] = weight(x);
-      }
-      n += got;
+    if (all > kSmLists) return false;
+#pragma unroll 4
+    for (int i = tid; i < all; i += T) {
+      const int p = part_of(i);
+      s.cand.raw[i] = sm_load(recs, p * S::kRec + S::kHead + (i - s.list[p]));
     }
+    __syncthreads();
+    // a run of the entries a thread, so that one sum gives their places
+    const int run = (all + T - 1) / T, i1 = (tid + 1) * run < all ? (tid + 1) * run : all;
+    const auto in = [&](int i) {
+      return need >= kSmBins - 1 || big - r.bin(sm_value((uint32_t)(s.cand.raw[i] >> 32))) <= need;
+    };
+    int mine_n = 0, at0;
+#pragma unroll 1
+    for (int i = tid * run; i < i1; ++i) mine_n += in(i) ? 1 : 0;
+    const int n = sm_scan<T>(mine_n, reinterpret_cast<int*>(s.wf), &at0);
+    if (n > kSmCand) return false;
+#pragma unroll 1
+    for (int i = tid * run; i < i1; ++i)
+      if (in(i)) {
+        s.cand.key[at0] = (uint32_t)(s.cand.raw[i] >> 32);
+        s.cand.col[at0++] = (uint32_t)s.cand.raw[i];
+      }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i < n; i += T) s.cand.w[i] = weight(sm_value(s.cand.key[i]));
     __syncthreads();
     // ranks in the tokens' order
     constexpr int kMine = kSmCand / T;
@@ -781,8 +970,25 @@ struct SmKernel {
   }
 };
 
+// Whether this is the row's last workgroup to get here, all stores of the others to be seen.
+template <class Shared>
+__device__ __forceinline__ bool sm_last(uint32_t* count, int parts, Shared& s) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (parts == 1) return true;
+  if (threadIdx.x == 0) {
+    const uint32_t old = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s.last = old == (uint32_t)parts - 1 ? 1 : 0;
+    if (s.last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  const bool last = s.last != 0;
+  asm volatile("" ::: "memory");
+  return last;
+}
+
 template <bool BF, int T>
-__global__ __launch_bounds__(T) void k_sample(SampleArgs a, int parts, uint32_t* count, uint64_t* recs) {
+__global__ __launch_bounds__(T) void k_sample(SampleArgs a, int parts, uint32_t* count, SmPlanned* plans, uint64_t* recs) {
   using K = SmKernel<BF, T>;
   __shared__ typename K::Shared s;
   const int64_t row = blockIdx.x / parts;
@@ -791,20 +997,29 @@ __global__ __launch_bounds__(T) void k_sample(SampleArgs a, int parts, uint32_t*
   uint64_t* const rec0 = recs + row * parts * SmShape<T>::kRec;
   K k = {a, s, (int)threadIdx.x, row, static_cast<const uint8_t*>(a.y) + row * a.ldy * (BF ? 2 : 4), parts, SmRow(a, row, temp)};
   k.part(p, temp, rec0 + (int64_t)p * SmShape<T>::kRec);
-  // this part's record is out: the row's last part goes on
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  if (parts > 1) {
-    if (threadIdx.x == 0) {
-      const uint32_t old = __hip_atomic_fetch_add(&count[row * kSmCountStep], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      s.last = old == (uint32_t)parts - 1 ? 1 : 0;
-      if (s.last) __hip_atomic_store(&count[row * kSmCountStep], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (!s.last) return;
-    asm volatile("" ::: "memory");
+  if (sm_last(&count[row * kSmCountStep], parts, s)) k.join(rec0, plans + row);
+}
+
+template <bool BF, int T>
+__global__ __launch_bounds__(T) void k_sample_cut(SampleArgs a, int parts, uint32_t* count, const SmPlanned* plans, uint64_t* recs) {
+  using K = SmKernel<BF, T>;
+  __shared__ typename K::Shared s;
+  const int64_t row = blockIdx.x / parts;
+  const SmPlanned plan = plans[row];
+  if (plan.state == 0) return;
+  const int p = (int)(blockIdx.x - row * parts);
+  if (plan.state == 2 && p > 0) return;
+  const float temp = a.temperature ? a.temperature[row] : 1.0f;
+  uint64_t* const rec0 = recs + row * parts * SmShape<T>::kRec;
+  K k = {a, s, (int)threadIdx.x, row, static_cast<const uint8_t*>(a.y) + row * a.ldy * (BF ? 2 : 4), parts, SmRow(a, row, temp)};
+  k.M = (double)plan.M;
+  k.top = sm_order(plan.M);
+  if (plan.state == 2) {
+    k.whole_row();
+    return;
   }
-  k.join(rec0);
+  k.cut_part(p, plan, rec0 + (int64_t)p * SmShape<T>::kRec);
+  if (sm_last(&count[row * kSmCountStep], parts, s)) k.cut_join(plan, rec0);
 }
 
 // Parts of 4096 logits while they are few for the chip (a row's latency), else of 16384 (records are then a
@@ -831,7 +1046,14 @@ static SmPlan sm_plan(const DevInfo& di, int64_t m, int64_t n) {
 uint64_t sample_scratch(const DevInfo& di, int64_t m, int64_t n, bool, uint64_t* zero) {
   const SmPlan p = sm_plan(di, m, n);
   *zero = (uint64_t)kSmRows * kSmCountStep * sizeof(uint32_t);
-  return *zero + (uint64_t)(p.rows * p.parts * p.rec);
+  return *zero + (uint64_t)(p.rows * (p.parts * p.rec + (int64_t)sizeof(SmPlanned)));
+}
+
+template <bool BF, int T>
+static void sm_go(dim3 grid, hipStream_t s, const SampleArgs& a, int parts, uint32_t* count, SmPlanned* plans, uint64_t* recs,
+                  bool cuts) {
+  hipLaunchKernelGGL((k_sample<BF, T>), grid, dim3(T), 0, s, a, parts, count, plans, recs);
+  if (cuts) hipLaunchKernelGGL((k_sample_cut<BF, T>), grid, dim3(T), 0, s, a, parts, count, plans, recs);
 }
 
 hipError_t launch_sample(const SampleArgs& a0, bool bf, void* scratch, hipStream_t s) {
@@ -842,14 +1064,16 @@ hipError_t launch_sample(const SampleArgs& a0, bool bf, void* scratch, hipStream
   if (p.parts > kSmParts) return hipErrorInvalidValue;
   SampleArgs a = a0;
   uint32_t* const count = static_cast<uint32_t*>(scratch);
-  uint64_t* const recs = reinterpret_cast<uint64_t*>(count + kSmRows * kSmCountStep);
+  SmPlanned* const plans = reinterpret_cast<SmPlanned*>(count + kSmRows * kSmCountStep);
+  uint64_t* const recs = reinterpret_cast<uint64_t*>(plans + p.rows);
+  const bool cuts = a.top_k || a.top_p || a.min_p;           // (without: nothing for the second kernel)
   for (int64_t r0 = 0; r0 < a0.m; r0 += p.rows) {
     a.m = a0.m - r0 < p.rows ? a0.m - r0 : p.rows;
-    const dim3 grid((unsigned)(a.m * p.parts)), block(p.wide ? 1024 : 256);
-    if (p.wide && bf) hipLaunchKernelGGL((k_sample<true, 1024>), grid, block, 0, s, a, p.parts, count, recs);
-    else if (p.wide) hipLaunchKernelGGL((k_sample<false, 1024>), grid, block, 0, s, a, p.parts, count, recs);
-    else if (bf) hipLaunchKernelGGL((k_sample<true, 256>), grid, block, 0, s, a, p.parts, count, recs);
-    else hipLaunchKernelGGL((k_sample<false, 256>), grid, block, 0, s, a, p.parts, count, recs);
+    const dim3 grid((unsigned)(a.m * p.parts));
+    if (p.wide && bf) sm_go<true, 1024>(grid, s, a, p.parts, count, plans, recs, cuts);
+    else if (p.wide) sm_go<false, 1024>(grid, s, a, p.parts, count, plans, recs, cuts);
+    else if (bf) sm_go<true, 256>(grid, s, a, p.parts, count, plans, recs, cuts);
+    else sm_go<false, 256>(grid, s, a, p.parts, count, plans, recs, cuts);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     a.y = static_cast<const uint8_t*>(a.y) + p.rows * a.ldy * (bf ? 2 : 4);
