@@ -500,12 +500,10 @@ int w12_attention(const uint16_t *q, int64_t ldq, int64_t m, int64_t hq, const w
  * temperature of NaN, token -1, logp NaN and kept 0.
  * Weights and sums that decide are held in double or in integers of 2^-42 of the largest weight, in a fixed
  * order: equal calls give equal results.  flags: W12_LOGITS_BF16.
- * scratch: w12_sample_scratch bytes of the caller's device memory (16-byte aligned; NULL when 0), in use until
- * the call's work on `stream` is finished.  Its first *zero bytes are counters that must be zero when the
- * work starts and are zero again when it ends: clear them once, then reuse the scratch for calls of any
- * sizes that follow each other on one stream.
+ * scratch: w12_sample_scratch bytes of the caller's device memory (16-byte aligned), in use until the
+ * call's work on `stream` is finished; its contents on entry do not matter.
  */
-int w12_sample_scratch(int64_t m, int64_t n, uint32_t flags, uint64_t *bytes, uint64_t *zero);
+int w12_sample_scratch(int64_t m, int64_t n, uint32_t flags, uint64_t *bytes);
 int w12_sample(const void *y, int64_t m, int64_t n, int64_t ldy, const float *temperature, const int32_t *top_k,
                const float *top_p, const float *min_p, const float *u, int32_t *token, float *logp,
                int32_t *kept, void *scratch, uint64_t scratch_bytes, uint32_t flags, void *stream);

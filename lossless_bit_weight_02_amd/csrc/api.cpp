@@ -897,14 +897,11 @@ int check_sample(int64_t m, int64_t n, uint32_t flags) {
 }
 }  // namespace
 
-int w12_sample_scratch(int64_t m, int64_t n, uint32_t flags, uint64_t* bytes, uint64_t* zero) {
-  if (!bytes || !zero) return fail(W12_ERR_ARG, "bytes or zero is NULL");
+int w12_sample_scratch(int64_t m, int64_t n, uint32_t flags, uint64_t* bytes) {
+  if (!bytes) return fail(W12_ERR_ARG, "bytes is NULL");
   int rc = check_sample(m, n, flags);
   if (rc) return rc;
-  w12::DevInfo di;
-  hipError_t e = w12::dev_info(&di);
-  if (e != hipSuccess) return hip_fail(e, "device query");
-  *bytes = w12::sample_scratch(di, m, n, (flags & W12_LOGITS_BF16) != 0, zero);
+  *bytes = w12::sample_scratch(m, n);
   return ok();
 }
 
@@ -921,22 +918,16 @@ int w12_sample(const void* y, int64_t m, int64_t n, int64_t ldy, const float* te
   if (!aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) || !aligned4(min_p) || !aligned4(u) ||
       !aligned4(token) || !aligned4(logp) || !aligned4(kept))
     return fail(W12_ERR_ALIGN, "the parameters and outputs must be 4-byte aligned");
-  w12::DevInfo di;
-  hipError_t e = w12::dev_info(&di);
-  if (e != hipSuccess) return hip_fail(e, "device query");
-  uint64_t zero = 0;
-  const uint64_t need = w12::sample_scratch(di, m, n, bf, &zero);
-  if (need > 0) {
-    if (!scratch || scratch_bytes < need)
-      return fail(W12_ERR_CAPACITY, "scratch of %llu bytes is needed (%llu given)", (unsigned long long)need,
-                  scratch ? (unsigned long long)scratch_bytes : 0ull);
-    if (!aligned16(scratch)) return fail(W12_ERR_ALIGN, "scratch must be 16-byte aligned");
-  }
+  const uint64_t need = w12::sample_scratch(m, n);
+  if (!scratch || scratch_bytes < need)
+    return fail(W12_ERR_CAPACITY, "scratch of %llu bytes is needed (%llu given)", (unsigned long long)need,
+                scratch ? (unsigned long long)scratch_bytes : 0ull);
+  if (!aligned16(scratch)) return fail(W12_ERR_ALIGN, "scratch must be 16-byte aligned");
   w12::SampleArgs a;
   a.y = y; a.m = m; a.n = n; a.ldy = ldy;
   a.temperature = temperature; a.top_k = top_k; a.top_p = top_p; a.min_p = min_p; a.u = u;
   a.token = token; a.logp = logp; a.kept = kept;
-  e = w12::launch_sample(a, bf, scratch, reinterpret_cast<hipStream_t>(stream));
+  const hipError_t e = w12::launch_sample(a, bf, scratch, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "sampling launch");
   return ok();
 }

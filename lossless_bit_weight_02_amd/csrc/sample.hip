@@ -5,15 +5,15 @@
 // The token drawn is the first kept one in column order at which the mass passes u * (mass of all kept).
 //
 // A row is cut into parts of 16 logits a thread, which a workgroup holds in registers (k_sample).  It leaves
-// the part's maximum, its mass, a histogram (count and mass of bins of a 32nd of a power of two of w, from
-// the part's maximum down) and, in column order, the part's largest logits as far as whole bins of them
-// fit a short list.  The row's last workgroup (counted) joins the parts: the histogram says how far down
+// the part's maximum, its mass, a histogram (of counts with top-k, else of masses, of bins of a 16th of a power of
+// two of w, from the part's maximum down) and, in column order, the part's largest logits as far as whole bins of
+// them fit a short list.  A workgroup a row joins the parts (k_sample_join): the histogram says how far down
 // what is kept can reach, and then
-//   lists    where everything down to there is in the lists, their logits are ranked, cut and drawn from;
+//   lists    where everything down to there is in the lists, their logits are sorted, cut and drawn from;
 //   no cut   without filters the parts' masses say which part the token is in, and that part is scanned;
-//   cut bin  else (thousands kept) a second kernel's parts (k_sample_cut; it has nothing to do for other
-//            rows) sum the masses above the bin that the cut falls in and list the bin's logits; the row's
-//            last sorts those, cuts exactly, and goes on as without a cut;
+//   cut bin  else (thousands kept) two more kernels, which have nothing to do for other rows, look again: the
+//            parts (k_sample_cut) sum the masses above the bin that the cut falls in and list the bin's logits,
+//            the rows (k_sample_cut_join) select the last one kept of those and go on as without a cut;
 //   radix    if even one bin holds too many (thousands of equal logits), or top-p cuts what a top-k of
 //            thousands leaves, one workgroup reads the row, 8 bits of the logits' order a time.
 //
@@ -28,15 +28,13 @@
 namespace w12 {
 
 constexpr int kSmElems = 16;                      // logits of a thread
-constexpr int kSmBins = 1024;
-constexpr float kSmPerOctave = 32.0f;             // bins of a power of two
+constexpr int kSmBins = 512;
+constexpr float kSmPerOctave = 16.0f;             // bins of a power of two of w
+constexpr double kSmPerUnit = 16.0;               // of a logit's 1.0 at most with top-k, whose last one may have any w
 constexpr int kSmParts = 64;                      // parts of a row at most
-constexpr int kSmCand = 2048;                     // candidates that the lists' way ranks
-constexpr int kSmLists = 4096;                    // entries of the lists that it takes
-constexpr int kSmSort = 2048;                     // logits of the cut's bin that are sorted
+constexpr int kSmSort = 2048;                     // logits that a row's join can sort
 constexpr int kSmAll = 2100000000;                // a cut's bin below every logit's
-constexpr int kSmRows = 4096;                     // rows of a launch, each with a count
-constexpr int kSmCountStep = 16;                  // counts 64 bytes apart
+constexpr int kSmRows = 4096;                     // rows of a launch
 constexpr uint32_t kSmMasked = 0x007FFFFFu;       // the order of -Inf
 constexpr double kSmFine = 4398046511104.0;       // 2^42: masses as integers, 2^20 logits of at most 1
 
@@ -48,7 +46,11 @@ struct SmShape {
   static constexpr int kPart = T * kSmElems;
   static constexpr int kList = T / 4;              // entries of a part's list
   static constexpr int kHead = 4;                  // a part's record, in 64-bit words
-  static constexpr int kRec = kHead + kList + kSmBins;
+  static constexpr int kCutList = 512;             // entries of the cut's list, which takes the place of both
+  static constexpr int kRec = kHead + kCutList;
+  static_assert(kList + kSmBins / 2 <= kCutList);
+  static constexpr int kBpt = (kSmBins + T - 1) / T;   // bins of a thread
+  static constexpr int kNone = (1 << 28) - 1;          // a word behind every record: reads as 0
 };
 
 __device__ __forceinline__ uint32_t sm_order(float x) {
@@ -59,14 +61,11 @@ __device__ __forceinline__ float sm_value(uint32_t ord) {
   return __uint_as_float((ord & 0x80000000u) ? (ord & 0x7FFFFFFFu) : ~ord);
 }
 
-__device__ __forceinline__ void sm_store(uint64_t* p, uint64_t v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// (of a row's records, `i` in words: as one of the device's dies stored it a moment ago)
-constexpr int kAuxAgent = 16;                     // sc1
+// (of a row's records, `i` in words of 64, 32 bits; behind them 0)
 __device__ __forceinline__ uint64_t sm_load(Rsrc rec, int i) {
-  return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(rec, 8 * i, 0, kAuxAgent));
+  return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(rec, 8 * i, 0, 0));
 }
+__device__ __forceinline__ uint32_t sm_load32(Rsrc rec, int i) { return __builtin_amdgcn_raw_buffer_load_b32(rec, 4 * i, 0, 0); }
 
 // 16 logits of a thread: V loads of 16 bytes, the workgroup's threads side by side in each.  Columns from n on are -Inf.
 template <bool BF, int T>
@@ -126,7 +125,7 @@ __device__ __forceinline__ double sm_exp2(double t) {
 // What a row asks for.
 struct SmRow {
   double c;               // log2 e / temperature
-  float bins;             // bins of one unit of logit
+  float bins;             // bins of a logit's 1.0
   bool hard;              // the largest logit
   int64_t k;              // n: off
   double p;               // 1 or more: off
@@ -134,13 +133,14 @@ struct SmRow {
   __device__ __forceinline__ SmRow(const SampleArgs& a, int64_t row, float temp) {
     hard = temp <= 0.0f;
     c = hard ? 1.4426950408889634 : 1.4426950408889634 / (double)temp;
-    bins = (float)(c * kSmPerOctave < 1e30 ? c * kSmPerOctave : 1e30);
     const int32_t kk = a.top_k ? a.top_k[row] : 0;
     const float pp = a.top_p ? a.top_p[row] : 1.0f, mp = a.min_p ? a.min_p[row] : 0.0f;
     const bool one = hard || mp > 1.0f;            // the first token alone
     k = one ? 1 : kk > 0 && kk < a.n ? kk : a.n;
     p = !one && pp < 1.0f ? (pp > 0.0f ? (double)pp : 0.0) : 1.0;
     min_p = !one && mp > 0.0f ? (double)mp : 0.0;
+    const double per = c * kSmPerOctave, most = k < a.n ? kSmPerUnit : 1e30;
+    bins = (float)(per < most ? per : most);
   }
   // bin of a logit above -Inf: never falls as x rises
   __device__ __forceinline__ int bin(float x) const {
@@ -171,6 +171,40 @@ __device__ __forceinline__ V sm_scan(V v, V* s_w, V* before) {   // *before: of 
   *before = lane > 0 ? pre + ahead : pre;
   return tot;
 }
+// N such sums at once, one wait for all.
+template <int T, int N>
+__device__ __forceinline__ void sm_scans(const unsigned long long (&v)[N], unsigned long long (*s_w)[4],
+                                         unsigned long long (&before)[N], unsigned long long (&tot)[N]) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  unsigned long long in[N];
+#pragma unroll
+  for (int z = 0; z < N; ++z) in[z] = v[z];
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+#pragma unroll
+    for (int z = 0; z < N; ++z) {
+      const unsigned long long up = __shfl_up(in[z], o);
+      if (lane >= o) in[z] += up;
+    }
+  }
+  __syncthreads();
+  if (lane == 63) {
+#pragma unroll
+    for (int z = 0; z < N; ++z) s_w[w][z] = in[z];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int z = 0; z < N; ++z) {
+    unsigned long long pre = 0;
+    tot[z] = 0;
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) {
+      if (i == w) pre = tot[z];
+      tot[z] += s_w[i][z];
+    }
+    before[z] = pre + in[z] - v[z];
+  }
+}
 template <int T, class V>
 __device__ __forceinline__ V sm_sum(V v, V* s_w) {
 #pragma unroll
@@ -200,68 +234,54 @@ struct SmPlanned {
   double W;               // the row's mass (top-k off)
 };
 
+// A row.
 template <bool BF, int T>
-struct SmKernel {
+struct SmOf {
   using S = SmShape<T>;
   using L = SmLoad<BF, T>;
 
-  // The workgroup's LDS; the row's last one uses the space of the histogram and more for its own.
-  struct Shared {
-    union {
-      unsigned long long hist[kSmBins];
-      struct {
-        union {
-          struct {
-            double w[kSmCand];                     // candidates in column order
-            double sorted[kSmCand];
-          };
-          uint64_t raw[kSmLists];                  // the lists, before
-        };
-        uint32_t key[kSmCand], col[kSmCand];
-      } cand;
-      unsigned long long sorting[kSmSort];         // the cut's bin: order, then the column's complement
-      struct {
-        unsigned long long mass[256];
-        uint32_t cnt[256];
-      } sort;
-    };
-    double wd[T / 64];
-    unsigned long long wu[T / 64];
-    float wf[T / 64];
-    // the parts
-    double scale[kSmParts], total[kSmParts];
-    unsigned long long mass[kSmParts];             // of what is kept, in 2^-42
-    uint32_t ties[kSmParts];
-    float top[kSmParts];
-    int shift[kSmParts], bound[kSmParts], list[kSmParts + 1], live[kSmParts];
-    int bad, last, n, found;
-    int at[4];
-    double val[4];
-    uint32_t cnt0, key0;
-  };
-
   const SampleArgs& a;
-  Shared& s;
   const int tid;
   const int64_t row;
   const uint8_t* const y;
   const int parts;
+  const float temp;
   const SmRow r;
   double M = 0.0;                                  // the row's largest logit
   uint32_t top = 0;                                // its order
 
+  __device__ __forceinline__ SmOf(const SampleArgs& args, int64_t row_, int parts_)
+      : a(args), tid((int)threadIdx.x), row(row_), y(static_cast<const uint8_t*>(args.y) + row_ * args.ldy * (BF ? 2 : 4)),
+        parts(parts_), temp(args.temperature ? args.temperature[row_] : 1.0f), r(args, row_, temp) {}
+  __device__ __forceinline__ void is_top(float x) {
+    M = (double)x;
+    top = sm_order(x);
+  }
   __device__ __forceinline__ double weight(float x) const { return sm_exp2(((double)x - M) * r.c); }
   __device__ __forceinline__ unsigned long long fine(double w) const { return (unsigned long long)(w * kSmFine + 0.5); }
   __device__ __forceinline__ bool passes(double w, uint32_t key) const { return w >= r.min_p || key == top; }
+};
 
-  __device__ __forceinline__ void put(int64_t token, double logp, int64_t kept) const {
-    if (a.token) a.token[row] = (int32_t)token;
-    if (a.logp) a.logp[row] = (float)logp;
-    if (a.kept) a.kept[row] = (int32_t)kept;
-  }
+// The parts' kernels.
+template <bool BF, int T>
+struct SmPart : SmOf<BF, T> {
+  using S = SmShape<T>;
+  using L = SmLoad<BF, T>;
+  using Of = SmOf<BF, T>;
+  using Of::a, Of::tid, Of::y, Of::temp, Of::r, Of::weight, Of::fine, Of::passes;
+
+  struct Shared {
+    unsigned long long hist[kSmBins];              // count << 48 | mass in 2^-30
+    double wd[T / 64];
+    unsigned long long wu[T / 64];
+    float wf[T / 64];
+    int bad, n;
+  };
+  Shared& s;
+  __device__ __forceinline__ SmPart(const SampleArgs& args, int64_t row_, int parts_, Shared& sh) : Of(args, row_, parts_), s(sh) {}
 
   // A part: its record into rec.
-  __device__ __forceinline__ void part(int p, float temp, uint64_t* rec) {
+  __device__ __forceinline__ void part(int p, uint64_t* rec) {
     const bool cuts = r.k < a.n || r.p < 1.0 || r.min_p > 0.0, masses = !(r.k < a.n);
     const int64_t c0 = (int64_t)p * S::kPart;
     float x[kSmElems];
@@ -289,9 +309,9 @@ struct SmKernel {
 #pragma unroll
     for (int e = 0; e < kSmElems; ++e) {
       const bool live = x[e] > -INFINITY && mx < INFINITY;
-      const double t = live ? ((double)x[e] - (double)mx) * r.c : -1e4;
-      const float tf = (float)(t > -200.0 ? t : -200.0);
+      float wf = 0.0f;
       if (masses) {
+        const double t = live ? ((double)x[e] - (double)mx) * r.c : -1e4;
         double w;
         if (__ballot(t > -24.0)) {
           w = sm_exp2(t);
@@ -299,13 +319,16 @@ struct SmKernel {
           const double n = __builtin_rint(t > -1000.0 ? t : -1000.0);
           w = __builtin_ldexp((double)__builtin_amdgcn_exp2f((float)((t > -1000.0 ? t : -1000.0) - n)), (int)n);
         }
-        tot += live ? w : 0.0;
+        w = live ? w : 0.0;
+        tot += w;
+        wf = (float)w;
       }
+      __builtin_amdgcn_sched_barrier(0);           // (else all 16 are in flight, in more registers than there are)
       rel[e] = kSmBins;
       if (cuts && live) {
         const int d = big - r.bin(x[e]);
         rel[e] = d < kSmBins ? d : kSmBins - 1;
-        atomicAdd(&s.hist[rel[e]], 1ull << 48 | (uint32_t)(__builtin_amdgcn_exp2f(tf) * 1073741824.0f + 0.5f));
+        atomicAdd(&s.hist[rel[e]], 1ull << 48 | (uint32_t)(wf * 1073741824.0f + 0.5f));
       }
     }
     if (masses) tot = sm_sum<T>(tot, s.wd);
@@ -318,21 +341,26 @@ struct SmKernel {
     }
     if (cuts) {
       // whole bins from the top while they fit the list
-      constexpr int kBpt = kSmBins / T;
-      int mine = 0;
+      int mine = 0, own[S::kBpt];
 #pragma unroll
-      for (int i = 0; i < kBpt; ++i) {
-        const unsigned long long h = s.hist[tid * kBpt + i];
-        mine += (int)(h >> 48);
-        sm_store(rec + S::kHead + S::kList + tid * kBpt + i, h);
+      for (int i = 0; i < S::kBpt; ++i) {
+        const int b = tid * S::kBpt + i;
+        own[i] = 0;
+        if (b < kSmBins) {
+          const unsigned long long h = s.hist[b];
+          own[i] = (int)(h >> 48);
+          reinterpret_cast<uint32_t*>(rec + S::kHead + S::kList)[b] =
+              masses ? __float_as_uint((float)(h & 0xFFFFFFFFFFFFull) * (1.0f / 1073741824.0f)) : (uint32_t)own[i];
+        }
+        mine += own[i];
       }
       int before;
       sm_scan<T>(mine, reinterpret_cast<int*>(s.wf), &before);
       int fit = 0;
 #pragma unroll
-      for (int i = 0; i < kBpt; ++i) {
-        before += (int)(s.hist[tid * kBpt + i] >> 48);
-        fit += before <= S::kList ? 1 : 0;
+      for (int i = 0; i < S::kBpt; ++i) {
+        before += own[i];
+        fit += tid * S::kBpt + i < kSmBins && before <= S::kList ? 1 : 0;
       }
       bound = sm_sum<T>(fit, reinterpret_cast<int*>(s.wf)) - 1;
       // (the counts of a load's logits, 16 bits each, in one sum)
@@ -348,67 +376,173 @@ struct SmKernel {
 #pragma unroll
         for (int i = 0; i < L::kPer; ++i) {
           const int e = v * L::kPer + i;
-          if (rel[e] <= bound) sm_store(rec + S::kHead + at++, (uint64_t)sm_order(x[e]) << 32 | (uint32_t)(c0 + L::column(e, tid)));
+          if (rel[e] <= bound) rec[S::kHead + at++] = (uint64_t)sm_order(x[e]) << 32 | (uint32_t)(c0 + L::column(e, tid));
         }
         base += (int)(all >> (16 * v) & 0xFFFFu);
       }
       listed = base;
     }
     if (tid == 0) {
-      sm_store(rec, (uint64_t)__float_as_uint(mx) << 32 | (uint32_t)s.bad);
-      sm_store(rec + 1, (uint64_t)(uint32_t)big << 32 | (uint32_t)(bound + 1));
-      sm_store(rec + 2, (uint64_t)(uint32_t)live << 32 | (uint32_t)listed);
-      sm_store(rec + 3, (uint64_t)__double_as_longlong(tot));
+      rec[0] = (uint64_t)__float_as_uint(mx) << 32 | (uint32_t)s.bad;
+      rec[1] = (uint64_t)(uint32_t)big << 32 | (uint32_t)(bound + 1);
+      rec[2] = (uint64_t)(uint32_t)live << 32 | (uint32_t)listed;
+      rec[3] = (uint64_t)__double_as_longlong(tot);
     }
+  }
+
+  // The second kernel's part of a row with a plan: masses and counts of what lies above the cut's bin (also of
+  // those that min-p leaves), and the bin's logits, into the record.
+  __device__ __forceinline__ void cut_part(int p, const SmPlanned& plan, uint64_t* rec) {
+    const int64_t c0 = (int64_t)p * S::kPart;
+    float x[kSmElems];
+    L::load(y, c0, a.n, tid, x);
+    if (tid == 0) s.n = 0;
+    __syncthreads();
+    double mass = 0.0;
+    unsigned long long left = 0, counts = 0;       // counts: above, and of those the ones min-p leaves << 32
+#pragma unroll
+    for (int e = 0; e < kSmElems; ++e) {
+      const int d = x[e] > -INFINITY ? plan.big - r.bin(x[e]) : 0x7FFFFFFF;
+      if (d < plan.bin) {
+        const double w = weight(x[e]);
+        mass += w;
+        const bool in = passes(w, sm_order(x[e]));
+        left += in ? fine(w) : 0;
+        counts += in ? 1ull << 32 | 1 : 1;
+      }
+      if (d == plan.bin) {
+        const int at = atomicAdd(&s.n, 1);
+        if (at < S::kCutList) rec[S::kHead + at] = (uint64_t)sm_order(x[e]) << 32 | (uint32_t)~(uint32_t)(c0 + L::column(e, tid));
+      }
+    }
+    mass = sm_sum<T>(mass, s.wd);
+    left = sm_sum<T>(left, s.wu);
+    counts = sm_sum<T>(counts, s.wu);
+    if (tid == 0) {
+      rec[0] = (uint64_t)__double_as_longlong(mass);
+      rec[1] = left;
+      rec[2] = counts;
+      rec[3] = (uint64_t)s.n;
+    }
+  }
+};
+
+// The rows' kernels: a workgroup a row.
+template <bool BF, int T>
+struct SmJoin : SmOf<BF, T> {
+  using S = SmShape<T>;
+  using L = SmLoad<BF, T>;
+  using Of = SmOf<BF, T>;
+  using Of::a, Of::tid, Of::row, Of::y, Of::parts, Of::r, Of::M, Of::top, Of::weight, Of::fine, Of::passes;
+
+  struct Shared {
+    union {
+      struct {
+        unsigned long long sorting[kSmSort];       // order, then the column's complement
+        unsigned long long cand[kSmSort];          // order, column; in column order
+      };
+      unsigned long long all[2 * kSmSort];         // the cut's bin: order, then the column's complement
+    };
+    unsigned long long mass8[256];
+    uint32_t cnt8[256];
+    double wd[T / 64];
+    unsigned long long wu[T / 64], wv[T / 64][4];
+    float wf[T / 64];
+    // the parts
+    double scale[kSmParts];
+    unsigned long long mass[kSmParts];             // of what is kept, in 2^-42
+    uint32_t ties[kSmParts];
+    int shift[kSmParts], list[kSmParts];
+    int found;
+    int at[2];
+    double val;
+  };
+  Shared& s;
+  __device__ __forceinline__ SmJoin(const SampleArgs& args, int64_t row_, int parts_, Shared& sh) : Of(args, row_, parts_), s(sh) {}
+
+  __device__ __forceinline__ void put(int64_t token, double logp, int64_t kept) const {
+    if (a.token) a.token[row] = (int32_t)token;
+    if (a.logp) a.logp[row] = (float)logp;
+    if (a.kept) a.kept[row] = (int32_t)kept;
+  }
+
+  // s.sorting's first `size` (a power of two, 64 or more) descending.  A wave has 128 of them to itself while the
+  // steps are short.
+  __device__ __forceinline__ void sort(int size) {
+    for (int len = 2; len <= size; len <<= 1)
+      for (int step = len >> 1; step > 0; step >>= 1) {
+        if (step >= 64) {
+          __syncthreads();
+        } else {
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+        }
+        for (int z = tid; z < size / 2; z += T) {
+          const int i = (z & ~(step - 1)) * 2 + (z & (step - 1)), j = i + step;
+          const unsigned long long u = s.sorting[i], v = s.sorting[j];
+          if ((u < v) == ((i & len) == 0)) {
+            s.sorting[i] = v;
+            s.sorting[j] = u;
+          }
+        }
+      }
+    __syncthreads();
   }
 
   // The token, where `cut` is known and s.mass holds the kept mass of every part (in 2^-42): the part, then in it.
   __device__ __forceinline__ void draw(SmCut cut, int64_t kept) {
-    unsigned long long sum = 0;
-    for (int p = 0; p < parts; ++p) sum += s.mass[p];
+    // (a lane a part, every wave alike)
+    const int lane = tid & 63;
+    const unsigned long long own = lane < parts ? s.mass[lane] : 0;
+    unsigned long long upto = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const unsigned long long up = __shfl_up(upto, o);
+      if (lane >= o) upto += up;
+    }
+    const unsigned long long sum = __shfl(upto, 63);
     const float u = a.u[row];
     unsigned long long want = u > 0.0f ? u < 1.0f ? (unsigned long long)((double)u * (double)sum) : sum - 1 : 0;
     if (want >= sum) want = sum - 1;
-    unsigned long long left = want;
-    int p = 0;
-    while (p < parts - 1 && left >= s.mass[p]) left -= s.mass[p++];
+    const int p = __popcll(__ballot(lane < parts - 1 && upto <= want));
+    const unsigned long long left = want - __shfl(upto - own, p);
     const int64_t c0 = (int64_t)p * S::kPart;
     float x[kSmElems];
     L::load(y, c0, a.n, tid, x);
-    unsigned long long m[kSmElems], before = 0, sofar = 0;
+    unsigned long long m[kSmElems], mine[L::kLoads], before[L::kLoads], tot[L::kLoads];
     uint32_t in = 0;
     if (tid == 0) s.found = -1;
 #pragma unroll
     for (int v = 0; v < L::kLoads; ++v) {
-      unsigned long long mine = 0;
+      mine[v] = 0;
 #pragma unroll
       for (int i = 0; i < L::kPer; ++i) {
         const int e = v * L::kPer + i;
         const uint32_t key = sm_order(x[e]);
-        m[e] = 0;
-        if (key > kSmMasked && cut.in(key, (uint32_t)(c0 + L::column(e, tid)))) {
-          const double w = weight(x[e]);
-          if (passes(w, key)) {
-            m[e] = fine(w);
-            in |= 1u << e;
-          }
-        }
-        mine += m[e];
+        const double w = weight(x[e] > -INFINITY ? x[e] : (float)M);
+        const bool is = (key > kSmMasked) & cut.in(key, (uint32_t)(c0 + L::column(e, tid))) & passes(w, key);
+        m[e] = is ? fine(w) : 0;
+        in |= is ? 1u << e : 0u;
+        mine[v] += m[e];
       }
-      const unsigned long long tot = sm_scan<T>(mine, s.wu, &before);
-      before += sofar;
+    }
+    sm_scans<T, L::kLoads>(mine, s.wv, before, tot);
+    unsigned long long sofar = 0;
+#pragma unroll
+    for (int v = 0; v < L::kLoads; ++v) {
+      unsigned long long at = sofar + before[v];
 #pragma unroll
       for (int i = 0; i < L::kPer; ++i) {
         const int e = v * L::kPer + i;
-        if (before <= left && left < before + m[e]) {
+        if (at <= left && left < at + m[e]) {
           s.found = (int)(c0 + L::column(e, tid));
-          s.val[0] = ((double)x[e] - M) * r.c;
+          s.val = ((double)x[e] - M) * r.c;
         }
-        // (the part's mass and its weights' may differ by a rounding: then the last one)
-        before += m[e];
+        at += m[e];
       }
-      sofar += tot;
+      sofar += tot[v];
     }
+    // (the part's mass and its weights' may differ by a rounding: then the last one)
     __syncthreads();
     if (s.found < 0) {
 #pragma unroll
@@ -418,10 +552,10 @@ struct SmKernel {
       const int f = s.found;
 #pragma unroll
       for (int e = 0; e < kSmElems; ++e)
-        if ((int)(c0 + L::column(e, tid)) == f) s.val[0] = ((double)x[e] - M) * r.c;
+        if ((int)(c0 + L::column(e, tid)) == f) s.val = ((double)x[e] - M) * r.c;
       __syncthreads();
     }
-    if (tid == 0) put(s.found, 0.6931471805599453 * (s.val[0] - log2((double)sum / kSmFine)), kept);
+    if (tid == 0) put(s.found, 0.6931471805599453 * (s.val - log2((double)sum / kSmFine)), kept);
   }
 
   // Every logit of the row, a part at a time: f(x, key, column, part).
@@ -465,29 +599,29 @@ struct SmKernel {
     for (int shift = 24; shift >= 0; shift -= 8) {
       __syncthreads();
       for (int b = tid; b < 256; b += T) {
-        s.sort.cnt[b] = 0;
-        s.sort.mass[b] = 0;
+        s.cnt8[b] = 0;
+        s.mass8[b] = 0;
       }
       __syncthreads();
       each([&](float x, uint32_t k, uint32_t col) {
         if ((k & mask) != key || !within.in(k, col)) return;
-        atomicAdd(&s.sort.cnt[k >> shift & 255u], 1u);
-        atomicAdd(&s.sort.mass[k >> shift & 255u], fine(weight(x)));
+        atomicAdd(&s.cnt8[k >> shift & 255u], 1u);
+        atomicAdd(&s.mass8[k >> shift & 255u], fine(weight(x)));
       }, [](int) {});
       __syncthreads();
       int bin = 0;
       unsigned long long n = had_n, m = had_m;
       for (int b = 255; b >= 0; --b) {               // (all threads alike)
-        const uint32_t c = s.sort.cnt[b];
+        const uint32_t c = s.cnt8[b];
         if (c == 0) continue;
         bin = b;
         had_n = n;
         had_m = m;
         n += c;
-        m += s.sort.mass[b];
+        m += s.mass8[b];
         if ((by_mass ? m : n) >= want) break;
       }
-      ties = s.sort.cnt[bin];
+      ties = s.cnt8[bin];
       key |= (uint32_t)bin << shift;
       mask |= 255u << shift;
     }
@@ -552,59 +686,65 @@ struct SmKernel {
   }
 
   // The row, from its parts' records.
-  __device__ __forceinline__ void join(uint64_t* rec0, SmPlanned* plan) {
+  __device__ __forceinline__ void join(const uint64_t* rec0, SmPlanned* plan) {
     const bool cuts = r.k < a.n || r.p < 1.0 || r.min_p > 0.0;
     const Rsrc recs = make_rsrc(rec0, (uint32_t)(parts * S::kRec * 8));
     if (tid == 0) plan->state = 0;
-    __syncthreads();
-    if (tid < parts) {
-      const int at = tid * S::kRec;
+    // a lane a part, every wave alike
+    const int lane = tid & 63;
+    float tops = -INFINITY;
+    bool bads = false;
+    int bigs = -1000000000, bounds = kSmBins - 1, lists_n = 0, lives = 0;
+    double totals = 0.0;
+    if (lane < parts) {
+      const int at = lane * S::kRec;
       const uint64_t h0 = sm_load(recs, at), h1 = sm_load(recs, at + 1), h2 = sm_load(recs, at + 2), h3 = sm_load(recs, at + 3);
-      s.top[tid] = __uint_as_float((uint32_t)(h0 >> 32));
-      s.ties[tid] = (uint32_t)h0;                  // bad
-      s.shift[tid] = (int)(uint32_t)(h1 >> 32);
-      s.bound[tid] = (int)(uint32_t)h1 - 1;
-      s.list[tid + 1] = (int)(uint32_t)h2;
-      s.live[tid] = (int)(h2 >> 32);
-      s.total[tid] = __longlong_as_double((long long)h3);
+      tops = __uint_as_float((uint32_t)(h0 >> 32));
+      bads = (uint32_t)h0 != 0;
+      bigs = (int)(uint32_t)(h1 >> 32);
+      bounds = (int)(uint32_t)h1 - 1;
+      lists_n = (int)(uint32_t)h2;
+      lives = (int)(h2 >> 32);
+      totals = __longlong_as_double((long long)h3);
     }
-    __syncthreads();
-    bool bad = false;
-    float mx = -INFINITY;
-    int big = -1000000000;
-    for (int p = 0; p < parts; ++p) {
-      bad |= s.ties[p] != 0;
-      mx = fmaxf(mx, s.top[p]);
-      big = s.shift[p] > big ? s.shift[p] : big;
+    float mx = tops;
+    int big = bigs;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      mx = fmaxf(mx, __shfl_xor(mx, o));
+      const int ob = __shfl_xor(big, o);
+      big = ob > big ? ob : big;
     }
+    const bool bad = __ballot(bads) != 0;
     if (bad || mx == -INFINITY) {
       if (tid == 0) put(-1, bad ? (double)__uint_as_float(0x7FC00000u) : -(double)INFINITY, 0);
       return;
     }
-    M = (double)mx;
-    top = sm_order(mx);
+    this->is_top(mx);
+    const double scale = tops > -INFINITY ? sm_exp2(((double)tops - M) * r.c) : 0.0;
+    const int shifts = big - bigs;
+    double W = totals * scale;                     // (top-k off: the row's mass)
     __syncthreads();
     if (tid < parts) {
-      s.scale[tid] = s.top[tid] > -INFINITY ? sm_exp2(((double)s.top[tid] - M) * r.c) : 0.0;
-      s.shift[tid] = big - s.shift[tid];
-      s.mass[tid] = fine(s.total[tid] * s.scale[tid]);
+      s.scale[tid] = scale;
+      s.shift[tid] = shifts;
+      s.list[tid] = lists_n;
+      s.mass[tid] = fine(W);
     }
-    if (tid == 0) {
-      s.list[0] = 0;
-      for (int p = 0; p < parts; ++p) s.list[p + 1] += s.list[p];
-    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) W += __shfl_xor(W, o);
     __syncthreads();
     if (!cuts) {
-      int64_t live = 0;
-      for (int p = 0; p < parts; ++p) live += s.live[p];
-      draw({kSmMasked + 1, 0xFFFFFFFFu}, live);
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) lives += __shfl_xor(lives, o);
+      draw({kSmMasked + 1, 0xFFFFFFFFu}, lives);
       return;
     }
-    double W = 0.0;                                // (top-k off: the row's mass)
-    for (int p = 0; p < parts; ++p) W += s.total[p] * s.scale[p];
 
-    // the row's histogram, a run of bins a thread, and how far down what is kept can reach
-    constexpr int kBpt = kSmBins / T;
+    // the row's histogram (with top-k of counts, else of masses), a run of bins a thread, and how far down what
+    // is kept can reach
+    const bool counted = r.k < a.n;
+    constexpr int kBpt = S::kBpt;
     int cnt[kBpt];
     double ms[kBpt];
     int cs = 0;
@@ -614,27 +754,27 @@ struct SmKernel {
       cnt[i] = 0;
       ms[i] = 0.0;
     }
-    constexpr int kAhead = 8;                      // parts in flight
+    constexpr int kAhead = 16;                     // parts in flight
     for (int p0 = 0; p0 < parts; p0 += kAhead) {
-      uint64_t v[kAhead][kBpt];
+      uint32_t v[kAhead][kBpt];
 #pragma unroll
       for (int z = 0; z < kAhead; ++z) {
         const int p = p0 + z < parts ? p0 + z : parts - 1;
-        const int h = p * S::kRec + S::kHead + S::kList, sh = s.shift[p];
+        const int h = (p * S::kRec + S::kHead + S::kList) * 2, sh = s.shift[p];
 #pragma unroll
         for (int i = 0; i < kBpt; ++i) {
           // (the last bin takes what lies below in its part, too)
           const int b = tid * kBpt + i - sh;
-          v[z][i] = sm_load(recs, p0 + z < parts && tid * kBpt + i < kSmBins - 1 && b >= 0 ? h + b : (1 << 28) - 1);
+          v[z][i] = sm_load32(recs, p0 + z < parts && tid * kBpt + i < kSmBins - 1 && b >= 0 ? h + b : S::kNone);
         }
       }
 #pragma unroll
       for (int z = 0; z < kAhead; ++z) {
-        const double sc = s.scale[p0 + z < parts ? p0 + z : parts - 1] * (1.0 / 1073741824.0);
+        const double sc = s.scale[p0 + z < parts ? p0 + z : parts - 1];
 #pragma unroll
         for (int i = 0; i < kBpt; ++i) {
-          cnt[i] += (int)(v[z][i] >> 48);
-          ms[i] += sc * (double)(v[z][i] & 0xFFFFFFFFFFFFull);
+          if (counted) cnt[i] += (int)v[z][i];
+          else ms[i] += sc * (double)__uint_as_float(v[z][i]);
         }
       }
     }
@@ -643,306 +783,264 @@ struct SmKernel {
       cs += cnt[i];
       md += ms[i];
     }
-    int c_before;
-    double m_before;
-    sm_scan<T>(cs, reinterpret_cast<int*>(s.wf), &c_before);
-    sm_scan<T>(md, s.wd, &m_before);
-    // the first bin with k tokens, or with p of the mass
-    int kb = kSmBins - 1;
-    if (tid == 0) {
-      s.at[0] = kSmBins - 1;
-      s.at[1] = kSmBins - 1;
-    }
-    __syncthreads();
-    int c = c_before;
-    if (r.k < a.n) {
+    int bin = kSmBins - 1;
+    if (tid == 0) s.at[0] = kSmBins - 1;
+    if (counted) {
+      int c;
+      sm_scan<T>(cs, reinterpret_cast<int*>(s.wf), &c);
 #pragma unroll
       for (int i = 0; i < kBpt; ++i) {
         if (c < r.k && c + cnt[i] >= r.k && tid * kBpt + i < kSmBins - 1) s.at[0] = tid * kBpt + i;
         c += cnt[i];
       }
       __syncthreads();
-      kb = s.at[0];
-    }
-    int need = kb, pb = kSmBins - 1;
-    if (r.p < 1.0 && !(r.k < a.n)) {
-      const double want = r.p * W * (1.0 + 1e-5);
-      double m = m_before;
+      bin = s.at[0];
+    } else if (r.p < 1.0) {
+      double m;
+      sm_scan<T>(md, s.wd, &m);
+      const double want = r.p * W;
 #pragma unroll
       for (int i = 0; i < kBpt; ++i) {
-        if (m < want && m + ms[i] >= want && tid * kBpt + i < kSmBins - 1) s.at[1] = tid * kBpt + i;
+        if (m < want && m + ms[i] >= want && tid * kBpt + i < kSmBins - 1) s.at[0] = tid * kBpt + i;
         m += ms[i];
       }
       __syncthreads();
-      pb = want > 0.0 ? s.at[1] : 0;
-      need = pb < need ? pb : need;
+      bin = want > 0.0 ? s.at[0] : 0;
     }
+    int need = bin;
     // (top-k and top-p together: the mass of all k is asked for)
     bool by_min = false;
     if (r.min_p > 0.0 && !(r.k < a.n && r.p < 1.0)) {
-      const double f = r.min_p < 1.0 ? -log2(r.min_p) * kSmPerOctave + 3.0 : 3.0;
+      const double f = r.min_p < 1.0 ? -log2(r.min_p) / r.c * (double)r.bins + 3.0 : 3.0;
       if (f < (double)need) {
         need = (int)f;
         by_min = true;
       }
     }
-    // whether the lists have all of that
-    bool lists = need < kSmBins - 1;
-    for (int p = 0; p < parts; ++p) lists = lists && need - s.shift[p] <= s.bound[p];
-    if (need >= kSmBins - 1) {
-      lists = true;                                // (all of every part)
-      for (int p = 0; p < parts; ++p) lists = lists && s.bound[p] == kSmBins - 1;
+    // how far down every list reaches (its last bin: all of a part)
+    int reach = bounds == kSmBins - 1 ? kSmAll : bounds + shifts;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      const int other = __shfl_xor(reach, o);
+      reach = other < reach ? other : reach;
     }
-    if (lists && from_lists(recs, need, by_min, big, W)) return;
+    const bool lists = need < kSmBins - 1 ? need <= reach : reach == kSmAll;
+    // top-p may end well before the last one of top-k, whose mass then hardly counts
+    const bool partly = !lists && counted && r.p < 1.0 && reach >= 0;
+    if (partly) need = reach < kSmBins - 2 ? reach : kSmBins - 2;
+    if ((lists || partly) && from_lists(recs, need, by_min, partly, big, W)) return;
     if (tid != 0) return;
-    const int bin = r.k < a.n ? kb : r.p < 1.0 ? pb : kSmAll;
-    plan->state = r.k < a.n && r.p < 1.0 ? 2 : bin == kSmBins - 1 ? 2 : 1;
+    bin = counted || r.p < 1.0 ? bin : kSmAll;
+    plan->state = (counted && r.p < 1.0) || bin == kSmBins - 1 ? 2 : 1;
     plan->bin = bin;
     plan->big = big;
     plan->M = mx;
     plan->W = W;
   }
 
-  // The second kernel's part of a row with a plan: masses and counts of what lies above the cut's bin (also of
-  // those that min-p leaves), and the bin's logits, into the record.
-  __device__ __forceinline__ void cut_part(int p, const SmPlanned& plan, uint64_t* rec) {
-    const int64_t c0 = (int64_t)p * S::kPart;
-    float x[kSmElems];
-    L::load(y, c0, a.n, tid, x);
-    if (tid == 0) s.n = 0;
-    __syncthreads();
-    double mass = 0.0;
-    unsigned long long left = 0, counts = 0;       // counts: above, and of those the ones min-p leaves << 32
-#pragma unroll
-    for (int e = 0; e < kSmElems; ++e) {
-      const int d = x[e] > -INFINITY ? plan.big - r.bin(x[e]) : 0x7FFFFFFF;
-      if (d < plan.bin) {
-        const double w = weight(x[e]);
-        mass += w;
-        const bool in = passes(w, sm_order(x[e]));
-        left += in ? fine(w) : 0;
-        counts += in ? 1ull << 32 | 1 : 1;
-      }
-      if (d == plan.bin) {
-        const int at = atomicAdd(&s.n, 1);
-        if (at < kSmBins) sm_store(rec + S::kHead + S::kList + at, (uint64_t)sm_order(x[e]) << 32 | (uint32_t)~(uint32_t)(c0 + L::column(e, tid)));
-      }
-    }
-    mass = sm_sum<T>(mass, s.wd);
-    left = sm_sum<T>(left, s.wu);
-    counts = sm_sum<T>(counts, s.wu);
-    if (tid == 0) {
-      sm_store(rec, (uint64_t)__double_as_longlong(mass));
-      sm_store(rec + 1, left);
-      sm_store(rec + 2, counts);
-      sm_store(rec + 3, (uint64_t)s.n);
-    }
-  }
-
-  // And the row's last one: the bin sorted and cut, the token drawn.
-  __device__ __forceinline__ void cut_join(const SmPlanned& plan, uint64_t* rec0) {
+  // A row with a plan, from its second records: the bin sorted and cut, the token drawn.
+  __device__ __forceinline__ void cut_join(const SmPlanned& plan, const uint64_t* rec0) {
     const Rsrc recs = make_rsrc(rec0, (uint32_t)(parts * S::kRec * 8));
-    __syncthreads();
-    if (tid < parts) {
-      const int at = tid * S::kRec;
-      s.total[tid] = __longlong_as_double((long long)sm_load(recs, at));
-      s.mass[tid] = sm_load(recs, at + 1);
-      const uint64_t c = sm_load(recs, at + 2);
-      s.ties[tid] = (uint32_t)c;
-      s.live[tid] = (int)(c >> 32);
-      s.list[tid + 1] = (int)sm_load(recs, at + 3);
-    }
-    if (tid == 0) s.list[0] = 0;
-    __syncthreads();
+    const int lane = tid & 63;
     double above = 0.0;
-    int64_t count = 0, kept = 0;
-    bool fits = true;
-    int n = 0;
-    for (int p = 0; p < parts; ++p) {
-      above += s.total[p];
-      count += s.ties[p];
-      kept += s.live[p];
-      fits = fits && s.list[p + 1] <= kSmBins;
-      n += s.list[p + 1];
+    int count = 0, kept = 0, mine_n = 0;
+    if (lane < parts) {
+      const int at = lane * S::kRec;
+      above = __longlong_as_double((long long)sm_load(recs, at));
+      const uint64_t m = sm_load(recs, at + 1), c = sm_load(recs, at + 2);
+      if (tid < parts) s.mass[tid] = m;
+      count = (int)(uint32_t)c;
+      kept = (int)(c >> 32);
+      mine_n = (int)sm_load(recs, at + 3);
     }
-    if (!fits || n > kSmSort) {
+    int upto_n = mine_n;
+    const bool fits = __ballot(mine_n > S::kCutList) == 0;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      above += __shfl_xor(above, o);
+      count += __shfl_xor(count, o);
+      kept += __shfl_xor(kept, o);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(upto_n, o);
+      if (lane >= o) upto_n += up;
+    }
+    const int n = __shfl(upto_n, 63);
+    if (!fits || n > 2 * kSmSort) {
       whole_row();
       return;
     }
     SmCut cut = {kSmMasked + 1, 0xFFFFFFFFu};
     if (plan.bin < kSmBins) {
+      if (tid < parts) s.list[tid] = upto_n - mine_n;
       __syncthreads();
-      if (tid == 0)
-        for (int p = 0; p < parts; ++p) s.list[p + 1] += s.list[p];
+      // the bin's logits, a wave a part
+      for (int p = tid >> 6; p < parts; p += T / 64) {
+        const int at = s.list[p], size = (p + 1 < parts ? s.list[p + 1] : n) - at;
+        for (int e = lane; e < size; e += 64) s.all[at + e] = sm_load(recs, p * S::kRec + S::kHead + e);
+      }
       __syncthreads();
-      int size = 64;                               // the sort's, a power of two
-      while (size < n) size <<= 1;
-      for (int i = tid; i < size; i += T) {
-        unsigned long long v = 0;
-        if (i < n) {
-          const int p = part_of(i);
-          v = sm_load(recs, p * S::kRec + S::kHead + S::kList + (i - s.list[p]));
-        }
-        s.sorting[i] = v;
-      }
-      // descending, by runs of twice the length each round
-      for (int len = 2; len <= size; len <<= 1)
-        for (int step = len >> 1; step > 0; step >>= 1) {
-          __syncthreads();
-          for (int z = tid; z < size / 2; z += T) {
-            const int i = (z / step * 2) * step + z % step, j = i + step;
-            const unsigned long long u = s.sorting[i], v = s.sorting[j];
-            if ((u < v) == ((i & len) == 0)) {
-              s.sorting[i] = v;
-              s.sorting[j] = u;
-            }
-          }
-        }
-      __syncthreads();
-      // the last one kept of them
-      constexpr int kMine = kSmSort / T;
-      double w[kMine], mine = 0.0, before;
-#pragma unroll
-      for (int q = 0; q < kMine; ++q) {
-        const int i = tid * kMine + q;
-        w[q] = i < n ? weight(sm_value((uint32_t)(s.sorting[i] >> 32))) : 0.0;
-        mine += w[q];
-      }
-      const double all = sm_scan<T>(mine, s.wd, &before);
-      int upto;                                    // how many are kept
-      if (r.k < a.n) {
-        upto = (int)(r.k - count);
-        if (r.k <= count || r.k > count + n) upto = 0;
-      } else {
-        const double want = r.p * plan.W - above;
-        int short_of = 0;
-#pragma unroll
-        for (int q = 0; q < kMine; ++q) {
-          before += w[q];
-          short_of += tid * kMine + q < n && before < want ? 1 : 0;
-        }
-        upto = sm_sum<T>(short_of, reinterpret_cast<int*>(s.wf)) + 1;
-        if ((want <= 0.0 && count > 0) || upto > n || all < want) upto = 0;
-      }
-      if (upto == 0) {                             // (the histogram's masses were off by a bin)
-        whole_row();
+      const double want = r.k < a.n ? (double)(r.k - count) : r.p * plan.W - above;
+      unsigned long long last;
+      if (!(want > 0.0 || count == 0) || !select(n, !(r.k < a.n), want, plan.bin, &last)) {
+        whole_row();                               // (the histogram's masses were off by a bin)
         return;
       }
-      const unsigned long long last = s.sorting[upto - 1];
       cut = {(uint32_t)(last >> 32), ~(uint32_t)last};
-      unsigned long long more = 0;
-      for (int i = tid; i < upto; i += T) {
-        const unsigned long long v = s.sorting[i];
+      int more = 0;
+      for (int i = tid; i < n; i += T) {
+        const unsigned long long v = s.all[i];
+        if (v < last) continue;
         const double wi = weight(sm_value((uint32_t)(v >> 32)));
         if (passes(wi, (uint32_t)(v >> 32))) {
           atomicAdd(&s.mass[~(uint32_t)v / (uint32_t)S::kPart], fine(wi));
           ++more;
         }
       }
-      kept += (int64_t)sm_sum<T>(more, s.wu);
+      kept += sm_sum<T>(more, reinterpret_cast<int*>(s.wf));
     }
     __syncthreads();
     draw(cut, kept);
   }
 
-  // the part that entry i of the lists is in
-  __device__ __forceinline__ int part_of(int i) const {
-    int lo = 0, hi = parts;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s.list[mid] <= i) lo = mid;
-      else hi = mid;
+  // Of s.all's n logits, all of bin `bin`, the one in descending order at which `want` of them (by_mass: that mass)
+  // have come; false if they never do.  8 bits of the order and the column at a time, from the first that
+  // differ; masses as integers of 2^-50 of the bin's.
+  __device__ __forceinline__ bool select(int n, bool by_mass, double want, int bin, unsigned long long* last) {
+    const unsigned long long first = s.all[0];
+    unsigned long long diff = 0;
+    for (int i = tid; i < n; i += T) diff |= s.all[i] ^ first;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) diff |= __shfl_xor(diff, o);
+    if ((tid & 63) == 0) s.wu[tid >> 6] = diff;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) diff |= s.wu[i];
+    const int scale = 49 + bin / (int)kSmPerOctave;
+    unsigned long long left = 1;                   // (at least one)
+    if (by_mass) {
+      const double f = ceil(__builtin_ldexp(want, scale));
+      if (f > 9e18) return false;
+      if (f > 1.0) left = (unsigned long long)f;
+    } else if (want > 1.0) {
+      left = (unsigned long long)want;
     }
-    return lo;
+    int shift = diff ? 63 - __builtin_clzll(diff) - 7 : 0;
+    shift = shift > 0 ? shift : 0;
+    unsigned long long mask = shift < 56 ? ~0ull << (shift + 8) : 0ull, key = first & mask;
+    for (bool again = false;; again = true) {
+      __syncthreads();
+      for (int b = tid; b < 256; b += T) {
+        s.mass8[b] = 0;
+        s.cnt8[b] = 0;
+      }
+      __syncthreads();
+      for (int i = tid; i < n; i += T) {
+        const unsigned long long v = s.all[i];
+        if ((v & mask) != key) continue;
+        const int d = (int)(v >> shift & 255u);
+        atomicAdd(&s.cnt8[d], 1u);
+        if (by_mass) atomicAdd(&s.mass8[d], (unsigned long long)(__builtin_ldexp(weight(sm_value((uint32_t)(v >> 32))), scale) + 0.5));
+      }
+      __syncthreads();
+      unsigned long long mine = 0, before;
+      if (tid < 256) mine = by_mass ? s.mass8[255 - tid] : s.cnt8[255 - tid];
+      const unsigned long long all = sm_scan<T>(mine, s.wu, &before);
+      if (!again && all < left) return false;
+      if (before < left && left <= before + mine) {
+        s.at[0] = 255 - tid;
+        s.wv[0][0] = before;
+      }
+      __syncthreads();
+      const int d = s.at[0];
+      left -= s.wv[0][0];
+      key |= (unsigned long long)d << shift;
+      mask |= 255ull << shift;
+      if (s.cnt8[d] == 1) break;
+      shift = shift > 8 ? shift - 8 : 0;
+    }
+    for (int i = tid; i < n; i += T)
+      if ((s.all[i] & mask) == key) s.wv[0][1] = s.all[i];
+    __syncthreads();
+    *last = s.wv[0][1];
+    return true;
   }
 
   // Cuts and draws from the lists' logits down to bin `need`; false if they turn out not to reach the cut.
-  __device__ __forceinline__ bool from_lists(Rsrc recs, int need, bool by_min, int big, double W) {
-    __syncthreads();
-    const int all = s.list[parts];
-    if (all > kSmLists) return false;
-#pragma unroll 4
-    for (int i = tid; i < all; i += T) {
-      const int p = part_of(i);
-      s.cand.raw[i] = sm_load(recs, p * S::kRec + S::kHead + (i - s.list[p]));
-    }
-    __syncthreads();
-    // a run of the entries a thread, so that one sum gives their places
-    const int run = (all + T - 1) / T, i1 = (tid + 1) * run < all ? (tid + 1) * run : all;
-    const auto in = [&](int i) {
-      return need >= kSmBins - 1 || big - r.bin(sm_value((uint32_t)(s.cand.raw[i] >> 32))) <= need;
-    };
-    int mine_n = 0, at0;
-#pragma unroll 1
-    for (int i = tid * run; i < i1; ++i) mine_n += in(i) ? 1 : 0;
-    const int n = sm_scan<T>(mine_n, reinterpret_cast<int*>(s.wf), &at0);
-    if (n > kSmCand) return false;
-#pragma unroll 1
-    for (int i = tid * run; i < i1; ++i)
-      if (in(i)) {
-        s.cand.key[at0] = (uint32_t)(s.cand.raw[i] >> 32);
-        s.cand.col[at0++] = (uint32_t)s.cand.raw[i];
-      }
-    __syncthreads();
-#pragma unroll 1
-    for (int i = tid; i < n; i += T) s.cand.w[i] = weight(sm_value(s.cand.key[i]));
-    __syncthreads();
-    // ranks in the tokens' order
-    constexpr int kMine = kSmCand / T;
-    int rank[kMine];
+  __device__ __forceinline__ bool from_lists(Rsrc recs, int need, bool by_min, bool partly, int big, double W) {
+    // a run of the lists' slots a thread, so that one sum gives their places
+    constexpr int kMost = kSmParts * S::kList / T;
+    const int slots = parts * S::kList, run = (slots + T - 1) / T;
+    uint64_t v[kMost];
 #pragma unroll
-    for (int q = 0; q < kMine; ++q) {
-      const int i = q * T + tid;
-      rank[q] = kSmCand;
-      if (i >= n) continue;
-      const uint32_t key = s.cand.key[i];
-      int k = 0;
-      for (int j = 0; j < n; ++j) {
-        const uint32_t o = s.cand.key[j];
-        k += o > key || (o == key && j < i) ? 1 : 0;
-      }
-      rank[q] = k;
-      s.cand.sorted[k] = s.cand.w[i];
+    for (int q = 0; q < kMost; ++q) {
+      const int i = tid * run + q, p = i / S::kList, e = i % S::kList;
+      const bool is = q < run && i < slots && e < s.list[i < slots ? p : 0];
+      v[q] = sm_load(recs, is ? p * S::kRec + S::kHead + e : S::kNone);     // (nothing: 0)
     }
+    uint32_t in = 0;
+    int at0, all = 0;
+#pragma unroll
+    for (int q = 0; q < kMost; ++q) {
+      in |= (v[q] != 0) & ((need >= kSmBins - 1) | (big - r.bin(sm_value((uint32_t)(v[q] >> 32))) <= need)) ? 1u << q : 0u;
+      all += v[q] != 0 ? 1 : 0;
+    }
+    const int n = sm_scan<T>((int)__popc(in), reinterpret_cast<int*>(s.wf), &at0);
+    all = sm_sum<T>(all, reinterpret_cast<int*>(s.wf));
+    if (n > kSmSort) return false;
+#pragma unroll
+    for (int q = 0; q < kMost; ++q)
+      if (in >> q & 1u) {
+        s.cand[at0] = v[q];
+        s.sorting[at0++] = v[q] ^ 0xFFFFFFFFu;
+      }
+    int size = 64;
+    while (size < n) size <<= 1;
+    for (int i = n + tid; i < size; i += T) s.sorting[i] = 0;
     __syncthreads();
-    // masses in that order (a run of ranks a thread)
+    sort(size);
+    // masses in the tokens' order, a run of them a thread
+    constexpr int kMine = kSmSort / T;
+    const int own_n = (n + T - 1) / T, r0 = tid * own_n, kk = r.k < n ? (int)r.k : n;
     double own[kMine], mine = 0.0, before;
-    const int r0 = tid * kMine, kk = r.k < n ? (int)r.k : n;
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
-      own[q] = r0 + q < kk ? s.cand.sorted[r0 + q] : 0.0;
+      own[q] = 0.0;
+      if (q < own_n && r0 + q < kk) own[q] = weight(sm_value((uint32_t)(s.sorting[r0 + q] >> 32)));
       mine += own[q];
     }
     const double listed = sm_scan<T>(mine, s.wd, &before);
-    const double mass = r.k < a.n ? listed : W, want = r.p * mass;
-    const bool ends = s.list[parts] == n && need >= kSmBins - 1;   // (nothing else is left)
+    const double want = r.p * (r.k < a.n ? listed : W);
+    // (of those of top-k that are not here, each is below the border of bin `need`)
+    const double most = partly ? r.p * (listed + (double)(r.k - n) * 1.001 * sm_exp2(-(double)need * r.c / (double)r.bins)) : want;
+    const bool ends = all == n && need >= kSmBins - 1;   // (nothing else is left)
     // is the end of what is kept among them?
-    if (!ends && !by_min && !(r.k < a.n ? n >= r.k : r.p < 1.0 && listed >= want)) return false;
-    int keep = 0;
+    if (!(partly ? listed >= most : ends || by_min || (r.k < a.n ? n >= r.k : r.p < 1.0 && listed >= want))) return false;
+    int keep = 0, keeps = 0;
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
       const int i = r0 + q;
-      if (i < kk && (i == 0 || ((r.p >= 1.0 || before < want) && own[q] >= r.min_p))) ++keep;
+      if (q < own_n && i < kk) {
+        if (i == 0 || ((r.p >= 1.0 || before < want) && own[q] >= r.min_p)) ++keep;
+        if (i == 0 || ((r.p >= 1.0 || before < most) && own[q] >= r.min_p)) ++keeps;
+      }
       before += own[q];
     }
     keep = sm_sum<T>(keep, reinterpret_cast<int*>(s.wf));
-    // in column order
+    if (partly && sm_sum<T>(keeps, reinterpret_cast<int*>(s.wf)) != keep) return false;
+    const unsigned long long last = s.sorting[keep - 1];
+    const SmCut cut = {(uint32_t)(last >> 32), ~(uint32_t)last};
+    // and in column order
     mine = 0.0;
-    double mw[kMine];
-    int at[kMine];
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < kMine; ++q) {
-      const int i = q * T + tid;
-      if (i < n && rank[q] >= keep) s.cand.w[i] = 0.0;
-    }
     if (tid == 0) s.found = -1;
-    __syncthreads();
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
-      at[q] = r0 + q;
-      mw[q] = at[q] < n ? s.cand.w[at[q]] : 0.0;
-      mine += mw[q];
+      const unsigned long long v1 = s.cand[q < own_n && r0 + q < n ? r0 + q : 0];
+      const bool is = q < own_n && r0 + q < n && cut.in((uint32_t)(v1 >> 32), (uint32_t)v1);
+      own[q] = 0.0;
+      if (is) own[q] = weight(sm_value((uint32_t)(v1 >> 32)));
+      mine += own[q];
     }
     const double sum = sm_scan<T>(mine, s.wd, &before);
     const float u = a.u[row];
@@ -950,90 +1048,73 @@ struct SmKernel {
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
       // (the border that the next one starts from is the one this one ends at)
-      const double end = before + mw[q];
-      if (mw[q] > 0.0 && before <= target && target < end) s.found = at[q];
+      const double end = before + own[q];
+      if (own[q] > 0.0 && before <= target && target < end) s.found = r0 + q;
       before = end;
     }
     __syncthreads();
     if (s.found < 0) {                             // u of 1 or more, or a rounding at the end
 #pragma unroll
       for (int q = 0; q < kMine; ++q)
-        if (mw[q] > 0.0) atomicMax(&s.found, at[q]);
+        if (own[q] > 0.0) atomicMax(&s.found, r0 + q);
       __syncthreads();
     }
     if (tid == 0) {
-      const int f = s.found;
-      const double d = ((double)sm_value(s.cand.key[f]) - M) * r.c;
-      put(s.cand.col[f], r.hard ? 0.0 : 0.6931471805599453 * (d - log2(sum)), keep);
+      const unsigned long long f = s.cand[s.found];
+      const double d = ((double)sm_value((uint32_t)(f >> 32)) - M) * r.c;
+      put((uint32_t)f, r.hard ? 0.0 : 0.6931471805599453 * (d - log2(sum)), keep);
     }
     return true;
   }
 };
 
-// Whether this is the row's last workgroup to get here, all stores of the others to be seen.
-template <class Shared>
-__device__ __forceinline__ bool sm_last(uint32_t* count, int parts, Shared& s) {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  if (parts == 1) return true;
-  if (threadIdx.x == 0) {
-    const uint32_t old = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    s.last = old == (uint32_t)parts - 1 ? 1 : 0;
-    if (s.last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  const bool last = s.last != 0;
-  asm volatile("" ::: "memory");
-  return last;
-}
-
 template <bool BF, int T>
-__global__ __launch_bounds__(T) void k_sample(SampleArgs a, int parts, uint32_t* count, SmPlanned* plans, uint64_t* recs) {
-  using K = SmKernel<BF, T>;
-  __shared__ typename K::Shared s;
+__global__ __launch_bounds__(T, 6) void k_sample(SampleArgs a, int parts, uint64_t* recs) {
+  __shared__ typename SmPart<BF, T>::Shared s;
   const int64_t row = blockIdx.x / parts;
-  const int p = (int)(blockIdx.x - row * parts);
-  const float temp = a.temperature ? a.temperature[row] : 1.0f;
-  uint64_t* const rec0 = recs + row * parts * SmShape<T>::kRec;
-  K k = {a, s, (int)threadIdx.x, row, static_cast<const uint8_t*>(a.y) + row * a.ldy * (BF ? 2 : 4), parts, SmRow(a, row, temp)};
-  k.part(p, temp, rec0 + (int64_t)p * SmShape<T>::kRec);
-  if (sm_last(&count[row * kSmCountStep], parts, s)) k.join(rec0, plans + row);
+  SmPart<BF, T> k(a, row, parts, s);
+  k.part((int)(blockIdx.x - row * parts), recs + (int64_t)blockIdx.x * SmShape<T>::kRec);
 }
-
 template <bool BF, int T>
-__global__ __launch_bounds__(T) void k_sample_cut(SampleArgs a, int parts, uint32_t* count, const SmPlanned* plans, uint64_t* recs) {
-  using K = SmKernel<BF, T>;
-  __shared__ typename K::Shared s;
+__global__ __launch_bounds__(T) void k_sample_join(SampleArgs a, int parts, SmPlanned* plans, const uint64_t* recs) {
+  __shared__ typename SmJoin<BF, T>::Shared s;
+  const int64_t row = blockIdx.x;
+  SmJoin<BF, T> k(a, row, parts, s);
+  k.join(recs + row * parts * SmShape<T>::kRec, plans + row);
+}
+template <bool BF, int T>
+__global__ __launch_bounds__(T, 6) void k_sample_cut(SampleArgs a, int parts, const SmPlanned* plans, uint64_t* recs) {
+  __shared__ typename SmPart<BF, T>::Shared s;
   const int64_t row = blockIdx.x / parts;
   const SmPlanned plan = plans[row];
+  if (plan.state != 1) return;
+  SmPart<BF, T> k(a, row, parts, s);
+  k.is_top(plan.M);
+  k.cut_part((int)(blockIdx.x - row * parts), plan, recs + (int64_t)blockIdx.x * SmShape<T>::kRec);
+}
+template <bool BF, int T>
+__global__ __launch_bounds__(T) void k_sample_cut_join(SampleArgs a, int parts, const SmPlanned* plans, const uint64_t* recs) {
+  __shared__ typename SmJoin<BF, T>::Shared s;
+  const int64_t row = blockIdx.x;
+  const SmPlanned plan = plans[row];
   if (plan.state == 0) return;
-  const int p = (int)(blockIdx.x - row * parts);
-  if (plan.state == 2 && p > 0) return;
-  const float temp = a.temperature ? a.temperature[row] : 1.0f;
-  uint64_t* const rec0 = recs + row * parts * SmShape<T>::kRec;
-  K k = {a, s, (int)threadIdx.x, row, static_cast<const uint8_t*>(a.y) + row * a.ldy * (BF ? 2 : 4), parts, SmRow(a, row, temp)};
-  k.M = (double)plan.M;
-  k.top = sm_order(plan.M);
-  if (plan.state == 2) {
-    k.whole_row();
-    return;
-  }
-  k.cut_part(p, plan, rec0 + (int64_t)p * SmShape<T>::kRec);
-  if (sm_last(&count[row * kSmCountStep], parts, s)) k.cut_join(plan, rec0);
+  SmJoin<BF, T> k(a, row, parts, s);
+  k.is_top(plan.M);
+  if (plan.state == 2) k.whole_row();
+  else k.cut_join(plan, recs + row * parts * SmShape<T>::kRec);
 }
 
-// Parts of 4096 logits while they are few for the chip (a row's latency), else of 16384 (records are then a
-// smaller share of what is read).
+// Parts of 4096 logits; of 16384 where a row would have more than 64 of them.
 struct SmPlan {
   bool wide;              // 1024 threads
   int parts;
   int64_t rec;            // bytes
   int64_t rows;           // of a launch
 };
-static SmPlan sm_plan(const DevInfo& di, int64_t m, int64_t n) {
+static SmPlan sm_plan(int64_t m, int64_t n) {
   SmPlan p;
   const int64_t few = (n + SmShape<256>::kPart - 1) / SmShape<256>::kPart;
-  p.wide = few > kSmParts || m * few > (int64_t)di.cus * 4;
+  p.wide = few > kSmParts;
   const int64_t size = p.wide ? SmShape<1024>::kPart : SmShape<256>::kPart;
   p.parts = (int)((n + size - 1) / size);
   p.rec = (p.wide ? SmShape<1024>::kRec : SmShape<256>::kRec) * 8;
@@ -1043,37 +1124,34 @@ static SmPlan sm_plan(const DevInfo& di, int64_t m, int64_t n) {
   return p;
 }
 
-uint64_t sample_scratch(const DevInfo& di, int64_t m, int64_t n, bool, uint64_t* zero) {
-  const SmPlan p = sm_plan(di, m, n);
-  *zero = (uint64_t)kSmRows * kSmCountStep * sizeof(uint32_t);
-  return *zero + (uint64_t)(p.rows * (p.parts * p.rec + (int64_t)sizeof(SmPlanned)));
+uint64_t sample_scratch(int64_t m, int64_t n) {
+  const SmPlan p = sm_plan(m, n);
+  return (uint64_t)(p.rows * (p.parts * p.rec + (int64_t)sizeof(SmPlanned)));
 }
 
 template <bool BF, int T>
-static void sm_go(dim3 grid, hipStream_t s, const SampleArgs& a, int parts, uint32_t* count, SmPlanned* plans, uint64_t* recs,
-                  bool cuts) {
-  hipLaunchKernelGGL((k_sample<BF, T>), grid, dim3(T), 0, s, a, parts, count, plans, recs);
-  if (cuts) hipLaunchKernelGGL((k_sample_cut<BF, T>), grid, dim3(T), 0, s, a, parts, count, plans, recs);
+static void sm_go(hipStream_t s, const SampleArgs& a, int parts, SmPlanned* plans, uint64_t* recs, bool cuts) {
+  const dim3 rows((unsigned)a.m), all((unsigned)(a.m * parts));
+  hipLaunchKernelGGL((k_sample<BF, T>), all, dim3(T), 0, s, a, parts, recs);
+  hipLaunchKernelGGL((k_sample_join<BF, T>), rows, dim3(T), 0, s, a, parts, plans, recs);
+  if (!cuts) return;
+  hipLaunchKernelGGL((k_sample_cut<BF, T>), all, dim3(T), 0, s, a, parts, plans, recs);
+  hipLaunchKernelGGL((k_sample_cut_join<BF, T>), rows, dim3(T), 0, s, a, parts, plans, recs);
 }
 
 hipError_t launch_sample(const SampleArgs& a0, bool bf, void* scratch, hipStream_t s) {
-  DevInfo di;
-  const hipError_t err = dev_info(&di);
-  if (err != hipSuccess) return err;
-  const SmPlan p = sm_plan(di, a0.m, a0.n);
+  const SmPlan p = sm_plan(a0.m, a0.n);
   if (p.parts > kSmParts) return hipErrorInvalidValue;
   SampleArgs a = a0;
-  uint32_t* const count = static_cast<uint32_t*>(scratch);
-  SmPlanned* const plans = reinterpret_cast<SmPlanned*>(count + kSmRows * kSmCountStep);
-  uint64_t* const recs = reinterpret_cast<uint64_t*>(plans + p.rows);
+  uint64_t* const recs = static_cast<uint64_t*>(scratch);
+  SmPlanned* const plans = reinterpret_cast<SmPlanned*>(recs + p.rows * p.parts * (p.rec / 8));
   const bool cuts = a.top_k || a.top_p || a.min_p;           // (without: nothing for the second kernel)
   for (int64_t r0 = 0; r0 < a0.m; r0 += p.rows) {
     a.m = a0.m - r0 < p.rows ? a0.m - r0 : p.rows;
-    const dim3 grid((unsigned)(a.m * p.parts));
-    if (p.wide && bf) sm_go<true, 1024>(grid, s, a, p.parts, count, plans, recs, cuts);
-    else if (p.wide) sm_go<false, 1024>(grid, s, a, p.parts, count, plans, recs, cuts);
-    else if (bf) sm_go<true, 256>(grid, s, a, p.parts, count, plans, recs, cuts);
-    else sm_go<false, 256>(grid, s, a, p.parts, count, plans, recs, cuts);
+    if (p.wide && bf) sm_go<true, 1024>(s, a, p.parts, plans, recs, cuts);
+    else if (p.wide) sm_go<false, 1024>(s, a, p.parts, plans, recs, cuts);
+    else if (bf) sm_go<true, 256>(s, a, p.parts, plans, recs, cuts);
+    else sm_go<false, 256>(s, a, p.parts, plans, recs, cuts);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     a.y = static_cast<const uint8_t*>(a.y) + p.rows * a.ldy * (bf ? 2 : 4);

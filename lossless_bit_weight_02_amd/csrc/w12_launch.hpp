@@ -188,7 +188,7 @@ uint64_t attention_scratch(const DevInfo& di, int64_t m, int64_t hq, const KvArg
 bool attention_fits(const DevInfo& di, int64_t m, int64_t hq, const KvArgs& kv, const BatchArgs& b);
 hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t hq, const KvArgs& kv,
                             const BatchArgs& b, float scale, uint16_t* y, void* scratch, hipStream_t s);
-// a token per row of logits (w12_sample); scratch: sample_scratch bytes, the first *zero of them counters
+// a token per row of logits (w12_sample); scratch: sample_scratch bytes
 struct SampleArgs {
   const void* y;
   int64_t m, n, ldy;
@@ -199,7 +199,7 @@ struct SampleArgs {
   float* logp;
   int32_t* kept;
 };
-uint64_t sample_scratch(const DevInfo& di, int64_t m, int64_t n, bool bf, uint64_t* zero);
+uint64_t sample_scratch(int64_t m, int64_t n);
 hipError_t launch_sample(const SampleArgs& a, bool bf, void* scratch, hipStream_t s);
 // dense bf16 [n][k] -> tiled storage order (baseline layout)
 hipError_t launch_bf16_tile(const uint16_t* w, int64_t n, int64_t k, uint16_t* out, hipStream_t s);

@@ -139,7 +139,7 @@ EXPORTS = {
                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32,
                                      ctypes.c_void_p]),
     "w12_sample_scratch": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_uint32,
-                                          ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)]),
+                                          ctypes.POINTER(ctypes.c_uint64)]),
     "w12_sample": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                   ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                   ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
@@ -886,20 +886,14 @@ def kv_append(qkv, kv: KVCache, batch: KVBatch, rope: torch.Tensor | None = None
 _step_buffers: dict = {}   # (operator, device, stream) -> scratch of the stream's calls
 
 
-def _step_scratch(what, need, zero, device, stream):
+def _step_scratch(what, need, device, stream):
     """Scratch of an attention or sample call on `stream`, kept for the stream's next one until
-    release_workspace; a call under graph capture gets its own, its counters cleared by the graph, since
-    graphs may be replayed on any stream."""
+    release_workspace; a call under graph capture gets its own, since graphs may be replayed on any stream."""
     if torch.cuda.is_current_stream_capturing():
-        buf = torch.empty(need, dtype=torch.uint8, device=device)
-        if zero:
-            buf[:zero].zero_()
-        return buf
+        return torch.empty(need, dtype=torch.uint8, device=device)
     buf = _step_buffers.get((what, device.index, stream))
     if buf is None or buf.numel() < need:
         buf = torch.empty(max(need, 1 << 18), dtype=torch.uint8, device=device)
-        if zero:
-            buf[:zero].zero_()
         _step_buffers[(what, device.index, stream)] = buf
     return buf
 
@@ -935,7 +929,7 @@ def attention(q: torch.Tensor, kv: KVCache, batch: KVBatch, scale: float | None 
             n = ctypes.c_uint64(0)
             _check(L.w12_attention_scratch(m, hq, kv._ref, batch._ref, ctypes.byref(n)))
             need = batch._sizes[key] = n.value
-        buf = _step_scratch("attention", need, 0, dev, stream)
+        buf = _step_scratch("attention", need, dev, stream)
         _check(L.w12_attention(qp, ldq, m, hq, kv._ref, batch._ref, dim ** -0.5 if scale is None else float(scale),
                                out.data_ptr(), buf.data_ptr(), need, 0, stream))
     return out
@@ -948,7 +942,7 @@ class Samples(NamedTuple):
     kept: torch.Tensor
 
 
-_sample_sizes: dict = {}   # (device, m, n, flags) -> (bytes, counter bytes)
+_sample_sizes: dict = {}   # (m, n, flags) -> bytes of scratch
 
 
 def sample(y: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = None,
@@ -989,19 +983,17 @@ def sample(y: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = 
     L = lib()
     with _on_device(dev):
         stream = _stream_handle(dev)
-        key = (dev.index, m, n, flags)
-        size = _sample_sizes.get(key)
-        if size is None:
-            nb, z = ctypes.c_uint64(0), ctypes.c_uint64(0)
-            _check(L.w12_sample_scratch(m, n, flags, ctypes.byref(nb), ctypes.byref(z)))
+        need = _sample_sizes.get((m, n, flags))
+        if need is None:
+            nb = ctypes.c_uint64(0)
+            _check(L.w12_sample_scratch(m, n, flags, ctypes.byref(nb)))
             if len(_sample_sizes) > 4096:
                 _sample_sizes.clear()
-            size = _sample_sizes[key] = (nb.value, z.value)
-        need, zero = size
-        buf = _step_scratch("sample", need, zero, dev, stream) if need else None
+            need = _sample_sizes[m, n, flags] = nb.value
+        buf = _step_scratch("sample", need, dev, stream)
         _check(L.w12_sample(y.data_ptr(), m, n, y.stride(0) if m > 1 else n, _ptr(temperature), _ptr(top_k),
                             _ptr(top_p), _ptr(min_p), u.data_ptr(), r.token.data_ptr(), r.logp.data_ptr(),
-                            r.kept.data_ptr(), _ptr(buf), need, flags, stream))
+                            r.kept.data_ptr(), buf.data_ptr(), need, flags, stream))
     return r
 
 

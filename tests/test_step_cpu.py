@@ -92,9 +92,8 @@ def test_null_structs_refused():
     b = ctypes.byref
     assert L.w12_attention(0x1000, 512, 3, 4, None, b(_batch()), 0.1, 0x1000, None, 0, 0, None) == w12.W12_ERR_ARG
     assert L.w12_attention(0x1000, 512, 3, 4, b(_kv()), None, 0.1, 0x1000, None, 0, 0, None) == w12.W12_ERR_ARG
-    n = ctypes.c_uint64(0)
     assert L.w12_attention_scratch(3, 4, b(_kv()), b(_batch()), None) == w12.W12_ERR_ARG
-    assert L.w12_sample_scratch(3, 4, 0, b(n), None) == w12.W12_ERR_ARG
+    assert L.w12_sample_scratch(3, 4, 0, None) == w12.W12_ERR_ARG
 
 
 @pytest.mark.parametrize("want,over", [
