@@ -27,7 +27,8 @@
 
 namespace w12 {
 
-constexpr int kSmElems = 16;                      // logits of a thread
+constexpr int kSmElems = 16;                      // logits of a part's thread
+constexpr int kSmJoin = 1024;                     // threads of a row's join
 constexpr int kSmBins = 512;
 constexpr float kSmPerOctave = 16.0f;             // bins of a power of two of w
 constexpr double kSmPerUnit = 16.0;               // of a logit's 1.0 at most with top-k, whose last one may have any w
@@ -37,9 +38,6 @@ constexpr int kSmAll = 2100000000;                // a cut's bin below every log
 constexpr int kSmRows = 4096;                     // rows of a launch
 constexpr uint32_t kSmMasked = 0x007FFFFFu;       // the order of -Inf
 constexpr double kSmFine = 4398046511104.0;       // 2^42: masses as integers, 2^20 logits of at most 1
-
-typedef uint32_t sm_u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint32_t sm_u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 
 template <int T>
 struct SmShape {
@@ -67,32 +65,31 @@ __device__ __forceinline__ uint64_t sm_load(Rsrc rec, int i) {
 }
 __device__ __forceinline__ uint32_t sm_load32(Rsrc rec, int i) { return __builtin_amdgcn_raw_buffer_load_b32(rec, 4 * i, 0, 0); }
 
-// 16 logits of a thread: V loads of 16 bytes, the workgroup's threads side by side in each.  Columns from n on are -Inf.
-template <bool BF, int T>
+// E logits of each of T threads: loads of 16 bytes (8 for 4 of bfloat16), the threads side by side in each.
+// Columns from n on are -Inf.
+template <bool BF, int T, int E>
 struct SmLoad {
-  static constexpr int kPer = BF ? 8 : 4, kLoads = kSmElems / kPer;
+  static constexpr int kPer = BF && E >= 8 ? 8 : 4, kLoads = E / kPer, kWords = BF ? kPer / 2 : kPer;
+  typedef uint32_t words __attribute__((ext_vector_type(kWords), aligned(BF ? 2 : 4)));
   static __device__ __forceinline__ int column(int e, int tid) { return (e / kPer * T + tid) * kPer + e % kPer; }
-  static __device__ __forceinline__ void load(const uint8_t* row, int64_t c0, int64_t n, int tid, float (&x)[kSmElems]) {
-    if (c0 + T * kSmElems <= n) {
+  static __device__ __forceinline__ void load(const uint8_t* row, int64_t c0, int64_t n, int tid, float (&x)[E]) {
+    if (c0 + T * E <= n) {
 #pragma unroll
       for (int v = 0; v < kLoads; ++v) {
-        const uint8_t* const at = row + (c0 + (int64_t)(v * T + tid) * kPer) * (BF ? 2 : 4);
-        if constexpr (BF) {
-          const sm_u32x4_a2 w = *reinterpret_cast<const sm_u32x4_a2*>(at);
+        const words w = *reinterpret_cast<const words*>(row + (c0 + (int64_t)(v * T + tid) * kPer) * (BF ? 2 : 4));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[8 * v + 2 * i] = __uint_as_float(w[i] << 16);
-            x[8 * v + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int i = 0; i < kWords; ++i) {
+          if constexpr (BF) {
+            x[kPer * v + 2 * i] = __uint_as_float(w[i] << 16);
+            x[kPer * v + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+          } else {
+            x[kPer * v + i] = __uint_as_float(w[i]);
           }
-        } else {
-          const sm_u32x4_a4 w = *reinterpret_cast<const sm_u32x4_a4*>(at);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[4 * v + i] = __uint_as_float(w[i]);
         }
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < kSmElems; ++e) {
+      for (int e = 0; e < E; ++e) {
         const int64_t c = c0 + column(e, tid);
         x[e] = -INFINITY;
         if (c < n) x[e] = BF ? bf16_to_float(reinterpret_cast<const uint16_t*>(row)[c]) : reinterpret_cast<const float*>(row)[c];
@@ -148,45 +145,52 @@ struct SmRow {
   }
 };
 
-// Sums over the workgroup's threads.
-template <int T, class V>
-__device__ __forceinline__ V sm_scan(V v, V* s_w, V* before) {   // *before: of the threads ahead
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  V in = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const V up = __shfl_up(in, o);
-    if (lane >= o) in += up;
-  }
-  const V ahead = __shfl_up(in, 1);
-  __syncthreads();
-  if (lane == 63) s_w[w] = in;
-  __syncthreads();
-  V tot = 0, pre = 0;
-#pragma unroll
-  for (int i = 0; i < T / 64; ++i) {
-    if (i == w) pre = tot;
-    tot += s_w[i];
-  }
-  *before = lane > 0 ? pre + ahead : pre;
-  return tot;
+// Inclusive sum over the wave's lanes up to each, of 64-bit values by DPP like lane_scan.
+template <int CTRL, int ROWS, class V>
+__device__ __forceinline__ V sm_lanes(V v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xF, false);
+  return v + __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
 }
-// N such sums at once, one wait for all.
-template <int T, int N>
-__device__ __forceinline__ void sm_scans(const unsigned long long (&v)[N], unsigned long long (*s_w)[4],
-                                         unsigned long long (&before)[N], unsigned long long (&tot)[N]) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  unsigned long long in[N];
-#pragma unroll
-  for (int z = 0; z < N; ++z) in[z] = v[z];
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-#pragma unroll
-    for (int z = 0; z < N; ++z) {
-      const unsigned long long up = __shfl_up(in[z], o);
-      if (lane >= o) in[z] += up;
-    }
+template <class V>
+__device__ __forceinline__ V sm_lane_scan(V v) {
+  if constexpr (sizeof(V) == 4) {
+    return (V)lane_scan((int)v);
+  } else {
+    v = sm_lanes<0x111, 0xF>(v);
+    v = sm_lanes<0x112, 0xF>(v);
+    v = sm_lanes<0x114, 0xF>(v);
+    v = sm_lanes<0x118, 0xF>(v);
+    v = sm_lanes<0x142, 0xA>(v);
+    return sm_lanes<0x143, 0xC>(v);
   }
+}
+template <class V>
+__device__ __forceinline__ V sm_last_lane(V v) {
+  if constexpr (sizeof(V) == 4) {
+    return (V)__builtin_amdgcn_readlane((int)v, 63);
+  } else {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63);
+    return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+  }
+}
+
+// The lane ahead's value, 0 in the first.
+template <class V>
+__device__ __forceinline__ V sm_ahead(V v) {
+  const V up = __shfl_up(v, 1);
+  return (threadIdx.x & 63) != 0 ? up : V(0);
+}
+
+// Sums over the workgroup's threads, in a fixed order.  N at once, one wait for all.
+template <int T, int N, class V>
+__device__ __forceinline__ void sm_scans(const V (&v)[N], V (*s_w)[N], V (&before)[N], V (&tot)[N]) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  V in[N];
+#pragma unroll
+  for (int z = 0; z < N; ++z) in[z] = sm_lane_scan(v[z]);
   __syncthreads();
   if (lane == 63) {
 #pragma unroll
@@ -195,20 +199,27 @@ __device__ __forceinline__ void sm_scans(const unsigned long long (&v)[N], unsig
   __syncthreads();
 #pragma unroll
   for (int z = 0; z < N; ++z) {
-    unsigned long long pre = 0;
+    V pre = 0;
     tot[z] = 0;
 #pragma unroll
     for (int i = 0; i < T / 64; ++i) {
       if (i == w) pre = tot[z];
       tot[z] += s_w[i][z];
     }
-    before[z] = pre + in[z] - v[z];
+    before[z] = pre + sm_ahead(in[z]);             // (not a difference, which a double would round)
   }
 }
 template <int T, class V>
+__device__ __forceinline__ V sm_scan(V v, V* s_w, V* before) {   // *before: of the threads ahead
+  const V vs[1] = {v};
+  V b[1], t[1];
+  sm_scans<T, 1>(vs, reinterpret_cast<V(*)[1]>(s_w), b, t);
+  *before = b[0];
+  return t[0];
+}
+template <int T, class V>
 __device__ __forceinline__ V sm_sum(V v, V* s_w) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  v = sm_last_lane(sm_lane_scan(v));
   __syncthreads();
   if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -235,11 +246,8 @@ struct SmPlanned {
 };
 
 // A row.
-template <bool BF, int T>
+template <bool BF>
 struct SmOf {
-  using S = SmShape<T>;
-  using L = SmLoad<BF, T>;
-
   const SampleArgs& a;
   const int tid;
   const int64_t row;
@@ -264,10 +272,10 @@ struct SmOf {
 
 // The parts' kernels.
 template <bool BF, int T>
-struct SmPart : SmOf<BF, T> {
+struct SmPart : SmOf<BF> {
   using S = SmShape<T>;
-  using L = SmLoad<BF, T>;
-  using Of = SmOf<BF, T>;
+  using L = SmLoad<BF, T, kSmElems>;
+  using Of = SmOf<BF>;
   using Of::a, Of::tid, Of::y, Of::temp, Of::r, Of::weight, Of::fine, Of::passes;
 
   struct Shared {
@@ -428,11 +436,13 @@ struct SmPart : SmOf<BF, T> {
 };
 
 // The rows' kernels: a workgroup a row.
-template <bool BF, int T>
-struct SmJoin : SmOf<BF, T> {
-  using S = SmShape<T>;
-  using L = SmLoad<BF, T>;
-  using Of = SmOf<BF, T>;
+template <bool BF, int P>
+struct SmJoin : SmOf<BF> {
+  static constexpr int T = kSmJoin;
+  using S = SmShape<P>;
+  static constexpr int kElems = S::kPart / T;
+  using L = SmLoad<BF, T, kElems>;
+  using Of = SmOf<BF>;
   using Of::a, Of::tid, Of::row, Of::y, Of::parts, Of::r, Of::M, Of::top, Of::weight, Of::fine, Of::passes;
 
   struct Shared {
@@ -442,11 +452,15 @@ struct SmJoin : SmOf<BF, T> {
         unsigned long long cand[kSmSort];          // order, column; in column order
       };
       unsigned long long all[2 * kSmSort];         // the cut's bin: order, then the column's complement
+      struct {
+        double ms[kSmJoin - kSmBins];
+        int cnt[kSmJoin - kSmBins];
+      };
     };
     unsigned long long mass8[256];
     uint32_t cnt8[256];
     double wd[T / 64];
-    unsigned long long wu[T / 64], wv[T / 64][4];
+    unsigned long long wu[T / 64], wv[T / 64][L::kLoads];
     float wf[T / 64];
     // the parts
     double scale[kSmParts];
@@ -454,6 +468,7 @@ struct SmJoin : SmOf<BF, T> {
     uint32_t ties[kSmParts];
     int shift[kSmParts], list[kSmParts];
     int found;
+    int place[256];
     int at[2];
     double val;
   };
@@ -494,22 +509,16 @@ struct SmJoin : SmOf<BF, T> {
     // (a lane a part, every wave alike)
     const int lane = tid & 63;
     const unsigned long long own = lane < parts ? s.mass[lane] : 0;
-    unsigned long long upto = own;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const unsigned long long up = __shfl_up(upto, o);
-      if (lane >= o) upto += up;
-    }
-    const unsigned long long sum = __shfl(upto, 63);
+    const unsigned long long upto = sm_lane_scan(own), sum = sm_last_lane(upto);
     const float u = a.u[row];
     unsigned long long want = u > 0.0f ? u < 1.0f ? (unsigned long long)((double)u * (double)sum) : sum - 1 : 0;
     if (want >= sum) want = sum - 1;
     const int p = __popcll(__ballot(lane < parts - 1 && upto <= want));
     const unsigned long long left = want - __shfl(upto - own, p);
     const int64_t c0 = (int64_t)p * S::kPart;
-    float x[kSmElems];
+    float x[kElems];
     L::load(y, c0, a.n, tid, x);
-    unsigned long long m[kSmElems], mine[L::kLoads], before[L::kLoads], tot[L::kLoads];
+    unsigned long long m[kElems], mine[L::kLoads], before[L::kLoads], tot[L::kLoads];
     uint32_t in = 0;
     if (tid == 0) s.found = -1;
 #pragma unroll
@@ -546,12 +555,12 @@ struct SmJoin : SmOf<BF, T> {
     __syncthreads();
     if (s.found < 0) {
 #pragma unroll
-      for (int e = 0; e < kSmElems; ++e)
+      for (int e = 0; e < kElems; ++e)
         if (in >> e & 1u) atomicMax(&s.found, (int)(c0 + L::column(e, tid)));
       __syncthreads();
       const int f = s.found;
 #pragma unroll
-      for (int e = 0; e < kSmElems; ++e)
+      for (int e = 0; e < kElems; ++e)
         if ((int)(c0 + L::column(e, tid)) == f) s.val = ((double)x[e] - M) * r.c;
       __syncthreads();
     }
@@ -563,10 +572,10 @@ struct SmJoin : SmOf<BF, T> {
   __device__ __forceinline__ void each(const F& f, const G& end) {
     for (int p = 0; p < parts; ++p) {
       const int64_t c0 = (int64_t)p * S::kPart;
-      float x[kSmElems];
+      float x[kElems];
       L::load(y, c0, a.n, tid, x);
 #pragma unroll
-      for (int e = 0; e < kSmElems; ++e)
+      for (int e = 0; e < kElems; ++e)
         if (x[e] > -INFINITY) f(x[e], sm_order(x[e]), (uint32_t)(c0 + L::column(e, tid)));
       end(p);
     }
@@ -642,7 +651,7 @@ struct SmJoin : SmOf<BF, T> {
     int p = 0;
     while (p < parts - 1 && seen + s.ties[p] < need) seen += s.ties[p++];
     const int64_t c0 = (int64_t)p * S::kPart;
-    float x[kSmElems];
+    float x[kElems];
     L::load(y, c0, a.n, tid, x);
     if (tid == 0) s.found = 0;
 #pragma unroll
@@ -731,79 +740,63 @@ struct SmJoin : SmOf<BF, T> {
       s.list[tid] = lists_n;
       s.mass[tid] = fine(W);
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) W += __shfl_xor(W, o);
+    W = sm_last_lane(sm_lane_scan(W));
     __syncthreads();
     if (!cuts) {
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) lives += __shfl_xor(lives, o);
-      draw({kSmMasked + 1, 0xFFFFFFFFu}, lives);
+      draw({kSmMasked + 1, 0xFFFFFFFFu}, sm_last_lane(lane_scan(lives)));
       return;
     }
 
     // the row's histogram (with top-k of counts, else of masses), a run of bins a thread, and how far down what
     // is kept can reach
     const bool counted = r.k < a.n;
-    constexpr int kBpt = S::kBpt;
-    int cnt[kBpt];
-    double ms[kBpt];
-    int cs = 0;
-    double md = 0.0;
-#pragma unroll
-    for (int i = 0; i < kBpt; ++i) {
-      cnt[i] = 0;
-      ms[i] = 0.0;
-    }
-    constexpr int kAhead = 16;                     // parts in flight
-    for (int p0 = 0; p0 < parts; p0 += kAhead) {
-      uint32_t v[kAhead][kBpt];
+    constexpr int kGroups = T / kSmBins, kAhead = 16;    // groups of parts, a group's parts in flight
+    const int mine = tid % kSmBins, group = tid / kSmBins;
+    int cnt = 0;
+    double ms = 0.0;
+    for (int p0 = group; p0 < parts; p0 += kAhead * kGroups) {
+      uint32_t v[kAhead];
 #pragma unroll
       for (int z = 0; z < kAhead; ++z) {
-        const int p = p0 + z < parts ? p0 + z : parts - 1;
-        const int h = (p * S::kRec + S::kHead + S::kList) * 2, sh = s.shift[p];
-#pragma unroll
-        for (int i = 0; i < kBpt; ++i) {
-          // (the last bin takes what lies below in its part, too)
-          const int b = tid * kBpt + i - sh;
-          v[z][i] = sm_load32(recs, p0 + z < parts && tid * kBpt + i < kSmBins - 1 && b >= 0 ? h + b : S::kNone);
-        }
+        // (the last bin takes what lies below in its part, too)
+        const int p = p0 + z * kGroups, b = mine - s.shift[p < parts ? p : 0];
+        v[z] = sm_load32(recs, p < parts && mine < kSmBins - 1 && b >= 0 ? (p * S::kRec + S::kHead + S::kList) * 2 + b : S::kNone);
       }
 #pragma unroll
       for (int z = 0; z < kAhead; ++z) {
-        const double sc = s.scale[p0 + z < parts ? p0 + z : parts - 1];
-#pragma unroll
-        for (int i = 0; i < kBpt; ++i) {
-          if (counted) cnt[i] += (int)v[z][i];
-          else ms[i] += sc * (double)__uint_as_float(v[z][i]);
-        }
+        const int p = p0 + z * kGroups;
+        if (counted) cnt += (int)v[z];
+        else ms += s.scale[p < parts ? p : 0] * (double)__uint_as_float(v[z]);
       }
     }
+    if (group > 0) {
+      s.cnt[tid - kSmBins] = cnt;
+      s.ms[tid - kSmBins] = ms;
+    }
+    __syncthreads();
+    if (group == 0) {
 #pragma unroll
-    for (int i = 0; i < kBpt; ++i) {
-      cs += cnt[i];
-      md += ms[i];
+      for (int g = 0; g < kGroups - 1; ++g) {
+        cnt += s.cnt[g * kSmBins + mine];
+        ms += s.ms[g * kSmBins + mine];
+      }
+    } else {
+      cnt = 0;
+      ms = 0.0;
     }
     int bin = kSmBins - 1;
     if (tid == 0) s.at[0] = kSmBins - 1;
     if (counted) {
       int c;
-      sm_scan<T>(cs, reinterpret_cast<int*>(s.wf), &c);
-#pragma unroll
-      for (int i = 0; i < kBpt; ++i) {
-        if (c < r.k && c + cnt[i] >= r.k && tid * kBpt + i < kSmBins - 1) s.at[0] = tid * kBpt + i;
-        c += cnt[i];
-      }
+      sm_scan<T>(cnt, reinterpret_cast<int*>(s.wf), &c);
+      if (c < r.k && c + cnt >= r.k && mine < kSmBins - 1) s.at[0] = mine;
       __syncthreads();
       bin = s.at[0];
     } else if (r.p < 1.0) {
       double m;
-      sm_scan<T>(md, s.wd, &m);
+      sm_scan<T>(ms, s.wd, &m);
       const double want = r.p * W;
-#pragma unroll
-      for (int i = 0; i < kBpt; ++i) {
-        if (m < want && m + ms[i] >= want && tid * kBpt + i < kSmBins - 1) s.at[0] = tid * kBpt + i;
-        m += ms[i];
-      }
+      if (m < want && m + ms >= want && mine < kSmBins - 1) s.at[0] = mine;
       __syncthreads();
       bin = want > 0.0 ? s.at[0] : 0;
     }
@@ -853,20 +846,11 @@ struct SmJoin : SmOf<BF, T> {
       kept = (int)(c >> 32);
       mine_n = (int)sm_load(recs, at + 3);
     }
-    int upto_n = mine_n;
     const bool fits = __ballot(mine_n > S::kCutList) == 0;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      above += __shfl_xor(above, o);
-      count += __shfl_xor(count, o);
-      kept += __shfl_xor(kept, o);
-    }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(upto_n, o);
-      if (lane >= o) upto_n += up;
-    }
-    const int n = __shfl(upto_n, 63);
+    above = sm_last_lane(sm_lane_scan(above));
+    count = sm_last_lane(lane_scan(count));
+    kept = sm_last_lane(lane_scan(kept));
+    const int upto_n = lane_scan(mine_n), n = sm_last_lane(upto_n);
     if (!fits || n > 2 * kSmSort) {
       whole_row();
       return;
@@ -986,8 +970,11 @@ struct SmJoin : SmOf<BF, T> {
       in |= (v[q] != 0) & ((need >= kSmBins - 1) | (big - r.bin(sm_value((uint32_t)(v[q] >> 32))) <= need)) ? 1u << q : 0u;
       all += v[q] != 0 ? 1 : 0;
     }
-    const int n = sm_scan<T>((int)__popc(in), reinterpret_cast<int*>(s.wf), &at0);
-    all = sm_sum<T>(all, reinterpret_cast<int*>(s.wf));
+    // (both sums in one: at most 2^14 of each)
+    const int sums = sm_scan<T>((int)__popc(in) | all << 16, reinterpret_cast<int*>(s.wf), &at0);
+    const int n = sums & 0xFFFF;
+    at0 &= 0xFFFF;
+    all = sums >> 16;
     if (n > kSmSort) return false;
 #pragma unroll
     for (int q = 0; q < kMost; ++q)
@@ -995,11 +982,27 @@ struct SmJoin : SmOf<BF, T> {
         s.cand[at0] = v[q];
         s.sorting[at0++] = v[q] ^ 0xFFFFFFFFu;
       }
-    int size = 64;
-    while (size < n) size <<= 1;
-    for (int i = n + tid; i < size; i += T) s.sorting[i] = 0;
     __syncthreads();
-    sort(size);
+    constexpr int kFew = 256;
+    if (n <= kFew) {
+      // a logit's place is the number of those ahead of it, counted by T / kFew threads
+      const int i = tid % kFew;
+      const unsigned long long own = s.sorting[i < n ? i : 0];
+      int place = 0;
+      for (int j = tid / kFew; j < n; j += T / kFew) place += s.sorting[j] > own ? 1 : 0;
+      if (tid < kFew) s.place[i] = place;
+      __syncthreads();
+      if (tid >= kFew && i < n) atomicAdd(&s.place[i], place);
+      __syncthreads();
+      if (tid < n) s.sorting[s.place[i]] = own;
+      __syncthreads();
+    } else {
+      int size = 64;
+      while (size < n) size <<= 1;
+      for (int i = n + tid; i < size; i += T) s.sorting[i] = 0;
+      __syncthreads();
+      sort(size);
+    }
     // masses in the tokens' order, a run of them a thread
     constexpr int kMine = kSmSort / T;
     const int own_n = (n + T - 1) / T, r0 = tid * own_n, kk = r.k < n ? (int)r.k : n;
@@ -1076,7 +1079,7 @@ __global__ __launch_bounds__(T, 6) void k_sample(SampleArgs a, int parts, uint64
   k.part((int)(blockIdx.x - row * parts), recs + (int64_t)blockIdx.x * SmShape<T>::kRec);
 }
 template <bool BF, int T>
-__global__ __launch_bounds__(T) void k_sample_join(SampleArgs a, int parts, SmPlanned* plans, const uint64_t* recs) {
+__global__ __launch_bounds__(kSmJoin) void k_sample_join(SampleArgs a, int parts, SmPlanned* plans, const uint64_t* recs) {
   __shared__ typename SmJoin<BF, T>::Shared s;
   const int64_t row = blockIdx.x;
   SmJoin<BF, T> k(a, row, parts, s);
@@ -1093,7 +1096,7 @@ __global__ __launch_bounds__(T, 6) void k_sample_cut(SampleArgs a, int parts, co
   k.cut_part((int)(blockIdx.x - row * parts), plan, recs + (int64_t)blockIdx.x * SmShape<T>::kRec);
 }
 template <bool BF, int T>
-__global__ __launch_bounds__(T) void k_sample_cut_join(SampleArgs a, int parts, const SmPlanned* plans, const uint64_t* recs) {
+__global__ __launch_bounds__(kSmJoin) void k_sample_cut_join(SampleArgs a, int parts, const SmPlanned* plans, const uint64_t* recs) {
   __shared__ typename SmJoin<BF, T>::Shared s;
   const int64_t row = blockIdx.x;
   const SmPlanned plan = plans[row];
@@ -1133,10 +1136,10 @@ template <bool BF, int T>
 static void sm_go(hipStream_t s, const SampleArgs& a, int parts, SmPlanned* plans, uint64_t* recs, bool cuts) {
   const dim3 rows((unsigned)a.m), all((unsigned)(a.m * parts));
   hipLaunchKernelGGL((k_sample<BF, T>), all, dim3(T), 0, s, a, parts, recs);
-  hipLaunchKernelGGL((k_sample_join<BF, T>), rows, dim3(T), 0, s, a, parts, plans, recs);
+  hipLaunchKernelGGL((k_sample_join<BF, T>), rows, dim3(kSmJoin), 0, s, a, parts, plans, recs);
   if (!cuts) return;
   hipLaunchKernelGGL((k_sample_cut<BF, T>), all, dim3(T), 0, s, a, parts, plans, recs);
-  hipLaunchKernelGGL((k_sample_cut_join<BF, T>), rows, dim3(T), 0, s, a, parts, plans, recs);
+  hipLaunchKernelGGL((k_sample_cut_join<BF, T>), rows, dim3(kSmJoin), 0, s, a, parts, plans, recs);
 }
 
 hipError_t launch_sample(const SampleArgs& a0, bool bf, void* scratch, hipStream_t s) {
