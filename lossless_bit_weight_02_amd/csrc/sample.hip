@@ -98,21 +98,26 @@ struct SmLoad {
   }
 };
 
+// (a constant in scalar registers: in vector ones a multiply-add takes two moves first)
+__device__ __forceinline__ double sm_scalar(double c) {
+  asm("" : "+s"(c));
+  return c;
+}
 // 2^t for t <= 0 (below 2^-1000: 0)
 __device__ __forceinline__ double sm_exp2(double t) {
   t = t > -1000.0 ? t : -1000.0;
   const double n = __builtin_rint(t);
   const double f = (t - n) * 0.693147180559945309417;
   double p = 1.0 / 479001600.0;
-  p = __builtin_fma(p, f, 1.0 / 39916800.0);
-  p = __builtin_fma(p, f, 1.0 / 3628800.0);
-  p = __builtin_fma(p, f, 1.0 / 362880.0);
-  p = __builtin_fma(p, f, 1.0 / 40320.0);
-  p = __builtin_fma(p, f, 1.0 / 5040.0);
-  p = __builtin_fma(p, f, 1.0 / 720.0);
-  p = __builtin_fma(p, f, 1.0 / 120.0);
-  p = __builtin_fma(p, f, 1.0 / 24.0);
-  p = __builtin_fma(p, f, 1.0 / 6.0);
+  p = __builtin_fma(p, f, sm_scalar(1.0 / 39916800.0));
+  p = __builtin_fma(p, f, sm_scalar(1.0 / 3628800.0));
+  p = __builtin_fma(p, f, sm_scalar(1.0 / 362880.0));
+  p = __builtin_fma(p, f, sm_scalar(1.0 / 40320.0));
+  p = __builtin_fma(p, f, sm_scalar(1.0 / 5040.0));
+  p = __builtin_fma(p, f, sm_scalar(1.0 / 720.0));
+  p = __builtin_fma(p, f, sm_scalar(1.0 / 120.0));
+  p = __builtin_fma(p, f, sm_scalar(1.0 / 24.0));
+  p = __builtin_fma(p, f, sm_scalar(1.0 / 6.0));
   p = __builtin_fma(p, f, 0.5);
   p = __builtin_fma(p, f, 1.0);
   p = __builtin_fma(p, f, 1.0);
