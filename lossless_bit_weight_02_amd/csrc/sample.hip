@@ -42,7 +42,11 @@ constexpr double kSmFine = 4398046511104.0;       // 2^42: masses as integers, 2
 template <int T>
 struct SmShape {
   static constexpr int kPart = T * kSmElems;
-  static constexpr int kList = T / 4;              // entries of a part's list
+  // Entries of a part's list: all are read by the row's join, and where a row's do not reach down to its cut the
+  // second pair of kernels runs.  Of 8 parts lists of 128 take 34 us, of 64 48 (33 rows of 32001); of 38
+  // parts 131 and 122 us (256 rows of 152064).
+  static constexpr int kList = T == 256 ? 128 : 256;
+  static __device__ __forceinline__ int list_bits(int parts) { return (T == 256 ? 7 : 8) - (parts > 16 ? 1 : 0); }
   static constexpr int kHead = 4;                  // a part's record, in 64-bit words
   static constexpr int kCutList = 512;             // entries of the cut's list, which takes the place of both
   static constexpr int kRec = kHead + kCutList;
@@ -373,7 +377,7 @@ struct SmPart : SmOf<BF> {
 #pragma unroll
       for (int i = 0; i < S::kBpt; ++i) {
         before += own[i];
-        fit += tid * S::kBpt + i < kSmBins && before <= S::kList ? 1 : 0;
+        fit += tid * S::kBpt + i < kSmBins && before <= 1 << S::list_bits(this->parts) ? 1 : 0;
       }
       bound = sm_sum<T>(fit, reinterpret_cast<int*>(s.wf)) - 1;
       // (the counts of a load's logits, 16 bits each, in one sum)
@@ -959,12 +963,13 @@ struct SmJoin : SmOf<BF> {
   // Cuts and draws from the lists' logits down to bin `need`; false if they turn out not to reach the cut.
   __device__ __forceinline__ bool from_lists(Rsrc recs, int need, bool by_min, bool partly, int big, double W) {
     // a run of the lists' slots a thread, so that one sum gives their places
-    constexpr int kMost = kSmParts * S::kList / T;
-    const int slots = parts * S::kList, run = (slots + T - 1) / T;
+    constexpr int kMost = kSmParts * S::kList / 2 / T;
+    static_assert(16 * S::kList <= kMost * T);
+    const int bits = S::list_bits(parts), slots = parts << bits, run = (slots + T - 1) / T;
     uint64_t v[kMost];
 #pragma unroll
     for (int q = 0; q < kMost; ++q) {
-      const int i = tid * run + q, p = i / S::kList, e = i % S::kList;
+      const int i = tid * run + q, p = i >> bits, e = i & ((1 << bits) - 1);
       const bool is = q < run && i < slots && e < s.list[i < slots ? p : 0];
       v[q] = sm_load(recs, is ? p * S::kRec + S::kHead + e : S::kNone);     // (nothing: 0)
     }
