@@ -10,6 +10,11 @@
 // that does not turn.  A thread takes a unit: every access is 16 bytes or more, the columns of a row that
 // neighbouring lanes hold lie side by side, and one token of 64 heads already spreads over two
 // workgroups.  A workgroup stays in one row, so its place, page and position are looked up once for all.
+//
+// What bounds it: memory for prompts (5 of 1024 .. 4096 tokens of 48 + 2 * 8 heads of 128 columns from float,
+// 595 MB in 108 us, 5.5 TB/s; a plain copy on this card 4.95), the launch for single tokens (the kernel
+// 3.2 us, the call 8.3), the lookups' chain of loads and the division by the scale for drafts (64 sequences
+// of 16 into e4m3, 25 MB in 8.4 us).
 #include "kv_device.hpp"
 
 namespace w12 {

@@ -21,19 +21,28 @@
 // Split.  The work of the whole batch is a line of units of 128 places (of one sequence, key head and
 // block of rows); every workgroup takes an equal run of it, found from the lengths on the device, so
 // uneven batches fill the chip alike and a captured graph follows its lengths.  A workgroup's four
-// waves take 32 of the 128 places each (kWr = 1), or 64 by pairs (2) or all of them (4) for as many blocks
-// of 16 rows more, and join through LDS.  A run that ends inside a sequence leaves
-// a partial (sum, maximum, unnormalised output) in the scratch; whoever counts itself last joins them.
+// waves take 32 of the 128 places each and join through LDS (k_attention: 16 or 32 rows), or its eight waves
+// take 16 rows each and all places (k_attention_rows: up to 128).  A run that ends inside a segment leaves a partial
+// (unnormalised sum, maximum, sum of probabilities) in the scratch, which a second kernel joins.
+//
+// What bounds it: few rows read the cache once, and the loads of keys and values (16 bytes a lane, past the
+// caches: nothing is read twice; 64 sequences of 60 .. 8192 places, 48 heads over 8 of 128 columns, 88 us
+// so, 92 through them) run at 6.4 TB/s in a long sequence (131071 places, 537 MB: 84 us and 10 to join), at 5.4
+// where 64 sequences end unevenly (76 + 12 us), at 6.0 over 256 sequences (1.67 GB: 277 + 10 us).  One
+// sequence of 517 places is a chain of steps, 11 us for 2 MB.  Trees of 16 drafts and 6 heads over an e4m3
+// cache of 256 columns (184 MB) take 78 us and 10 to join, the LDS reads of the shared operands
+// the most of it (without loads 61 us, without products 54).
 #include "kv_device.hpp"
 
 namespace w12 {
 
 constexpr int kAtUnit = 128;                      // places of a unit
-
-
-
-constexpr int kAtPiece = 8;                       // units of a segment worth a workgroup of their own
-constexpr int kAtStart = 2;                       // units that a segment's beginning and end cost
+// Units of a segment worth a workgroup of their own: with 8, one sequence of 517 places takes 11.5 us and 16
+// trees over 1000 .. 16384 places 88, with 4 15.9 and 88, with 16 11.5 and 98.
+constexpr int kAtPiece = 8;
+// Units that a segment's beginning and end cost: with 2, 64 and 256 sequences take 89 and 289 us, with 0
+// 121 and 308, with 4 90 and 299.
+constexpr int kAtStart = 2;
 constexpr float kAtLog2e = 1.44269504088896340736f;
 constexpr float kAtSlack = 8.0f;                  // powers of two a probability may pass 1 by
 constexpr int kAtWideRows = 128, kAtWide = 512;   // rows and threads of k_attention_rows
@@ -954,7 +963,11 @@ __global__ __launch_bounds__(kAtWide, 2) void k_attention_rows(AttnArgs a) {
   if (tid == 0) a.split[blockIdx.x] = split;
 }
 
-// Rows of q a workgroup takes at once, by the average of a sequence.
+// Rows of q a workgroup takes at once, by the average of a sequence (which is all the host knows): 16 up to 16,
+// since 32 hold registers that loads in flight need (64 sequences of one token, 6 rows each: 89 us, with 32
+// 103; of 1 or 2 tokens, 56 and 59); 32 up to 32 where they fit, else 128 (16 sequences of 3000 .. 5000 places and
+// 1 .. 8 tokens, 27 rows on average: 77 us, with 128 83); 128 beyond (54 rows on average: 96, with
+// 32, the sequence read again for each 32, 99).
 struct AttnPlan {
   int rows;               // 16, 32: k_attention, 128: k_attention_rows
   int wgs;

@@ -17,11 +17,17 @@
 //   radix    if even one bin holds too many (thousands of equal logits), or top-p cuts what a top-k of
 //            thousands leaves, one workgroup reads the row, 8 bits of the logits' order a time.
 //
+// What bounds it: the chain of a row's join for few rows (1 row of 152064: 6 us for the parts, 12 for the
+// join, 3 for two kernels that find nothing to do; 21 in all), instructions for many: the parts of 64 rows take
+// 27 us (39 MB; 6 of them the exponentials in double, 2 the lists, the histogram nothing), of 256
+// rows of bfloat16 60 (78 MB).  Those need 73 and 123 us in all: the rest is joins of 256 rows at once (25 us) and
+// the second pair of kernels (20 + 22 us) for rows that keep tens of thousands.
+//
 // A border between two tokens has to fall as it does in the formula: where each border were off by 1e-7, as
 // sums of 152064 floats are, one draw in a hundred from a flat row would be a neighbour's.  So weights
 // that decide are e^(..) in double (their own 2^f by a polynomial: |f ln 2| < 0.35, 12 terms,
 // 1e-14), those below 2^-24 of the maximum in float times an exact power of two (1e-7 of 2^-24), and sums are doubles in a
-// fixed order or integers, the same whichever workgroup is last.  The histogram's masses, which only choose
+// fixed order or integers.  The histogram's masses, which only choose
 // where to look, are floats rounded to 2^-30.
 #include "kv_device.hpp"
 
@@ -993,7 +999,7 @@ struct SmJoin : SmOf<BF> {
         s.sorting[at0++] = v[q] ^ 0xFFFFFFFFu;
       }
     __syncthreads();
-    constexpr int kFew = 256;
+    constexpr int kFew = 256;                      // (1 row with top-k 20: 21 us, by sorting 24)
     if (n <= kFew) {
       // a logit's place is the number of those ahead of it, counted by T / kFew threads
       const int i = tid % kFew;
