@@ -855,7 +855,7 @@ int w12_attention_scratch(int64_t m, int64_t hq, const w12_kv* kv, const w12_kv_
   hipError_t e = w12::dev_info(&di);
   if (e != hipSuccess) return hip_fail(e, "device query");
   if (!w12::attention_fits(di, m, hq, kv_of(kv), batch_of(batch)))
-    return fail(W12_ERR_RANGE, "the batch is too large (m * hq from 2^30, or its rows of 16 x tiles of 128 places from 2^31 on)");
+    return fail(W12_ERR_RANGE, "the batch is too large (m * hq, or its rows of 16 x tiles of 128 places, from 2^30 on)");
   *bytes = w12::attention_scratch(di, m, hq, kv_of(kv), batch_of(batch));
   return ok();
 }
@@ -874,7 +874,7 @@ int w12_attention(const uint16_t* q, int64_t ldq, int64_t m, int64_t hq, const w
   hipError_t e = w12::dev_info(&di);
   if (e != hipSuccess) return hip_fail(e, "device query");
   if (!w12::attention_fits(di, m, hq, kv_of(kv), batch_of(batch)))
-    return fail(W12_ERR_RANGE, "the batch is too large (m * hq from 2^30, or its rows of 16 x tiles of 128 places from 2^31 on)");
+    return fail(W12_ERR_RANGE, "the batch is too large (m * hq, or its rows of 16 x tiles of 128 places, from 2^30 on)");
   const uint64_t need = w12::attention_scratch(di, m, hq, kv_of(kv), batch_of(batch));
   if (need > 0) {
     if (!scratch || scratch_bytes < need)

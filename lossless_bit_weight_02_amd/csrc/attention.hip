@@ -242,16 +242,24 @@ struct UnitLine {
   }
   __device__ __forceinline__ int all(int lane) {
     int sum = 0;
+    int64_t rows_n = 0;
     for (int s = lane; s < a.b.seqs; s += 64) {
       read(s);
       sum += mine();
+      rows_n += count;
     }
-    return lane_get(lane_scan(sum), 63);
+    return apart(rows_n) ? lane_get(lane_scan(sum), 63) : 0;
+  }
+  // whether the sequences' rows can be apart: a q_start that falls may give more of them than there are, and the
+  // line's length and the scratch are made for no more (it is left alone then)
+  __device__ __forceinline__ bool apart(int64_t rows_n) const {
+    return a.b.q_start == nullptr || last_lane(lane_scan(rows_n)) <= a.m;
   }
   // the share of each workgroup; returns the line's length
   __device__ __forceinline__ int start(int lane) {
     if (a.b.seqs <= 64) {
       read(lane);
+      if (!apart(count)) return 0;
       scan();
       if (total <= a.wgs) return total;
       pieces = false;
@@ -978,8 +986,8 @@ static AttnPlan attn_plan(const DevInfo& di, int64_t m, int64_t hq, const KvArgs
   AttnPlan p;
   p.rows = avg <= 16 ? 16 : avg <= 32 && kv.dim <= 128 ? 32 : kAtWideRows;
   const double most = ((double)m * group / p.rows + (double)b.seqs) * (double)kv.heads *
-                      ((double)b.cols * kv.page / kAtUnit + 1.0);
-  p.fits = most < 2147483648.0 && m * hq < (int64_t(1) << 30);
+                      ((double)b.cols * kv.page / kAtUnit + 1.0 + kAtStart);
+  p.fits = most < 1073741824.0 && m * hq < (int64_t(1) << 30);
   p.wgs = di.cus;
   return p;
 }

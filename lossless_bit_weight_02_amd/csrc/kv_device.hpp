@@ -18,6 +18,32 @@ __device__ __forceinline__ int lane_scan(int v) {
   return v;
 }
 
+// The same of 64-bit values.
+template <int CTRL, int ROWS, class V>
+__device__ __forceinline__ V lane_step(V v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xF, false);
+  return v + __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+}
+template <class V>
+__device__ __forceinline__ V lane_scan(V v) {
+  static_assert(sizeof(V) == 8);
+  v = lane_step<0x111, 0xF>(v);
+  v = lane_step<0x112, 0xF>(v);
+  v = lane_step<0x114, 0xF>(v);
+  v = lane_step<0x118, 0xF>(v);
+  v = lane_step<0x142, 0xA>(v);
+  return lane_step<0x143, 0xC>(v);
+}
+__device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
+template <class V>
+__device__ __forceinline__ V last_lane(V v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63);
+  return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+}
+
 // A sequence's rows and lengths.
 struct SeqRows {
   int64_t first;      // its first new token's row

@@ -160,38 +160,6 @@ struct SmRow {
   }
 };
 
-// Inclusive sum over the wave's lanes up to each, of 64-bit values by DPP like lane_scan.
-template <int CTRL, int ROWS, class V>
-__device__ __forceinline__ V sm_lanes(V v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xF, false);
-  return v + __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
-}
-template <class V>
-__device__ __forceinline__ V sm_lane_scan(V v) {
-  if constexpr (sizeof(V) == 4) {
-    return (V)lane_scan((int)v);
-  } else {
-    v = sm_lanes<0x111, 0xF>(v);
-    v = sm_lanes<0x112, 0xF>(v);
-    v = sm_lanes<0x114, 0xF>(v);
-    v = sm_lanes<0x118, 0xF>(v);
-    v = sm_lanes<0x142, 0xA>(v);
-    return sm_lanes<0x143, 0xC>(v);
-  }
-}
-template <class V>
-__device__ __forceinline__ V sm_last_lane(V v) {
-  if constexpr (sizeof(V) == 4) {
-    return (V)__builtin_amdgcn_readlane((int)v, 63);
-  } else {
-    const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63);
-    return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
-  }
-}
-
 // The lane ahead's value, 0 in the first.
 template <class V>
 __device__ __forceinline__ V sm_ahead(V v) {
@@ -205,7 +173,7 @@ __device__ __forceinline__ void sm_scans(const V (&v)[N], V (*s_w)[N], V (&befor
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   V in[N];
 #pragma unroll
-  for (int z = 0; z < N; ++z) in[z] = sm_lane_scan(v[z]);
+  for (int z = 0; z < N; ++z) in[z] = lane_scan(v[z]);
   __syncthreads();
   if (lane == 63) {
 #pragma unroll
@@ -234,7 +202,7 @@ __device__ __forceinline__ V sm_scan(V v, V* s_w, V* before) {   // *before: of 
 }
 template <int T, class V>
 __device__ __forceinline__ V sm_sum(V v, V* s_w) {
-  v = sm_last_lane(sm_lane_scan(v));
+  v = last_lane(lane_scan(v));
   __syncthreads();
   if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -524,7 +492,7 @@ struct SmJoin : SmOf<BF> {
     // (a lane a part, every wave alike)
     const int lane = tid & 63;
     const unsigned long long own = lane < parts ? s.mass[lane] : 0;
-    const unsigned long long upto = sm_lane_scan(own), sum = sm_last_lane(upto);
+    const unsigned long long upto = lane_scan(own), sum = last_lane(upto);
     const float u = a.u[row];
     unsigned long long want = u > 0.0f ? u < 1.0f ? (unsigned long long)((double)u * (double)sum) : sum - 1 : 0;
     if (want >= sum) want = sum - 1;
@@ -755,10 +723,10 @@ struct SmJoin : SmOf<BF> {
       s.list[tid] = lists_n;
       s.mass[tid] = fine(W);
     }
-    W = sm_last_lane(sm_lane_scan(W));
+    W = last_lane(lane_scan(W));
     __syncthreads();
     if (!cuts) {
-      draw({kSmMasked + 1, 0xFFFFFFFFu}, sm_last_lane(lane_scan(lives)));
+      draw({kSmMasked + 1, 0xFFFFFFFFu}, last_lane(lane_scan(lives)));
       return;
     }
 
@@ -862,10 +830,10 @@ struct SmJoin : SmOf<BF> {
       mine_n = (int)sm_load(recs, at + 3);
     }
     const bool fits = __ballot(mine_n > S::kCutList) == 0;
-    above = sm_last_lane(sm_lane_scan(above));
-    count = sm_last_lane(lane_scan(count));
-    kept = sm_last_lane(lane_scan(kept));
-    const int upto_n = lane_scan(mine_n), n = sm_last_lane(upto_n);
+    above = last_lane(lane_scan(above));
+    count = last_lane(lane_scan(count));
+    kept = last_lane(lane_scan(kept));
+    const int upto_n = lane_scan(mine_n), n = last_lane(upto_n);
     if (!fits || n > 2 * kSmSort) {
       whole_row();
       return;

@@ -302,3 +302,28 @@ def test_sample_more_rows_than_a_launch(w12):
     y = torch.randn(m, n, generator=torch.Generator().manual_seed(2)).cuda() * 3
     say("sample rows")
     check_sample(w12, y, np.random.default_rng(1).random(m).astype(np.float32), params(m, 3))
+
+
+def test_rows_that_overlap(w12):
+    """A q_start that falls back gives more rows than there are: attention writes nothing, and the next call is right."""
+    say("overlapping rows")
+    for seqs in (2, 90):
+        st = Step(w12, [40] * (2 * seqs), [3] * (2 * seqs), 2, 64, 16)
+        q = queries(st, 8)
+        good = st.batch
+        start = np.tile([0, st.rows], seqs + 1)[:2 * seqs + 1].astype(np.int32)
+        bad = w12.KVBatch(good.table, good.lens, q_start=torch.tensor(start).cuda())
+        y = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        w12.attention(q, st.kv, bad, out=y)
+        assert (y == 7.0).all()
+        check_attention(st, q, 8, w12.attention(q, st.kv, good))
+
+
+def test_batch_too_large(w12):
+    """Lengths that the table allows are refused where their work could not be counted."""
+    say("batch too large")
+    kv = w12.kv_cache(1, 128, 64, page=16)
+    batch = w12.KVBatch(torch.zeros((1, 1 << 26), dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda"))
+    with pytest.raises(w12.W12Error) as e:
+        w12.attention(torch.zeros((1, 128 * 64), dtype=torch.bfloat16, device="cuda"), kv, batch)
+    assert e.value.status == w12.W12_ERR_RANGE
