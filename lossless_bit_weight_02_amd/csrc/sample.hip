@@ -999,11 +999,14 @@ struct SmJoin : SmOf<BF> {
     }
     const double listed = sm_scan<T>(mine, s.wd, &before);
     const double want = r.p * (r.k < a.n ? listed : W);
-    // (of those of top-k that are not here, each is below the border of bin `need`)
-    const double most = partly ? r.p * (listed + (double)(r.k - n) * 1.001 * sm_exp2(-(double)need * r.c / (double)r.bins)) : want;
+    // (what is not here is below all that is, bins never falling as logits rise: so are those of top-k)
+    const double least = weight(sm_value((uint32_t)(s.sorting[n - 1] >> 32)));
+    const double most = partly ? r.p * (listed + (double)(r.k - n) * least) : want;
     const bool ends = all == n && need >= kSmBins - 1;   // (nothing else is left)
+    // min-p's three bins more cover what rounding x * bins may move, while that is below 2^21 (a quarter of a bin)
+    const bool min_ends = by_min && (least < r.min_p || fabs(M * (double)r.bins) < 2097152.0);
     // is the end of what is kept among them?
-    if (!(partly ? listed >= most : ends || by_min || (r.k < a.n ? n >= r.k : r.p < 1.0 && listed >= want))) return false;
+    if (!(partly ? listed >= most : ends || min_ends || (r.k < a.n ? n >= r.k : r.p < 1.0 && listed >= want))) return false;
     int keep = 0, keeps = 0;
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {

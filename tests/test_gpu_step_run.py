@@ -297,6 +297,20 @@ def test_sample_ways(w12, m, n, bf16, sigma, temp, k, p, mp):
         check_sample(w12, y, rng.random(m).astype(np.float32), kw)
 
 
+@pytest.mark.parametrize("base,step", [(3e7, 2.0), (-3e7, 2.0), (1e9, 64.0), (-1e12, 65536.0), (0.0, 2.0)])
+def test_sample_large_logits(w12, base, step):
+    """Logits whose own steps are coarse: the filters' ends fall as they do near zero."""
+    m, n = 12, 9001
+    rng = np.random.default_rng(int(abs(base)) % 1000 + 1)
+    y = torch.tensor(base - step * np.floor(rng.random((m, n)) ** 3 * 400), dtype=torch.float32).cuda()
+    say(f"sample logits about {base}")
+    for kw in (dict(min_p=0.3), dict(min_p=0.011), dict(top_k=700, min_p=0.05), dict(top_k=700, top_p=0.937), dict(top_p=0.937),
+               dict(top_p=0.937, min_p=0.1)):
+        kw = {k: np.full(m, v, np.int32 if k == "top_k" else np.float32) for k, v in kw.items()}
+        for temp in (2.0 * step, 0.25 * step, 0.01 * step):
+            check_sample(w12, y, rng.random(m).astype(np.float32), dict(kw, temperature=np.full(m, temp, np.float32)))
+
+
 def test_sample_more_rows_than_a_launch(w12):
     m, n = 9001, 67
     y = torch.randn(m, n, generator=torch.Generator().manual_seed(2)).cuda() * 3
