@@ -9,6 +9,8 @@
 // two of w, from the part's maximum down) and, in column order, the part's largest logits as far as whole bins of
 // them fit a short list.  A workgroup a row joins the parts (k_sample_join): the histogram says how far down
 // what is kept can reach, and then
+//   one      a row that keeps one token (temperature 0, top-k 1, min-p above 1) needs the first column of the
+//            largest logit alone, which is in the first part that has it;
 //   lists    where everything down to there is in the lists, their logits are sorted, cut and drawn from;
 //   no cut   without filters the parts' masses say which part the token is in, and that part is scanned;
 //   cut bin  else (thousands kept) two more kernels, which have nothing to do for other rows, look again: the
@@ -138,16 +140,15 @@ __device__ __forceinline__ double sm_exp2(double t) {
 struct SmRow {
   double c;               // log2 e / temperature
   float bins;             // bins of a logit's 1.0
-  bool hard;              // the largest logit
-  int64_t k;              // n: off
+  int64_t k;              // n: off; 1: the first token alone
   double p;               // 1 or more: off
   double min_p;           // 0: off
   __device__ __forceinline__ SmRow(const SampleArgs& a, int64_t row, float temp) {
-    hard = temp <= 0.0f;
+    const bool hard = temp <= 0.0f;
     c = hard ? 1.4426950408889634 : 1.4426950408889634 / (double)temp;
     const int32_t kk = a.top_k ? a.top_k[row] : 0;
     const float pp = a.top_p ? a.top_p[row] : 1.0f, mp = a.min_p ? a.min_p[row] : 0.0f;
-    const bool one = hard || mp > 1.0f;            // the first token alone
+    const bool one = hard || mp > 1.0f;
     k = one ? 1 : kk > 0 && kk < a.n ? kk : a.n;
     p = !one && pp < 1.0f ? (pp > 0.0f ? (double)pp : 0.0) : 1.0;
     min_p = !one && mp > 0.0f ? (double)mp : 0.0;
@@ -677,6 +678,28 @@ struct SmJoin : SmOf<BF> {
     draw(cut, kept);
   }
 
+  // The first column of the row's largest logit, in part p.
+  __device__ __forceinline__ void first_of(float mx, int p) {
+    const int64_t c0 = (int64_t)p * S::kPart;
+    float x[kElems];
+    L::load(y, c0, a.n, tid, x);
+    int first = 0x7FFFFFFF;
+#pragma unroll
+    for (int e = kElems - 1; e >= 0; --e)
+      if (x[e] == mx) first = (int)c0 + L::column(e, tid);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      const int other = __shfl_xor(first, o);
+      first = other < first ? other : first;
+    }
+    if ((tid & 63) == 0) s.list[tid >> 6] = first;
+    __syncthreads();
+    if (tid != 0) return;
+#pragma unroll
+    for (int i = 1; i < T / 64; ++i) first = s.list[i] < first ? s.list[i] : first;
+    put(first, 0.0, 1);
+  }
+
   // The row, from its parts' records.
   __device__ __forceinline__ void join(const uint64_t* rec0, SmPlanned* plan) {
     const bool cuts = r.k < a.n || r.p < 1.0 || r.min_p > 0.0;
@@ -710,6 +733,10 @@ struct SmJoin : SmOf<BF> {
     const bool bad = __ballot(bads) != 0;
     if (bad || mx == -INFINITY) {
       if (tid == 0) put(-1, bad ? (double)__uint_as_float(0x7FC00000u) : -(double)INFINITY, 0);
+      return;
+    }
+    if (r.k == 1) {
+      first_of(mx, __ffsll((unsigned long long)__ballot(lane < parts && tops == mx)) - 1);
       return;
     }
     this->is_top(mx);
@@ -1052,7 +1079,7 @@ struct SmJoin : SmOf<BF> {
     if (tid == 0) {
       const unsigned long long f = s.cand[s.found];
       const double d = ((double)sm_value((uint32_t)(f >> 32)) - M) * r.c;
-      put((uint32_t)f, r.hard ? 0.0 : 0.6931471805599453 * (d - log2(sum)), keep);
+      put((uint32_t)f, 0.6931471805599453 * (d - log2(sum)), keep);
     }
     return true;
   }
@@ -1135,7 +1162,8 @@ hipError_t launch_sample(const SampleArgs& a0, bool bf, void* scratch, hipStream
   SampleArgs a = a0;
   uint64_t* const recs = static_cast<uint64_t*>(scratch);
   SmPlanned* const plans = reinterpret_cast<SmPlanned*>(recs + p.rows * p.parts * (p.rec / 8));
-  const bool cuts = a.top_k || a.top_p || a.min_p;           // (without: nothing for the second kernel)
+  // (without a filter nothing is left for the second pair: a temperature alone keeps one token or all)
+  const bool cuts = a.top_k || a.top_p || a.min_p;
   for (int64_t r0 = 0; r0 < a0.m; r0 += p.rows) {
     a.m = a0.m - r0 < p.rows ? a0.m - r0 : p.rows;
     if (p.wide && bf) sm_go<true, 1024>(s, a, p.parts, plans, recs, cuts);

@@ -1,0 +1,123 @@
+"""Edges of cache append, attention and sampling: calls with some of the settings absent, random numbers at
+the ends of their range, non-finite values that some rows see, rows past the step's.  Tolerances as in
+test_gpu_step.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+
+import oracle
+from tests.gpu_util import say
+from tests.test_gpu_step import U, f64
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def w12():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from lossless_bit_weight_02_amd import w12 as mod
+    mod.lib()
+    return mod
+
+
+# ---- sampling ----
+POISON = -77
+
+
+def raw_sample(w12, y, u, **kw):
+    """w12_sample into outputs that hold POISON, as numpy arrays; settings that are not in kw are NULL."""
+    m, n = y.shape
+    flags = w12.LOGITS_BF16 if y.dtype == torch.bfloat16 else 0
+    out = [torch.full((m,), POISON, dtype=t, device="cuda") for t in (torch.int32, torch.float32, torch.int32)]
+    dev = {a: torch.tensor(b).cuda() for a, b in kw.items()}
+    need = ctypes.c_uint64(0)
+    assert w12.lib().w12_sample_scratch(m, n, flags, ctypes.byref(need)) == 0
+    scratch = torch.full((need.value,), 0x5A, dtype=torch.uint8, device="cuda")
+    ud = torch.tensor(u).cuda()
+    ptr = [None if a not in dev else dev[a].data_ptr() for a in ("temperature", "top_k", "top_p", "min_p")]
+    assert w12.lib().w12_sample(y.data_ptr(), m, n, y.stride(0) if m > 1 else n, *ptr, ud.data_ptr(), *(t.data_ptr() for t in out),
+                                scratch.data_ptr(), need.value, flags, torch.cuda.current_stream().cuda_stream) == 0
+    return tuple(t.cpu().numpy() for t in out)
+
+
+def check_raw(w12, y, u, **kw):
+    got = raw_sample(w12, y, u, **kw)
+    tok, logp, kept = oracle.sample64(f64(y), u.astype(np.float64),
+                                      **{a: b.astype(np.float64) if b.dtype != np.int32 else b for a, b in kw.items()})
+    assert np.array_equal(got[2], kept), (np.argwhere(got[2] != kept)[:5], got[2][got[2] != kept][:5])
+    assert np.array_equal(got[0], tok), (np.argwhere(got[0] != tok)[:5], got[0][got[0] != tok][:5], tok[got[0] != tok][:5])
+    fin = np.isfinite(logp)
+    lp = got[1].astype(np.float64)
+    assert np.array_equal(np.isnan(lp), np.isnan(logp)) and np.array_equal(np.isneginf(lp), np.isneginf(logp))
+    assert np.all(np.abs(lp[fin] - logp[fin]) <= U * np.abs(logp[fin]) + 1e-9)
+    return got
+
+
+def greedy_rows(m, n, seed):
+    """Rows whose largest logit is one of thousands alike, of few, or of magnitudes where steps are coarse."""
+    g = torch.Generator().manual_seed(seed)
+    y = torch.randn(m, n, generator=g)
+    y[0] = 0.0
+    y[1] = -0.0
+    y[1, n // 2:] = 0.0
+    y[2] *= 0.01
+    y[3] = y[3].round()
+    y[4] = torch.where(torch.rand(n, generator=g) < 0.5, 3e38, -3e38)
+    y[5] = y[5] * 1e6 + 3e9
+    y[6] = -1e30
+    y[7] = -float("inf")
+    y[8] = -float("inf")
+    y[8, n - 1] = -3e38
+    y[9, n // 3] = float("nan")
+    y[10, n - 1] = float("inf")
+    y[11, n - 1] = 50.0
+    return y
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("n", [1, 2, 200, 20011, 152064, 262145, 300007])
+def test_greedy_alone(w12, n, bf16):
+    """Temperatures of 0 and below with no other setting given; some rows are drawn."""
+    m = 14
+    y = greedy_rows(m, n, n)
+    y = (y.to(torch.bfloat16) if bf16 else y).cuda()
+    u = np.random.default_rng(n).random(m).astype(np.float32)
+    say(f"greedy n={n} bf16={bf16}")
+    for temps in ([0.0], [-1.0, 0.0, -float("inf")]):
+        check_raw(w12, y, u, temperature=np.resize(np.array(temps, np.float32), m))
+    mixed = np.zeros(m, np.float32)
+    mixed[[0, 2, 11, 13]] = [1.0, 1.5, 0.7, float("nan")]
+    check_raw(w12, y, u, temperature=mixed)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("n", [1, 63, 5003, 65537, 300007])
+def test_one_token_kept(w12, n, bf16):
+    """The settings that keep the first token alone, each given by itself, as greedy rows."""
+    m = 14
+    y = greedy_rows(m, n, n + 1)
+    y = (y.to(torch.bfloat16) if bf16 else y).cuda()
+    u = np.random.default_rng(n).random(m).astype(np.float32)
+    say(f"one token kept n={n} bf16={bf16}")
+    a = check_raw(w12, y, u, temperature=np.zeros(m, np.float32))
+    for kw in (dict(top_k=np.ones(m, np.int32)), dict(top_p=np.zeros(m, np.float32)), dict(min_p=np.full(m, 1.5, np.float32)),
+               dict(top_k=np.ones(m, np.int32), top_p=np.full(m, 0.5, np.float32), min_p=np.full(m, 0.5, np.float32))):
+        b = check_raw(w12, y, u, **kw)
+        assert all(np.array_equal(s, t, equal_nan=True) for s, t in zip(a, b))
+
+
+def test_greedy_batch(w12):
+    """A server's batch of greedy rows, and greedy ones among filtered ones."""
+    m, n = 256, 32001
+    y = (torch.randn(m, n, generator=torch.Generator().manual_seed(3)) * 3).to(torch.bfloat16).cuda()
+    rng = np.random.default_rng(4)
+    u = rng.random(m).astype(np.float32)
+    say("greedy batch")
+    check_raw(w12, y, u, temperature=np.zeros(m, np.float32))
+    check_raw(w12, y, u, temperature=np.where(np.arange(m) % 3 == 0, 0.0, 0.8).astype(np.float32),
+              top_k=rng.choice([0, 1, 40], m).astype(np.int32))
