@@ -654,6 +654,9 @@ __global__ __launch_bounds__(kBlock, 1) void k_attention(AttnArgs a) {
         for (int e = 0; e < 8; ++e)
           odd |= (there(e) & val.odd(e)) ? 1u << e : 0u;
         if (__ballot(odd != 0)) {
+          // (a place's columns are in 16 lanes, one of which may have it: all 16 take it out)
+#pragma unroll
+          for (int d = 1; d < 16; d <<= 1) odd |= __shfl_xor(odd, d);
           int go = g;
           asm volatile("" : "+v"(go));
 #pragma unroll 1

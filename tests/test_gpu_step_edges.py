@@ -9,7 +9,7 @@ import pytest
 
 import oracle
 from tests.gpu_util import say
-from tests.test_gpu_step import U, f64
+from tests.test_gpu_step import U, Step, attend, check_attention, f64, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +121,46 @@ def test_greedy_batch(w12):
     check_raw(w12, y, u, temperature=np.zeros(m, np.float32))
     check_raw(w12, y, u, temperature=np.where(np.arange(m) % 3 == 0, 0.0, 0.8).astype(np.float32),
               top_k=rng.choice([0, 1, 40], m).astype(np.int32))
+
+
+# ---- attention ----
+def bad_place(st, s, c, col, val):
+    st.v[int(st.table[s, c // st.page]), :, c % st.page, col] = val
+
+
+@pytest.mark.parametrize("dim,e4m3,group,t", [
+    (64, False, 4, 1), (128, False, 6, 1), (256, False, 6, 1), (64, True, 4, 1), (128, True, 6, 1), (256, True, 6, 1),
+    (128, False, 6, 2), (256, True, 6, 2), (64, False, 6, 4), (128, True, 6, 4), (128, False, 6, 4), (256, False, 6, 4),
+    (128, False, 6, 9)])
+def test_attention_seen_value(w12, dim, e4m3, group, t):
+    """A NaN or an infinity in one column of a new token reaches that column of the rows that see the token, and
+    no other: what stands behind the sequences is NaN, too.  (Up to 16, up to 32 and more rows a sequence.)"""
+    lens = [t, t + 1, 17 + t, 31, 33, 47, 64, 129, 300, 530]
+    st = Step(w12, lens, [t] * len(lens), 2, dim, 16, e4m3)
+    hq = 2 * group
+    q = queries(st, hq)
+    bad = float("nan") if e4m3 else float("inf")
+    for s, n in enumerate(lens):                                  # stale places of the last page
+        for c in range(n, (n + 15) // 16 * 16):
+            for x in (st.k, st.v):
+                x[int(st.table[s, c // 16]), :, c % 16] = float("nan")
+    say(f"attention seen value dim={dim} e4m3={e4m3} group={group} t={t}")
+    for j in range(0, t, 3):
+        for col in (0, 5, dim - 1):
+            keep = st.v.clone()
+            for s, n in enumerate(lens):
+                bad_place(st, s, n - t + j, col, 0.0)
+            zeroed = st.v.clone()
+            for s, n in enumerate(lens):
+                bad_place(st, s, n - t + j, col, bad)
+            y = attend(w12, st, q)
+            got = f64(y).reshape(-1, t, hq, dim)
+            hit = ~np.isfinite(got)
+            want = np.zeros_like(hit)
+            want[:, j:, :, col] = True
+            assert np.array_equal(hit, want), np.argwhere(hit != want)[:5]
+            # the other columns, and the rows before, are what they are without it
+            st.v.copy_(zeroed)
+            y2 = torch.where(torch.tensor(want).cuda().reshape(y.shape), attend(w12, st, q), y)
+            check_attention(st, q, hq, y2)
+            st.v.copy_(keep)
