@@ -537,7 +537,9 @@ struct SmJoin : SmOf<BF> {
     }
     // (the part's mass and its weights' may differ by a rounding: then the last one)
     __syncthreads();
-    if (s.found < 0) {
+    const int found = s.found;
+    __syncthreads();                               // (all have read it before some write it again)
+    if (found < 0) {
 #pragma unroll
       for (int e = 0; e < kElems; ++e)
         if (in >> e & 1u) atomicMax(&s.found, (int)(c0 + L::column(e, tid)));
@@ -1070,7 +1072,9 @@ struct SmJoin : SmOf<BF> {
       before = end;
     }
     __syncthreads();
-    if (s.found < 0) {                             // u of 1 or more, or a rounding at the end
+    const int found = s.found;
+    __syncthreads();                               // (all have read it before some write it again)
+    if (found < 0) {                               // u of 1 or more, or a rounding at the end
 #pragma unroll
       for (int q = 0; q < kMine; ++q)
         if (own[q] > 0.0) atomicMax(&s.found, r0 + q);

@@ -123,6 +123,21 @@ def test_greedy_batch(w12):
               top_k=rng.choice([0, 1, 40], m).astype(np.int32))
 
 
+@pytest.mark.parametrize("kw", [dict(top_k=1500), dict(top_k=9000), dict(top_p=0.9), dict(min_p=0.05), dict(min_p=0.4),
+                                dict(top_k=2000, top_p=0.95, min_p=0.01), dict(top_k=20000, top_p=0.8), {}])
+@pytest.mark.parametrize("sigma", [0.5, 2.0])
+def test_sample_last_of_many(w12, kw, sigma):
+    """u of 1 and more over kept tokens that every wave of a row's join holds some of, again and again alike."""
+    m, n = 40, 33001
+    y = (torch.randn(m, n, generator=torch.Generator().manual_seed(8)) * sigma).cuda()
+    kw = {a: np.full(m, b, np.int32 if a == "top_k" else np.float32) for a, b in kw.items()}
+    say(f"sample last of many sigma={sigma} {list(kw)}")
+    u = np.resize(np.array([1.0, 1.5, np.inf], np.float32), m)
+    a = check_raw(w12, y, u, **kw)
+    for _ in range(4):
+        assert all(np.array_equal(s, t) for s, t in zip(a, raw_sample(w12, y, u, **kw)))
+
+
 # ---- attention ----
 def bad_place(st, s, c, col, val):
     st.v[int(st.table[s, c // st.page]), :, c % st.page, col] = val
