@@ -46,6 +46,7 @@ constexpr int kSmAll = 2100000000;                // a cut's bin below every log
 constexpr int kSmRows = 4096;                     // rows of a launch
 constexpr uint32_t kSmMasked = 0x007FFFFFu;       // the order of -Inf
 constexpr double kSmFine = 4398046511104.0;       // 2^42: masses as integers, 2^20 logits of at most 1
+constexpr double kSmNear = 1048576.0;             // 2^20 of those: what the roundings of 2^20 logits come to
 
 template <int T>
 struct SmShape {
@@ -488,6 +489,17 @@ struct SmJoin : SmOf<BF> {
     __syncthreads();
   }
 
+  // The weight of a logit where it is kept, else 0.
+  __device__ __forceinline__ double kept_weight(SmCut cut, float x, uint32_t col) const {
+    const uint32_t key = sm_order(x);
+    const double w = weight(x > -INFINITY ? x : (float)M);
+    return (key > kSmMasked) & cut.in(key, col) & passes(w, key) ? w : 0.0;
+  }
+  // (s.found and s.val, the token and its logit, are written; sum: of all kept, in 2^-42)
+  __device__ __forceinline__ void put_drawn(unsigned long long sum, int64_t kept) const {
+    if (tid == 0) put(s.found, 0.6931471805599453 * (s.val - log2((double)sum / kSmFine)), kept);
+  }
+
   // The token, where `cut` is known and s.mass holds the kept mass of every part (in 2^-42): the part, then in it.
   __device__ __forceinline__ void draw(SmCut cut, int64_t kept) {
     // (a lane a part, every wave alike)
@@ -495,15 +507,31 @@ struct SmJoin : SmOf<BF> {
     const unsigned long long own = lane < parts ? s.mass[lane] : 0;
     const unsigned long long upto = lane_scan(own), sum = last_lane(upto);
     const float u = a.u[row];
-    unsigned long long want = u > 0.0f ? u < 1.0f ? (unsigned long long)((double)u * (double)sum) : sum - 1 : 0;
-    if (want >= sum) want = sum - 1;
-    const int p = __popcll(__ballot(lane < parts - 1 && upto <= want));
-    const unsigned long long left = want - __shfl(upto - own, p);
-    const int64_t c0 = (int64_t)p * S::kPart;
+    const double target = u > 0.0f ? (double)u * (double)sum : 0.0;
+    bool last = u >= 1.0f;
+    int64_t stop = a.n;
+    if (!last && target >= kSmNear) {
+      unsigned long long want = (unsigned long long)target;
+      if (want >= sum) want = sum - 1;
+      const int p = __popcll(__ballot(lane < parts - 1 && upto <= want));
+      const int64_t c0 = (int64_t)p * S::kPart;
+      if (draw_part(cut, c0, want - __shfl(upto - own, p))) {
+        put_drawn(sum, kept);
+        return;
+      }
+      // the part's mass was more than its weights' by their roundings: its last one
+      last = true;
+      stop = c0 + S::kPart < a.n ? c0 + S::kPart : a.n;
+    }
+    draw_end(cut, stop, last, target * (1.0 / kSmFine));
+    put_drawn(sum, kept);
+  }
+
+  // In the part from column c0 on the token at which the mass passes `left`, into s.found; false if it never does.
+  __device__ __forceinline__ bool draw_part(SmCut cut, int64_t c0, unsigned long long left) {
     float x[kElems];
     L::load(y, c0, a.n, tid, x);
     unsigned long long m[kElems], mine[L::kLoads], before[L::kLoads], tot[L::kLoads];
-    uint32_t in = 0;
     if (tid == 0) s.found = -1;
 #pragma unroll
     for (int v = 0; v < L::kLoads; ++v) {
@@ -511,11 +539,7 @@ struct SmJoin : SmOf<BF> {
 #pragma unroll
       for (int i = 0; i < L::kPer; ++i) {
         const int e = v * L::kPer + i;
-        const uint32_t key = sm_order(x[e]);
-        const double w = weight(x[e] > -INFINITY ? x[e] : (float)M);
-        const bool is = (key > kSmMasked) & cut.in(key, (uint32_t)(c0 + L::column(e, tid))) & passes(w, key);
-        m[e] = is ? fine(w) : 0;
-        in |= is ? 1u << e : 0u;
+        m[e] = fine(kept_weight(cut, x[e], (uint32_t)(c0 + L::column(e, tid))));
         mine[v] += m[e];
       }
     }
@@ -535,22 +559,48 @@ struct SmJoin : SmOf<BF> {
       }
       sofar += tot[v];
     }
-    // (the part's mass and its weights' may differ by a rounding: then the last one)
     __syncthreads();
     const int found = s.found;
     __syncthreads();                               // (all have read it before some write it again)
-    if (found < 0) {
+    return found >= 0;
+  }
+
+  // The same at u's ends, where the roundings to 2^-42 could decide: of the columns before `stop` the last kept one of
+  // any mass, or the first at which the mass passes target, in doubles, 4 logits a thread at a time from that end.
+  __device__ __forceinline__ void draw_end(SmCut cut, int64_t stop, bool last, double target) {
+    using Q = SmLoad<BF, T, 4>;
+    constexpr int kRun = 4 * T, kNone = 0x7FFFFFFF;
+    const int runs = (int)((stop + kRun - 1) / kRun);
+    double sofar = 0.0;
+    for (int i = 0; i < runs; ++i) {
+      const int64_t c0 = (int64_t)(last ? runs - 1 - i : i) * kRun;
+      float x[4];
+      Q::load(y, c0, stop, tid, x);
+      if (tid == 0) s.found = last ? -1 : kNone;
+      double w[4], mine = 0.0, before;
 #pragma unroll
-      for (int e = 0; e < kElems; ++e)
-        if (in >> e & 1u) atomicMax(&s.found, (int)(c0 + L::column(e, tid)));
-      __syncthreads();
-      const int f = s.found;
+      for (int e = 0; e < 4; ++e) {
+        w[e] = kept_weight(cut, x[e], (uint32_t)(c0 + Q::column(e, tid)));
+        mine += w[e];
+      }
+      const double all = sm_scan<T>(mine, s.wd, &before);
+      double end = sofar + before;
 #pragma unroll
-      for (int e = 0; e < kElems; ++e)
-        if ((int)(c0 + L::column(e, tid)) == f) s.val = ((double)x[e] - M) * r.c;
+      for (int e = 0; e < 4; ++e) {
+        end += w[e];
+        if (!(w[e] > 0.0)) continue;
+        if (last) atomicMax(&s.found, (int)(c0 + Q::column(e, tid)));
+        else if (end > target) atomicMin(&s.found, (int)(c0 + Q::column(e, tid)));
+      }
+      sofar += all;
       __syncthreads();
+      const int found = s.found;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((int)(c0 + Q::column(e, tid)) == found) s.val = ((double)x[e] - M) * r.c;
+      __syncthreads();                             // (and all have read s.found before the next run's)
+      if (last ? found >= 0 : found != kNone) return;
     }
-    if (tid == 0) put(s.found, 0.6931471805599453 * (s.val - log2((double)sum / kSmFine)), kept);
   }
 
   // Every logit of the row, a part at a time: f(x, key, column, part).
@@ -661,10 +711,10 @@ struct SmJoin : SmOf<BF> {
     return cut;
   }
 
-  // The cuts by k and p over the row itself, and the end.
-  __device__ __forceinline__ void whole_row() {
+  // The cuts by k and p over the row itself.
+  __device__ __forceinline__ void whole_row(SmCut& cut, int64_t& kept) {
     const SmCut all = {kSmMasked + 1, 0xFFFFFFFFu};
-    SmCut cut = all;
+    cut = all;
     unsigned long long mass = 0;
     if (r.k < a.n) cut = radix((unsigned long long)r.k, false, all, &mass);
     if (r.p < 1.0) {
@@ -676,8 +726,7 @@ struct SmJoin : SmOf<BF> {
       unsigned long long up_to;
       cut = radix((unsigned long long)ceil(r.p * (double)mass), true, cut, &up_to);
     }
-    const int64_t kept = part_masses(cut);
-    draw(cut, kept);
+    kept = part_masses(cut);
   }
 
   // The first column of the row's largest logit, in part p.
@@ -843,8 +892,15 @@ struct SmJoin : SmOf<BF> {
     plan->W = W;
   }
 
-  // A row with a plan, from its second records: the bin sorted and cut, the token drawn.
+  // A row with a plan: its cut, and the token.
   __device__ __forceinline__ void cut_join(const SmPlanned& plan, const uint64_t* rec0) {
+    SmCut cut = {kSmMasked + 1, 0xFFFFFFFFu};
+    int64_t kept = 0;
+    if (plan.state == 2 || !cut_bin(plan, rec0, cut, kept)) whole_row(cut, kept);
+    draw(cut, kept);
+  }
+  // The cut from the second records: the bin's logits, selected from; false if it is not in them.
+  __device__ __forceinline__ bool cut_bin(const SmPlanned& plan, const uint64_t* rec0, SmCut& cut, int64_t& all) {
     const Rsrc recs = make_rsrc(rec0, (uint32_t)(parts * S::kRec * 8));
     const int lane = tid & 63;
     double above = 0.0;
@@ -863,11 +919,7 @@ struct SmJoin : SmOf<BF> {
     count = last_lane(lane_scan(count));
     kept = last_lane(lane_scan(kept));
     const int upto_n = lane_scan(mine_n), n = last_lane(upto_n);
-    if (!fits || n > 2 * kSmSort) {
-      whole_row();
-      return;
-    }
-    SmCut cut = {kSmMasked + 1, 0xFFFFFFFFu};
+    if (!fits || n > 2 * kSmSort) return false;
     if (plan.bin < kSmBins) {
       if (tid < parts) s.list[tid] = upto_n - mine_n;
       __syncthreads();
@@ -879,10 +931,8 @@ struct SmJoin : SmOf<BF> {
       __syncthreads();
       const double want = r.k < a.n ? (double)(r.k - count) : r.p * plan.W - above;
       unsigned long long last;
-      if (!(want > 0.0 || count == 0) || !select(n, !(r.k < a.n), want, plan.bin, &last)) {
-        whole_row();                               // (the histogram's masses were off by a bin)
-        return;
-      }
+      // (the histogram's masses may be off by a bin)
+      if (!(want > 0.0 || count == 0) || !select(n, !(r.k < a.n), want, plan.bin, &last)) return false;
       cut = {(uint32_t)(last >> 32), ~(uint32_t)last};
       int more = 0;
       for (int i = tid; i < n; i += T) {
@@ -897,7 +947,8 @@ struct SmJoin : SmOf<BF> {
       kept += sm_sum<T>(more, reinterpret_cast<int*>(s.wf));
     }
     __syncthreads();
-    draw(cut, kept);
+    all = kept;
+    return true;
   }
 
   // Of s.all's n logits, all of bin `bin`, the one in descending order at which `want` of them (by_mass: that mass)
@@ -1121,8 +1172,7 @@ __global__ __launch_bounds__(kSmJoin) void k_sample_cut_join(SampleArgs a, int p
   if (plan.state == 0) return;
   SmJoin<BF, T> k(a, row, parts, s);
   k.is_top(plan.M);
-  if (plan.state == 2) k.whole_row();
-  else k.cut_join(plan, recs + row * parts * SmShape<T>::kRec);
+  k.cut_join(plan, recs + row * parts * SmShape<T>::kRec);
 }
 
 // Parts of 4096 logits; of 16384 where a row would have more than 64 of them.

@@ -138,6 +138,44 @@ def test_sample_last_of_many(w12, kw, sigma):
         assert all(np.array_equal(s, t) for s, t in zip(a, raw_sample(w12, y, u, **kw)))
 
 
+def lonely_rows(n, bf16):
+    """Rows whose first and last columns weigh 10^-18 to 10^-300 of the best, or nothing, with a few heavy ones between."""
+    y = torch.randn(6, n, generator=torch.Generator().manual_seed(n))
+    y[0, : n // 3] = -60.0
+    y[0, -(n // 3):] = -70.0
+    y[1, : n // 3] = -300.0
+    y[1, -5:] = -250.0
+    y[2, :7] = -1e30
+    y[2, 7] = -45.0
+    y[2, -9:] = -1e30
+    y[2, -10] = -400.0
+    y[3] = -50.0
+    y[3, n // 2] = 9.0
+    y[4] = -float("inf")
+    y[4, n // 2] = 2.0
+    y[4, n // 4] = -90.0
+    y[4, n - n // 4] = -90.0
+    y[5, ::2] = -80.0
+    return (y.to(torch.bfloat16) if bf16 else y).cuda()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("n", [40, 5003, 70001, 300007])
+def test_sample_ends_of_u(w12, n, bf16):
+    """u of 0 and below takes the first kept column of any mass, of 1 and above the last, a tiny one the column
+    that its mass reaches; kept by no filter, and by ones that leave all but few."""
+    y = lonely_rows(n, bf16)
+    m = y.shape[0]
+    say(f"sample ends of u n={n} bf16={bf16}")
+    for u in (0.0, -3.0, float("nan"), 1.0, 2.0, float("inf"), 1e-28, 1e-20, 3e-9, 1.0 - 2.0 ** -24):
+        uu = np.full(m, u, np.float32)
+        for kw in ({}, dict(top_k=np.full(m, n - n // 8 + 1, np.int32)), dict(min_p=np.full(m, 1e-37, np.float32)),
+                   dict(top_p=np.full(m, 0.99, np.float32)), dict(top_k=np.full(m, 17, np.int32), top_p=np.full(m, 0.8, np.float32))):
+            a = check_raw(w12, y, uu, **kw)
+            b = raw_sample(w12, y, uu, **kw)
+            assert all(np.array_equal(s, t, equal_nan=True) for s, t in zip(a, b))
+
+
 # ---- attention ----
 def bad_place(st, s, c, col, val):
     st.v[int(st.table[s, c // st.page]), :, c % st.page, col] = val
