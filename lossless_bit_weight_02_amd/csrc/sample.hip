@@ -1102,8 +1102,9 @@ struct SmJoin : SmOf<BF> {
     const unsigned long long last = s.sorting[keep - 1];
     const SmCut cut = {(uint32_t)(last >> 32), ~(uint32_t)last};
     // and in column order
+    constexpr int kNone = 0x7FFFFFFF;
     mine = 0.0;
-    if (tid == 0) s.found = -1;
+    if (tid == 0) s.found = kNone;
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
       const unsigned long long v1 = s.cand[q < own_n && r0 + q < n ? r0 + q : 0];
@@ -1114,18 +1115,23 @@ struct SmJoin : SmOf<BF> {
     }
     const double sum = sm_scan<T>(mine, s.wd, &before);
     const float u = a.u[row];
-    const double target = u > 0.0f ? u < 1.0f ? (double)u * sum : sum : 0.0;
+    const double target = u > 0.0f ? (double)u * sum : 0.0;
+    // the first one past target (one thread's last border and the next one's first may differ by a rounding: where
+    // target lies between them, the next one's is it), a wave's first for all of it
+    int at = kNone;
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
-      // (the border that the next one starts from is the one this one ends at)
-      const double end = before + own[q];
-      if (own[q] > 0.0 && before <= target && target < end) s.found = r0 + q;
-      before = end;
+      before += own[q];
+      if (u < 1.0f || !(u > 0.0f)) at = own[q] > 0.0 && before > target && at == kNone ? r0 + q : at;
     }
+    const uint64_t some = __ballot(at != kNone);
+    if (some && (tid & 63) == __ffsll((unsigned long long)some) - 1) atomicMin(&s.found, at);
     __syncthreads();
     const int found = s.found;
     __syncthreads();                               // (all have read it before some write it again)
-    if (found < 0) {                               // u of 1 or more, or a rounding at the end
+    if (found == kNone) {                          // u of 1 or more, or a rounding at the end: the last one
+      if (tid == 0) s.found = 0;                   // (the largest logit has a weight, and a place from 0 on)
+      __syncthreads();
 #pragma unroll
       for (int q = 0; q < kMine; ++q)
         if (own[q] > 0.0) atomicMax(&s.found, r0 + q);

@@ -176,6 +176,39 @@ def test_sample_ends_of_u(w12, n, bf16):
             assert all(np.array_equal(s, t, equal_nan=True) for s, t in zip(a, b))
 
 
+@pytest.mark.parametrize("n,kw", [(1000, dict(top_k=600)), (4000, dict(top_p=0.7)), (4000, {}), (2000, dict(min_p=0.2))])
+def test_sample_on_the_border(w12, n, kw):
+    """Rows of two equal halves and u = 1/2, so the number drawn for is a border up to the rounding of the sums: the
+    token is the last of the one half that is kept or the first of the other."""
+    m = 64
+    half = torch.randn(m, n // 2, generator=torch.Generator().manual_seed(n))
+    y = torch.cat([half, half], 1).cuda()
+    kw = {a: np.full(m, b, np.int32 if a == "top_k" else np.float32) for a, b in kw.items()}
+    say(f"sample on the border n={n}")
+    got = raw_sample(w12, y, np.full(m, 0.5, np.float32), **kw)
+    for r in range(m):
+        x = f64(half[r])
+        order = np.argsort(-x, kind="stable")
+        w = np.exp(x - x.max())
+        # (each logit twice: k / 2 of a half; the same share, the same least weight)
+        k = len(order)
+        if "top_k" in kw:
+            k = kw["top_k"][0] // 2
+        if "top_p" in kw:
+            k = None
+        if "min_p" in kw:
+            k = int((w >= kw["min_p"][0]).sum())
+        if k is None:
+            tok, _, kept = oracle.sample64(f64(y[r:r + 1]), [0.5], top_p=[float(np.float32(0.7))])
+            assert got[2][r] == kept[0]
+            if kept[0] % 2:
+                assert got[0][r] == tok[0]
+                continue
+            k = int(kept[0]) // 2
+        cols = np.sort(order[:k])
+        assert got[2][r] == 2 * k and got[0][r] in (cols[-1], n // 2 + cols[0]), r
+
+
 # ---- attention ----
 def bad_place(st, s, c, col, val):
     st.v[int(st.table[s, c // st.page]), :, c % st.page, col] = val
