@@ -454,7 +454,8 @@ struct SmJoin : SmOf<BF> {
     int shift[kSmParts], list[kSmParts];
     int found;
     int place[256];
-    int at[2];
+    int at;
+    unsigned long long ahead, last;                // a selection's: ahead of its bin, what it selects
     double val;
   };
   Shared& s;
@@ -846,20 +847,20 @@ struct SmJoin : SmOf<BF> {
       ms = 0.0;
     }
     int bin = kSmBins - 1;
-    if (tid == 0) s.at[0] = kSmBins - 1;
+    if (tid == 0) s.at = kSmBins - 1;
     if (counted) {
       int c;
       sm_scan<T>(cnt, reinterpret_cast<int*>(s.wf), &c);
-      if (c < r.k && c + cnt >= r.k && mine < kSmBins - 1) s.at[0] = mine;
+      if (c < r.k && c + cnt >= r.k && mine < kSmBins - 1) s.at = mine;
       __syncthreads();
-      bin = s.at[0];
+      bin = s.at;
     } else if (r.p < 1.0) {
       double m;
       sm_scan<T>(ms, s.wd, &m);
       const double want = r.p * W;
-      if (m < want && m + ms >= want && mine < kSmBins - 1) s.at[0] = mine;
+      if (m < want && m + ms >= want && mine < kSmBins - 1) s.at = mine;
       __syncthreads();
-      bin = want > 0.0 ? s.at[0] : 0;
+      bin = want > 0.0 ? s.at : 0;
     }
     int need = bin;
     // (top-k and top-p together: the mass of all k is asked for)
@@ -996,21 +997,21 @@ struct SmJoin : SmOf<BF> {
       const unsigned long long all = sm_scan<T>(mine, s.wu, &before);
       if (!again && all < left) return false;
       if (before < left && left <= before + mine) {
-        s.at[0] = 255 - tid;
-        s.wv[0][0] = before;
+        s.at = 255 - tid;
+        s.ahead = before;
       }
       __syncthreads();
-      const int d = s.at[0];
-      left -= s.wv[0][0];
+      const int d = s.at;
+      left -= s.ahead;
       key |= (unsigned long long)d << shift;
       mask |= 255ull << shift;
       if (s.cnt8[d] == 1) break;
       shift = shift > 8 ? shift - 8 : 0;
     }
     for (int i = tid; i < n; i += T)
-      if ((s.all[i] & mask) == key) s.wv[0][1] = s.all[i];
+      if ((s.all[i] & mask) == key) s.last = s.all[i];
     __syncthreads();
-    *last = s.wv[0][1];
+    *last = s.last;
     return true;
   }
 
