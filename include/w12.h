@@ -426,9 +426,10 @@ typedef struct w12_kv {
  * Rows from q_start[seqs] on (padding) belong to no sequence: nothing is read or written for them.
  * All arrays are device memory, read when the work runs, so a captured graph takes new lengths and
  * tables on each replay.  A place outside the table, or on a page outside 0 .. pages - 1, does not exist:
- * nothing is appended there and nobody sees it.  q_start must not fall; with other values the result is
- * undefined (where sequences' rows add up to more than m, w12_attention writes nothing), but nothing outside
- * the arrays is accessed.
+ * nothing is appended there and nobody sees it.  A q_start may pass m: the rows below m exist, with the places
+ * that they have among all T_s, the others are nothing.  q_start must not fall; with other values the result is
+ * undefined (where sequences' rows below m add up to more than m, w12_attention writes nothing), but nothing
+ * outside the arrays is accessed.
  */
 typedef struct w12_kv_batch {
     int64_t seqs;             /* below 2^20                                        */

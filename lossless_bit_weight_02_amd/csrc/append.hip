@@ -78,7 +78,7 @@ __global__ __launch_bounds__(kBlock) void k_append(AppendArgs a, KvArgs kv, Batc
   const int unit = (int)(blockIdx.x % chunks) * kBlock + threadIdx.x;
   const int64_t s = find_seq(b, row);
   if (s < 0) return;
-  const SeqRows sr = seq_rows(b, s, a.m);
+  const SeqRows sr = seq_rows(b, s);
   if (row >= sr.first + sr.count) return;
   const int64_t place = sr.len - sr.count + (row - sr.first);
   const int64_t pos = b.positions ? b.positions[row] : place;

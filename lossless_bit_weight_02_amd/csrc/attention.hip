@@ -229,13 +229,18 @@ struct UnitLine {
   __device__ __forceinline__ void read(int s) {
     count = 0;
     if (s < a.b.seqs) {
-      const SeqRows r = seq_rows(a.b, s, a.m);
+      const SeqRows r = seq_rows(a.b, s);
       first = (int)r.first;
       count = (int)r.count;
       len = (int)r.len;
     }
   }
-  __device__ __forceinline__ int mine() const { return blocks(count) * (int)a.kv.heads * length(tiles(len)); }
+  // of a sequence's new tokens' rows those there are
+  __device__ __forceinline__ int exist(int first, int count) const {
+    const int most = first >= 0 && first < a.m ? a.m - first : 0;
+    return count < most ? count : most;
+  }
+  __device__ __forceinline__ int mine() const { return blocks(exist(first, count)) * (int)a.kv.heads * length(tiles(len)); }
   __device__ __forceinline__ void scan() {
     upto = lane_scan(mine());
     total = lane_get(upto, 63);
@@ -246,7 +251,7 @@ struct UnitLine {
     for (int s = lane; s < a.b.seqs; s += 64) {
       read(s);
       sum += mine();
-      rows_n += count;
+      rows_n += exist(first, count);
     }
     return apart(rows_n) ? lane_get(lane_scan(sum), 63) : 0;
   }
@@ -259,7 +264,7 @@ struct UnitLine {
   __device__ __forceinline__ int start(int lane) {
     if (a.b.seqs <= 64) {
       read(lane);
-      if (!apart(count)) return 0;
+      if (!apart(exist(first, count))) return 0;
       scan();
       if (total <= a.wgs) return total;
       pieces = false;
@@ -292,7 +297,7 @@ struct UnitLine {
 
 // What a workgroup has of the segment at place u of the line.
 struct Segment {
-  int first, count, len, seen;                               // its sequence
+  int first, count, old, seen;                               // its sequence; old: places before its new tokens
   int s, hk, block, tiles;
   int tile0, tile1;                                          // this workgroup's units
   int from, to;                                              // the workgroups that have some
@@ -302,8 +307,11 @@ struct Segment {
     const int own = line.find(u, lane);
     s = line.c0 + own;
     first = lane_get(line.first, own);
-    count = lane_get(line.count, own);
-    len = lane_get(line.len, own);
+    const int all = lane_get(line.count, own), len = lane_get(line.len, own);
+    count = line.exist(first, all);
+    // (below -2^30 no place is within 2^30, the most rows there are, of the first new token, or in a mask)
+    const int64_t before = (int64_t)len - all;
+    old = before > -(1 << 30) ? (int)before : -(1 << 30);
     tiles = line.tiles(len);
     seen = line.seen(len);
     const int blocks = line.blocks(count), each = line.length(tiles);
@@ -576,7 +584,7 @@ __global__ __launch_bounds__(kBlock, 1) void k_attention(AttnArgs a) {
     const Segment sg(line, u, end, lane);
     u = sg.next;
     if (sg.tile1 <= sg.tile0) continue;
-    const int base = (sg.len < 0 ? 0 : sg.len) - sg.count;   // (fewer than 2^30 rows)
+    const int base = sg.old;
     const int t_end = sg.tile1 * kAtUnit < sg.seen ? sg.tile1 * kAtUnit : sg.seen;
     const int32_t* const table = a.b.table + (int64_t)sg.s * a.b.table_stride;
     const uint8_t* const kp = static_cast<const uint8_t*>(a.kv.k) + (int64_t)sg.hk * a.kv.head_stride * S::kSize;
@@ -790,7 +798,7 @@ __global__ __launch_bounds__(kAtWide, 2) void k_attention_rows(AttnArgs a) {
     const Segment sg(line, u, end, lane);
     u = sg.next;
     if (sg.tile1 <= sg.tile0) continue;
-    const int base = (sg.len < 0 ? 0 : sg.len) - sg.count;
+    const int base = sg.old;
     const int t_end = sg.tile1 * kAtUnit < sg.seen ? sg.tile1 * kAtUnit : sg.seen;
     const int32_t* const table = a.b.table + (int64_t)sg.s * a.b.table_stride;
     const uint8_t* const src = static_cast<const uint8_t*>(keys ? a.kv.k : a.kv.v) + (int64_t)sg.hk * a.kv.head_stride * S::kSize;

@@ -47,21 +47,20 @@ __device__ __forceinline__ V last_lane(V v) {
 // A sequence's rows and lengths.
 struct SeqRows {
   int64_t first;      // its first new token's row
-  int64_t count;      // T, 0 for an empty or senseless one
+  int64_t count;      // T, 0 for an empty or senseless one (their rows from m on do not exist)
   int64_t len;        // places it has, new ones included
 };
 
-__device__ __forceinline__ SeqRows seq_rows(const BatchArgs& b, int64_t s, int64_t m) {
+__device__ __forceinline__ SeqRows seq_rows(const BatchArgs& b, int64_t s) {
   SeqRows r;
   r.len = b.lens[s];
   if (b.q_start == nullptr) {
     r.first = s;
-    r.count = s < m ? 1 : 0;
+    r.count = 1;
     return r;
   }
   r.first = b.q_start[s];
-  int64_t end = b.q_start[s + 1];
-  if (end > m) end = m;
+  const int64_t end = b.q_start[s + 1];
   r.count = r.first >= 0 && end > r.first ? end - r.first : 0;
   return r;
 }

@@ -9,7 +9,7 @@ import pytest
 
 import oracle
 from tests.gpu_util import say
-from tests.test_gpu_step import U, Step, attend, check_attention, f64, queries
+from tests.test_gpu_step import U, Step, attend, check_append, check_attention, f64, queries, rope_table
 
 pytestmark = pytest.mark.gpu
 
@@ -250,3 +250,43 @@ def test_attention_seen_value(w12, dim, e4m3, group, t):
             y2 = torch.where(torch.tensor(want).cuda().reshape(y.shape), attend(w12, st, q), y)
             check_attention(st, q, hq, y2)
             st.v.copy_(keep)
+
+
+# ---- rows past the step's ----
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("group,news,rows", [(3, [2, 5, 9], 11), (3, [1, 1, 1], 2), (8, [30, 40, 50], 75), (2, [4, 6, 3], 10)])
+def test_sequence_past_the_rows(w12, e4m3, group, news, rows):
+    """A q_start that passes the step's rows: the rows that exist keep their places, the others do nothing."""
+    lens = [n + 40 * i for i, n in enumerate(news)]
+    for tree in (False, True):
+        masks = np.random.default_rng(rows).integers(0, 2 ** 63, rows, dtype=np.int64) if tree else None
+        st = Step(w12, lens, news, 2, 64, 16, e4m3, tree=masks)
+        hq = 2 * group
+        g = torch.Generator().manual_seed(1)
+        qkv = torch.randn(rows, (hq + 4) * 64, generator=g).cuda()
+        before = (st.k.clone(), st.v.clone())
+        rope = rope_table(max(lens) + 1, 64)
+        out = torch.full((rows, hq * 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        say(f"sequence past the rows news={news} rows={rows} e4m3={e4m3} tree={tree}")
+        w12.kv_append(qkv, st.kv, st.batch, rope=torch.tensor(rope).cuda(), out=out)
+        check_append(st, qkv, hq, rope, False, out, before, rows)
+        st.rows = rows
+        q = queries(st, hq)
+        check_attention(st, q, hq, attend(w12, st, q))
+
+
+def test_sequence_far_past_the_rows(w12):
+    """The same by 2^31 rows, where nothing but the last places' bounds holds them."""
+    st = Step(w12, [70, 40, 30], [1, 2, 3], 2, 64, 16)
+    st.start = np.array([0, 1, 2, 2 ** 31 - 1], np.int32)
+    st.make()
+    say("sequence far past the rows")
+    before = (st.k.clone(), st.v.clone())
+    qkv = torch.randn(5, 8 * 64, generator=torch.Generator().manual_seed(1)).cuda()
+    q = w12.kv_append(qkv, st.kv, st.batch)
+    y = attend(w12, st, q)
+    # the last sequence's new tokens have places far below 0 .. 29, so they see nothing and put nothing
+    assert (y[2:] == 0).all()
+    touched = ((st.k != before[0]).any(dim=(1, 3)), (st.v != before[1]).any(dim=(1, 3)))
+    for x in touched:
+        assert x.sum() == 2 and x[int(st.table[0, 4]), 5] and x[int(st.table[1, 2]), 7]
