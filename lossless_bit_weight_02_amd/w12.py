@@ -722,11 +722,19 @@ def logprobs(y: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0) 
     return r
 
 
+def _kept(name: str):
+    """A tensor that a structure of the library holds the address of: read-only."""
+    return property(lambda self: self._tensors[name])
+
+
 class KVCache:
     """A paged key/value cache: k and v [pages, heads, page, dim], bfloat16 or float8_e4m3fn (then standing
     for value * scale of the head, k_scale and v_scale float32 [heads]), with equal strides, columns
     contiguous.  The memory order of pages, heads and places is free (a transposed [pages, page, heads, dim]
-    tensor will do).  page is a multiple of 16, dim 64, 128 or 256."""
+    tensor will do).  page is a multiple of 16, dim 64, 128 or 256.  The tensors are the cache's for its life: their
+    values may change, other tensors make another KVCache."""
+
+    k, v, k_scale, v_scale = (_kept(n) for n in ("k", "v", "k_scale", "v_scale"))
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         for t, what in ((k, "k"), (v, "v")):
@@ -748,9 +756,9 @@ class KVCache:
                 raise TypeError(f"{what} must be float32, got {t.dtype}")
             if t.shape != (k.shape[1],) or not t.is_contiguous() or t.device != k.device:
                 raise ValueError(f"{what} must be contiguous [{k.shape[1]}] on {k.device}")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._tensors = dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale)
         self.pages, self.heads, self.page, self.dim = k.shape
-        self.device = k.device
+        self.device, self.dtype = k.device, k.dtype
         # (in sizes of 1 a stride says nothing, and torch lets it be anything)
         st = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
         self._c = _W12KV(self.pages, self.heads, self.page, self.dim, k.data_ptr(), v.data_ptr(), *st,
@@ -774,7 +782,10 @@ class KVBatch:
     q_start[s] .. of the step; place c is on page table[s, c // page].  All int32 on the device and read when
     the work runs: table [seqs, pages of the longest], lens [seqs], q_start [seqs + 1], positions
     [rows] for the rotation (default: the place).  tree int64 [rows]: bit b of a row's mask lets it see its
-    sequence's b-th new token (default: those up to its own)."""
+    sequence's b-th new token (default: those up to its own).  The tensors are the batch's for its life: update
+    them in place from step to step, other tensors make another KVBatch."""
+
+    table, lens, q_start, positions, tree = (_kept(n) for n in ("table", "lens", "q_start", "positions", "tree"))
 
     def __init__(self, table, lens, q_start=None, positions=None, tree=None):
         i32 = torch.int32
@@ -796,20 +807,22 @@ class KVBatch:
                 raise ValueError(f"{what} must be contiguous [{'rows' if n is None else n}]")
         if table.stride(1) != 1 and table.shape[1] > 1 or table.stride(0) < table.shape[1] and seqs > 1:
             raise ValueError("the rows of table must be contiguous and apart")
-        self.table, self.lens, self.q_start, self.positions, self.tree = table, lens, q_start, positions, tree
+        self._tensors = dict(table=table, lens=lens, q_start=q_start, positions=positions, tree=tree)
         self.seqs = seqs
         self.device = table.device
         self._c = _W12KVBatch(seqs, table.data_ptr(), table.shape[1], table.stride(0) if seqs > 1 else table.shape[1],
                               lens.data_ptr(), _ptr(q_start), _ptr(positions), _ptr(tree))
         self._ref = ctypes.byref(self._c)
         self._sizes = {}        # scratch of attention calls
+        self._fixed = [(n, what) for n, what in ((seqs if q_start is None else None, "lens"),
+                                                 (None if positions is None else positions.shape[0], "positions"),
+                                                 (None if tree is None else tree.shape[0], "tree")) if n is not None]
 
     def _rows(self, m: int):
-        if self.q_start is None and m != self.seqs:
-            raise ValueError(f"{m} rows for {self.seqs} sequences of one new token each")
-        for t, what in ((self.positions, "positions"), (self.tree, "tree")):
-            if t is not None and t.shape[0] != m:
-                raise ValueError(f"{what} has {t.shape[0]} entries for {m} rows")
+        for n, what in self._fixed:
+            if n != m:
+                raise ValueError(f"{m} rows for {n} sequences of one new token each" if what == "lens" else
+                                 f"{what} has {n} entries for {m} rows")
 
 
 def _check_step(kv: KVCache, batch: KVBatch):
@@ -923,7 +936,7 @@ def attention(q: torch.Tensor, kv: KVCache, batch: KVBatch, scale: float | None 
     L = lib()
     with _on_device(dev):
         stream = _stream_handle(dev)
-        key = (m, hq, kv.heads, dim, kv.page, kv.k.dtype)
+        key = (m, hq, kv.heads, dim, kv.page, kv.dtype)
         need = batch._sizes.get(key)
         if need is None:
             n = ctypes.c_uint64(0)
