@@ -897,6 +897,7 @@ def kv_append(qkv, kv: KVCache, batch: KVBatch, rope: torch.Tensor | None = None
 
 
 _step_buffers: dict = {}   # (operator, device, stream) -> scratch of the stream's calls
+_step_lock = threading.Lock()
 
 
 def _step_scratch(what, need, device, stream):
@@ -909,6 +910,13 @@ def _step_scratch(what, need, device, stream):
         buf = torch.empty(max(need, 1 << 18), dtype=torch.uint8, device=device)
         _step_buffers[(what, device.index, stream)] = buf
     return buf
+
+
+def _step_call(what, need, device, stream, call):
+    """call(address of scratch) with no other call between its launches: two threads on one stream share
+    its buffer, which holds for one call's kernels at a time."""
+    with _step_lock:
+        _check(call(_step_scratch(what, need, device, stream).data_ptr()))
 
 
 def attention(q: torch.Tensor, kv: KVCache, batch: KVBatch, scale: float | None = None,
@@ -942,9 +950,9 @@ def attention(q: torch.Tensor, kv: KVCache, batch: KVBatch, scale: float | None 
             n = ctypes.c_uint64(0)
             _check(L.w12_attention_scratch(m, hq, kv._ref, batch._ref, ctypes.byref(n)))
             need = batch._sizes[key] = n.value
-        buf = _step_scratch("attention", need, dev, stream)
-        _check(L.w12_attention(qp, ldq, m, hq, kv._ref, batch._ref, dim ** -0.5 if scale is None else float(scale),
-                               out.data_ptr(), buf.data_ptr(), need, 0, stream))
+        scale = dim ** -0.5 if scale is None else float(scale)
+        _step_call("attention", need, dev, stream, lambda buf: L.w12_attention(
+            qp, ldq, m, hq, kv._ref, batch._ref, scale, out.data_ptr(), buf, need, 0, stream))
     return out
 
 
@@ -1003,10 +1011,9 @@ def sample(y: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = 
             if len(_sample_sizes) > 4096:
                 _sample_sizes.clear()
             need = _sample_sizes[m, n, flags] = nb.value
-        buf = _step_scratch("sample", need, dev, stream)
-        _check(L.w12_sample(y.data_ptr(), m, n, y.stride(0) if m > 1 else n, _ptr(temperature), _ptr(top_k),
-                            _ptr(top_p), _ptr(min_p), u.data_ptr(), r.token.data_ptr(), r.logp.data_ptr(),
-                            r.kept.data_ptr(), buf.data_ptr(), need, flags, stream))
+        _step_call("sample", need, dev, stream, lambda buf: L.w12_sample(
+            y.data_ptr(), m, n, y.stride(0) if m > 1 else n, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+            u.data_ptr(), r.token.data_ptr(), r.logp.data_ptr(), r.kept.data_ptr(), buf, need, flags, stream))
     return r
 
 
@@ -1060,8 +1067,9 @@ def release_workspace(stream: "torch.cuda.Stream | None" = None, device=None):
     with torch.cuda.device(stream.device):
         _check(lib().w12_release_workspace(stream.cuda_stream))
     key = (stream.device.index, stream.cuda_stream)
-    held = [d for d in ((_lp_buffers, key), *((_step_buffers, (w, *key)) for w in ("attention", "sample"))) if d[1] in d[0]]
-    if held:
-        stream.synchronize()
-        for bufs, k in held:
-            bufs.pop(k, None)
+    with _step_lock:
+        held = [d for d in ((_lp_buffers, key), *((_step_buffers, (w, *key)) for w in ("attention", "sample"))) if d[1] in d[0]]
+        if held:
+            stream.synchronize()
+            for bufs, k in held:
+                bufs.pop(k, None)

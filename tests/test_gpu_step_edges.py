@@ -3,6 +3,7 @@ the ends of their range, non-finite values that some rows see, rows past the ste
 test_gpu_step.
 """
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -290,3 +291,37 @@ def test_sequence_far_past_the_rows(w12):
     touched = ((st.k != before[0]).any(dim=(1, 3)), (st.v != before[1]).any(dim=(1, 3)))
     for x in touched:
         assert x.sum() == 2 and x[int(st.table[0, 4]), 5] and x[int(st.table[1, 2]), 7]
+
+
+# ---- threads ----
+def test_two_threads_on_one_stream(w12):
+    """Attention that ends in a join and sampling of several kernels, called from two threads on the same stream: each
+    call's results are as alone."""
+    say("two threads on one stream")
+    sets = []
+    for seed, lens in ((1, [9000, 40, 3]), (2, [5, 7000, 800])):
+        st = Step(w12, lens, None, 2, 128, 64, seed=seed)
+        g = torch.Generator().manual_seed(seed)
+        y = (torch.randn(3, 60011, generator=g) * 2).cuda()
+        sets.append((st, queries(st, 16, seed), y, torch.rand(3, generator=g).cuda(), torch.full((3,), 0.97).cuda()))
+
+    def call(s):
+        st, q, y, u, p = s
+        return (w12.attention(q, st.kv, st.batch), *w12.sample(y, u, top_p=p))
+
+    want = [call(s) for s in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        for _ in range(100):
+            got[i].append(call(sets[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for mine, w in zip(got, want):
+        assert len(mine) == 100 and all(torch.equal(a, b) for r in mine for a, b in zip(r, w))
