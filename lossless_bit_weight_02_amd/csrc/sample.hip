@@ -52,10 +52,12 @@ template <int T>
 struct SmShape {
   static constexpr int kPart = T * kSmElems;
   // Entries of a part's list: all are read by the row's join, and where a row's do not reach down to its cut the
-  // second pair of kernels runs.  Of 8 parts lists of 128 take 34 us, of 64 48 (33 rows of 32001); of 38
-  // parts 131 and 122 us (256 rows of 152064).
-  static constexpr int kList = T == 256 ? 128 : 256;
-  static __device__ __forceinline__ int list_bits(int parts) { return (T == 256 ? 7 : 8) - (parts > 16 ? 1 : 0); }
+  // second pair of kernels runs.  128 instead of 64 save that for rows that a mask leaves few of (64 rows, 97 % masked,
+  // of 8, 16, 17, 24 and 38 parts: 38, 44, 49, 52, 78 us with 128, 52, 61, 61, 68, 79 with 64) and cost others up to
+  // a tenth (top-p 0.95: 40, 63, 64, 71, 83 us with 128, 45, 60, 59, 68, 82 with 64; top-k 20 as much either way).
+  // Vocabularies up to 65536 (16 parts), of which a mask leaves more parts with few, have 128.
+  static constexpr int kList = 128;
+  static __device__ __forceinline__ int list_bits(int parts) { return T == 256 && parts > 16 ? 6 : 7; }
   static constexpr int kHead = 4;                  // a part's record, in 64-bit words
   static constexpr int kCutList = 512;             // entries of the cut's list, which takes the place of both
   static constexpr int kRec = kHead + kCutList;
@@ -1018,7 +1020,7 @@ struct SmJoin : SmOf<BF> {
   // Cuts and draws from the lists' logits down to bin `need`; false if they turn out not to reach the cut.
   __device__ __forceinline__ bool from_lists(Rsrc recs, int need, bool by_min, bool partly, int big, double W) {
     // a run of the lists' slots a thread, so that one sum gives their places
-    constexpr int kMost = kSmParts * S::kList / 2 / T;
+    constexpr int kMost = kSmParts * (P == 256 ? S::kList / 2 : S::kList) / T;
     static_assert(16 * S::kList <= kMost * T);
     const int bits = S::list_bits(parts), slots = parts << bits, run = (slots + T - 1) / T;
     uint64_t v[kMost];
