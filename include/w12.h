@@ -501,9 +501,9 @@ int w12_attention(const uint16_t *q, int64_t ldq, int64_t m, int64_t hq, const w
  * (token or logp or kept may be NULL).  A temperature of 0 or less takes the first token of the order.
  * A row of -Inf alone gives token -1, logp -Inf and kept 0, one with a NaN or +Inf logit, or a
  * temperature of NaN, token -1, logp NaN and kept 0.
- * Weights and sums that decide are held in double or, where thousands are kept, in integers of 2^-42 of the largest
- * weight (from u * mass = 2^-22 on; in the sum of a whole row, weights below 2^-24 of those around them to
- * float's 24 bits), in a fixed order: equal calls give equal results.  flags: W12_LOGITS_BF16.
+ * Weights and sums that decide are held in double or, where thousands are kept, in integers of 2^-61 of what may
+ * be kept (in the sum of a whole row, weights below 2^-24 of those around them to float's 24 bits), in a fixed
+ * order: equal calls give equal results.  flags: W12_LOGITS_BF16.
  * scratch: w12_sample_scratch bytes of the caller's device memory (16-byte aligned), in use until the
  * call's work on `stream` is finished; its contents on entry do not matter.
  */

@@ -29,7 +29,7 @@
 // sums of 152064 floats are, one draw in a hundred from a flat row would be a neighbour's.  So weights
 // that decide are e^(..) in double (their own 2^f by a polynomial: |f ln 2| < 0.35, 12 terms,
 // 1e-14), those below 2^-24 of the maximum in float times an exact power of two (1e-7 of 2^-24), and sums are doubles in a
-// fixed order or integers.  The histogram's masses, which only choose
+// fixed order or integers of 2^-61 of what can be kept.  The histogram's masses, which only choose
 // where to look, are floats rounded to 2^-30.
 #include "kv_device.hpp"
 
@@ -45,8 +45,7 @@ constexpr int kSmSort = 2048;                     // logits that a row's join ca
 constexpr int kSmAll = 2100000000;                // a cut's bin below every logit's
 constexpr int kSmRows = 4096;                     // rows of a launch
 constexpr uint32_t kSmMasked = 0x007FFFFFu;       // the order of -Inf
-constexpr double kSmFine = 4398046511104.0;       // 2^42: masses as integers, 2^20 logits of at most 1
-constexpr double kSmNear = 1048576.0;             // 2^20 of those: what the roundings of 2^20 logits come to
+constexpr double kSmNear = 1048576.0;             // 2^20 grains (SmOf): what the roundings of 2^20 logits come to
 
 template <int T>
 struct SmShape {
@@ -204,6 +203,20 @@ __device__ __forceinline__ V sm_scan(V v, V* s_w, V* before) {   // *before: of 
   *before = b[0];
   return t[0];
 }
+template <int T>
+__device__ __forceinline__ unsigned long long sm_most(unsigned long long v, unsigned long long* s_w) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const unsigned long long other = __shfl_xor(v, o);
+    v = other > v ? other : v;
+  }
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = v;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < T / 64; ++i) v = s_w[i] > v ? s_w[i] : v;
+  return v;
+}
 template <int T, class V>
 __device__ __forceinline__ V sm_sum(V v, V* s_w) {
   v = last_lane(lane_scan(v));
@@ -253,7 +266,6 @@ struct SmOf {
     top = sm_order(x);
   }
   __device__ __forceinline__ double weight(float x) const { return sm_exp2(((double)x - M) * r.c); }
-  __device__ __forceinline__ unsigned long long fine(double w) const { return (unsigned long long)(w * kSmFine + 0.5); }
   __device__ __forceinline__ bool passes(double w, uint32_t key) const { return w >= r.min_p || key == top; }
 };
 
@@ -263,7 +275,7 @@ struct SmPart : SmOf<BF> {
   using S = SmShape<T>;
   using L = SmLoad<BF, T, kSmElems>;
   using Of = SmOf<BF>;
-  using Of::a, Of::tid, Of::y, Of::temp, Of::r, Of::weight, Of::fine, Of::passes;
+  using Of::a, Of::tid, Of::y, Of::temp, Of::r, Of::weight, Of::passes;
 
   struct Shared {
     unsigned long long hist[kSmBins];              // count << 48 | mass in 2^-30
@@ -393,8 +405,8 @@ struct SmPart : SmOf<BF> {
     L::load(y, c0, a.n, tid, x);
     if (tid == 0) s.n = 0;
     __syncthreads();
-    double mass = 0.0;
-    unsigned long long left = 0, counts = 0;       // counts: above, and of those the ones min-p leaves << 32
+    double mass = 0.0, left = 0.0;
+    unsigned long long counts = 0;                 // above, and of those the ones min-p leaves << 32
 #pragma unroll
     for (int e = 0; e < kSmElems; ++e) {
       const int d = x[e] > -INFINITY ? plan.big - r.bin(x[e]) : 0x7FFFFFFF;
@@ -402,7 +414,7 @@ struct SmPart : SmOf<BF> {
         const double w = weight(x[e]);
         mass += w;
         const bool in = passes(w, sm_order(x[e]));
-        left += in ? fine(w) : 0;
+        left += in ? w : 0.0;
         counts += in ? 1ull << 32 | 1 : 1;
       }
       if (d == plan.bin) {
@@ -411,11 +423,11 @@ struct SmPart : SmOf<BF> {
       }
     }
     mass = sm_sum<T>(mass, s.wd);
-    left = sm_sum<T>(left, s.wu);
+    left = sm_sum<T>(left, s.wd);
     counts = sm_sum<T>(counts, s.wu);
     if (tid == 0) {
       rec[0] = (uint64_t)__double_as_longlong(mass);
-      rec[1] = left;
+      rec[1] = (uint64_t)__double_as_longlong(left);
       rec[2] = counts;
       rec[3] = (uint64_t)s.n;
     }
@@ -430,7 +442,7 @@ struct SmJoin : SmOf<BF> {
   static constexpr int kElems = S::kPart / T;
   using L = SmLoad<BF, T, kElems>;
   using Of = SmOf<BF>;
-  using Of::a, Of::tid, Of::row, Of::y, Of::parts, Of::r, Of::M, Of::top, Of::weight, Of::fine, Of::passes;
+  using Of::a, Of::tid, Of::row, Of::y, Of::parts, Of::r, Of::M, Of::top, Of::weight, Of::passes;
 
   struct Shared {
     union {
@@ -451,7 +463,7 @@ struct SmJoin : SmOf<BF> {
     float wf[T / 64];
     // the parts
     double scale[kSmParts];
-    unsigned long long mass[kSmParts];             // of what is kept, in 2^-42
+    unsigned long long mass[kSmParts];             // of what is kept, in grains
     uint32_t ties[kSmParts];
     int shift[kSmParts], list[kSmParts];
     int found;
@@ -461,7 +473,15 @@ struct SmJoin : SmOf<BF> {
     double val;
   };
   Shared& s;
+  double grain = 0.0;                              // masses that are added in any order are integers of 1 / grain
   __device__ __forceinline__ SmJoin(const SampleArgs& args, int64_t row_, int parts_, Shared& sh) : Of(args, row_, parts_), s(sh) {}
+
+  // What is kept, of a mass up to `most`, is less than 2^62 grains.  (With a grain for all rows, 2^-42 of the largest
+  // weight, 150000 logits 22.5 below one that stands alone were cut, and drawn from, some places off.)
+  __device__ __forceinline__ void set_grain(double most) {
+    grain = __builtin_ldexp(1.0, 61 - ((int)(__double_as_longlong(most) >> 52) - 1023));
+  }
+  __device__ __forceinline__ unsigned long long fine(double w) const { return (unsigned long long)(w * grain + 0.5); }
 
   __device__ __forceinline__ void put(int64_t token, double logp, int64_t kept) const {
     if (a.token) a.token[row] = (int32_t)token;
@@ -496,14 +516,14 @@ struct SmJoin : SmOf<BF> {
   __device__ __forceinline__ double kept_weight(SmCut cut, float x, uint32_t col) const {
     const uint32_t key = sm_order(x);
     const double w = weight(x > -INFINITY ? x : (float)M);
-    return (key > kSmMasked) & cut.in(key, col) & passes(w, key) ? w : 0.0;
+    return key > kSmMasked && cut.in(key, col) && passes(w, key) ? w : 0.0;
   }
-  // (s.found and s.val, the token and its logit, are written; sum: of all kept, in 2^-42)
+  // (s.found and s.val, the token and its logit, are written; sum: of all kept, in grains)
   __device__ __forceinline__ void put_drawn(unsigned long long sum, int64_t kept) const {
-    if (tid == 0) put(s.found, 0.6931471805599453 * (s.val - log2((double)sum / kSmFine)), kept);
+    if (tid == 0) put(s.found, 0.6931471805599453 * (s.val - log2((double)sum / grain)), kept);
   }
 
-  // The token, where `cut` is known and s.mass holds the kept mass of every part (in 2^-42): the part, then in it.
+  // The token, where `cut` is known and s.mass holds the kept mass of every part (in grains): the part, then in it.
   __device__ __forceinline__ void draw(SmCut cut, int64_t kept) {
     // (a lane a part, every wave alike)
     const int lane = tid & 63;
@@ -526,7 +546,7 @@ struct SmJoin : SmOf<BF> {
       last = true;
       stop = c0 + S::kPart < a.n ? c0 + S::kPart : a.n;
     }
-    draw_end(cut, stop, last, target * (1.0 / kSmFine));
+    draw_end(cut, stop, last, target / grain);
     put_drawn(sum, kept);
   }
 
@@ -568,7 +588,7 @@ struct SmJoin : SmOf<BF> {
     return found >= 0;
   }
 
-  // The same at u's ends, where the roundings to 2^-42 could decide: of the columns before `stop` the last kept one of
+  // The same at u's ends, where the roundings to grains could decide: of the columns before `stop` the last kept one of
   // any mass, or the first at which the mass passes target, in doubles, 4 logits a thread at a time from that end.
   __device__ __forceinline__ void draw_end(SmCut cut, int64_t stop, bool last, double target) {
     using Q = SmLoad<BF, T, 4>;
@@ -639,11 +659,11 @@ struct SmJoin : SmOf<BF> {
     return (int64_t)kept;
   }
 
-  // The first token in order at which `want` tokens (by_mass: that mass, in 2^-42) have come, the last one there
-  // is where they never do, by 8 bits of the order at a time; *mass: of the tokens up to and with it.
-  __device__ SmCut radix(unsigned long long want, bool by_mass, SmCut within, unsigned long long* mass) {
+  // The first token in order at which `want` tokens (by_mass: that mass, in grains) have come, the last one there
+  // is where they never do, by 8 bits of the order at a time.
+  __device__ SmCut radix(unsigned long long want, bool by_mass, SmCut within) {
     uint32_t key = 0, mask = 0;
-    unsigned long long had_n = 0, had_m = 0, ties = 0;
+    unsigned long long had = 0, ties = 0;
     for (int shift = 24; shift >= 0; shift -= 8) {
       __syncthreads();
       for (int b = tid; b < 256; b += T) {
@@ -654,32 +674,28 @@ struct SmJoin : SmOf<BF> {
       each([&](float x, uint32_t k, uint32_t col) {
         if ((k & mask) != key || !within.in(k, col)) return;
         atomicAdd(&s.cnt8[k >> shift & 255u], 1u);
-        atomicAdd(&s.mass8[k >> shift & 255u], fine(weight(x)));
+        if (by_mass) atomicAdd(&s.mass8[k >> shift & 255u], fine(weight(x)));
       }, [](int) {});
       __syncthreads();
       int bin = 0;
-      unsigned long long n = had_n, m = had_m;
+      unsigned long long upto = had;
       for (int b = 255; b >= 0; --b) {               // (all threads alike)
         const uint32_t c = s.cnt8[b];
         if (c == 0) continue;
         bin = b;
-        had_n = n;
-        had_m = m;
-        n += c;
-        m += s.mass8[b];
-        if ((by_mass ? m : n) >= want) break;
+        had = upto;
+        upto += by_mass ? s.mass8[b] : c;
+        if (upto >= want) break;
       }
       ties = s.cnt8[bin];
       key |= (uint32_t)bin << shift;
       mask |= 255u << shift;
     }
     // of the equal ones, as many as it takes: the column of the last of them
-    const unsigned long long one = fine(weight(sm_value(key)));
     unsigned long long need = 1;
-    const unsigned long long had = by_mass ? had_m : had_n, step = by_mass ? one : 1;
+    const unsigned long long step = by_mass ? fine(weight(sm_value(key))) : 1;
     if (want > had && step > 0) need = (want - had + step - 1) / step;
     if (need > ties) need = ties;
-    *mass = had_m + need * one;
     unsigned long long cnt = 0, seen = 0;
     each([&](float, uint32_t k, uint32_t) { cnt += k == key ? 1 : 0; }, [&](int p) {
       const unsigned long long t = sm_sum<T>(cnt, s.wu);
@@ -718,17 +734,12 @@ struct SmJoin : SmOf<BF> {
   __device__ __forceinline__ void whole_row(SmCut& cut, int64_t& kept) {
     const SmCut all = {kSmMasked + 1, 0xFFFFFFFFu};
     cut = all;
-    unsigned long long mass = 0;
-    if (r.k < a.n) cut = radix((unsigned long long)r.k, false, all, &mass);
-    if (r.p < 1.0) {
-      if (!(r.k < a.n)) {
-        unsigned long long mine = 0;
-        each([&](float x, uint32_t, uint32_t) { mine += fine(weight(x)); }, [](int) {});
-        mass = sm_sum<T>(mine, s.wu);
-      }
-      unsigned long long up_to;
-      cut = radix((unsigned long long)ceil(r.p * (double)mass), true, cut, &up_to);
-    }
+    if (r.k < a.n) cut = radix((unsigned long long)r.k, false, all);
+    double mine = 0.0;
+    each([&](float x, uint32_t key, uint32_t col) { mine += cut.in(key, col) ? weight(x) : 0.0; }, [](int) {});
+    const double mass = sm_sum<T>(mine, s.wd);
+    set_grain(mass);
+    if (r.p < 1.0) cut = radix((unsigned long long)ceil(r.p * mass * grain), true, cut);
     kept = part_masses(cut);
   }
 
@@ -802,9 +813,11 @@ struct SmJoin : SmOf<BF> {
       s.scale[tid] = scale;
       s.shift[tid] = shifts;
       s.list[tid] = lists_n;
-      s.mass[tid] = fine(W);
     }
+    const double own = W;
     W = last_lane(lane_scan(W));
+    set_grain(W);
+    if (tid < parts) s.mass[tid] = fine(own);
     __syncthreads();
     if (!cuts) {
       draw({kSmMasked + 1, 0xFFFFFFFFu}, last_lane(lane_scan(lives)));
@@ -906,13 +919,13 @@ struct SmJoin : SmOf<BF> {
   __device__ __forceinline__ bool cut_bin(const SmPlanned& plan, const uint64_t* rec0, SmCut& cut, int64_t& all) {
     const Rsrc recs = make_rsrc(rec0, (uint32_t)(parts * S::kRec * 8));
     const int lane = tid & 63;
-    double above = 0.0;
+    double above = 0.0, left = 0.0;
     int count = 0, kept = 0, mine_n = 0;
     if (lane < parts) {
       const int at = lane * S::kRec;
       above = __longlong_as_double((long long)sm_load(recs, at));
-      const uint64_t m = sm_load(recs, at + 1), c = sm_load(recs, at + 2);
-      if (tid < parts) s.mass[tid] = m;
+      left = __longlong_as_double((long long)sm_load(recs, at + 1));
+      const uint64_t c = sm_load(recs, at + 2);
       count = (int)(uint32_t)c;
       kept = (int)(c >> 32);
       mine_n = (int)sm_load(recs, at + 3);
@@ -923,6 +936,7 @@ struct SmJoin : SmOf<BF> {
     kept = last_lane(lane_scan(kept));
     const int upto_n = lane_scan(mine_n), n = last_lane(upto_n);
     if (!fits || n > 2 * kSmSort) return false;
+    double most = last_lane(lane_scan(left));
     if (plan.bin < kSmBins) {
       if (tid < parts) s.list[tid] = upto_n - mine_n;
       __syncthreads();
@@ -937,6 +951,16 @@ struct SmJoin : SmOf<BF> {
       // (the histogram's masses may be off by a bin)
       if (!(want > 0.0 || count == 0) || !select(n, !(r.k < a.n), want, plan.bin, &last)) return false;
       cut = {(uint32_t)(last >> 32), ~(uint32_t)last};
+      // (none of the bin's weighs more than its first)
+      unsigned long long first = 0;
+      for (int i = tid; i < n; i += T) first = s.all[i] > first ? s.all[i] : first;
+      most += (double)n * weight(sm_value((uint32_t)(sm_most<T>(first, s.wu) >> 32)));
+    }
+    set_grain(most);
+    if (tid < parts) s.mass[tid] = fine(left);
+    if (plan.bin < kSmBins) {
+      __syncthreads();
+      const unsigned long long last = (unsigned long long)cut.key << 32 | (uint32_t)~cut.col;
       int more = 0;
       for (int i = tid; i < n; i += T) {
         const unsigned long long v = s.all[i];

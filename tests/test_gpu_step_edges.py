@@ -210,6 +210,31 @@ def test_sample_on_the_border(w12, n, kw):
         assert got[2][r] == 2 * k and got[0][r] in (cols[-1], n // 2 + cols[0]), r
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("n", [3000, 60013, 152064, 300007])
+@pytest.mark.parametrize("kw", [{}, dict(min_p=1e-13), dict(top_k=2900), dict(top_p=0.99999), dict(top_k=100000, top_p=0.999999)])
+def test_sample_long_tails(w12, kw, n, bf16):
+    """One logit far above a row of ties and near ties, which weigh 2^-26 to 2^-40 of it and come first: what is kept and
+    drawn among them is decided to a part of one of them."""
+    g = torch.Generator().manual_seed(n)
+    y = torch.randn(12, n, generator=g)
+    y[0] = -22.5
+    y[1] = -18.3
+    y[2] = -27.1
+    y[3] = (y[3] * 8).round() / 8 - 20.0
+    y[4:8] = y[4:8] * 0.5 - 21.0
+    y[8:] = y[8:] * 2.0 - 24.0
+    y[:, -1] = 0.4
+    y = (y.to(torch.bfloat16) if bf16 else y).cuda()
+    rng = np.random.default_rng(n)
+    tail = np.exp(f64(y)[:, :-1] - f64(y)[:, -1:]).sum(axis=1)
+    m = y.shape[0]
+    kw = {a: np.full(m, min(b, n - 1) if a == "top_k" else b, np.int32 if a == "top_k" else np.float32) for a, b in kw.items()}
+    say(f"sample long tails n={n} bf16={bf16} {list(kw)}")
+    for _ in range(4):
+        check_raw(w12, y, (rng.random(m) * tail).astype(np.float32), **kw)
+
+
 # ---- attention ----
 def bad_place(st, s, c, col, val):
     st.v[int(st.table[s, c // st.page]), :, c % st.page, col] = val
