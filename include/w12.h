@@ -473,7 +473,10 @@ int w12_kv_append(const void *q, int64_t ldq, const void *k, int64_t ldk, const 
  * Values of places that a row does not see never reach it, NaN and infinities included; a NaN or an
  * infinity it sees gives NaN or an infinity.  q: bfloat16, row i at q + i * ldq elements (16-byte aligned, ldq a multiple of 8); y:
  * [m][hq * dim] bfloat16 (16-byte aligned), rounded once to nearest even.  Scores, softmax and sums
- * are held in float, the probabilities that meet v in 16 significant bits (11 over an e4m3 cache).
+ * are held in float, the probabilities that meet v in 16 significant bits (over an e4m3 cache in 22, but
+ * in 11 where a key head has more than 32 rows of q a sequence on average, 16 at 256 columns).  Their products
+ * add up before they are divided by the probabilities' sum: v times the places seen times 2^8 (e4m3: 2^15)
+ * must stay below float's largest.  y must not overlap q.
  * scratch: w12_attention_scratch bytes of the caller's device memory (16-byte aligned), in use until
  * the call's work on `stream` is finished; what it holds before does not matter.  Calls with different
  * scratch never touch each other's.  Which places are summed together depends on the lengths of the

@@ -15,8 +15,11 @@
 //                  permute per pair).  No value passes between lanes, and nothing goes through LDS.
 // Probabilities meet bfloat16 values as two bfloat16 terms (the leading 8 bits and the rest, 16 bits
 // together): one would be off by as much again as the output's own rounding.  e4m3 values are float16
-// exactly, so there one float16 term (11 bits) does, the probabilities brought up to 2^15: those too
-// small for it are off by 2^-32 of the largest.
+// exactly, so there float16 terms do (11 bits each), the probabilities brought up to 2^15: those too
+// small for it are off by 2^-32 of the largest.  Two terms (22 bits) cost k_attention nothing (64 sequences of one token,
+// 6 rows each, 67.2 us with one, 67.9 with two); k_attention_rows, whose products are the most of it, has one (16 trees
+// of 256 columns 90 us, with two 120; of 128 columns 93 and 108): there the output is off by 0.9e-3 of
+// its size from what float probabilities give, half its own rounding (1.7e-3 in all, as without).
 //
 // Split.  The work of the whole batch is a line of units of 128 places (of one sequence, key head and
 // block of rows); every workgroup takes an equal run of it, found from the lengths on the device, so
@@ -367,8 +370,8 @@ __device__ __forceinline__ SeenBy load_query(const AttnArgs& a, const Segment& s
 }
 
 // Scores of eight places into probabilities relative to the running maximum m (see the top), added to l, as
-// B operands (lo: bfloat16 only).
-template <bool E4M3, int SUBS>
+// B operands, in one term (hi) or TWO.
+template <bool E4M3, bool TWO, int SUBS>
 __device__ __forceinline__ void soften(const float (&x)[8], float& m, float& l, floatx4 (&acc)[SUBS], u32x4& hi, u32x4& lo) {
   constexpr float kUp = E4M3 ? 7.0f : 0.0f;
   float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
@@ -394,6 +397,10 @@ __device__ __forceinline__ void soften(const float (&x)[8], float& m, float& l, 
     if constexpr (E4M3) {
       const f16x2 rr = {(_Float16)p[2 * e], (_Float16)p[2 * e + 1]};
       hi[e] = __builtin_bit_cast(uint32_t, rr);
+      if constexpr (TWO) {
+        const f16x2 ll = {(_Float16)(p[2 * e] - (float)rr[0]), (_Float16)(p[2 * e + 1] - (float)rr[1])};
+        lo[e] = __builtin_bit_cast(uint32_t, ll);
+      }
     } else {
       hi[e] = __builtin_amdgcn_perm(__float_as_uint(p[2 * e + 1]), __float_as_uint(p[2 * e]), 0x07060302u);
       const bf16x2 rr = {(__bf16)(p[2 * e] - __uint_as_float(hi[e] << 16)),
@@ -652,7 +659,7 @@ __global__ __launch_bounds__(kBlock, 1) void k_attention(AttnArgs a) {
           for (int e = 0; e < 8; ++e)
             x[e] = (there(e) & sees[n](tm + (e < 4 ? e : 12 + e) - base)) ? x[e] : -INFINITY;
         }
-        soften<E4M3>(x, m[n], l[n], acc[n], ph[n], pl[n]);
+        soften<E4M3, true>(x, m[n], l[n], acc[n], ph[n], pl[n]);
       }
       if (masked) {
         // places of V with a NaN or an infinity, where some rows may not see them: one at a time, for the
@@ -682,7 +689,7 @@ __global__ __launch_bounds__(kBlock, 1) void k_attention(AttnArgs a) {
               for (int n = 0; n < NQ; ++n) {
                 floatx4 one = {0.0f, 0.0f, 0.0f, 0.0f};
                 one = mfma_pv<E4M3>(vf, ph[n], one);
-                if constexpr (!E4M3) one = mfma_pv<E4M3>(vf, pl[n], one);
+                one = mfma_pv<E4M3>(vf, pl[n], one);
                 acc[n][c] = sees[n](bit) ? acc[n][c] + one : acc[n][c];
               }
               __builtin_amdgcn_sched_barrier(0);             // (one block's registers at a time)
@@ -698,7 +705,7 @@ __global__ __launch_bounds__(kBlock, 1) void k_attention(AttnArgs a) {
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
           acc[n][c] = mfma_pv<E4M3>(vf, ph[n], acc[n][c]);
-          if constexpr (!E4M3) acc[n][c] = mfma_pv<E4M3>(vf, pl[n], acc[n][c]);
+          acc[n][c] = mfma_pv<E4M3>(vf, pl[n], acc[n][c]);
         }
       }
 #pragma unroll
@@ -777,6 +784,7 @@ template <int DIM, bool E4M3>
 __global__ __launch_bounds__(kAtWide, 2) void k_attention_rows(AttnArgs a) {
   using S = AttnShape<DIM, E4M3>;
   constexpr int kRows = kAtWideRows;
+  constexpr bool kTwo = !E4M3;                               // terms of a probability
   // two waves share 32 places where one's would take too many registers: steps are of 64 then
   constexpr int kParts = DIM * S::kSize > 256 ? 2 : 1, kSlices = 4 / kParts, kStep = 32 * kSlices;
   __shared__ u32x4 s_kv[kSlices][2 * S::kSubs][64];          // per 32 places: keys (two 16s), then values
@@ -910,7 +918,7 @@ __global__ __launch_bounds__(kAtWide, 2) void k_attention_rows(AttnArgs a) {
             }
           }
           u32x4 ph, pl;
-          soften<E4M3>(x, m, l, acc, ph, pl);
+          soften<E4M3, kTwo>(x, m, l, acc, ph, pl);
           const uint32_t odd = __builtin_amdgcn_readfirstlane(s_odd[k][0] | s_odd[k][kParts - 1]);
           if (odd == 0) {
 #pragma unroll
@@ -920,7 +928,7 @@ __global__ __launch_bounds__(kAtWide, 2) void k_attention_rows(AttnArgs a) {
 #pragma unroll
               for (int z = 0; z < 4; ++z) {
                 acc[c + z] = mfma_pv<E4M3>(op[now][z], ph, acc[c + z]);
-                if constexpr (!E4M3) acc[c + z] = mfma_pv<E4M3>(op[now][z], pl, acc[c + z]);
+                if constexpr (kTwo) acc[c + z] = mfma_pv<E4M3>(op[now][z], pl, acc[c + z]);
               }
             }
           } else {
@@ -944,7 +952,7 @@ __global__ __launch_bounds__(kAtWide, 2) void k_attention_rows(AttnArgs a) {
                 const u32x4 vf = s_kv[k][S::kSubs + c][lane] & part;
                 floatx4 one = {0.0f, 0.0f, 0.0f, 0.0f};
                 one = mfma_pv<E4M3>(vf, ph, one);
-                if constexpr (!E4M3) one = mfma_pv<E4M3>(vf, pl, one);
+                if constexpr (kTwo) one = mfma_pv<E4M3>(vf, pl, one);
                 acc[c] = seen ? acc[c] + one : acc[c];
                 __builtin_amdgcn_sched_barrier(0);
               }

@@ -10,7 +10,7 @@ import pytest
 
 import oracle
 from tests.gpu_util import say
-from tests.test_gpu_step import U, Step, attend, check_append, check_attention, f64, queries, rope_table
+from tests.test_gpu_step import H, U, Step, attend, check_append, check_attention, f64, queries, rope_table
 
 pytestmark = pytest.mark.gpu
 
@@ -276,6 +276,36 @@ def test_attention_seen_value(w12, dim, e4m3, group, t):
             y2 = torch.where(torch.tensor(want).cuda().reshape(y.shape), attend(w12, st, q), y)
             check_attention(st, q, hq, y2)
             st.v.copy_(keep)
+
+
+@pytest.mark.parametrize("dim,e4m3,t,group", [(128, False, 1, 6), (64, True, 1, 6), (128, True, 1, 6), (256, True, 1, 6),
+                                              (128, True, 4, 6), (128, False, 4, 6), (64, False, 20, 6), (256, True, 20, 6)])
+def test_attention_differences(w12, dim, e4m3, t, group):
+    """Pairs of places with nearly equal scores and opposite values, whose difference is left: it keeps the bits that the
+    probabilities that meet the values have (16; over e4m3 22, in many rows 11; half a unit each), and float's of
+    their sums and scores (as in test_gpu_step: scores are at most 1 here)."""
+    st = Step(w12, [64 + t] * 3, [t] * 3, 1, dim, 16, e4m3, scales=False)
+    rng = np.random.default_rng(dim + t)
+    k, v = np.zeros((st.pages, 1, 16, dim)), np.zeros((st.pages, 1, 16, dim))
+    for s in range(3):
+        for c in range(0, 64, 2):
+            val = rng.choice([1.0, 16.0, 448.0], dim) * rng.choice([-1, 1], dim)
+            for at, sign in ((c, 1.0), (c + 1, -1.0)):
+                p, o = int(st.table[s, at // 16]), at % 16
+                v[p, 0, o] = sign * val
+                k[p, 0, o, 0] = 0.5 * sign * 2.0 ** -int(rng.integers(3, 7))
+    st.k.copy_(torch.tensor(k).to(st.k.dtype))
+    st.v.copy_(torch.tensor(v).to(st.v.dtype))
+    assert np.array_equal(st.values(0), k) and np.array_equal(st.values(1), v)
+    q = torch.zeros((st.rows, group * dim), dtype=torch.bfloat16, device="cuda")
+    q.view(st.rows, group, dim)[:, :, 0] = torch.tensor(rng.uniform(0.2, 1.0, (st.rows, group))).to(torch.bfloat16).cuda()
+    say(f"attention differences dim={dim} e4m3={e4m3} t={t}")
+    y = f64(attend(w12, st, q, scale=1.0)).reshape(st.rows, group, dim)
+    want, mag, big = oracle.attention64(f64(q).reshape(st.rows, group, dim), k, v, st.table, st.lens, st.start, None, 1.0)
+    bits = (2.0 ** -11 if t * group > 32 else 2.0 ** -22) if e4m3 else 2.0 ** -16
+    rel = bits + 2 * (dim + 8) * U * big[:, :, None] + 4 * U + (64 + t + 8) * U
+    bad = ~(np.abs(y - want) <= H * np.abs(want) + (1 + H) * rel * mag)
+    assert not bad.any(), np.argwhere(bad)[:5]
 
 
 # ---- rows past the step's ----
