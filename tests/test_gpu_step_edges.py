@@ -235,6 +235,23 @@ def test_sample_long_tails(w12, kw, n, bf16):
         check_raw(w12, y, (rng.random(m) * tail).astype(np.float32), **kw)
 
 
+@pytest.mark.parametrize("temp", [1e-38, 1e-30, 1e-3, 1e6, 1e30, float("inf")])
+@pytest.mark.parametrize("n", [77, 9001, 70001])
+def test_sample_extreme_temperatures(w12, n, temp):
+    """Temperatures that leave one token or make all alike, with each filter."""
+    m = 6
+    y = torch.randn(m, n, generator=torch.Generator().manual_seed(n)) * 3
+    y[1] = (y[1] * 4).round() / 4
+    y[2, ::3] = -float("inf")
+    y[3] *= 1e30
+    y = y.cuda()
+    rng = np.random.default_rng(n)
+    say(f"sample n={n} temperature={temp}")
+    for kw in (dict(top_k=5), dict(top_k=3000), dict(top_p=0.8713), dict(min_p=0.3), dict(top_k=60, top_p=0.7171, min_p=0.01)):
+        kw = {a: np.full(m, b, np.int32 if a == "top_k" else np.float32) for a, b in kw.items()}
+        check_raw(w12, y, rng.random(m).astype(np.float32), temperature=np.full(m, temp, np.float32), **kw)
+
+
 # ---- attention ----
 def bad_place(st, s, c, col, val):
     st.v[int(st.table[s, c // st.page]), :, c % st.page, col] = val
@@ -276,6 +293,35 @@ def test_attention_seen_value(w12, dim, e4m3, group, t):
             y2 = torch.where(torch.tensor(want).cuda().reshape(y.shape), attend(w12, st, q), y)
             check_attention(st, q, hq, y2)
             st.v.copy_(keep)
+
+
+@pytest.mark.parametrize("dim,e4m3,t,group", [(128, False, 3, 4), (64, True, 5, 3), (256, False, 4, 3), (128, True, 5, 6), (128, False, 8, 6)])
+def test_attention_seen_value_in_a_tree(w12, dim, e4m3, t, group):
+    """The same with masks: rows whose mask has the token's bit have the value, the others' are as if it were zero."""
+    lens = [t, 19 + t, 32 + t, 61, 200]
+    m = t * len(lens)
+    rng = np.random.default_rng(dim + t)
+    masks = rng.integers(0, 1 << t, m, dtype=np.int64)
+    st = Step(w12, lens, [t] * len(lens), 1, dim, 16, e4m3, tree=masks)
+    q = queries(st, group)
+    bad = float("nan") if e4m3 else float("-inf")
+    say(f"attention seen value in a tree dim={dim} e4m3={e4m3} t={t}")
+    for j in range(t):
+        col = int(rng.integers(dim))
+        keep = st.v.clone()
+        for s, n in enumerate(lens):
+            bad_place(st, s, n - t + j, col, 0.0)
+        zeroed = st.v.clone()
+        for s, n in enumerate(lens):
+            bad_place(st, s, n - t + j, col, bad)
+        y = attend(w12, st, q)
+        want = np.zeros((m, group, dim), bool)
+        want[(masks >> j & 1) == 1, :, col] = True
+        hit = ~np.isfinite(f64(y).reshape(want.shape))
+        assert np.array_equal(hit, want), np.argwhere(hit != want)[:5]
+        st.v.copy_(zeroed)
+        check_attention(st, q, group, torch.where(torch.tensor(want).cuda().reshape(y.shape), attend(w12, st, q), y))
+        st.v.copy_(keep)
 
 
 @pytest.mark.parametrize("dim,e4m3,t,group", [(128, False, 1, 6), (64, True, 1, 6), (128, True, 1, 6), (256, True, 1, 6),
@@ -346,6 +392,22 @@ def test_sequence_far_past_the_rows(w12):
     touched = ((st.k != before[0]).any(dim=(1, 3)), (st.v != before[1]).any(dim=(1, 3)))
     for x in touched:
         assert x.sum() == 2 and x[int(st.table[0, 4]), 5] and x[int(st.table[1, 2]), 7]
+
+
+def test_e4m3_cache(w12):
+    """An e4m3 cache from kv_cache, appended to and read."""
+    say("e4m3 cache")
+    scale = torch.tensor([0.02, 0.05]).cuda()
+    kv = w12.kv_cache(4, 2, 64, page=16, dtype=torch.float8_e4m3fn, k_scale=scale, v_scale=scale)
+    assert kv.k.dtype == torch.float8_e4m3fn and kv.nbytes() == 2 * 4 * 2 * 16 * 64 and not kv.k.view(torch.uint8).any()
+    st = Step(w12, [20, 9], [20, 9], 2, 64, 16, e4m3=True, spare=1)
+    st.k, st.v, st.sc, st.pages = kv.k, kv.v, (scale, scale), 4
+    st.make()
+    qkv = torch.randn(29, 8 * 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    before = (st.k.clone(), st.v.clone())
+    q = w12.kv_append(qkv, kv, st.batch)
+    check_append(st, qkv, 4, None, False, q, before, 29)
+    check_attention(st, q, 4, w12.attention(q, kv, st.batch))
 
 
 # ---- threads ----
