@@ -35,6 +35,9 @@
  *     16-byte aligned; the caller owns every buffer and keeps it alive until the stream work
  *     is finished.  The only device memory the library allocates is the GEMM workspace below;
  *     it keeps no other per-call state.
+ *   - Calls may come from several threads.  Those that share a stream's GEMM workspace or the same scratch
+ *     must not be made at the same time: a call may launch several kernels, and another's would fall
+ *     between them.
  *   - GEMM workspace: a GEMM call whose shape has too few 16-row tiles to occupy the device
  *     (for example W [1024, 5120], or [5120, 17408] at up to 32 rows of x) splits each row into
  *     k ranges whose partial sums go to a 64 MiB device buffer, then adds them in range order;

@@ -12,8 +12,8 @@
 // workgroups.  A workgroup stays in one row, so its place, page and position are looked up once for all.
 //
 // What bounds it: memory for prompts (5 of 1024 .. 4096 tokens of 48 + 2 * 8 heads of 128 columns from float,
-// 595 MB in 108 us, 5.5 TB/s; a plain copy on this card 4.95), the launch for single tokens (the kernel
-// 3.2 us, the call 8.3), the lookups' chain of loads and the division by the scale for drafts (64 sequences
+// 595 MB in 106 us, 5.6 TB/s; a plain copy on this card 4.95), the launch for single tokens (the kernel
+// 3.2 us, the call 8.4), the lookups' chain of loads and the division by the scale for drafts (64 sequences
 // of 16 into e4m3, 25 MB in 8.4 us).
 #include "kv_device.hpp"
 

@@ -33,8 +33,13 @@
 // so, 92 through them) run at 6.4 TB/s in a long sequence (131071 places, 537 MB: 84 us and 10 to join), at 5.4
 // where 64 sequences end unevenly (76 + 12 us), at 6.0 over 256 sequences (1.67 GB: 277 + 10 us).  One
 // sequence of 517 places is a chain of steps, 11 us for 2 MB.  Trees of 16 drafts and 6 heads over an e4m3
-// cache of 256 columns (184 MB) take 78 us and 10 to join, the LDS reads of the shared operands
-// the most of it (without loads 61 us, without products 54).
+// cache of 256 columns (184 MB) take 79 us and 10 to join: their 1 .. 16 drafts fill 1 .. 6 of a block's eight waves, which
+// wait 69 % of their time, the idle ones at the barriers and the others for a step's chain of LDS reads, products
+// and softmax with less than one of them a SIMD (LDS is in use 29 % of the time, the vector units 19, the matrix
+// cores 10; without loads 61 us, without products 54).
+// Prompts are not what this split is for: a block of rows goes through all of its sequence's places, also those behind
+// its last row's, and has every step of a whole prompt as a masked one (5 of 1206 .. 3941 tokens, 48 heads: 2.6 ms, the
+// products alone 0.33; 2048 tokens behind 32768 places 3.9 ms, 1.4).
 #include "kv_device.hpp"
 
 namespace w12 {
@@ -994,7 +999,8 @@ __global__ __launch_bounds__(kAtWide, 2) void k_attention_rows(AttnArgs a) {
 // since 32 hold registers that loads in flight need (64 sequences of one token, 6 rows each: 89 us, with 32
 // 103; of 1 or 2 tokens, 56 and 59); 32 up to 32 where they fit, else 128 (16 sequences of 3000 .. 5000 places and
 // 1 .. 8 tokens, 27 rows on average: 77 us, with 128 83); 128 beyond (54 rows on average: 96, with
-// 32, the sequence read again for each 32, 99).
+// 32, the sequence read again for each 32, 99).  A batch of both kinds has one of them: 63 single tokens of 2048 places
+// and a chunk of 2048 tokens take 760 us together, 88 and 547 apart; 255 and a chunk of 100 452, 339 and 56.
 struct AttnPlan {
   int rows;               // 16, 32: k_attention, 128: k_attention_rows
   int wgs;

@@ -19,11 +19,13 @@
 //   radix    if even one bin holds too many (thousands of equal logits), or top-p cuts what a top-k of
 //            thousands leaves, one workgroup reads the row, 8 bits of the logits' order a time.
 //
-// What bounds it: the chain of a row's join for few rows (1 row of 152064: 6 us for the parts, 12 for the
-// join, 3 for two kernels that find nothing to do; 21 in all), instructions for many: the parts of 64 rows take
-// 27 us (39 MB; 6 of them the exponentials in double, 2 the lists, the histogram nothing), of 256
-// rows of bfloat16 60 (78 MB).  Those need 73 and 123 us in all: the rest is joins of 256 rows at once (25 us) and
-// the second pair of kernels (20 + 22 us) for rows that keep tens of thousands.
+// What bounds it: the chain of a row's join for few rows (1 row of 152064: 6 us for the parts, 13 for the
+// join, 3 for two kernels that find nothing to do; 22 in all), instructions for many: the parts of 64 rows take
+// 27 us (39 MB) for 77 vector instructions a logit (18 of them in double, 6 conversions, 9 of integers), whose issue
+// is busy 71 % of the time; of 256 rows of bfloat16 60 (78 MB).  Those need 81 and 126 us in all: the rest is joins
+// (25 and 27 us) and the second pair of kernels (9 + 16 and 19 + 25 us) for rows that keep thousands.  Greedy rows take
+// 14 us (1 row), 17 (64), 41 (256 of bfloat16).  The radix reads a row up to 11 times, its parts one after the other:
+// 520 us for one row with a top-k of 5000 and top-p, 620 for 64.
 //
 // A border between two tokens has to fall as it does in the formula: where each border were off by 1e-7, as
 // sums of 152064 floats are, one draw in a hundred from a flat row would be a neighbour's.  So weights

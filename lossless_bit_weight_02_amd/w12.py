@@ -848,7 +848,8 @@ def kv_append(qkv, kv: KVCache, batch: KVBatch, rope: torch.Tensor | None = None
     float32, or a tuple of q, k and v rows (q None: only k and v, returns None).  rope float32 [positions,
     rot]: the cosines of a position's rot / 2 angles, then their sines; pairs are (i, i + rot / 2), or
     (2 i, 2 i + 1) with ``interleaved``.  A token without a place in the cache, or with a position outside
-    the table, is not appended (the latter's q is zero); rows behind the last sequence are left alone."""
+    the table, is not appended (the latter's q is zero); rows behind the last sequence are left alone.  out must
+    not overlap q, k or v."""
     _check_step(kv, batch)
     dev, dim, heads = kv.device, kv.dim, kv.heads
     if isinstance(qkv, torch.Tensor):
@@ -925,7 +926,7 @@ def attention(q: torch.Tensor, kv: KVCache, batch: KVBatch, scale: float | None 
     multiple of the cache's heads; returns [m, hq * dim] bfloat16, the output projection's x.  A row sees
     its sequence's places before the new tokens and the new ones up to its own (or those of its tree mask).
     scale: of the scores, default 1 / sqrt(dim).  A row that sees nothing gives zeros; rows behind the last
-    sequence are left alone.  Keeps a scratch buffer per stream; release_workspace frees it."""
+    sequence are left alone.  out must not overlap q.  Keeps a scratch buffer per stream; release_workspace frees it."""
     _check_step(kv, batch)
     dev, dim = kv.device, kv.dim
     if q.dtype != torch.bfloat16:
