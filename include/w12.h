@@ -458,7 +458,7 @@ typedef struct w12_kv_batch {
  * clamped to +-448 first; NaN stays NaN).  q and q_out may be NULL (hq = 0).  A token without a place
  * in the cache, or with a position outside 0 .. rope_rows - 1, is not appended; the latter's row of
  * q_out is zero.  Two tokens with one place (a page shared by tables) leave either's values.
- * q_out must not overlap q, k or v.  Uses no workspace.
+ * q_out may be q itself (bfloat16, ldq = hq * dim), and else must not overlap q, k or v.  Uses no workspace.
  */
 #define W12_IN_F32     0x100u
 #define W12_ROPE_PAIRS 0x200u
@@ -479,7 +479,7 @@ int w12_kv_append(const void *q, int64_t ldq, const void *k, int64_t ldk, const 
  * are held in float, the probabilities that meet v in 16 significant bits (over an e4m3 cache in 22, but
  * in 11 where a key head has more than 32 rows of q a sequence on average, 16 at 256 columns).  Their products
  * add up before they are divided by the probabilities' sum: v times the places seen times 2^8 (e4m3: 2^15)
- * must stay below float's largest.  y must not overlap q.
+ * must stay below float's largest.  y may be q itself (ldq = hq * dim), and else must not overlap it.
  * scratch: w12_attention_scratch bytes of the caller's device memory (16-byte aligned), in use until
  * the call's work on `stream` is finished; what it holds before does not matter.  Calls with different
  * scratch never touch each other's.  Which places are summed together depends on the lengths of the

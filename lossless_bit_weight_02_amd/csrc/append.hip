@@ -10,6 +10,7 @@
 // that does not turn.  A thread takes a unit: every access is 16 bytes or more, the columns of a row that
 // neighbouring lanes hold lie side by side, and one token of 64 heads already spreads over two
 // workgroups.  A workgroup stays in one row, so its place, page and position are looked up once for all.
+// A unit of q is written by the thread that has read it, so q_out may be q.
 //
 // What bounds it: memory for prompts (5 of 1024 .. 4096 tokens of 48 + 2 * 8 heads of 128 columns from float,
 // 595 MB in 106 us, 5.6 TB/s; a plain copy on this card 4.95), the launch for single tokens (the kernel

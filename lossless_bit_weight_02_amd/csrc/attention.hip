@@ -436,7 +436,8 @@ struct Pages {
   }
 };
 
-// Four columns of row `rq` of a sequence's rows for key head hk.
+// Four columns of row `rq` of a sequence's rows for key head hk.  (y may be q: a segment's rows of q are read by the
+// workgroups that have some of it, before the one that has all of it, or the join, writes them.)
 template <int DIM>
 __device__ __forceinline__ void attn_put(const AttnArgs& a, int first, int hk, uint32_t rq, int col, floatx4 o) {
   const uint32_t j = rq / (uint32_t)a.group, h = rq - j * a.group;

@@ -841,6 +841,15 @@ def _step_rows(t, m, cols, device, what):
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
 
 
+def _check_apart(out, what, at, m, cols, ld, size, same=False):
+    """Refuses an output that overlaps rows it is computed from; with ``same`` it may be those rows themselves (every
+    value is read before it is written)."""
+    to = out.data_ptr()
+    if to < at + ((m - 1) * ld + cols) * size and at < to + out.numel() * out.element_size():
+        if not (same and to == at and size == out.element_size() and (m == 1 or ld == cols)):
+            raise ValueError(f"out overlaps {what}")
+
+
 def kv_append(qkv, kv: KVCache, batch: KVBatch, rope: torch.Tensor | None = None, interleaved: bool = False,
               out: torch.Tensor | None = None):
     """Rotates the new tokens' q and k by position and puts k and v into the cache; returns the rotated q
@@ -848,8 +857,8 @@ def kv_append(qkv, kv: KVCache, batch: KVBatch, rope: torch.Tensor | None = None
     float32, or a tuple of q, k and v rows (q None: only k and v, returns None).  rope float32 [positions,
     rot]: the cosines of a position's rot / 2 angles, then their sines; pairs are (i, i + rot / 2), or
     (2 i, 2 i + 1) with ``interleaved``.  A token without a place in the cache, or with a position outside
-    the table, is not appended (the latter's q is zero); rows behind the last sequence are left alone.  out must
-    not overlap q, k or v."""
+    the table, is not appended (the latter's q is zero); rows behind the last sequence are left alone.  out may be
+    the rows of q themselves, and else must not overlap q, k or v."""
     _check_step(kv, batch)
     dev, dim, heads = kv.device, kv.dim, kv.heads
     if isinstance(qkv, torch.Tensor):
@@ -886,6 +895,11 @@ def kv_append(qkv, kv: KVCache, batch: KVBatch, rope: torch.Tensor | None = None
         if hq == 0:
             raise ValueError("out without q")
         _check_out(out, (m, hq * dim), (torch.bfloat16,), dev)
+        if m:
+            size = 4 if dt == torch.float32 else 2
+            _check_apart(out, "q", q, m, hq * dim, ldq, size, same=True)
+            _check_apart(out, "k", k, m, heads * dim, ldk, size)
+            _check_apart(out, "v", v, m, heads * dim, ldv, size)
     elif hq:
         out = batch.lens.new_empty((m, hq * dim), dtype=torch.bfloat16)
     if m == 0:
@@ -926,7 +940,7 @@ def attention(q: torch.Tensor, kv: KVCache, batch: KVBatch, scale: float | None 
     multiple of the cache's heads; returns [m, hq * dim] bfloat16, the output projection's x.  A row sees
     its sequence's places before the new tokens and the new ones up to its own (or those of its tree mask).
     scale: of the scores, default 1 / sqrt(dim).  A row that sees nothing gives zeros; rows behind the last
-    sequence are left alone.  out must not overlap q.  Keeps a scratch buffer per stream; release_workspace frees it."""
+    sequence are left alone.  out may be q itself, and else must not overlap it.  Keeps a scratch buffer per stream; release_workspace frees it."""
     _check_step(kv, batch)
     dev, dim = kv.device, kv.dim
     if q.dtype != torch.bfloat16:
@@ -940,6 +954,8 @@ def attention(q: torch.Tensor, kv: KVCache, batch: KVBatch, scale: float | None 
         out = q.new_empty((m, hq * dim))
     else:
         _check_out(out, (m, hq * dim), (torch.bfloat16,), dev)
+        if m:
+            _check_apart(out, "q", qp, m, hq * dim, ldq, 2, same=True)
     if m == 0:
         return out
     L = lib()

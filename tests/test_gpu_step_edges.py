@@ -410,6 +410,33 @@ def test_e4m3_cache(w12):
     check_attention(st, q, 4, w12.attention(q, kv, st.batch))
 
 
+# ---- outputs over inputs ----
+def test_in_place(w12):
+    """Rotation and attention into the rows of q themselves, of whole and split sequences, few rows and many; other
+    overlaps are refused."""
+    for lens, news, dim in (([5000, 40, 3], [1, 1, 1], 128), ([300, 40], [20, 40], 64), ([700, 9000], [2, 30], 256)):
+        st = Step(w12, lens, news, 2, dim, 16)
+        q = queries(st, 12)
+        say(f"in place lens={lens} news={news}")
+        want = w12.attention(q, st.kv, st.batch)
+        y = q.clone()
+        assert w12.attention(y, st.kv, st.batch, out=y) is y and torch.equal(y, want)
+        k, v = queries(st, 2, seed=5), queries(st, 2, seed=6)
+        rope = torch.tensor(rope_table(max(lens) + 1, dim)).cuda()
+        for pairs in (False, True):
+            r = w12.kv_append((q, k, v), st.kv, st.batch, rope=rope, interleaved=pairs)
+            z = q.clone()
+            w12.kv_append((z, k, v), st.kv, st.batch, rope=rope, interleaved=pairs, out=z)
+            assert torch.equal(z, r)
+    wide = torch.zeros((st.rows + 1) * 16 * dim, dtype=torch.bfloat16, device="cuda")
+    qkv = wide[:st.rows * 16 * dim].view(st.rows, 16 * dim)
+    for out in (wide[:st.rows * 12 * dim], wide[8:8 + st.rows * 12 * dim], wide[-st.rows * 12 * dim:]):
+        with pytest.raises(ValueError):
+            w12.kv_append(qkv, st.kv, st.batch, out=out.view(st.rows, 12 * dim))
+        with pytest.raises(ValueError):
+            w12.attention(qkv[:, :12 * dim], st.kv, st.batch, out=out.view(st.rows, 12 * dim))
+
+
 # ---- threads ----
 def test_two_threads_on_one_stream(w12):
     """Attention that ends in a join and sampling of several kernels, called from two threads on the same stream: each

@@ -47,3 +47,23 @@ def test_one_call_at_a_time(monkeypatch):
     with pytest.raises(w12.W12Error):
         w12._step_call("attention", 1000, torch.device("cpu"), 0, lambda buf: w12.W12_ERR_ARG)
     work()
+
+
+def test_output_apart_from_inputs():
+    torch = pytest.importorskip("torch")
+    buf = torch.zeros(1000, dtype=torch.bfloat16)
+    out = buf[:64].view(4, 16)
+
+    def check(at, m=4, cols=16, ld=16, size=2, same=False):
+        w12._check_apart(out, "q", buf.data_ptr() + 2 * at, m, cols, ld, size, same)
+
+    check(64)                                           # side by side
+    check(0, same=True)                                 # the rows themselves
+    check(0, m=1, ld=99, same=True)
+    for bad in (dict(at=0), dict(at=0, ld=32, same=True), dict(at=8, same=True), dict(at=63), dict(at=0, size=4, same=True)):
+        with pytest.raises(ValueError):
+            check(**bad)
+    out = buf[64:128].view(4, 16)
+    check(0)
+    with pytest.raises(ValueError):
+        check(0, ld=17)
